@@ -1,4 +1,4 @@
-"""ctypes view of the C ABI declared in include/spec_verify.h.
+"""ctypes view of the C ABI declared in include/spec_verify.h and spec_logits.h.
 
 Argument marshalling only: the structures below mirror the C structs field
 for field, and ``lib()`` loads the in-tree libspecverify.so.  There is no
@@ -17,6 +17,7 @@ SPEC_F32, SPEC_BF16 = 0, 1
 SPEC_GREEDY, SPEC_SAMPLE = 0, 1
 SPEC_NOALLOC_SCRATCH_BYTES = 8 << 20
 ERR_TOKEN, ERR_PARENT, ERR_NONFINITE, ERR_ZERO_MASS, ERR_INTERNAL, ERR_WINDOW = 1, 2, 4, 8, 16, 32
+ERR_MASK = 64
 
 _vp = C.c_void_p
 
@@ -124,6 +125,37 @@ class ClaspArgs(C.Structure):
     ]
 
 
+class ProcessArgs(C.Structure):
+    _fields_ = [
+        ("B", C.c_int), ("n", C.c_int), ("V", C.c_int), ("dtype", C.c_int),
+        ("ld", C.c_longlong), ("out_ld", C.c_longlong), ("logits", _vp), ("out", _vp),
+        ("tokens", _vp), ("parent", _vp), ("tokens_ld", C.c_int), ("history_ld", C.c_int),
+        ("history", _vp), ("history_len", _vp), ("prompt_len", _vp),
+        ("repetition", _vp), ("frequency", _vp), ("presence", _vp),
+        ("bias_tokens", _vp), ("bias_values", _vp), ("bias_len", _vp),
+        ("bias_ld", C.c_int), ("mask_rows", C.c_int), ("mask", _vp), ("mask_ld", C.c_longlong),
+        ("mask_index", _vp), ("seq_error", _vp), ("error_word", _vp)
+    ]
+
+
+class QuantizeInt4Args(C.Structure):
+    _fields_ = [
+        ("V", C.c_int), ("d", C.c_int), ("group", C.c_int), ("dtype", C.c_int),
+        ("ld", C.c_longlong), ("codes_ld", C.c_longlong), ("scales_ld", C.c_longlong), ("zeros_ld", C.c_longlong),
+        ("weights", _vp), ("codes", _vp), ("scales", _vp), ("zeros", _vp)
+    ]
+
+
+class Int4ProductArgs(C.Structure):
+    _fields_ = [
+        ("R", C.c_int), ("V", C.c_int), ("d", C.c_int), ("group", C.c_int), ("out_dtype", C.c_int),
+        ("x_ld", C.c_longlong), ("codes_ld", C.c_longlong), ("scales_ld", C.c_longlong),
+        ("zeros_ld", C.c_longlong), ("out_ld", C.c_longlong),
+        ("x", _vp), ("codes", _vp), ("scales", _vp), ("zeros", _vp), ("out", _vp), ("error_word", _vp),
+        ("workspace", _vp), ("workspace_bytes", C.c_size_t)
+    ]
+
+
 # every symbol include/spec_verify.h declares, with its ctypes signature
 SIGNATURES = {
     "spec_chain_workspace_size": (C.c_size_t, [C.c_int, C.c_int, C.c_int]),
@@ -147,6 +179,14 @@ SIGNATURES = {
     "spec_verify_chain_lm_head": (C.c_int, [C.POINTER(LmHeadChainArgs), _vp]),
 }
 
+# every symbol include/spec_logits.h declares
+LOGITS_SIGNATURES = {
+    "spec_process_logits": (C.c_int, [C.POINTER(ProcessArgs), _vp]),
+    "spec_quantize_int4": (C.c_int, [C.POINTER(QuantizeInt4Args), _vp]),
+    "spec_int4_product_workspace_size": (C.c_size_t, [C.c_int, C.c_int, C.c_int, C.c_int]),
+    "spec_int4_product": (C.c_int, [C.POINTER(Int4ProductArgs), _vp]),
+}
+
 _LIB = None
 
 
@@ -160,7 +200,7 @@ def lib() -> C.CDLL:
                 f"{path} is missing: build it with `python -m draft_verification_gb300.build` "
                 "(there is no CPU fallback)")
         handle = C.CDLL(path)
-        for name, (res, args) in SIGNATURES.items():
+        for name, (res, args) in {**SIGNATURES, **LOGITS_SIGNATURES}.items():
             fn = getattr(handle, name)
             fn.restype = res
             fn.argtypes = args

@@ -1,0 +1,519 @@
+// Per-request processing of logits: penalties for repeated tokens, biases and
+// grammar masks, each row with the tokens before its own position (chain or
+// tree).  The arithmetic and the argument meanings are in spec_logits.h.
+//
+// process_kernel: a CTA owns one slab of the vocabulary of one sequence and
+// streams that slab of the sequence's rows.  It builds one table for the slab
+// in shared memory - per token a 32-bit word (low 31 bits: occurrences that
+// count, bit 31: occurs in the prompt), the sum of its bias entries, and a
+// bitmap of the tokens that have either - by reading the whole history once,
+// and reuses it for every row.  From row to row only the drafted tokens on
+// the path change: where one of them lies in the slab (rows marked
+// beforehand, all in parallel) the CTA synchronises and one thread updates
+// the table; all other rows follow one another without a barrier.
+//
+// An element is read once and written once, in 16-byte vectors aligned in
+// memory: a row that starts at element m of its vector has tokens
+// [k e - m, k e - m + e) in vector k, so the table starts e - 1 tokens before
+// the slab and bitmap and mask bits are taken by funnel shifts.  Vectors that
+// stick out of the row, and rows whose output starts at another offset than
+// the input, are written element by element.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "common.cuh"
+#include "internal.h"
+#include "spec_logits.h"
+
+namespace sv {
+namespace {
+
+constexpr int kProcThreads = 256;
+constexpr int kMaxRows = 1024;       // rows per sequence
+constexpr unsigned kInPrompt = 1u << 31;
+
+struct ProcessParams {
+  int B, n, V;
+  long long ld, out_ld;
+  const void* logits;
+  void* out;
+  const int* tokens;
+  const int* parent;
+  int tokens_ld, history_ld;
+  const int* history;
+  const int* history_len;
+  const int* prompt_len;
+  const float* repetition;
+  const float* frequency;
+  const float* presence;
+  const int* bias_tokens;
+  const float* bias_values;
+  const int* bias_len;
+  int bias_ld, mask_rows;
+  const unsigned* mask;
+  long long mask_ld;
+  const int* mask_index;
+  int* seq_error;
+  int* error_word;
+  int rows_per_cta;
+};
+
+// 16 bytes of logits.  Not the read-only path: the output may be the input.
+__device__ __forceinline__ uint4 ld_row16(const void* p) {
+  if (kDebugChecks && misaligned16(p)) return make_uint4(0x7fc00000u, 0x7fc00000u, 0x7fc00000u, 0x7fc00000u);
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
+template <typename T>
+struct Lanes;  // the elements of a 16-byte vector
+
+template <>
+struct Lanes<bf16_t> {
+  static constexpr int kN = 8;
+  static __device__ __forceinline__ float get(const uint32_t (&w)[4], int j) {
+    return (j & 1) ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
+  }
+  static __device__ __forceinline__ uint32_t bits(const uint32_t (&w)[4], int j) {
+    return (j & 1) ? w[j >> 1] >> 16 : w[j >> 1] & 0xffffu;
+  }
+  static __device__ __forceinline__ void set_bits(uint32_t (&w)[4], int j, uint32_t b) {
+    w[j >> 1] = (j & 1) ? (w[j >> 1] & 0xffffu) | (b << 16) : (w[j >> 1] & 0xffff0000u) | b;
+  }
+  static __device__ __forceinline__ uint32_t round(float x) {
+    uint16_t r;
+    asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(r) : "f"(x));
+    return r;
+  }
+  static constexpr uint32_t kNegInf = 0xff80u;
+};
+
+template <>
+struct Lanes<float> {
+  static constexpr int kN = 4;
+  static __device__ __forceinline__ float get(const uint32_t (&w)[4], int j) { return __uint_as_float(w[j]); }
+  static __device__ __forceinline__ uint32_t bits(const uint32_t (&w)[4], int j) { return w[j]; }
+  static __device__ __forceinline__ void set_bits(uint32_t (&w)[4], int j, uint32_t b) { w[j] = b; }
+  static __device__ __forceinline__ uint32_t round(float x) { return __float_as_uint(x); }
+  static constexpr uint32_t kNegInf = 0xff800000u;
+};
+
+template <typename T>
+__device__ __forceinline__ uint32_t load_bits(const T* p) {
+  if constexpr (sizeof(T) == 2) {
+    return *reinterpret_cast<const volatile unsigned short*>(p);
+  } else {
+    return *reinterpret_cast<const volatile unsigned*>(p);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store_bits(T* p, uint32_t b) {
+  if constexpr (sizeof(T) == 2) {
+    *reinterpret_cast<unsigned short*>(p) = static_cast<unsigned short>(b);
+  } else {
+    *reinterpret_cast<unsigned*>(p) = b;
+  }
+}
+
+__host__ __device__ constexpr int slab_tokens(int elems, int vecs) { return kProcThreads * vecs * elems; }
+// table entries: the slab and the e - 1 tokens before it
+__host__ __device__ constexpr int table_tokens(int elems, int vecs) { return slab_tokens(elems, vecs) + elems - 1; }
+__host__ __device__ constexpr int bitmap_words(int elems, int vecs) { return (table_tokens(elems, vecs) + 31) / 32 + 1; }
+
+template <typename T, int kVecs>
+__global__ void __launch_bounds__(kProcThreads) process_kernel(const ProcessParams P) {
+  using L = Lanes<T>;
+  constexpr int E = L::kN;
+  constexpr uint32_t kFull = (1u << E) - 1u;
+  constexpr int kTable = table_tokens(E, kVecs);
+  constexpr int kWords = bitmap_words(E, kVecs);
+
+  extern __shared__ unsigned proc_dyn[];
+  unsigned* count = proc_dyn;                         // [kTable]
+  unsigned* touched = count + kTable;                 // [kWords]
+  unsigned* change = touched + kWords;                // [kMaxRows / 32] rows before which the table changes
+  int* s_tok = reinterpret_cast<int*>(change + kMaxRows / 32);  // [n]
+  int* s_par = s_tok + P.n;                           // [n]
+  int* s_mask = s_par + P.n;                          // [n]
+  float* bias = reinterpret_cast<float*>(s_mask + P.n);  // [kTable], with biases
+  __shared__ int s_err;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b = blockIdx.z;
+  const int r0 = blockIdx.y * P.rows_per_cta;
+  const int r1 = min(P.n, r0 + P.rows_per_cta);
+  const int v0 = blockIdx.x * (kProcThreads * kVecs);  // first vector of the slab
+  const int lo = v0 * E - (E - 1);                     // first token of the table
+  const bool checks = blockIdx.x == 0 && blockIdx.y == 0;
+  const bool tree = P.parent != nullptr;
+  const bool biased = P.bias_tokens != nullptr;
+
+  uint32_t cur[kVecs][4], nxt[kVecs][4];
+  uint32_t cur_ok[kVecs], nxt_ok[kVecs];  // mask bits of each vector
+
+  // Read row i's vectors and mask bits; mrow < 0: not masked.
+  auto load_row = [&](int i, int mrow, uint32_t (&w)[kVecs][4], uint32_t (&ok)[kVecs]) {
+    const long long row = static_cast<long long>(b) * P.n + i;
+    const T* src = static_cast<const T*>(P.logits) + row * P.ld;
+    const int m = static_cast<int>((row * P.ld) % E);
+    const unsigned* mk = mrow >= 0 ? P.mask + static_cast<long long>(mrow) * P.mask_ld : nullptr;
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      const int t0 = (v0 + j * kProcThreads + tid) * E - m;
+      ok[j] = kFull;
+      if (t0 >= P.V) continue;
+      if (mk) {
+        if (t0 < 0) {
+          ok[j] = (__ldg(mk) << -t0) & kFull;
+        } else {
+          const int q = t0 >> 5, s = t0 & 31;
+          const unsigned a = __ldg(mk + q);
+          const unsigned c = (s + E > 32 && (q + 1) * 32 < P.V) ? __ldg(mk + q + 1) : 0u;
+          ok[j] = __funnelshift_r(a, c, s) & kFull;
+        }
+      }
+      if (t0 >= 0 && t0 + E <= P.V) {
+        const uint4 x = ld_row16(src + t0);
+        w[j][0] = x.x;
+        w[j][1] = x.y;
+        w[j][2] = x.z;
+        w[j][3] = x.w;
+      } else {
+        w[j][0] = w[j][1] = w[j][2] = w[j][3] = 0u;
+#pragma unroll
+        for (int k = 0; k < E; ++k)
+          if (t0 + k >= 0 && t0 + k < P.V) L::set_bits(w[j], k, load_bits(src + t0 + k));
+      }
+    }
+  };
+  auto mask_row = [&](int i) {
+    if (!P.mask) return -1;
+    const long long row = static_cast<long long>(b) * P.n + i;
+    const long long mr = P.mask_index ? static_cast<long long>(__ldg(P.mask_index + row)) : row;
+    return mr < P.mask_rows ? static_cast<int>(mr) : -1;
+  };
+
+  // the first row's loads are in flight while the table is built
+  load_row(r0, mask_row(r0), cur, cur_ok);
+
+  for (int i = tid; i < kTable; i += kProcThreads) count[i] = 0u;
+  for (int i = tid; i < kWords; i += kProcThreads) touched[i] = 0u;
+  for (int i = tid; i < kMaxRows / 32; i += kProcThreads) change[i] = 0u;
+  if (biased)
+    for (int i = tid; i < kTable; i += kProcThreads) bias[i] = 0.f;
+  if (tid == 0) s_err = 0;
+  __syncthreads();
+
+  int err = 0;
+  const auto touch = [&](int at) { atomicOr(&touched[at >> 5], 1u << (at & 31)); };
+
+  // the drafted tokens, the tree and the mask rows
+  for (int i = tid; i < P.n; i += kProcThreads) {
+    int t = -1, p = 0;
+    if (P.tokens && i < P.tokens_ld) t = __ldg(P.tokens + static_cast<long long>(b) * P.tokens_ld + i);
+    const bool used = tree ? i > 0 : (P.tokens && i < P.n - 1);
+    if (used && (t < 0 || t >= P.V)) {
+      err |= SPEC_ERR_TOKEN;
+      t = -1;
+    }
+    if (tree && i > 0) {
+      p = __ldg(P.parent + static_cast<long long>(b) * P.n + i);
+      if (p < 0 || p >= i) {
+        err |= SPEC_ERR_PARENT;
+        p = 0;
+      }
+    }
+    s_tok[i] = used ? t : -1;
+    s_par[i] = p;
+    s_mask[i] = mask_row(i);
+    if (P.mask && P.mask_index) {
+      const int mi = __ldg(P.mask_index + static_cast<long long>(b) * P.n + i);
+      if (mi < -1 || mi >= P.mask_rows) err |= SPEC_ERR_MASK;
+    }
+  }
+
+  // the history
+  if (P.history) {
+    int len = P.history_len ? __ldg(P.history_len + b) : P.history_ld;
+    if (len < 0 || len > P.history_ld) {
+      err |= SPEC_ERR_TOKEN;
+      len = len < 0 ? 0 : P.history_ld;
+    }
+    const int prompt = P.prompt_len ? __ldg(P.prompt_len + b) : 0;
+    const int* h = P.history + static_cast<long long>(b) * P.history_ld;
+    constexpr int kU = 8;
+    for (int base = 0; base < len; base += kProcThreads * kU) {
+      int t[kU];
+#pragma unroll
+      for (int k = 0; k < kU; ++k) {
+        const int at = base + k * kProcThreads + tid;
+        t[k] = at < len ? __ldg(h + at) : lo - 1;
+      }
+#pragma unroll
+      for (int k = 0; k < kU; ++k) {
+        const int at = base + k * kProcThreads + tid;
+        if (at < len && (t[k] < 0 || t[k] >= P.V)) {
+          err |= SPEC_ERR_TOKEN;
+          continue;
+        }
+        const unsigned o = static_cast<unsigned>(t[k] - lo);
+        if (at < len && o < static_cast<unsigned>(kTable)) {
+          if (at < prompt) atomicOr(&count[o], kInPrompt);
+          else atomicAdd(&count[o], 1u);
+          touch(static_cast<int>(o));
+        }
+      }
+    }
+  }
+
+  // the biases, one warp, in their order (entries of one token add up as listed)
+  if (biased && warp == 0) {
+    int len = P.bias_len ? __ldg(P.bias_len + b) : P.bias_ld;
+    if (len < 0 || len > P.bias_ld) {
+      err |= SPEC_ERR_TOKEN;
+      len = len < 0 ? 0 : P.bias_ld;
+    }
+    for (int base = 0; base < len; base += 32) {
+      const int at = base + lane;
+      const long long src = static_cast<long long>(b) * P.bias_ld + at;
+      int t = -1;
+      float x = 0.f;
+      if (at < len) {
+        t = __ldg(P.bias_tokens + src);
+        x = __ldg(P.bias_values + src);
+        if (t < 0 || t >= P.V) {
+          err |= SPEC_ERR_TOKEN;
+          t = -1;
+        }
+      }
+      const unsigned o = static_cast<unsigned>(t - lo);
+      const bool mine = t >= 0 && o < static_cast<unsigned>(kTable);
+      const unsigned peers = __match_any_sync(0xffffffffu, mine ? static_cast<int>(o) : -1 - lane);
+      const bool alone = !mine || (peers & (peers - 1)) == 0;
+      if (__all_sync(0xffffffffu, alone)) {
+        if (mine) bias[o] += x;
+      } else {
+        for (int l = 0; l < 32; ++l) {
+          if (l == lane && mine) bias[o] += x;
+          __syncwarp();
+        }
+      }
+      if (mine) touch(static_cast<int>(o));
+      __syncwarp();
+    }
+  }
+  if (checks && err) atomicOr(&s_err, err);
+  __syncthreads();
+
+  // the drafted tokens before row r0, and the rows before which the table changes
+  const auto in_slab = [&](int t) { return t >= 0 && static_cast<unsigned>(t - lo) < static_cast<unsigned>(kTable); };
+  if (!tree) {
+    for (int j = tid; j < r0; j += kProcThreads)
+      if (in_slab(s_tok[j])) {
+        atomicAdd(&count[s_tok[j] - lo], 1u);
+        touch(s_tok[j] - lo);
+      }
+    for (int i = r0 + 1 + tid; i < r1; i += kProcThreads)
+      if (in_slab(s_tok[i - 1])) atomicOr(&change[i >> 5], 1u << (i & 31));
+  } else {
+    if (tid == 0)
+      for (int a = r0; a > 0; a = s_par[a])
+        if (in_slab(s_tok[a])) {
+          atomicAdd(&count[s_tok[a] - lo], 1u);
+          touch(s_tok[a] - lo);
+        }
+    for (int i = r0 + 1 + tid; i < r1; i += kProcThreads) {
+      int x = i - 1, y = i;
+      bool any = false;
+      while (x != y && !any) {
+        const int z = x > y ? x : y;
+        any = in_slab(s_tok[z]);
+        if (x > y) x = s_par[x];
+        else y = s_par[y];
+      }
+      if (any) atomicOr(&change[i >> 5], 1u << (i & 31));
+    }
+  }
+  __syncthreads();
+  if (checks && tid == 0) {
+    if (P.seq_error) P.seq_error[b] = s_err;
+    if (s_err && P.error_word) atomicOr(P.error_word, s_err);
+  }
+
+  const float rep = P.repetition ? __ldg(P.repetition + b) : 1.f;
+  const float freq = P.frequency ? __ldg(P.frequency + b) : 0.f;
+  const float pres = P.presence ? __ldg(P.presence + b) : 0.f;
+
+  for (int i = r0; i < r1; ++i) {
+    if (i + 1 < r1) load_row(i + 1, s_mask[i + 1], nxt, nxt_ok);
+    if (i > r0 && (change[i >> 5] >> (i & 31)) & 1u) {
+      __syncthreads();  // everyone is done with the previous row's table
+      if (tid == 0) {
+        const auto add = [&](int t, unsigned d) {
+          if (!in_slab(t)) return;
+          count[t - lo] += d;
+          touched[(t - lo) >> 5] |= 1u << ((t - lo) & 31);
+        };
+        if (!tree) {
+          add(s_tok[i - 1], 1u);
+        } else {
+          int x = i - 1, y = i;  // leave x's path, enter y's, up to their last common node
+          while (x != y) {
+            if (x > y) {
+              add(s_tok[x], ~0u);
+              x = s_par[x];
+            } else {
+              add(s_tok[y], 1u);
+              y = s_par[y];
+            }
+          }
+        }
+      }
+      __syncthreads();
+    }
+    const long long row = static_cast<long long>(b) * P.n + i;
+    const int m = static_cast<int>((row * P.ld) % E);
+    T* dst = static_cast<T*>(P.out) + row * P.out_ld;
+    const bool same = static_cast<int>((row * P.out_ld) % E) == m;
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      const int t0 = (v0 + j * kProcThreads + tid) * E - m;
+      if (t0 >= P.V) continue;
+      const int at = t0 - lo;
+      const uint32_t hit =
+          __funnelshift_r(touched[at >> 5], touched[(at >> 5) + 1], at & 31) & cur_ok[j] & kFull;
+      if (hit) {
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+          if (!((hit >> k) & 1u)) continue;
+          const unsigned c = count[at + k];
+          float x = L::get(cur[j], k);
+          if (c) x = x > 0.f ? __fdiv_rn(x, rep) : __fmul_rn(x, rep);
+          const unsigned made = c & ~kInPrompt;
+          if (made) x = __fsub_rn(x, __fmaf_rn(freq, static_cast<float>(made), pres));
+          const float plus = biased ? bias[at + k] : 0.f;
+          if (plus != 0.f) x = __fadd_rn(x, plus);
+          if (c || plus != 0.f) L::set_bits(cur[j], k, L::round(x));
+        }
+      }
+      if (cur_ok[j] != kFull) {
+#pragma unroll
+        for (int k = 0; k < E; ++k)
+          if (!((cur_ok[j] >> k) & 1u)) L::set_bits(cur[j], k, L::kNegInf);
+      }
+      if (same && t0 >= 0 && t0 + E <= P.V) {
+        if (!(kDebugChecks && misaligned16(dst + t0)))
+          *reinterpret_cast<uint4*>(dst + t0) = make_uint4(cur[j][0], cur[j][1], cur[j][2], cur[j][3]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < E; ++k)
+          if (t0 + k >= 0 && t0 + k < P.V) store_bits(dst + t0 + k, L::bits(cur[j], k));
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) cur[j][k] = nxt[j][k];
+      cur_ok[j] = nxt_ok[j];
+    }
+  }
+}
+
+template <typename T, int kVecs>
+size_t process_smem(const ProcessParams& p) {
+  constexpr int E = Lanes<T>::kN;
+  size_t words = table_tokens(E, kVecs) + bitmap_words(E, kVecs) + kMaxRows / 32 + 3 * static_cast<size_t>(p.n);
+  if (p.bias_tokens) words += table_tokens(E, kVecs);
+  return words * 4;
+}
+
+int slabs_of(const ProcessParams& p, int elems, int vecs) {
+  // vectors of the longest row: a row may start anywhere in its first vector
+  const int lead = p.ld % elems ? elems - 1 : 0;
+  const int nvec = (p.V + lead + elems - 1) / elems;
+  return (nvec + kProcThreads * vecs - 1) / (kProcThreads * vecs);
+}
+
+template <typename T, int kVecs>
+cudaError_t launch_process(ProcessParams p, cudaStream_t s) {
+  const size_t dyn = process_smem<T, kVecs>(p);
+  cudaError_t e = cudaFuncSetAttribute(process_kernel<T, kVecs>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(dyn));
+  if (e != cudaSuccess) return e;
+  const int slabs = slabs_of(p, Lanes<T>::kN, kVecs);
+  // few sequences and slabs: a sequence's rows are split as well (each part
+  // reads the history again)
+  const long long have = static_cast<long long>(slabs) * p.B;
+  const long long parts = have >= 304 ? 1 : (304 + have - 1) / have;
+  const int chunks = static_cast<int>(parts < p.n ? parts : p.n);
+  p.rows_per_cta = (p.n + chunks - 1) / chunks;
+  const dim3 grid(static_cast<unsigned>(slabs), static_cast<unsigned>((p.n + p.rows_per_cta - 1) / p.rows_per_cta),
+                  static_cast<unsigned>(p.B));
+  process_kernel<T, kVecs><<<grid, kProcThreads, dyn, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t dispatch_process(const ProcessParams& p, cudaStream_t s) {
+  // long slabs read the history fewer times; short ones fill the GPU
+  if (static_cast<long long>(slabs_of(p, Lanes<T>::kN, 4)) * p.B >= 304) return launch_process<T, 4>(p, s);
+  return launch_process<T, 1>(p, s);
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+}  // namespace
+}  // namespace sv
+
+extern "C" spec_status spec_process_logits(const spec_process_args* a, cudaStream_t stream) {
+  using namespace sv;
+  NvtxRange nvtx_range("spec_process_logits");
+  if (a == nullptr) return SPEC_EINVAL;
+  if (a->dtype != SPEC_F32 && a->dtype != SPEC_BF16) return SPEC_EDTYPE;
+  if (a->B < 1 || a->B > kMaxSeq || a->n < 1 || a->n > kMaxRows || a->V < 1 || a->V > 2097152) return SPEC_EINVAL;
+  if (a->ld < a->V || a->out_ld < a->V || !a->logits || !a->out) return SPEC_EINVAL;
+  if (a->logits == a->out && a->ld != a->out_ld) return SPEC_EINVAL;
+  if (a->parent && !a->tokens) return SPEC_EINVAL;
+  if (a->tokens && a->tokens_ld < (a->parent ? a->n : a->n - 1)) return SPEC_EINVAL;
+  if (a->history && a->history_ld < 0) return SPEC_EINVAL;
+  if (a->bias_tokens && (!a->bias_values || a->bias_ld < 0)) return SPEC_EINVAL;
+  if (a->mask && (a->mask_rows < 1 || a->mask_ld < (a->V + 31) / 32)) return SPEC_EINVAL;
+  if (a->mask && !a->mask_index && a->mask_rows < static_cast<long long>(a->B) * a->n) return SPEC_EINVAL;
+  if (!aligned16(a->logits) || !aligned16(a->out)) return SPEC_EALIGN;
+  ProcessParams p{};
+  p.B = a->B;
+  p.n = a->n;
+  p.V = a->V;
+  p.ld = a->ld;
+  p.out_ld = a->out_ld;
+  p.logits = a->logits;
+  p.out = a->out;
+  p.tokens = a->tokens;
+  p.parent = a->parent;
+  p.tokens_ld = a->tokens_ld;
+  p.history = a->history_ld > 0 ? a->history : nullptr;
+  p.history_ld = a->history_ld;
+  p.history_len = a->history_len;
+  p.prompt_len = a->prompt_len;
+  p.repetition = a->repetition;
+  p.frequency = a->frequency;
+  p.presence = a->presence;
+  p.bias_tokens = a->bias_ld > 0 ? a->bias_tokens : nullptr;
+  p.bias_values = a->bias_values;
+  p.bias_len = a->bias_len;
+  p.bias_ld = a->bias_ld;
+  p.mask = a->mask;
+  p.mask_rows = a->mask_rows;
+  p.mask_ld = a->mask_ld;
+  p.mask_index = a->mask_index;
+  p.seq_error = a->seq_error;
+  p.error_word = a->error_word;
+  const cudaError_t e =
+      a->dtype == SPEC_BF16 ? dispatch_process<bf16_t>(p, stream) : dispatch_process<float>(p, stream);
+  return e == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
+}

@@ -27,11 +27,13 @@ Modules
 ``pipeline_async`` the PipeSpec stages at independent buffer offsets (each
                   stage a chain verification of its own window, then the
                   rollbacks).
+``logits``        the logit-side operators: processing of logits, 4-bit
+                  quantisation and products with 4-bit weights.
 
 Every function states the passage it follows.  Points where the pages are
 silent or ambiguous follow the readings listed in the design notes; each is
 repeated in the docstring that depends on it.
 """
 
-from . import (clasp, closed_forms, compact, consulted, consulted_tree, lm_head, pipeline,  # noqa: F401
-               pipeline_async, verify)
+from . import (clasp, closed_forms, compact, consulted, consulted_tree, lm_head, logits,  # noqa: F401
+               pipeline, pipeline_async, verify)
