@@ -1,0 +1,688 @@
+// Products of a few bfloat16 rows with a 4-bit matrix (layout and rule in
+// spec_logits.h):
+//   y(r, v) = sum_g s(g, v) * D_g(v, r),
+//   D_g(v, r) = sum over k in group g of (q(v, k) - z(g, v)) x(r, k).
+//
+// q - z is an integer of at most 15 in magnitude, exact in bfloat16, so D_g is
+// a tensor-core product of exact operands with a float32 accumulator, and the
+// scale multiplies it in float32: no weight is rounded.  Folding the scale into
+// the weights instead would round each of them to 8 bits.
+//
+// A tile is 128 vocabulary entries (M) by N rows (N = 16, 32, 64 or 128).  The
+// weights are the A operand: they are unpacked in registers and stored to
+// tensor memory, which tcgen05.mma reads A from, so they cross shared memory
+// once, packed.  Roles of a CTA's 16 warps:
+//   warp 0          copies weight stages (128 entries x 256 columns, 16 KB)
+//                   into a ring with TMA, and requests the scales and zero
+//                   points of the same columns into L2;
+//   warp 1          issues the MMAs (one thread);
+//   warp 2          copies the rows' chunks (N x 128 columns) with TMA;
+//   unpack warps    8 (N <= 64) or 4: thread t of a warpgroup owns entry t of
+//                   the tile; it reads 128 columns (64 bytes) of its entry,
+//                   turns them into q - z and stores them to 64 columns of
+//                   tensor memory (a ring of 4 chunks);
+//   epilogue warps  4 (N <= 64) or 8 (N = 128, half of the rows each): thread
+//                   t owns entry t, reads each group's D_g and adds s D_g to
+//                   its float32 sums.
+//
+// The work is a list of units (one weight stage of one tile, tile by tile)
+// that the CTAs divide evenly, so that a tile may be shared by CTAs along the
+// width: each leaves its partial sums in the workspace, and whichever arrives
+// last at the tile's counter adds them in the order of the columns, so the
+// result does not depend on who that is.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <map>
+#include <mutex>
+
+#include "common.cuh"
+#include "internal.h"
+#include "spec_logits.h"
+#include "tc.cuh"
+#include "tma_host.h"
+
+namespace sv {
+namespace {
+
+constexpr int kTileV = 128;                 // vocabulary entries per tile (MMA M)
+constexpr int kStageK = 256;                // columns of a weight stage: 128 packed bytes per entry
+constexpr int kChunkK = 128;                // columns of a chunk: what one A slot holds
+constexpr int kStageBytes = kTileV * kStageK / 2;
+constexpr int kASlots = 4;                  // A ring: 4 x 64 tensor-memory columns
+constexpr int kACols = kChunkK / 2;
+constexpr int kDCols = 256;                 // accumulators: the other 256 columns
+constexpr int kMaxCtas = 152;               // persistent CTAs the workspace is sized for
+constexpr int kI4Threads = 512;
+constexpr int kMaxWStages = 8;
+constexpr int kMaxXStages = 8;
+constexpr int kMaxDBufs = 8;
+constexpr int kRing = 200 * 1024;           // shared memory of both rings
+constexpr size_t kCounterBytes = 1024;      // workspace: one counter per CTA, then the partial sums
+static_assert(kMaxCtas * 4 <= kCounterBytes, "one counter per CTA");
+
+struct I4Params {
+  int R, V, d, group, group_log;
+  int ntv, nk;              // tiles of the vocabulary, weight stages of the width
+  int units;                // row blocks * ntv * nk
+  int per_job;              // groups whose D_g are handed to the epilogue together
+  int jobs;                 // jobs per chunk
+  int dbufs;                // accumulator buffers of per_job * N columns
+  int wstages, xstages;
+  long long scales_ld, zeros_ld, out_ld;
+  const unsigned short* scales;
+  const unsigned char* zeros;
+  void* out;
+  int out_bf16;
+  int* counters;
+  float* partials;          // [2 * CTAs][N][128]
+  int* error_word;
+};
+
+// Wait that every role shares: gives up when the bound is reached or another
+// role did, so that all of them leave.
+__device__ __forceinline__ bool i4_wait(uint64_t* bar, unsigned parity, volatile int* fault) {
+  for (int i = 0; i < kMaxPolls; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*fault) return false;
+  }
+  *fault = 1;
+  return false;
+}
+// The same by a whole warp, which decides together.
+__device__ __forceinline__ bool i4_wait_warp(uint64_t* bar, unsigned parity, volatile int* fault) {
+  return __all_sync(0xffffffffu, i4_wait(bar, parity, fault));
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]^T, M = 128, N x 16, bfloat16 in, float32 out.
+__device__ __forceinline__ void umma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                             bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1 : 0)
+      : "memory");
+}
+
+// 32 columns of this warp's 32 lanes from 32 registers.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 8 codes (one word, columns ascending from the low nibble) -> 4 packed pairs
+// of q - z in bfloat16.  0x4300 | q is 128 + q exactly, and (128 + q) -
+// (128 + z) is exact; `base` holds 128 + z twice.
+__device__ __forceinline__ void unpack8(uint32_t w, uint32_t base, uint32_t* out) {
+  const uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu;
+  const uint32_t a = __byte_perm(even, odd, 0x5140);  // codes 0, 1, 2, 3
+  const uint32_t b = __byte_perm(even, odd, 0x7362);  // codes 4, 5, 6, 7
+  const uint32_t k = 0x43434343u;
+  uint32_t p[4] = {__byte_perm(a, k, 0x4140), __byte_perm(a, k, 0x4342), __byte_perm(b, k, 0x4140),
+                   __byte_perm(b, k, 0x4342)};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(out[i]) : "r"(p[i]), "r"(base));
+}
+
+// Place in the CTA's list of units: tile vt of row block rb, weight stage k.
+struct Cursor {
+  int rb, vt, k;
+  __device__ __forceinline__ void set(int u, const I4Params& P) {
+    const int t = u / P.nk;
+    k = u - t * P.nk;
+    rb = t / P.ntv;
+    vt = t - rb * P.ntv;
+  }
+  __device__ __forceinline__ void next(const I4Params& P) {
+    if (++k == P.nk) {
+      k = 0;
+      if (++vt == P.ntv) {
+        vt = 0;
+        ++rb;
+      }
+    }
+  }
+};
+
+// first unit of CTA c of G
+__host__ __device__ __forceinline__ int first_unit(int c, int G, int units) {
+  return static_cast<int>(static_cast<long long>(c) * units / G);
+}
+
+template <int N>
+struct Shape {
+  static constexpr int kEpiGroups = N == 128 ? 2 : 1;
+  static constexpr int kUnpackGroups = 3 - kEpiGroups;
+  static constexpr int kCols = N / kEpiGroups;           // rows of x per epilogue thread
+  static constexpr int kXBytes = N * kChunkK * 2;        // one chunk of the rows: two 64-column blocks
+  static constexpr int kLd = kCols == 32 ? 32 : 16;      // tensor-memory columns per load (64 sums leave registers for 16)
+};
+
+template <int N>
+__global__ void __launch_bounds__(kI4Threads, 1)
+    int4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                        const I4Params P) {
+  using S = Shape<N>;
+  extern __shared__ __align__(1024) unsigned char i4_dyn[];
+  __shared__ uint64_t wfull[kMaxWStages], wempty[kMaxWStages], xfull[kMaxXStages], xempty[kMaxXStages];
+  __shared__ uint64_t afull[kASlots], aempty[kASlots], dfull[kMaxDBufs], dempty[kMaxDBufs], drain, joint;
+  __shared__ uint32_t tmem_s;
+  __shared__ int fault_s, last_s, w_issued_s, x_issued_s;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  unsigned char* wring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(i4_dyn) + 1023) &
+                                                          ~static_cast<uintptr_t>(1023));
+  unsigned char* xring = wring + static_cast<size_t>(P.wstages) * kStageBytes;
+  const int G = gridDim.x, cta = blockIdx.x;
+  const int u0 = first_unit(cta, G, P.units), u1 = first_unit(cta + 1, G, P.units);
+  volatile int* fault = &fault_s;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < P.wstages; ++s) {
+      mbar_init(&wfull[s], 1);
+      mbar_init(&wempty[s], 4 * S::kUnpackGroups);
+    }
+    for (int s = 0; s < P.xstages; ++s) {
+      mbar_init(&xfull[s], 1);
+      mbar_init(&xempty[s], 1);
+    }
+    for (int s = 0; s < kASlots; ++s) {
+      mbar_init(&afull[s], 4);
+      mbar_init(&aempty[s], 1);
+    }
+    for (int s = 0; s < P.dbufs; ++s) {
+      mbar_init(&dfull[s], 1);
+      mbar_init(&dempty[s], 4 * S::kEpiGroups);
+    }
+    mbar_init(&drain, 1);
+    mbar_init(&joint, 4 * S::kEpiGroups);
+    fault_s = 0;
+    w_issued_s = 0;
+    x_issued_s = 0;
+    mbar_fence_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_s, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_a = tmem_s, tmem_d = tmem_s + kASlots * kACols;
+
+  if (warp == 0) {
+    // ---------------- weight stages ----------------
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_w);
+      Cursor c;
+      c.set(u0, P);
+      const int per_stage = kStageK / P.group;
+      for (int u = u0; u < u1; ++u, c.next(P)) {
+        const int it = u - u0, s = it % P.wstages;
+        if (!i4_wait(&wempty[s], (static_cast<unsigned>(it / P.wstages) & 1u) ^ 1u, fault)) break;
+        mbar_expect_tx(&wfull[s], kStageBytes);
+        tma_load_2d(wring + static_cast<size_t>(s) * kStageBytes, &tm_w, c.k * (kStageK / 2), c.vt * kTileV,
+                    &wfull[s]);
+        w_issued_s = it + 1;
+        const int v0 = c.vt * kTileV, vl = min(P.V - 1, v0 + kTileV - 1);
+        for (int i = 0; i < per_stage; ++i) {
+          const long long g = c.k * per_stage + i;
+          if (g * P.group >= P.d) break;
+          const unsigned short* sp = P.scales + g * P.scales_ld;
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(sp + v0));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(sp + min(v0 + 64, vl)));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(sp + vl));
+          if (P.zeros) {
+            const unsigned char* zp = P.zeros + g * P.zeros_ld;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(zp + v0));
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(zp + vl));
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------- MMAs ----------------
+    if (lane == 0) {
+      const uint32_t idesc = umma_idesc_bf16_f32(kTileV, N);
+      const int ksteps = P.group / 16;
+      int chunk = 0, job = 0;
+      Cursor c;
+      c.set(u0, P);
+      bool ok = true;
+      for (int u = u0; u < u1 && ok; ++u, c.next(P)) {
+        for (int h = 0; h < kStageK / kChunkK && ok; ++h, ++chunk) {
+          const int as = chunk % kASlots, xs = chunk % P.xstages;
+          ok = i4_wait(&xfull[xs], static_cast<unsigned>(chunk / P.xstages) & 1u, fault) &&
+               i4_wait(&afull[as], static_cast<unsigned>(chunk / kASlots) & 1u, fault);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t dx = umma_desc_sw128(smem_addr(xring + static_cast<size_t>(xs) * S::kXBytes));
+          const uint32_t a = tmem_a + as * kACols;
+          const int left = P.d - (c.k * kStageK + h * kChunkK);  // columns of the chunk inside the width
+          int ks = 0;                                            // K step of 16 within the chunk
+          for (int j = 0; j < P.jobs; ++j, ++job) {
+            const int b = job % P.dbufs;
+            ok = i4_wait(&dempty[b], (static_cast<unsigned>(job / P.dbufs) & 1u) ^ 1u, fault);
+            if (!ok) break;
+            tc_fence_after();
+            for (int g = 0; g < P.per_job; ++g) {
+              const uint32_t dst = tmem_d + (b * P.per_job + g) * N;
+              for (int k = 0; k < ksteps; ++k, ++ks) {
+                // K step ks: 8 columns of A; of the rows' block ks / 4, 32 bytes further per step
+                if (ks * 16 < left)
+                  umma_bf16_ta(dst, a + ks * 8, dx + static_cast<uint64_t>((ks >> 2) * (N * 128 >> 4) + (ks & 3) * 2),
+                               idesc, k > 0);
+              }
+            }
+            umma_commit(&dfull[b]);
+          }
+          umma_commit(&aempty[as]);
+          umma_commit(&xempty[xs]);
+        }
+      }
+      // every MMA issued has completed before tensor memory is released
+      umma_commit(&drain);
+      mbar_wait(&drain, 0);
+    }
+  } else if (warp == 2) {
+    // ---------------- the rows' chunks ----------------
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_x);
+      int chunk = 0;
+      Cursor c;
+      c.set(u0, P);
+      bool ok = true;
+      for (int u = u0; u < u1 && ok; ++u, c.next(P)) {
+        for (int h = 0; h < kStageK / kChunkK; ++h, ++chunk) {
+          const int s = chunk % P.xstages;
+          ok = i4_wait(&xempty[s], (static_cast<unsigned>(chunk / P.xstages) & 1u) ^ 1u, fault);
+          if (!ok) break;
+          unsigned char* st = xring + static_cast<size_t>(s) * S::kXBytes;
+          const int k = c.k * kStageK + h * kChunkK;
+          mbar_expect_tx(&xfull[s], S::kXBytes);
+          tma_load_2d(st, &tm_x, k, c.rb * N, &xfull[s]);
+          tma_load_2d(st + N * 128, &tm_x, k + 64, c.rb * N, &xfull[s]);
+          x_issued_s = chunk + 1;
+        }
+      }
+    }
+  } else if (warp >= 4 && warp < 4 + 4 * S::kUnpackGroups) {
+    // ---------------- unpacking ----------------
+    const int grp = (warp - 4) >> 2, q = warp & 3;
+    const int row = q * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
+    Cursor c, cn;  // this unit, and the one whose zero points are loaded ahead
+    c.set(u0, P);
+    uint32_t zero[4] = {0x43084308u, 0x43084308u, 0x43084308u, 0x43084308u};
+    uint32_t znext[4] = {0x43084308u, 0x43084308u, 0x43084308u, 0x43084308u};
+    // zero points of the 4 x 32 columns of one chunk, as 128 + z twice
+    const auto load_zeros = [&](const Cursor& at, int h, uint32_t (&z)[4]) {
+      if (!P.zeros) return;
+      const int v = at.vt * kTileV + row;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int k = at.k * kStageK + h * kChunkK + i * 32;
+        if (v < P.V && k < P.d)
+          z[i] = (0x4300u | __ldg(P.zeros + static_cast<long long>(k >> P.group_log) * P.zeros_ld + v)) * 0x10001u;
+      }
+    };
+    const int h_first = S::kUnpackGroups == 2 ? grp : 0;
+    const int h_step = S::kUnpackGroups;
+    load_zeros(c, h_first, zero);
+    bool ok = true;
+    for (int u = u0; u < u1 && ok; ++u, c.next(P)) {
+      const int it = u - u0, s = it % P.wstages;
+      for (int h = h_first; h < kStageK / kChunkK; h += h_step) {
+        // the next chunk's zero points
+        cn = c;
+        int hn = h + h_step;
+        if (hn >= kStageK / kChunkK) {
+          cn.next(P);
+          hn = h_first;
+        }
+        if (u + 1 < u1 || hn > h) load_zeros(cn, hn, znext);
+        const int chunk = it * (kStageK / kChunkK) + h;
+        const int as = chunk % kASlots;
+        if (h == h_first) {
+          ok = i4_wait_warp(&wfull[s], static_cast<unsigned>(it / P.wstages) & 1u, fault);
+          if (!ok) break;
+        }
+        const unsigned char* src = wring + static_cast<size_t>(s) * kStageBytes + row * (kStageK / 2);
+        uint4 w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = lds16(src + (((h * 4 + i) ^ (row & 7)) << 4));
+        if (h + h_step >= kStageK / kChunkK) {  // this warp's last read of the stage
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&wempty[s]);
+        }
+        ok = i4_wait_warp(&aempty[as], (static_cast<unsigned>(chunk / kASlots) & 1u) ^ 1u, fault);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t r[32];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint4 x = w[2 * i + j];
+            const uint32_t z = zero[2 * i + j];
+            unpack8(x.x, z, r + 16 * j);
+            unpack8(x.y, z, r + 16 * j + 4);
+            unpack8(x.z, z, r + 16 * j + 8);
+            unpack8(x.w, z, r + 16 * j + 12);
+          }
+          tmem_st32(tmem_a + as * kACols + lanes + 32 * i, r);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&afull[as]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) zero[i] = znext[i];
+      }
+    }
+  } else if (warp >= 4 + 4 * S::kUnpackGroups) {
+    // ---------------- epilogue ----------------
+    const int grp = (warp - 4 - 4 * S::kUnpackGroups) >> 2, q = warp & 3;
+    const int row = q * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
+    const int col0 = grp * S::kCols;
+    const int per_chunk = kChunkK / P.group;  // 1, 2 or 4 groups
+    // a barrier of the epilogue warps that gives up with the others
+    unsigned met = 0;
+    const auto meet = [&] {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&joint);
+      const bool all = i4_wait_warp(&joint, met & 1u, fault);
+      ++met;
+      return all;
+    };
+    float2 acc[S::kCols / 2];
+#pragma unroll
+    for (int i = 0; i < S::kCols / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+    Cursor c, ca;
+    c.set(u0, P);
+    ca = c;
+    int ha = 0, ua = u0;  // the chunk whose scales are loaded next
+    float s0[4], s1[4], s2[4];
+    const auto load_scales = [&](float (&s)[4]) {
+      const int v = ca.vt * kTileV + row;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[i] = 0.f;
+        const int k = ca.k * kStageK + ha * kChunkK + i * P.group;
+        if (i < per_chunk && ua < u1 && v < P.V && k < P.d)
+          s[i] = load_elem(P.scales + static_cast<long long>(k >> P.group_log) * P.scales_ld + v);
+      }
+      if (++ha == kStageK / kChunkK) {
+        ha = 0;
+        ++ua;
+        ca.next(P);
+      }
+    };
+    load_scales(s0);
+    load_scales(s1);
+    int job = 0;
+    int begin = c.k;  // first weight stage of the sums in hand
+    bool ok = true;
+    for (int u = u0; u < u1 && ok; ++u) {
+      for (int h = 0; h < kStageK / kChunkK && ok; ++h) {
+        load_scales(s2);
+        const int left = P.d - (c.k * kStageK + h * kChunkK);
+        for (int j = 0; j < P.jobs; ++j, ++job) {
+          const int b = job % P.dbufs;
+          ok = i4_wait_warp(&dfull[b], static_cast<unsigned>(job / P.dbufs) & 1u, fault);
+          if (!ok) break;
+          tc_fence_after();
+          for (int g = 0; g < P.per_job; ++g) {
+            const int gi = j * P.per_job + g;
+            if (gi * P.group >= left) break;
+            const float s = gi == 0 ? s0[0] : gi == 1 ? s0[1] : gi == 2 ? s0[2] : s0[3];
+            const float2 ss = make_float2(s, s);
+            const uint32_t src = tmem_d + (b * P.per_job + g) * N + col0 + lanes;
+#pragma unroll
+            for (int i = 0; i < S::kCols; i += S::kLd) {
+              float v[S::kLd];
+              if constexpr (S::kLd == 32) tmem_ld32(src + i, v);
+              else tmem_ld16(src + i, v);
+#pragma unroll
+              for (int e = 0; e < S::kLd; e += 2)
+                acc[(i + e) / 2] = ffma2(ss, make_float2(v[e], v[e + 1]), acc[(i + e) / 2]);
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&dempty[b]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s0[i] = s1[i];
+          s1[i] = s2[i];
+        }
+      }
+      if (!ok) break;
+      const bool whole_end = c.k + 1 == P.nk;
+      if (whole_end || u + 1 == u1) {
+        const int tile = c.rb * P.ntv + c.vt;
+        const int tu0 = tile * P.nk, tu1 = tu0 + P.nk;  // the tile's units
+        bool write = true;
+        if (begin != 0 || !whole_end) {
+          // shared: leave the sums in this CTA's slot; the last to arrive adds all of them
+          int first = static_cast<int>(static_cast<long long>(tu0) * G / P.units);  // CTA of the tile's first unit
+          while (first_unit(first + 1, G, P.units) <= tu0) ++first;
+          while (first_unit(first, G, P.units) > tu0) --first;
+          int last = first;
+          while (first_unit(last + 1, G, P.units) < tu1) ++last;
+          const int slot = 2 * cta + (begin == 0 ? 1 : 0);
+          float* mine = P.partials + (static_cast<long long>(slot) * N + col0) * kTileV + row;
+#pragma unroll
+          for (int i = 0; i < S::kCols / 2; ++i) {
+            __stcg(mine + (2 * i) * kTileV, acc[i].x);
+            __stcg(mine + (2 * i + 1) * kTileV, acc[i].y);
+          }
+          __threadfence();
+          ok = meet();
+          if (!ok) break;
+          if (threadIdx.x == kI4Threads - 1) {
+            // the counter wraps to zero with the last arrival: the workspace is as it was
+            __threadfence();
+            last_s = atomicInc(reinterpret_cast<unsigned*>(P.counters + first),
+                               static_cast<unsigned>(last - first)) == static_cast<unsigned>(last - first);
+          }
+          ok = meet();
+          if (!ok) break;
+          write = last_s != 0;
+          if (write) {
+            __threadfence();
+#pragma unroll
+            for (int i = 0; i < S::kCols / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+            for (int o = first; o <= last; ++o) {
+              const int os = 2 * o + (o == first ? 1 : 0);
+              const float* src = P.partials + (static_cast<long long>(os) * N + col0) * kTileV + row;
+#pragma unroll
+              for (int i = 0; i < S::kCols / 2; ++i) {
+                acc[i].x = __fadd_rn(acc[i].x, __ldcg(src + (2 * i) * kTileV));
+                acc[i].y = __fadd_rn(acc[i].y, __ldcg(src + (2 * i + 1) * kTileV));
+              }
+            }
+          }
+        }
+        const int v = c.vt * kTileV + row;
+        if (write && v < P.V) {
+          const int r0 = c.rb * N + col0;
+          const long long at = static_cast<long long>(r0) * P.out_ld + v;
+#pragma unroll
+          for (int i = 0; i < S::kCols; ++i) {
+            if (r0 + i >= P.R) break;
+            const float y = (i & 1) ? acc[i / 2].y : acc[i / 2].x;
+            if (P.out_bf16) {
+              unsigned short bits;
+              asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(bits) : "f"(y));
+              static_cast<unsigned short*>(P.out)[at + i * P.out_ld] = bits;
+            } else {
+              static_cast<float*>(P.out)[at + i * P.out_ld] = y;
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < S::kCols / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+        begin = 0;
+      }
+      c.next(P);
+    }
+  }
+
+  __syncthreads();
+  if (*fault && threadIdx.x == 0) {
+    // copies still in flight land before the CTA exits: wait (bounded) for
+    // the last phase of every stage that was issued
+    for (int k = max(0, w_issued_s - P.wstages); k < w_issued_s; ++k)
+      mbar_wait(&wfull[k % P.wstages], static_cast<unsigned>(k / P.wstages) & 1u);
+    for (int k = max(0, x_issued_s - P.xstages); k < x_issued_s; ++k)
+      mbar_wait(&xfull[k % P.xstages], static_cast<unsigned>(k / P.xstages) & 1u);
+    if (P.error_word) atomicOr(P.error_word, SPEC_ERR_INTERNAL);
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_s, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+bool good_shape(int R, int V, int d, int group) {
+  return R >= 1 && R <= 65535 && V >= 1 && V <= 2097152 && (group == 32 || group == 64 || group == 128) && d >= 32 &&
+         d <= 65536 && d % group == 0;
+}
+
+// MMA N: the rows of a block, rounded up to a width that has a kernel
+int rows_tile(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128; }
+
+size_t product_workspace(int R) {
+  return kCounterBytes + static_cast<size_t>(2) * kMaxCtas * rows_tile(R) * kTileV * sizeof(float);
+}
+
+// Packed weights [V, d / 2] bytes: boxes of 128 entries x 128 bytes, 128-byte swizzle, zeros outside.
+bool weight_map(CUtensorMap* map, const void* base, int V, int d, long long ld) {
+  EncodeTiled fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(d / 2), static_cast<cuuint64_t>(V)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
+  const cuuint32_t box[2] = {kStageK / 2, kTileV};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows [R, d] bfloat16: boxes of N rows x 64 columns, 128-byte swizzle, zeros outside.
+bool rows_map(CUtensorMap* map, const void* base, int R, int d, long long ld, int N) {
+  EncodeTiled fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(R)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(N)};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The kernel's dynamic shared memory limit, raised once per device.
+template <int N>
+cudaError_t raise_smem() {
+  static std::mutex mu;
+  static std::map<int, bool> done;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mu);
+  if (done.count(dev)) return cudaSuccess;
+  e = cudaFuncSetAttribute(int4_product_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing + 1024);
+  if (e == cudaSuccess) done[dev] = true;
+  return e;
+}
+
+template <int N>
+spec_status launch_product(const spec_int4_product_args& a, cudaStream_t s) {
+  using S = Shape<N>;
+  I4Params P{};
+  P.R = a.R;
+  P.V = a.V;
+  P.d = a.d;
+  P.group = a.group;
+  P.group_log = a.group == 32 ? 5 : a.group == 64 ? 6 : 7;
+  P.ntv = (a.V + kTileV - 1) / kTileV;
+  P.nk = (a.d + kStageK - 1) / kStageK;
+  const long long units = static_cast<long long>((a.R + N - 1) / N) * P.ntv * P.nk;
+  if (units > 0x3fffffff) return SPEC_EINVAL;
+  P.units = static_cast<int>(units);
+  // groups handed over together: as many of a chunk's as leave two buffers
+  P.per_job = kChunkK / a.group;
+  while (2 * P.per_job * N > kDCols) P.per_job /= 2;
+  P.jobs = kChunkK / (a.group * P.per_job);
+  P.dbufs = min(kMaxDBufs, kDCols / (P.per_job * N));
+  // the rows' ring: enough chunks to cover L2's latency; the rest goes to the
+  // weights, whose latency is HBM's
+  P.xstages = min(kMaxXStages, max(3, 48 * 1024 / S::kXBytes));
+  P.wstages = min(kMaxWStages, (kRing - P.xstages * S::kXBytes) / kStageBytes);
+  P.scales_ld = a.scales_ld;
+  P.zeros_ld = a.zeros_ld;
+  P.out_ld = a.out_ld;
+  P.scales = static_cast<const unsigned short*>(a.scales);
+  P.zeros = a.zeros;
+  P.out = a.out;
+  P.out_bf16 = a.out_dtype == SPEC_BF16;
+  P.counters = static_cast<int*>(a.workspace);
+  P.partials = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kCounterBytes);
+  P.error_word = a.error_word;
+  const int nsm = sm_count();
+  if (nsm < 1) return SPEC_ECUDA;
+  const int ctas = min(min(nsm, kMaxCtas), P.units);
+  CUtensorMap tw, tx;
+  if (!weight_map(&tw, a.codes, a.V, a.d, a.codes_ld) || !rows_map(&tx, a.x, a.R, a.d, a.x_ld, N)) return SPEC_ECUDA;
+  if (raise_smem<N>() != cudaSuccess) return SPEC_ECUDA;
+  const int dyn = P.wstages * kStageBytes + P.xstages * S::kXBytes + 1024;
+  int4_product_kernel<N><<<ctas, kI4Threads, dyn, s>>>(tw, tx, P);
+  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
+}
+
+}  // namespace
+}  // namespace sv
+
+extern "C" size_t spec_int4_product_workspace_size(int R, int V, int d, int group) {
+  return sv::good_shape(R, V, d, group) ? sv::product_workspace(R) : 0;
+}
+
+extern "C" spec_status spec_int4_product(const spec_int4_product_args* a, cudaStream_t stream) {
+  using namespace sv;
+  NvtxRange nvtx_range("spec_int4_product");
+  if (a == nullptr) return SPEC_EINVAL;
+  if (a->out_dtype != SPEC_F32 && a->out_dtype != SPEC_BF16) return SPEC_EDTYPE;
+  if (!good_shape(a->R, a->V, a->d, a->group)) return SPEC_EINVAL;
+  if (!a->x || !a->codes || !a->scales || !a->out) return SPEC_EINVAL;
+  if (a->x_ld < a->d || a->x_ld % 8 || a->codes_ld < a->d / 2 || a->codes_ld % 16) return SPEC_EINVAL;
+  if (a->scales_ld < a->V || a->out_ld < a->V || (a->zeros && a->zeros_ld < a->V)) return SPEC_EINVAL;
+  if (!aligned(a->x, 16) || !aligned(a->codes, 16) || !aligned(a->scales, 2) ||
+      !aligned(a->out, a->out_dtype == SPEC_F32 ? 4 : 2))
+    return SPEC_EALIGN;
+  if (!a->workspace || a->workspace_bytes < product_workspace(a->R) || !aligned(a->workspace, 256))
+    return SPEC_EWORKSPACE;
+  switch (rows_tile(a->R)) {
+    case 16: return launch_product<16>(*a, stream);
+    case 32: return launch_product<32>(*a, stream);
+    case 64: return launch_product<64>(*a, stream);
+    default: return launch_product<128>(*a, stream);
+  }
+}

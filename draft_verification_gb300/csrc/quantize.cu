@@ -1,5 +1,6 @@
-// 4-bit weights with group scales (the layout is in spec_logits.h): their
-// quantisation and their products with a few bfloat16 rows.
+// Quantisation to 4-bit weights with group scales (the rule and the layout are
+// in spec_logits.h).
+//
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -13,9 +14,6 @@ namespace {
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// ---------------------------------------------------------------------------
-// quantisation
-// ---------------------------------------------------------------------------
 // A warp takes 256 columns of one row at a time, 8 consecutive ones per lane,
 // so a group is 4, 8 or 16 neighbouring lanes: its extremes come from three
 // to four shuffles, every weight is read once and a lane's 8 codes are one
@@ -163,63 +161,6 @@ cudaError_t launch_quantize(const QuantParams& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// ---------------------------------------------------------------------------
-// products
-// ---------------------------------------------------------------------------
-// A warp owns one vocabulary entry and 8 rows; a lane takes 8 consecutive
-// columns at a time (one 32-bit word of codes, inside one group).
-constexpr int kProdThreads = 256;
-constexpr int kProdRows = 8;
-
-struct ProductParams {
-  int R, V, d, group;
-  long long x_ld, codes_ld, scales_ld, zeros_ld, out_ld;
-  const bf16_t* x;
-  const unsigned char* codes;
-  const unsigned short* scales;
-  const unsigned char* zeros;
-  void* out;
-};
-
-template <typename T>
-__global__ void __launch_bounds__(kProdThreads) product_kernel(const ProductParams P) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int v = static_cast<int>(blockIdx.x) * (kProdThreads / 32) + warp;
-  if (v >= P.V) return;
-  const int r0 = static_cast<int>(blockIdx.y) * kProdRows;
-  float acc[kProdRows];
-#pragma unroll
-  for (int r = 0; r < kProdRows; ++r) acc[r] = 0.f;
-  for (int k = lane * 8; k < P.d; k += 256) {
-    const int g = k / P.group;
-    const uint32_t c = __ldg(reinterpret_cast<const uint32_t*>(P.codes + v * P.codes_ld + (k >> 1)));
-    const float s = __uint_as_float(static_cast<uint32_t>(__ldg(P.scales + g * P.scales_ld + v)) << 16);
-    const int z = P.zeros ? __ldg(P.zeros + g * P.zeros_ld + v) : 8;
-#pragma unroll
-    for (int r = 0; r < kProdRows; ++r) {
-      if (r0 + r >= P.R) break;
-      const uint4 x = ld16(P.x + (r0 + r) * P.x_ld + k);
-      const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-      float sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float q = static_cast<float>(static_cast<int>((c >> (4 * j)) & 15u) - z);
-        sum = __fmaf_rn(q, (j & 1) ? bf16_hi(u[j >> 1]) : bf16_lo(u[j >> 1]), sum);
-      }
-      acc[r] = __fmaf_rn(s, sum, acc[r]);
-    }
-  }
-#pragma unroll
-  for (int r = 0; r < kProdRows; ++r) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) acc[r] = __fadd_rn(acc[r], __shfl_xor_sync(0xffffffffu, acc[r], o));
-    if (lane == 0 && r0 + r < P.R) {
-      if constexpr (sizeof(T) == 2) static_cast<unsigned short*>(P.out)[(r0 + r) * P.out_ld + v] = to_bf16(acc[r]);
-      else static_cast<float*>(P.out)[(r0 + r) * P.out_ld + v] = acc[r];
-    }
-  }
-}
-
 bool good_shape(int V, int d, int group) {
   return V >= 1 && V <= 2097152 && (group == 32 || group == 64 || group == 128) && d >= 32 && d <= 65536 &&
          d % group == 0;
@@ -254,45 +195,4 @@ extern "C" spec_status spec_quantize_int4(const spec_quantize_int4_args* a, cuda
   const cudaError_t e =
       a->dtype == SPEC_BF16 ? launch_quantize<bf16_t>(p, stream) : launch_quantize<float>(p, stream);
   return e == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
-}
-
-extern "C" size_t spec_int4_product_workspace_size(int R, int V, int d, int group) {
-  if (R < 1 || R > 65535 || !sv::good_shape(V, d, group)) return 0;
-  return 256;
-}
-
-extern "C" spec_status spec_int4_product(const spec_int4_product_args* a, cudaStream_t stream) {
-  using namespace sv;
-  NvtxRange nvtx_range("spec_int4_product");
-  if (a == nullptr) return SPEC_EINVAL;
-  if (a->out_dtype != SPEC_F32 && a->out_dtype != SPEC_BF16) return SPEC_EDTYPE;
-  if (a->R < 1 || a->R > 65535 || !good_shape(a->V, a->d, a->group)) return SPEC_EINVAL;
-  if (!a->x || !a->codes || !a->scales || !a->out) return SPEC_EINVAL;
-  if (a->x_ld < a->d || a->x_ld % 8 || a->codes_ld < a->d / 2 || a->codes_ld % 16) return SPEC_EINVAL;
-  if (a->scales_ld < a->V || a->out_ld < a->V || (a->zeros && a->zeros_ld < a->V)) return SPEC_EINVAL;
-  if (!aligned(a->x, 16) || !aligned(a->codes, 16) || !aligned(a->scales, 2) ||
-      !aligned(a->out, a->out_dtype == SPEC_F32 ? 4 : 2))
-    return SPEC_EALIGN;
-  if (!a->workspace || a->workspace_bytes < spec_int4_product_workspace_size(a->R, a->V, a->d, a->group) ||
-      !aligned(a->workspace, 256))
-    return SPEC_EWORKSPACE;
-  ProductParams p{};
-  p.R = a->R;
-  p.V = a->V;
-  p.d = a->d;
-  p.group = a->group;
-  p.x_ld = a->x_ld;
-  p.codes_ld = a->codes_ld;
-  p.scales_ld = a->scales_ld;
-  p.zeros_ld = a->zeros_ld;
-  p.out_ld = a->out_ld;
-  p.x = static_cast<const bf16_t*>(a->x);
-  p.codes = static_cast<const unsigned char*>(a->codes);
-  p.scales = static_cast<const unsigned short*>(a->scales);
-  p.zeros = a->zeros;
-  p.out = a->out;
-  const dim3 grid(static_cast<unsigned>((a->V + 7) / 8), static_cast<unsigned>((a->R + kProdRows - 1) / kProdRows));
-  if (a->out_dtype == SPEC_BF16) product_kernel<bf16_t><<<grid, kProdThreads, 0, stream>>>(p);
-  else product_kernel<float><<<grid, kProdThreads, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
 }

@@ -183,7 +183,8 @@ class Int4ProductPlan(_Plan):
     spec_int4_product.
 
     x bfloat16 [R, d] (or [B, n, d]), codes, scales and zeros as
-    quantize_int4 returns them (rows of codes and x may be padded).  ``run()``
+    quantize_int4 returns them (rows of codes and x may be padded).  A workspace
+    that the caller passes must hold zeros before its first use.  ``run()``
     returns logits [R, V] (or [B, n, V]) of out_dtype and error_word."""
 
     def __init__(self, x, codes, scales, zeros=None, *, group=128, out_dtype=torch.bfloat16, out=None,
@@ -221,7 +222,7 @@ class Int4ProductPlan(_Plan):
         out_ld = _logit_rows(out, "out") if out.dim() == 3 else _matrix_ld(out, "out")
         _on(dev, codes=codes, scales=scales, zeros=zeros, out=out)
         if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace = torch.zeros(need, dtype=torch.uint8, device=dev)
         self.workspace = workspace
         self.keep = [x, codes, scales, zeros]
         self.out = dict(logits=out, error_word=torch.zeros(1, dtype=torch.int32, device=dev))

@@ -149,6 +149,11 @@ spec_status spec_quantize_int4(const spec_quantize_int4_args* args, cudaStream_t
 /* rounded once to its type.                                               */
 /*  - Rows cost little until the products bound the call: up to 128 rows   */
 /*    share one pass over the weights; more rows take further passes.      */
+/*  - One kernel launch of at most one CTA per SM.  An entry whose width is */
+/*    shared by several CTAs is summed in the order of the columns.        */
+/*  - Workspace: its first 1024 bytes must be zero before its first use    */
+/*    (and again after a call that reported SPEC_ERR_INTERNAL); a call     */
+/*    leaves them zero, so calls that follow one another may share it.     */
 /* ---------------------------------------------------------------------- */
 typedef struct spec_int4_product_args {
   int R;                       /* rows, 1..65535                                   */
