@@ -47,29 +47,20 @@ namespace sv {
 namespace {
 
 constexpr int kTileV = 128;                 // vocabulary entries per tile (MMA M)
-constexpr int kStageK = 256;                // columns of a weight stage: 128 packed bytes per entry
-constexpr int kChunkK = 128;                // columns of a chunk: what one A slot holds
+constexpr int kStageK = 256;                // columns of a stage (a unit): 128 packed bytes per entry
 constexpr int kStageBytes = kTileV * kStageK / 2;
-constexpr int kASlots = 4;                  // A ring: 4 x 64 tensor-memory columns
-constexpr int kACols = kChunkK / 2;
-constexpr int kDCols = 256;                 // accumulators: the other 256 columns
+constexpr int kSlots = 4;                   // chunks in flight between unpacking and epilogue
+constexpr int kACols = 256;                 // tensor memory: the chunks' weights, then the accumulators
+constexpr int kDCols = 256;
 constexpr int kMaxCtas = 152;               // persistent CTAs the workspace is sized for
 constexpr int kI4Threads = 512;
-constexpr int kMaxWStages = 8;
-constexpr int kMaxXStages = 8;
-constexpr int kMaxDBufs = 8;
-constexpr int kRing = 200 * 1024;           // shared memory of both rings
 constexpr size_t kCounterBytes = 1024;      // workspace: one counter per CTA, then the partial sums
 static_assert(kMaxCtas * 4 <= kCounterBytes, "one counter per CTA");
 
 struct I4Params {
-  int R, V, d, group, group_log;
-  int ntv, nk;              // tiles of the vocabulary, weight stages of the width
+  int R, V, d;
+  int ntv, nk;              // tiles of the vocabulary, stages of the width
   int units;                // row blocks * ntv * nk
-  int per_job;              // groups whose D_g are handed to the epilogue together
-  int jobs;                 // jobs per chunk
-  int dbufs;                // accumulator buffers of per_job * N columns
-  int wstages, xstages;
   long long scales_ld, zeros_ld, out_ld;
   const unsigned short* scales;
   const unsigned char* zeros;
@@ -78,6 +69,40 @@ struct I4Params {
   int* counters;
   float* partials;          // [2 * CTAs][N][128]
   int* error_word;
+};
+
+// N rows and groups of G columns.
+template <int N, int G>
+struct Shape {
+  static constexpr int kEpiGroups = N == 128 ? 2 : 1;    // warpgroups
+  static constexpr int kUnpackGroups = 3 - kEpiGroups;
+  static constexpr int kCols = N / kEpiGroups;           // rows of x per epilogue thread
+  // a chunk: at most 128 columns, and few enough groups that their
+  // accumulators take 128 tensor-memory columns (two buffers fit)
+  static constexpr int kChunkK = N * (128 / G) <= 128 ? 128 : 128 * G / N;
+  static constexpr int kChunks = kStageK / kChunkK;      // per unit
+  static constexpr int kGroups = kChunkK / G;            // per chunk
+  static constexpr int kDBuf = kGroups * N;              // columns of a chunk's accumulators
+  static constexpr int kDBufs = kDCols / kDBuf < kSlots ? kDCols / kDBuf : kSlots;
+  static constexpr int kXBytes = N * kStageK * 2;        // the rows' columns of a unit: four 64-column blocks
+  // the rows come from L2, the weights from HBM: the weights' ring is the deep one
+  static constexpr int kXStages = N <= 32 ? 4 : N == 64 ? 3 : 2;
+  static constexpr int kWStages = N <= 32 ? 8 : N == 64 ? 6 : 4;
+  static constexpr int kLd = kCols == 32 ? 32 : 16;      // tensor-memory columns per load
+  static constexpr int kSmem = kXStages * kXBytes + kWStages * kStageBytes + 1024;
+};
+
+// A place in a ring: slot and the parity of its current round.
+template <int kSize>
+struct Ring {
+  int slot = 0;
+  unsigned parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == kSize) {
+      slot = 0;
+      parity ^= 1u;
+    }
+  }
 };
 
 // Wait that every role shares: gives up when the bound is reached or another
@@ -114,6 +139,14 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
       "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -157,50 +190,46 @@ __host__ __device__ __forceinline__ int first_unit(int c, int G, int units) {
   return static_cast<int>(static_cast<long long>(c) * units / G);
 }
 
-template <int N>
-struct Shape {
-  static constexpr int kEpiGroups = N == 128 ? 2 : 1;
-  static constexpr int kUnpackGroups = 3 - kEpiGroups;
-  static constexpr int kCols = N / kEpiGroups;           // rows of x per epilogue thread
-  static constexpr int kXBytes = N * kChunkK * 2;        // one chunk of the rows: two 64-column blocks
-  static constexpr int kLd = kCols == 32 ? 32 : 16;      // tensor-memory columns per load (64 sums leave registers for 16)
-};
+// One lane of the warp, the same at every call.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
 
-template <int N>
+template <int N, int G>
 __global__ void __launch_bounds__(kI4Threads, 1)
     int4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                         const I4Params P) {
-  using S = Shape<N>;
+  using S = Shape<N, G>;
   extern __shared__ __align__(1024) unsigned char i4_dyn[];
-  __shared__ uint64_t wfull[kMaxWStages], wempty[kMaxWStages], xfull[kMaxXStages], xempty[kMaxXStages];
-  __shared__ uint64_t afull[kASlots], aempty[kASlots], dfull[kMaxDBufs], dempty[kMaxDBufs], drain, joint;
+  __shared__ uint64_t wfull[S::kWStages], wempty[S::kWStages], xfull[S::kXStages], xempty[S::kXStages];
+  // ready: a chunk's weights are in tensor memory and its accumulators are
+  // free; done: its products are complete (its weights' slot is free again)
+  __shared__ uint64_t ready[kSlots], done[kSlots], drain, joint;
   __shared__ uint32_t tmem_s;
   __shared__ int fault_s, last_s, w_issued_s, x_issued_s;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   unsigned char* wring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(i4_dyn) + 1023) &
                                                           ~static_cast<uintptr_t>(1023));
-  unsigned char* xring = wring + static_cast<size_t>(P.wstages) * kStageBytes;
-  const int G = gridDim.x, cta = blockIdx.x;
-  const int u0 = first_unit(cta, G, P.units), u1 = first_unit(cta + 1, G, P.units);
+  unsigned char* xring = wring + S::kWStages * kStageBytes;
+  const int ctas = gridDim.x, cta = blockIdx.x;
+  const int u0 = first_unit(cta, ctas, P.units), u1 = first_unit(cta + 1, ctas, P.units);
   volatile int* fault = &fault_s;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < P.wstages; ++s) {
+    for (int s = 0; s < S::kWStages; ++s) {
       mbar_init(&wfull[s], 1);
       mbar_init(&wempty[s], 4 * S::kUnpackGroups);
     }
-    for (int s = 0; s < P.xstages; ++s) {
+    for (int s = 0; s < S::kXStages; ++s) {
       mbar_init(&xfull[s], 1);
       mbar_init(&xempty[s], 1);
     }
-    for (int s = 0; s < kASlots; ++s) {
-      mbar_init(&afull[s], 4);
-      mbar_init(&aempty[s], 1);
-    }
-    for (int s = 0; s < P.dbufs; ++s) {
-      mbar_init(&dfull[s], 1);
-      mbar_init(&dempty[s], 4 * S::kEpiGroups);
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&ready[s], 4 + 4 * S::kEpiGroups);
+      mbar_init(&done[s], 1);
     }
     mbar_init(&drain, 1);
     mbar_init(&joint, 4 * S::kEpiGroups);
@@ -210,13 +239,13 @@ __global__ void __launch_bounds__(kI4Threads, 1)
     mbar_fence_init();
   }
   if (warp == 1) {
-    tmem_alloc(&tmem_s, 512);
+    tmem_alloc(&tmem_s, kACols + kDCols);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem_a = tmem_s, tmem_d = tmem_s + kASlots * kACols;
+  const uint32_t tmem_a = tmem_s, tmem_d = tmem_s + kACols;
 
   if (warp == 0) {
     // ---------------- weight stages ----------------
@@ -224,18 +253,17 @@ __global__ void __launch_bounds__(kI4Threads, 1)
       tma_prefetch_desc(&tm_w);
       Cursor c;
       c.set(u0, P);
-      const int per_stage = kStageK / P.group;
-      for (int u = u0; u < u1; ++u, c.next(P)) {
-        const int it = u - u0, s = it % P.wstages;
-        if (!i4_wait(&wempty[s], (static_cast<unsigned>(it / P.wstages) & 1u) ^ 1u, fault)) break;
-        mbar_expect_tx(&wfull[s], kStageBytes);
-        tma_load_2d(wring + static_cast<size_t>(s) * kStageBytes, &tm_w, c.k * (kStageK / 2), c.vt * kTileV,
-                    &wfull[s]);
-        w_issued_s = it + 1;
+      Ring<S::kWStages> w;
+      for (int u = u0; u < u1; ++u, c.next(P), w.next()) {
+        if (!i4_wait(&wempty[w.slot], w.parity ^ 1u, fault)) break;
+        mbar_expect_tx(&wfull[w.slot], kStageBytes);
+        tma_load_2d(wring + w.slot * kStageBytes, &tm_w, c.k * (kStageK / 2), c.vt * kTileV, &wfull[w.slot]);
+        w_issued_s = u - u0 + 1;
+        // the scales and zero points of the same columns, into L2
         const int v0 = c.vt * kTileV, vl = min(P.V - 1, v0 + kTileV - 1);
-        for (int i = 0; i < per_stage; ++i) {
-          const long long g = c.k * per_stage + i;
-          if (g * P.group >= P.d) break;
+        for (int i = 0; i < kStageK / G; ++i) {
+          const long long g = c.k * (kStageK / G) + i;
+          if (g * G >= P.d) break;
           const unsigned short* sp = P.scales + g * P.scales_ld;
           asm volatile("prefetch.global.L2 [%0];" ::"l"(sp + v0));
           asm volatile("prefetch.global.L2 [%0];" ::"l"(sp + min(v0 + 64, vl)));
@@ -250,151 +278,157 @@ __global__ void __launch_bounds__(kI4Threads, 1)
     }
   } else if (warp == 1) {
     // ---------------- MMAs ----------------
-    if (lane == 0) {
-      const uint32_t idesc = umma_idesc_bf16_f32(kTileV, N);
-      const int ksteps = P.group / 16;
-      int chunk = 0, job = 0;
-      Cursor c;
-      c.set(u0, P);
-      bool ok = true;
-      for (int u = u0; u < u1 && ok; ++u, c.next(P)) {
-        for (int h = 0; h < kStageK / kChunkK && ok; ++h, ++chunk) {
-          const int as = chunk % kASlots, xs = chunk % P.xstages;
-          ok = i4_wait(&xfull[xs], static_cast<unsigned>(chunk / P.xstages) & 1u, fault) &&
-               i4_wait(&afull[as], static_cast<unsigned>(chunk / kASlots) & 1u, fault);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t dx = umma_desc_sw128(smem_addr(xring + static_cast<size_t>(xs) * S::kXBytes));
-          const uint32_t a = tmem_a + as * kACols;
-          const int left = P.d - (c.k * kStageK + h * kChunkK);  // columns of the chunk inside the width
-          int ks = 0;                                            // K step of 16 within the chunk
-          for (int j = 0; j < P.jobs; ++j, ++job) {
-            const int b = job % P.dbufs;
-            ok = i4_wait(&dempty[b], (static_cast<unsigned>(job / P.dbufs) & 1u) ^ 1u, fault);
-            if (!ok) break;
-            tc_fence_after();
-            for (int g = 0; g < P.per_job; ++g) {
-              const uint32_t dst = tmem_d + (b * P.per_job + g) * N;
-              for (int k = 0; k < ksteps; ++k, ++ks) {
-                // K step ks: 8 columns of A; of the rows' block ks / 4, 32 bytes further per step
-                if (ks * 16 < left)
-                  umma_bf16_ta(dst, a + ks * 8, dx + static_cast<uint64_t>((ks >> 2) * (N * 128 >> 4) + (ks & 3) * 2),
-                               idesc, k > 0);
-              }
-            }
-            umma_commit(&dfull[b]);
+    // The whole warp keeps the loop's values, so that they stay in uniform
+    // registers, and one lane issues; everything that varies from MMA to MMA
+    // is a constant: a lone thread's instruction latency is the limit here.
+    constexpr uint32_t idesc = umma_idesc_bf16_f32(kTileV, N);
+    const bool leader = elect_one();
+    Ring<S::kXStages> x;
+    Ring<kSlots> a;
+    int db = 0;
+    bool ok = true;
+    for (int u = u0; u < u1; ++u) {
+      ok = i4_wait_warp(&xfull[x.slot], x.parity, fault);
+      if (!ok) break;
+      const uint64_t dx = umma_desc_sw128(smem_addr(xring + x.slot * S::kXBytes));
+#pragma unroll
+      for (int i = 0; i < S::kChunks; ++i) {
+        ok = i4_wait_warp(&ready[a.slot], a.parity, fault);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t at = tmem_a + a.slot * (S::kChunkK / 2), dt = tmem_d + db * S::kDBuf;
+        if (leader) {
+#pragma unroll
+          for (int k = 0; k < S::kChunkK / 16; ++k) {
+            // K step ks of the unit: 8 columns of A; of the rows' block
+            // ks / 4, 32 bytes further per step
+            const int ks = i * (S::kChunkK / 16) + k;
+            umma_bf16_ta(dt + (k * 16 / G) * N, at + k * 8,
+                         dx + static_cast<uint64_t>((ks >> 2) * (N * 128 >> 4) + (ks & 3) * 2), idesc,
+                         k * 16 % G != 0);
           }
-          umma_commit(&aempty[as]);
-          umma_commit(&xempty[xs]);
+          umma_commit(&done[a.slot]);
+          if (i + 1 == S::kChunks) umma_commit(&xempty[x.slot]);
         }
+        a.next();
+        if (++db == S::kDBufs) db = 0;
       }
-      // every MMA issued has completed before tensor memory is released
-      umma_commit(&drain);
-      mbar_wait(&drain, 0);
+      if (!ok) break;
+      x.next();
     }
+    // every MMA issued has completed before tensor memory is released
+    if (leader) umma_commit(&drain);
+    __syncwarp();
+    mbar_wait(&drain, 0);
   } else if (warp == 2) {
-    // ---------------- the rows' chunks ----------------
+    // ---------------- the rows' columns ----------------
     if (lane == 0) {
       tma_prefetch_desc(&tm_x);
-      int chunk = 0;
       Cursor c;
       c.set(u0, P);
-      bool ok = true;
-      for (int u = u0; u < u1 && ok; ++u, c.next(P)) {
-        for (int h = 0; h < kStageK / kChunkK; ++h, ++chunk) {
-          const int s = chunk % P.xstages;
-          ok = i4_wait(&xempty[s], (static_cast<unsigned>(chunk / P.xstages) & 1u) ^ 1u, fault);
-          if (!ok) break;
-          unsigned char* st = xring + static_cast<size_t>(s) * S::kXBytes;
-          const int k = c.k * kStageK + h * kChunkK;
-          mbar_expect_tx(&xfull[s], S::kXBytes);
-          tma_load_2d(st, &tm_x, k, c.rb * N, &xfull[s]);
-          tma_load_2d(st + N * 128, &tm_x, k + 64, c.rb * N, &xfull[s]);
-          x_issued_s = chunk + 1;
-        }
+      Ring<S::kXStages> x;
+      for (int u = u0; u < u1; ++u, c.next(P), x.next()) {
+        if (!i4_wait(&xempty[x.slot], x.parity ^ 1u, fault)) break;
+        unsigned char* st = xring + x.slot * S::kXBytes;
+        mbar_expect_tx(&xfull[x.slot], S::kXBytes);
+#pragma unroll
+        for (int i = 0; i < kStageK / 64; ++i)
+          tma_load_2d(st + i * N * 128, &tm_x, c.k * kStageK + i * 64, c.rb * N, &xfull[x.slot]);
+        x_issued_s = u - u0 + 1;
       }
     }
   } else if (warp >= 4 && warp < 4 + 4 * S::kUnpackGroups) {
     // ---------------- unpacking ----------------
+    // chunk i of a unit is unpacked by warpgroup i % kUnpackGroups
+    constexpr int kMine = S::kChunks / S::kUnpackGroups;  // chunks per unit
+    constexpr int kVecs = S::kChunkK / 32;                // 16-byte vectors of an entry's chunk, one zero point each
     const int grp = (warp - 4) >> 2, q = warp & 3;
     const int row = q * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
-    Cursor c, cn;  // this unit, and the one whose zero points are loaded ahead
-    c.set(u0, P);
-    uint32_t zero[4] = {0x43084308u, 0x43084308u, 0x43084308u, 0x43084308u};
-    uint32_t znext[4] = {0x43084308u, 0x43084308u, 0x43084308u, 0x43084308u};
-    // zero points of the 4 x 32 columns of one chunk, as 128 + z twice
-    const auto load_zeros = [&](const Cursor& at, int h, uint32_t (&z)[4]) {
-      if (!P.zeros) return;
-      const int v = at.vt * kTileV + row;
+    const uint32_t key = static_cast<uint32_t>(row & 7);
+    Cursor cn;  // the unit whose zero points are loaded: one ahead
+    cn.set(u0, P);
+    uint32_t zero[kMine * kVecs], znext[kMine * kVecs];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int k = at.k * kStageK + h * kChunkK + i * 32;
-        if (v < P.V && k < P.d)
-          z[i] = (0x4300u | __ldg(P.zeros + static_cast<long long>(k >> P.group_log) * P.zeros_ld + v)) * 0x10001u;
-      }
+    for (int i = 0; i < kMine * kVecs; ++i) zero[i] = znext[i] = 0x43084308u;
+    // zero points of this warpgroup's 32-column vectors of unit cn, as 128 + z twice
+    const auto load_zeros = [&](uint32_t (&z)[kMine * kVecs]) {
+      const int v = cn.vt * kTileV + row;
+#pragma unroll
+      for (int j = 0; j < kMine; ++j)
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+          const int k = cn.k * kStageK + (j * S::kUnpackGroups + grp) * S::kChunkK + i * 32;
+          if (v < P.V && k < P.d)
+            z[j * kVecs + i] = (0x4300u | __ldg(P.zeros + static_cast<long long>(k / G) * P.zeros_ld + v)) * 0x10001u;
+        }
     };
-    const int h_first = S::kUnpackGroups == 2 ? grp : 0;
-    const int h_step = S::kUnpackGroups;
-    load_zeros(c, h_first, zero);
+    if (P.zeros) load_zeros(zero);
+    Ring<S::kWStages> w;
+    Ring<kSlots> a;
+    for (int i = 0; i < grp; ++i) a.next();
     bool ok = true;
-    for (int u = u0; u < u1 && ok; ++u, c.next(P)) {
-      const int it = u - u0, s = it % P.wstages;
-      for (int h = h_first; h < kStageK / kChunkK; h += h_step) {
-        // the next chunk's zero points
-        cn = c;
-        int hn = h + h_step;
-        if (hn >= kStageK / kChunkK) {
-          cn.next(P);
-          hn = h_first;
-        }
-        if (u + 1 < u1 || hn > h) load_zeros(cn, hn, znext);
-        const int chunk = it * (kStageK / kChunkK) + h;
-        const int as = chunk % kASlots;
-        if (h == h_first) {
-          ok = i4_wait_warp(&wfull[s], static_cast<unsigned>(it / P.wstages) & 1u, fault);
-          if (!ok) break;
-        }
-        const unsigned char* src = wring + static_cast<size_t>(s) * kStageBytes + row * (kStageK / 2);
-        uint4 w[4];
+    for (int u = u0; u < u1 && ok; ++u, w.next()) {
+      cn.next(P);
+      if (P.zeros && u + 1 < u1) load_zeros(znext);
+      ok = i4_wait_warp(&wfull[w.slot], w.parity, fault);
+      if (!ok) break;
+      const unsigned char* src = wring + w.slot * kStageBytes + row * (kStageK / 2);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = lds16(src + (((h * 4 + i) ^ (row & 7)) << 4));
-        if (h + h_step >= kStageK / kChunkK) {  // this warp's last read of the stage
+      for (int j = 0; j < kMine; ++j) {
+        const int i = j * S::kUnpackGroups + grp;  // chunk of the unit
+        uint4 code[kVecs];
+#pragma unroll
+        for (int e = 0; e < kVecs; ++e) code[e] = lds16(src + (((i * kVecs + e) ^ key) << 4));
+        if (j + 1 == kMine) {  // this warp's last read of the stage
           __syncwarp();
-          if (lane == 0) mbar_arrive(&wempty[s]);
+          if (lane == 0) mbar_arrive(&wempty[w.slot]);
         }
-        ok = i4_wait_warp(&aempty[as], (static_cast<unsigned>(chunk / kASlots) & 1u) ^ 1u, fault);
+        ok = i4_wait_warp(&done[a.slot], a.parity ^ 1u, fault);
         if (!ok) break;
         tc_fence_after();
+        const uint32_t dst = tmem_a + a.slot * (S::kChunkK / 2) + lanes;
+        if constexpr (kVecs >= 2) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t r[32];
+          for (int h = 0; h < kVecs / 2; ++h) {
+            uint32_t r[32];
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint4 x = w[2 * i + j];
-            const uint32_t z = zero[2 * i + j];
-            unpack8(x.x, z, r + 16 * j);
-            unpack8(x.y, z, r + 16 * j + 4);
-            unpack8(x.z, z, r + 16 * j + 8);
-            unpack8(x.w, z, r + 16 * j + 12);
+            for (int e = 0; e < 2; ++e) {
+              const uint4 x = code[2 * h + e];
+              const uint32_t z = zero[j * kVecs + 2 * h + e];
+              unpack8(x.x, z, r + 16 * e);
+              unpack8(x.y, z, r + 16 * e + 4);
+              unpack8(x.z, z, r + 16 * e + 8);
+              unpack8(x.w, z, r + 16 * e + 12);
+            }
+            tmem_st32(dst + 32 * h, r);
           }
-          tmem_st32(tmem_a + as * kACols + lanes + 32 * i, r);
+        } else {
+          uint32_t r[16];
+          const uint32_t z = zero[j];
+          unpack8(code[0].x, z, r);
+          unpack8(code[0].y, z, r + 4);
+          unpack8(code[0].z, z, r + 8);
+          unpack8(code[0].w, z, r + 12);
+          tmem_st16(dst, r);
         }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&afull[as]);
+        if (lane == 0) mbar_arrive(&ready[a.slot]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) zero[i] = znext[i];
+        for (int n = 0; n < S::kUnpackGroups; ++n) a.next();
       }
+#pragma unroll
+      for (int i = 0; i < kMine * kVecs; ++i) zero[i] = znext[i];
     }
   } else if (warp >= 4 + 4 * S::kUnpackGroups) {
     // ---------------- epilogue ----------------
+    constexpr int kPer = kStageK / G;  // groups per unit
     const int grp = (warp - 4 - 4 * S::kUnpackGroups) >> 2, q = warp & 3;
     const int row = q * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
     const int col0 = grp * S::kCols;
-    const int per_chunk = kChunkK / P.group;  // 1, 2 or 4 groups
     // a barrier of the epilogue warps that gives up with the others
     unsigned met = 0;
     const auto meet = [&] {
@@ -407,65 +441,60 @@ __global__ void __launch_bounds__(kI4Threads, 1)
     float2 acc[S::kCols / 2];
 #pragma unroll
     for (int i = 0; i < S::kCols / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-    Cursor c, ca;
+    Cursor c, cn;
     c.set(u0, P);
-    ca = c;
-    int ha = 0, ua = u0;  // the chunk whose scales are loaded next
-    float s0[4], s1[4], s2[4];
-    const auto load_scales = [&](float (&s)[4]) {
-      const int v = ca.vt * kTileV + row;
+    cn = c;
+    // the scales of a unit's groups, loaded one unit ahead (they wait in L2)
+    float s_now[kPer], s_next[kPer] = {};
+    const auto load_scales = [&](const Cursor& at, float (&s)[kPer]) {
+      const int v = at.vt * kTileV + row;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kPer; ++i) {
         s[i] = 0.f;
-        const int k = ca.k * kStageK + ha * kChunkK + i * P.group;
-        if (i < per_chunk && ua < u1 && v < P.V && k < P.d)
-          s[i] = load_elem(P.scales + static_cast<long long>(k >> P.group_log) * P.scales_ld + v);
-      }
-      if (++ha == kStageK / kChunkK) {
-        ha = 0;
-        ++ua;
-        ca.next(P);
+        const int g = at.k * kPer + i;
+        if (v < P.V && g * G < P.d) s[i] = load_elem(P.scales + static_cast<long long>(g) * P.scales_ld + v);
       }
     };
-    load_scales(s0);
-    load_scales(s1);
-    int job = 0;
-    int begin = c.k;  // first weight stage of the sums in hand
+    load_scales(c, s_now);
+    // the accumulators of the first chunks are free
+    if (lane == 0)
+      for (int i = 0; i < S::kDBufs; ++i) mbar_arrive(&ready[i]);
+    Ring<kSlots> a;
+    int db = 0;
+    int begin = c.k;  // first stage of the sums in hand
     bool ok = true;
     for (int u = u0; u < u1 && ok; ++u) {
-      for (int h = 0; h < kStageK / kChunkK && ok; ++h) {
-        load_scales(s2);
-        const int left = P.d - (c.k * kStageK + h * kChunkK);
-        for (int j = 0; j < P.jobs; ++j, ++job) {
-          const int b = job % P.dbufs;
-          ok = i4_wait_warp(&dfull[b], static_cast<unsigned>(job / P.dbufs) & 1u, fault);
-          if (!ok) break;
-          tc_fence_after();
-          for (int g = 0; g < P.per_job; ++g) {
-            const int gi = j * P.per_job + g;
-            if (gi * P.group >= left) break;
-            const float s = gi == 0 ? s0[0] : gi == 1 ? s0[1] : gi == 2 ? s0[2] : s0[3];
-            const float2 ss = make_float2(s, s);
-            const uint32_t src = tmem_d + (b * P.per_job + g) * N + col0 + lanes;
+      cn.next(P);
+      if (u + 1 < u1) load_scales(cn, s_next);
+      const int left = P.d - c.k * kStageK;
 #pragma unroll
-            for (int i = 0; i < S::kCols; i += S::kLd) {
+      for (int i = 0; i < S::kChunks; ++i) {
+        ok = i4_wait_warp(&done[a.slot], a.parity, fault);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int g = 0; g < S::kGroups; ++g) {
+          if (i * S::kChunkK + g * G < left) {
+            const float s = s_now[i * S::kGroups + g];
+            const float2 ss = make_float2(s, s);
+            const uint32_t src = tmem_d + db * S::kDBuf + g * N + col0 + lanes;
+#pragma unroll
+            for (int n = 0; n < S::kCols; n += S::kLd) {
               float v[S::kLd];
-              if constexpr (S::kLd == 32) tmem_ld32(src + i, v);
-              else tmem_ld16(src + i, v);
+              if constexpr (S::kLd == 32) tmem_ld32(src + n, v);
+              else tmem_ld16(src + n, v);
 #pragma unroll
               for (int e = 0; e < S::kLd; e += 2)
-                acc[(i + e) / 2] = ffma2(ss, make_float2(v[e], v[e + 1]), acc[(i + e) / 2]);
+                acc[(n + e) / 2] = ffma2(ss, make_float2(v[e], v[e + 1]), acc[(n + e) / 2]);
             }
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&dempty[b]);
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s0[i] = s1[i];
-          s1[i] = s2[i];
-        }
+        tc_fence_before();
+        __syncwarp();
+        // these accumulators are the ones of the chunk kDBufs further on
+        if (lane == 0) mbar_arrive(&ready[(a.slot + S::kDBufs) % kSlots]);
+        a.next();
+        if (++db == S::kDBufs) db = 0;
       }
       if (!ok) break;
       const bool whole_end = c.k + 1 == P.nk;
@@ -475,11 +504,11 @@ __global__ void __launch_bounds__(kI4Threads, 1)
         bool write = true;
         if (begin != 0 || !whole_end) {
           // shared: leave the sums in this CTA's slot; the last to arrive adds all of them
-          int first = static_cast<int>(static_cast<long long>(tu0) * G / P.units);  // CTA of the tile's first unit
-          while (first_unit(first + 1, G, P.units) <= tu0) ++first;
-          while (first_unit(first, G, P.units) > tu0) --first;
+          int first = static_cast<int>(static_cast<long long>(tu0) * ctas / P.units);  // CTA of the tile's first unit
+          while (first_unit(first + 1, ctas, P.units) <= tu0) ++first;
+          while (first_unit(first, ctas, P.units) > tu0) --first;
           int last = first;
-          while (first_unit(last + 1, G, P.units) < tu1) ++last;
+          while (first_unit(last + 1, ctas, P.units) < tu1) ++last;
           const int slot = 2 * cta + (begin == 0 ? 1 : 0);
           float* mine = P.partials + (static_cast<long long>(slot) * N + col0) * kTileV + row;
 #pragma unroll
@@ -516,18 +545,23 @@ __global__ void __launch_bounds__(kI4Threads, 1)
         }
         const int v = c.vt * kTileV + row;
         if (write && v < P.V) {
-          const int r0 = c.rb * N + col0;
+          const int r0 = c.rb * N + col0, rows = min(S::kCols, P.R - r0);
           const long long at = static_cast<long long>(r0) * P.out_ld + v;
+          if (P.out_bf16) {
+            unsigned short* y = static_cast<unsigned short*>(P.out) + at;
 #pragma unroll
-          for (int i = 0; i < S::kCols; ++i) {
-            if (r0 + i >= P.R) break;
-            const float y = (i & 1) ? acc[i / 2].y : acc[i / 2].x;
-            if (P.out_bf16) {
+            for (int i = 0; i < S::kCols; ++i, y += P.out_ld) {
+              if (i >= rows) break;
               unsigned short bits;
-              asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(bits) : "f"(y));
-              static_cast<unsigned short*>(P.out)[at + i * P.out_ld] = bits;
-            } else {
-              static_cast<float*>(P.out)[at + i * P.out_ld] = y;
+              asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(bits) : "f"((i & 1) ? acc[i / 2].y : acc[i / 2].x));
+              *y = bits;
+            }
+          } else {
+            float* y = static_cast<float*>(P.out) + at;
+#pragma unroll
+            for (int i = 0; i < S::kCols; ++i, y += P.out_ld) {
+              if (i >= rows) break;
+              *y = (i & 1) ? acc[i / 2].y : acc[i / 2].x;
             }
           }
         }
@@ -536,6 +570,8 @@ __global__ void __launch_bounds__(kI4Threads, 1)
         begin = 0;
       }
       c.next(P);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) s_now[i] = s_next[i];
     }
   }
 
@@ -543,16 +579,16 @@ __global__ void __launch_bounds__(kI4Threads, 1)
   if (*fault && threadIdx.x == 0) {
     // copies still in flight land before the CTA exits: wait (bounded) for
     // the last phase of every stage that was issued
-    for (int k = max(0, w_issued_s - P.wstages); k < w_issued_s; ++k)
-      mbar_wait(&wfull[k % P.wstages], static_cast<unsigned>(k / P.wstages) & 1u);
-    for (int k = max(0, x_issued_s - P.xstages); k < x_issued_s; ++k)
-      mbar_wait(&xfull[k % P.xstages], static_cast<unsigned>(k / P.xstages) & 1u);
+    for (int k = max(0, w_issued_s - S::kWStages); k < w_issued_s; ++k)
+      mbar_wait(&wfull[k % S::kWStages], static_cast<unsigned>(k / S::kWStages) & 1u);
+    for (int k = max(0, x_issued_s - S::kXStages); k < x_issued_s; ++k)
+      mbar_wait(&xfull[k % S::kXStages], static_cast<unsigned>(k / S::kXStages) & 1u);
     if (P.error_word) atomicOr(P.error_word, SPEC_ERR_INTERNAL);
   }
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_s, 512);
+    tmem_dealloc(tmem_s, kACols + kDCols);
   }
 }
 
@@ -600,7 +636,7 @@ bool rows_map(CUtensorMap* map, const void* base, int R, int d, long long ld, in
 }
 
 // The kernel's dynamic shared memory limit, raised once per device.
-template <int N>
+template <int N, int G>
 cudaError_t raise_smem() {
   static std::mutex mu;
   static std::map<int, bool> done;
@@ -609,34 +645,23 @@ cudaError_t raise_smem() {
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lock(mu);
   if (done.count(dev)) return cudaSuccess;
-  e = cudaFuncSetAttribute(int4_product_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing + 1024);
+  e = cudaFuncSetAttribute(int4_product_kernel<N, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Shape<N, G>::kSmem);
   if (e == cudaSuccess) done[dev] = true;
   return e;
 }
 
-template <int N>
+template <int N, int G>
 spec_status launch_product(const spec_int4_product_args& a, cudaStream_t s) {
-  using S = Shape<N>;
   I4Params P{};
   P.R = a.R;
   P.V = a.V;
   P.d = a.d;
-  P.group = a.group;
-  P.group_log = a.group == 32 ? 5 : a.group == 64 ? 6 : 7;
   P.ntv = (a.V + kTileV - 1) / kTileV;
   P.nk = (a.d + kStageK - 1) / kStageK;
   const long long units = static_cast<long long>((a.R + N - 1) / N) * P.ntv * P.nk;
   if (units > 0x3fffffff) return SPEC_EINVAL;
   P.units = static_cast<int>(units);
-  // groups handed over together: as many of a chunk's as leave two buffers
-  P.per_job = kChunkK / a.group;
-  while (2 * P.per_job * N > kDCols) P.per_job /= 2;
-  P.jobs = kChunkK / (a.group * P.per_job);
-  P.dbufs = min(kMaxDBufs, kDCols / (P.per_job * N));
-  // the rows' ring: enough chunks to cover L2's latency; the rest goes to the
-  // weights, whose latency is HBM's
-  P.xstages = min(kMaxXStages, max(3, 48 * 1024 / S::kXBytes));
-  P.wstages = min(kMaxWStages, (kRing - P.xstages * S::kXBytes) / kStageBytes);
   P.scales_ld = a.scales_ld;
   P.zeros_ld = a.zeros_ld;
   P.out_ld = a.out_ld;
@@ -652,10 +677,18 @@ spec_status launch_product(const spec_int4_product_args& a, cudaStream_t s) {
   const int ctas = min(min(nsm, kMaxCtas), P.units);
   CUtensorMap tw, tx;
   if (!weight_map(&tw, a.codes, a.V, a.d, a.codes_ld) || !rows_map(&tx, a.x, a.R, a.d, a.x_ld, N)) return SPEC_ECUDA;
-  if (raise_smem<N>() != cudaSuccess) return SPEC_ECUDA;
-  const int dyn = P.wstages * kStageBytes + P.xstages * S::kXBytes + 1024;
-  int4_product_kernel<N><<<ctas, kI4Threads, dyn, s>>>(tw, tx, P);
+  if (raise_smem<N, G>() != cudaSuccess) return SPEC_ECUDA;
+  int4_product_kernel<N, G><<<ctas, kI4Threads, Shape<N, G>::kSmem, s>>>(tw, tx, P);
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
+}
+
+template <int N>
+spec_status launch_product(const spec_int4_product_args& a, cudaStream_t s) {
+  switch (a.group) {
+    case 32: return launch_product<N, 32>(a, s);
+    case 64: return launch_product<N, 64>(a, s);
+    default: return launch_product<N, 128>(a, s);
+  }
 }
 
 }  // namespace
