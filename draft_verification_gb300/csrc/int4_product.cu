@@ -13,8 +13,8 @@
 // tensor memory, which tcgen05.mma reads A from, so they cross shared memory
 // once, packed.  Roles of a CTA's 16 warps:
 //   warp 0          copies weight stages (128 entries x 256 columns, 16 KB)
-//                   into a ring with TMA, and requests the scales and zero
-//                   points of the same columns into L2;
+//                   into a ring with TMA, with the scales and zero points of
+//                   the same columns;
 //   warp 1          issues the MMAs (one thread);
 //   warp 2          copies the rows' chunks (N x 128 columns) with TMA;
 //   unpack warps    8 (N <= 64) or 4: thread t of a warpgroup owns entry t of
@@ -49,6 +49,10 @@ namespace {
 constexpr int kTileV = 128;                 // vocabulary entries per tile (MMA M)
 constexpr int kStageK = 256;                // columns of a stage (a unit): 128 packed bytes per entry
 constexpr int kStageBytes = kTileV * kStageK / 2;
+// 128 scales (256 bytes) or zero points (128) that may start anywhere are copied
+// as the 16-byte blocks they lie in
+constexpr int kScalePitch = 272;
+constexpr int kZeroPitch = 144;
 constexpr int kSlots = 4;                   // chunks in flight between unpacking and epilogue
 constexpr int kACols = 256;                 // tensor memory: the chunks' weights, then the accumulators
 constexpr int kDCols = 256;
@@ -89,7 +93,18 @@ struct Shape {
   static constexpr int kXStages = N <= 32 ? 4 : N == 64 ? 3 : 2;
   static constexpr int kWStages = N <= 32 ? 8 : N == 64 ? 6 : 4;
   static constexpr int kLd = kCols == 32 ? 32 : 16;      // tensor-memory columns per load
-  static constexpr int kSmem = kXStages * kXBytes + kWStages * kStageBytes + 1024;
+  // registers per thread (warps 0-3, unpacking, epilogue): the launch gives
+  // every thread 128, and the shares add up to no more
+  static constexpr int kRegsCopy = 64;
+  static constexpr int kRegsUnpack = kUnpackGroups == 2 ? 96 : 104;
+  static constexpr int kRegsEpi = kEpiGroups == 1 ? 200 : 168;
+  static_assert(128 * (kRegsCopy + kUnpackGroups * kRegsUnpack + kEpiGroups * kRegsEpi) <= kI4Threads * 128,
+                "no more registers than the launch holds");
+  // scales and zero points of a weight stage: one row of a tile per group
+  static constexpr int kPer = kStageK / G;
+  static constexpr int kSideBytes = kPer * (kScalePitch + kZeroPitch);
+  static constexpr int kSmem = kXStages * kXBytes + kWStages * (kStageBytes + kSideBytes) + 1024;
+  static_assert(kSmem <= 225 * 1024, "one CTA's shared memory");
 };
 
 // A place in a ring: slot and the parity of its current round.
@@ -105,19 +120,19 @@ struct Ring {
   }
 };
 
-// Wait that every role shares: gives up when the bound is reached or another
-// role did, so that all of them leave.
+// A whole warp's wait: gives up when the bound is reached or another role did,
+// so that all of them leave.  The lanes vote on every poll, which keeps the
+// warp together: a warp whose lanes part over a wait runs several times slower
+// (it is put to sleep and woken lane set by lane set), and so does every role
+// that depends on it.
 __device__ __forceinline__ bool i4_wait(uint64_t* bar, unsigned parity, volatile int* fault) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   for (int i = 0; i < kMaxPolls; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*fault) return false;
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, *fault)) return false;
   }
   *fault = 1;
   return false;
-}
-// The same by a whole warp, which decides together.
-__device__ __forceinline__ bool i4_wait_warp(uint64_t* bar, unsigned parity, volatile int* fault) {
-  return __all_sync(0xffffffffu, i4_wait(bar, parity, fault));
 }
 
 // D[tmem] (+)= A[tmem] * B[smem]^T, M = 128, N x 16, bfloat16 in, float32 out.
@@ -152,21 +167,51 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // 8 codes (one word, columns ascending from the low nibble) -> 4 packed pairs
-// of q - z in bfloat16.  0x4300 | q is 128 + q exactly, and (128 + q) -
-// (128 + z) is exact; `base` holds 128 + z twice.
-__device__ __forceinline__ void unpack8(uint32_t w, uint32_t base, uint32_t* out) {
-  const uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu;
-  const uint32_t a = __byte_perm(even, odd, 0x5140);  // codes 0, 1, 2, 3
-  const uint32_t b = __byte_perm(even, odd, 0x7362);  // codes 4, 5, 6, 7
-  const uint32_t k = 0x43434343u;
-  uint32_t p[4] = {__byte_perm(a, k, 0x4140), __byte_perm(a, k, 0x4342), __byte_perm(b, k, 0x4140),
-                   __byte_perm(b, k, 0x4342)};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(out[i]) : "r"(p[i]), "r"(base));
+// of (q - z) / 64 in bfloat16.  The codes of one byte are neighbouring columns
+// and go to the two halves of a register as they lie in the byte: a small
+// integer in the low bits of a bfloat16 is a subnormal, and the first binade
+// continues the subnormals, so the low nibble (bits 0-3) reads as q 2^-133 and
+// the high one (bits 4-7) as q 2^-129.  One multiply-add by (2^127, 2^123)
+// makes both q / 64 and subtracts z / 64, all exact.  (The unused bytes are
+// sign copies of the low nibble's byte: zero.)  Two logic operations, four
+// byte permutations and four multiply-adds for 8 weights: the byte and logic
+// operations run at half the rate of the multiply-adds and bound the unpacking.
+constexpr uint32_t kUnpackScale = 0x7d007f00u;  // (2^127, 2^123)
+constexpr float kUnpackUnit = 64.f;
+__device__ __forceinline__ uint32_t fma2_bf16(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+// Four bytes of a (0-3) and b (4-7); selector 8 + i: copies of byte i's sign.
+__device__ __forceinline__ uint32_t pick(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+  return d;
+}
+// -z / 64 twice
+__device__ __forceinline__ uint32_t minus_zero(uint32_t z) {
+  return fma2_bf16(z * 0x10001u, 0xff00ff00u, 0x80008000u);  // z 2^-133 times -2^127
+}
+__device__ __forceinline__ void unpack8(uint32_t w, uint32_t mz, uint32_t* out) {
+  const uint32_t even = w & 0x0f0f0f0fu, odd = w & 0xf0f0f0f0u;
+  out[0] = fma2_bf16(pick(even, odd, 0x8480u), kUnpackScale, mz);
+  out[1] = fma2_bf16(pick(even, odd, 0x9591u), kUnpackScale, mz);
+  out[2] = fma2_bf16(pick(even, odd, 0xa6a2u), kUnpackScale, mz);
+  out[3] = fma2_bf16(pick(even, odd, 0xb7b3u), kUnpackScale, mz);
 }
 
-// Place in the CTA's list of units: tile vt of row block rb, weight stage k.
-struct Cursor {
+// first unit of CTA c of `ctas`
+__host__ __device__ __forceinline__ int first_unit(int c, int ctas, int units) {
+  return static_cast<int>(static_cast<long long>(c) * units / ctas);
+}
+
+// Place in the CTA's list of units: stage k of tile vt of row block rb.  The
+// CTA has units [u0, u1), but begins at `start`, the first unit of the tile
+// that it shares with the next CTA, goes on at u0 with the tile that it shares
+// with the one before, and ends with whole tiles: shared tiles are complete
+// early, and nobody's last work is a sum that others must contribute to.
+struct Place {
   int rb, vt, k;
   __device__ __forceinline__ void set(int u, const I4Params& P) {
     const int t = u / P.nk;
@@ -174,20 +219,49 @@ struct Cursor {
     rb = t / P.ntv;
     vt = t - rb * P.ntv;
   }
+};
+struct Cursor {
+  Place at, again;  // here; where [u0, ...) begins (kept: no division in the loops)
+  int left;         // units to go before u0
+  __device__ __forceinline__ Cursor(int start, int u0, int u1, const I4Params& P) : left(u1 - start) {
+    at.set(start, P);
+    again.set(u0, P);
+  }
   __device__ __forceinline__ void next(const I4Params& P) {
-    if (++k == P.nk) {
-      k = 0;
-      if (++vt == P.ntv) {
-        vt = 0;
-        ++rb;
+    if (--left == 0) {
+      at = again;
+    } else if (++at.k == P.nk) {
+      at.k = 0;
+      if (++at.vt == P.ntv) {
+        at.vt = 0;
+        ++at.rb;
       }
     }
   }
 };
 
-// first unit of CTA c of G
-__host__ __device__ __forceinline__ int first_unit(int c, int G, int units) {
-  return static_cast<int>(static_cast<long long>(c) * units / G);
+// The tile of a unit, its units' CTAs and its first unit.
+struct SharedTile {
+  int u0, first, last;
+  __device__ __forceinline__ void find(int u, int ctas, const I4Params& P) {
+    u0 = u / P.nk * P.nk;
+    first = static_cast<int>(static_cast<long long>(u0) * ctas / P.units);
+    while (first_unit(first + 1, ctas, P.units) <= u0) ++first;
+    while (first_unit(first, ctas, P.units) > u0) --first;
+    last = first;
+    while (first_unit(last + 1, ctas, P.units) < u0 + P.nk) ++last;
+  }
+};
+
+// The 16-byte blocks that `bytes` bytes at `src` lie in: their size, and a copy
+// of them (the data is at the same place within its first block).
+__device__ __forceinline__ unsigned blocks_of(const void* src, int bytes) {
+  const unsigned lead = static_cast<unsigned>(reinterpret_cast<uintptr_t>(src)) & 15u;
+  return (lead + bytes + 15u) & ~15u;
+}
+__device__ __forceinline__ void load_blocks(void* dst, const void* src, int bytes, uint64_t* bar) {
+  bulk_load(dst, reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(src) & ~static_cast<uintptr_t>(15)),
+            blocks_of(src, bytes), bar);
 }
 
 // One lane of the warp, the same at every call.
@@ -206,22 +280,32 @@ __global__ void __launch_bounds__(kI4Threads, 1)
   __shared__ uint64_t wfull[S::kWStages], wempty[S::kWStages], xfull[S::kXStages], xempty[S::kXStages];
   // ready: a chunk's weights are in tensor memory and its accumulators are
   // free; done: its products are complete (its weights' slot is free again)
-  __shared__ uint64_t ready[kSlots], done[kSlots], drain, joint;
+  __shared__ uint64_t ready[kSlots], done[kSlots], drain;
+  // left: the epilogue's partial sums of the CTA's i-th shared tile are in the
+  // workspace; settled: it is known whether this CTA adds them all (won_s)
+  __shared__ uint64_t left_s[2], settled[2];
   __shared__ uint32_t tmem_s;
-  __shared__ int fault_s, last_s, w_issued_s, x_issued_s;
+  __shared__ int fault_s, won_s[2], w_issued_s, x_issued_s;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const bool leader = elect_one();  // one lane issues what a warp does once
   unsigned char* wring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(i4_dyn) + 1023) &
                                                           ~static_cast<uintptr_t>(1023));
   unsigned char* xring = wring + S::kWStages * kStageBytes;
+  unsigned char* sring = xring + S::kXStages * S::kXBytes;
   const int ctas = gridDim.x, cta = blockIdx.x;
   const int u0 = first_unit(cta, ctas, P.units), u1 = first_unit(cta + 1, ctas, P.units);
+  const int units = u1 - u0;
+  int start = u1 - u1 % P.nk;
+  if (start <= u0 || start == u1) start = u0;
+  // shared tiles: start's, which the next CTA ends, and u0's, which another began
+  const bool tail = u1 % P.nk != 0, head = u0 % P.nk != 0 && !(start == u0 && tail);
   volatile int* fault = &fault_s;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kWStages; ++s) {
       mbar_init(&wfull[s], 1);
-      mbar_init(&wempty[s], 4 * S::kUnpackGroups);
+      mbar_init(&wempty[s], 4 * (S::kUnpackGroups + S::kEpiGroups));
     }
     for (int s = 0; s < S::kXStages; ++s) {
       mbar_init(&xfull[s], 1);
@@ -232,7 +316,10 @@ __global__ void __launch_bounds__(kI4Threads, 1)
       mbar_init(&done[s], 1);
     }
     mbar_init(&drain, 1);
-    mbar_init(&joint, 4 * S::kEpiGroups);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&left_s[i], 4 * S::kEpiGroups);
+      mbar_init(&settled[i], 1);
+    }
     fault_s = 0;
     w_issued_s = 0;
     x_issued_s = 0;
@@ -247,98 +334,124 @@ __global__ void __launch_bounds__(kI4Threads, 1)
   tc_fence_after();
   const uint32_t tmem_a = tmem_s, tmem_d = tmem_s + kACols;
 
-  if (warp == 0) {
-    // ---------------- weight stages ----------------
-    if (lane == 0) {
-      tma_prefetch_desc(&tm_w);
-      Cursor c;
-      c.set(u0, P);
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsCopy));
+    if (warp == 0) {
+      // ---------------- weight stages ----------------
+      if (leader) tma_prefetch_desc(&tm_w);
+      Cursor c(start, u0, u1, P);
       Ring<S::kWStages> w;
-      for (int u = u0; u < u1; ++u, c.next(P), w.next()) {
+      for (int it = 0; it < units; ++it, c.next(P), w.next()) {
         if (!i4_wait(&wempty[w.slot], w.parity ^ 1u, fault)) break;
-        mbar_expect_tx(&wfull[w.slot], kStageBytes);
-        tma_load_2d(wring + w.slot * kStageBytes, &tm_w, c.k * (kStageK / 2), c.vt * kTileV, &wfull[w.slot]);
-        w_issued_s = u - u0 + 1;
-        // the scales and zero points of the same columns, into L2
-        const int v0 = c.vt * kTileV, vl = min(P.V - 1, v0 + kTileV - 1);
-        for (int i = 0; i < kStageK / G; ++i) {
-          const long long g = c.k * (kStageK / G) + i;
-          if (g * G >= P.d) break;
-          const unsigned short* sp = P.scales + g * P.scales_ld;
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(sp + v0));
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(sp + min(v0 + 64, vl)));
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(sp + vl));
-          if (P.zeros) {
-            const unsigned char* zp = P.zeros + g * P.zeros_ld;
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(zp + v0));
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(zp + vl));
-          }
-        }
-      }
-    }
-  } else if (warp == 1) {
-    // ---------------- MMAs ----------------
-    // The whole warp keeps the loop's values, so that they stay in uniform
-    // registers, and one lane issues; everything that varies from MMA to MMA
-    // is a constant: a lone thread's instruction latency is the limit here.
-    constexpr uint32_t idesc = umma_idesc_bf16_f32(kTileV, N);
-    const bool leader = elect_one();
-    Ring<S::kXStages> x;
-    Ring<kSlots> a;
-    int db = 0;
-    bool ok = true;
-    for (int u = u0; u < u1; ++u) {
-      ok = i4_wait_warp(&xfull[x.slot], x.parity, fault);
-      if (!ok) break;
-      const uint64_t dx = umma_desc_sw128(smem_addr(xring + x.slot * S::kXBytes));
-#pragma unroll
-      for (int i = 0; i < S::kChunks; ++i) {
-        ok = i4_wait_warp(&ready[a.slot], a.parity, fault);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t at = tmem_a + a.slot * (S::kChunkK / 2), dt = tmem_d + db * S::kDBuf;
+        const int v0 = c.at.vt * kTileV, n = min(kTileV, P.V - v0), g0 = c.at.k * S::kPer;
+        const int groups = min(S::kPer, P.d / G - g0);
+        // lane i < kPer: the scales of group i of the stage; lane 16 + i: its zero points
+        const int g = lane & 15;
+        const bool zeros = lane >= 16;
+        const bool mine = g < groups && (!zeros || P.zeros);
+        const char* src = zeros ? reinterpret_cast<const char*>(P.zeros) + (g0 + g) * P.zeros_ld + v0
+                                : reinterpret_cast<const char*>(P.scales + (g0 + g) * P.scales_ld + v0);
+        const int len = zeros ? n : 2 * n;
+        const unsigned bytes = __reduce_add_sync(0xffffffffu, mine ? blocks_of(src, len) : 0u);
         if (leader) {
-#pragma unroll
-          for (int k = 0; k < S::kChunkK / 16; ++k) {
-            // K step ks of the unit: 8 columns of A; of the rows' block
-            // ks / 4, 32 bytes further per step
-            const int ks = i * (S::kChunkK / 16) + k;
-            umma_bf16_ta(dt + (k * 16 / G) * N, at + k * 8,
-                         dx + static_cast<uint64_t>((ks >> 2) * (N * 128 >> 4) + (ks & 3) * 2), idesc,
-                         k * 16 % G != 0);
-          }
-          umma_commit(&done[a.slot]);
-          if (i + 1 == S::kChunks) umma_commit(&xempty[x.slot]);
+          mbar_expect_tx(&wfull[w.slot], kStageBytes + bytes);
+          tma_load_2d(wring + w.slot * kStageBytes, &tm_w, c.at.k * (kStageK / 2), v0, &wfull[w.slot]);
+          w_issued_s = it + 1;
         }
-        a.next();
-        if (++db == S::kDBufs) db = 0;
+        __syncwarp();  // the stage expects its bytes before any of them arrives
+        unsigned char* side = sring + w.slot * S::kSideBytes;
+        if (mine)
+          load_blocks(zeros ? side + S::kPer * kScalePitch + g * kZeroPitch : side + g * kScalePitch, src, len,
+                      &wfull[w.slot]);
+        __syncwarp();
       }
-      if (!ok) break;
-      x.next();
-    }
-    // every MMA issued has completed before tensor memory is released
-    if (leader) umma_commit(&drain);
-    __syncwarp();
-    mbar_wait(&drain, 0);
-  } else if (warp == 2) {
-    // ---------------- the rows' columns ----------------
-    if (lane == 0) {
-      tma_prefetch_desc(&tm_x);
-      Cursor c;
-      c.set(u0, P);
+    } else if (warp == 1) {
+      // ---------------- MMAs ----------------
+      // The whole warp keeps the loop's values, so that they stay in uniform
+      // registers, and one lane issues; everything that varies from MMA to MMA
+      // is a constant: a lone thread's instruction latency is the limit here.
+      constexpr uint32_t idesc = umma_idesc_bf16_f32(kTileV, N);
       Ring<S::kXStages> x;
-      for (int u = u0; u < u1; ++u, c.next(P), x.next()) {
+      Ring<kSlots> a;
+      int db = 0;
+      bool ok = true;
+      for (int it = 0; it < units; ++it) {
+        ok = i4_wait(&xfull[x.slot], x.parity, fault);
+        if (!ok) break;
+        const uint64_t dx = umma_desc_sw128(smem_addr(xring + x.slot * S::kXBytes));
+  #pragma unroll
+        for (int i = 0; i < S::kChunks; ++i) {
+          ok = i4_wait(&ready[a.slot], a.parity, fault);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t at = tmem_a + a.slot * (S::kChunkK / 2), dt = tmem_d + db * S::kDBuf;
+          if (leader) {
+  #pragma unroll
+            for (int k = 0; k < S::kChunkK / 16; ++k) {
+              // K step ks of the unit: 8 columns of A; of the rows' block
+              // ks / 4, 32 bytes further per step
+              const int ks = i * (S::kChunkK / 16) + k;
+              umma_bf16_ta(dt + (k * 16 / G) * N, at + k * 8,
+                           dx + static_cast<uint64_t>((ks >> 2) * (N * 128 >> 4) + (ks & 3) * 2), idesc,
+                           k * 16 % G != 0);
+            }
+            umma_commit(&done[a.slot]);
+            if (i + 1 == S::kChunks) umma_commit(&xempty[x.slot]);
+          }
+          a.next();
+          if (++db == S::kDBufs) db = 0;
+        }
+        if (!ok) break;
+        x.next();
+      }
+      // every MMA issued has completed before tensor memory is released
+      if (leader) umma_commit(&drain);
+      __syncwarp();
+      mbar_wait(&drain, 0);
+    } else if (warp == 2) {
+      // ---------------- the rows' columns ----------------
+      if (leader) tma_prefetch_desc(&tm_x);
+      Cursor c(start, u0, u1, P);
+      Ring<S::kXStages> x;
+      for (int it = 0; it < units; ++it, c.next(P), x.next()) {
         if (!i4_wait(&xempty[x.slot], x.parity ^ 1u, fault)) break;
-        unsigned char* st = xring + x.slot * S::kXBytes;
-        mbar_expect_tx(&xfull[x.slot], S::kXBytes);
+        if (leader) {
+          unsigned char* st = xring + x.slot * S::kXBytes;
+          mbar_expect_tx(&xfull[x.slot], S::kXBytes);
 #pragma unroll
-        for (int i = 0; i < kStageK / 64; ++i)
-          tma_load_2d(st + i * N * 128, &tm_x, c.k * kStageK + i * 64, c.rb * N, &xfull[x.slot]);
-        x_issued_s = u - u0 + 1;
+          for (int i = 0; i < kStageK / 64; ++i)
+            tma_load_2d(st + i * N * 128, &tm_x, c.at.k * kStageK + i * 64, c.at.rb * N, &xfull[x.slot]);
+          x_issued_s = it + 1;
+        }
+        __syncwarp();
+      }
+    } else if (warp == 3) {
+      // ---------------- shared tiles ----------------
+      // In the order in which the epilogue leaves them: the tile of unit
+      // `start` where the CTA does not end it, then that of u0 where it does
+      // not begin it.  One arrival per part; the last one's CTA adds them up.
+      int n = 0;
+      for (int i = 0; i < 2; ++i) {
+        if (!(i == 0 ? tail : head)) continue;
+        SharedTile t;
+        t.find(i == 0 ? start : u0, ctas, P);
+        if (!i4_wait(&left_s[n], 0u, fault)) break;
+        if (leader) {
+          // the counter wraps to zero with the last arrival: the workspace is as it was
+          asm volatile("fence.acq_rel.gpu;" ::: "memory");
+          const unsigned before =
+              atomicInc(reinterpret_cast<unsigned*>(P.counters + t.first), static_cast<unsigned>(t.last - t.first));
+          asm volatile("fence.acq_rel.gpu;" ::: "memory");
+          won_s[n] = before == static_cast<unsigned>(t.last - t.first);
+          mbar_arrive(&settled[n]);
+        }
+        __syncwarp();
+        ++n;
       }
     }
-  } else if (warp >= 4 && warp < 4 + 4 * S::kUnpackGroups) {
+  } else if (warp < 4 + 4 * S::kUnpackGroups) {
     // ---------------- unpacking ----------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsUnpack));
     // chunk i of a unit is unpacked by warpgroup i % kUnpackGroups
     constexpr int kMine = S::kChunks / S::kUnpackGroups;  // chunks per unit
     constexpr int kVecs = S::kChunkK / 32;                // 16-byte vectors of an entry's chunk, one zero point each
@@ -346,33 +459,32 @@ __global__ void __launch_bounds__(kI4Threads, 1)
     const int row = q * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
     const uint32_t key = static_cast<uint32_t>(row & 7);
-    Cursor cn;  // the unit whose zero points are loaded: one ahead
-    cn.set(u0, P);
-    uint32_t zero[kMine * kVecs], znext[kMine * kVecs];
+    Cursor c(start, u0, u1, P);
+    // low bits of addresses: where a row of zero points starts in its first block
+    const uint32_t zeros_at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(P.zeros));
+    const uint32_t zeros_ld = static_cast<uint32_t>(P.zeros_ld);
+    uint32_t zero[kMine * kVecs];  // of this warpgroup's 32-column vectors
 #pragma unroll
-    for (int i = 0; i < kMine * kVecs; ++i) zero[i] = znext[i] = 0x43084308u;
-    // zero points of this warpgroup's 32-column vectors of unit cn, as 128 + z twice
-    const auto load_zeros = [&](uint32_t (&z)[kMine * kVecs]) {
-      const int v = cn.vt * kTileV + row;
-#pragma unroll
-      for (int j = 0; j < kMine; ++j)
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-          const int k = cn.k * kStageK + (j * S::kUnpackGroups + grp) * S::kChunkK + i * 32;
-          if (v < P.V && k < P.d)
-            z[j * kVecs + i] = (0x4300u | __ldg(P.zeros + static_cast<long long>(k / G) * P.zeros_ld + v)) * 0x10001u;
-        }
-    };
-    if (P.zeros) load_zeros(zero);
+    for (int i = 0; i < kMine * kVecs; ++i) zero[i] = 8u;
     Ring<S::kWStages> w;
     Ring<kSlots> a;
     for (int i = 0; i < grp; ++i) a.next();
     bool ok = true;
-    for (int u = u0; u < u1 && ok; ++u, w.next()) {
-      cn.next(P);
-      if (P.zeros && u + 1 < u1) load_zeros(znext);
-      ok = i4_wait_warp(&wfull[w.slot], w.parity, fault);
+    for (int it = 0; it < units && ok; ++it, w.next(), c.next(P)) {
+      ok = i4_wait(&wfull[w.slot], w.parity, fault);
       if (!ok) break;
+      if (P.zeros) {
+        const unsigned char* z = sring + w.slot * S::kSideBytes + S::kPer * kScalePitch + row;
+        const uint32_t lead = zeros_at + static_cast<uint32_t>(c.at.vt * kTileV);
+#pragma unroll
+        for (int j = 0; j < kMine; ++j)
+#pragma unroll
+          for (int i = 0; i < kVecs; ++i) {
+            const int g = ((j * S::kUnpackGroups + grp) * S::kChunkK + i * 32) / G;  // of the unit
+            zero[j * kVecs + i] =
+                z[g * kZeroPitch + ((lead + static_cast<uint32_t>(c.at.k * S::kPer + g) * zeros_ld) & 15u)];
+          }
+      }
       const unsigned char* src = wring + w.slot * kStageBytes + row * (kStageK / 2);
 #pragma unroll
       for (int j = 0; j < kMine; ++j) {
@@ -384,7 +496,7 @@ __global__ void __launch_bounds__(kI4Threads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&wempty[w.slot]);
         }
-        ok = i4_wait_warp(&done[a.slot], a.parity ^ 1u, fault);
+        ok = i4_wait(&done[a.slot], a.parity ^ 1u, fault);
         if (!ok) break;
         tc_fence_after();
         const uint32_t dst = tmem_a + a.slot * (S::kChunkK / 2) + lanes;
@@ -395,7 +507,7 @@ __global__ void __launch_bounds__(kI4Threads, 1)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const uint4 x = code[2 * h + e];
-              const uint32_t z = zero[j * kVecs + 2 * h + e];
+              const uint32_t z = minus_zero(zero[j * kVecs + 2 * h + e]);
               unpack8(x.x, z, r + 16 * e);
               unpack8(x.y, z, r + 16 * e + 4);
               unpack8(x.z, z, r + 16 * e + 8);
@@ -405,7 +517,7 @@ __global__ void __launch_bounds__(kI4Threads, 1)
           }
         } else {
           uint32_t r[16];
-          const uint32_t z = zero[j];
+          const uint32_t z = minus_zero(zero[j]);
           unpack8(code[0].x, z, r);
           unpack8(code[0].y, z, r + 4);
           unpack8(code[0].z, z, r + 8);
@@ -419,63 +531,82 @@ __global__ void __launch_bounds__(kI4Threads, 1)
 #pragma unroll
         for (int n = 0; n < S::kUnpackGroups; ++n) a.next();
       }
-#pragma unroll
-      for (int i = 0; i < kMine * kVecs; ++i) zero[i] = znext[i];
     }
-  } else if (warp >= 4 + 4 * S::kUnpackGroups) {
+  } else {
     // ---------------- epilogue ----------------
-    constexpr int kPer = kStageK / G;  // groups per unit
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kRegsEpi));
     const int grp = (warp - 4 - 4 * S::kUnpackGroups) >> 2, q = warp & 3;
     const int row = q * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
     const int col0 = grp * S::kCols;
-    // a barrier of the epilogue warps that gives up with the others
-    unsigned met = 0;
-    const auto meet = [&] {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&joint);
-      const bool all = i4_wait_warp(&joint, met & 1u, fault);
-      ++met;
-      return all;
+    // this thread's sums of a tile, to their places in out
+    const auto store = [&](const Place& at, const float2 (&acc)[S::kCols / 2]) {
+      const int v = at.vt * kTileV + row;
+      if (v >= P.V) return;
+      const int r0 = at.rb * N + col0, rows = min(S::kCols, P.R - r0);
+      const long long first = static_cast<long long>(r0) * P.out_ld + v;
+      if (P.out_bf16) {
+        unsigned short* y = static_cast<unsigned short*>(P.out) + first;
+#pragma unroll
+        for (int i = 0; i < S::kCols; ++i, y += P.out_ld) {
+          if (i >= rows) break;
+          unsigned short bits;
+          asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(bits) : "f"(kUnpackUnit * ((i & 1) ? acc[i / 2].y : acc[i / 2].x)));
+          *y = bits;
+        }
+      } else {
+        float* y = static_cast<float*>(P.out) + first;
+#pragma unroll
+        for (int i = 0; i < S::kCols; ++i, y += P.out_ld) {
+          if (i >= rows) break;
+          *y = kUnpackUnit * ((i & 1) ? acc[i / 2].y : acc[i / 2].x);
+        }
+      }
     };
     float2 acc[S::kCols / 2];
 #pragma unroll
     for (int i = 0; i < S::kCols / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-    Cursor c, cn;
-    c.set(u0, P);
-    cn = c;
-    // the scales of a unit's groups, loaded one unit ahead (they wait in L2)
-    float s_now[kPer], s_next[kPer] = {};
-    const auto load_scales = [&](const Cursor& at, float (&s)[kPer]) {
-      const int v = at.vt * kTileV + row;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        s[i] = 0.f;
-        const int g = at.k * kPer + i;
-        if (v < P.V && g * G < P.d) s[i] = load_elem(P.scales + static_cast<long long>(g) * P.scales_ld + v);
-      }
-    };
-    load_scales(c, s_now);
+    Cursor cn(start, u0, u1, P);  // one unit ahead
+    Place c = cn.at;
+    const uint32_t scales_at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(P.scales));
+    const uint32_t scales_ld = static_cast<uint32_t>(P.scales_ld);
     // the accumulators of the first chunks are free
     if (lane == 0)
       for (int i = 0; i < S::kDBufs; ++i) mbar_arrive(&ready[i]);
+    Ring<S::kWStages> w;
     Ring<kSlots> a;
     int db = 0;
     int begin = c.k;  // first stage of the sums in hand
+    int shared = 0;   // shared tiles so far
+    int tail_left = u1 - start;  // units until the list leaves the tail
     bool ok = true;
-    for (int u = u0; u < u1 && ok; ++u) {
+    for (int it = 0; it < units && ok; ++it) {
       cn.next(P);
-      if (u + 1 < u1) load_scales(cn, s_next);
+      // the scales of the unit's groups
+      ok = i4_wait(&wfull[w.slot], w.parity, fault);
+      if (!ok) break;
+      uint32_t s_now[S::kPer];
+      {
+        const unsigned char* sp = sring + w.slot * S::kSideBytes + row * 2;
+        const uint32_t lead = scales_at + static_cast<uint32_t>(c.vt * kTileV) * 2u;
+#pragma unroll
+        for (int i = 0; i < S::kPer; ++i)
+          s_now[i] = *reinterpret_cast<const unsigned short*>(
+              sp + i * kScalePitch + ((lead + static_cast<uint32_t>(c.k * S::kPer + i) * scales_ld * 2u) & 15u));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&wempty[w.slot]);
+        w.next();
+      }
       const int left = P.d - c.k * kStageK;
 #pragma unroll
       for (int i = 0; i < S::kChunks; ++i) {
-        ok = i4_wait_warp(&done[a.slot], a.parity, fault);
+        ok = i4_wait(&done[a.slot], a.parity, fault);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
         for (int g = 0; g < S::kGroups; ++g) {
           if (i * S::kChunkK + g * G < left) {
-            const float s = s_now[i * S::kGroups + g];
+            const float s = __uint_as_float(s_now[i * S::kGroups + g] << 16);
             const float2 ss = make_float2(s, s);
             const uint32_t src = tmem_d + db * S::kDBuf + g * N + col0 + lanes;
 #pragma unroll
@@ -497,81 +628,47 @@ __global__ void __launch_bounds__(kI4Threads, 1)
         if (++db == S::kDBufs) db = 0;
       }
       if (!ok) break;
-      const bool whole_end = c.k + 1 == P.nk;
-      if (whole_end || u + 1 == u1) {
-        const int tile = c.rb * P.ntv + c.vt;
-        const int tu0 = tile * P.nk, tu1 = tu0 + P.nk;  // the tile's units
-        bool write = true;
-        if (begin != 0 || !whole_end) {
-          // shared: leave the sums in this CTA's slot; the last to arrive adds all of them
-          int first = static_cast<int>(static_cast<long long>(tu0) * ctas / P.units);  // CTA of the tile's first unit
-          while (first_unit(first + 1, ctas, P.units) <= tu0) ++first;
-          while (first_unit(first, ctas, P.units) > tu0) --first;
-          int last = first;
-          while (first_unit(last + 1, ctas, P.units) < tu1) ++last;
-          const int slot = 2 * cta + (begin == 0 ? 1 : 0);
-          float* mine = P.partials + (static_cast<long long>(slot) * N + col0) * kTileV + row;
+      const bool ends = c.k + 1 == P.nk, leaves = --tail_left == 0;
+      if (ends || leaves) {
+        if (begin == 0 && ends) {
+          store(c, acc);
+        } else {
+          // a shared tile: leave the sums in this CTA's slot
+          float* mine = P.partials + (static_cast<long long>(2 * cta + (begin == 0 ? 1 : 0)) * N + col0) * kTileV + row;
 #pragma unroll
           for (int i = 0; i < S::kCols / 2; ++i) {
             __stcg(mine + (2 * i) * kTileV, acc[i].x);
             __stcg(mine + (2 * i + 1) * kTileV, acc[i].y);
           }
-          __threadfence();
-          ok = meet();
-          if (!ok) break;
-          if (threadIdx.x == kI4Threads - 1) {
-            // the counter wraps to zero with the last arrival: the workspace is as it was
-            __threadfence();
-            last_s = atomicInc(reinterpret_cast<unsigned*>(P.counters + first),
-                               static_cast<unsigned>(last - first)) == static_cast<unsigned>(last - first);
-          }
-          ok = meet();
-          if (!ok) break;
-          write = last_s != 0;
-          if (write) {
-            __threadfence();
-#pragma unroll
-            for (int i = 0; i < S::kCols / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-            for (int o = first; o <= last; ++o) {
-              const int os = 2 * o + (o == first ? 1 : 0);
-              const float* src = P.partials + (static_cast<long long>(os) * N + col0) * kTileV + row;
-#pragma unroll
-              for (int i = 0; i < S::kCols / 2; ++i) {
-                acc[i].x = __fadd_rn(acc[i].x, __ldcg(src + (2 * i) * kTileV));
-                acc[i].y = __fadd_rn(acc[i].y, __ldcg(src + (2 * i + 1) * kTileV));
-              }
-            }
-          }
-        }
-        const int v = c.vt * kTileV + row;
-        if (write && v < P.V) {
-          const int r0 = c.rb * N + col0, rows = min(S::kCols, P.R - r0);
-          const long long at = static_cast<long long>(r0) * P.out_ld + v;
-          if (P.out_bf16) {
-            unsigned short* y = static_cast<unsigned short*>(P.out) + at;
-#pragma unroll
-            for (int i = 0; i < S::kCols; ++i, y += P.out_ld) {
-              if (i >= rows) break;
-              unsigned short bits;
-              asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(bits) : "f"((i & 1) ? acc[i / 2].y : acc[i / 2].x));
-              *y = bits;
-            }
-          } else {
-            float* y = static_cast<float*>(P.out) + at;
-#pragma unroll
-            for (int i = 0; i < S::kCols; ++i, y += P.out_ld) {
-              if (i >= rows) break;
-              *y = (i & 1) ? acc[i / 2].y : acc[i / 2].x;
-            }
-          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&left_s[shared]);
+          ++shared;
         }
 #pragma unroll
         for (int i = 0; i < S::kCols / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-        begin = 0;
+        begin = cn.at.k;
       }
-      c.next(P);
+      c = cn.at;
+    }
+    // the shared tiles whose last part this CTA was: all parts, in the order of the columns
+    for (int i = 0; i < shared && ok; ++i) {
+      ok = i4_wait(&settled[i], 0u, fault);
+      if (!ok || !won_s[i]) continue;
+      SharedTile t;
+      t.find(tail && i == 0 ? start : u0, ctas, P);
+      c.set(t.u0, P);
+      for (int o = t.first; o <= t.last; ++o) {
+        const float* src =
+            P.partials + (static_cast<long long>(2 * o + (o == t.first ? 1 : 0)) * N + col0) * kTileV + row;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) s_now[i] = s_next[i];
+        for (int n = 0; n < S::kCols / 2; ++n) {
+          acc[n].x = __fadd_rn(acc[n].x, __ldcg(src + (2 * n) * kTileV));
+          acc[n].y = __fadd_rn(acc[n].y, __ldcg(src + (2 * n + 1) * kTileV));
+        }
+      }
+      store(c, acc);
+#pragma unroll
+      for (int n = 0; n < S::kCols / 2; ++n) acc[n] = make_float2(0.f, 0.f);
     }
   }
 
