@@ -53,9 +53,7 @@ constexpr int kStageBytes = kTileV * kStageK / 2;
 // as the 16-byte blocks they lie in
 constexpr int kScalePitch = 272;
 constexpr int kZeroPitch = 144;
-constexpr int kSlots = 4;                   // chunks in flight between unpacking and epilogue
-constexpr int kACols = 256;                 // tensor memory: the chunks' weights, then the accumulators
-constexpr int kDCols = 256;
+constexpr int kTmemCols = 512;              // the chunks' weights, then the accumulators
 constexpr int kMaxCtas = 152;               // persistent CTAs the workspace is sized for
 constexpr int kI4Threads = 512;
 constexpr size_t kCounterBytes = 1024;      // workspace: one counter per CTA, then the partial sums
@@ -81,18 +79,25 @@ struct Shape {
   static constexpr int kEpiGroups = N == 128 ? 2 : 1;    // warpgroups
   static constexpr int kUnpackGroups = 3 - kEpiGroups;
   static constexpr int kCols = N / kEpiGroups;           // rows of x per epilogue thread
-  // a chunk: at most 128 columns, and few enough groups that their
-  // accumulators take 128 tensor-memory columns (two buffers fit)
-  static constexpr int kChunkK = N * (128 / G) <= 128 ? 128 : 128 * G / N;
+  // a chunk (what is handed from unpacking to MMA to epilogue at once): the
+  // whole unit, or as many columns as leave its accumulators 128
+  // tensor-memory columns
+  static constexpr int kChunkK = N * (kStageK / G) <= 128 ? kStageK : 128 * G / N;
   static constexpr int kChunks = kStageK / kChunkK;      // per unit
   static constexpr int kGroups = kChunkK / G;            // per chunk
   static constexpr int kDBuf = kGroups * N;              // columns of a chunk's accumulators
-  static constexpr int kDBufs = kDCols / kDBuf < kSlots ? kDCols / kDBuf : kSlots;
+  // chunks in flight: their weights take kChunkK / 2 columns each
+  static constexpr int kSlots = kChunkK < kStageK ? 4 : kDBuf <= 64 ? 3 : 2;
+  static constexpr int kACols = kSlots * (kChunkK / 2);
+  static constexpr int kDBufs = (kTmemCols - kACols) / kDBuf < kSlots ? (kTmemCols - kACols) / kDBuf : kSlots;
+  static_assert(kDBufs >= 2, "products and epilogue overlap");
+  // a piece: what one warpgroup unpacks at a time
+  static constexpr int kPieceK = kChunkK < 128 ? kChunkK : 128;
+  static constexpr int kPieces = kStageK / kPieceK / kUnpackGroups;  // per unit and warpgroup
   static constexpr int kXBytes = N * kStageK * 2;        // the rows' columns of a unit: four 64-column blocks
   // the rows come from L2, the weights from HBM: the weights' ring is the deep one
   static constexpr int kXStages = N <= 32 ? 4 : N == 64 ? 3 : 2;
   static constexpr int kWStages = N <= 32 ? 8 : N == 64 ? 6 : 4;
-  static constexpr int kLd = kCols == 32 ? 32 : 16;      // tensor-memory columns per load
   // registers per thread (warps 0-3, unpacking, epilogue): the launch gives
   // every thread 128, and the shares add up to no more
   static constexpr int kRegsCopy = 64;
@@ -143,6 +148,35 @@ __device__ __forceinline__ void umma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, u
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1 : 0)
       : "memory");
+}
+
+// kN (16, 32 or 64) consecutive float32 columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float* v) {
+  uint32_t r[64];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, "
+      "%37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, "
+      "%59, %60, %61, %62, %63}, [%64];\n tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+}
+template <int kN>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float* v) {
+  static_assert(kN == 16 || kN == 32 || kN == 64, "widths that have a load");
+  if constexpr (kN == 16) tmem_ld16(taddr, v);
+  else if constexpr (kN == 32) tmem_ld32(taddr, v);
+  else tmem_ld64(taddr, v);
 }
 
 // 32 columns of this warp's 32 lanes from 32 registers.
@@ -280,7 +314,7 @@ __global__ void __launch_bounds__(kI4Threads, 1)
   __shared__ uint64_t wfull[S::kWStages], wempty[S::kWStages], xfull[S::kXStages], xempty[S::kXStages];
   // ready: a chunk's weights are in tensor memory and its accumulators are
   // free; done: its products are complete (its weights' slot is free again)
-  __shared__ uint64_t ready[kSlots], done[kSlots], drain;
+  __shared__ uint64_t ready[S::kSlots], done[S::kSlots], drain;
   // left: the epilogue's partial sums of the CTA's i-th shared tile are in the
   // workspace; settled: it is known whether this CTA adds them all (won_s)
   __shared__ uint64_t left_s[2], settled[2];
@@ -311,8 +345,8 @@ __global__ void __launch_bounds__(kI4Threads, 1)
       mbar_init(&xfull[s], 1);
       mbar_init(&xempty[s], 1);
     }
-    for (int s = 0; s < kSlots; ++s) {
-      mbar_init(&ready[s], 4 + 4 * S::kEpiGroups);
+    for (int s = 0; s < S::kSlots; ++s) {
+      mbar_init(&ready[s], 4 * (S::kChunkK / S::kPieceK) + 4 * S::kEpiGroups);
       mbar_init(&done[s], 1);
     }
     mbar_init(&drain, 1);
@@ -326,13 +360,13 @@ __global__ void __launch_bounds__(kI4Threads, 1)
     mbar_fence_init();
   }
   if (warp == 1) {
-    tmem_alloc(&tmem_s, kACols + kDCols);
+    tmem_alloc(&tmem_s, kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem_a = tmem_s, tmem_d = tmem_s + kACols;
+  const uint32_t tmem_a = tmem_s, tmem_d = tmem_s + S::kACols;
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsCopy));
@@ -372,7 +406,7 @@ __global__ void __launch_bounds__(kI4Threads, 1)
       // is a constant: a lone thread's instruction latency is the limit here.
       constexpr uint32_t idesc = umma_idesc_bf16_f32(kTileV, N);
       Ring<S::kXStages> x;
-      Ring<kSlots> a;
+      Ring<S::kSlots> a;
       int db = 0;
       bool ok = true;
       for (int it = 0; it < units; ++it) {
@@ -452,9 +486,8 @@ __global__ void __launch_bounds__(kI4Threads, 1)
   } else if (warp < 4 + 4 * S::kUnpackGroups) {
     // ---------------- unpacking ----------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsUnpack));
-    // chunk i of a unit is unpacked by warpgroup i % kUnpackGroups
-    constexpr int kMine = S::kChunks / S::kUnpackGroups;  // chunks per unit
-    constexpr int kVecs = S::kChunkK / 32;                // 16-byte vectors of an entry's chunk, one zero point each
+    // piece i of a unit is unpacked by warpgroup i % kUnpackGroups
+    constexpr int kVecs = S::kPieceK / 32;  // 16-byte vectors of an entry's piece, one zero point each
     const int grp = (warp - 4) >> 2, q = warp & 3;
     const int row = q * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
@@ -463,43 +496,47 @@ __global__ void __launch_bounds__(kI4Threads, 1)
     // low bits of addresses: where a row of zero points starts in its first block
     const uint32_t zeros_at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(P.zeros));
     const uint32_t zeros_ld = static_cast<uint32_t>(P.zeros_ld);
-    uint32_t zero[kMine * kVecs];  // of this warpgroup's 32-column vectors
+    uint32_t minus[S::kPieces * kVecs];  // -z / 64 twice, of this warpgroup's 32-column vectors
 #pragma unroll
-    for (int i = 0; i < kMine * kVecs; ++i) zero[i] = 8u;
+    for (int i = 0; i < S::kPieces * kVecs; ++i) minus[i] = minus_zero(8u);
     Ring<S::kWStages> w;
-    Ring<kSlots> a;
-    for (int i = 0; i < grp; ++i) a.next();
+    Ring<S::kSlots> a;
+    if constexpr (S::kPieceK == S::kChunkK)
+      for (int i = 0; i < grp; ++i) a.next();
     bool ok = true;
-    for (int it = 0; it < units && ok; ++it, w.next(), c.next(P)) {
+    for (int it = 0; it < units && ok; ++it) {
       ok = i4_wait(&wfull[w.slot], w.parity, fault);
       if (!ok) break;
       if (P.zeros) {
         const unsigned char* z = sring + w.slot * S::kSideBytes + S::kPer * kScalePitch + row;
         const uint32_t lead = zeros_at + static_cast<uint32_t>(c.at.vt * kTileV);
 #pragma unroll
-        for (int j = 0; j < kMine; ++j)
+        for (int j = 0; j < S::kPieces; ++j)
 #pragma unroll
           for (int i = 0; i < kVecs; ++i) {
-            const int g = ((j * S::kUnpackGroups + grp) * S::kChunkK + i * 32) / G;  // of the unit
-            zero[j * kVecs + i] =
-                z[g * kZeroPitch + ((lead + static_cast<uint32_t>(c.at.k * S::kPer + g) * zeros_ld) & 15u)];
+            const int g = ((j * S::kUnpackGroups + grp) * S::kPieceK + i * 32) / G;  // of the unit
+            minus[j * kVecs + i] = minus_zero(
+                z[g * kZeroPitch + ((lead + static_cast<uint32_t>(c.at.k * S::kPer + g) * zeros_ld) & 15u)]);
           }
+        c.next(P);
       }
       const unsigned char* src = wring + w.slot * kStageBytes + row * (kStageK / 2);
 #pragma unroll
-      for (int j = 0; j < kMine; ++j) {
-        const int i = j * S::kUnpackGroups + grp;  // chunk of the unit
+      for (int j = 0; j < S::kPieces; ++j) {
+        const int i = j * S::kUnpackGroups + grp;  // piece of the unit
         uint4 code[kVecs];
 #pragma unroll
         for (int e = 0; e < kVecs; ++e) code[e] = lds16(src + (((i * kVecs + e) ^ key) << 4));
-        if (j + 1 == kMine) {  // this warp's last read of the stage
+        if (j + 1 == S::kPieces) {  // this warp's last read of the stage
           __syncwarp();
-          if (lane == 0) mbar_arrive(&wempty[w.slot]);
+          if (leader) mbar_arrive(&wempty[w.slot]);
+          w.next();
         }
         ok = i4_wait(&done[a.slot], a.parity ^ 1u, fault);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t dst = tmem_a + a.slot * (S::kChunkK / 2) + lanes;
+        const uint32_t dst =
+            tmem_a + a.slot * (S::kChunkK / 2) + (i * S::kPieceK % S::kChunkK) / 2 + lanes;
         if constexpr (kVecs >= 2) {
 #pragma unroll
           for (int h = 0; h < kVecs / 2; ++h) {
@@ -507,7 +544,7 @@ __global__ void __launch_bounds__(kI4Threads, 1)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const uint4 x = code[2 * h + e];
-              const uint32_t z = minus_zero(zero[j * kVecs + 2 * h + e]);
+              const uint32_t z = minus[j * kVecs + 2 * h + e];
               unpack8(x.x, z, r + 16 * e);
               unpack8(x.y, z, r + 16 * e + 4);
               unpack8(x.z, z, r + 16 * e + 8);
@@ -517,7 +554,7 @@ __global__ void __launch_bounds__(kI4Threads, 1)
           }
         } else {
           uint32_t r[16];
-          const uint32_t z = minus_zero(zero[j]);
+          const uint32_t z = minus[j];
           unpack8(code[0].x, z, r);
           unpack8(code[0].y, z, r + 4);
           unpack8(code[0].z, z, r + 8);
@@ -527,9 +564,13 @@ __global__ void __launch_bounds__(kI4Threads, 1)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ready[a.slot]);
+        if (leader) mbar_arrive(&ready[a.slot]);
+        if constexpr (S::kPieceK == S::kChunkK) {
 #pragma unroll
-        for (int n = 0; n < S::kUnpackGroups; ++n) a.next();
+          for (int n = 0; n < S::kUnpackGroups; ++n) a.next();
+        } else if (S::kUnpackGroups == 2 || j == 1) {
+          a.next();
+        }
       }
     }
   } else {
@@ -566,89 +607,99 @@ __global__ void __launch_bounds__(kI4Threads, 1)
     float2 acc[S::kCols / 2];
 #pragma unroll
     for (int i = 0; i < S::kCols / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-    Cursor cn(start, u0, u1, P);  // one unit ahead
-    Place c = cn.at;
-    const uint32_t scales_at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(P.scales));
-    const uint32_t scales_ld = static_cast<uint32_t>(P.scales_ld);
     // the accumulators of the first chunks are free
-    if (lane == 0)
+    if (leader)
       for (int i = 0; i < S::kDBufs; ++i) mbar_arrive(&ready[i]);
     Ring<S::kWStages> w;
-    Ring<kSlots> a;
+    Ring<S::kSlots> a;
     int db = 0;
-    int begin = c.k;  // first stage of the sums in hand
-    int shared = 0;   // shared tiles so far
-    int tail_left = u1 - start;  // units until the list leaves the tail
+    int shared = 0;  // shared tiles so far
+    // a run of units of one tile at a time
+    Place c;
+    c.set(start, P);
+    int todo = units, run = min(P.nk - c.k, u1 - start), begin = c.k;
     bool ok = true;
-    for (int it = 0; it < units && ok; ++it) {
-      cn.next(P);
-      // the scales of the unit's groups
-      ok = i4_wait(&wfull[w.slot], w.parity, fault);
-      if (!ok) break;
-      uint32_t s_now[S::kPer];
-      {
-        const unsigned char* sp = sring + w.slot * S::kSideBytes + row * 2;
-        const uint32_t lead = scales_at + static_cast<uint32_t>(c.vt * kTileV) * 2u;
-#pragma unroll
-        for (int i = 0; i < S::kPer; ++i)
-          s_now[i] = *reinterpret_cast<const unsigned short*>(
-              sp + i * kScalePitch + ((lead + static_cast<uint32_t>(c.k * S::kPer + i) * scales_ld * 2u) & 15u));
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&wempty[w.slot]);
-        w.next();
-      }
-      const int left = P.d - c.k * kStageK;
-#pragma unroll
-      for (int i = 0; i < S::kChunks; ++i) {
-        ok = i4_wait(&done[a.slot], a.parity, fault);
+    while (todo > 0) {
+      // low bits of addresses: where a row of scales starts in its first block
+      const uint32_t step = static_cast<uint32_t>(P.scales_ld) * 2u;
+      uint32_t lead = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(P.scales)) +
+                      static_cast<uint32_t>(c.vt * kTileV) * 2u + static_cast<uint32_t>(c.k * S::kPer) * step;
+      int width = P.d - c.k * kStageK;  // columns from the unit's first on
+      for (int it = 0; it < run; ++it, width -= kStageK) {
+        ok = i4_wait(&wfull[w.slot], w.parity, fault);
         if (!ok) break;
-        tc_fence_after();
+        uint32_t s_now[S::kPer];  // the scales of the unit's groups
+        const unsigned char* sp = sring + w.slot * S::kSideBytes + row * 2;
 #pragma unroll
-        for (int g = 0; g < S::kGroups; ++g) {
-          if (i * S::kChunkK + g * G < left) {
-            const float s = __uint_as_float(s_now[i * S::kGroups + g] << 16);
-            const float2 ss = make_float2(s, s);
-            const uint32_t src = tmem_d + db * S::kDBuf + g * N + col0 + lanes;
+        for (int i = 0; i < S::kPer; ++i, lead += step)
+          s_now[i] = *reinterpret_cast<const unsigned short*>(sp + i * kScalePitch + (lead & 15u));
+        __syncwarp();
+        if (leader) mbar_arrive(&wempty[w.slot]);
+        w.next();
 #pragma unroll
-            for (int n = 0; n < S::kCols; n += S::kLd) {
-              float v[S::kLd];
-              if constexpr (S::kLd == 32) tmem_ld32(src + n, v);
-              else tmem_ld16(src + n, v);
+        for (int i = 0; i < S::kChunks; ++i) {
+          ok = i4_wait(&done[a.slot], a.parity, fault);
+          if (!ok) break;
+          tc_fence_after();
+          // the chunk's accumulators, group by group, in loads of at most 64 columns
+          constexpr int kAll = S::kGroups * S::kCols;
+          constexpr int kLd = kAll < 64 ? kAll : 64;
+          const uint32_t src = tmem_d + db * S::kDBuf + lanes;
 #pragma unroll
-              for (int e = 0; e < S::kLd; e += 2)
-                acc[(n + e) / 2] = ffma2(ss, make_float2(v[e], v[e + 1]), acc[(n + e) / 2]);
+          for (int n = 0; n < kAll; n += kLd) {
+            float v[kLd];
+            // (with two epilogue warpgroups a chunk of more than one group is read group by group)
+            tmem_ld<kLd>(src + n / S::kCols * N + col0 + n % S::kCols, v);
+#pragma unroll
+            for (int e = 0; e < kLd; e += 2) {
+              const int g = i * S::kGroups + (n + e) / S::kCols;
+              // (a group beyond the width has no scale and is not added)
+              if (g * G < width) {
+                const float s = __uint_as_float(s_now[g] << 16);
+                float2& sum = acc[(n + e) % S::kCols / 2];
+                sum = ffma2(make_float2(s, s), make_float2(v[e], v[e + 1]), sum);
+              }
             }
           }
+          tc_fence_before();
+          __syncwarp();
+          // these accumulators are the ones of the chunk kDBufs further on
+          if (leader) mbar_arrive(&ready[(a.slot + S::kDBufs) % S::kSlots]);
+          a.next();
+          if (++db == S::kDBufs) db = 0;
         }
-        tc_fence_before();
-        __syncwarp();
-        // these accumulators are the ones of the chunk kDBufs further on
-        if (lane == 0) mbar_arrive(&ready[(a.slot + S::kDBufs) % kSlots]);
-        a.next();
-        if (++db == S::kDBufs) db = 0;
+        if (!ok) break;
       }
       if (!ok) break;
-      const bool ends = c.k + 1 == P.nk, leaves = --tail_left == 0;
-      if (ends || leaves) {
-        if (begin == 0 && ends) {
-          store(c, acc);
-        } else {
-          // a shared tile: leave the sums in this CTA's slot
-          float* mine = P.partials + (static_cast<long long>(2 * cta + (begin == 0 ? 1 : 0)) * N + col0) * kTileV + row;
+      todo -= run;
+      c.k += run;
+      if (begin == 0 && c.k == P.nk) {
+        store(c, acc);
+      } else {
+        // a shared tile: leave the sums in this CTA's slot
+        float* mine = P.partials + (static_cast<long long>(2 * cta + (begin == 0 ? 1 : 0)) * N + col0) * kTileV + row;
 #pragma unroll
-          for (int i = 0; i < S::kCols / 2; ++i) {
-            __stcg(mine + (2 * i) * kTileV, acc[i].x);
-            __stcg(mine + (2 * i + 1) * kTileV, acc[i].y);
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&left_s[shared]);
-          ++shared;
+        for (int i = 0; i < S::kCols / 2; ++i) {
+          __stcg(mine + (2 * i) * kTileV, acc[i].x);
+          __stcg(mine + (2 * i + 1) * kTileV, acc[i].y);
         }
-#pragma unroll
-        for (int i = 0; i < S::kCols / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-        begin = cn.at.k;
+        __syncwarp();
+        if (leader) mbar_arrive(&left_s[shared]);
+        ++shared;
       }
-      c = cn.at;
+#pragma unroll
+      for (int i = 0; i < S::kCols / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+      if (c.k < P.nk) {
+        c.set(u0, P);  // the tail was left: on to the head
+      } else {
+        c.k = 0;
+        if (++c.vt == P.ntv) {
+          c.vt = 0;
+          ++c.rb;
+        }
+      }
+      run = min(P.nk - c.k, todo);
+      begin = c.k;
     }
     // the shared tiles whose last part this CTA was: all parts, in the order of the columns
     for (int i = 0; i < shared && ok; ++i) {
@@ -685,7 +736,7 @@ __global__ void __launch_bounds__(kI4Threads, 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_s, kACols + kDCols);
+    tmem_dealloc(tmem_s, kTmemCols);
   }
 }
 
