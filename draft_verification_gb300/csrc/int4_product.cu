@@ -55,7 +55,6 @@ constexpr int kScalePitch = 272;
 constexpr int kZeroPitch = 144;
 constexpr int kTmemCols = 512;              // the chunks' weights, then the accumulators
 constexpr int kMaxCtas = 152;               // persistent CTAs the workspace is sized for
-constexpr int kI4Threads = 512;
 constexpr size_t kCounterBytes = 1024;      // workspace: one counter per CTA, then the partial sums
 static_assert(kMaxCtas * 4 <= kCounterBytes, "one counter per CTA");
 
@@ -77,7 +76,8 @@ struct I4Params {
 template <int N, int G>
 struct Shape {
   static constexpr int kEpiGroups = N == 128 ? 2 : 1;    // warpgroups
-  static constexpr int kUnpackGroups = 3 - kEpiGroups;
+  static constexpr int kUnpackGroups = N == 128 ? 2 : 4;
+  static constexpr int kThreads = 128 * (1 + kUnpackGroups + kEpiGroups);
   static constexpr int kCols = N / kEpiGroups;           // rows of x per epilogue thread
   // a chunk (what is handed from unpacking to MMA to epilogue at once): the
   // whole unit, or as many columns as leave its accumulators 128
@@ -92,18 +92,19 @@ struct Shape {
   static constexpr int kDBufs = (kTmemCols - kACols) / kDBuf < kSlots ? (kTmemCols - kACols) / kDBuf : kSlots;
   static_assert(kDBufs >= 2, "products and epilogue overlap");
   // a piece: what one warpgroup unpacks at a time
-  static constexpr int kPieceK = kChunkK < 128 ? kChunkK : 128;
+  static constexpr int kPieceK = kChunkK < 64 ? kChunkK : 64;
   static constexpr int kPieces = kStageK / kPieceK / kUnpackGroups;  // per unit and warpgroup
   static constexpr int kXBytes = N * kStageK * 2;        // the rows' columns of a unit: four 64-column blocks
   // the rows come from L2, the weights from HBM: the weights' ring is the deep one
   static constexpr int kXStages = N <= 32 ? 4 : N == 64 ? 3 : 2;
   static constexpr int kWStages = N <= 32 ? 8 : N == 64 ? 6 : 4;
-  // registers per thread (warps 0-3, unpacking, epilogue): the launch gives
-  // every thread 128, and the shares add up to no more
-  static constexpr int kRegsCopy = 64;
-  static constexpr int kRegsUnpack = kUnpackGroups == 2 ? 96 : 104;
-  static constexpr int kRegsEpi = kEpiGroups == 1 ? 200 : 168;
-  static_assert(128 * (kRegsCopy + kUnpackGroups * kRegsUnpack + kEpiGroups * kRegsEpi) <= kI4Threads * 128,
+  // registers per thread (warps 0-3, unpacking, epilogue): shares of what the
+  // launch holds
+  static constexpr int kRegsLaunch = 65536 / kThreads / 8 * 8;
+  static constexpr int kRegsCopy = 40;
+  static constexpr int kRegsUnpack = kUnpackGroups == 4 ? 72 : 80;
+  static constexpr int kRegsEpi = kEpiGroups == 1 ? 152 : 136;
+  static_assert(128 * (kRegsCopy + kUnpackGroups * kRegsUnpack + kEpiGroups * kRegsEpi) <= kThreads * kRegsLaunch,
                 "no more registers than the launch holds");
   // scales and zero points of a weight stage: one row of a tile per group
   static constexpr int kPer = kStageK / G;
@@ -150,33 +151,12 @@ __device__ __forceinline__ void umma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, u
       : "memory");
 }
 
-// kN (16, 32 or 64) consecutive float32 columns of this warp's 32 lanes.
-__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float* v) {
-  uint32_t r[64];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, "
-      "%37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, "
-      "%59, %60, %61, %62, %63}, [%64];\n tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
-        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
-        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
-        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
-        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
-      : "r"(taddr)
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
-}
+// kN (16 or 32) consecutive float32 columns of this warp's 32 lanes.
 template <int kN>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, float* v) {
-  static_assert(kN == 16 || kN == 32 || kN == 64, "widths that have a load");
+  static_assert(kN == 16 || kN == 32, "widths that have a load");
   if constexpr (kN == 16) tmem_ld16(taddr, v);
-  else if constexpr (kN == 32) tmem_ld32(taddr, v);
-  else tmem_ld64(taddr, v);
+  else tmem_ld32(taddr, v);
 }
 
 // 32 columns of this warp's 32 lanes from 32 registers.
@@ -306,7 +286,7 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 template <int N, int G>
-__global__ void __launch_bounds__(kI4Threads, 1)
+__global__ void __launch_bounds__(Shape<N, G>::kThreads, 1)
     int4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                         const I4Params P) {
   using S = Shape<N, G>;
@@ -500,9 +480,6 @@ __global__ void __launch_bounds__(kI4Threads, 1)
 #pragma unroll
     for (int i = 0; i < S::kPieces * kVecs; ++i) minus[i] = minus_zero(8u);
     Ring<S::kWStages> w;
-    Ring<S::kSlots> a;
-    if constexpr (S::kPieceK == S::kChunkK)
-      for (int i = 0; i < grp; ++i) a.next();
     bool ok = true;
     for (int it = 0; it < units && ok; ++it) {
       ok = i4_wait(&wfull[w.slot], w.parity, fault);
@@ -532,45 +509,29 @@ __global__ void __launch_bounds__(kI4Threads, 1)
           if (leader) mbar_arrive(&wempty[w.slot]);
           w.next();
         }
-        ok = i4_wait(&done[a.slot], a.parity ^ 1u, fault);
+        // the piece's chunk, counted from the CTA's first
+        const unsigned n = static_cast<unsigned>(it * S::kChunks + i * S::kPieceK / S::kChunkK);
+        const unsigned slot = n % S::kSlots;
+        ok = i4_wait(&done[slot], ((n / S::kSlots) & 1u) ^ 1u, fault);
         if (!ok) break;
         tc_fence_after();
         const uint32_t dst =
-            tmem_a + a.slot * (S::kChunkK / 2) + (i * S::kPieceK % S::kChunkK) / 2 + lanes;
-        if constexpr (kVecs >= 2) {
+            tmem_a + slot * (S::kChunkK / 2) + static_cast<uint32_t>(i * S::kPieceK % S::kChunkK) / 2 + lanes;
+        uint32_t r[16 * kVecs];
 #pragma unroll
-          for (int h = 0; h < kVecs / 2; ++h) {
-            uint32_t r[32];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint4 x = code[2 * h + e];
-              const uint32_t z = minus[j * kVecs + 2 * h + e];
-              unpack8(x.x, z, r + 16 * e);
-              unpack8(x.y, z, r + 16 * e + 4);
-              unpack8(x.z, z, r + 16 * e + 8);
-              unpack8(x.w, z, r + 16 * e + 12);
-            }
-            tmem_st32(dst + 32 * h, r);
-          }
-        } else {
-          uint32_t r[16];
-          const uint32_t z = minus[j];
-          unpack8(code[0].x, z, r);
-          unpack8(code[0].y, z, r + 4);
-          unpack8(code[0].z, z, r + 8);
-          unpack8(code[0].w, z, r + 12);
-          tmem_st16(dst, r);
+        for (int e = 0; e < kVecs; ++e) {
+          const uint32_t z = minus[j * kVecs + e];
+          unpack8(code[e].x, z, r + 16 * e);
+          unpack8(code[e].y, z, r + 16 * e + 4);
+          unpack8(code[e].z, z, r + 16 * e + 8);
+          unpack8(code[e].w, z, r + 16 * e + 12);
         }
+        if constexpr (kVecs == 2) tmem_st32(dst, r);
+        else tmem_st16(dst, r);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (leader) mbar_arrive(&ready[a.slot]);
-        if constexpr (S::kPieceK == S::kChunkK) {
-#pragma unroll
-          for (int n = 0; n < S::kUnpackGroups; ++n) a.next();
-        } else if (S::kUnpackGroups == 2 || j == 1) {
-          a.next();
-        }
+        if (leader) mbar_arrive(&ready[slot]);
       }
     }
   } else {
@@ -641,9 +602,9 @@ __global__ void __launch_bounds__(kI4Threads, 1)
           ok = i4_wait(&done[a.slot], a.parity, fault);
           if (!ok) break;
           tc_fence_after();
-          // the chunk's accumulators, group by group, in loads of at most 64 columns
+          // the chunk's accumulators, group by group, in loads of at most 32 columns
           constexpr int kAll = S::kGroups * S::kCols;
-          constexpr int kLd = kAll < 64 ? kAll : 64;
+          constexpr int kLd = kAll < 32 ? kAll : 32;
           const uint32_t src = tmem_d + db * S::kDBuf + lanes;
 #pragma unroll
           for (int n = 0; n < kAll; n += kLd) {
@@ -826,7 +787,7 @@ spec_status launch_product(const spec_int4_product_args& a, cudaStream_t s) {
   CUtensorMap tw, tx;
   if (!weight_map(&tw, a.codes, a.V, a.d, a.codes_ld) || !rows_map(&tx, a.x, a.R, a.d, a.x_ld, N)) return SPEC_ECUDA;
   if (raise_smem<N, G>() != cudaSuccess) return SPEC_ECUDA;
-  int4_product_kernel<N, G><<<ctas, kI4Threads, Shape<N, G>::kSmem, s>>>(tw, tx, P);
+  int4_product_kernel<N, G><<<ctas, Shape<N, G>::kThreads, Shape<N, G>::kSmem, s>>>(tw, tx, P);
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
 }
 
