@@ -75,8 +75,8 @@ struct I4Params {
 // N rows and groups of G columns.
 template <int N, int G>
 struct Shape {
-  static constexpr int kEpiGroups = N == 128 ? 2 : 1;    // warpgroups
-  static constexpr int kUnpackGroups = N == 128 ? 2 : 4;
+  static constexpr int kEpiGroups = N >= 64 ? 2 : 1;     // warpgroups
+  static constexpr int kUnpackGroups = N == 128 ? 3 : 4;
   static constexpr int kThreads = 128 * (1 + kUnpackGroups + kEpiGroups);
   static constexpr int kCols = N / kEpiGroups;           // rows of x per epilogue thread
   // a chunk (what is handed from unpacking to MMA to epilogue at once): the
@@ -91,9 +91,9 @@ struct Shape {
   static constexpr int kACols = kSlots * (kChunkK / 2);
   static constexpr int kDBufs = (kTmemCols - kACols) / kDBuf < kSlots ? (kTmemCols - kACols) / kDBuf : kSlots;
   static_assert(kDBufs >= 2, "products and epilogue overlap");
-  // a piece: what one warpgroup unpacks at a time
-  static constexpr int kPieceK = kChunkK < 64 ? kChunkK : 64;
-  static constexpr int kPieces = kStageK / kPieceK / kUnpackGroups;  // per unit and warpgroup
+  // a piece: what one warpgroup unpacks at a time; the warpgroups take turns
+  static constexpr int kPieceK = kChunkK < 128 ? kChunkK : 128;
+  static constexpr int kPieces = kStageK / kPieceK;      // per unit
   static constexpr int kXBytes = N * kStageK * 2;        // the rows' columns of a unit: four 64-column blocks
   // the rows come from L2, the weights from HBM: the weights' ring is the deep one
   static constexpr int kXStages = N <= 32 ? 4 : N == 64 ? 3 : 2;
@@ -102,8 +102,8 @@ struct Shape {
   // launch holds
   static constexpr int kRegsLaunch = 65536 / kThreads / 8 * 8;
   static constexpr int kRegsCopy = 40;
-  static constexpr int kRegsUnpack = kUnpackGroups == 4 ? 72 : 80;
-  static constexpr int kRegsEpi = kEpiGroups == 1 ? 152 : 136;
+  static constexpr int kRegsUnpack = kThreads == 896 ? 64 : 72;
+  static constexpr int kRegsEpi = N == 128 ? 112 : N == 64 ? 104 : 152;
   static_assert(128 * (kRegsCopy + kUnpackGroups * kRegsUnpack + kEpiGroups * kRegsEpi) <= kThreads * kRegsLaunch,
                 "no more registers than the launch holds");
   // scales and zero points of a weight stage: one row of a tile per group
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(Shape<N, G>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kWStages; ++s) {
       mbar_init(&wfull[s], 1);
-      mbar_init(&wempty[s], 4 * (S::kUnpackGroups + S::kEpiGroups));
+      mbar_init(&wempty[s], 4 * (S::kPieces + S::kEpiGroups));
     }
     for (int s = 0; s < S::kXStages; ++s) {
       mbar_init(&xfull[s], 1);
@@ -466,73 +466,74 @@ __global__ void __launch_bounds__(Shape<N, G>::kThreads, 1)
   } else if (warp < 4 + 4 * S::kUnpackGroups) {
     // ---------------- unpacking ----------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsUnpack));
-    // piece i of a unit is unpacked by warpgroup i % kUnpackGroups
     constexpr int kVecs = S::kPieceK / 32;  // 16-byte vectors of an entry's piece, one zero point each
     const int grp = (warp - 4) >> 2, q = warp & 3;
     const int row = q * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
     const uint32_t key = static_cast<uint32_t>(row & 7);
-    Cursor c(start, u0, u1, P);
+    Cursor c(start, u0, u1, P);  // (with zero points) the piece's unit
+    int c_it = 0;
     // low bits of addresses: where a row of zero points starts in its first block
     const uint32_t zeros_at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(P.zeros));
     const uint32_t zeros_ld = static_cast<uint32_t>(P.zeros_ld);
-    uint32_t minus[S::kPieces * kVecs];  // -z / 64 twice, of this warpgroup's 32-column vectors
+    uint32_t minus[kVecs];  // -z / 64 twice, of the piece's 32-column vectors
 #pragma unroll
-    for (int i = 0; i < S::kPieces * kVecs; ++i) minus[i] = minus_zero(8u);
-    Ring<S::kWStages> w;
-    bool ok = true;
-    for (int it = 0; it < units && ok; ++it) {
-      ok = i4_wait(&wfull[w.slot], w.parity, fault);
-      if (!ok) break;
+    for (int i = 0; i < kVecs; ++i) minus[i] = minus_zero(8u);
+    // pieces counted from the CTA's first; this warpgroup's are n % kUnpackGroups == grp
+    for (int n = grp; n < units * S::kPieces; n += S::kUnpackGroups) {
+      const int it = n / S::kPieces, i = n % S::kPieces;  // unit, and piece of the unit
+      const int ws = it % S::kWStages;
+      if (!i4_wait(&wfull[ws], static_cast<unsigned>(it / S::kWStages) & 1u, fault)) break;
+      const unsigned char* src = wring + ws * kStageBytes + row * (kStageK / 2);
+      uint4 code[kVecs];
+#pragma unroll
+      for (int e = 0; e < kVecs; ++e) code[e] = lds16(src + (((i * kVecs + e) ^ key) << 4));
       if (P.zeros) {
-        const unsigned char* z = sring + w.slot * S::kSideBytes + S::kPer * kScalePitch + row;
+        for (; c_it < it; ++c_it) c.next(P);
+        const unsigned char* z = sring + ws * S::kSideBytes + S::kPer * kScalePitch + row;
         const uint32_t lead = zeros_at + static_cast<uint32_t>(c.at.vt * kTileV);
 #pragma unroll
-        for (int j = 0; j < S::kPieces; ++j)
-#pragma unroll
-          for (int i = 0; i < kVecs; ++i) {
-            const int g = ((j * S::kUnpackGroups + grp) * S::kPieceK + i * 32) / G;  // of the unit
-            minus[j * kVecs + i] = minus_zero(
-                z[g * kZeroPitch + ((lead + static_cast<uint32_t>(c.at.k * S::kPer + g) * zeros_ld) & 15u)]);
-          }
-        c.next(P);
-      }
-      const unsigned char* src = wring + w.slot * kStageBytes + row * (kStageK / 2);
-#pragma unroll
-      for (int j = 0; j < S::kPieces; ++j) {
-        const int i = j * S::kUnpackGroups + grp;  // piece of the unit
-        uint4 code[kVecs];
-#pragma unroll
-        for (int e = 0; e < kVecs; ++e) code[e] = lds16(src + (((i * kVecs + e) ^ key) << 4));
-        if (j + 1 == S::kPieces) {  // this warp's last read of the stage
-          __syncwarp();
-          if (leader) mbar_arrive(&wempty[w.slot]);
-          w.next();
-        }
-        // the piece's chunk, counted from the CTA's first
-        const unsigned n = static_cast<unsigned>(it * S::kChunks + i * S::kPieceK / S::kChunkK);
-        const unsigned slot = n % S::kSlots;
-        ok = i4_wait(&done[slot], ((n / S::kSlots) & 1u) ^ 1u, fault);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t dst =
-            tmem_a + slot * (S::kChunkK / 2) + static_cast<uint32_t>(i * S::kPieceK % S::kChunkK) / 2 + lanes;
-        uint32_t r[16 * kVecs];
-#pragma unroll
         for (int e = 0; e < kVecs; ++e) {
-          const uint32_t z = minus[j * kVecs + e];
-          unpack8(code[e].x, z, r + 16 * e);
-          unpack8(code[e].y, z, r + 16 * e + 4);
-          unpack8(code[e].z, z, r + 16 * e + 8);
-          unpack8(code[e].w, z, r + 16 * e + 12);
+          const int g = (i * S::kPieceK + e * 32) / G;  // of the unit
+          minus[e] = minus_zero(
+              z[g * kZeroPitch + ((lead + static_cast<uint32_t>(c.at.k * S::kPer + g) * zeros_ld) & 15u)]);
         }
-        if constexpr (kVecs == 2) tmem_st32(dst, r);
-        else tmem_st16(dst, r);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (leader) mbar_arrive(&ready[slot]);
       }
+      __syncwarp();
+      if (leader) mbar_arrive(&wempty[ws]);
+      const unsigned chunk = static_cast<unsigned>(it * S::kChunks + i * S::kPieceK / S::kChunkK);
+      const unsigned slot = chunk % S::kSlots;
+      if (!i4_wait(&done[slot], ((chunk / S::kSlots) & 1u) ^ 1u, fault)) break;
+      tc_fence_after();
+      const uint32_t dst =
+          tmem_a + slot * (S::kChunkK / 2) + static_cast<uint32_t>(i * S::kPieceK % S::kChunkK) / 2 + lanes;
+      if constexpr (kVecs == 1) {
+        uint32_t r[16];
+        unpack8(code[0].x, minus[0], r);
+        unpack8(code[0].y, minus[0], r + 4);
+        unpack8(code[0].z, minus[0], r + 8);
+        unpack8(code[0].w, minus[0], r + 12);
+        tmem_st16(dst, r);
+      } else {
+#pragma unroll
+        for (int h = 0; h < kVecs / 2; ++h) {
+          uint32_t r[32];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint4 x = code[2 * h + e];
+            const uint32_t z = minus[2 * h + e];
+            unpack8(x.x, z, r + 16 * e);
+            unpack8(x.y, z, r + 16 * e + 4);
+            unpack8(x.z, z, r + 16 * e + 8);
+            unpack8(x.w, z, r + 16 * e + 12);
+          }
+          tmem_st32(dst + 32 * h, r);
+        }
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (leader) mbar_arrive(&ready[slot]);
     }
   } else {
     // ---------------- epilogue ----------------
