@@ -2,22 +2,30 @@
 // grammar masks, each row with the tokens before its own position (chain or
 // tree).  The arithmetic and the argument meanings are in spec_logits.h.
 //
-// process_kernel: a CTA owns one slab of the vocabulary of one sequence and
-// streams that slab of the sequence's rows.  It builds one table for the slab
-// in shared memory - per token a 32-bit word (low 31 bits: occurrences that
-// count, bit 31: occurs in the prompt), the sum of its bias entries, and a
-// bitmap of the tokens that have either - by reading the whole history once,
-// and reuses it for every row.  From row to row only the drafted tokens on
-// the path change: where one of them lies in the slab (rows marked
-// beforehand, all in parallel) the CTA synchronises and one thread updates
-// the table; all other rows follow one another without a barrier.
+// process_kernel: a CTA owns one slab of the vocabulary of one sequence.  It
+// first streams that slab of the sequence's rows: a masked copy, which needs
+// nothing but the mask bits (a vector whose bits are all 0 is not read; in
+// place without masks nothing is streamed at all).  Then it rewrites the few
+// tokens that something applies to, read again from the input (through L2)
+// with all lanes busy: handled inside the stream, a token in a hundred would
+// put nearly every warp on the slow path.
 //
-// An element is read once and written once, in 16-byte vectors aligned in
-// memory: a row that starts at element m of its vector has tokens
-// [k e - m, k e - m + e) in vector k, so the table starts e - 1 tokens before
-// the slab and bitmap and mask bits are taken by funnel shifts.  Vectors that
-// stick out of the row, and rows whose output starts at another offset than
-// the input, are written element by element.
+// What applies is a table of the slab in shared memory - per token a 32-bit
+// word (low 31 bits: occurrences that count, bit 31: occurs in the prompt) and
+// the sum of its bias entries - built by reading the whole history once while
+// the first rows are in flight, and two lists of tokens: those that only the
+// history and the biases touch, which are the same for every row, so that all
+// (token, row) pairs are rewritten in any order; and those that are drafted,
+// whose counts depend on the row.  For the latter the rows go in order, and one
+// thread takes the table from row to row (leaving one path and entering the
+// next, up to their last common node) where a drafted token of the slab is
+// concerned (rows marked beforehand, all in parallel).
+//
+// The stream goes in 16-byte vectors aligned in memory: a row that starts at
+// element m of its vector has tokens [k e - m, k e - m + e) in vector k, so the
+// table starts e - 1 tokens before the slab and mask bits are taken by funnel
+// shifts.  Vectors that stick out of the row, and rows whose output starts at
+// another offset than the input, are written element by element.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -76,9 +84,6 @@ struct Lanes;  // the elements of a 16-byte vector
 template <>
 struct Lanes<bf16_t> {
   static constexpr int kN = 8;
-  static __device__ __forceinline__ float get(const uint32_t (&w)[4], int j) {
-    return (j & 1) ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
-  }
   static __device__ __forceinline__ uint32_t bits(const uint32_t (&w)[4], int j) {
     return (j & 1) ? w[j >> 1] >> 16 : w[j >> 1] & 0xffffu;
   }
@@ -90,17 +95,20 @@ struct Lanes<bf16_t> {
     asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(r) : "f"(x));
     return r;
   }
+  static __device__ __forceinline__ float widen(uint32_t b) { return __uint_as_float(b << 16); }
   static constexpr uint32_t kNegInf = 0xff80u;
+  static constexpr uint32_t kNegInf4 = 0xff80ff80u;
 };
 
 template <>
 struct Lanes<float> {
   static constexpr int kN = 4;
-  static __device__ __forceinline__ float get(const uint32_t (&w)[4], int j) { return __uint_as_float(w[j]); }
   static __device__ __forceinline__ uint32_t bits(const uint32_t (&w)[4], int j) { return w[j]; }
   static __device__ __forceinline__ void set_bits(uint32_t (&w)[4], int j, uint32_t b) { w[j] = b; }
   static __device__ __forceinline__ uint32_t round(float x) { return __float_as_uint(x); }
+  static __device__ __forceinline__ float widen(uint32_t b) { return __uint_as_float(b); }
   static constexpr uint32_t kNegInf = 0xff800000u;
+  static constexpr uint32_t kNegInf4 = 0xff800000u;
 };
 
 template <typename T>
@@ -120,28 +128,31 @@ __device__ __forceinline__ void store_bits(T* p, uint32_t b) {
   }
 }
 
-__host__ __device__ constexpr int slab_tokens(int elems, int vecs) { return kProcThreads * vecs * elems; }
 // table entries: the slab and the e - 1 tokens before it
-__host__ __device__ constexpr int table_tokens(int elems, int vecs) { return slab_tokens(elems, vecs) + elems - 1; }
-__host__ __device__ constexpr int bitmap_words(int elems, int vecs) { return (table_tokens(elems, vecs) + 31) / 32 + 1; }
+__host__ __device__ constexpr int table_tokens(int elems, int vecs) { return kProcThreads * vecs * elems + elems - 1; }
+__host__ __device__ constexpr int bitmap_words(int elems, int vecs) { return (table_tokens(elems, vecs) + 31) / 32; }
 
 template <typename T, int kVecs>
 __global__ void __launch_bounds__(kProcThreads) process_kernel(const ProcessParams P) {
   using L = Lanes<T>;
   constexpr int E = L::kN;
   constexpr uint32_t kFull = (1u << E) - 1u;
+  constexpr int kSlab = kProcThreads * kVecs * E;
   constexpr int kTable = table_tokens(E, kVecs);
   constexpr int kWords = bitmap_words(E, kVecs);
 
   extern __shared__ unsigned proc_dyn[];
   unsigned* count = proc_dyn;                         // [kTable]
-  unsigned* touched = count + kTable;                 // [kWords]
-  unsigned* change = touched + kWords;                // [kMaxRows / 32] rows before which the table changes
+  unsigned* drafted = count + kTable;                 // [kWords] tokens that some row's path may hold
+  unsigned* listed = drafted + kWords;                // [kWords] tokens in either list
+  unsigned* change = listed + kWords;                 // [kMaxRows / 32] rows before which the table changes
   int* s_tok = reinterpret_cast<int*>(change + kMaxRows / 32);  // [n]
   int* s_par = s_tok + P.n;                           // [n]
   int* s_mask = s_par + P.n;                          // [n]
   float* bias = reinterpret_cast<float*>(s_mask + P.n);  // [kTable], with biases
-  __shared__ int s_err;
+  // the lists grow towards each other: fixed tokens from the front, drafted ones from the back
+  unsigned short* list = reinterpret_cast<unsigned short*>(bias + (P.bias_tokens ? kTable : 0));  // [kTable]
+  __shared__ int s_err, s_fixed, s_drafted;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.z;
@@ -152,22 +163,26 @@ __global__ void __launch_bounds__(kProcThreads) process_kernel(const ProcessPara
   const bool checks = blockIdx.x == 0 && blockIdx.y == 0;
   const bool tree = P.parent != nullptr;
   const bool biased = P.bias_tokens != nullptr;
+  const bool stream = P.mask != nullptr || P.logits != P.out;
 
-  uint32_t cur[kVecs][4], nxt[kVecs][4];
-  uint32_t cur_ok[kVecs], nxt_ok[kVecs];  // mask bits of each vector
-
-  // Read row i's vectors and mask bits; mrow < 0: not masked.
-  auto load_row = [&](int i, int mrow, uint32_t (&w)[kVecs][4], uint32_t (&ok)[kVecs]) {
+  const auto mask_row = [&](int i) {
+    if (!P.mask) return -1;
     const long long row = static_cast<long long>(b) * P.n + i;
-    const T* src = static_cast<const T*>(P.logits) + row * P.ld;
-    const int m = static_cast<int>((row * P.ld) % E);
+    const long long mr = P.mask_index ? static_cast<long long>(__ldg(P.mask_index + row)) : row;
+    return mr < P.mask_rows ? static_cast<int>(mr) : -1;
+  };
+  const auto lead_of = [&](int i) {  // element of its first vector at which row i starts
+    return static_cast<int>(((static_cast<long long>(b) * P.n + i) * P.ld) % E);
+  };
+  // the mask bits of row i's vectors (mrow < 0: not masked; 0 for vectors outside the row)
+  const auto load_mask = [&](int i, int mrow, uint32_t (&ok)[kVecs]) {
+    const int m = lead_of(i);
     const unsigned* mk = mrow >= 0 ? P.mask + static_cast<long long>(mrow) * P.mask_ld : nullptr;
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
       const int t0 = (v0 + j * kProcThreads + tid) * E - m;
-      ok[j] = kFull;
-      if (t0 >= P.V) continue;
-      if (mk) {
+      ok[j] = t0 < P.V ? kFull : 0u;
+      if (mk && t0 < P.V) {
         if (t0 < 0) {
           ok[j] = (__ldg(mk) << -t0) & kFull;
         } else {
@@ -177,6 +192,16 @@ __global__ void __launch_bounds__(kProcThreads) process_kernel(const ProcessPara
           ok[j] = __funnelshift_r(a, c, s) & kFull;
         }
       }
+    }
+  };
+  // row i's vectors that have an allowed token
+  const auto load_row = [&](int i, const uint32_t (&ok)[kVecs], uint32_t (&w)[kVecs][4]) {
+    const T* src = static_cast<const T*>(P.logits) + (static_cast<long long>(b) * P.n + i) * P.ld;
+    const int m = lead_of(i);
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      const int t0 = (v0 + j * kProcThreads + tid) * E - m;
+      if (!ok[j]) continue;
       if (t0 >= 0 && t0 + E <= P.V) {
         const uint4 x = ld_row16(src + t0);
         w[j][0] = x.x;
@@ -191,26 +216,53 @@ __global__ void __launch_bounds__(kProcThreads) process_kernel(const ProcessPara
       }
     }
   };
-  auto mask_row = [&](int i) {
-    if (!P.mask) return -1;
+  const auto store_row = [&](int i, const uint32_t (&ok)[kVecs], uint32_t (&w)[kVecs][4]) {
     const long long row = static_cast<long long>(b) * P.n + i;
-    const long long mr = P.mask_index ? static_cast<long long>(__ldg(P.mask_index + row)) : row;
-    return mr < P.mask_rows ? static_cast<int>(mr) : -1;
+    T* dst = static_cast<T*>(P.out) + row * P.out_ld;
+    const int m = lead_of(i);
+    const bool same = static_cast<int>((row * P.out_ld) % E) == m;
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      const int t0 = (v0 + j * kProcThreads + tid) * E - m;
+      if (t0 >= P.V) continue;
+      if (!ok[j]) {
+        w[j][0] = w[j][1] = w[j][2] = w[j][3] = L::kNegInf4;
+      } else if (ok[j] != kFull) {
+#pragma unroll
+        for (int k = 0; k < E; ++k)
+          if (!((ok[j] >> k) & 1u)) L::set_bits(w[j], k, L::kNegInf);
+      }
+      if (same && t0 >= 0 && t0 + E <= P.V) {
+        if (!(kDebugChecks && misaligned16(dst + t0)))
+          *reinterpret_cast<uint4*>(dst + t0) = make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < E; ++k)
+          if (t0 + k >= 0 && t0 + k < P.V) store_bits(dst + t0 + k, L::bits(w[j], k));
+      }
+    }
   };
 
-  // the first row's loads are in flight while the table is built
-  load_row(r0, mask_row(r0), cur, cur_ok);
+  // The first row's vectors are in flight while the table is built, the
+  // second row's mask bits as well: the stream always reads the vectors of one
+  // row and the mask bits of the next ahead.
+  uint32_t cur[kVecs][4], nxt[kVecs][4], ok0[kVecs], ok1[kVecs], ok2[kVecs];
+  if (stream) {
+    load_mask(r0, mask_row(r0), ok0);
+    if (r0 + 1 < r1) load_mask(r0 + 1, mask_row(r0 + 1), ok1);
+    load_row(r0, ok0, cur);
+  }
 
   for (int i = tid; i < kTable; i += kProcThreads) count[i] = 0u;
-  for (int i = tid; i < kWords; i += kProcThreads) touched[i] = 0u;
+  for (int i = tid; i < kWords; i += kProcThreads) drafted[i] = listed[i] = 0u;
   for (int i = tid; i < kMaxRows / 32; i += kProcThreads) change[i] = 0u;
   if (biased)
     for (int i = tid; i < kTable; i += kProcThreads) bias[i] = 0.f;
-  if (tid == 0) s_err = 0;
+  if (tid == 0) s_err = s_fixed = s_drafted = 0;
   __syncthreads();
 
   int err = 0;
-  const auto touch = [&](int at) { atomicOr(&touched[at >> 5], 1u << (at & 31)); };
+  const auto in_slab = [&](int t) { return t >= 0 && static_cast<unsigned>(t - lo) < static_cast<unsigned>(kTable); };
 
   // the drafted tokens, the tree and the mask rows
   for (int i = tid; i < P.n; i += kProcThreads) {
@@ -228,15 +280,28 @@ __global__ void __launch_bounds__(kProcThreads) process_kernel(const ProcessPara
         p = 0;
       }
     }
-    s_tok[i] = used ? t : -1;
+    if (!used) t = -1;
+    s_tok[i] = t;
     s_par[i] = p;
     s_mask[i] = mask_row(i);
+    if (in_slab(t)) {
+      const int at = t - lo;
+      if (!((atomicOr(&drafted[at >> 5], 1u << (at & 31)) >> (at & 31)) & 1u))
+        list[kTable - 1 - atomicAdd(&s_drafted, 1)] = static_cast<unsigned short>(at);
+    }
     if (P.mask && P.mask_index) {
       const int mi = __ldg(P.mask_index + static_cast<long long>(b) * P.n + i);
       if (mi < -1 || mi >= P.mask_rows) err |= SPEC_ERR_MASK;
     }
   }
+  __syncthreads();
 
+  // a token that the history or a bias touches: into the list of fixed tokens unless it is drafted
+  const auto touch = [&](unsigned at) {
+    const unsigned bit = 1u << (at & 31);
+    if (!((drafted[at >> 5] | listed[at >> 5]) & bit) && !(atomicOr(&listed[at >> 5], bit) & bit))
+      list[atomicAdd(&s_fixed, 1)] = static_cast<unsigned short>(at);
+  };
   // the history
   if (P.history) {
     int len = P.history_len ? __ldg(P.history_len + b) : P.history_ld;
@@ -252,20 +317,20 @@ __global__ void __launch_bounds__(kProcThreads) process_kernel(const ProcessPara
 #pragma unroll
       for (int k = 0; k < kU; ++k) {
         const int at = base + k * kProcThreads + tid;
-        t[k] = at < len ? __ldg(h + at) : lo - 1;
+        t[k] = at < len ? __ldg(h + at) : 0x7fffffff;
       }
 #pragma unroll
       for (int k = 0; k < kU; ++k) {
         const int at = base + k * kProcThreads + tid;
-        if (at < len && (t[k] < 0 || t[k] >= P.V)) {
-          err |= SPEC_ERR_TOKEN;
+        if (t[k] < 0 || t[k] >= P.V) {
+          if (at < len) err |= SPEC_ERR_TOKEN;
           continue;
         }
         const unsigned o = static_cast<unsigned>(t[k] - lo);
-        if (at < len && o < static_cast<unsigned>(kTable)) {
+        if (o < static_cast<unsigned>(kTable)) {
           if (at < prompt) atomicOr(&count[o], kInPrompt);
           else atomicAdd(&count[o], 1u);
-          touch(static_cast<int>(o));
+          touch(o);
         }
       }
     }
@@ -303,40 +368,25 @@ __global__ void __launch_bounds__(kProcThreads) process_kernel(const ProcessPara
           __syncwarp();
         }
       }
-      if (mine) touch(static_cast<int>(o));
+      if (mine) touch(o);
       __syncwarp();
     }
   }
   if (checks && err) atomicOr(&s_err, err);
-  __syncthreads();
 
-  // the drafted tokens before row r0, and the rows before which the table changes
-  const auto in_slab = [&](int t) { return t >= 0 && static_cast<unsigned>(t - lo) < static_cast<unsigned>(kTable); };
-  if (!tree) {
-    for (int j = tid; j < r0; j += kProcThreads)
-      if (in_slab(s_tok[j])) {
-        atomicAdd(&count[s_tok[j] - lo], 1u);
-        touch(s_tok[j] - lo);
+  // the stream
+  if (stream) {
+    for (int i = r0; i < r1; ++i) {
+      if (i + 1 < r1) load_row(i + 1, ok1, nxt);
+      if (i + 2 < r1) load_mask(i + 2, s_mask[i + 2], ok2);
+      store_row(i, ok0, cur);
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) cur[j][k] = nxt[j][k];
+        ok0[j] = ok1[j];
+        ok1[j] = ok2[j];
       }
-    for (int i = r0 + 1 + tid; i < r1; i += kProcThreads)
-      if (in_slab(s_tok[i - 1])) atomicOr(&change[i >> 5], 1u << (i & 31));
-  } else {
-    if (tid == 0)
-      for (int a = r0; a > 0; a = s_par[a])
-        if (in_slab(s_tok[a])) {
-          atomicAdd(&count[s_tok[a] - lo], 1u);
-          touch(s_tok[a] - lo);
-        }
-    for (int i = r0 + 1 + tid; i < r1; i += kProcThreads) {
-      int x = i - 1, y = i;
-      bool any = false;
-      while (x != y && !any) {
-        const int z = x > y ? x : y;
-        any = in_slab(s_tok[z]);
-        if (x > y) x = s_par[x];
-        else y = s_par[y];
-      }
-      if (any) atomicOr(&change[i >> 5], 1u << (i & 31));
     }
   }
   __syncthreads();
@@ -346,18 +396,87 @@ __global__ void __launch_bounds__(kProcThreads) process_kernel(const ProcessPara
   }
 
   const float rep = P.repetition ? __ldg(P.repetition + b) : 1.f;
+  const float inv = __frcp_rn(rep);
   const float freq = P.frequency ? __ldg(P.frequency + b) : 0.f;
   const float pres = P.presence ? __ldg(P.presence + b) : 0.f;
+  // Whether this CTA writes table entry `at` in row i: rows that start within
+  // a vector shift the slab's tokens, and the mask must allow the token.
+  const auto writes = [&](int i, int at) {
+    const int v = lo + at;
+    const int t = v + lead_of(i) - v0 * E;
+    if (v < 0 || v >= P.V || t < 0 || t >= kSlab) return false;
+    const int mrow = s_mask[i];
+    return mrow < 0 || ((__ldg(P.mask + static_cast<long long>(mrow) * P.mask_ld + (v >> 5)) >> (v & 31)) & 1u);
+  };
+  const auto value = [&](int i, int at) {
+    return static_cast<const T*>(P.logits) + (static_cast<long long>(b) * P.n + i) * P.ld + (lo + at);
+  };
+  const auto rewrite = [&](int i, int at, uint32_t bits) {
+    const unsigned c = count[at];
+    float x = L::widen(bits);
+    if (c) x = __fmul_rn(x, x > 0.f ? inv : rep);
+    const unsigned made = c & ~kInPrompt;
+    if (made) x = __fsub_rn(x, __fmaf_rn(freq, static_cast<float>(made), pres));
+    const float plus = biased ? bias[at] : 0.f;
+    if (plus != 0.f) x = __fadd_rn(x, plus);
+    if (c || plus != 0.f)
+      store_bits(static_cast<T*>(P.out) + (static_cast<long long>(b) * P.n + i) * P.out_ld + (lo + at), L::round(x));
+  };
 
+  // tokens that are the same for every row: all (token, row) pairs, four in flight per thread
+  const int fixed = s_fixed;
+  const int pairs = fixed * (r1 - r0);
+  constexpr int kU = 4;
+  for (int base = tid; base < pairs; base += kProcThreads * kU) {
+    int row[kU], at[kU];
+    uint32_t x[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int p = base + u * kProcThreads;
+      at[u] = -1;
+      if (p < pairs) {
+        const int i = p / fixed;
+        row[u] = r0 + i;
+        at[u] = list[p - i * fixed];
+        if (!writes(row[u], at[u])) at[u] = -1;
+      }
+      if (at[u] >= 0) x[u] = load_bits(value(row[u], at[u]));
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+      if (at[u] >= 0) rewrite(row[u], at[u], x[u]);
+  }
+
+  // drafted tokens: row by row
+  const int moving = s_drafted;
+  if (moving == 0) return;
+  if (!tree) {
+    for (int j = tid; j < r0; j += kProcThreads)
+      if (in_slab(s_tok[j])) atomicAdd(&count[s_tok[j] - lo], 1u);
+    for (int i = r0 + 1 + tid; i < r1; i += kProcThreads)
+      if (in_slab(s_tok[i - 1])) atomicOr(&change[i >> 5], 1u << (i & 31));
+  } else {
+    if (tid == 0)
+      for (int a = r0; a > 0; a = s_par[a])
+        if (in_slab(s_tok[a])) count[s_tok[a] - lo] += 1u;
+    for (int i = r0 + 1 + tid; i < r1; i += kProcThreads) {
+      int x = i - 1, y = i;
+      bool any = false;
+      while (x != y && !any) {
+        any = in_slab(s_tok[x > y ? x : y]);
+        if (x > y) x = s_par[x];
+        else y = s_par[y];
+      }
+      if (any) atomicOr(&change[i >> 5], 1u << (i & 31));
+    }
+  }
+  __syncthreads();
   for (int i = r0; i < r1; ++i) {
-    if (i + 1 < r1) load_row(i + 1, s_mask[i + 1], nxt, nxt_ok);
     if (i > r0 && (change[i >> 5] >> (i & 31)) & 1u) {
-      __syncthreads();  // everyone is done with the previous row's table
+      __syncthreads();  // everyone is done with the previous row's counts
       if (tid == 0) {
         const auto add = [&](int t, unsigned d) {
-          if (!in_slab(t)) return;
-          count[t - lo] += d;
-          touched[(t - lo) >> 5] |= 1u << ((t - lo) & 31);
+          if (in_slab(t)) count[t - lo] += d;
         };
         if (!tree) {
           add(s_tok[i - 1], 1u);
@@ -376,50 +495,9 @@ __global__ void __launch_bounds__(kProcThreads) process_kernel(const ProcessPara
       }
       __syncthreads();
     }
-    const long long row = static_cast<long long>(b) * P.n + i;
-    const int m = static_cast<int>((row * P.ld) % E);
-    T* dst = static_cast<T*>(P.out) + row * P.out_ld;
-    const bool same = static_cast<int>((row * P.out_ld) % E) == m;
-#pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
-      const int t0 = (v0 + j * kProcThreads + tid) * E - m;
-      if (t0 >= P.V) continue;
-      const int at = t0 - lo;
-      const uint32_t hit =
-          __funnelshift_r(touched[at >> 5], touched[(at >> 5) + 1], at & 31) & cur_ok[j] & kFull;
-      if (hit) {
-#pragma unroll
-        for (int k = 0; k < E; ++k) {
-          if (!((hit >> k) & 1u)) continue;
-          const unsigned c = count[at + k];
-          float x = L::get(cur[j], k);
-          if (c) x = x > 0.f ? __fdiv_rn(x, rep) : __fmul_rn(x, rep);
-          const unsigned made = c & ~kInPrompt;
-          if (made) x = __fsub_rn(x, __fmaf_rn(freq, static_cast<float>(made), pres));
-          const float plus = biased ? bias[at + k] : 0.f;
-          if (plus != 0.f) x = __fadd_rn(x, plus);
-          if (c || plus != 0.f) L::set_bits(cur[j], k, L::round(x));
-        }
-      }
-      if (cur_ok[j] != kFull) {
-#pragma unroll
-        for (int k = 0; k < E; ++k)
-          if (!((cur_ok[j] >> k) & 1u)) L::set_bits(cur[j], k, L::kNegInf);
-      }
-      if (same && t0 >= 0 && t0 + E <= P.V) {
-        if (!(kDebugChecks && misaligned16(dst + t0)))
-          *reinterpret_cast<uint4*>(dst + t0) = make_uint4(cur[j][0], cur[j][1], cur[j][2], cur[j][3]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < E; ++k)
-          if (t0 + k >= 0 && t0 + k < P.V) store_bits(dst + t0 + k, L::bits(cur[j], k));
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) cur[j][k] = nxt[j][k];
-      cur_ok[j] = nxt_ok[j];
+    for (int e = tid; e < moving; e += kProcThreads) {
+      const int at = list[kTable - 1 - e];
+      if (writes(i, at)) rewrite(i, at, load_bits(value(i, at)));
     }
   }
 }
@@ -427,9 +505,10 @@ __global__ void __launch_bounds__(kProcThreads) process_kernel(const ProcessPara
 template <typename T, int kVecs>
 size_t process_smem(const ProcessParams& p) {
   constexpr int E = Lanes<T>::kN;
-  size_t words = table_tokens(E, kVecs) + bitmap_words(E, kVecs) + kMaxRows / 32 + 3 * static_cast<size_t>(p.n);
-  if (p.bias_tokens) words += table_tokens(E, kVecs);
-  return words * 4;
+  constexpr size_t table = table_tokens(E, kVecs);
+  size_t words = table + 2 * bitmap_words(E, kVecs) + kMaxRows / 32 + 3 * static_cast<size_t>(p.n);
+  if (p.bias_tokens) words += table;
+  return words * 4 + (table + 1) / 2 * 4;
 }
 
 int slabs_of(const ProcessParams& p, int elems, int vecs) {

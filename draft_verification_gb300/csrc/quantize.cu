@@ -14,12 +14,26 @@ namespace {
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// A warp takes 256 columns of one row at a time, 8 consecutive ones per lane,
-// so a group is 4, 8 or 16 neighbouring lanes: its extremes come from three
-// to four shuffles, every weight is read once and a lane's 8 codes are one
-// 32-bit store.  The scales of one group lie a vocabulary apart for one row,
-// so a CTA of 8 warps covers 32 rows and hands their scales through shared
-// memory: 32 neighbouring values per store.
+// A warp takes 256 columns of four rows at a time, 8 consecutive columns per
+// lane and row, so a group is 4, 8 or 16 neighbouring lanes: its extremes come
+// from two to four shuffles, every weight is read once and a lane's 8 codes are
+// one 32-bit store.  What is computed once per group (a division, a reciprocal)
+// is computed by a lane for one of its four rows and handed round.  The scales
+// of one group lie a vocabulary apart for one row, so a CTA of 8 warps covers 32
+// rows and hands their scales through shared memory: 32 neighbouring values per
+// store.
+//
+// The codes are rint(w / s) with an IEEE division, without dividing:
+//   bfloat16 weights  w and s have 8 significant bits, so w / s is half way
+//     between two integers exactly or differs from every such point by 1/1020
+//     or more.  One fma puts w (1 / s) on a grid of 2^-11 (adding 6144, whose
+//     float32 neighbours are that far apart): an exact half lands on itself,
+//     anything else stays on its side, and rounding the grid point to even is
+//     rounding the quotient.
+//   float32 weights   w (1 / s) is within 3e-6 of the quotient, so its rounding
+//     is the quotient's unless it lies within 1e-4 of half way: those few
+//     weights are divided.
+// Groups whose scale is below 2^-120 (or 0, or not finite) are divided.
 constexpr int kQuantThreads = 256;
 constexpr int kQuantRows = 32;             // rows per CTA, 4 per warp
 constexpr int kQuantCols = 256;            // columns per CTA
@@ -72,6 +86,10 @@ __device__ __forceinline__ void load8(const T* p, float (&w)[8]) {
   }
 }
 
+constexpr float kGrid = 6144.f;            // float32 neighbours 2^-11 apart
+constexpr float kWhole = 12582912.f;       // 1.5 * 2^23: neighbours 1 apart
+constexpr float kTiny = 7.5231638e-37f;    // 2^-120
+
 template <typename T, bool kVec, bool kZeros>
 __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantParams P) {
   __shared__ unsigned short s_scale[kQuantGroups][kQuantRows];
@@ -81,6 +99,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantPara
   const int k0 = static_cast<int>(blockIdx.y) * kQuantCols;
   const int k = k0 + lane * 8;
   constexpr int kPer = kQuantRows / (kQuantThreads / 32);
+  static_assert(kPer == 4, "a group has at least 4 lanes: one for each row");
   float w[kPer][8];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -93,55 +112,88 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantPara
     }
   }
   const int lanes = P.group >> 3;  // lanes of a group
+  // extremes of this lane's group in each row, 0 included; NaN-propagating
+  // (lo holds max(0, -min))
+  float hi = 0.f, lo = 0.f;  // of row lane % 4
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int r = warp * kPer + i;
-    const int v = v0 + r;
-    float lo = 0.f, hi = 0.f;  // extremes, 0 included; NaN-propagating
+    float h = 0.f, l = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      hi = fmax_nan(hi, kZeros ? w[i][j] : fabsf(w[i][j]));
-      if constexpr (kZeros) lo = fmax_nan(lo, -w[i][j]);  // lo holds max(0, -min)
+      h = fmax_nan(h, kZeros ? w[i][j] : fabsf(w[i][j]));
+      if constexpr (kZeros) l = fmax_nan(l, -w[i][j]);
     }
     for (int o = lanes >> 1; o > 0; o >>= 1) {
-      hi = fmax_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-      if constexpr (kZeros) lo = fmax_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      h = fmax_nan(h, __shfl_xor_sync(0xffffffffu, h, o));
+      if constexpr (kZeros) l = fmax_nan(l, __shfl_xor_sync(0xffffffffu, l, o));
     }
-    const float span = kZeros ? __fdiv_rn(__fadd_rn(hi, lo), 15.f) : __fdiv_rn(hi, 7.f);
-    unsigned short sb = to_bf16(span);
-    float s = __uint_as_float(static_cast<uint32_t>(sb) << 16);
-    if (!(s < kInf)) {  // a NaN or an infinity in the group, or an overflow of s
-      sb = 0x7fc0;
-      s = 0.f;
+    if ((lane & 3) == i) {
+      hi = h;
+      lo = l;
     }
-    float z = 0.f;
-    if constexpr (kZeros) {
-      if (s > 0.f) z = fminf(rintf(__fdiv_rn(lo, s)), 15.f);
-    }
-    const float low = kZeros ? 0.f : -8.f, high = kZeros ? 15.f : 7.f;
-    uint32_t packed = 0;
+  }
+  // row lane % 4: the scale, its reciprocal and the zero point
+  unsigned short sb = to_bf16(kZeros ? __fdiv_rn(__fadd_rn(hi, lo), 15.f) : __fdiv_rn(hi, 7.f));
+  float s = __uint_as_float(static_cast<uint32_t>(sb) << 16);
+  if (!(s < kInf)) {  // a NaN or an infinity in the group, or an overflow of s
+    sb = 0x7fc0;
+    s = 0.f;
+  }
+  const float r = s >= kTiny ? __frcp_rn(s) : 0.f;
+  float z = 8.f;
+  if constexpr (kZeros) z = s > 0.f ? fminf(rintf(__fdiv_rn(lo, s)), 15.f) : 0.f;
+  if ((lane & (lanes - 1)) < kPer) {
+    s_scale[lane / lanes][warp * kPer + (lane & 3)] = sb;
+    if constexpr (kZeros) s_zero[lane / lanes][warp * kPer + (lane & 3)] = static_cast<unsigned char>(z);
+  }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float q = s > 0.f ? rintf(__fdiv_rn(w[i][j], s)) : 0.f;
-      q = fminf(fmaxf(__fadd_rn(q, z), low), high);
-      packed |= static_cast<uint32_t>(static_cast<int>(q) + (kZeros ? 0 : 8)) << (4 * j);
+  for (int i = 0; i < kPer; ++i) {
+    const int v = v0 + warp * kPer + i;
+    const int from = (lane & ~3) | i;
+    const float ri = __shfl_sync(0xffffffffu, r, from);
+    const float zi = kZeros ? __shfl_sync(0xffffffffu, z, from) : 8.f;
+    const float si = __shfl_sync(0xffffffffu, s, from);
+    float c[8];
+    if (ri > 0.f) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if constexpr (sizeof(T) == 2) {
+          const float t = __fadd_rn(__fmaf_rn(w[i][j], ri, kGrid), kWhole - kGrid);
+          c[j] = __fadd_rn(t, zi - kWhole);
+        } else {
+          const float q = __fmul_rn(w[i][j], ri);
+          float t = __fadd_rn(__fadd_rn(q, kWhole), -kWhole);
+          if (fabsf(__fadd_rn(q, -t)) > 0.4999f) t = rintf(__fdiv_rn(w[i][j], si));
+          c[j] = __fadd_rn(t, zi);
+        }
+        // without zeros |w / s| < 7.5, and with them w / s rounds to -z or more
+        if constexpr (kZeros) c[j] = fminf(c[j], 15.f);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float q = si > 0.f ? rintf(__fdiv_rn(w[i][j], si)) : 0.f;
+        c[j] = fminf(fmaxf(__fadd_rn(q, zi), 0.f), 15.f);
+      }
     }
+    // four codes at a time, exact in float32, then as an integer
+    const auto four = [](const float* x) {
+      const float p = __fmaf_rn(__fmaf_rn(__fmaf_rn(x[3], 16.f, x[2]), 16.f, x[1]), 16.f, x[0]);
+      return __float_as_uint(__fadd_rn(p, 8388608.f));  // 2^23: the low bits are the integer
+    };
     if (v < P.V && k < P.d)
-      *reinterpret_cast<uint32_t*>(P.codes + static_cast<long long>(v) * P.codes_ld + (k >> 1)) = packed;
-    if ((lane & (lanes - 1)) == 0) {
-      s_scale[lane / lanes][r] = sb;
-      if constexpr (kZeros) s_zero[lane / lanes][r] = static_cast<unsigned char>(z);
-    }
+      *reinterpret_cast<uint32_t*>(P.codes + static_cast<long long>(v) * P.codes_ld + (k >> 1)) =
+          __byte_perm(four(c), four(c + 4), 0x5410);
   }
   __syncthreads();
   const int groups = kQuantCols / P.group;
   for (int i = tid; i < groups * kQuantRows; i += kQuantThreads) {
-    const int g = i / kQuantRows, r = i % kQuantRows;
-    const int v = v0 + r;
+    const int g = i / kQuantRows, q = i % kQuantRows;
+    const int v = v0 + q;
     if (v < P.V && k0 + g * P.group < P.d) {
       const long long row = k0 / P.group + g;
-      P.scales[row * P.scales_ld + v] = s_scale[g][r];
-      if constexpr (kZeros) P.zeros[row * P.zeros_ld + v] = s_zero[g][r];
+      P.scales[row * P.scales_ld + v] = s_scale[g][q];
+      if constexpr (kZeros) P.zeros[row * P.zeros_ld + v] = s_zero[g][q];
     }
   }
 }

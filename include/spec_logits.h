@@ -36,7 +36,7 @@ extern "C" {
 /*    root's token is the history's last).                                 */
 /* With s(v) = token v occurs in the history or on the path, and c(v) = its */
 /* occurrences in the history from prompt_len[b] on and on the path:       */
-/*    x1 = s ? (x > 0 ? x / repetition : x * repetition) : x               */
+/*    x1 = s ? (x > 0 ? x * (1 / repetition) : x * repetition) : x         */
 /*    x2 = x1 - (frequency * c + (c > 0 ? presence : 0))                   */
 /*    x3 = x2 + the sum of b's bias entries for v, in their order          */
 /*    y  = allowed ? x3 : -inf                                             */
