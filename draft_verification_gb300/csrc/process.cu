@@ -40,6 +40,7 @@ namespace {
 constexpr int kProcThreads = 256;
 constexpr int kMaxRows = 1024;       // rows per sequence
 constexpr unsigned kInPrompt = 1u << 31;
+constexpr int kFill = 152 * 5;       // CTAs that fill the GPU (shared memory: 5 per SM with long slabs)
 
 struct ProcessParams {
   int B, n, V;
@@ -311,26 +312,52 @@ __global__ void __launch_bounds__(kProcThreads) process_kernel(const ProcessPara
     }
     const int prompt = P.prompt_len ? __ldg(P.prompt_len + b) : 0;
     const int* h = P.history + static_cast<long long>(b) * P.history_ld;
-    constexpr int kU = 8;
-    for (int base = 0; base < len; base += kProcThreads * kU) {
-      int t[kU];
-#pragma unroll
-      for (int k = 0; k < kU; ++k) {
-        const int at = base + k * kProcThreads + tid;
-        t[k] = at < len ? __ldg(h + at) : 0x7fffffff;
+    const auto take = [&](int t, int at) {
+      if (at >= len) return;
+      if (t < 0 || t >= P.V) {
+        err |= SPEC_ERR_TOKEN;
+        return;
       }
+      const unsigned o = static_cast<unsigned>(t - lo);
+      if (o < static_cast<unsigned>(kTable)) {
+        if (at < prompt) atomicOr(&count[o], kInPrompt);
+        else atomicAdd(&count[o], 1u);
+        touch(o);
+      }
+    };
+    // a thread's loads go out together: 8192 tokens per round where rows allow 16-byte loads
+    constexpr int kU = 8;
+    if (P.history_ld % 4 == 0 && !misaligned16(P.history)) {
+      for (int base = 4 * tid; base < len; base += 4 * kProcThreads * kU) {
+        int4 t[kU];
 #pragma unroll
-      for (int k = 0; k < kU; ++k) {
-        const int at = base + k * kProcThreads + tid;
-        if (t[k] < 0 || t[k] >= P.V) {
-          if (at < len) err |= SPEC_ERR_TOKEN;
-          continue;
+        for (int k = 0; k < kU; ++k) {
+          const int at = base + 4 * k * kProcThreads;
+          if (at < len) t[k] = __ldg(reinterpret_cast<const int4*>(h + at));
         }
-        const unsigned o = static_cast<unsigned>(t[k] - lo);
-        if (o < static_cast<unsigned>(kTable)) {
-          if (at < prompt) atomicOr(&count[o], kInPrompt);
-          else atomicAdd(&count[o], 1u);
-          touch(o);
+#pragma unroll
+        for (int k = 0; k < kU; ++k) {
+          const int at = base + 4 * k * kProcThreads;
+          if (at >= len) break;
+          take(t[k].x, at);
+          take(t[k].y, at + 1);
+          take(t[k].z, at + 2);
+          take(t[k].w, at + 3);
+        }
+      }
+    } else {
+      for (int base = tid; base < len; base += kProcThreads * kU) {
+        int t[kU];
+#pragma unroll
+        for (int k = 0; k < kU; ++k) {
+          const int at = base + k * kProcThreads;
+          if (at < len) t[k] = __ldg(h + at);
+        }
+#pragma unroll
+        for (int k = 0; k < kU; ++k) {
+          const int at = base + k * kProcThreads;
+          if (at >= len) break;
+          take(t[k], at);
         }
       }
     }
@@ -343,18 +370,30 @@ __global__ void __launch_bounds__(kProcThreads) process_kernel(const ProcessPara
       err |= SPEC_ERR_TOKEN;
       len = len < 0 ? 0 : P.bias_ld;
     }
+    constexpr int kAhead = 4;  // 32 entries a step, the loads of four steps at once
+    int ts[kAhead];
+    float xs[kAhead];
     for (int base = 0; base < len; base += 32) {
-      const int at = base + lane;
-      const long long src = static_cast<long long>(b) * P.bias_ld + at;
-      int t = -1;
-      float x = 0.f;
-      if (at < len) {
-        t = __ldg(P.bias_tokens + src);
-        x = __ldg(P.bias_values + src);
-        if (t < 0 || t >= P.V) {
-          err |= SPEC_ERR_TOKEN;
-          t = -1;
+      const int step = base / 32 % kAhead;
+      if (step == 0) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const int at = base + 32 * k + lane;
+          const long long src = static_cast<long long>(b) * P.bias_ld + at;
+          ts[k] = at < len ? __ldg(P.bias_tokens + src) : -1;
+          xs[k] = at < len ? __ldg(P.bias_values + src) : 0.f;
         }
+      }
+      int t = ts[0];
+      float x = xs[0];
+#pragma unroll
+      for (int k = 1; k < kAhead; ++k) {
+        t = step == k ? ts[k] : t;
+        x = step == k ? xs[k] : x;
+      }
+      if (base + lane < len && (t < 0 || t >= P.V)) {
+        err |= SPEC_ERR_TOKEN;
+        t = -1;
       }
       const unsigned o = static_cast<unsigned>(t - lo);
       const bool mine = t >= 0 && o < static_cast<unsigned>(kTable);
@@ -528,7 +567,7 @@ cudaError_t launch_process(ProcessParams p, cudaStream_t s) {
   // few sequences and slabs: a sequence's rows are split as well (each part
   // reads the history again)
   const long long have = static_cast<long long>(slabs) * p.B;
-  const long long parts = have >= 304 ? 1 : (304 + have - 1) / have;
+  const long long parts = (kFill + have - 1) / have;
   const int chunks = static_cast<int>(parts < p.n ? parts : p.n);
   p.rows_per_cta = (p.n + chunks - 1) / chunks;
   const dim3 grid(static_cast<unsigned>(slabs), static_cast<unsigned>((p.n + p.rows_per_cta - 1) / p.rows_per_cta),
@@ -540,7 +579,7 @@ cudaError_t launch_process(ProcessParams p, cudaStream_t s) {
 template <typename T>
 cudaError_t dispatch_process(const ProcessParams& p, cudaStream_t s) {
   // long slabs read the history fewer times; short ones fill the GPU
-  if (static_cast<long long>(slabs_of(p, Lanes<T>::kN, 4)) * p.B >= 304) return launch_process<T, 4>(p, s);
+  if (static_cast<long long>(slabs_of(p, Lanes<T>::kN, 2)) * p.B * p.n >= kFill) return launch_process<T, 2>(p, s);
   return launch_process<T, 1>(p, s);
 }
 
