@@ -134,7 +134,8 @@ class ProcessArgs(C.Structure):
         ("repetition", _vp), ("frequency", _vp), ("presence", _vp),
         ("bias_tokens", _vp), ("bias_values", _vp), ("bias_len", _vp),
         ("bias_ld", C.c_int), ("mask_rows", C.c_int), ("mask", _vp), ("mask_ld", C.c_longlong),
-        ("mask_index", _vp), ("seq_error", _vp), ("error_word", _vp)
+        ("mask_index", _vp), ("seq_error", _vp), ("error_word", _vp),
+        ("workspace", _vp), ("workspace_bytes", C.c_size_t)
     ]
 
 
@@ -181,6 +182,7 @@ SIGNATURES = {
 
 # every symbol include/spec_logits.h declares
 LOGITS_SIGNATURES = {
+    "spec_process_workspace_size": (C.c_size_t, [C.c_int, C.c_int, C.c_int, C.c_int, C.c_int]),
     "spec_process_logits": (C.c_int, [C.POINTER(ProcessArgs), _vp]),
     "spec_quantize_int4": (C.c_int, [C.POINTER(QuantizeInt4Args), _vp]),
     "spec_int4_product_workspace_size": (C.c_size_t, [C.c_int, C.c_int, C.c_int, C.c_int]),

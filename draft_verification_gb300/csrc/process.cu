@@ -2,45 +2,56 @@
 // grammar masks, each row with the tokens before its own position (chain or
 // tree).  The arithmetic and the argument meanings are in spec_logits.h.
 //
-// process_kernel: a CTA owns one slab of the vocabulary of one sequence.  It
-// first streams that slab of the sequence's rows: a masked copy, which needs
-// nothing but the mask bits (a vector whose bits are all 0 is not read; in
-// place without masks nothing is streamed at all).  Then it rewrites the few
-// tokens that something applies to, read again from the input (through L2)
-// with all lanes busy: handled inside the stream, a token in a hundred would
-// put nearly every warp on the slow path.
+// A CTA owns one slab of the vocabulary of one sequence.  Row by row its part
+// goes through shared memory: 16-byte vectors are read (those whose mask bits
+// are all 0 are not), masked elements become -inf, the few tokens that anything
+// else applies to are rewritten in shared memory with all lanes busy, and the
+// vectors are written.  Rewritten in the registers of the stream, a token in a
+// hundred would put nearly every warp on the slow path; rewritten in global
+// memory afterwards, two-byte accesses a sector apart run at 25 to 50 per
+// nanosecond on the whole GPU, which was slower than the stream itself.
 //
-// What applies is a table of the slab in shared memory - per token a 32-bit
-// word (low 31 bits: occurrences that count, bit 31: occurs in the prompt) and
-// the sum of its bias entries - built by reading the whole history once while
-// the first rows are in flight, and two lists of tokens: those that only the
-// history and the biases touch, which are the same for every row, so that all
-// (token, row) pairs are rewritten in any order; and those that are drafted,
-// whose counts depend on the row.  For the latter the rows go in order, and one
-// thread takes the table from row to row (leaving one path and entering the
-// next, up to their last common node) where a drafted token of the slab is
-// concerned (rows marked beforehand, all in parallel).
+// What applies to a token is an entry: a 32-bit word (low bits: occurrences
+// that count; bit 31: occurs in the prompt; bit 30: drafted, its occurrences on
+// the way to a row are counted for each row; bit 29: has a bias) and the sum of its bias entries.
+//  - Small calls (latency) build the slab's entries in the same kernel, as a
+//    table of the slab in shared memory, from the whole history, which is read
+//    while the first row's vectors are in flight.
+//  - Large calls would read each history once per slab and hold 10 bytes of
+//    table per token, too much for enough CTAs to overlap their phases.
+//    collect_kernel gathers each sequence's distinct tokens once and writes
+//    their entries in ascending order to the workspace; the slabs' CTAs
+//    (launched dependent: their first vectors are in flight meanwhile) read a
+//    few hundred entries each.
 //
-// The stream goes in 16-byte vectors aligned in memory: a row that starts at
-// element m of its vector has tokens [k e - m, k e - m + e) in vector k, so the
-// table starts e - 1 tokens before the slab and mask bits are taken by funnel
-// shifts.  Vectors that stick out of the row, and rows whose output starts at
-// another offset than the input, are written element by element.
+// Vectors are aligned in memory: a row that starts at element m of its vector
+// has tokens [k e - m, k e - m + e) in vector k, so a row's part is the slab
+// shifted by m (entries of the slab before may belong to it), and mask bits are
+// taken by funnel shifts.  Vectors that stick out of the row, and rows whose
+// output starts at another offset than the input, are read or written element
+// by element.
+//
+// In place and without masks only the touched elements are read and written.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
+#include <map>
+#include <mutex>
 
 #include "common.cuh"
 #include "internal.h"
 #include "spec_logits.h"
+#include "tma_host.h"
 
 namespace sv {
 namespace {
 
-constexpr int kProcThreads = 256;
 constexpr int kMaxRows = 1024;       // rows per sequence
-constexpr unsigned kInPrompt = 1u << 31;
-constexpr int kFill = 152 * 5;       // CTAs that fill the GPU (shared memory: 5 per SM with long slabs)
+constexpr int kMaxSlabs = 2097152 / 4096 + 2;  // slabs of a large call
+// bits of a token's word; the low ones count its occurrences
+constexpr unsigned kInPrompt = 1u << 31, kDrafted = 1u << 30, kBiased = 1u << 29;
+constexpr unsigned kMade = kBiased - 1u;
 
 struct ProcessParams {
   int B, n, V;
@@ -66,6 +77,14 @@ struct ProcessParams {
   int* seq_error;
   int* error_word;
   int rows_per_cta;
+  int window;          // collecting: entries gathered at a time
+  int slab_tokens;     // collecting: tokens of a slab
+  int slabs;
+  int capacity;        // entries of a sequence in the workspace
+  int* offsets;        // workspace [B][slabs + 1]: where each slab's entries start
+  int* entry_token;    // workspace [B][capacity]
+  unsigned* entry_count;
+  float* entry_bias;
 };
 
 // 16 bytes of logits.  Not the read-only path: the output may be the input.
@@ -129,39 +148,322 @@ __device__ __forceinline__ void store_bits(T* p, uint32_t b) {
   }
 }
 
-// table entries: the slab and the e - 1 tokens before it
-__host__ __device__ constexpr int table_tokens(int elems, int vecs) { return kProcThreads * vecs * elems + elems - 1; }
-__host__ __device__ constexpr int bitmap_words(int elems, int vecs) { return (table_tokens(elems, vecs) + 31) / 32; }
+// What a sequence's arguments say, clamped to what they may.
+struct Lengths {
+  int history, prompt, bias;
+};
+__device__ __forceinline__ Lengths lengths_of(const ProcessParams& P, int b, int& err) {
+  Lengths n{0, 0, 0};
+  if (P.history) {
+    n.history = P.history_len ? __ldg(P.history_len + b) : P.history_ld;
+    if (n.history < 0 || n.history > P.history_ld) {
+      err |= SPEC_ERR_TOKEN;
+      n.history = n.history < 0 ? 0 : P.history_ld;
+    }
+    if (P.prompt_len) n.prompt = __ldg(P.prompt_len + b);
+  }
+  if (P.bias_tokens) {
+    n.bias = P.bias_len ? __ldg(P.bias_len + b) : P.bias_ld;
+    if (n.bias < 0 || n.bias > P.bias_ld) {
+      err |= SPEC_ERR_TOKEN;
+      n.bias = n.bias < 0 ? 0 : P.bias_ld;
+    }
+  }
+  return n;
+}
 
-template <typename T, int kVecs>
-__global__ void __launch_bounds__(kProcThreads) process_kernel(const ProcessParams P) {
-  using L = Lanes<T>;
-  constexpr int E = L::kN;
-  constexpr uint32_t kFull = (1u << E) - 1u;
-  constexpr int kSlab = kProcThreads * kVecs * E;
-  constexpr int kTable = table_tokens(E, kVecs);
-  constexpr int kWords = bitmap_words(E, kVecs);
+// The drafted token of row i (-1: none) and its parent.
+__device__ __forceinline__ void draft_of(const ProcessParams& P, int b, int i, int& token, int& parent, int& err) {
+  const bool tree = P.parent != nullptr;
+  token = -1;
+  parent = 0;
+  if (tree ? i > 0 : (P.tokens && i < P.n - 1)) {
+    token = __ldg(P.tokens + static_cast<long long>(b) * P.tokens_ld + i);
+    if (token < 0 || token >= P.V) {
+      err |= SPEC_ERR_TOKEN;
+      token = -1;
+    }
+  }
+  if (tree && i > 0) {
+    parent = __ldg(P.parent + static_cast<long long>(b) * P.n + i);
+    if (parent < 0 || parent >= i) {
+      err |= SPEC_ERR_PARENT;
+      parent = 0;
+    }
+  }
+  if (P.mask && P.mask_index) {
+    const int mi = __ldg(P.mask_index + static_cast<long long>(b) * P.n + i);
+    if (mi < -1 || mi >= P.mask_rows) err |= SPEC_ERR_MASK;
+  }
+}
 
-  extern __shared__ unsigned proc_dyn[];
-  unsigned* count = proc_dyn;                         // [kTable]
-  unsigned* drafted = count + kTable;                 // [kWords] tokens that some row's path may hold
-  unsigned* listed = drafted + kWords;                // [kWords] tokens in either list
-  unsigned* change = listed + kWords;                 // [kMaxRows / 32] rows before which the table changes
-  int* s_tok = reinterpret_cast<int*>(change + kMaxRows / 32);  // [n]
-  int* s_par = s_tok + P.n;                           // [n]
-  int* s_mask = s_par + P.n;                          // [n]
-  float* bias = reinterpret_cast<float*>(s_mask + P.n);  // [kTable], with biases
-  // the lists grow towards each other: fixed tokens from the front, drafted ones from the back
-  unsigned short* list = reinterpret_cast<unsigned short*>(bias + (P.bias_tokens ? kTable : 0));  // [kTable]
-  __shared__ int s_err, s_fixed, s_drafted;
+// take(token, place) for the history's tokens, four at a time where rows allow
+// 16-byte loads, the next four loading meanwhile.  One copy of `take`: a CTA
+// runs it a few times, and straight-line copies of it would each wait for
+// their instructions longer than they take to run.
+template <int kThreads, typename F>
+__device__ __forceinline__ void for_history(const ProcessParams& P, int b, int len, F&& take) {
+  const int* h = P.history + static_cast<long long>(b) * P.history_ld;
+  const bool wide = P.history_ld % 4 == 0 && !misaligned16(P.history);
+  const int width = wide ? 4 : 1;
+  const auto load = [&](int at) {
+    int4 t = make_int4(0, 0, 0, 0);
+    if (at < len) {
+      if (wide) t = __ldg(reinterpret_cast<const int4*>(h + at));
+      else t.x = __ldg(h + at);
+    }
+    return t;
+  };
+  int4 next = load(width * static_cast<int>(threadIdx.x));
+  for (int at = width * static_cast<int>(threadIdx.x); at < len; at += width * kThreads) {
+    int4 t = next;
+    next = load(at + width * kThreads);
+#pragma unroll 1
+    for (int k = 0; k < width && at + k < len; ++k) {
+      take(t.x, at + k);
+      t.x = t.y;
+      t.y = t.z;
+      t.z = t.w;
+    }
+  }
+}
+
+// The biases.  enter(token) gives a token's place (negative: not of this
+// table); words and bias are the tables' words and sums.  Entries of different
+// tokens go in at once; where a token has several, one warp adds all of them up
+// in their order, so that the sum is always the same.  Ends synchronised.
+template <int kThreads, typename Enter>
+__device__ __forceinline__ void add_biases(const ProcessParams& P, int b, int len, unsigned* words, float* bias,
+                                           int* again, int& err, Enter&& enter) {
+  if (len == 0) {
+    __syncthreads();
+    return;
+  }
+  const int tid = threadIdx.x, lane = tid & 31;
+  const long long src = static_cast<long long>(b) * P.bias_ld;
+  if (tid == 0) *again = 0;
+  __syncthreads();
+  for (int e = tid; e < len; e += kThreads) {
+    const int t = __ldg(P.bias_tokens + src + e);
+    const float x = __ldg(P.bias_values + src + e);
+    if (t < 0 || t >= P.V) {
+      err |= SPEC_ERR_TOKEN;
+      continue;
+    }
+    const int at = enter(t);
+    if (at < 0) continue;
+    if (atomicOr(&words[at], kBiased) & kBiased) *again = 1;
+    else bias[at] = x;
+  }
+  __syncthreads();
+  if (!*again) return;
+  if (tid < 32) {
+    for (int pass = 0; pass < 2; ++pass) {  // clear, then add
+      for (int base = 0; base < len; base += 32) {
+        const int t = base + lane < len ? __ldg(P.bias_tokens + src + base + lane) : -1;
+        const float x = base + lane < len ? __ldg(P.bias_values + src + base + lane) : 0.f;
+        const int at = t >= 0 && t < P.V ? enter(t) : -1;
+        __syncwarp();
+        // entries of one token: the lowest lane first
+        unsigned peers = __match_any_sync(0xffffffffu, at >= 0 ? at : -1 - lane);
+        bool todo = at >= 0;
+        while (__any_sync(0xffffffffu, todo)) {
+          const int lowest = __ffs(peers) - 1;
+          if (todo && lowest == lane) {
+            bias[at] = pass == 0 ? 0.f : bias[at] + x;
+            todo = false;
+          }
+          peers &= peers - 1;
+          __syncwarp();
+        }
+      }
+    }
+  }
+  __syncthreads();
+}
+
+// ---------------------------------------------------------------------------
+// collecting
+// ---------------------------------------------------------------------------
+// One CTA per sequence: a bitmap of the vocabulary marks the tokens, the bits
+// before each word are counted, and a token's rank among the marked ones is its
+// place.  No probing and no appending, so that every thread's work is a few
+// instructions per token, and the entries come out sorted: a slab's start is
+// the count at its first word.  (A hash table with appended entries took 25 to
+// 45 us for 4000 to 8000 tokens, most of it in a warp's longest probe.)  Larger
+// vocabularies go range by range, more than kWindow tokens window by window.
+constexpr int kCollectThreads = 512;
+constexpr int kRangeWords = 8192;    // 262,144 tokens
+constexpr int kWindow = 8192;
+
+__global__ void __launch_bounds__(kCollectThreads) collect_kernel(const ProcessParams P) {
+  extern __shared__ unsigned collect_dyn[];
+  pdl_launch_dependents();
+  const int words = min((P.V + 31) / 32, kRangeWords);
+  unsigned* marked = collect_dyn;                             // [words] bitmap of the range
+  unsigned* before = marked + words;                          // [words] marked tokens before the word
+  unsigned* count = before + words;                           // [P.window] of the window's tokens
+  float* bias = reinterpret_cast<float*>(count + P.window);   // [P.window]
+  __shared__ unsigned s_warp[kCollectThreads / 32];
+  __shared__ int s_err, s_again;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b = blockIdx.x;
+  int err = 0;
+  const Lengths len = lengths_of(P, b, err);
+  if (tid == 0) s_err = 0;
+  const long long out = static_cast<long long>(b) * P.capacity;
+  int* offsets = P.offsets + static_cast<long long>(b) * (P.slabs + 1);
+  int base = 0;  // entries of the ranges before
+  for (int first = 0; first < P.V; first += words * 32) {
+    // the word of a token in this range, or a negative number
+    const auto word_of = [&](int t) {
+      const int w = (t - first) >> 5;
+      return t >= first && w < words ? w : -1;
+    };
+    const auto mark = [&](int t) {
+      const int w = word_of(t);
+      const unsigned bit = 1u << (t & 31);
+      if (w >= 0 && !(*const_cast<volatile unsigned*>(marked + w) & bit)) atomicOr(&marked[w], bit);
+    };
+    for (int i = tid; i < words; i += kCollectThreads) marked[i] = 0u;
+    __syncthreads();
+    for (int i = tid; i < P.n; i += kCollectThreads) {
+      int t, p;
+      draft_of(P, b, i, t, p, err);
+      if (t >= 0) mark(t);
+    }
+    for_history<kCollectThreads>(P, b, len.history, [&](int t, int) {
+      if (t < 0 || t >= P.V) err |= SPEC_ERR_TOKEN;
+      else mark(t);
+    });
+    for (int e = tid; e < len.bias; e += kCollectThreads) {
+      const int t = __ldg(P.bias_tokens + static_cast<long long>(b) * P.bias_ld + e);
+      if (t < 0 || t >= P.V) err |= SPEC_ERR_TOKEN;
+      else mark(t);
+    }
+    if (first == 0 && err) atomicOr(&s_err, err);
+    __syncthreads();
+    if (first == 0 && tid == 0) {
+      if (P.seq_error) P.seq_error[b] = s_err;
+      if (s_err && P.error_word) atomicOr(P.error_word, s_err);
+    }
+
+    // marked tokens before each word: a thread's words, the warp's, the CTA's
+    const int per = (words + kCollectThreads - 1) / kCollectThreads;
+    const int w0 = min(words, tid * per), w1 = min(words, w0 + per);
+    unsigned own = 0;
+    for (int i = w0; i < w1; ++i) own += __popc(marked[i]);
+    unsigned sum = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned up = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += up;
+    }
+    if (lane == 31) s_warp[warp] = sum;
+    __syncthreads();
+    unsigned run = sum - own, total = 0;
+    for (int i = 0; i < kCollectThreads / 32; ++i) {
+      if (i < warp) run += s_warp[i];
+      total += s_warp[i];
+    }
+    for (int i = w0; i < w1; ++i) {
+      unsigned m = marked[i];
+      before[i] = run;
+      // where the slab that begins here starts, and the marked tokens themselves
+      const int t0 = first + i * 32;
+      if (t0 % P.slab_tokens == 0) offsets[t0 / P.slab_tokens] = base + static_cast<int>(run);
+      for (; m; m &= m - 1) P.entry_token[out + base + run++] = t0 + __ffs(m) - 1;
+    }
+
+    for (int window = 0; window < static_cast<int>(total); window += P.window) {
+      const auto place = [&](int t) {
+        const int w = word_of(t);
+        if (w < 0) return -1;
+        const int at = static_cast<int>(before[w] + __popc(marked[w] & ((1u << (t & 31)) - 1u))) - window;
+        return at >= 0 && at < P.window ? at : -1;
+      };
+      for (int i = tid; i < P.window; i += kCollectThreads) {
+        count[i] = 0u;
+        bias[i] = 0.f;
+      }
+      __syncthreads();
+      for (int i = tid; i < P.n; i += kCollectThreads) {
+        int t, p;
+        draft_of(P, b, i, t, p, err);
+        const int at = t >= 0 ? place(t) : -1;
+        if (at >= 0) atomicOr(&count[at], kDrafted);
+      }
+      for_history<kCollectThreads>(P, b, len.history, [&](int t, int i) {
+        const int at = t >= 0 && t < P.V ? place(t) : -1;
+        if (at < 0) return;
+        if (i < len.prompt) atomicOr(&count[at], kInPrompt);
+        else atomicAdd(&count[at], 1u);
+      });
+      add_biases<kCollectThreads>(P, b, len.bias, count, bias, &s_again, err, place);
+      const int n = min(P.window, static_cast<int>(total) - window);
+      for (int i = tid; i < n; i += kCollectThreads) {
+        P.entry_count[out + base + window + i] = count[i];
+        P.entry_bias[out + base + window + i] = bias[i];
+      }
+      __syncthreads();
+    }
+    base += static_cast<int>(total);
+    __syncthreads();
+  }
+  // slabs past the vocabulary's last token, and the end
+  for (int s = (P.V - 1) / P.slab_tokens + 1 + tid; s <= P.slabs; s += kCollectThreads) offsets[s] = base;
+}
+
+// ---------------------------------------------------------------------------
+// the rows
+// ---------------------------------------------------------------------------
+// kThreads threads with kVecs vectors each: the slab.  kListed: the entries
+// come from the workspace.
+template <typename T, int kThreads, int kVecs, bool kListed>
+struct Slab {
+  static constexpr int kE = Lanes<T>::kN;
+  static constexpr int kTokens = kThreads * kVecs * kE;
+  static constexpr int kTable = kTokens + kE - 1;        // and the e - 1 tokens before it
+  static constexpr int kWords = (kTable + 31) / 32;      // a bitmap of the table
+  static constexpr int kTileBytes = kTokens * static_cast<int>(sizeof(T));
+  static constexpr int kCache = 1024;                    // listed entries kept in shared memory
+  static size_t smem(const ProcessParams& p) {
+    const size_t rows = kTileBytes + 12 * static_cast<size_t>(p.n);
+    if (kListed) return rows + 12 * static_cast<size_t>(kCache);
+    return rows + 4 * (static_cast<size_t>(kTable) * (p.bias_tokens ? 2 : 1) + 2 * kWords) + 2 * static_cast<size_t>(kTable);
+  }
+};
+
+template <typename T, int kThreads, int kVecs, bool kListed>
+__global__ void __launch_bounds__(kThreads, (kListed ? 1536 : 1024) / kThreads) process_kernel(const ProcessParams P) {
+  using L = Lanes<T>;
+  using S = Slab<T, kThreads, kVecs, kListed>;
+  constexpr int E = S::kE;
+  constexpr uint32_t kFull = (1u << E) - 1u;
+
+  extern __shared__ __align__(16) unsigned char proc_dyn[];
+  T* tile = reinterpret_cast<T*>(proc_dyn);                              // [kTokens] one row's part
+  int* s_tok = reinterpret_cast<int*>(proc_dyn + S::kTileBytes);         // [n]
+  int* s_par = s_tok + P.n;                                              // [n]
+  int* s_mask = s_par + P.n;                                             // [n]
+  // listed: the first kCache entries
+  int* c_token = s_mask + P.n;
+  unsigned* c_count = reinterpret_cast<unsigned*>(c_token + S::kCache);
+  float* c_bias = reinterpret_cast<float*>(c_count + S::kCache);
+  // else: the table, two bitmaps and the list of touched tokens
+  unsigned* count = reinterpret_cast<unsigned*>(s_mask + P.n);           // [kTable]
+  unsigned* listed = count + S::kTable;                                  // [kWords]
+  float* bias = reinterpret_cast<float*>(listed + S::kWords);            // [kTable], with biases
+  unsigned short* list = reinterpret_cast<unsigned short*>(bias + (P.bias_tokens ? S::kTable : 0));  // [kTable]
+  __shared__ int s_err, s_used, s_again;
+
+  const int tid = threadIdx.x;
   const int b = blockIdx.z;
   const int r0 = blockIdx.y * P.rows_per_cta;
   const int r1 = min(P.n, r0 + P.rows_per_cta);
-  const int v0 = blockIdx.x * (kProcThreads * kVecs);  // first vector of the slab
-  const int lo = v0 * E - (E - 1);                     // first token of the table
-  const bool checks = blockIdx.x == 0 && blockIdx.y == 0;
+  const int v0 = blockIdx.x * (kThreads * kVecs);  // first vector of the slab
+  const int lo = v0 * E - (E - 1);                 // first token of the table
   const bool tree = P.parent != nullptr;
   const bool biased = P.bias_tokens != nullptr;
   const bool stream = P.mask != nullptr || P.logits != P.out;
@@ -181,7 +483,7 @@ __global__ void __launch_bounds__(kProcThreads) process_kernel(const ProcessPara
     const unsigned* mk = mrow >= 0 ? P.mask + static_cast<long long>(mrow) * P.mask_ld : nullptr;
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
-      const int t0 = (v0 + j * kProcThreads + tid) * E - m;
+      const int t0 = (v0 + j * kThreads + tid) * E - m;
       ok[j] = t0 < P.V ? kFull : 0u;
       if (mk && t0 < P.V) {
         if (t0 < 0) {
@@ -201,7 +503,7 @@ __global__ void __launch_bounds__(kProcThreads) process_kernel(const ProcessPara
     const int m = lead_of(i);
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
-      const int t0 = (v0 + j * kProcThreads + tid) * E - m;
+      const int t0 = (v0 + j * kThreads + tid) * E - m;
       if (!ok[j]) continue;
       if (t0 >= 0 && t0 + E <= P.V) {
         const uint4 x = ld_row16(src + t0);
@@ -217,376 +519,300 @@ __global__ void __launch_bounds__(kProcThreads) process_kernel(const ProcessPara
       }
     }
   };
-  const auto store_row = [&](int i, const uint32_t (&ok)[kVecs], uint32_t (&w)[kVecs][4]) {
-    const long long row = static_cast<long long>(b) * P.n + i;
-    T* dst = static_cast<T*>(P.out) + row * P.out_ld;
-    const int m = lead_of(i);
-    const bool same = static_cast<int>((row * P.out_ld) % E) == m;
-#pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
-      const int t0 = (v0 + j * kProcThreads + tid) * E - m;
-      if (t0 >= P.V) continue;
-      if (!ok[j]) {
-        w[j][0] = w[j][1] = w[j][2] = w[j][3] = L::kNegInf4;
-      } else if (ok[j] != kFull) {
-#pragma unroll
-        for (int k = 0; k < E; ++k)
-          if (!((ok[j] >> k) & 1u)) L::set_bits(w[j], k, L::kNegInf);
-      }
-      if (same && t0 >= 0 && t0 + E <= P.V) {
-        if (!(kDebugChecks && misaligned16(dst + t0)))
-          *reinterpret_cast<uint4*>(dst + t0) = make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < E; ++k)
-          if (t0 + k >= 0 && t0 + k < P.V) store_bits(dst + t0 + k, L::bits(w[j], k));
-      }
-    }
-  };
 
-  // The first row's vectors are in flight while the table is built, the
-  // second row's mask bits as well: the stream always reads the vectors of one
-  // row and the mask bits of the next ahead.
-  uint32_t cur[kVecs][4], nxt[kVecs][4], ok0[kVecs], ok1[kVecs], ok2[kVecs];
+  // The stream reads the vectors of one row and the mask bits of the next
+  // ahead; the first ones are in flight while the entries are fetched or built.
+  uint32_t w[kVecs][4], ok0[kVecs], ok1[kVecs];
   if (stream) {
     load_mask(r0, mask_row(r0), ok0);
     if (r0 + 1 < r1) load_mask(r0 + 1, mask_row(r0 + 1), ok1);
-    load_row(r0, ok0, cur);
+    load_row(r0, ok0, w);
   }
 
-  for (int i = tid; i < kTable; i += kProcThreads) count[i] = 0u;
-  for (int i = tid; i < kWords; i += kProcThreads) drafted[i] = listed[i] = 0u;
-  for (int i = tid; i < kMaxRows / 32; i += kProcThreads) change[i] = 0u;
-  if (biased)
-    for (int i = tid; i < kTable; i += kProcThreads) bias[i] = 0.f;
-  if (tid == 0) s_err = s_fixed = s_drafted = 0;
-  __syncthreads();
-
   int err = 0;
-  const auto in_slab = [&](int t) { return t >= 0 && static_cast<unsigned>(t - lo) < static_cast<unsigned>(kTable); };
-
-  // the drafted tokens, the tree and the mask rows
-  for (int i = tid; i < P.n; i += kProcThreads) {
-    int t = -1, p = 0;
-    if (P.tokens && i < P.tokens_ld) t = __ldg(P.tokens + static_cast<long long>(b) * P.tokens_ld + i);
-    const bool used = tree ? i > 0 : (P.tokens && i < P.n - 1);
-    if (used && (t < 0 || t >= P.V)) {
-      err |= SPEC_ERR_TOKEN;
-      t = -1;
-    }
-    if (tree && i > 0) {
-      p = __ldg(P.parent + static_cast<long long>(b) * P.n + i);
-      if (p < 0 || p >= i) {
-        err |= SPEC_ERR_PARENT;
-        p = 0;
-      }
-    }
-    if (!used) t = -1;
+  if constexpr (!kListed) {
+    for (int i = tid; i < S::kTable + S::kWords; i += kThreads) count[i] = 0u;  // and the bitmap
+    if (biased)
+      for (int i = tid; i < S::kTable; i += kThreads) bias[i] = 0.f;
+    if (tid == 0) s_err = s_used = 0;
+    __syncthreads();
+  }
+  // a token of the slab that something applies to: into the list
+  const auto touch = [&](unsigned at) {
+    const unsigned bit = 1u << (at & 31);
+    if (!(listed[at >> 5] & bit) && !(atomicOr(&listed[at >> 5], bit) & bit))
+      list[atomicAdd(&s_used, 1)] = static_cast<unsigned short>(at);
+  };
+  const auto place_of = [&](int t) {
+    const unsigned at = static_cast<unsigned>(t - lo);
+    return t >= 0 && at < static_cast<unsigned>(S::kTable) ? static_cast<int>(at) : -1;
+  };
+  for (int i = tid; i < P.n; i += kThreads) {
+    int t, p;
+    draft_of(P, b, i, t, p, err);
     s_tok[i] = t;
     s_par[i] = p;
     s_mask[i] = mask_row(i);
-    if (in_slab(t)) {
-      const int at = t - lo;
-      if (!((atomicOr(&drafted[at >> 5], 1u << (at & 31)) >> (at & 31)) & 1u))
-        list[kTable - 1 - atomicAdd(&s_drafted, 1)] = static_cast<unsigned short>(at);
-    }
-    if (P.mask && P.mask_index) {
-      const int mi = __ldg(P.mask_index + static_cast<long long>(b) * P.n + i);
-      if (mi < -1 || mi >= P.mask_rows) err |= SPEC_ERR_MASK;
+    if constexpr (!kListed) {
+      const int at = place_of(t);
+      if (at >= 0) {
+        atomicOr(&count[at], kDrafted);
+        touch(at);
+      }
     }
   }
-  __syncthreads();
-
-  // a token that the history or a bias touches: into the list of fixed tokens unless it is drafted
-  const auto touch = [&](unsigned at) {
-    const unsigned bit = 1u << (at & 31);
-    if (!((drafted[at >> 5] | listed[at >> 5]) & bit) && !(atomicOr(&listed[at >> 5], bit) & bit))
-      list[atomicAdd(&s_fixed, 1)] = static_cast<unsigned short>(at);
-  };
-  // the history
-  if (P.history) {
-    int len = P.history_len ? __ldg(P.history_len + b) : P.history_ld;
-    if (len < 0 || len > P.history_ld) {
-      err |= SPEC_ERR_TOKEN;
-      len = len < 0 ? 0 : P.history_ld;
+  int e0 = 0, tokens;  // listed: the entries' first, in the workspace
+  if constexpr (kListed) {
+    pdl_wait();
+    const int* offsets = P.offsets + static_cast<long long>(b) * (P.slabs + 1);
+    // rows that start within a vector take up to e - 1 tokens of the slab before
+    const int slab = blockIdx.x, from = P.ld % E && slab > 0 ? slab - 1 : slab;
+    e0 = __ldcg(offsets + from);
+    tokens = __ldcg(offsets + slab + 1) - e0;
+    const long long src = static_cast<long long>(b) * P.capacity + e0;
+    for (int e = tid; e < min(tokens, S::kCache); e += kThreads) {
+      c_token[e] = __ldcg(P.entry_token + src + e);
+      c_count[e] = __ldcg(P.entry_count + src + e);
+      c_bias[e] = __ldcg(P.entry_bias + src + e);
     }
-    const int prompt = P.prompt_len ? __ldg(P.prompt_len + b) : 0;
-    const int* h = P.history + static_cast<long long>(b) * P.history_ld;
-    const auto take = [&](int t, int at) {
-      if (at >= len) return;
+    __syncthreads();
+  } else {
+    const Lengths len = lengths_of(P, b, err);
+    for_history<kThreads>(P, b, len.history, [&](int t, int at) {
       if (t < 0 || t >= P.V) {
         err |= SPEC_ERR_TOKEN;
         return;
       }
-      const unsigned o = static_cast<unsigned>(t - lo);
-      if (o < static_cast<unsigned>(kTable)) {
-        if (at < prompt) atomicOr(&count[o], kInPrompt);
-        else atomicAdd(&count[o], 1u);
-        touch(o);
-      }
-    };
-    // a thread's loads go out together: 8192 tokens per round where rows allow 16-byte loads
-    constexpr int kU = 8;
-    if (P.history_ld % 4 == 0 && !misaligned16(P.history)) {
-      for (int base = 4 * tid; base < len; base += 4 * kProcThreads * kU) {
-        int4 t[kU];
-#pragma unroll
-        for (int k = 0; k < kU; ++k) {
-          const int at = base + 4 * k * kProcThreads;
-          if (at < len) t[k] = __ldg(reinterpret_cast<const int4*>(h + at));
-        }
-#pragma unroll
-        for (int k = 0; k < kU; ++k) {
-          const int at = base + 4 * k * kProcThreads;
-          if (at >= len) break;
-          take(t[k].x, at);
-          take(t[k].y, at + 1);
-          take(t[k].z, at + 2);
-          take(t[k].w, at + 3);
-        }
-      }
-    } else {
-      for (int base = tid; base < len; base += kProcThreads * kU) {
-        int t[kU];
-#pragma unroll
-        for (int k = 0; k < kU; ++k) {
-          const int at = base + k * kProcThreads;
-          if (at < len) t[k] = __ldg(h + at);
-        }
-#pragma unroll
-        for (int k = 0; k < kU; ++k) {
-          const int at = base + k * kProcThreads;
-          if (at >= len) break;
-          take(t[k], at);
-        }
-      }
+      const int o = place_of(t);
+      if (o < 0) return;
+      if (at < len.prompt) atomicOr(&count[o], kInPrompt);
+      else atomicAdd(&count[o], 1u);
+      touch(o);
+    });
+    add_biases<kThreads>(P, b, len.bias, count, bias, &s_again, err, [&](int t) {
+      const int at = place_of(t);
+      if (at >= 0) touch(at);
+      return at;
+    });
+    const bool checks = blockIdx.x == 0 && blockIdx.y == 0;
+    if (checks && err) atomicOr(&s_err, err);
+    __syncthreads();
+    if (checks && tid == 0) {
+      if (P.seq_error) P.seq_error[b] = s_err;
+      if (s_err && P.error_word) atomicOr(P.error_word, s_err);
     }
-  }
-
-  // the biases, one warp, in their order (entries of one token add up as listed)
-  if (biased && warp == 0) {
-    int len = P.bias_len ? __ldg(P.bias_len + b) : P.bias_ld;
-    if (len < 0 || len > P.bias_ld) {
-      err |= SPEC_ERR_TOKEN;
-      len = len < 0 ? 0 : P.bias_ld;
-    }
-    constexpr int kAhead = 4;  // 32 entries a step, the loads of four steps at once
-    int ts[kAhead];
-    float xs[kAhead];
-    for (int base = 0; base < len; base += 32) {
-      const int step = base / 32 % kAhead;
-      if (step == 0) {
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-          const int at = base + 32 * k + lane;
-          const long long src = static_cast<long long>(b) * P.bias_ld + at;
-          ts[k] = at < len ? __ldg(P.bias_tokens + src) : -1;
-          xs[k] = at < len ? __ldg(P.bias_values + src) : 0.f;
-        }
-      }
-      int t = ts[0];
-      float x = xs[0];
-#pragma unroll
-      for (int k = 1; k < kAhead; ++k) {
-        t = step == k ? ts[k] : t;
-        x = step == k ? xs[k] : x;
-      }
-      if (base + lane < len && (t < 0 || t >= P.V)) {
-        err |= SPEC_ERR_TOKEN;
-        t = -1;
-      }
-      const unsigned o = static_cast<unsigned>(t - lo);
-      const bool mine = t >= 0 && o < static_cast<unsigned>(kTable);
-      const unsigned peers = __match_any_sync(0xffffffffu, mine ? static_cast<int>(o) : -1 - lane);
-      const bool alone = !mine || (peers & (peers - 1)) == 0;
-      if (__all_sync(0xffffffffu, alone)) {
-        if (mine) bias[o] += x;
-      } else {
-        for (int l = 0; l < 32; ++l) {
-          if (l == lane && mine) bias[o] += x;
-          __syncwarp();
-        }
-      }
-      if (mine) touch(o);
-      __syncwarp();
-    }
-  }
-  if (checks && err) atomicOr(&s_err, err);
-
-  // the stream
-  if (stream) {
-    for (int i = r0; i < r1; ++i) {
-      if (i + 1 < r1) load_row(i + 1, ok1, nxt);
-      if (i + 2 < r1) load_mask(i + 2, s_mask[i + 2], ok2);
-      store_row(i, ok0, cur);
-#pragma unroll
-      for (int j = 0; j < kVecs; ++j) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) cur[j][k] = nxt[j][k];
-        ok0[j] = ok1[j];
-        ok1[j] = ok2[j];
-      }
-    }
-  }
-  __syncthreads();
-  if (checks && tid == 0) {
-    if (P.seq_error) P.seq_error[b] = s_err;
-    if (s_err && P.error_word) atomicOr(P.error_word, s_err);
+    tokens = s_used;
   }
 
   const float rep = P.repetition ? __ldg(P.repetition + b) : 1.f;
   const float inv = __frcp_rn(rep);
   const float freq = P.frequency ? __ldg(P.frequency + b) : 0.f;
   const float pres = P.presence ? __ldg(P.presence + b) : 0.f;
-  // Whether this CTA writes table entry `at` in row i: rows that start within
-  // a vector shift the slab's tokens, and the mask must allow the token.
-  const auto writes = [&](int i, int at) {
-    const int v = lo + at;
-    const int t = v + lead_of(i) - v0 * E;
-    if (v < 0 || v >= P.V || t < 0 || t >= kSlab) return false;
-    const int mrow = s_mask[i];
-    return mrow < 0 || ((__ldg(P.mask + static_cast<long long>(mrow) * P.mask_ld + (v >> 5)) >> (v & 31)) & 1u);
-  };
-  const auto value = [&](int i, int at) {
-    return static_cast<const T*>(P.logits) + (static_cast<long long>(b) * P.n + i) * P.ld + (lo + at);
-  };
-  const auto rewrite = [&](int i, int at, uint32_t bits) {
-    const unsigned c = count[at];
-    float x = L::widen(bits);
-    if (c) x = __fmul_rn(x, x > 0.f ? inv : rep);
-    const unsigned made = c & ~kInPrompt;
-    if (made) x = __fsub_rn(x, __fmaf_rn(freq, static_cast<float>(made), pres));
-    const float plus = biased ? bias[at] : 0.f;
-    if (plus != 0.f) x = __fadd_rn(x, plus);
-    if (c || plus != 0.f)
-      store_bits(static_cast<T*>(P.out) + (static_cast<long long>(b) * P.n + i) * P.out_ld + (lo + at), L::round(x));
+  // Rewrites entry e's element of row i, which starts at element m of its first
+  // vector; `part` is the row's part of the slab.  (A masked element is -inf by
+  // now and stays.)
+  const auto rewrite = [&](int i, int e, T* part, int m) {
+    int at;
+    unsigned c;
+    float plus;
+    if constexpr (kListed) {
+      if (e < S::kCache) {
+        at = c_token[e] - lo;
+        c = c_count[e];
+        plus = c_bias[e];
+      } else {
+        const long long src = static_cast<long long>(b) * P.capacity + e0 + e;
+        at = __ldcg(P.entry_token + src) - lo;
+        c = __ldcg(P.entry_count + src);
+        plus = __ldcg(P.entry_bias + src);
+      }
+    } else {
+      at = list[e];
+      c = count[at];
+      plus = biased ? bias[at] : 0.f;
+    }
+    // rows that start within a vector shift the slab: the neighbours' tokens are not ours
+    const int place = at - (E - 1) + m;
+    if (place < 0 || place >= S::kTokens) return;
+    if (c & kDrafted) {  // its occurrences on the way to the row
+      const int t = lo + at;
+      if (tree) {
+        for (int a = i; a > 0; a = s_par[a]) c += s_tok[a] == t;
+      } else {
+        for (int a = 0; a < i; ++a) c += s_tok[a] == t;
+      }
+    }
+    c &= kInPrompt | kMade;
+    if (!c && plus == 0.f) return;
+    const uint32_t x = load_bits(part + place);
+    if (x == L::kNegInf) return;
+    float y = L::widen(x);
+    if (c) y = __fmul_rn(y, y > 0.f ? inv : rep);
+    const unsigned made = c & kMade;
+    if (made) y = __fsub_rn(y, __fmaf_rn(freq, static_cast<float>(made), pres));
+    if (plus != 0.f) y = __fadd_rn(y, plus);
+    store_bits(part + place, L::round(y));
   };
 
-  // tokens that are the same for every row: all (token, row) pairs, four in flight per thread
-  const int fixed = s_fixed;
-  const int pairs = fixed * (r1 - r0);
-  constexpr int kU = 4;
-  for (int base = tid; base < pairs; base += kProcThreads * kU) {
-    int row[kU], at[kU];
-    uint32_t x[kU];
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int p = base + u * kProcThreads;
-      at[u] = -1;
-      if (p < pairs) {
-        const int i = p / fixed;
-        row[u] = r0 + i;
-        at[u] = list[p - i * fixed];
-        if (!writes(row[u], at[u])) at[u] = -1;
-      }
-      if (at[u] >= 0) x[u] = load_bits(value(row[u], at[u]));
+  if (!stream) {
+    // in place: consecutive threads take the tokens of one row
+    const long long pairs = static_cast<long long>(tokens) * (r1 - r0);
+    for (long long p = tid; p < pairs; p += kThreads) {
+      const int i = r0 + static_cast<int>(p / tokens), e = static_cast<int>(p % tokens), m = lead_of(i);
+      rewrite(i, e,
+              static_cast<T*>(P.out) + (static_cast<long long>(b) * P.n + i) * P.out_ld +
+                  (static_cast<long long>(v0) * E - m),
+              m);
     }
-#pragma unroll
-    for (int u = 0; u < kU; ++u)
-      if (at[u] >= 0) rewrite(row[u], at[u], x[u]);
+    return;
   }
 
-  // drafted tokens: row by row
-  const int moving = s_drafted;
-  if (moving == 0) return;
-  if (!tree) {
-    for (int j = tid; j < r0; j += kProcThreads)
-      if (in_slab(s_tok[j])) atomicAdd(&count[s_tok[j] - lo], 1u);
-    for (int i = r0 + 1 + tid; i < r1; i += kProcThreads)
-      if (in_slab(s_tok[i - 1])) atomicOr(&change[i >> 5], 1u << (i & 31));
-  } else {
-    if (tid == 0)
-      for (int a = r0; a > 0; a = s_par[a])
-        if (in_slab(s_tok[a])) count[s_tok[a] - lo] += 1u;
-    for (int i = r0 + 1 + tid; i < r1; i += kProcThreads) {
-      int x = i - 1, y = i;
-      bool any = false;
-      while (x != y && !any) {
-        any = in_slab(s_tok[x > y ? x : y]);
-        if (x > y) x = s_par[x];
-        else y = s_par[y];
-      }
-      if (any) atomicOr(&change[i >> 5], 1u << (i & 31));
-    }
-  }
-  __syncthreads();
   for (int i = r0; i < r1; ++i) {
-    if (i > r0 && (change[i >> 5] >> (i & 31)) & 1u) {
-      __syncthreads();  // everyone is done with the previous row's counts
-      if (tid == 0) {
-        const auto add = [&](int t, unsigned d) {
-          if (in_slab(t)) count[t - lo] += d;
-        };
-        if (!tree) {
-          add(s_tok[i - 1], 1u);
-        } else {
-          int x = i - 1, y = i;  // leave x's path, enter y's, up to their last common node
-          while (x != y) {
-            if (x > y) {
-              add(s_tok[x], ~0u);
-              x = s_par[x];
-            } else {
-              add(s_tok[y], 1u);
-              y = s_par[y];
-            }
-          }
-        }
+    const long long row = static_cast<long long>(b) * P.n + i;
+    const int m = lead_of(i);
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      if (!ok0[j]) {
+        w[j][0] = w[j][1] = w[j][2] = w[j][3] = L::kNegInf4;
+      } else if (ok0[j] != kFull) {
+#pragma unroll
+        for (int k = 0; k < E; ++k)
+          if (!((ok0[j] >> k) & 1u)) L::set_bits(w[j], k, L::kNegInf);
       }
+      reinterpret_cast<uint4*>(tile)[j * kThreads + tid] = make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
+      ok0[j] = ok1[j];
+    }
+    if (i + 1 < r1) load_row(i + 1, ok0, w);
+    if (i + 2 < r1) load_mask(i + 2, s_mask[i + 2], ok1);
+    if (tokens > 0) {
+      __syncthreads();
+      for (int e = tid; e < tokens; e += kThreads) rewrite(i, e, tile, m);
       __syncthreads();
     }
-    for (int e = tid; e < moving; e += kProcThreads) {
-      const int at = list[kTable - 1 - e];
-      if (writes(i, at)) rewrite(i, at, load_bits(value(i, at)));
+    T* dst = static_cast<T*>(P.out) + row * P.out_ld;
+    const bool same = static_cast<int>((row * P.out_ld) % E) == m;
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      const int t0 = (v0 + j * kThreads + tid) * E - m;
+      if (t0 >= P.V) continue;
+      const uint4 x = reinterpret_cast<const uint4*>(tile)[j * kThreads + tid];
+      if (same && t0 >= 0 && t0 + E <= P.V) {
+        if (!(kDebugChecks && misaligned16(dst + t0))) *reinterpret_cast<uint4*>(dst + t0) = x;
+      } else {
+        const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int k = 0; k < E; ++k)
+          if (t0 + k >= 0 && t0 + k < P.V) store_bits(dst + t0 + k, L::bits(y, k));
+      }
     }
+    // (a thread writes its own vectors of the next row, after it has read these)
   }
 }
 
-template <typename T, int kVecs>
-size_t process_smem(const ProcessParams& p) {
-  constexpr int E = Lanes<T>::kN;
-  constexpr size_t table = table_tokens(E, kVecs);
-  size_t words = table + 2 * bitmap_words(E, kVecs) + kMaxRows / 32 + 3 * static_cast<size_t>(p.n);
-  if (p.bias_tokens) words += table;
-  return words * 4 + (table + 1) / 2 * 4;
-}
-
-int slabs_of(const ProcessParams& p, int elems, int vecs) {
-  // vectors of the longest row: a row may start anywhere in its first vector
-  const int lead = p.ld % elems ? elems - 1 : 0;
-  const int nvec = (p.V + lead + elems - 1) / elems;
-  return (nvec + kProcThreads * vecs - 1) / (kProcThreads * vecs);
-}
-
-template <typename T, int kVecs>
-cudaError_t launch_process(ProcessParams p, cudaStream_t s) {
-  const size_t dyn = process_smem<T, kVecs>(p);
-  cudaError_t e = cudaFuncSetAttribute(process_kernel<T, kVecs>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(dyn));
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+// A kernel's dynamic shared memory limit, raised where a call needs more.
+template <typename K>
+cudaError_t raise_smem(K kernel, size_t bytes, std::map<int, size_t>& done) {
+  static std::mutex mu;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const int slabs = slabs_of(p, Lanes<T>::kN, kVecs);
-  // few sequences and slabs: a sequence's rows are split as well (each part
-  // reads the history again)
+  std::lock_guard<std::mutex> lock(mu);
+  if (done[dev] >= bytes) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e == cudaSuccess) done[dev] = bytes;
+  return e;
+}
+
+template <typename T, int kThreads, int kVecs>
+int slabs_of(int V, long long ld) {
+  constexpr int E = Lanes<T>::kN;
+  // vectors of the longest row: a row may start anywhere in its first vector
+  const int lead = ld % E ? E - 1 : 0;
+  const int nvec = (V + lead + E - 1) / E;
+  return (nvec + kThreads * kVecs - 1) / (kThreads * kVecs);
+}
+
+template <typename T, int kThreads, int kVecs, bool kListed>
+cudaError_t launch_process(ProcessParams p, int nsm, cudaStream_t s) {
+  using S = Slab<T, kThreads, kVecs, kListed>;
+  static std::map<int, size_t> done;
+  const size_t dyn = S::smem(p);
+  const auto kernel = process_kernel<T, kThreads, kVecs, kListed>;
+  cudaError_t e = raise_smem(kernel, dyn, done);
+  if (e != cudaSuccess) return e;
+  const int slabs = slabs_of<T, kThreads, kVecs>(p.V, p.ld);
+  // few sequences and slabs: a sequence's rows are split as well
   const long long have = static_cast<long long>(slabs) * p.B;
-  const long long parts = (kFill + have - 1) / have;
-  const int chunks = static_cast<int>(parts < p.n ? parts : p.n);
-  p.rows_per_cta = (p.n + chunks - 1) / chunks;
-  const dim3 grid(static_cast<unsigned>(slabs), static_cast<unsigned>((p.n + p.rows_per_cta - 1) / p.rows_per_cta),
-                  static_cast<unsigned>(p.B));
-  process_kernel<T, kVecs><<<grid, kProcThreads, dyn, s>>>(p);
+  const long long fill = (kListed ? 1536LL : 1024LL) / kThreads * nsm;
+  const long long parts = std::min<long long>(p.n, std::max<long long>(1, fill / have));  // one round of CTAs
+  p.rows_per_cta = static_cast<int>((p.n + parts - 1) / parts);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(slabs), static_cast<unsigned>((p.n + p.rows_per_cta - 1) / p.rows_per_cta),
+                     static_cast<unsigned>(p.B));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = dyn;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = kListed ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+// The entries' places in the workspace.
+struct ProcessLayout {
+  int capacity;
+  size_t token, count, bias, total;
+};
+ProcessLayout process_layout(long long B, int n, int V, int history, int biases) {
+  ProcessLayout l{};
+  const long long most = static_cast<long long>(n) + history + biases;
+  l.capacity = static_cast<int>(std::min<long long>(most, V));
+  const size_t part = align256(static_cast<size_t>(B) * l.capacity * 4);
+  l.token = align256(static_cast<size_t>(B) * (kMaxSlabs + 1) * 4);
+  l.count = l.token + part;
+  l.bias = l.count + part;
+  l.total = l.bias + part;
+  return l;
+}
+
+cudaError_t launch_collect(ProcessParams p, cudaStream_t s) {
+  static std::map<int, size_t> done;
+  p.window = std::min(kWindow, (p.capacity + 31) / 32 * 32);
+  const size_t dyn = 8 * (static_cast<size_t>(std::min((p.V + 31) / 32, kRangeWords)) + p.window);
+  const cudaError_t e = raise_smem(collect_kernel, dyn, done);
+  if (e != cudaSuccess) return e;
+  collect_kernel<<<p.B, kCollectThreads, dyn, s>>>(p);
   return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t dispatch_process(const ProcessParams& p, cudaStream_t s) {
-  // long slabs read the history fewer times; short ones fill the GPU
-  if (static_cast<long long>(slabs_of(p, Lanes<T>::kN, 2)) * p.B * p.n >= kFill) return launch_process<T, 2>(p, s);
-  return launch_process<T, 1>(p, s);
+cudaError_t run_process(ProcessParams p, int nsm, cudaStream_t s) {
+  using Large = Slab<T, 512, 2, true>;
+  // One kernel where its CTAs come to a few rounds at most; beyond, the second
+  // launch costs less than the histories read per slab.
+  const long long ctas = static_cast<long long>(slabs_of<T, 512, 2>(p.V, p.ld)) * p.B;
+  if (ctas * p.n < 2LL * nsm) return launch_process<T, 256, 1, false>(p, nsm, s);
+  p.slab_tokens = Large::kTokens;
+  p.slabs = slabs_of<T, 512, 2>(p.V, p.ld);
+  const cudaError_t e = launch_collect(p, s);
+  return e == cudaSuccess ? launch_process<T, 512, 2, true>(p, nsm, s) : e;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace
 }  // namespace sv
+
+extern "C" size_t spec_process_workspace_size(int B, int n, int V, int history_ld, int bias_ld) {
+  if (B < 1 || B > sv::kMaxSeq || n < 1 || n > sv::kMaxRows || V < 1 || V > 2097152 || history_ld < 0 || bias_ld < 0)
+    return 0;
+  return sv::process_layout(B, n, V, history_ld, bias_ld).total;
+}
 
 extern "C" spec_status spec_process_logits(const spec_process_args* a, cudaStream_t stream) {
   using namespace sv;
@@ -603,6 +829,12 @@ extern "C" spec_status spec_process_logits(const spec_process_args* a, cudaStrea
   if (a->mask && (a->mask_rows < 1 || a->mask_ld < (a->V + 31) / 32)) return SPEC_EINVAL;
   if (a->mask && !a->mask_index && a->mask_rows < static_cast<long long>(a->B) * a->n) return SPEC_EINVAL;
   if (!aligned16(a->logits) || !aligned16(a->out)) return SPEC_EALIGN;
+  const int history = a->history ? a->history_ld : 0, biases = a->bias_tokens ? a->bias_ld : 0;
+  const ProcessLayout layout = process_layout(a->B, a->n, a->V, history, biases);
+  if (!a->workspace || a->workspace_bytes < layout.total || (reinterpret_cast<uintptr_t>(a->workspace) & 255u))
+    return SPEC_EWORKSPACE;
+  const int nsm = sm_count();
+  if (nsm < 1) return SPEC_ECUDA;
   ProcessParams p{};
   p.B = a->B;
   p.n = a->n;
@@ -631,7 +863,13 @@ extern "C" spec_status spec_process_logits(const spec_process_args* a, cudaStrea
   p.mask_index = a->mask_index;
   p.seq_error = a->seq_error;
   p.error_word = a->error_word;
+  char* ws = static_cast<char*>(a->workspace);
+  p.capacity = layout.capacity;
+  p.offsets = reinterpret_cast<int*>(ws);
+  p.entry_token = reinterpret_cast<int*>(ws + layout.token);
+  p.entry_count = reinterpret_cast<unsigned*>(ws + layout.count);
+  p.entry_bias = reinterpret_cast<float*>(ws + layout.bias);
   const cudaError_t e =
-      a->dtype == SPEC_BF16 ? dispatch_process<bf16_t>(p, stream) : dispatch_process<float>(p, stream);
+      a->dtype == SPEC_BF16 ? run_process<bf16_t>(p, nsm, stream) : run_process<float>(p, nsm, stream);
   return e == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
 }

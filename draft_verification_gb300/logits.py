@@ -74,7 +74,7 @@ class ProcessLogitsPlan(_Plan):
 
     def __init__(self, logits, tokens=None, *, parent=None, history=None, history_len=None, prompt_len=None,
                  repetition=None, frequency=None, presence=None, bias_tokens=None, bias_values=None, bias_len=None,
-                 mask=None, mask_index=None, out=None):
+                 mask=None, mask_index=None, out=None, workspace=None):
         ld = _logit_rows(logits, "logits")
         B, n, V = logits.shape
         dev = logits.device
@@ -126,6 +126,13 @@ class ProcessLogitsPlan(_Plan):
                      bias_tokens, bias_values, bias_len, mask, mask_index]
         self.out = dict(logits=out, seq_error=torch.empty(B, dtype=torch.int32, device=dev),
                         error_word=torch.zeros(1, dtype=torch.int32, device=dev))
+        need = int(lib.spec_process_workspace_size(B, n, V, 0 if history is None else history.shape[1],
+                                                   0 if bias_tokens is None else bias_tokens.shape[1]))
+        if need == 0:
+            raise ValueError(f"process_logits: sizes out of range: B={B} n={n} V={V}")
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        self.workspace = workspace
         a = L.ProcessArgs()
         a.B, a.n, a.V, a.dtype = B, n, V, _DTYPES[logits.dtype]
         a.ld, a.out_ld = ld, out_ld
@@ -142,6 +149,7 @@ class ProcessLogitsPlan(_Plan):
         a.mask, a.mask_index = _ptr(mask), _ptr(_i32(mask_index, "mask_index"))
         a.mask_rows, a.mask_ld = (0, 0) if mask is None else (mask.shape[0], mask_ld)
         a.seq_error, a.error_word = _ptr(self.out["seq_error"]), _ptr(self.out["error_word"])
+        a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel()
         self.args = a
         self._call = lib.spec_process_logits
 

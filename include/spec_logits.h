@@ -41,8 +41,8 @@ extern "C" {
 /*    x3 = x2 + the sum of b's bias entries for v, in their order          */
 /*    y  = allowed ? x3 : -inf                                             */
 /* in float32, rounded once to the logits' type; an element that nothing   */
-/* applies to keeps its bits.  A masked element is -inf whatever it held   */
-/* (NaN included); a row whose mask allows nothing is all -inf, which the  */
+/* applies to keeps its bits, and -inf stays -inf.  A masked element is     */
+/* -inf whatever it held (NaN included); a row whose mask allows nothing is all -inf, which the  */
 /* verification reports as SPEC_ERR_NONFINITE.                             */
 /*  - `out` may be `logits` itself (with the same ld) or must not overlap  */
 /*    it.                                                                  */
@@ -52,7 +52,8 @@ extern "C" {
 /*    SPEC_ERR_PARENT and counts as the root's child.  A mask_index        */
 /*    outside [-1, mask_rows) sets SPEC_ERR_MASK: the row is not masked.   */
 /*    Everything else of the sequence is processed all the same.           */
-/*  - One kernel launch.                                                   */
+/*  - One kernel launch for small calls; for large ones two, of which the   */
+/*    first gathers the sequences' distinct tokens in the workspace.        */
 /* ---------------------------------------------------------------------- */
 typedef struct spec_process_args {
   int B;                       /* sequences, 1..65535                              */
@@ -92,11 +93,17 @@ typedef struct spec_process_args {
                                /* NULL: row (b, i) uses mask row b * n + i         */
   int* seq_error;              /* out [B], optional                                */
   int* error_word;             /* in/out, optional: error bits OR-ed in            */
+  void* workspace;             /* 256-byte aligned; needs no initialisation        */
+  size_t workspace_bytes;
 } spec_process_args;
 
+/* history_ld and bias_ld as in the arguments (0 without a history, without   */
+/* biases).  0 for sizes outside the limits.                                  */
+size_t spec_process_workspace_size(int B, int n, int V, int history_ld, int bias_ld);
 /* SPEC_EINVAL: a size outside the limits, a NULL required pointer, or out =  */
 /* logits with another stride; SPEC_EDTYPE; SPEC_EALIGN: logits or out not    */
-/* 16-byte aligned; SPEC_ECUDA: the launch failed.                            */
+/* 16-byte aligned; SPEC_EWORKSPACE: workspace NULL, short or not 256-byte     */
+/* aligned; SPEC_ECUDA: a launch failed.                                      */
 spec_status spec_process_logits(const spec_process_args* args, cudaStream_t stream);
 
 /* ---------------------------------------------------------------------- */

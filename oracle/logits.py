@@ -96,7 +96,7 @@ def process_logits(logits, tokens=None, parent=None, history=None, history_len=N
                 x1 = np.where(seen, np.where(x > 0, x / rho, x * rho), x)
                 pen = np.where(made > 0, freq * made + pres, 0.0)
                 x2 = np.where(made > 0, x1 - pen, x1)
-                x3 = np.where(biased, x2 + bias, x2)
+                x3 = np.where(np.isneginf(x), x, np.where(biased, x2 + bias, x2))  # -inf stays -inf
                 scale[b, i] = (np.abs(x1) + np.abs(freq * made) + abs(pres) + np.abs(pen) + np.abs(x2) + bias_abs
                                + np.abs(x3))
             t = seen | biased

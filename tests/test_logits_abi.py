@@ -77,7 +77,9 @@ def _process(**kw):
     a = _lib.ProcessArgs()
     a.B, a.n, a.V, a.dtype, a.ld, a.out_ld = 2, 4, 100, _lib.SPEC_BF16, 100, 100
     a.tokens_ld, a.history_ld, a.bias_ld, a.mask_rows, a.mask_ld = 4, 7, 3, 8, 4
-    return _fill(a, ("logits", "tokens", "history", "bias_tokens", "bias_values", "mask"), {"out": 0x20000, **kw})
+    a.workspace_bytes = 1 << 30
+    return _fill(a, ("logits", "tokens", "history", "bias_tokens", "bias_values", "mask", "workspace"),
+                 {"out": 0x20000, **kw})
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -87,7 +89,7 @@ def _process(**kw):
     (dict(out=FAKE + 2), -3), (dict(out=FAKE, out_ld=104), -1), (dict(tokens_ld=2), -1),
     (dict(parent=FAKE, tokens_ld=3), -1), (dict(parent=FAKE, tokens=None), -1), (dict(history_ld=-1), -1),
     (dict(bias_values=None), -1), (dict(bias_ld=-1), -1), (dict(mask_rows=0), -1), (dict(mask_rows=7), -1),
-    (dict(mask_ld=3), -1),
+    (dict(mask_ld=3), -1), (dict(workspace=None), -4), (dict(workspace_bytes=64), -4), (dict(workspace=FAKE + 16), -4),
 ])
 def test_process_refusals(lib, kw, code):
     assert lib.spec_process_logits(C.byref(_process(**kw)), None) == code
@@ -140,6 +142,14 @@ def test_product_workspace_size_is_zero_outside_the_limits(lib):
     assert size(1, 1000, 256, 128) > 0
     for bad in [(0, 10, 256, 64), (65536, 10, 256, 64), (1, 0, 256, 64), (1, 2097153, 256, 64), (1, 10, 96, 64),
                 (1, 10, 256, 16), (1, 10, 65664, 128)]:
+        assert size(*bad) == 0, bad
+
+
+def test_process_workspace_size_is_zero_outside_the_limits(lib):
+    size = lib.spec_process_workspace_size
+    assert size(1, 1, 10, 0, 0) > 0
+    for bad in [(0, 1, 10, 0, 0), (65536, 1, 10, 0, 0), (1, 0, 10, 0, 0), (1, 1025, 10, 0, 0), (1, 1, 0, 0, 0),
+                (1, 1, 2097153, 0, 0), (1, 1, 10, -1, 0), (1, 1, 10, 0, -1)]:
         assert size(*bad) == 0, bad
 
 
