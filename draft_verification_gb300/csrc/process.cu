@@ -245,7 +245,6 @@ __device__ __forceinline__ void add_biases(const ProcessParams& P, int b, int le
   __syncthreads();
   for (int e = tid; e < len; e += kThreads) {
     const int t = __ldg(P.bias_tokens + src + e);
-    const float x = __ldg(P.bias_values + src + e);
     if (t < 0 || t >= P.V) {
       err |= SPEC_ERR_TOKEN;
       continue;
@@ -253,29 +252,35 @@ __device__ __forceinline__ void add_biases(const ProcessParams& P, int b, int le
     const int at = enter(t);
     if (at < 0) continue;
     if (atomicOr(&words[at], kBiased) & kBiased) *again = 1;
-    else bias[at] = x;
   }
   __syncthreads();
-  if (!*again) return;
-  if (tid < 32) {
-    for (int pass = 0; pass < 2; ++pass) {  // clear, then add
-      for (int base = 0; base < len; base += 32) {
-        const int t = base + lane < len ? __ldg(P.bias_tokens + src + base + lane) : -1;
-        const float x = base + lane < len ? __ldg(P.bias_values + src + base + lane) : 0.f;
-        const int at = t >= 0 && t < P.V ? enter(t) : -1;
-        __syncwarp();
-        // entries of one token: the lowest lane first
-        unsigned peers = __match_any_sync(0xffffffffu, at >= 0 ? at : -1 - lane);
-        bool todo = at >= 0;
-        while (__any_sync(0xffffffffu, todo)) {
-          const int lowest = __ffs(peers) - 1;
-          if (todo && lowest == lane) {
-            bias[at] = pass == 0 ? 0.f : bias[at] + x;
-            todo = false;
-          }
-          peers &= peers - 1;
-          __syncwarp();
+  if (!*again) {
+    for (int e = tid; e < len; e += kThreads) {
+      const int t = __ldg(P.bias_tokens + src + e);
+      const int at = t >= 0 && t < P.V ? enter(t) : -1;
+      if (at >= 0) bias[at] = __ldg(P.bias_values + src + e);
+    }
+  } else if (tid < 32) {
+    int t_next = lane < len ? __ldg(P.bias_tokens + src + lane) : -1;
+    float x_next = lane < len ? __ldg(P.bias_values + src + lane) : 0.f;
+    for (int base = 0; base < len; base += 32) {
+      const int t = t_next;
+      const float x = x_next;
+      const int ahead = base + 32 + lane;
+      t_next = ahead < len ? __ldg(P.bias_tokens + src + ahead) : -1;
+      x_next = ahead < len ? __ldg(P.bias_values + src + ahead) : 0.f;
+      const int at = t >= 0 && t < P.V ? enter(t) : -1;
+      __syncwarp();
+      // entries of one token: the lowest lane first
+      unsigned peers = __match_any_sync(0xffffffffu, at >= 0 ? at : -1 - lane);
+      bool todo = at >= 0;
+      while (__any_sync(0xffffffffu, todo)) {
+        if (todo && __ffs(peers) - 1 == lane) {
+          bias[at] += x;
+          todo = false;
         }
+        peers &= peers - 1;
+        __syncwarp();
       }
     }
   }
@@ -426,11 +431,12 @@ struct Slab {
   static constexpr int kTokens = kThreads * kVecs * kE;
   static constexpr int kTable = kTokens + kE - 1;        // and the e - 1 tokens before it
   static constexpr int kWords = (kTable + 31) / 32;      // a bitmap of the table
-  static constexpr int kTileBytes = kTokens * static_cast<int>(sizeof(T));
-  static constexpr int kCache = 1024;                    // listed entries kept in shared memory
+  static constexpr int kTileBytes = kTokens * static_cast<int>(sizeof(T));  // a row's part; there are two
+  static constexpr int kCache = 4096;                    // listed entries kept in shared memory
+  static_assert(!kListed || kTable <= 0x3fff, "an entry's place and two flags in 16 bits");
   static size_t smem(const ProcessParams& p) {
-    const size_t rows = kTileBytes + 12 * static_cast<size_t>(p.n);
-    if (kListed) return rows + 12 * static_cast<size_t>(kCache);
+    const size_t rows = 2 * kTileBytes + 12 * static_cast<size_t>(p.n);
+    if (kListed) return rows + 6 * static_cast<size_t>(kCache);
     return rows + 4 * (static_cast<size_t>(kTable) * (p.bias_tokens ? 2 : 1) + 2 * kWords) + 2 * static_cast<size_t>(kTable);
   }
 };
@@ -443,14 +449,15 @@ __global__ void __launch_bounds__(kThreads, (kListed ? 1536 : 1024) / kThreads) 
   constexpr uint32_t kFull = (1u << E) - 1u;
 
   extern __shared__ __align__(16) unsigned char proc_dyn[];
-  T* tile = reinterpret_cast<T*>(proc_dyn);                              // [kTokens] one row's part
-  int* s_tok = reinterpret_cast<int*>(proc_dyn + S::kTileBytes);         // [n]
+  T* tile = reinterpret_cast<T*>(proc_dyn);                              // [2][kTokens] rows' parts
+  int* s_tok = reinterpret_cast<int*>(proc_dyn + 2 * S::kTileBytes);     // [n]
   int* s_par = s_tok + P.n;                                              // [n]
   int* s_mask = s_par + P.n;                                             // [n]
-  // listed: the first kCache entries
-  int* c_token = s_mask + P.n;
-  unsigned* c_count = reinterpret_cast<unsigned*>(c_token + S::kCache);
-  float* c_bias = reinterpret_cast<float*>(c_count + S::kCache);
+  // listed: the first kCache entries, as they apply to every row: what is added,
+  // and the place in the table with two flags (bit 14: repetition; bit 15:
+  // drafted, so that the row matters and the entry is read again)
+  float* c_add = reinterpret_cast<float*>(s_mask + P.n);
+  unsigned short* c_place = reinterpret_cast<unsigned short*>(c_add + S::kCache);
   // else: the table, two bitmaps and the list of touched tokens
   unsigned* count = reinterpret_cast<unsigned*>(s_mask + P.n);           // [kTable]
   unsigned* listed = count + S::kTable;                                  // [kWords]
@@ -561,6 +568,15 @@ __global__ void __launch_bounds__(kThreads, (kListed ? 1536 : 1024) / kThreads) 
       }
     }
   }
+  const float rep = P.repetition ? __ldg(P.repetition + b) : 1.f;
+  const float inv = __frcp_rn(rep);
+  const float freq = P.frequency ? __ldg(P.frequency + b) : 0.f;
+  const float pres = P.presence ? __ldg(P.presence + b) : 0.f;
+  // what a word and a bias add to an element after its repetition penalty
+  const auto added = [&](unsigned c, float plus) {
+    const unsigned made = c & kMade;
+    return made ? __fsub_rn(plus, __fmaf_rn(freq, static_cast<float>(made), pres)) : plus;
+  };
   int e0 = 0, tokens;  // listed: the entries' first, in the workspace
   if constexpr (kListed) {
     pdl_wait();
@@ -571,9 +587,12 @@ __global__ void __launch_bounds__(kThreads, (kListed ? 1536 : 1024) / kThreads) 
     tokens = __ldcg(offsets + slab + 1) - e0;
     const long long src = static_cast<long long>(b) * P.capacity + e0;
     for (int e = tid; e < min(tokens, S::kCache); e += kThreads) {
-      c_token[e] = __ldcg(P.entry_token + src + e);
-      c_count[e] = __ldcg(P.entry_count + src + e);
-      c_bias[e] = __ldcg(P.entry_bias + src + e);
+      const int at = __ldcg(P.entry_token + src + e) - lo;
+      const unsigned c = __ldcg(P.entry_count + src + e);
+      c_add[e] = added(c, __ldcg(P.entry_bias + src + e));
+      // (places beyond the table: tokens of the slab before that no row takes)
+      c_place[e] = static_cast<unsigned short>((at < 0 ? 0x3fff : at) | (c & (kInPrompt | kMade) ? 0x4000 : 0) |
+                                               (c & kDrafted ? 0x8000 : 0));
     }
     __syncthreads();
   } else {
@@ -604,53 +623,57 @@ __global__ void __launch_bounds__(kThreads, (kListed ? 1536 : 1024) / kThreads) 
     tokens = s_used;
   }
 
-  const float rep = P.repetition ? __ldg(P.repetition + b) : 1.f;
-  const float inv = __frcp_rn(rep);
-  const float freq = P.frequency ? __ldg(P.frequency + b) : 0.f;
-  const float pres = P.presence ? __ldg(P.presence + b) : 0.f;
   // Rewrites entry e's element of row i, which starts at element m of its first
   // vector; `part` is the row's part of the slab.  (A masked element is -inf by
   // now and stays.)
   const auto rewrite = [&](int i, int e, T* part, int m) {
     int at;
-    unsigned c;
-    float plus;
+    unsigned c = 0;
+    float add = 0.f;
+    bool seen, again = true;
     if constexpr (kListed) {
       if (e < S::kCache) {
-        at = c_token[e] - lo;
-        c = c_count[e];
-        plus = c_bias[e];
+        at = c_place[e];
+        add = c_add[e];
+        seen = at & 0x4000;
+        again = at & 0x8000;
+        at &= 0x3fff;
       } else {
-        const long long src = static_cast<long long>(b) * P.capacity + e0 + e;
-        at = __ldcg(P.entry_token + src) - lo;
-        c = __ldcg(P.entry_count + src);
-        plus = __ldcg(P.entry_bias + src);
+        at = __ldcg(P.entry_token + static_cast<long long>(b) * P.capacity + e0 + e) - lo;
       }
     } else {
       at = list[e];
-      c = count[at];
-      plus = biased ? bias[at] : 0.f;
     }
     // rows that start within a vector shift the slab: the neighbours' tokens are not ours
     const int place = at - (E - 1) + m;
     if (place < 0 || place >= S::kTokens) return;
-    if (c & kDrafted) {  // its occurrences on the way to the row
-      const int t = lo + at;
-      if (tree) {
-        for (int a = i; a > 0; a = s_par[a]) c += s_tok[a] == t;
+    if (again) {
+      float plus;
+      if constexpr (kListed) {
+        const long long src = static_cast<long long>(b) * P.capacity + e0 + e;
+        c = __ldcg(P.entry_count + src);
+        plus = __ldcg(P.entry_bias + src);
       } else {
-        for (int a = 0; a < i; ++a) c += s_tok[a] == t;
+        c = count[at];
+        plus = biased ? bias[at] : 0.f;
       }
+      if (c & kDrafted) {  // its occurrences on the way to the row
+        const int t = lo + at;
+        if (tree) {
+          for (int a = i; a > 0; a = s_par[a]) c += s_tok[a] == t;
+        } else {
+          for (int a = 0; a < i; ++a) c += s_tok[a] == t;
+        }
+      }
+      seen = c & (kInPrompt | kMade);
+      add = added(c, plus);
     }
-    c &= kInPrompt | kMade;
-    if (!c && plus == 0.f) return;
+    if (!seen && add == 0.f) return;
     const uint32_t x = load_bits(part + place);
     if (x == L::kNegInf) return;
     float y = L::widen(x);
-    if (c) y = __fmul_rn(y, y > 0.f ? inv : rep);
-    const unsigned made = c & kMade;
-    if (made) y = __fsub_rn(y, __fmaf_rn(freq, static_cast<float>(made), pres));
-    if (plus != 0.f) y = __fadd_rn(y, plus);
+    if (seen) y = __fmul_rn(y, y > 0.f ? inv : rep);
+    if (add != 0.f) y = __fadd_rn(y, add);
     store_bits(part + place, L::round(y));
   };
 
@@ -667,9 +690,9 @@ __global__ void __launch_bounds__(kThreads, (kListed ? 1536 : 1024) / kThreads) 
     return;
   }
 
-  for (int i = r0; i < r1; ++i) {
-    const long long row = static_cast<long long>(b) * P.n + i;
-    const int m = lead_of(i);
+  // Row i's vectors, masked, into its tile; then the loads of row i + 1 go out.
+  const auto fill = [&](int i) {
+    uint4* to = reinterpret_cast<uint4*>(tile + ((i - r0) & 1) * S::kTokens);
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
       if (!ok0[j]) {
@@ -679,23 +702,31 @@ __global__ void __launch_bounds__(kThreads, (kListed ? 1536 : 1024) / kThreads) 
         for (int k = 0; k < E; ++k)
           if (!((ok0[j] >> k) & 1u)) L::set_bits(w[j], k, L::kNegInf);
       }
-      reinterpret_cast<uint4*>(tile)[j * kThreads + tid] = make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
+      to[j * kThreads + tid] = make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
       ok0[j] = ok1[j];
     }
     if (i + 1 < r1) load_row(i + 1, ok0, w);
     if (i + 2 < r1) load_mask(i + 2, s_mask[i + 2], ok1);
-    if (tokens > 0) {
-      __syncthreads();
-      for (int e = tid; e < tokens; e += kThreads) rewrite(i, e, tile, m);
-      __syncthreads();
-    }
+  };
+  // While row i is rewritten in one tile, row i + 1 fills the other: one
+  // barrier per row.  (A thread fills a tile again after it has written out its
+  // own vectors of it, which nobody else touches in between.)
+  fill(r0);
+  __syncthreads();
+  for (int i = r0; i < r1; ++i) {
+    const long long row = static_cast<long long>(b) * P.n + i;
+    const int m = lead_of(i);
+    T* part = tile + ((i - r0) & 1) * S::kTokens;
+    for (int e = tid; e < tokens; e += kThreads) rewrite(i, e, part, m);
+    if (i + 1 < r1) fill(i + 1);
+    if (tokens > 0) __syncthreads();
     T* dst = static_cast<T*>(P.out) + row * P.out_ld;
     const bool same = static_cast<int>((row * P.out_ld) % E) == m;
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
       const int t0 = (v0 + j * kThreads + tid) * E - m;
       if (t0 >= P.V) continue;
-      const uint4 x = reinterpret_cast<const uint4*>(tile)[j * kThreads + tid];
+      const uint4 x = reinterpret_cast<const uint4*>(part)[j * kThreads + tid];
       if (same && t0 >= 0 && t0 + E <= P.V) {
         if (!(kDebugChecks && misaligned16(dst + t0))) *reinterpret_cast<uint4*>(dst + t0) = x;
       } else {
@@ -705,7 +736,6 @@ __global__ void __launch_bounds__(kThreads, (kListed ? 1536 : 1024) / kThreads) 
           if (t0 + k >= 0 && t0 + k < P.V) store_bits(dst + t0 + k, L::bits(y, k));
       }
     }
-    // (a thread writes its own vectors of the next row, after it has read these)
   }
 }
 
