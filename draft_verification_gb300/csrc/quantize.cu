@@ -54,22 +54,35 @@ __device__ __forceinline__ unsigned short to_bf16(float x) {
   return r;
 }
 
+// 8 consecutive weights as they are in memory, their extremes, and one of them.
 template <typename T, bool kVec>
-__device__ __forceinline__ void load8(const T* p, float (&w)[8]) {
-  if constexpr (sizeof(T) == 2) {
+struct Eight;
+
+template <bool kVec>
+struct Eight<bf16_t, kVec> {
+  uint32_t u[4];
+  __device__ __forceinline__ void load(const bf16_t* p) {
     if constexpr (kVec) {
       const uint4 v = ld_stream16(p);
-      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        w[2 * j] = bf16_lo(u[j]);
-        w[2 * j + 1] = bf16_hi(u[j]);
-      }
+      u[0] = v.x;
+      u[1] = v.y;
+      u[2] = v.z;
+      u[3] = v.w;
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = load_elem(p + j);
+      for (int j = 0; j < 4; ++j)
+        u[j] = __ldg(reinterpret_cast<const unsigned short*>(p) + 2 * j) |
+               static_cast<uint32_t>(__ldg(reinterpret_cast<const unsigned short*>(p) + 2 * j + 1)) << 16;
     }
-  } else {
+  }
+  __device__ __forceinline__ void clear() { u[0] = u[1] = u[2] = u[3] = 0u; }
+  __device__ __forceinline__ float get(int j) const { return (j & 1) ? bf16_hi(u[j >> 1]) : bf16_lo(u[j >> 1]); }
+};
+
+template <bool kVec>
+struct Eight<float, kVec> {
+  float w[8];
+  __device__ __forceinline__ void load(const float* p) {
     if constexpr (kVec) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -83,6 +96,77 @@ __device__ __forceinline__ void load8(const T* p, float (&w)[8]) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) w[j] = load_elem(p + j);
     }
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = 0.f;
+  }
+  __device__ __forceinline__ float get(int j) const { return w[j]; }
+};
+
+// Extremes of the groups (`lanes` lanes) of four rows, 0 included and
+// NaN-propagating; this lane keeps those of row lane % 4.  hi: max w (max |w|
+// without zeros); lo: max(0, -min w).
+template <bool kZeros, bool kVec>
+__device__ __forceinline__ void extremes(const Eight<float, kVec> (&x)[4], int lanes, float& hi, float& lo) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float h = 0.f, l = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      h = fmax_nan(h, kZeros ? x[i].w[j] : fabsf(x[i].w[j]));
+      if constexpr (kZeros) l = fmax_nan(l, -x[i].w[j]);
+    }
+    for (int o = lanes >> 1; o > 0; o >>= 1) {
+      h = fmax_nan(h, __shfl_xor_sync(0xffffffffu, h, o));
+      if constexpr (kZeros) l = fmax_nan(l, __shfl_xor_sync(0xffffffffu, l, o));
+    }
+    if ((lane & 3) == i) {
+      hi = h;
+      lo = l;
+    }
+  }
+}
+// bfloat16: two values to a register all the way (the extremes of bfloat16
+// values are bfloat16), two rows or both extremes of one row per shuffle.
+template <bool kZeros, bool kVec>
+__device__ __forceinline__ void extremes(const Eight<bf16_t, kVec> (&x)[4], int lanes, float& hi, float& lo) {
+  const int lane = threadIdx.x & 31;
+  const auto both = [](uint32_t a, uint32_t b, uint32_t c, uint32_t d) {  // the maximum of eight, in both halves
+    const uint32_t m = bmax2_nan(bmax2_nan(a, b), bmax2_nan(c, d));
+    return bmax2_nan(m, __byte_perm(m, m, 0x1032));
+  };
+  constexpr int kRegs = kZeros ? 4 : 2;
+  uint32_t m[kRegs];
+  if constexpr (kZeros) {
+    const uint32_t sign = 0x80008000u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t(&u)[4] = x[i].u;
+      m[i] = __byte_perm(both(u[0], u[1], u[2], u[3]), both(u[0] ^ sign, u[1] ^ sign, u[2] ^ sign, u[3] ^ sign), 0x5410);
+    }
+  } else {
+    const uint32_t magnitude = 0x7fff7fffu;
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      const uint32_t(&u)[4] = x[i].u;
+      const uint32_t(&v)[4] = x[i + 1].u;
+      m[i / 2] = __byte_perm(both(u[0] & magnitude, u[1] & magnitude, u[2] & magnitude, u[3] & magnitude),
+                             both(v[0] & magnitude, v[1] & magnitude, v[2] & magnitude, v[3] & magnitude), 0x5410);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kRegs; ++i)
+    for (int o = lanes >> 1; o > 0; o >>= 1) m[i] = bmax2_nan(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
+  if constexpr (kZeros) {
+    const uint32_t mine = (lane & 2) ? ((lane & 1) ? m[3] : m[2]) : ((lane & 1) ? m[1] : m[0]);
+    hi = fmax_nan(0.f, bf16_lo(mine));
+    lo = fmax_nan(0.f, bf16_hi(mine));
+  } else {
+    const uint32_t mine = (lane & 2) ? m[1] : m[0];
+    hi = (lane & 1) ? bf16_hi(mine) : bf16_lo(mine);
+    lo = 0.f;
   }
 }
 
@@ -100,38 +184,16 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantPara
   const int k = k0 + lane * 8;
   constexpr int kPer = kQuantRows / (kQuantThreads / 32);
   static_assert(kPer == 4, "a group has at least 4 lanes: one for each row");
-  float w[kPer][8];
+  Eight<T, kVec> x[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int v = v0 + warp * kPer + i;
-    if (v < P.V && k < P.d) {
-      load8<T, kVec>(static_cast<const T*>(P.weights) + static_cast<long long>(v) * P.ld + k, w[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w[i][j] = 0.f;
-    }
+    if (v < P.V && k < P.d) x[i].load(static_cast<const T*>(P.weights) + static_cast<long long>(v) * P.ld + k);
+    else x[i].clear();
   }
   const int lanes = P.group >> 3;  // lanes of a group
-  // extremes of this lane's group in each row, 0 included; NaN-propagating
-  // (lo holds max(0, -min))
-  float hi = 0.f, lo = 0.f;  // of row lane % 4
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    float h = 0.f, l = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      h = fmax_nan(h, kZeros ? w[i][j] : fabsf(w[i][j]));
-      if constexpr (kZeros) l = fmax_nan(l, -w[i][j]);
-    }
-    for (int o = lanes >> 1; o > 0; o >>= 1) {
-      h = fmax_nan(h, __shfl_xor_sync(0xffffffffu, h, o));
-      if constexpr (kZeros) l = fmax_nan(l, __shfl_xor_sync(0xffffffffu, l, o));
-    }
-    if ((lane & 3) == i) {
-      hi = h;
-      lo = l;
-    }
-  }
+  float hi = 0.f, lo = 0.f;        // the group's in row lane % 4
+  extremes<kZeros>(x, lanes, hi, lo);
   // row lane % 4: the scale, its reciprocal and the zero point
   unsigned short sb = to_bf16(kZeros ? __fdiv_rn(__fadd_rn(hi, lo), 15.f) : __fdiv_rn(hi, 7.f));
   float s = __uint_as_float(static_cast<uint32_t>(sb) << 16);
@@ -158,12 +220,12 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantPara
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if constexpr (sizeof(T) == 2) {
-          const float t = __fadd_rn(__fmaf_rn(w[i][j], ri, kGrid), kWhole - kGrid);
+          const float t = __fadd_rn(__fmaf_rn(x[i].get(j), ri, kGrid), kWhole - kGrid);
           c[j] = __fadd_rn(t, zi - kWhole);
         } else {
-          const float q = __fmul_rn(w[i][j], ri);
+          const float q = __fmul_rn(x[i].get(j), ri);
           float t = __fadd_rn(__fadd_rn(q, kWhole), -kWhole);
-          if (fabsf(__fadd_rn(q, -t)) > 0.4999f) t = rintf(__fdiv_rn(w[i][j], si));
+          if (fabsf(__fadd_rn(q, -t)) > 0.4999f) t = rintf(__fdiv_rn(x[i].get(j), si));
           c[j] = __fadd_rn(t, zi);
         }
         // without zeros |w / s| < 7.5, and with them w / s rounds to -z or more
@@ -172,7 +234,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantPara
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float q = si > 0.f ? rintf(__fdiv_rn(w[i][j], si)) : 0.f;
+        const float q = si > 0.f ? rintf(__fdiv_rn(x[i].get(j), si)) : 0.f;
         c[j] = fminf(fmaxf(__fadd_rn(q, zi), 0.f), 15.f);
       }
     }
