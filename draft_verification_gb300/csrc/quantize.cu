@@ -104,11 +104,11 @@ struct Eight<float, kVec> {
   __device__ __forceinline__ float get(int j) const { return w[j]; }
 };
 
-// Extremes of the groups (`lanes` lanes) of four rows, 0 included and
+// Extremes of the groups (kLanes lanes) of four rows, 0 included and
 // NaN-propagating; this lane keeps those of row lane % 4.  hi: max w (max |w|
 // without zeros); lo: max(0, -min w).
-template <bool kZeros, bool kVec>
-__device__ __forceinline__ void extremes(const Eight<float, kVec> (&x)[4], int lanes, float& hi, float& lo) {
+template <bool kZeros, int kLanes, bool kVec>
+__device__ __forceinline__ void extremes(const Eight<float, kVec> (&x)[4], float& hi, float& lo) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -118,7 +118,8 @@ __device__ __forceinline__ void extremes(const Eight<float, kVec> (&x)[4], int l
       h = fmax_nan(h, kZeros ? x[i].w[j] : fabsf(x[i].w[j]));
       if constexpr (kZeros) l = fmax_nan(l, -x[i].w[j]);
     }
-    for (int o = lanes >> 1; o > 0; o >>= 1) {
+#pragma unroll
+    for (int o = kLanes >> 1; o > 0; o >>= 1) {
       h = fmax_nan(h, __shfl_xor_sync(0xffffffffu, h, o));
       if constexpr (kZeros) l = fmax_nan(l, __shfl_xor_sync(0xffffffffu, l, o));
     }
@@ -130,8 +131,8 @@ __device__ __forceinline__ void extremes(const Eight<float, kVec> (&x)[4], int l
 }
 // bfloat16: two values to a register all the way (the extremes of bfloat16
 // values are bfloat16), two rows or both extremes of one row per shuffle.
-template <bool kZeros, bool kVec>
-__device__ __forceinline__ void extremes(const Eight<bf16_t, kVec> (&x)[4], int lanes, float& hi, float& lo) {
+template <bool kZeros, int kLanes, bool kVec>
+__device__ __forceinline__ void extremes(const Eight<bf16_t, kVec> (&x)[4], float& hi, float& lo) {
   const int lane = threadIdx.x & 31;
   const auto both = [](uint32_t a, uint32_t b, uint32_t c, uint32_t d) {  // the maximum of eight, in both halves
     const uint32_t m = bmax2_nan(bmax2_nan(a, b), bmax2_nan(c, d));
@@ -157,8 +158,9 @@ __device__ __forceinline__ void extremes(const Eight<bf16_t, kVec> (&x)[4], int 
     }
   }
 #pragma unroll
-  for (int i = 0; i < kRegs; ++i)
-    for (int o = lanes >> 1; o > 0; o >>= 1) m[i] = bmax2_nan(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
+  for (int o = kLanes >> 1; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < kRegs; ++i) m[i] = bmax2_nan(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
   if constexpr (kZeros) {
     const uint32_t mine = (lane & 2) ? ((lane & 1) ? m[3] : m[2]) : ((lane & 1) ? m[1] : m[0]);
     hi = fmax_nan(0.f, bf16_lo(mine));
@@ -174,7 +176,7 @@ constexpr float kGrid = 6144.f;            // float32 neighbours 2^-11 apart
 constexpr float kWhole = 12582912.f;       // 1.5 * 2^23: neighbours 1 apart
 constexpr float kTiny = 7.5231638e-37f;    // 2^-120
 
-template <typename T, bool kVec, bool kZeros>
+template <typename T, int kGroup, bool kVec, bool kZeros>
 __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantParams P) {
   __shared__ unsigned short s_scale[kQuantGroups][kQuantRows];
   __shared__ unsigned char s_zero[kQuantGroups][kQuantRows];
@@ -182,18 +184,20 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantPara
   const int v0 = static_cast<int>(blockIdx.x) * kQuantRows;
   const int k0 = static_cast<int>(blockIdx.y) * kQuantCols;
   const int k = k0 + lane * 8;
+  constexpr int kLanes = kGroup / 8;  // of a group
   constexpr int kPer = kQuantRows / (kQuantThreads / 32);
   static_assert(kPer == 4, "a group has at least 4 lanes: one for each row");
   Eight<T, kVec> x[kPer];
+  const int row0 = v0 + warp * kPer;
+  const int rows = k < P.d ? P.V - row0 : 0;  // this lane's (4 or more: all of the warp's)
+  const T* src = static_cast<const T*>(P.weights) + static_cast<long long>(row0) * P.ld + k;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int v = v0 + warp * kPer + i;
-    if (v < P.V && k < P.d) x[i].load(static_cast<const T*>(P.weights) + static_cast<long long>(v) * P.ld + k);
+    if (i < rows) x[i].load(src + i * P.ld);
     else x[i].clear();
   }
-  const int lanes = P.group >> 3;  // lanes of a group
   float hi = 0.f, lo = 0.f;        // the group's in row lane % 4
-  extremes<kZeros>(x, lanes, hi, lo);
+  extremes<kZeros, kLanes>(x, hi, lo);
   // row lane % 4: the scale, its reciprocal and the zero point
   unsigned short sb = to_bf16(kZeros ? __fdiv_rn(__fadd_rn(hi, lo), 15.f) : __fdiv_rn(hi, 7.f));
   float s = __uint_as_float(static_cast<uint32_t>(sb) << 16);
@@ -204,13 +208,13 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantPara
   const float r = s >= kTiny ? __frcp_rn(s) : 0.f;
   float z = 8.f;
   if constexpr (kZeros) z = s > 0.f ? fminf(rintf(__fdiv_rn(lo, s)), 15.f) : 0.f;
-  if ((lane & (lanes - 1)) < kPer) {
-    s_scale[lane / lanes][warp * kPer + (lane & 3)] = sb;
-    if constexpr (kZeros) s_zero[lane / lanes][warp * kPer + (lane & 3)] = static_cast<unsigned char>(z);
+  if ((lane & (kLanes - 1)) < kPer) {
+    s_scale[lane / kLanes][warp * kPer + (lane & 3)] = sb;
+    if constexpr (kZeros) s_zero[lane / kLanes][warp * kPer + (lane & 3)] = static_cast<unsigned char>(z);
   }
+  unsigned char* dst = P.codes + static_cast<long long>(row0) * P.codes_ld + (k >> 1);
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int v = v0 + warp * kPer + i;
     const int from = (lane & ~3) | i;
     const float ri = __shfl_sync(0xffffffffu, r, from);
     const float zi = kZeros ? __shfl_sync(0xffffffffu, z, from) : 8.f;
@@ -243,36 +247,43 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantPara
       const float p = __fmaf_rn(__fmaf_rn(__fmaf_rn(x[3], 16.f, x[2]), 16.f, x[1]), 16.f, x[0]);
       return __float_as_uint(__fadd_rn(p, 8388608.f));  // 2^23: the low bits are the integer
     };
-    if (v < P.V && k < P.d)
-      *reinterpret_cast<uint32_t*>(P.codes + static_cast<long long>(v) * P.codes_ld + (k >> 1)) =
-          __byte_perm(four(c), four(c + 4), 0x5410);
+    if (i < rows) *reinterpret_cast<uint32_t*>(dst + i * P.codes_ld) = __byte_perm(four(c), four(c + 4), 0x5410);
   }
   __syncthreads();
-  const int groups = kQuantCols / P.group;
+  constexpr int groups = kQuantCols / kGroup;
   for (int i = tid; i < groups * kQuantRows; i += kQuantThreads) {
     const int g = i / kQuantRows, q = i % kQuantRows;
     const int v = v0 + q;
-    if (v < P.V && k0 + g * P.group < P.d) {
-      const long long row = k0 / P.group + g;
+    if (v < P.V && k0 + g * kGroup < P.d) {
+      const long long row = k0 / kGroup + g;
       P.scales[row * P.scales_ld + v] = s_scale[g][q];
       if constexpr (kZeros) P.zeros[row * P.zeros_ld + v] = s_zero[g][q];
     }
   }
 }
 
-template <typename T>
+template <typename T, int kGroup>
 cudaError_t launch_quantize(const QuantParams& p, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>((p.V + kQuantRows - 1) / kQuantRows),
                   static_cast<unsigned>((p.d + kQuantCols - 1) / kQuantCols));
   const bool vec = aligned(p.weights, 16) && (p.ld * static_cast<long long>(sizeof(T))) % 16 == 0;
   if (vec) {
-    if (p.zeros) quantize_kernel<T, true, true><<<grid, kQuantThreads, 0, s>>>(p);
-    else quantize_kernel<T, true, false><<<grid, kQuantThreads, 0, s>>>(p);
+    if (p.zeros) quantize_kernel<T, kGroup, true, true><<<grid, kQuantThreads, 0, s>>>(p);
+    else quantize_kernel<T, kGroup, true, false><<<grid, kQuantThreads, 0, s>>>(p);
   } else {
-    if (p.zeros) quantize_kernel<T, false, true><<<grid, kQuantThreads, 0, s>>>(p);
-    else quantize_kernel<T, false, false><<<grid, kQuantThreads, 0, s>>>(p);
+    if (p.zeros) quantize_kernel<T, kGroup, false, true><<<grid, kQuantThreads, 0, s>>>(p);
+    else quantize_kernel<T, kGroup, false, false><<<grid, kQuantThreads, 0, s>>>(p);
   }
   return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_quantize(const QuantParams& p, cudaStream_t s) {
+  switch (p.group) {
+    case 32: return launch_quantize<T, 32>(p, s);
+    case 64: return launch_quantize<T, 64>(p, s);
+    default: return launch_quantize<T, 128>(p, s);
+  }
 }
 
 bool good_shape(int V, int d, int group) {
