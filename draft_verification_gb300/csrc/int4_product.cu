@@ -102,8 +102,8 @@ struct Shape {
   // launch holds
   static constexpr int kRegsLaunch = 65536 / kThreads / 8 * 8;
   static constexpr int kRegsCopy = 40;
-  static constexpr int kRegsUnpack = kThreads == 896 ? 64 : 72;
-  static constexpr int kRegsEpi = N == 128 ? 112 : N == 64 ? 104 : 152;
+  static constexpr int kRegsUnpack = N <= 32 ? 72 : 64;
+  static constexpr int kRegsEpi = N == 128 ? 120 : N == 64 ? 104 : 152;
   static_assert(128 * (kRegsCopy + kUnpackGroups * kRegsUnpack + kEpiGroups * kRegsEpi) <= kThreads * kRegsLaunch,
                 "no more registers than the launch holds");
   // scales and zero points of a weight stage: one row of a tile per group
@@ -254,6 +254,37 @@ struct Cursor {
   }
 };
 
+// The same list as runs of units of one tile.
+struct Runs {
+  Place at;  // the run's first unit
+  int run;   // its units
+  int todo, u0;
+  bool begun = false;
+  __device__ __forceinline__ Runs(int start, int u0_, int u1, const I4Params& P) : run(0), todo(u1 - u0_), u0(u0_) {
+    at.set(start, P);
+    run = min(P.nk - at.k, u1 - start);
+  }
+  // on to the next run (at first: to the first); false at the end
+  __device__ __forceinline__ bool next(const I4Params& P) {
+    if (begun) {
+      todo -= run;
+      at.k += run;
+      if (at.k < P.nk) {
+        at.set(u0, P);  // the tail was left: on to the head
+      } else {
+        at.k = 0;
+        if (++at.vt == P.ntv) {
+          at.vt = 0;
+          ++at.rb;
+        }
+      }
+      run = min(P.nk - at.k, todo);
+    }
+    begun = true;
+    return todo > 0;
+  }
+};
+
 // The tile of a unit, its units' CTAs and its first unit.
 struct SharedTile {
   int u0, first, last;
@@ -276,6 +307,11 @@ __device__ __forceinline__ unsigned blocks_of(const void* src, int bytes) {
 __device__ __forceinline__ void load_blocks(void* dst, const void* src, int bytes, uint64_t* bar) {
   bulk_load(dst, reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(src) & ~static_cast<uintptr_t>(15)),
             blocks_of(src, bytes), bar);
+}
+
+// Announce more bytes of bulk copies on a barrier, without an arrival.
+__device__ __forceinline__ void mbar_expect_more(uint64_t* bar, unsigned bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
 }
 
 // One lane of the warp, the same at every call.
@@ -352,33 +388,41 @@ __global__ void __launch_bounds__(Shape<N, G>::kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsCopy));
     if (warp == 0) {
       // ---------------- weight stages ----------------
+      // (what a warp does here per unit is on every unit's path: addresses are
+      // carried along, and each lane announces its own bytes)
       if (leader) tma_prefetch_desc(&tm_w);
-      Cursor c(start, u0, u1, P);
       Ring<S::kWStages> w;
-      for (int it = 0; it < units; ++it, c.next(P), w.next()) {
-        if (!i4_wait(&wempty[w.slot], w.parity ^ 1u, fault)) break;
-        const int v0 = c.at.vt * kTileV, n = min(kTileV, P.V - v0), g0 = c.at.k * S::kPer;
-        const int groups = min(S::kPer, P.d / G - g0);
-        // lane i < kPer: the scales of group i of the stage; lane 16 + i: its zero points
-        const int g = lane & 15;
-        const bool zeros = lane >= 16;
-        const bool mine = g < groups && (!zeros || P.zeros);
-        const char* src = zeros ? reinterpret_cast<const char*>(P.zeros) + (g0 + g) * P.zeros_ld + v0
-                                : reinterpret_cast<const char*>(P.scales + (g0 + g) * P.scales_ld + v0);
-        const int len = zeros ? n : 2 * n;
-        const unsigned bytes = __reduce_add_sync(0xffffffffu, mine ? blocks_of(src, len) : 0u);
-        if (leader) {
-          mbar_expect_tx(&wfull[w.slot], kStageBytes + bytes);
-          tma_load_2d(wring + w.slot * kStageBytes, &tm_w, c.at.k * (kStageK / 2), v0, &wfull[w.slot]);
-          w_issued_s = it + 1;
+      // lane i < kPer: the scales of group i of the stage; lane 16 + i: its zero points
+      const int g = lane & 15;
+      const bool zeros = lane >= 16;
+      const bool serves = g < S::kPer && (!zeros || P.zeros);
+      const long long step = S::kPer * (zeros ? P.zeros_ld : 2 * P.scales_ld);  // bytes from unit to unit
+      unsigned char* side = sring + (zeros ? S::kPer * kScalePitch + g * kZeroPitch : g * kScalePitch);
+      int issued = 0;
+      bool ok = true;
+      for (Runs runs(start, u0, u1, P); ok && runs.next(P);) {
+        const int v0 = runs.at.vt * kTileV, len = min(kTileV, P.V - v0) * (zeros ? 1 : 2);
+        int left = P.d / G - runs.at.k * S::kPer;  // groups from the unit's first on
+        const long long first = static_cast<long long>(runs.at.k * S::kPer + g);
+        const char* src = zeros ? reinterpret_cast<const char*>(P.zeros) + first * P.zeros_ld + v0
+                                : reinterpret_cast<const char*>(P.scales + first * P.scales_ld + v0);
+        for (int x = runs.at.k * (kStageK / 2), n = runs.run; n > 0; --n, x += kStageK / 2, src += step, left -= S::kPer) {
+          ok = i4_wait(&wempty[w.slot], w.parity ^ 1u, fault);
+          if (!ok) break;
+          if (serves && g < left) {
+            mbar_expect_more(&wfull[w.slot], blocks_of(src, len));
+            load_blocks(side + w.slot * S::kSideBytes, src, len, &wfull[w.slot]);
+          }
+          __syncwarp();  // the stage expects all its bytes before its one arrival
+          if (leader) {
+            mbar_expect_tx(&wfull[w.slot], kStageBytes);
+            tma_load_2d(wring + w.slot * kStageBytes, &tm_w, x, v0, &wfull[w.slot]);
+          }
+          w.next();
+          ++issued;
         }
-        __syncwarp();  // the stage expects its bytes before any of them arrives
-        unsigned char* side = sring + w.slot * S::kSideBytes;
-        if (mine)
-          load_blocks(zeros ? side + S::kPer * kScalePitch + g * kZeroPitch : side + g * kScalePitch, src, len,
-                      &wfull[w.slot]);
-        __syncwarp();
       }
+      if (leader) w_issued_s = issued;
     } else if (warp == 1) {
       // ---------------- MMAs ----------------
       // The whole warp keeps the loop's values, so that they stay in uniform
@@ -425,20 +469,26 @@ __global__ void __launch_bounds__(Shape<N, G>::kThreads, 1)
     } else if (warp == 2) {
       // ---------------- the rows' columns ----------------
       if (leader) tma_prefetch_desc(&tm_x);
-      Cursor c(start, u0, u1, P);
       Ring<S::kXStages> x;
-      for (int it = 0; it < units; ++it, c.next(P), x.next()) {
-        if (!i4_wait(&xempty[x.slot], x.parity ^ 1u, fault)) break;
-        if (leader) {
-          unsigned char* st = xring + x.slot * S::kXBytes;
-          mbar_expect_tx(&xfull[x.slot], S::kXBytes);
+      int issued = 0;
+      bool ok = true;
+      for (Runs runs(start, u0, u1, P); ok && runs.next(P);) {
+        for (int k = runs.at.k * kStageK, n = runs.run; n > 0; --n, k += kStageK) {
+          ok = i4_wait(&xempty[x.slot], x.parity ^ 1u, fault);
+          if (!ok) break;
+          if (leader) {
+            unsigned char* st = xring + x.slot * S::kXBytes;
+            mbar_expect_tx(&xfull[x.slot], S::kXBytes);
 #pragma unroll
-          for (int i = 0; i < kStageK / 64; ++i)
-            tma_load_2d(st + i * N * 128, &tm_x, c.at.k * kStageK + i * 64, c.at.rb * N, &xfull[x.slot]);
-          x_issued_s = it + 1;
+            for (int i = 0; i < kStageK / 64; ++i)
+              tma_load_2d(st + i * N * 128, &tm_x, k + i * 64, runs.at.rb * N, &xfull[x.slot]);
+          }
+          __syncwarp();
+          x.next();
+          ++issued;
         }
-        __syncwarp();
       }
+      if (leader) x_issued_s = issued;
     } else if (warp == 3) {
       // ---------------- shared tiles ----------------
       // In the order in which the epilogue leaves them: the tile of unit
@@ -576,18 +626,15 @@ __global__ void __launch_bounds__(Shape<N, G>::kThreads, 1)
     Ring<S::kSlots> a;
     int db = 0;
     int shared = 0;  // shared tiles so far
-    // a run of units of one tile at a time
-    Place c;
-    c.set(start, P);
-    int todo = units, run = min(P.nk - c.k, u1 - start), begin = c.k;
     bool ok = true;
-    while (todo > 0) {
+    for (Runs runs(start, u0, u1, P); ok && runs.next(P);) {
+      const Place& c = runs.at;
       // low bits of addresses: where a row of scales starts in its first block
       const uint32_t step = static_cast<uint32_t>(P.scales_ld) * 2u;
       uint32_t lead = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(P.scales)) +
                       static_cast<uint32_t>(c.vt * kTileV) * 2u + static_cast<uint32_t>(c.k * S::kPer) * step;
       int width = P.d - c.k * kStageK;  // columns from the unit's first on
-      for (int it = 0; it < run; ++it, width -= kStageK) {
+      for (int it = 0; it < runs.run; ++it, width -= kStageK) {
         ok = i4_wait(&wfull[w.slot], w.parity, fault);
         if (!ok) break;
         uint32_t s_now[S::kPer];  // the scales of the unit's groups
@@ -633,13 +680,11 @@ __global__ void __launch_bounds__(Shape<N, G>::kThreads, 1)
         if (!ok) break;
       }
       if (!ok) break;
-      todo -= run;
-      c.k += run;
-      if (begin == 0 && c.k == P.nk) {
+      if (runs.run == P.nk) {
         store(c, acc);
       } else {
         // a shared tile: leave the sums in this CTA's slot
-        float* mine = P.partials + (static_cast<long long>(2 * cta + (begin == 0 ? 1 : 0)) * N + col0) * kTileV + row;
+        float* mine = P.partials + (static_cast<long long>(2 * cta + (c.k == 0 ? 1 : 0)) * N + col0) * kTileV + row;
 #pragma unroll
         for (int i = 0; i < S::kCols / 2; ++i) {
           __stcg(mine + (2 * i) * kTileV, acc[i].x);
@@ -651,17 +696,6 @@ __global__ void __launch_bounds__(Shape<N, G>::kThreads, 1)
       }
 #pragma unroll
       for (int i = 0; i < S::kCols / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-      if (c.k < P.nk) {
-        c.set(u0, P);  // the tail was left: on to the head
-      } else {
-        c.k = 0;
-        if (++c.vt == P.ntv) {
-          c.vt = 0;
-          ++c.rb;
-        }
-      }
-      run = min(P.nk - c.k, todo);
-      begin = c.k;
     }
     // the shared tiles whose last part this CTA was: all parts, in the order of the columns
     for (int i = 0; i < shared && ok; ++i) {
@@ -669,6 +703,7 @@ __global__ void __launch_bounds__(Shape<N, G>::kThreads, 1)
       if (!ok || !won_s[i]) continue;
       SharedTile t;
       t.find(tail && i == 0 ? start : u0, ctas, P);
+      Place c;
       c.set(t.u0, P);
       for (int o = t.first; o <= t.last; ++o) {
         const float* src =
