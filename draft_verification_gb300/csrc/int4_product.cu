@@ -75,8 +75,8 @@ struct I4Params {
 // N rows and groups of G columns.
 template <int N, int G>
 struct Shape {
-  static constexpr int kEpiGroups = N >= 64 ? 2 : 1;     // warpgroups
-  static constexpr int kUnpackGroups = N == 128 ? 3 : 4;
+  static constexpr int kEpiGroups = N == 128 ? 4 : N == 64 ? 2 : 1;  // warpgroups
+  static constexpr int kUnpackGroups = N == 128 ? 2 : 4;
   static constexpr int kThreads = 128 * (1 + kUnpackGroups + kEpiGroups);
   static constexpr int kCols = N / kEpiGroups;           // rows of x per epilogue thread
   // a chunk (what is handed from unpacking to MMA to epilogue at once): the
@@ -102,8 +102,8 @@ struct Shape {
   // launch holds
   static constexpr int kRegsLaunch = 65536 / kThreads / 8 * 8;
   static constexpr int kRegsCopy = 40;
-  static constexpr int kRegsUnpack = N <= 32 ? 72 : 64;
-  static constexpr int kRegsEpi = N == 128 ? 120 : N == 64 ? 104 : 152;
+  static constexpr int kRegsUnpack = N == 64 ? 64 : 72;
+  static constexpr int kRegsEpi = N == 128 ? 80 : N == 64 ? 104 : 152;
   static_assert(128 * (kRegsCopy + kUnpackGroups * kRegsUnpack + kEpiGroups * kRegsEpi) <= kThreads * kRegsLaunch,
                 "no more registers than the launch holds");
   // scales and zero points of a weight stage: one row of a tile per group
