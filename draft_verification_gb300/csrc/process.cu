@@ -377,7 +377,8 @@ __global__ void __launch_bounds__(kCollectThreads) collect_kernel(const ProcessP
       before[i] = run;
       // where the slab that begins here starts, and the marked tokens themselves
       const int t0 = first + i * 32;
-      if (t0 % P.slab_tokens == 0) offsets[t0 / P.slab_tokens] = base + static_cast<int>(run);
+      if (t0 < P.V && t0 % P.slab_tokens == 0)
+        offsets[t0 / P.slab_tokens] = base + static_cast<int>(run);
       for (; m; m &= m - 1) P.entry_token[out + base + run++] = t0 + __ffs(m) - 1;
     }
 

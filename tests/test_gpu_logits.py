@@ -155,6 +155,34 @@ def test_process(cuda_device, B, n, V, pad, dtype, kw):
     assert np.array_equal(bits(x), first)
 
 
+@pytest.mark.parametrize("B,n,V,pad,dtype,kw", [
+    # more tokens than one bitmap holds
+    (3, 3, 300001, 0, "bf16", dict(H=500, bias=40, density=0.5)),
+    (3, 2, 300001, 3, "f32", dict(H=501, bias=3)),
+    # exactly one bitmap, and one token more
+    (6, 2, 262144, 0, "bf16", dict(H=300, tree=True)),
+    (6, 2, 262145, 7, "bf16", dict(H=300)),
+    # more distinct tokens than one window holds
+    (40, 2, 66000, 0, "bf16", dict(H=40000, bias=500)),
+    (24, 2, 66001, 0, "f32", dict(H=40001, bias=9)),
+    # more entries in a slab than are kept in shared memory, from one slab and from two
+    (60, 2, 20000, 0, "bf16", dict(H=40000, bias=10, density=0.8)),
+    (60, 2, 20001, 0, "bf16", dict(H=40002, bias=10)),
+    # a wide tree
+    (2, 257, 33000, 8, "bf16", dict(H=64, tree=True)),
+], ids=lambda v: str(v) if not isinstance(v, dict) else None)
+def test_process_large(cuda_device, B, n, V, pad, dtype, kw):
+    rng = np.random.default_rng(B * 7919 + n * 104729 + V)
+    w = make_process(rng, B, n, V, **kw)
+    w["history_len"][::2] = kw["H"]
+    x = strided(B, n, V, pad, DTYPES[dtype], cuda_device)
+    x.copy_(torch.from_numpy(rng.normal(0, 3, (B, n, V)).astype(np.float32)))
+    out = run_process(x, w, cuda_device)
+    check_process(x, out, w)
+    first = bits(out["logits"]).copy()
+    assert np.array_equal(bits(run_process(x, w, cuda_device, out=x)["logits"]), first)
+
+
 def test_process_special_values(cuda_device):
     """Infinities and NaN in masked, penalised and untouched places; a mask
     row of nothing; biases of -inf and of the type's lowest value."""
@@ -192,9 +220,10 @@ def test_process_a_deep_and_a_wide_tree(cuda_device):
         check_process(x, run_process(x, w, cuda_device), w)
 
 
-def test_process_data_errors(cuda_device):
+@pytest.mark.parametrize("V", [900, 70000])  # one kernel, and two
+def test_process_data_errors(cuda_device, V):
     rng = np.random.default_rng(6)
-    B, n, V = 9, 4, 900
+    B, n = 9, 4
     for tree in (False, True):
         w = make_process(rng, B, n, V, H=30, tree=tree, density=0.5)
         w["history_len"][:] = 30
