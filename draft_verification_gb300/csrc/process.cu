@@ -13,16 +13,25 @@
 //
 // What applies to a token is an entry: a 32-bit word (low bits: occurrences
 // that count; bit 31: occurs in the prompt; bit 30: drafted, its occurrences on
-// the way to a row are counted for each row; bit 29: has a bias) and the sum of its bias entries.
-//  - Small calls (latency) build the slab's entries in the same kernel, as a
-//    table of the slab in shared memory, from the whole history, which is read
-//    while the first row's vectors are in flight.
-//  - Large calls would read each history once per slab and hold 10 bytes of
-//    table per token, too much for enough CTAs to overlap their phases.
-//    collect_kernel gathers each sequence's distinct tokens once and writes
-//    their entries in ascending order to the workspace; the slabs' CTAs
-//    (launched dependent: their first vectors are in flight meanwhile) read a
-//    few hundred entries each.
+// the way to a row are counted for each row; bit 29: has a bias) and the sum of
+// its bias entries.
+//  - Most calls build a slab's entries in the same kernel, as a table of the
+//    slab in shared memory, from the whole history, which is read while the
+//    first row's vectors are in flight.
+//  - Where the slabs would read too much history between them (long histories
+//    of many sequences over a large vocabulary), collect_kernel gathers each
+//    sequence's distinct tokens once and writes their entries in ascending
+//    order to the workspace; the slabs' CTAs (launched dependent: their first
+//    vectors are in flight meanwhile) read a few hundred entries each.
+// run_process has the rule and what it measured.
+//
+// What bounds it: HBM, which has to read every element with an allowed token
+// and write every element.  128 sequences of 9 rows of 128256 bfloat16 logits
+// with grammar masks and histories of up to 8192 tokens (613 MB): 161 us, of
+// which the masked copy alone takes 108, the collecting that is not hidden 20
+// and the rewriting 33; a copy of that size takes 90.5 at the measured 6.8 TB/s,
+// and writing it alone 76.  16 trees of 64 nodes over 50257 tokens (212 MB):
+// 54 us against 31.  One row: 7 us, the launch.
 //
 // Vectors are aligned in memory: a row that starts at element m of its vector
 // has tokens [k e - m, k e - m + e) in vector k, so a row's part is the slab
@@ -197,12 +206,14 @@ __device__ __forceinline__ void draft_of(const ProcessParams& P, int b, int i, i
   }
 }
 
-// take(token, place) for the history's tokens, four at a time where rows allow
-// 16-byte loads, the next four loading meanwhile.  One copy of `take`: a CTA
-// runs it a few times, and straight-line copies of it would each wait for
-// their instructions longer than they take to run.
+// take(token, place) for the history's tokens within [first, first + count),
+// four at a time where rows allow 16-byte loads, the next four loading
+// meanwhile.  Most tokens are of other slabs: four are sifted by a subtraction
+// and a comparison each, and only the rest take a branch.  bad: also look for
+// tokens outside the vocabulary.
 template <int kThreads, typename F>
-__device__ __forceinline__ void for_history(const ProcessParams& P, int b, int len, F&& take) {
+__device__ __forceinline__ void for_history(const ProcessParams& P, int b, int len, int first, int count, bool* bad,
+                                            F&& take) {
   const int* h = P.history + static_cast<long long>(b) * P.history_ld;
   const bool wide = P.history_ld % 4 == 0 && !misaligned16(P.history);
   const int width = wide ? 4 : 1;
@@ -214,16 +225,19 @@ __device__ __forceinline__ void for_history(const ProcessParams& P, int b, int l
     }
     return t;
   };
+  const auto within = [](const int4& t, int from, int n) {
+    const auto in = [&](int v) { return static_cast<unsigned>(v - from) < static_cast<unsigned>(n); };
+    return (in(t.x) ? 1u : 0u) | (in(t.y) ? 2u : 0u) | (in(t.z) ? 4u : 0u) | (in(t.w) ? 8u : 0u);
+  };
   int4 next = load(width * static_cast<int>(threadIdx.x));
   for (int at = width * static_cast<int>(threadIdx.x); at < len; at += width * kThreads) {
-    int4 t = next;
+    const int4 t = next;
     next = load(at + width * kThreads);
-#pragma unroll 1
-    for (int k = 0; k < width && at + k < len; ++k) {
-      take(t.x, at + k);
-      t.x = t.y;
-      t.y = t.z;
-      t.z = t.w;
+    const unsigned there = (1u << min(width, len - at)) - 1u;
+    if (bad && (there & ~within(t, 0, P.V))) *bad = true;
+    for (unsigned todo = there & within(t, first, count); todo; todo &= todo - 1) {
+      const int k = __ffs(todo) - 1;
+      take(k < 2 ? (k == 0 ? t.x : t.y) : (k == 2 ? t.z : t.w), at + k);
     }
   }
 }
@@ -321,6 +335,7 @@ __global__ void __launch_bounds__(kCollectThreads) collect_kernel(const ProcessP
   int* offsets = P.offsets + static_cast<long long>(b) * (P.slabs + 1);
   int base = 0;  // entries of the ranges before
   for (int first = 0; first < P.V; first += words * 32) {
+    const int count_in = min(words * 32, P.V - first);  // the range's tokens
     // the word of a token in this range, or a negative number
     const auto word_of = [&](int t) {
       const int w = (t - first) >> 5;
@@ -338,10 +353,10 @@ __global__ void __launch_bounds__(kCollectThreads) collect_kernel(const ProcessP
       draft_of(P, b, i, t, p, err);
       if (t >= 0) mark(t);
     }
-    for_history<kCollectThreads>(P, b, len.history, [&](int t, int) {
-      if (t < 0 || t >= P.V) err |= SPEC_ERR_TOKEN;
-      else mark(t);
-    });
+    bool bad = false;
+    for_history<kCollectThreads>(P, b, len.history, first, count_in, first == 0 ? &bad : nullptr,
+                                 [&](int t, int) { mark(t); });
+    if (bad) err |= SPEC_ERR_TOKEN;
     for (int e = tid; e < len.bias; e += kCollectThreads) {
       const int t = __ldg(P.bias_tokens + static_cast<long long>(b) * P.bias_ld + e);
       if (t < 0 || t >= P.V) err |= SPEC_ERR_TOKEN;
@@ -400,8 +415,8 @@ __global__ void __launch_bounds__(kCollectThreads) collect_kernel(const ProcessP
         const int at = t >= 0 ? place(t) : -1;
         if (at >= 0) atomicOr(&count[at], kDrafted);
       }
-      for_history<kCollectThreads>(P, b, len.history, [&](int t, int i) {
-        const int at = t >= 0 && t < P.V ? place(t) : -1;
+      for_history<kCollectThreads>(P, b, len.history, first, count_in, nullptr, [&](int t, int i) {
+        const int at = place(t);
         if (at < 0) return;
         if (i < len.prompt) atomicOr(&count[at], kInPrompt);
         else atomicAdd(&count[at], 1u);
@@ -598,23 +613,22 @@ __global__ void __launch_bounds__(kThreads, (kListed ? 1536 : 1024) / kThreads) 
     __syncthreads();
   } else {
     const Lengths len = lengths_of(P, b, err);
-    for_history<kThreads>(P, b, len.history, [&](int t, int at) {
-      if (t < 0 || t >= P.V) {
-        err |= SPEC_ERR_TOKEN;
-        return;
-      }
-      const int o = place_of(t);
-      if (o < 0) return;
-      if (at < len.prompt) atomicOr(&count[o], kInPrompt);
-      else atomicAdd(&count[o], 1u);
-      touch(o);
-    });
+    const bool checks = blockIdx.x == 0 && blockIdx.y == 0;
+    const int t0 = max(lo, 0);
+    bool bad = false;
+    for_history<kThreads>(P, b, len.history, t0, min(lo + S::kTable, P.V) - t0, checks ? &bad : nullptr,
+                          [&](int t, int at) {
+                            const int o = t - lo;
+                            if (at < len.prompt) atomicOr(&count[o], kInPrompt);
+                            else atomicAdd(&count[o], 1u);
+                            touch(o);
+                          });
+    if (bad) err |= SPEC_ERR_TOKEN;
     add_biases<kThreads>(P, b, len.bias, count, bias, &s_again, err, [&](int t) {
       const int at = place_of(t);
       if (at >= 0) touch(at);
       return at;
     });
-    const bool checks = blockIdx.x == 0 && blockIdx.y == 0;
     if (checks && err) atomicOr(&s_err, err);
     __syncthreads();
     if (checks && tid == 0) {
@@ -766,6 +780,16 @@ int slabs_of(int V, long long ld) {
   return (nvec + kThreads * kVecs - 1) / (kThreads * kVecs);
 }
 
+// Rows that a CTA takes: few sequences and slabs have a sequence's rows split
+// as well, into one round of CTAs.
+template <typename T, int kThreads, int kVecs, bool kListed>
+int rows_of(const ProcessParams& p, int nsm) {
+  const long long have = static_cast<long long>(slabs_of<T, kThreads, kVecs>(p.V, p.ld)) * p.B;
+  const long long fill = (kListed ? 1536LL : 1024LL) / kThreads * nsm;
+  const long long parts = std::min<long long>(p.n, std::max<long long>(1, fill / have));
+  return static_cast<int>((p.n + parts - 1) / parts);
+}
+
 template <typename T, int kThreads, int kVecs, bool kListed>
 cudaError_t launch_process(ProcessParams p, int nsm, cudaStream_t s) {
   using S = Slab<T, kThreads, kVecs, kListed>;
@@ -775,11 +799,7 @@ cudaError_t launch_process(ProcessParams p, int nsm, cudaStream_t s) {
   cudaError_t e = raise_smem(kernel, dyn, done);
   if (e != cudaSuccess) return e;
   const int slabs = slabs_of<T, kThreads, kVecs>(p.V, p.ld);
-  // few sequences and slabs: a sequence's rows are split as well
-  const long long have = static_cast<long long>(slabs) * p.B;
-  const long long fill = (kListed ? 1536LL : 1024LL) / kThreads * nsm;
-  const long long parts = std::min<long long>(p.n, std::max<long long>(1, fill / have));  // one round of CTAs
-  p.rows_per_cta = static_cast<int>((p.n + parts - 1) / parts);
+  p.rows_per_cta = rows_of<T, kThreads, kVecs, kListed>(p, nsm);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(slabs), static_cast<unsigned>((p.n + p.rows_per_cta - 1) / p.rows_per_cta),
                      static_cast<unsigned>(p.B));
@@ -824,10 +844,24 @@ cudaError_t launch_collect(ProcessParams p, cudaStream_t s) {
 template <typename T>
 cudaError_t run_process(ProcessParams p, int nsm, cudaStream_t s) {
   using Large = Slab<T, 512, 2, true>;
-  // One kernel where its CTAs come to a few rounds at most; beyond, the second
-  // launch costs less than the histories read per slab.
-  const long long ctas = static_cast<long long>(slabs_of<T, 512, 2>(p.V, p.ld)) * p.B;
-  if (ctas * p.n < 2LL * nsm) return launch_process<T, 256, 1, false>(p, nsm, s);
+  // One kernel or two: the one kernel's slabs each read the whole history, which
+  // costs about a microsecond per million tokens read; the second launch and the
+  // entries' way through the workspace cost 10 to 15.  Measured (bfloat16, 128
+  // sequences of 9 rows, V = 128256; one kernel, two): histories of 500 tokens,
+  // 4M read, 111 and 120 us; 4000, 32M, 132 and 126; 8192, 66M, 212 and 163.
+  // With 32 sequences of 4000, 8M read: 37 and 49.
+  const int reads = (p.history ? p.history_ld : 0) + (p.bias_tokens ? p.bias_ld : 0);
+  const long long slabs = slabs_of<T, 128, 2>(p.V, p.ld);
+  if (slabs * p.B * reads <= (1LL << 24)) {
+    // Narrow CTAs stream better (more of them overlap their phases), wide ones
+    // get through a history sooner.  Where a row's part comes to less than 1/512
+    // of the reading, the history decides.  Measured (256 and 128 threads;
+    // V = 32000, 9 rows): 32 sequences of 200 tokens 12.2 and 9.8 us, 128 of
+    // them 40 and 33; 1 sequence with 1 row and 2000 tokens 4.0 and 5.2, 8
+    // with 4 rows 5.8 and 6.0.
+    if (reads > 512LL * rows_of<T, 128, 2, false>(p, nsm)) return launch_process<T, 256, 1, false>(p, nsm, s);
+    return launch_process<T, 128, 2, false>(p, nsm, s);
+  }
   p.slab_tokens = Large::kTokens;
   p.slabs = slabs_of<T, 512, 2>(p.V, p.ld);
   const cudaError_t e = launch_collect(p, s);

@@ -170,6 +170,12 @@ def test_process(cuda_device, B, n, V, pad, dtype, kw):
     (60, 2, 20001, 0, "bf16", dict(H=40002, bias=10)),
     # a wide tree
     (2, 257, 33000, 8, "bf16", dict(H=64, tree=True)),
+    # the same sizes with histories long enough to be gathered first
+    (3, 3, 300001, 0, "bf16", dict(H=60000, bias=40, density=0.5)),
+    (3, 2, 300001, 3, "f32", dict(H=30001, bias=3)),
+    (6, 2, 262144, 0, "bf16", dict(H=30000, tree=True)),
+    (6, 2, 262145, 7, "bf16", dict(H=30000, density=0.3)),
+    (40, 5, 66000, 3, "bf16", dict(H=14000, tree=True, bias=0)),
 ], ids=lambda v: str(v) if not isinstance(v, dict) else None)
 def test_process_large(cuda_device, B, n, V, pad, dtype, kw):
     rng = np.random.default_rng(B * 7919 + n * 104729 + V)
@@ -220,16 +226,16 @@ def test_process_a_deep_and_a_wide_tree(cuda_device):
         check_process(x, run_process(x, w, cuda_device), w)
 
 
-@pytest.mark.parametrize("V", [900, 70000])  # one kernel, and two
-def test_process_data_errors(cuda_device, V):
+@pytest.mark.parametrize("V,H", [(900, 30), (70000, 30), (300000, 30000)])  # the last: gathered first
+def test_process_data_errors(cuda_device, V, H):
     rng = np.random.default_rng(6)
     B, n = 9, 4
     for tree in (False, True):
-        w = make_process(rng, B, n, V, H=30, tree=tree, density=0.5)
-        w["history_len"][:] = 30
+        w = make_process(rng, B, n, V, H=H, tree=tree, density=0.5)
+        w["history_len"][:] = H
         w["bias_len"][:] = 5
         w["history"][0, 3], w["history"][1, 29] = -1, V
-        w["history_len"][2], w["history_len"][3] = 31, -2
+        w["history_len"][2], w["history_len"][3] = H + 1, -2
         w["tokens"][4, 1] = V + 5
         w["bias_tokens"][5, 2] = -7
         w["bias_len"][6] = 6
