@@ -79,6 +79,12 @@ struct Shape {
   static constexpr int kUnpackGroups = N == 128 ? 2 : 4;
   static constexpr int kThreads = 128 * (1 + kUnpackGroups + kEpiGroups);
   static constexpr int kCols = N / kEpiGroups;           // rows of x per epilogue thread
+  // the epilogue computes its places in the rings from the unit's number, or
+  // carries them along: at 80 registers carrying spills (128 rows, d = 4096,
+  // groups of 128 and 32: 131 and 255 us, computed 122 and 247); with room for
+  // them, computing costs more (64 rows, groups of 64 and 32: 133 and 252 us,
+  // carried 103 and 144)
+  static constexpr bool kCounted = N == 128;
   // a chunk (what is handed from unpacking to MMA to epilogue at once): the
   // whole unit, or as many columns as leave its accumulators 128
   // tensor-memory columns
@@ -626,34 +632,39 @@ __global__ void __launch_bounds__(Shape<N, G>::kThreads, 1)
     Ring<S::kSlots> a;
     int db = 0;
     int shared = 0;  // shared tiles so far
+    int unit0 = 0;   // the run's first unit, counted from the CTA's first
     bool ok = true;
-    for (Runs runs(start, u0, u1, P); ok && runs.next(P);) {
+    for (Runs runs(start, u0, u1, P); ok && runs.next(P); unit0 += runs.run) {
       const Place& c = runs.at;
       // low bits of addresses: where a row of scales starts in its first block
       const uint32_t step = static_cast<uint32_t>(P.scales_ld) * 2u;
       uint32_t lead = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(P.scales)) +
                       static_cast<uint32_t>(c.vt * kTileV) * 2u + static_cast<uint32_t>(c.k * S::kPer) * step;
       int width = P.d - c.k * kStageK;  // columns from the unit's first on
-      for (int it = 0; it < runs.run; ++it, width -= kStageK) {
-        ok = i4_wait(&wfull[w.slot], w.parity, fault);
+      for (int j = 0; j < runs.run; ++j, width -= kStageK) {
+        const int it = unit0 + j;
+        const int ws = S::kCounted ? it % S::kWStages : w.slot;
+        ok = i4_wait(&wfull[ws], S::kCounted ? static_cast<unsigned>(it / S::kWStages) & 1u : w.parity, fault);
         if (!ok) break;
         uint32_t s_now[S::kPer];  // the scales of the unit's groups
-        const unsigned char* sp = sring + w.slot * S::kSideBytes + row * 2;
+        const unsigned char* sp = sring + ws * S::kSideBytes + row * 2;
 #pragma unroll
         for (int i = 0; i < S::kPer; ++i, lead += step)
           s_now[i] = *reinterpret_cast<const unsigned short*>(sp + i * kScalePitch + (lead & 15u));
         __syncwarp();
-        if (leader) mbar_arrive(&wempty[w.slot]);
-        w.next();
+        if (leader) mbar_arrive(&wempty[ws]);
+        if (!S::kCounted) w.next();
 #pragma unroll
         for (int i = 0; i < S::kChunks; ++i) {
-          ok = i4_wait(&done[a.slot], a.parity, fault);
+          const unsigned chunk = static_cast<unsigned>(it * S::kChunks + i);
+          const unsigned slot = S::kCounted ? chunk % S::kSlots : a.slot;
+          ok = i4_wait(&done[slot], S::kCounted ? (chunk / S::kSlots) & 1u : a.parity, fault);
           if (!ok) break;
           tc_fence_after();
           // the chunk's accumulators, group by group, in loads of at most 32 columns
           constexpr int kAll = S::kGroups * S::kCols;
           constexpr int kLd = kAll < 32 ? kAll : 32;
-          const uint32_t src = tmem_d + db * S::kDBuf + lanes;
+          const uint32_t src = tmem_d + (S::kCounted ? chunk % S::kDBufs : db) * S::kDBuf + lanes;
 #pragma unroll
           for (int n = 0; n < kAll; n += kLd) {
             float v[kLd];
@@ -673,9 +684,9 @@ __global__ void __launch_bounds__(Shape<N, G>::kThreads, 1)
           tc_fence_before();
           __syncwarp();
           // these accumulators are the ones of the chunk kDBufs further on
-          if (leader) mbar_arrive(&ready[(a.slot + S::kDBufs) % S::kSlots]);
-          a.next();
-          if (++db == S::kDBufs) db = 0;
+          if (leader) mbar_arrive(&ready[(slot + S::kDBufs) % S::kSlots]);
+          if (!S::kCounted) a.next();
+          if (!S::kCounted && ++db == S::kDBufs) db = 0;
         }
         if (!ok) break;
       }
