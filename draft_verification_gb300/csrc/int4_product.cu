@@ -11,25 +11,39 @@
 // A tile is 128 vocabulary entries (M) by N rows (N = 16, 32, 64 or 128).  The
 // weights are the A operand: they are unpacked in registers and stored to
 // tensor memory, which tcgen05.mma reads A from, so they cross shared memory
-// once, packed.  Roles of a CTA's 16 warps:
-//   warp 0          copies weight stages (128 entries x 256 columns, 16 KB)
-//                   into a ring with TMA, with the scales and zero points of
-//                   the same columns;
+// once, packed.  A unit of work is 256 columns of a tile.  Roles of a CTA:
+//   warp 0          copies units of weights (128 entries x 128 bytes) into a
+//                   ring with TMA, with the scales and zero points of the same
+//                   columns;
 //   warp 1          issues the MMAs (one thread);
-//   warp 2          copies the rows' chunks (N x 128 columns) with TMA;
-//   unpack warps    8 (N <= 64) or 4: thread t of a warpgroup owns entry t of
-//                   the tile; it reads 128 columns (64 bytes) of its entry,
-//                   turns them into q - z and stores them to 64 columns of
-//                   tensor memory (a ring of 4 chunks);
-//   epilogue warps  4 (N <= 64) or 8 (N = 128, half of the rows each): thread
-//                   t owns entry t, reads each group's D_g and adds s D_g to
-//                   its float32 sums.
+//   warp 2          copies the rows' columns (N x 256) with TMA;
+//   warp 3          settles the tiles shared with other CTAs;
+//   unpacking       four warpgroups (two for 128 rows) in turns: thread t owns
+//                   entry t of the tile, reads up to 128 of its columns (64
+//                   bytes), turns them into q - z and stores them to tensor
+//                   memory, a ring of two to four chunks;
+//   epilogue        one warpgroup (two for 64 rows, four for 128, each with
+//                   some of the rows): thread t owns entry t, reads each
+//                   group's D_g and adds s D_g to its float32 sums.
 //
-// The work is a list of units (one weight stage of one tile, tile by tile)
-// that the CTAs divide evenly, so that a tile may be shared by CTAs along the
-// width: each leaves its partial sums in the workspace, and whichever arrives
-// last at the tile's counter adds them in the order of the columns, so the
-// result does not depend on who that is.
+// The work is a list of units, tile by tile, that the CTAs divide evenly, so
+// that a tile may be shared by CTAs along the width: each leaves its partial
+// sums in the workspace, and whichever arrives last at the tile's counter adds
+// them in the order of the columns, so the result does not depend on who that
+// is.  (Whole tiles to a CTA would leave the last round nearly empty: a head of
+// 128256 entries has 6.6 rounds of 152 tiles.)
+//
+// What bounds it: for few rows HBM, which has to read half a byte per weight.
+// With 128256 x 4096 weights in groups of 128 (271 MB, 40 us at the measured
+// 6.8 TB/s) 1 row takes 65 us, 4.2 TB/s; 16 rows 66, 32 rows 74, 64 rows 85. No
+// role is alone at fault: a unit takes about 1150 cycles, of which the copying,
+// MMA and epilogue warps are each busy for 700 or more, and the warp schedulers
+// issue in 62 % of all cycles, most of it the unpacking.  Without the
+// unpacking's arithmetic it is 60 us, without the epilogue's 62, without the
+// weights' copies 64, with one MMA of sixteen 66.  128 rows (134 GFLOP, 70.6 us
+// at the measured bfloat16 rate) take 122 us: there the epilogue's reads of
+// tensor memory, N values per entry and group, are the longest.  Small groups
+// multiply those reads: with groups of 32, 16 rows take 87 us and 128 rows 247.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -75,7 +89,11 @@ struct I4Params {
 // N rows and groups of G columns.
 template <int N, int G>
 struct Shape {
-  static constexpr int kEpiGroups = N == 128 ? 4 : N == 64 ? 2 : 1;  // warpgroups
+  // Warpgroups.  The epilogue's work grows with the rows, the unpacking's does
+  // not.  Measured (V = 128256, d = 4096; epilogue + unpacking): 128 rows, groups
+  // of 128: 4 + 2 131 us, 2 + 4 147; 64 rows, groups of 64: 2 + 4 103 us, 2 + 3
+  // 103, 4 + 3 114, 4 + 2 115; 32 rows: 1 + 4 84 us, 2 + 3 84.
+  static constexpr int kEpiGroups = N == 128 ? 4 : N == 64 ? 2 : 1;
   static constexpr int kUnpackGroups = N == 128 ? 2 : 4;
   static constexpr int kThreads = 128 * (1 + kUnpackGroups + kEpiGroups);
   static constexpr int kCols = N / kEpiGroups;           // rows of x per epilogue thread
@@ -112,6 +130,8 @@ struct Shape {
   static constexpr int kRegsEpi = N == 128 ? 80 : N == 64 ? 104 : 152;
   static_assert(128 * (kRegsCopy + kUnpackGroups * kRegsUnpack + kEpiGroups * kRegsEpi) <= kThreads * kRegsLaunch,
                 "no more registers than the launch holds");
+  static_assert(kRegsCopy <= kRegsLaunch && kRegsUnpack <= kRegsLaunch && kRegsEpi >= kRegsLaunch,
+                "the first two give registers back, the last takes them");
   // scales and zero points of a weight stage: one row of a tile per group
   static constexpr int kPer = kStageK / G;
   static constexpr int kSideBytes = kPer * (kScalePitch + kZeroPitch);
@@ -412,7 +432,8 @@ __global__ void __launch_bounds__(Shape<N, G>::kThreads, 1)
         const long long first = static_cast<long long>(runs.at.k * S::kPer + g);
         const char* src = zeros ? reinterpret_cast<const char*>(P.zeros) + first * P.zeros_ld + v0
                                 : reinterpret_cast<const char*>(P.scales + first * P.scales_ld + v0);
-        for (int x = runs.at.k * (kStageK / 2), n = runs.run; n > 0; --n, x += kStageK / 2, src += step, left -= S::kPer) {
+        int x = runs.at.k * (kStageK / 2);  // packed byte column
+        for (int n = runs.run; n > 0; --n, x += kStageK / 2, src += step, left -= S::kPer) {
           ok = i4_wait(&wempty[w.slot], w.parity ^ 1u, fault);
           if (!ok) break;
           if (serves && g < left) {
@@ -758,7 +779,9 @@ bool good_shape(int R, int V, int d, int group) {
          d <= 65536 && d % group == 0;
 }
 
-// MMA N: the rows of a block, rounded up to a width that has a kernel
+// MMA N: the rows of a block, rounded up to a width that has a kernel.  (The
+// narrowest that fits: with 128256 x 4096 weights in groups of 128 the widths
+// take 66, 74, 85 and 122 us whatever part of their rows is used.)
 int rows_tile(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128; }
 
 size_t product_workspace(int R) {

@@ -453,7 +453,8 @@ struct Slab {
   static size_t smem(const ProcessParams& p) {
     const size_t rows = 2 * kTileBytes + 12 * static_cast<size_t>(p.n);
     if (kListed) return rows + 6 * static_cast<size_t>(kCache);
-    return rows + 4 * (static_cast<size_t>(kTable) * (p.bias_tokens ? 2 : 1) + 2 * kWords) + 2 * static_cast<size_t>(kTable);
+    return rows + 4 * (static_cast<size_t>(kTable) * (p.bias_tokens ? 2 : 1) + 2 * kWords) +
+           2 * static_cast<size_t>(kTable);
   }
 };
 

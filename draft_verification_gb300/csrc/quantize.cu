@@ -34,6 +34,13 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 //     is the quotient's unless it lies within 1e-4 of half way: those few
 //     weights are divided.
 // Groups whose scale is below 2^-120 (or 0, or not finite) are divided.
+//
+// What bounds it: instruction issue, with HBM (2.5 bytes per bfloat16 weight)
+// not far behind.  128256 x 4096 bfloat16 weights in groups of 128 (1.32 GB, 195
+// us at the measured 6.8 TB/s): 244 us, 5.4 TB/s, the schedulers issuing in 76 %
+// of all cycles.  With a division per weight it took 623 us; with the group's
+// size known only at run time 273 us, with the extremes found in float32 320.
+// 50257 x 1024 in groups of 64 with zero points (131 MB, 19 us): 31 us.
 constexpr int kQuantThreads = 256;
 constexpr int kQuantRows = 32;             // rows per CTA, 4 per warp
 constexpr int kQuantCols = 256;            // columns per CTA

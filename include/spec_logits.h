@@ -41,9 +41,9 @@ extern "C" {
 /*    x3 = x2 + the sum of b's bias entries for v, in their order          */
 /*    y  = allowed ? x3 : -inf                                             */
 /* in float32, rounded once to the logits' type; an element that nothing   */
-/* applies to keeps its bits, and -inf stays -inf.  A masked element is     */
-/* -inf whatever it held (NaN included); a row whose mask allows nothing is all -inf, which the  */
-/* verification reports as SPEC_ERR_NONFINITE.                             */
+/* applies to keeps its bits, and -inf stays -inf.  A masked element is    */
+/* -inf whatever it held (NaN included); a row whose mask allows nothing   */
+/* is all -inf, which the verification reports as SPEC_ERR_NONFINITE.      */
 /*  - `out` may be `logits` itself (with the same ld) or must not overlap  */
 /*    it.                                                                  */
 /*  - A history, drafted or bias token outside [0, V) and a history_len or */
@@ -52,8 +52,8 @@ extern "C" {
 /*    SPEC_ERR_PARENT and counts as the root's child.  A mask_index        */
 /*    outside [-1, mask_rows) sets SPEC_ERR_MASK: the row is not masked.   */
 /*    Everything else of the sequence is processed all the same.           */
-/*  - One kernel launch for small calls; for large ones two, of which the   */
-/*    first gathers the sequences' distinct tokens in the workspace.        */
+/*  - One kernel launch; two where many long histories over a large        */
+/*    vocabulary are first gathered in the workspace.                      */
 /* ---------------------------------------------------------------------- */
 typedef struct spec_process_args {
   int B;                       /* sequences, 1..65535                              */
