@@ -125,6 +125,21 @@ struct Lanes<bf16_t> {
     return r;
   }
   static __device__ __forceinline__ float widen(uint32_t b) { return __uint_as_float(b << 16); }
+  // Elements whose bit of ok is 0 become -inf.  Four bits are spread to the
+  // sign bits of four bytes by a product (their partial products do not meet),
+  // and a byte permutation makes a mask of each sign: 11 operations for eight
+  // elements, where a test and a selection of each took three times as many.
+  static __device__ __forceinline__ void only(uint32_t (&w)[4], uint32_t ok) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t signs = ((ok >> 4 * h) & 15u) * 0x10204080u;
+      uint32_t a, b;
+      asm("prmt.b32 %0, %1, 0, 0x9988;" : "=r"(a) : "r"(signs));
+      asm("prmt.b32 %0, %1, 0, 0xbbaa;" : "=r"(b) : "r"(signs));
+      w[2 * h] = (w[2 * h] & a) | (kNegInf4 & ~a);
+      w[2 * h + 1] = (w[2 * h + 1] & b) | (kNegInf4 & ~b);
+    }
+  }
   static constexpr uint32_t kNegInf = 0xff80u;
   static constexpr uint32_t kNegInf4 = 0xff80ff80u;
 };
@@ -136,6 +151,10 @@ struct Lanes<float> {
   static __device__ __forceinline__ void set_bits(uint32_t (&w)[4], int j, uint32_t b) { w[j] = b; }
   static __device__ __forceinline__ uint32_t round(float x) { return __float_as_uint(x); }
   static __device__ __forceinline__ float widen(uint32_t b) { return __uint_as_float(b); }
+  static __device__ __forceinline__ void only(uint32_t (&w)[4], uint32_t ok) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = (ok >> k) & 1u ? w[k] : kNegInf;
+  }
   static constexpr uint32_t kNegInf = 0xff800000u;
   static constexpr uint32_t kNegInf4 = 0xff800000u;
 };
@@ -714,9 +733,7 @@ __global__ void __launch_bounds__(kThreads, (kListed ? 1536 : 1024) / kThreads) 
       if (!ok0[j]) {
         w[j][0] = w[j][1] = w[j][2] = w[j][3] = L::kNegInf4;
       } else if (ok0[j] != kFull) {
-#pragma unroll
-        for (int k = 0; k < E; ++k)
-          if (!((ok0[j] >> k) & 1u)) L::set_bits(w[j], k, L::kNegInf);
+        L::only(w[j], ok0[j]);
       }
       to[j * kThreads + tid] = make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
       ok0[j] = ok1[j];
