@@ -276,19 +276,24 @@ __device__ __forceinline__ void add_biases(const ProcessParams& P, int b, int le
   const long long src = static_cast<long long>(b) * P.bias_ld;
   if (tid == 0) *again = 0;
   __syncthreads();
+  int first_at = -1;  // entry tid's place and value (most lists are no longer than the CTA)
+  float first_x = 0.f;
   for (int e = tid; e < len; e += kThreads) {
     const int t = __ldg(P.bias_tokens + src + e);
+    if (e == tid) first_x = __ldg(P.bias_values + src + e);
     if (t < 0 || t >= P.V) {
       err |= SPEC_ERR_TOKEN;
       continue;
     }
     const int at = enter(t);
     if (at < 0) continue;
+    if (e == tid) first_at = at;
     if (atomicOr(&words[at], kBiased) & kBiased) *again = 1;
   }
   __syncthreads();
   if (!*again) {
-    for (int e = tid; e < len; e += kThreads) {
+    if (first_at >= 0) bias[first_at] = first_x;
+    for (int e = tid + kThreads; e < len; e += kThreads) {
       const int t = __ldg(P.bias_tokens + src + e);
       const int at = t >= 0 && t < P.V ? enter(t) : -1;
       if (at >= 0) bias[at] = __ldg(P.bias_values + src + e);
@@ -303,18 +308,17 @@ __device__ __forceinline__ void add_biases(const ProcessParams& P, int b, int le
       t_next = ahead < len ? __ldg(P.bias_tokens + src + ahead) : -1;
       x_next = ahead < len ? __ldg(P.bias_values + src + ahead) : 0.f;
       const int at = t >= 0 && t < P.V ? enter(t) : -1;
-      __syncwarp();
-      // entries of one token: the lowest lane first
-      unsigned peers = __match_any_sync(0xffffffffu, at >= 0 ? at : -1 - lane);
-      bool todo = at >= 0;
-      while (__any_sync(0xffffffffu, todo)) {
-        if (todo && __ffs(peers) - 1 == lane) {
-          bias[at] += x;
-          todo = false;
-        }
-        peers &= peers - 1;
-        __syncwarp();
+      if (!__any_sync(0xffffffffu, at >= 0)) continue;
+      // the lanes whose entries are one token's all add them up, lowest lane first
+      const unsigned peers = __match_any_sync(0xffffffffu, at);
+      float sum = at >= 0 ? bias[at] : 0.f;
+      for (unsigned todo = at >= 0 ? peers : 0u; __any_sync(0xffffffffu, todo != 0u); todo &= todo - 1) {
+        const float y = __shfl_sync(0xffffffffu, x, todo ? __ffs(todo) - 1 : 0);
+        if (todo) sum = __fadd_rn(sum, y);
       }
+      __syncwarp();
+      if (at >= 0) bias[at] = sum;  // (the same value from each of them)
+      __syncwarp();
     }
   }
   __syncthreads();
