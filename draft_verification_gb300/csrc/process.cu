@@ -346,6 +346,7 @@ __global__ void __launch_bounds__(kCollectThreads) collect_kernel(const ProcessP
   unsigned* before = marked + words;                          // [words] marked tokens before the word
   unsigned* count = before + words;                           // [P.window] of the window's tokens
   float* bias = reinterpret_cast<float*>(count + P.window);   // [P.window]
+  int* token = reinterpret_cast<int*>(bias + P.window);       // [P.window]
   __shared__ unsigned s_warp[kCollectThreads / 32];
   __shared__ int s_err, s_again;
 
@@ -405,27 +406,26 @@ __global__ void __launch_bounds__(kCollectThreads) collect_kernel(const ProcessP
     }
     if (lane == 31) s_warp[warp] = sum;
     __syncthreads();
-    unsigned run = sum - own, total = 0;
-    for (int i = 0; i < kCollectThreads / 32; ++i) {
-      if (i < warp) run += s_warp[i];
-      total += s_warp[i];
-    }
+    static_assert(kCollectThreads == 32 * 32, "a lane per warp");
+    const unsigned total = __reduce_add_sync(0xffffffffu, s_warp[lane]);
+    unsigned run = sum - own + __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[lane] : 0u);
     for (int i = w0; i < w1; ++i) {
-      unsigned m = marked[i];
       before[i] = run;
-      // where the slab that begins here starts, and the marked tokens themselves
+      // where the slab that begins here starts (slab_tokens is a power of two)
       const int t0 = first + i * 32;
-      if (t0 < P.V && t0 % P.slab_tokens == 0)
-        offsets[t0 / P.slab_tokens] = base + static_cast<int>(run);
-      for (; m; m &= m - 1) P.entry_token[out + base + run++] = t0 + __ffs(m) - 1;
+      if (t0 < P.V && (t0 & (P.slab_tokens - 1)) == 0) offsets[t0 / P.slab_tokens] = base + static_cast<int>(run);
+      run += __popc(marked[i]);
     }
 
     for (int window = 0; window < static_cast<int>(total); window += P.window) {
-      const auto place = [&](int t) {
+      // a token's place in the window; whoever comes to a place leaves the token there
+      const auto enter = [&](int t) {
         const int w = word_of(t);
         if (w < 0) return -1;
         const int at = static_cast<int>(before[w] + __popc(marked[w] & ((1u << (t & 31)) - 1u))) - window;
-        return at >= 0 && at < P.window ? at : -1;
+        if (at < 0 || at >= P.window) return -1;
+        token[at] = t;
+        return at;
       };
       for (int i = tid; i < P.window; i += kCollectThreads) {
         count[i] = 0u;
@@ -435,18 +435,19 @@ __global__ void __launch_bounds__(kCollectThreads) collect_kernel(const ProcessP
       for (int i = tid; i < P.n; i += kCollectThreads) {
         int t, p;
         draft_of(P, b, i, t, p, err);
-        const int at = t >= 0 ? place(t) : -1;
+        const int at = t >= 0 ? enter(t) : -1;
         if (at >= 0) atomicOr(&count[at], kDrafted);
       }
       for_history<kCollectThreads>(P, b, len.history, first, count_in, nullptr, [&](int t, int i) {
-        const int at = place(t);
+        const int at = enter(t);
         if (at < 0) return;
         if (i < len.prompt) atomicOr(&count[at], kInPrompt);
         else atomicAdd(&count[at], 1u);
       });
-      add_biases<kCollectThreads>(P, b, len.bias, count, bias, &s_again, err, place);
+      add_biases<kCollectThreads>(P, b, len.bias, count, bias, &s_again, err, enter);
       const int n = min(P.window, static_cast<int>(total) - window);
       for (int i = tid; i < n; i += kCollectThreads) {
+        P.entry_token[out + base + window + i] = token[i];
         P.entry_count[out + base + window + i] = count[i];
         P.entry_bias[out + base + window + i] = bias[i];
       }
@@ -856,7 +857,7 @@ ProcessLayout process_layout(long long B, int n, int V, int history, int biases)
 cudaError_t launch_collect(ProcessParams p, cudaStream_t s) {
   static std::map<int, size_t> done;
   p.window = std::min(kWindow, (p.capacity + 31) / 32 * 32);
-  const size_t dyn = 8 * (static_cast<size_t>(std::min((p.V + 31) / 32, kRangeWords)) + p.window);
+  const size_t dyn = 8 * static_cast<size_t>(std::min((p.V + 31) / 32, kRangeWords)) + 12 * static_cast<size_t>(p.window);
   const cudaError_t e = raise_smem(collect_kernel, dyn, done);
   if (e != cudaSuccess) return e;
   collect_kernel<<<p.B, kCollectThreads, dyn, s>>>(p);
@@ -885,6 +886,7 @@ cudaError_t run_process(ProcessParams p, int nsm, cudaStream_t s) {
     return launch_process<T, 128, 2, false>(p, nsm, s);
   }
   p.slab_tokens = Large::kTokens;
+  static_assert((Large::kTokens & (Large::kTokens - 1)) == 0, "collecting tests for a slab's start with a mask");
   p.slabs = slabs_of<T, 512, 2>(p.V, p.ld);
   const cudaError_t e = launch_collect(p, s);
   return e == cudaSuccess ? launch_process<T, 512, 2, true>(p, nsm, s) : e;
