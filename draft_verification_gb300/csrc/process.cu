@@ -507,10 +507,10 @@ __global__ void __launch_bounds__(kThreads, (kListed ? 1536 : 1024) / kThreads) 
   __shared__ int s_err, s_used, s_again;
 
   const int tid = threadIdx.x;
-  const int b = blockIdx.z;
+  const int b = blockIdx.x;
   const int r0 = blockIdx.y * P.rows_per_cta;
   const int r1 = min(P.n, r0 + P.rows_per_cta);
-  const int v0 = blockIdx.x * (kThreads * kVecs);  // first vector of the slab
+  const int v0 = blockIdx.z * (kThreads * kVecs);  // first vector of the slab
   const int lo = v0 * E - (E - 1);                 // first token of the table
   const bool tree = P.parent != nullptr;
   const bool biased = P.bias_tokens != nullptr;
@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, (kListed ? 1536 : 1024) / kThreads) 
     pdl_wait();
     const int* offsets = P.offsets + static_cast<long long>(b) * (P.slabs + 1);
     // rows that start within a vector take up to e - 1 tokens of the slab before
-    const int slab = blockIdx.x, from = P.ld % E && slab > 0 ? slab - 1 : slab;
+    const int slab = blockIdx.z, from = P.ld % E && slab > 0 ? slab - 1 : slab;
     e0 = __ldcg(offsets + from);
     tokens = __ldcg(offsets + slab + 1) - e0;
     const long long src = static_cast<long long>(b) * P.capacity + e0;
@@ -638,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, (kListed ? 1536 : 1024) / kThreads) 
     __syncthreads();
   } else {
     const Lengths len = lengths_of(P, b, err);
-    const bool checks = blockIdx.x == 0 && blockIdx.y == 0;
+    const bool checks = blockIdx.z == 0 && blockIdx.y == 0;
     const int t0 = max(lo, 0);
     bool bad = false;
     for_history<kThreads>(P, b, len.history, t0, min(lo + S::kTable, P.V) - t0, checks ? &bad : nullptr,
@@ -824,8 +824,10 @@ cudaError_t launch_process(ProcessParams p, int nsm, cudaStream_t s) {
   const int slabs = slabs_of<T, kThreads, kVecs>(p.V, p.ld);
   p.rows_per_cta = rows_of<T, kThreads, kVecs, kListed>(p, nsm);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(slabs), static_cast<unsigned>((p.n + p.rows_per_cta - 1) / p.rows_per_cta),
-                     static_cast<unsigned>(p.B));
+  // sequences first: a slab that takes long (the first, with the frequent tokens
+  // of a vocabulary) does so for every sequence, and what takes long starts early
+  cfg.gridDim = dim3(static_cast<unsigned>(p.B), static_cast<unsigned>((p.n + p.rows_per_cta - 1) / p.rows_per_cta),
+                     static_cast<unsigned>(slabs));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = dyn;
   cfg.stream = s;
