@@ -27,11 +27,11 @@
 //
 // What bounds it: HBM, which has to read every element with an allowed token
 // and write every element.  128 sequences of 9 rows of 128256 bfloat16 logits
-// with grammar masks and histories of up to 8192 tokens (613 MB): 161 us, of
-// which the masked copy alone takes 108, the collecting that is not hidden 20
-// and the rewriting 33; a copy of that size takes 90.5 at the measured 6.8 TB/s,
-// and writing it alone 76.  16 trees of 64 nodes over 50257 tokens (212 MB):
-// 54 us against 31.  One row: 7 us, the launch.
+// with grammar masks and histories of up to 8192 tokens (613 MB): 130 us; a copy
+// of that size takes 90.5 at the measured 6.8 TB/s, and writing it alone 76.
+// Without the rewriting it is 109, and 10 to 15 go to the collecting that is not
+// hidden.  16 trees of 64 nodes over 50257 tokens (212 MB): 52 us against 31, of
+// which the rewriting takes 9.  One row: 7 us, the launch.
 //
 // Vectors are aligned in memory: a row that starts at element m of its vector
 // has tokens [k e - m, k e - m + e) in vector k, so a row's part is the slab
@@ -57,7 +57,6 @@ namespace sv {
 namespace {
 
 constexpr int kMaxRows = 1024;       // rows per sequence
-constexpr int kMaxSlabs = 2097152 / 4096 + 2;  // slabs of a large call
 // bits of a token's word; the low ones count its occurrences
 constexpr unsigned kInPrompt = 1u << 31, kDrafted = 1u << 30, kBiased = 1u << 29;
 constexpr unsigned kMade = kBiased - 1u;
@@ -334,7 +333,9 @@ __device__ __forceinline__ void add_biases(const ProcessParams& P, int b, int le
 // the count at its first word.  (A hash table with appended entries took 25 to
 // 45 us for 4000 to 8000 tokens, most of it in a warp's longest probe.)  Larger
 // vocabularies go range by range, more than kWindow tokens window by window.
-constexpr int kCollectThreads = 1024;  // the call above: 256 threads 177 us, 512 163, 1024 160
+// (Calls with 128 histories of 8192 tokens: 177 us with 256 threads, 163 with
+// 512, 160 with 1024.)
+constexpr int kCollectThreads = 1024;
 constexpr int kRangeWords = 8192;    // 262,144 tokens
 constexpr int kWindow = 8192;
 
@@ -472,7 +473,7 @@ struct Slab {
   static constexpr int kTable = kTokens + kE - 1;        // and the e - 1 tokens before it
   static constexpr int kWords = (kTable + 31) / 32;      // a bitmap of the table
   static constexpr int kTileBytes = kTokens * static_cast<int>(sizeof(T));  // a row's part; there are two
-  static constexpr int kCache = 4096;                    // listed entries kept in shared memory
+  static constexpr int kCache = 1024;                    // listed entries kept in shared memory
   static_assert(!kListed || kTable <= 0x3fff, "an entry's place and two flags in 16 bits");
   static size_t smem(const ProcessParams& p) {
     const size_t rows = 2 * kTileBytes + 12 * static_cast<size_t>(p.n);
@@ -849,7 +850,7 @@ ProcessLayout process_layout(long long B, int n, int V, int history, int biases)
   const long long most = static_cast<long long>(n) + history + biases;
   l.capacity = static_cast<int>(std::min<long long>(most, V));
   const size_t part = align256(static_cast<size_t>(B) * l.capacity * 4);
-  l.token = align256(static_cast<size_t>(B) * (kMaxSlabs + 1) * 4);
+  l.token = align256(static_cast<size_t>(B) * (V / 1024 + 4) * 4);  // slabs of 1024 tokens or more, and the end
   l.count = l.token + part;
   l.bias = l.count + part;
   l.total = l.bias + part;
@@ -859,7 +860,8 @@ ProcessLayout process_layout(long long B, int n, int V, int history, int biases)
 cudaError_t launch_collect(ProcessParams p, cudaStream_t s) {
   static std::map<int, size_t> done;
   p.window = std::min(kWindow, (p.capacity + 31) / 32 * 32);
-  const size_t dyn = 8 * static_cast<size_t>(std::min((p.V + 31) / 32, kRangeWords)) + 12 * static_cast<size_t>(p.window);
+  const size_t dyn =
+      8 * static_cast<size_t>(std::min((p.V + 31) / 32, kRangeWords)) + 12 * static_cast<size_t>(p.window);
   const cudaError_t e = raise_smem(collect_kernel, dyn, done);
   if (e != cudaSuccess) return e;
   collect_kernel<<<p.B, kCollectThreads, dyn, s>>>(p);
@@ -868,30 +870,30 @@ cudaError_t launch_collect(ProcessParams p, cudaStream_t s) {
 
 template <typename T>
 cudaError_t run_process(ProcessParams p, int nsm, cudaStream_t s) {
-  using Large = Slab<T, 512, 2, true>;
-  // One kernel or two: the one kernel's slabs each read the whole history, which
-  // costs about a microsecond per million tokens read; the second launch and the
-  // entries' way through the workspace cost 10 to 15.  Measured (bfloat16, 128
-  // sequences of 9 rows, V = 128256; one kernel, two): histories of 500 tokens,
-  // 4M read, 111 and 120 us; 4000, 32M, 132 and 126; 8192, 66M, 212 and 163.
-  // With 32 sequences of 4000, 8M read: 37 and 49.
+  // One kernel or two: the one kernel's slabs each read the whole history; the
+  // second launch and the entries' way through the workspace cost 5 to 8 us.
+  // Measured (bfloat16, 9 rows, V = 128256; one kernel, two): 128 sequences of
+  // 500 tokens, 4M tokens read, 110 and 113 us; of 2000, 16M, 116 and 115; of
+  // 8000, 65M, 137 and 124, and where most of them are frequent tokens 180 and
+  // 130; 32 sequences of 4000, 8M, 35 and 43.
   const int reads = (p.history ? p.history_ld : 0) + (p.bias_tokens ? p.bias_ld : 0);
-  const long long slabs = slabs_of<T, 128, 2>(p.V, p.ld);
-  if (slabs * p.B * reads <= (1LL << 24)) {
-    // Narrow CTAs stream better (more of them overlap their phases), wide ones
-    // get through a history sooner.  Where a row's part comes to less than 1/512
-    // of the reading, the history decides.  Measured (256 and 128 threads;
-    // V = 32000, 9 rows): 32 sequences of 200 tokens 12.2 and 9.8 us, 128 of
-    // them 40 and 33; 1 sequence with 1 row and 2000 tokens 4.0 and 5.2, 8
-    // with 4 rows 5.8 and 6.0.
-    if (reads > 512LL * rows_of<T, 128, 2, false>(p, nsm)) return launch_process<T, 256, 1, false>(p, nsm, s);
+  p.slabs = slabs_of<T, 128, 2>(p.V, p.ld);
+  if (static_cast<long long>(p.slabs) * p.B * reads <= (1LL << 24)) {
+    // CTAs of 128 threads stream better (more of them overlap their phases),
+    // those of 256 get through a history sooner and read it half as often: worth
+    // it where reading comes to 400 tokens per row or more.  Measured (bfloat16,
+    // 9 rows; 128 and 256 threads): V = 32000, 32 sequences of 200 tokens, 40 per
+    // row, 9.4 and 10.2 us; 2000, 400, 12.0 and 11.5; 8000, 1600, 24.9 and 20.1;
+    // V = 128256, 128 sequences of 500, 56 per row, 110 and 112.
+    if (reads > 400LL * rows_of<T, 128, 2, false>(p, nsm)) return launch_process<T, 256, 2, false>(p, nsm, s);
     return launch_process<T, 128, 2, false>(p, nsm, s);
   }
-  p.slab_tokens = Large::kTokens;
-  static_assert((Large::kTokens & (Large::kTokens - 1)) == 0, "collecting tests for a slab's start with a mask");
-  p.slabs = slabs_of<T, 512, 2>(p.V, p.ld);
+  using Listed = Slab<T, 128, 2, true>;
+  static_assert((Listed::kTokens & (Listed::kTokens - 1)) == 0 && Listed::kTokens >= 1024,
+                "collecting tests for a slab's start with a mask; the workspace's offsets");
+  p.slab_tokens = Listed::kTokens;
   const cudaError_t e = launch_collect(p, s);
-  return e == cudaSuccess ? launch_process<T, 512, 2, true>(p, nsm, s) : e;
+  return e == cudaSuccess ? launch_process<T, 128, 2, true>(p, nsm, s) : e;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
