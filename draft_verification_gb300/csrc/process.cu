@@ -27,11 +27,10 @@
 //
 // What bounds it: HBM, which has to read every element with an allowed token
 // and write every element.  128 sequences of 9 rows of 128256 bfloat16 logits
-// with grammar masks and histories of up to 8192 tokens (613 MB): 130 us; a copy
-// of that size takes 90.5 at the measured 6.8 TB/s, and writing it alone 76.
-// Without the rewriting it is 109, and 10 to 15 go to the collecting that is not
-// hidden.  16 trees of 64 nodes over 50257 tokens (212 MB): 52 us against 31, of
-// which the rewriting takes 9.  One row: 7 us, the launch.
+// with grammar masks and histories of up to 8192 tokens (613 MB): 111 us; a copy
+// of that size takes 90.5 at the measured 6.8 TB/s, and writing it alone 76.  16
+// trees of 64 nodes over 50257 tokens, whose rows start anywhere (212 MB): 52 us
+// against 31, of which the rewriting takes 9.  One row: 7 us, the launch.
 //
 // Vectors are aligned in memory: a row that starts at element m of its vector
 // has tokens [k e - m, k e - m + e) in vector k, so a row's part is the slab
@@ -483,8 +482,14 @@ struct Slab {
   }
 };
 
-template <typename T, int kThreads, int kVecs, bool kListed>
-__global__ void __launch_bounds__(kThreads, (kListed ? 1536 : 1024) / kThreads) process_kernel(const ProcessParams P) {
+// Threads an SM holds: as many as leave the kernel its registers (56, and 40
+// with listed entries).  Without the list, 128 sequences of 9 rows of 128256
+// tokens: 1024 threads 108 us, 1152 103, 1280 107; 16 trees of 64 rows of 50257:
+// 51, 52, 68.
+__host__ __device__ constexpr int resident_threads(bool listed) { return listed ? 1536 : 1152; }
+
+template <typename T, int kThreads, int kVecs, bool kListed, bool kAligned>
+__global__ void __launch_bounds__(kThreads, resident_threads(kListed) / kThreads) process_kernel(const ProcessParams P) {
   using L = Lanes<T>;
   using S = Slab<T, kThreads, kVecs, kListed>;
   constexpr int E = S::kE;
@@ -524,6 +529,7 @@ __global__ void __launch_bounds__(kThreads, (kListed ? 1536 : 1024) / kThreads) 
     return mr < P.mask_rows ? static_cast<int>(mr) : -1;
   };
   const auto lead_of = [&](int i) {  // element of its first vector at which row i starts
+    if constexpr (kAligned) return 0;
     return static_cast<int>(((static_cast<long long>(b) * P.n + i) * P.ld) % E);
   };
   // the mask bits of row i's vectors (mrow < 0: not masked; 0 for vectors outside the row)
@@ -535,7 +541,9 @@ __global__ void __launch_bounds__(kThreads, (kListed ? 1536 : 1024) / kThreads) 
       const int t0 = (v0 + j * kThreads + tid) * E - m;
       ok[j] = t0 < P.V ? kFull : 0u;
       if (mk && t0 < P.V) {
-        if (t0 < 0) {
+        if constexpr (kAligned) {  // (a vector's bits lie in one word)
+          ok[j] = (__ldg(mk + (t0 >> 5)) >> (t0 & 31)) & kFull;
+        } else if (t0 < 0) {
           ok[j] = (__ldg(mk) << -t0) & kFull;
         } else {
           const int q = t0 >> 5, s = t0 & 31;
@@ -554,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, (kListed ? 1536 : 1024) / kThreads) 
     for (int j = 0; j < kVecs; ++j) {
       const int t0 = (v0 + j * kThreads + tid) * E - m;
       if (!ok[j]) continue;
-      if (t0 >= 0 && t0 + E <= P.V) {
+      if ((kAligned || t0 >= 0) && t0 + E <= P.V) {
         const uint4 x = ld_row16(src + t0);
         w[j][0] = x.x;
         w[j][1] = x.y;
@@ -760,13 +768,13 @@ __global__ void __launch_bounds__(kThreads, (kListed ? 1536 : 1024) / kThreads) 
     if (i + 1 < r1) fill(i + 1);
     if (tokens > 0) __syncthreads();
     T* dst = static_cast<T*>(P.out) + row * P.out_ld;
-    const bool same = static_cast<int>((row * P.out_ld) % E) == m;
+    const bool same = kAligned || static_cast<int>((row * P.out_ld) % E) == m;
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
       const int t0 = (v0 + j * kThreads + tid) * E - m;
       if (t0 >= P.V) continue;
       const uint4 x = reinterpret_cast<const uint4*>(part)[j * kThreads + tid];
-      if (same && t0 >= 0 && t0 + E <= P.V) {
+      if (same && (kAligned || t0 >= 0) && t0 + E <= P.V) {
         if (!(kDebugChecks && misaligned16(dst + t0))) *reinterpret_cast<uint4*>(dst + t0) = x;
       } else {
         const uint32_t y[4] = {x.x, x.y, x.z, x.w};
@@ -809,17 +817,17 @@ int slabs_of(int V, long long ld) {
 template <typename T, int kThreads, int kVecs, bool kListed>
 int rows_of(const ProcessParams& p, int nsm) {
   const long long have = static_cast<long long>(slabs_of<T, kThreads, kVecs>(p.V, p.ld)) * p.B;
-  const long long fill = (kListed ? 1536LL : 1024LL) / kThreads * nsm;
+  const long long fill = static_cast<long long>(resident_threads(kListed) / kThreads) * nsm;
   const long long parts = std::min<long long>(p.n, std::max<long long>(1, fill / have));
   return static_cast<int>((p.n + parts - 1) / parts);
 }
 
-template <typename T, int kThreads, int kVecs, bool kListed>
-cudaError_t launch_process(ProcessParams p, int nsm, cudaStream_t s) {
+template <typename T, int kThreads, int kVecs, bool kListed, bool kAligned>
+cudaError_t launch_rows(ProcessParams p, int nsm, cudaStream_t s) {
   using S = Slab<T, kThreads, kVecs, kListed>;
   static std::map<int, size_t> done;
   const size_t dyn = S::smem(p);
-  const auto kernel = process_kernel<T, kThreads, kVecs, kListed>;
+  const auto kernel = process_kernel<T, kThreads, kVecs, kListed, kAligned>;
   cudaError_t e = raise_smem(kernel, dyn, done);
   if (e != cudaSuccess) return e;
   const int slabs = slabs_of<T, kThreads, kVecs>(p.V, p.ld);
@@ -838,6 +846,17 @@ cudaError_t launch_process(ProcessParams p, int nsm, cudaStream_t s) {
   cfg.attrs = at;
   cfg.numAttrs = kListed ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+// Rows that all start and end up on a vector boundary need no shifts of their
+// mask bits and no choice of how to store.  Measured (128 sequences of 9 rows of
+// 128256 bfloat16 logits, masks, histories of 8192 tokens): 111 us, by the
+// kernel for any alignment 130; without masks 108 and 110.
+template <typename T, int kThreads, int kVecs, bool kListed>
+cudaError_t launch_process(const ProcessParams& p, int nsm, cudaStream_t s) {
+  constexpr int E = Lanes<T>::kN;
+  if (p.ld % E == 0 && p.out_ld % E == 0) return launch_rows<T, kThreads, kVecs, kListed, true>(p, nsm, s);
+  return launch_rows<T, kThreads, kVecs, kListed, false>(p, nsm, s);
 }
 
 // The entries' places in the workspace.
