@@ -118,6 +118,10 @@ struct Shape {
   // a piece: what one warpgroup unpacks at a time; the warpgroups take turns
   static constexpr int kPieceK = kChunkK < 128 ? kChunkK : 128;
   static constexpr int kPieces = kStageK / kPieceK;      // per unit
+  // A warpgroup that comes to a chunk finished one at most kSlots before, whose
+  // slot was free then: so the slot it waits for is one round behind at most,
+  // and the round's parity says which.
+  static_assert(kUnpackGroups * kPieceK <= kSlots * kChunkK, "no slot two rounds behind");
   static constexpr int kXBytes = N * kStageK * 2;        // the rows' columns of a unit: four 64-column blocks
   // the rows come from L2, the weights from HBM: the weights' ring is the deep one
   static constexpr int kXStages = N <= 32 ? 4 : N == 64 ? 3 : 2;
