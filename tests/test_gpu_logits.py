@@ -249,10 +249,10 @@ def test_process_data_errors(cuda_device, V, H):
         assert out["seq_error"].tolist() == want
 
 
-def test_process_deterministic_on_a_side_stream_and_in_a_graph(cuda_device):
+@pytest.mark.parametrize("B,n,V,H", [(20, 5, 30001, 500), (60, 2, 20000, 30000)])  # one kernel, and gathered first
+def test_process_deterministic_on_a_side_stream_and_in_a_graph(cuda_device, B, n, V, H):
     rng = np.random.default_rng(7)
-    B, n, V = 20, 5, 30001
-    w = make_process(rng, B, n, V, H=500, density=0.5, bias=40)
+    w = make_process(rng, B, n, V, H=H, density=0.5, bias=40)
     x = torch.from_numpy(rng.normal(0, 3, (B, n, V)).astype(np.float32)).to(cuda_device, torch.bfloat16)
     first = bits(run_process(x, w, cuda_device)["logits"]).copy()
     side = torch.cuda.Stream()
