@@ -26,27 +26,28 @@
 //                   some of the rows): thread t owns entry t, reads each
 //                   group's D_g and adds s D_g to its float32 sums.
 //
-// The work is a list of units, tile by tile, that the CTAs divide evenly, so
-// that a tile may be shared by CTAs along the width: each leaves its partial
-// sums in the workspace, and whichever arrives last at the tile's counter adds
-// them in the order of the columns, so the result does not depend on who that
-// is.  (Whole tiles to a CTA would leave the last round nearly empty: a head of
-// 128256 entries has 6.6 rounds of 152 tiles.)
+// The work is a list of units, tile by tile, divided over the CTAs: by whole
+// tiles or equal parts of tiles where that is even enough, else evenly
+// (launch_product has the rule).  Where a tile is shared along the width each
+// CTA leaves its partial sums in the workspace, and whichever arrives last at
+// the tile's counter adds them in the order of the columns, so the result does
+// not depend on who that is.
 //
 // What bounds it: for few rows HBM, which has to read half a byte per weight.
 // With 128256 x 4096 weights in groups of 128 (271 MB, 40 us at the measured
-// 6.8 TB/s) 1 row takes 65 us, 4.2 TB/s; 16 rows 66, 32 rows 74, 64 rows 85. No
-// role is alone at fault: a unit takes about 1150 cycles, of which the copying,
-// MMA and epilogue warps are each busy for 700 or more, and the warp schedulers
-// issue in 62 % of all cycles, most of it the unpacking.  Without the
-// unpacking's arithmetic it is 60 us, without the epilogue's 62, without the
-// weights' copies 64, with one MMA of sixteen 66.  128 rows (134 GFLOP, 70.6 us
-// at the measured bfloat16 rate) take 122 us: there the epilogue's reads of
-// tensor memory, N values per entry and group, are the longest.  Small groups
-// multiply those reads: with groups of 32, 16 rows take 87 us and 128 rows 247.
+// 6.8 TB/s) 1 row takes 64 us, 4.2 TB/s; 64 rows 80.  No role is alone at
+// fault: a unit takes about 1150 cycles, of which the copying, MMA and epilogue
+// warps are each busy for 600 or more, and the warp schedulers issue in 62 % of
+// all cycles, most of it the unpacking.  Of 66 us (before tiles stayed whole)
+// 60 were left without the unpacking's arithmetic, 62 without the epilogue's, 64
+// without the weights' copies, 66 with one MMA of sixteen.  128 rows (134 GFLOP,
+// 70.6 us at the measured bfloat16 rate) take 114 us: there the epilogue's reads
+// of tensor memory, N values per entry and group, are the longest.  Small groups
+// multiply those reads: with groups of 32, 16 rows took 87 us and 128 rows 247.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <map>
 #include <mutex>
@@ -76,6 +77,7 @@ struct I4Params {
   int R, V, d;
   int ntv, nk;              // tiles of the vocabulary, stages of the width
   int units;                // row blocks * ntv * nk
+  int grain, grains;        // units that stay together: 1 or a tile's; and how many
   long long scales_ld, zeros_ld, out_ld;
   const unsigned short* scales;
   const unsigned char* zeros;
@@ -246,8 +248,8 @@ __device__ __forceinline__ void unpack8(uint32_t w, uint32_t mz, uint32_t* out) 
 }
 
 // first unit of CTA c of `ctas`
-__host__ __device__ __forceinline__ int first_unit(int c, int ctas, int units) {
-  return static_cast<int>(static_cast<long long>(c) * units / ctas);
+__device__ __forceinline__ int first_unit(int c, int ctas, const I4Params& P) {
+  return static_cast<int>(static_cast<long long>(c) * P.grains / ctas) * P.grain;
 }
 
 // Place in the CTA's list of units: stage k of tile vt of row block rb.  The
@@ -321,10 +323,10 @@ struct SharedTile {
   __device__ __forceinline__ void find(int u, int ctas, const I4Params& P) {
     u0 = u / P.nk * P.nk;
     first = static_cast<int>(static_cast<long long>(u0) * ctas / P.units);
-    while (first_unit(first + 1, ctas, P.units) <= u0) ++first;
-    while (first_unit(first, ctas, P.units) > u0) --first;
+    while (first_unit(first + 1, ctas, P) <= u0) ++first;
+    while (first_unit(first, ctas, P) > u0) --first;
     last = first;
-    while (first_unit(last + 1, ctas, P.units) < u0 + P.nk) ++last;
+    while (first_unit(last + 1, ctas, P) < u0 + P.nk) ++last;
   }
 };
 
@@ -374,7 +376,7 @@ __global__ void __launch_bounds__(Shape<N, G>::kThreads, 1)
   unsigned char* xring = wring + S::kWStages * kStageBytes;
   unsigned char* sring = xring + S::kXStages * S::kXBytes;
   const int ctas = gridDim.x, cta = blockIdx.x;
-  const int u0 = first_unit(cta, ctas, P.units), u1 = first_unit(cta + 1, ctas, P.units);
+  const int u0 = first_unit(cta, ctas, P), u1 = first_unit(cta + 1, ctas, P);
   const int units = u1 - u0;
   int start = u1 - u1 % P.nk;
   if (start <= u0 || start == u1) start = u0;
@@ -784,8 +786,9 @@ bool good_shape(int R, int V, int d, int group) {
 }
 
 // MMA N: the rows of a block, rounded up to a width that has a kernel.  (The
-// narrowest that fits: with 128256 x 4096 weights in groups of 128 the widths
-// take 66, 74, 85 and 122 us whatever part of their rows is used.)
+// narrowest that fits: with 128256 x 4096 weights in groups of 128, evenly
+// divided, the widths take 66, 74, 85 and 122 us whatever part of their rows is
+// used.)
 int rows_tile(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128; }
 
 size_t product_workspace(int R) {
@@ -857,7 +860,26 @@ spec_status launch_product(const spec_int4_product_args& a, cudaStream_t s) {
   P.error_word = a.error_word;
   const int nsm = sm_count();
   if (nsm < 1) return SPEC_ECUDA;
-  const int ctas = min(min(nsm, kMaxCtas), P.units);
+  // A tile shared by CTAs that each have parts of two tiles costs them 4 to 8 us
+  // at the end of the call, its join included.  So tiles stay whole, or are cut
+  // into the same number of equal parts (of 4 units or more, which begin and end
+  // with a tile), where the longest CTA has at most 8 units more than an even
+  // division would give it.  Measured (V, d, group; evenly divided, and so):
+  // 128 rows 128256, 4096, 128 124 and 114 us, 1 row 66 and 64; 33 rows 50257,
+  // 2048, 64 31 and 27; 128 rows 1000, 8192, 64 33 and 23, 12800, 4096, 128
+  // 27 and 22.  With 12 instead of 8 units: 16 rows 25000, 4096, 128 21 and 23,
+  // 12800, 8192, 128 23 and 21.
+  const int most = std::min(nsm, kMaxCtas), tiles = P.units / P.nk;
+  const int even = (P.units + most - 1) / most;
+  int ctas = std::min(most, P.units);
+  P.grain = 1;
+  if (tiles > most) {
+    if ((tiles + most - 1) / most * P.nk <= even + 8) P.grain = P.nk;
+  } else {
+    const int parts = std::min(most / tiles, std::max(1, P.nk / 4));
+    if ((P.nk + parts - 1) / parts <= even + 8) ctas = tiles * parts;
+  }
+  P.grains = P.units / P.grain;
   CUtensorMap tw, tx;
   if (!weight_map(&tw, a.codes, a.V, a.d, a.codes_ld) || !rows_map(&tx, a.x, a.R, a.d, a.x_ld, N)) return SPEC_ECUDA;
   if (raise_smem<N, G>() != cudaSuccess) return SPEC_ECUDA;

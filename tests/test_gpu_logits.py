@@ -398,6 +398,24 @@ def test_product(cuda_device, R, V, d, group, zeros, dtype):
     assert np.array_equal(bits(out["logits"]), first)
 
 
+@pytest.mark.parametrize("R,V,d,group,zeros,dtype", [
+    (5, 1000, 8192, 128, False, "f32"),     # equal parts of tiles
+    (300, 10000, 1024, 32, True, "bf16"),   # whole tiles, more than CTAs
+    (70, 9000, 512, 64, True, "f32"),       # whole tiles, fewer
+    (9, 9800, 5120, 64, True, "bf16"),      # evenly, fewer tiles than CTAs
+    (400, 4990, 4096, 128, False, "f32"),   # evenly, more
+])
+def test_product_divisions(cuda_device, R, V, d, group, zeros, dtype):
+    import draft_verification_gb300 as dv
+    x, codes, scales, z = make_product(R, V, d, group, zeros, R + V, cuda_device)
+    plan = dv.Int4ProductPlan(x, codes, scales, z, group=group, out_dtype=DTYPES[dtype])
+    first = plan.run()["logits"].clone()
+    check_product(first, x, codes, scales, z, group)
+    for _ in range(5):
+        assert torch.equal(plan.run()["logits"], first)
+    assert int(plan.out["error_word"]) == 0
+
+
 @pytest.mark.parametrize("R,V,d,group", [(1, 300, 512, 128), (33, 1000, 1024, 64), (128, 260, 768, 32)])
 def test_product_of_small_integers_is_exact(cuda_device, R, V, d, group):
     """Integer hidden states and power-of-two scales: every sum is exact in float32, whatever its order."""
