@@ -9,10 +9,14 @@ the logits that a verification reads.
 
 As for the verifications, a plan binds its buffers once and ``run()`` launches
 without Python-side allocation; the functions take one call's tensors (device
-tensors stay on the device, CPU tensors are copied there and the results back).
+tensors stay on the device; CPU tensors are copied there and the results back,
+complete on return).  With ``stream`` all of a function's work goes to that
+stream, behind what the current one holds; the results belong to it.
 """
 
 from __future__ import annotations
+
+import contextlib
 
 import torch
 
@@ -244,6 +248,30 @@ class Int4ProductPlan(_Plan):
         self._call = lib.spec_int4_product
 
 
+@contextlib.contextmanager
+def _work_on(stream, tensors):
+    """What a call allocates, clears, copies and launches inside goes to `stream`,
+    behind the work that the current one holds.  `tensors`: the call's inputs,
+    whose memory stays theirs until `stream` is done with them."""
+    if stream is None or stream == torch.cuda.current_stream():
+        yield
+        return
+    stream.wait_stream(torch.cuda.current_stream())
+    for t in tensors:
+        if t is not None and t.device.type == "cuda":
+            t.record_stream(stream)
+    with torch.cuda.stream(stream):
+        yield
+
+
+def _results(out, host):
+    """A call's results: the device's tensors, or complete copies on the host."""
+    out = _finish(out, host)
+    if host:
+        torch.cuda.current_stream().synchronize()
+    return out
+
+
 def process_logits(logits, tokens=None, *, parent=None, history=None, history_len=None, prompt_len=None,
                    repetition=None, frequency=None, presence=None, bias_tokens=None, bias_values=None,
                    bias_len=None, mask=None, mask_index=None, out=None, device="cuda", stream=None):
@@ -253,27 +281,30 @@ def process_logits(logits, tokens=None, *, parent=None, history=None, history_le
     given = dict(parent=parent, history=history, history_len=history_len, prompt_len=prompt_len,
                  repetition=repetition, frequency=frequency, presence=presence, bias_tokens=bias_tokens,
                  bias_values=bias_values, bias_len=bias_len, mask=mask, mask_index=mask_index)
-    if host:
-        if out is not None:
-            raise ValueError("out: device tensors only")
-        logits, tokens = _to_device([logits, tokens], device)
-        given = dict(zip(given, _to_device(list(given.values()), device)))
-    return _finish(ProcessLogitsPlan(logits, tokens, out=out, **given).run(stream), host)
+    if host and out is not None:
+        raise ValueError("out: device tensors only")
+    with _work_on(stream, [logits, tokens, out, *given.values()]):
+        if host:
+            logits, tokens = _to_device([logits, tokens], device)
+            given = dict(zip(given, _to_device(list(given.values()), device)))
+        return _results(ProcessLogitsPlan(logits, tokens, out=out, **given).run(), host)
 
 
 def quantize_int4(weights, *, group=128, zeros=False, device="cuda", stream=None):
     """Quantise a matrix to 4 bits; returns codes, scales and, with
     ``zeros=True``, zeros.  See QuantizeInt4Plan."""
     host = weights.device.type == "cpu"
-    if host:
-        (weights,) = _to_device([weights], device)
-    return _finish(QuantizeInt4Plan(weights, group=group, zeros=zeros).run(stream), host)
+    with _work_on(stream, [weights]):
+        if host:
+            (weights,) = _to_device([weights], device)
+        return _results(QuantizeInt4Plan(weights, group=group, zeros=zeros).run(), host)
 
 
 def int4_product(x, codes, scales, zeros=None, *, group=128, out_dtype=torch.bfloat16, device="cuda", stream=None):
     """Products of x's rows with a 4-bit matrix; returns logits, error_word.
     See Int4ProductPlan."""
     host = x.device.type == "cpu"
-    if host:
-        x, codes, scales, zeros = _to_device([x, codes, scales, zeros], device)
-    return _finish(Int4ProductPlan(x, codes, scales, zeros, group=group, out_dtype=out_dtype).run(stream), host)
+    with _work_on(stream, [x, codes, scales, zeros]):
+        if host:
+            x, codes, scales, zeros = _to_device([x, codes, scales, zeros], device)
+        return _results(Int4ProductPlan(x, codes, scales, zeros, group=group, out_dtype=out_dtype).run(), host)

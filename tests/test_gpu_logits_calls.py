@@ -1,0 +1,75 @@
+"""How the logit-side operators are called: streams, host tensors, workspaces,
+buffers that do not begin or end where a copy would like them to, and the
+limits of the arguments.  The tolerances are those of test_gpu_logits."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import logits as O
+
+from . import test_gpu_logits as T
+
+pytestmark = pytest.mark.gpu
+
+
+def later(t, device):
+    """A copy of t that the current stream finishes some ten milliseconds from now."""
+    r = torch.zeros_like(t, device=device)
+    torch.cuda._sleep(20_000_000)
+    r.copy_(t)
+    return r
+
+
+def test_functions_do_all_their_work_on_the_given_stream(cuda_device):
+    """Inputs that the current stream has yet to write, free memory full of
+    ones (a workspace taken from it has to be cleared in order), results read
+    after the given stream alone."""
+    import draft_verification_gb300 as dv
+    side = torch.cuda.Stream()
+    for stream in (torch.cuda.current_stream(), side):
+        with torch.cuda.stream(stream):
+            for n in (1 << 9, 1 << 12, 3 << 20, 3 << 20, 20 << 20):
+                torch.full((n,), 0xff, dtype=torch.uint8, device=cuda_device)
+    R, V, d, group = 5, 1000, 8192, 128  # every tile is shared by CTAs
+    x, codes, scales, z = T.make_product(R, V, d, group, True, 21, cuda_device)
+    late = later(x, cuda_device)
+    out = dv.int4_product(late, codes, scales, z, group=group, out_dtype=torch.float32, stream=side)
+    del late
+    torch.full((R, d), 1e9, dtype=torch.bfloat16, device=cuda_device)  # (the freed input's block, used again)
+    side.synchronize()
+    assert int(out["error_word"]) == 0
+    T.check_product(out["logits"], x, codes, scales, z, group)
+
+    w = torch.randn(300, 256, generator=torch.Generator().manual_seed(22)).to(cuda_device)
+    out = dv.quantize_int4(later(w, cuda_device), group=64, zeros=True, stream=side)
+    side.synchronize()
+    T.check_quantize(w, out, 64, True)
+
+    rng = np.random.default_rng(23)
+    B, n, V = 3, 4, 5000
+    p = T.make_process(rng, B, n, V, H=300, density=0.5)
+    x = torch.from_numpy(rng.normal(0, 3, (B, n, V)).astype(np.float32)).to(cuda_device)
+    kw = {k: T.dev(v, cuda_device) for k, v in p.items()}
+    out = dv.process_logits(later(x, cuda_device), stream=side, **kw)
+    side.synchronize()
+    T.check_process(x, out, p)
+
+
+@pytest.mark.parametrize("own_stream", [False, True])
+def test_functions_return_complete_host_tensors(cuda_device, own_stream):
+    """Host tensors in: the host may read the results as soon as the call returns."""
+    import draft_verification_gb300 as dv
+    stream = torch.cuda.Stream() if own_stream else None
+    rng = np.random.default_rng(24)
+    for k in range(3):
+        x, codes, scales, z = T.make_product(40, 9000, 1024, 64, True, 25 + k, "cpu")
+        out = dv.int4_product(x, codes, scales, z, group=64, stream=stream)
+        assert out["logits"].device.type == "cpu"
+        T.check_product(out["logits"].clone(), x, codes, scales, z, 64)
+        w = torch.from_numpy(rng.normal(0, 1, (2000, 512)).astype(np.float32))
+        T.check_quantize(w, {k: v.clone() for k, v in dv.quantize_int4(w, group=32, stream=stream).items()}, 32, False)
+        p = T.make_process(rng, 4, 5, 30000, H=300, density=0.5)
+        y = torch.from_numpy(rng.normal(0, 3, (4, 5, 30000)).astype(np.float32))
+        out = dv.process_logits(y, stream=stream, **{k: torch.from_numpy(v) for k, v in p.items()})
+        T.check_process(y, {k: v.clone() for k, v in out.items()}, p)
