@@ -156,12 +156,14 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, unsigned bytes) {
 }
 // Copy `bytes` (a multiple of 16; both addresses 16-byte aligned) from global
 // to this CTA's shared memory; completion is counted on `bar`.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, unsigned bytes, uint64_t* bar) {
-  if (kDebugChecks && (misaligned16(dst) || misaligned16(src) || (bytes & 15u))) return;
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_addr(dst)),
+__device__ __forceinline__ void bulk_load_at(uint32_t dst, const void* src, unsigned bytes, uint64_t* bar) {
+  if (kDebugChecks && ((dst & 15u) || misaligned16(src) || (bytes & 15u))) return;
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(smem_addr(bar))
                : "memory");
+}
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, unsigned bytes, uint64_t* bar) {
+  bulk_load_at(smem_addr(dst), src, bytes, bar);
 }
 __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, unsigned parity) {
   uint32_t ok;

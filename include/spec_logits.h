@@ -158,6 +158,9 @@ spec_status spec_quantize_int4(const spec_quantize_int4_args* args, cudaStream_t
 /*    share one pass over the weights; more rows take further passes.      */
 /*  - One kernel launch of at most one CTA per SM.  An entry whose width is */
 /*    shared by several CTAs is summed in the order of the columns.        */
+/*  - Nothing before a matrix's first entry or after its last one is read,  */
+/*    wherever it starts; of what lies between rows (strides larger than    */
+/*    the width) some bytes may be, and are not used.                       */
 /*  - Workspace: its first 1024 bytes must be zero before its first use    */
 /*    (and again after a call that reported SPEC_ERR_INTERNAL); a call     */
 /*    leaves them zero, so calls that follow one another may share it.     */

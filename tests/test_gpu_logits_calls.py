@@ -73,3 +73,28 @@ def test_functions_return_complete_host_tensors(cuda_device, own_stream):
         y = torch.from_numpy(rng.normal(0, 3, (4, 5, 30000)).astype(np.float32))
         out = dv.process_logits(y, stream=stream, **{k: torch.from_numpy(v) for k, v in p.items()})
         T.check_process(y, {k: v.clone() for k, v in out.items()}, p)
+
+
+@pytest.mark.parametrize("V", [1, 7, 15, 16, 17, 100, 128, 129, 143, 144, 257, 400])
+@pytest.mark.parametrize("group,d", [(32, 96), (128, 384), (64, 1024)])
+def test_product_of_matrices_that_start_and_end_anywhere(cuda_device, V, group, d):
+    """Scales and zero points at every byte that their type allows, between bytes that would show: NaN scales,
+    zero points beyond 15."""
+    import draft_verification_gb300 as dv
+    x, codes, scales, z = T.make_product(3, V, d, group, True, V + d, cuda_device)
+    rows = d // group
+    first = None
+    for k, pad in enumerate((0, 1, 3, 8, 0, 5, 16, 0)):
+        def within(t, lead, fill):
+            flat = torch.full((lead + (rows - 1) * (V + pad) + V + 16,), fill, dtype=t.dtype, device=cuda_device)
+            view = flat.as_strided((rows, V), (V + pad, 1), lead)
+            view.copy_(t)
+            return view
+        for zl in (2 * k, 2 * k + 1):
+            out = dv.int4_product(x, codes, within(scales, k, float("nan")), within(z, zl, 255), group=group,
+                                  out_dtype=torch.float32)
+            assert int(out["error_word"]) == 0
+            if first is None:
+                T.check_product(out["logits"], x, codes, scales, z, group)
+                first = out["logits"]
+            assert torch.equal(out["logits"], first)
