@@ -56,9 +56,13 @@ namespace sv {
 namespace {
 
 constexpr int kMaxRows = 1024;       // rows per sequence
+// entries of a history or a bias list: with the rows' tokens their occurrences
+// stay below a word's flags, and the loops' positions below 2^31
+constexpr int kMaxList = 1 << 28;
 // bits of a token's word; the low ones count its occurrences
 constexpr unsigned kInPrompt = 1u << 31, kDrafted = 1u << 30, kBiased = 1u << 29;
 constexpr unsigned kMade = kBiased - 1u;
+static_assert(static_cast<unsigned>(kMaxList) + kMaxRows <= kMade, "the occurrences fit their bits");
 
 struct ProcessParams {
   int B, n, V;
@@ -921,7 +925,8 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 }  // namespace sv
 
 extern "C" size_t spec_process_workspace_size(int B, int n, int V, int history_ld, int bias_ld) {
-  if (B < 1 || B > sv::kMaxSeq || n < 1 || n > sv::kMaxRows || V < 1 || V > 2097152 || history_ld < 0 || bias_ld < 0)
+  if (B < 1 || B > sv::kMaxSeq || n < 1 || n > sv::kMaxRows || V < 1 || V > 2097152 || history_ld < 0 || bias_ld < 0 ||
+      history_ld > sv::kMaxList || bias_ld > sv::kMaxList)
     return 0;
   return sv::process_layout(B, n, V, history_ld, bias_ld).total;
 }
@@ -936,8 +941,8 @@ extern "C" spec_status spec_process_logits(const spec_process_args* a, cudaStrea
   if (a->logits == a->out && a->ld != a->out_ld) return SPEC_EINVAL;
   if (a->parent && !a->tokens) return SPEC_EINVAL;
   if (a->tokens && a->tokens_ld < (a->parent ? a->n : a->n - 1)) return SPEC_EINVAL;
-  if (a->history && a->history_ld < 0) return SPEC_EINVAL;
-  if (a->bias_tokens && (!a->bias_values || a->bias_ld < 0)) return SPEC_EINVAL;
+  if (a->history && (a->history_ld < 0 || a->history_ld > kMaxList)) return SPEC_EINVAL;
+  if (a->bias_tokens && (!a->bias_values || a->bias_ld < 0 || a->bias_ld > kMaxList)) return SPEC_EINVAL;
   if (a->mask && (a->mask_rows < 1 || a->mask_ld < (a->V + 31) / 32)) return SPEC_EINVAL;
   if (a->mask && !a->mask_index && a->mask_rows < static_cast<long long>(a->B) * a->n) return SPEC_EINVAL;
   if (!aligned16(a->logits) || !aligned16(a->out)) return SPEC_EALIGN;

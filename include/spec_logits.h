@@ -70,7 +70,7 @@ typedef struct spec_process_args {
   const int* parent;           /* [B, n] parent of each node, entry 0 not read;    */
                                /* NULL: a chain                                    */
   int tokens_ld;               /* >= n - 1 (chain), >= n (tree)                    */
-  int history_ld;              /* tokens per history row, >= 0                     */
+  int history_ld;              /* tokens per history row, 0..268,435,456           */
   const int* history;          /* [B, history_ld] prompt and generated tokens, or  */
                                /* NULL: empty                                      */
   const int* history_len;      /* [B] tokens of each history, 0..history_ld; NULL: */
@@ -84,7 +84,7 @@ typedef struct spec_process_args {
   const float* bias_values;    /* [B, bias_ld]                                     */
   const int* bias_len;         /* [B] entries of each list, 0..bias_ld; NULL:      */
                                /* bias_ld                                          */
-  int bias_ld;                 /* >= 0                                             */
+  int bias_ld;                 /* 0..268,435,456                                   */
   int mask_rows;               /* rows of mask, >= 1 when mask is given            */
   const unsigned* mask;        /* [mask_rows, mask_ld] words: bit v % 32 of word   */
                                /* v / 32 is 1 where v is allowed; NULL: no masks   */
