@@ -184,21 +184,13 @@ struct Lengths {
 };
 __device__ __forceinline__ Lengths lengths_of(const ProcessParams& P, int b, int& err) {
   Lengths n{0, 0, 0};
-  if (P.history) {
-    n.history = P.history_len ? __ldg(P.history_len + b) : P.history_ld;
-    if (n.history < 0 || n.history > P.history_ld) {
-      err |= SPEC_ERR_TOKEN;
-      n.history = n.history < 0 ? 0 : P.history_ld;
-    }
-    if (P.prompt_len) n.prompt = __ldg(P.prompt_len + b);
-  }
-  if (P.bias_tokens) {
-    n.bias = P.bias_len ? __ldg(P.bias_len + b) : P.bias_ld;
-    if (n.bias < 0 || n.bias > P.bias_ld) {
-      err |= SPEC_ERR_TOKEN;
-      n.bias = n.bias < 0 ? 0 : P.bias_ld;
-    }
-  }
+  const auto within = [&](int len, int most) {
+    if (len < 0 || len > most) err |= SPEC_ERR_TOKEN;
+    return min(max(len, 0), most);
+  };
+  n.history = within(P.history_len ? __ldg(P.history_len + b) : P.history_ld, P.history_ld);
+  if (P.prompt_len) n.prompt = __ldg(P.prompt_len + b);
+  n.bias = within(P.bias_len ? __ldg(P.bias_len + b) : P.bias_ld, P.bias_ld);
   return n;
 }
 
@@ -899,7 +891,7 @@ cudaError_t run_process(ProcessParams p, int nsm, cudaStream_t s) {
   // 500 tokens, 4M tokens read, 110 and 113 us; of 2000, 16M, 116 and 115; of
   // 8000, 65M, 137 and 124, and where most of them are frequent tokens 180 and
   // 130; 32 sequences of 4000, 8M, 35 and 43.
-  const int reads = (p.history ? p.history_ld : 0) + (p.bias_tokens ? p.bias_ld : 0);
+  const int reads = p.history_ld + p.bias_ld;
   p.slabs = slabs_of<T, 128, 2>(p.V, p.ld);
   if (static_cast<long long>(p.slabs) * p.B * reads <= (1LL << 24)) {
     // CTAs of 128 threads stream better (more of them overlap their phases),
@@ -963,17 +955,18 @@ extern "C" spec_status spec_process_logits(const spec_process_args* a, cudaStrea
   p.tokens = a->tokens;
   p.parent = a->parent;
   p.tokens_ld = a->tokens_ld;
-  p.history = a->history_ld > 0 ? a->history : nullptr;
-  p.history_ld = a->history_ld;
-  p.history_len = a->history_len;
-  p.prompt_len = a->prompt_len;
+  // (a list of width 0 may have no address, but has lengths; without a list they are not read)
+  p.history = history > 0 ? a->history : nullptr;
+  p.history_ld = history;
+  p.history_len = a->history || a->history_ld == 0 ? a->history_len : nullptr;
+  p.prompt_len = a->history ? a->prompt_len : nullptr;
   p.repetition = a->repetition;
   p.frequency = a->frequency;
   p.presence = a->presence;
-  p.bias_tokens = a->bias_ld > 0 ? a->bias_tokens : nullptr;
+  p.bias_tokens = biases > 0 ? a->bias_tokens : nullptr;
   p.bias_values = a->bias_values;
-  p.bias_len = a->bias_len;
-  p.bias_ld = a->bias_ld;
+  p.bias_len = a->bias_tokens || a->bias_ld == 0 ? a->bias_len : nullptr;
+  p.bias_ld = biases;
   p.mask = a->mask;
   p.mask_rows = a->mask_rows;
   p.mask_ld = a->mask_ld;

@@ -73,8 +73,9 @@ typedef struct spec_process_args {
   int history_ld;              /* tokens per history row, 0..268,435,456           */
   const int* history;          /* [B, history_ld] prompt and generated tokens, or  */
                                /* NULL: empty                                      */
-  const int* history_len;      /* [B] tokens of each history, 0..history_ld; NULL: */
-                               /* history_ld                                       */
+  const int* history_len;      /* [B] tokens of each history, 0..history_ld (0 for */
+                               /* a history of width 0, whose address may be NULL; */
+                               /* not read without a history); NULL: history_ld    */
   const int* prompt_len;       /* [B] leading history tokens that are the prompt   */
                                /* (clamped to the history); NULL: 0                */
   const float* repetition;     /* [B], > 0; NULL: 1                                */
@@ -82,8 +83,8 @@ typedef struct spec_process_args {
   const float* presence;       /* [B]; NULL: 0                                     */
   const int* bias_tokens;      /* [B, bias_ld], or NULL: no biases                 */
   const float* bias_values;    /* [B, bias_ld]                                     */
-  const int* bias_len;         /* [B] entries of each list, 0..bias_ld; NULL:      */
-                               /* bias_ld                                          */
+  const int* bias_len;         /* [B] entries of each list, 0..bias_ld (likewise); */
+                               /* NULL: bias_ld                                    */
   int bias_ld;                 /* 0..268,435,456                                   */
   int mask_rows;               /* rows of mask, >= 1 when mask is given            */
   const unsigned* mask;        /* [mask_rows, mask_ld] words: bit v % 32 of word   */

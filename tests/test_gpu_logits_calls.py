@@ -98,3 +98,26 @@ def test_product_of_matrices_that_start_and_end_anywhere(cuda_device, V, group, 
                 T.check_product(out["logits"], x, codes, scales, z, group)
                 first = out["logits"]
             assert torch.equal(out["logits"], first)
+
+
+@pytest.mark.parametrize("addressed", [False, True])
+def test_process_lengths_beyond_lists_of_width_zero(cuda_device, addressed):
+    """A length of a list that holds nothing is out of its range too, whether or not the list has an address."""
+    import draft_verification_gb300 as dv
+    rng = np.random.default_rng(31)
+    B, n, V = 4, 3, 500
+    x = torch.from_numpy(rng.normal(0, 3, (B, n, V)).astype(np.float32)).to(cuda_device)
+    w = dict(tokens=rng.integers(0, V, (B, n), dtype=np.int32), history=np.zeros((B, 0), np.int32),
+             history_len=np.array([0, 1, -1, 0], np.int32), prompt_len=np.zeros(B, np.int32),
+             bias_tokens=np.zeros((B, 0), np.int32), bias_values=np.zeros((B, 0), np.float32),
+             bias_len=np.array([0, 0, 0, 2], np.int32), frequency=np.full(B, 0.5, np.float32))
+    kw = {k: T.dev(v, cuda_device) for k, v in w.items()}
+    if addressed:
+        for k in ("history", "bias_tokens", "bias_values"):
+            kw[k] = torch.ones((B, 4), dtype=kw[k].dtype, device=cuda_device)[:, :0]
+    out = dv.ProcessLogitsPlan(x, kw.pop("tokens"), **kw).run()
+    T.check_process(x, out, w)
+    assert out["seq_error"].tolist() == [0, 1, 1, 1]
+    # without the lists at all their lengths do not exist
+    out = dv.ProcessLogitsPlan(x, T.dev(w["tokens"], cuda_device), frequency=kw["frequency"]).run()
+    assert out["seq_error"].tolist() == [0, 0, 0, 0]
