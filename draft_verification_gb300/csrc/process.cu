@@ -496,9 +496,10 @@ __global__ void __launch_bounds__(kThreads, resident_threads(kListed) / kThreads
   int* s_tok = reinterpret_cast<int*>(proc_dyn + 2 * S::kTileBytes);     // [n]
   int* s_par = s_tok + P.n;                                              // [n]
   int* s_mask = s_par + P.n;                                             // [n]
-  // listed: the first kCache entries, as they apply to every row: what is added,
-  // and the place in the table with two flags (bit 14: repetition; bit 15:
-  // drafted, so that the row matters and the entry is read again)
+  // listed: the first kCache entries, as they apply to every row: what is added
+  // (a penalty's negative or a bias), and the place in the table with two flags
+  // (bit 14: repetition; bit 15: the entry is read again, because it is drafted,
+  // so that the row matters, or has both a penalty and a bias)
   float* c_add = reinterpret_cast<float*>(s_mask + P.n);
   unsigned short* c_place = reinterpret_cast<unsigned short*>(c_add + S::kCache);
   // else: the table, two bitmaps and the list of touched tokens
@@ -618,10 +619,10 @@ __global__ void __launch_bounds__(kThreads, resident_threads(kListed) / kThreads
   const float inv = __frcp_rn(rep);
   const float freq = P.frequency ? __ldg(P.frequency + b) : 0.f;
   const float pres = P.presence ? __ldg(P.presence + b) : 0.f;
-  // what a word and a bias add to an element after its repetition penalty
-  const auto added = [&](unsigned c, float plus) {
+  // the penalty of a word's occurrences (one rounding for both terms)
+  const auto penalty = [&](unsigned c) {
     const unsigned made = c & kMade;
-    return made ? __fsub_rn(plus, __fmaf_rn(freq, static_cast<float>(made), pres)) : plus;
+    return made ? __fmaf_rn(freq, static_cast<float>(made), pres) : 0.f;
   };
   int e0 = 0, tokens;  // listed: the entries' first, in the workspace
   if constexpr (kListed) {
@@ -635,10 +636,13 @@ __global__ void __launch_bounds__(kThreads, resident_threads(kListed) / kThreads
     for (int e = tid; e < min(tokens, S::kCache); e += kThreads) {
       const int at = __ldcg(P.entry_token + src + e) - lo;
       const unsigned c = __ldcg(P.entry_count + src + e);
-      c_add[e] = added(c, __ldcg(P.entry_bias + src + e));
+      const float minus = penalty(c), plus = __ldcg(P.entry_bias + src + e);
+      // (a penalty and a bias are two additions: such entries are read again)
+      const bool both = minus != 0.f && plus != 0.f;
+      c_add[e] = minus != 0.f ? -minus : plus;
       // (places beyond the table: tokens of the slab before that no row takes)
       c_place[e] = static_cast<unsigned short>((at < 0 ? 0x3fff : at) | (c & (kInPrompt | kMade) ? 0x4000 : 0) |
-                                               (c & kDrafted ? 0x8000 : 0));
+                                               (c & kDrafted || both ? 0x8000 : 0));
     }
     __syncthreads();
   } else {
@@ -673,13 +677,12 @@ __global__ void __launch_bounds__(kThreads, resident_threads(kListed) / kThreads
   // now and stays.)
   const auto rewrite = [&](int i, int e, T* part, int m) {
     int at;
-    unsigned c = 0;
-    float add = 0.f;
+    float first = 0.f, plus = 0.f;  // what is added: the penalty's negative, then the bias
     bool seen, again = true;
     if constexpr (kListed) {
       if (e < S::kCache) {
         at = c_place[e];
-        add = c_add[e];
+        first = c_add[e];
         seen = at & 0x4000;
         again = at & 0x8000;
         at &= 0x3fff;
@@ -693,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, resident_threads(kListed) / kThreads
     const int place = at - (E - 1) + m;
     if (place < 0 || place >= S::kTokens) return;
     if (again) {
-      float plus;
+      unsigned c;
       if constexpr (kListed) {
         const long long src = static_cast<long long>(b) * P.capacity + e0 + e;
         c = __ldcg(P.entry_count + src);
@@ -711,14 +714,15 @@ __global__ void __launch_bounds__(kThreads, resident_threads(kListed) / kThreads
         }
       }
       seen = c & (kInPrompt | kMade);
-      add = added(c, plus);
+      first = -penalty(c);
     }
-    if (!seen && add == 0.f) return;
+    if (!seen && first == 0.f && plus == 0.f) return;
     const uint32_t x = load_bits(part + place);
     if (x == L::kNegInf) return;
     float y = L::widen(x);
     if (seen) y = __fmul_rn(y, y > 0.f ? inv : rep);
-    if (add != 0.f) y = __fadd_rn(y, add);
+    if (first != 0.f) y = __fadd_rn(y, first);
+    if (plus != 0.f) y = __fadd_rn(y, plus);
     store_bits(part + place, L::round(y));
   };
 

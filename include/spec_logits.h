@@ -40,7 +40,8 @@ extern "C" {
 /*    x2 = x1 - (frequency * c + (c > 0 ? presence : 0))                   */
 /*    x3 = x2 + the sum of b's bias entries for v, in their order          */
 /*    y  = allowed ? x3 : -inf                                             */
-/* in float32, rounded once to the logits' type; an element that nothing   */
+/* in float32, a rounding per operation (the penalty's product and sum are  */
+/* one), rounded once more to the logits' type; an element that nothing    */
 /* applies to keeps its bits, and -inf stays -inf.  A masked element is    */
 /* -inf whatever it held (NaN included); a row whose mask allows nothing   */
 /* is all -inf, which the verification reports as SPEC_ERR_NONFINITE.      */

@@ -121,3 +121,64 @@ def test_process_lengths_beyond_lists_of_width_zero(cuda_device, addressed):
     # without the lists at all their lengths do not exist
     out = dv.ProcessLogitsPlan(x, T.dev(w["tokens"], cuda_device), frequency=kw["frequency"]).run()
     assert out["seq_error"].tolist() == [0, 0, 0, 0]
+
+
+@pytest.mark.parametrize("B,n,V,H", [(3, 3, 2000, 60), (128, 2, 66000, 9000)])  # one kernel, and gathered first
+def test_process_takes_the_stated_float32_steps(cuda_device, B, n, V, H):
+    """Bit by bit."""
+    f = np.float32
+    rng = np.random.default_rng(32)
+    K = 60
+    w = dict(tokens=rng.integers(0, V, (B, n), dtype=np.int32), history=rng.integers(0, V, (B, H), dtype=np.int32),
+             prompt_len=np.full(B, H // 3, np.int32), repetition=rng.uniform(0.7, 1.6, B).astype(f),
+             frequency=np.full(B, 0.5, f), presence=np.full(B, 0.25, f),
+             bias_tokens=np.stack([rng.permutation(V)[:K] for _ in range(B)]).astype(np.int32),
+             bias_values=(rng.choice([1e-9, 1.0, -3e38, 3e38], (B, K)) * rng.uniform(0.5, 1.0, (B, K))).astype(f))
+    # half of the biased tokens occur, some of them drafted
+    w["bias_tokens"][:, ::2] = w["history"][:, -(K // 2):]
+    w["tokens"][:, 0] = w["bias_tokens"][:, 2]
+    x = rng.choice([0.75, 1.25, -0.75, 2.0, 3e38, -3e38], (B, n, V)).astype(f)
+    want = np.empty_like(x)
+    for b in range(B):
+        made0 = np.bincount(w["history"][b, H // 3:], minlength=V)
+        seen0 = np.bincount(w["history"][b], minlength=V) > 0
+        bias = np.zeros(V, f)
+        for t, v in zip(w["bias_tokens"][b], w["bias_values"][b]):
+            with np.errstate(over="ignore"):
+                bias[t] = f(bias[t] + v)  # in their order
+        rho = w["repetition"][b]
+        inv = f(1) / rho
+        for i in range(n):
+            path = np.bincount(w["tokens"][b, :i], minlength=V)
+            made, seen = made0 + path, seen0 | (path > 0)
+            with np.errstate(over="ignore"):
+                x1 = np.where(seen, x[b, i] * np.where(x[b, i] > 0, inv, rho), x[b, i])
+                x2 = np.where(made > 0, x1 - (0.5 * made + 0.25).astype(f), x1)  # (exact: small multiples of 1/4)
+                want[b, i] = np.where(bias != 0, x2 + bias, x2)
+    assert want.dtype == f
+    out = T.run_process(T.dev(x, cuda_device), w, cuda_device)
+    assert out["seq_error"].abs().sum() == 0
+    assert np.array_equal(out["logits"].cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("B,n,V,H", [(2, 3, 2000, 60), (128, 2, 66000, 9000)])  # one kernel, and gathered first
+def test_process_subtracts_the_penalty_before_it_adds_the_bias(cuda_device, B, n, V, H):
+    """An element that the penalty cancels keeps a small bias; one that it takes past float32's end stays there."""
+    f = np.float32
+    history = np.full((B, H), 3, np.int32)
+    history[:, 0], history[:, H // 2], history[:, H - 1] = 5, 7, V - 1
+    w = dict(tokens=np.full((B, n), 11, np.int32), history=history,
+             presence=np.where(np.arange(B) % 2, f(-3e38), f(0.75)).astype(f),
+             bias_tokens=np.tile(np.array([5, 7, 11, V - 1], np.int32), (B, 1)),
+             bias_values=np.where(np.arange(B)[:, None] % 2, f(-3e38), f(1e-9)).repeat(4, 1).astype(f))
+    x = np.where(np.arange(B)[:, None, None] % 2, f(3e38), f(0.75)) * np.ones((B, n, V), f)
+    want = x.copy()
+    for b in range(B):
+        for i in range(n):
+            for t in (3, 5, 7, V - 1) + ((11,) if i else ()):
+                want[b, i, t] = np.inf if b % 2 else 0.0
+            for t in (5, 7, 11, V - 1):
+                with np.errstate(over="ignore"):
+                    want[b, i, t] = f(want[b, i, t] + w["bias_values"][b, 0])
+    out = T.run_process(T.dev(x, cuda_device), w, cuda_device)
+    assert np.array_equal(out["logits"].cpu().numpy(), want)
