@@ -13,5 +13,7 @@ from .api import (  # noqa: F401
 from .logits import (  # noqa: F401
     Int4ProductPlan, ProcessLogitsPlan, QuantizeInt4Plan, int4_product, process_logits, quantize_int4,
 )
-from ._lib import ERR_MASK, ERR_NONFINITE, ERR_PARENT, ERR_TOKEN, ERR_WINDOW, ERR_ZERO_MASS  # noqa: F401
+from ._lib import (  # noqa: F401
+    ERR_INTERNAL, ERR_MASK, ERR_NONFINITE, ERR_PARENT, ERR_TOKEN, ERR_WINDOW, ERR_ZERO_MASS,
+)
 from .build import build as build_library, lib_path  # noqa: F401

@@ -24,6 +24,9 @@ from . import _lib as L
 from .api import _DTYPES, _Plan, _f32, _finish, _i32, _ptr, _to_device
 
 
+COUNTER_BYTES = 1024  # of a product's workspace: what has to be zero before a run
+
+
 def _logit_rows(t: torch.Tensor, name: str) -> int:
     """Row stride (elements) of a [B, n, V] view whose rows are evenly strided."""
     if t.dim() != 3:
@@ -197,7 +200,10 @@ class Int4ProductPlan(_Plan):
     x bfloat16 [R, d] (or [B, n, d]), codes, scales and zeros as
     quantize_int4 returns them (rows of codes and x may be padded).  A workspace
     that the caller passes must hold zeros before its first use.  ``run()``
-    returns logits [R, V] (or [B, n, V]) of out_dtype and error_word."""
+    returns logits [R, V] (or [B, n, V]) of out_dtype and error_word.  After a
+    run that set ERR_INTERNAL in error_word (a bounded wait gave up), call
+    ``reset()`` before the next: the run may have left counts of half-summed
+    tiles in the workspace."""
 
     def __init__(self, x, codes, scales, zeros=None, *, group=128, out_dtype=torch.bfloat16, out=None,
                  workspace=None):
@@ -246,6 +252,13 @@ class Int4ProductPlan(_Plan):
         a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel()
         self.args = a
         self._call = lib.spec_int4_product
+
+    def reset(self, stream=None):
+        """Clear the workspace's counters and error_word, on the run's stream
+        (None: the current one)."""
+        with torch.cuda.stream(stream):
+            self.workspace.view(torch.uint8)[:COUNTER_BYTES].zero_()
+            self.out["error_word"].zero_()
 
 
 @contextlib.contextmanager

@@ -182,3 +182,28 @@ def test_process_subtracts_the_penalty_before_it_adds_the_bias(cuda_device, B, n
                     want[b, i, t] = f(want[b, i, t] + w["bias_values"][b, 0])
     out = T.run_process(T.dev(x, cuda_device), w, cuda_device)
     assert np.array_equal(out["logits"].cpu().numpy(), want)
+
+
+def test_product_reset_clears_what_a_given_up_run_leaves(cuda_device):
+    """Counters that a run which gave up would leave (planted: some tiles counted once) are gone after reset(), on
+    the stream it is given; so is the error word."""
+    import draft_verification_gb300 as dv
+    R, V, d, group = 5, 1000, 8192, 128  # every tile is shared by CTAs
+    x, codes, scales, z = T.make_product(R, V, d, group, True, 41, cuda_device)
+    need = dv.Int4ProductPlan(x, codes, scales, z, group=group).workspace.numel()
+    for workspace in (None, torch.zeros(need, dtype=torch.uint8, device=cuda_device)):
+        plan = dv.Int4ProductPlan(x, codes, scales, z, group=group, out_dtype=torch.float32, workspace=workspace)
+        first = plan.run()["logits"].clone()
+        T.check_product(first, x, codes, scales, z, group)
+        for stream in (None, torch.cuda.Stream()):
+            plan.workspace[:1024].view(torch.int32)[::3] = 1
+            plan.out["error_word"].fill_(dv.ERR_INTERNAL)
+            plan.out["logits"].fill_(7.0)
+            if stream is not None:
+                stream.wait_stream(torch.cuda.current_stream())
+            plan.reset(stream)
+            out = plan.run(stream)
+            torch.cuda.synchronize()
+            assert int(out["error_word"]) == 0
+            assert torch.equal(out["logits"], first)
+        assert not plan.workspace[:1024].any()
