@@ -240,7 +240,8 @@ class Int4ProductPlan(_Plan):
         out_ld = _logit_rows(out, "out") if out.dim() == 3 else _matrix_ld(out, "out")
         _on(dev, codes=codes, scales=scales, zeros=zeros, out=out)
         if workspace is None:
-            workspace = torch.zeros(need, dtype=torch.uint8, device=dev)
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace[:COUNTER_BYTES].zero_()
         self.workspace = workspace
         self.keep = [x, codes, scales, zeros]
         self.out = dict(logits=out, error_word=torch.zeros(1, dtype=torch.int32, device=dev))
