@@ -62,7 +62,27 @@ def _matrix_ld(t: torch.Tensor, name: str) -> int:
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
-class ProcessLogitsPlan(_Plan):
+class _DevicePlan(_Plan):
+    """A plan that runs on the GPU's tensors only (a host address never reaches a kernel)."""
+
+    def _bind(self, call, dev):
+        self._call, self._dev = call, dev
+        if dev.type != "cuda":
+            self.run = self._refuse
+
+    def _refuse(self, stream=None):
+        raise ValueError(f"{type(self).__name__}: bound to tensors on {self._dev}, CUDA tensors required")
+
+
+def _workspace(t, dev):
+    """A caller's workspace, and its bytes."""
+    _on(dev, workspace=t)
+    if not t.is_contiguous():
+        raise ValueError("workspace: expected a contiguous tensor")
+    return t.numel() * t.element_size()
+
+
+class ProcessLogitsPlan(_DevicePlan):
     """Per-request processing of logits bound to fixed buffers.  See
     spec_process_logits.
 
@@ -156,12 +176,12 @@ class ProcessLogitsPlan(_Plan):
         a.mask, a.mask_index = _ptr(mask), _ptr(_i32(mask_index, "mask_index"))
         a.mask_rows, a.mask_ld = (0, 0) if mask is None else (mask.shape[0], mask_ld)
         a.seq_error, a.error_word = _ptr(self.out["seq_error"]), _ptr(self.out["error_word"])
-        a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel()
+        a.workspace, a.workspace_bytes = _ptr(workspace), _workspace(workspace, dev)
         self.args = a
-        self._call = lib.spec_process_logits
+        self._bind(lib.spec_process_logits, dev)
 
 
-class QuantizeInt4Plan(_Plan):
+class QuantizeInt4Plan(_DevicePlan):
     """4-bit quantisation with group scales bound to fixed buffers.  See
     spec_quantize_int4.
 
@@ -190,10 +210,10 @@ class QuantizeInt4Plan(_Plan):
         a.weights, a.codes, a.scales = _ptr(weights), _ptr(self.out["codes"]), _ptr(self.out["scales"])
         a.zeros = _ptr(self.out.get("zeros"))
         self.args = a
-        self._call = lib.spec_quantize_int4
+        self._bind(lib.spec_quantize_int4, dev)
 
 
-class Int4ProductPlan(_Plan):
+class Int4ProductPlan(_DevicePlan):
     """Products of a few rows with a 4-bit matrix bound to fixed buffers.  See
     spec_int4_product.
 
@@ -250,9 +270,9 @@ class Int4ProductPlan(_Plan):
         a.x_ld, a.codes_ld, a.scales_ld, a.zeros_ld, a.out_ld = x_ld, codes_ld, scales_ld, zeros_ld, out_ld
         a.x, a.codes, a.scales, a.zeros, a.out = _ptr(x), _ptr(codes), _ptr(scales), _ptr(zeros), _ptr(out)
         a.error_word = _ptr(self.out["error_word"])
-        a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel()
+        a.workspace, a.workspace_bytes = _ptr(workspace), _workspace(workspace, dev)
         self.args = a
-        self._call = lib.spec_int4_product
+        self._bind(lib.spec_int4_product, dev)
 
     def reset(self, stream=None):
         """Clear the workspace's counters and error_word, on the run's stream

@@ -26,3 +26,27 @@ def test_product_plan_clears_its_counters_alone(lib, monkeypatch):
     assert sum(t.numel() * t.element_size() for t in cleared) <= 1024
     assert plan.workspace.numel() > 1 << 20
     assert not plan.workspace[:1024].any() and bool((plan.workspace[1024:] == 1).all())
+
+
+def plans():
+    import draft_verification_gb300 as dv
+    return [lambda **k: dv.ProcessLogitsPlan(torch.zeros(2, 3, 50), **k),
+            lambda **k: dv.Int4ProductPlan(*product_tensors(), group=64, **k),
+            lambda **k: dv.QuantizeInt4Plan(torch.zeros(50, 128), **k)]
+
+
+def test_plans_of_host_tensors_launch_nothing(lib):
+    for make in plans():
+        with pytest.raises(ValueError, match="CUDA tensors"):
+            make().run()
+
+
+def test_plans_check_their_workspace(lib):
+    for make in plans()[:2]:
+        need = make().workspace.numel()
+        for elsewhere in (torch.zeros(need, dtype=torch.uint8, device="meta"),
+                          torch.zeros(2 * need, dtype=torch.uint8)[::2]):
+            with pytest.raises(ValueError):
+                make(workspace=elsewhere)
+        # counted in bytes, whatever the elements
+        assert make(workspace=torch.zeros((need + 7) // 8, dtype=torch.int64)).args.workspace_bytes >= need
