@@ -95,7 +95,8 @@ class ProcessLogitsPlan(_DevicePlan):
     v % 32 of word v // 32 set where token v is allowed, mask_index int32
     [B, n] (-1: not masked; None: row (b, i) uses mask row b * n + i).  out:
     a [B, n, V] tensor of the same type, ``logits`` itself to work in place,
-    or None: allocated with logits' row stride.
+    or None: allocated with logits' row stride, or where that is twice a row or
+    more, with the least one of the same remainder by 16 bytes.
 
     ``run()`` returns logits (out), seq_error int32 [B] and error_word."""
 
@@ -106,7 +107,10 @@ class ProcessLogitsPlan(_DevicePlan):
         B, n, V = logits.shape
         dev = logits.device
         if out is None:
-            out = torch.empty((B, n, ld), dtype=logits.dtype, device=dev)[:, :, :V]
+            # (rows of one position of many, or of a wider matrix: not the memory between them as well, but a
+            # stride after which rows start at the same place of a 16-byte vector, so that whole vectors are stored)
+            width = ld if ld < 2 * V else V + (ld - V) % (16 // logits.element_size())
+            out = torch.empty((B, n, width), dtype=logits.dtype, device=dev)[:, :, :V]
         if out.dtype != logits.dtype:
             raise TypeError("out: the type of logits required")
         _shape(out, (B, n, V), "out")

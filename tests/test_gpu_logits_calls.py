@@ -207,3 +207,16 @@ def test_product_reset_clears_what_a_given_up_run_leaves(cuda_device):
             assert int(out["error_word"]) == 0
             assert torch.equal(out["logits"], first)
         assert not plan.workspace[:1024].any()
+
+
+def test_process_one_position_of_many(cuda_device):
+    """Rows that lie far apart: the output's are close, and the same."""
+    rng = np.random.default_rng(42)
+    for V, dtype in ((5000, torch.bfloat16), (5001, torch.float32)):
+        B = 6
+        w = T.make_process(rng, B, 1, V, H=100, density=0.5)
+        x = torch.from_numpy(rng.normal(0, 3, (B, 9, V)).astype(np.float32)).to(cuda_device, dtype)
+        rows = x[:, :1]
+        out = T.run_process(rows, w, cuda_device)
+        assert out["logits"].untyped_storage().nbytes() < 2 * B * V * dtype.itemsize
+        T.check_process(rows.contiguous(), out, w)

@@ -50,3 +50,21 @@ def test_plans_check_their_workspace(lib):
                 make(workspace=elsewhere)
         # counted in bytes, whatever the elements
         assert make(workspace=torch.zeros((need + 7) // 8, dtype=torch.int64)).args.workspace_bytes >= need
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [50, 56, 1001])
+def test_process_plan_allocates_what_its_rows_need(lib, dtype, V):
+    """One position of many, and columns of a wider matrix: the output takes rows, not the memory between them."""
+    from draft_verification_gb300 import ProcessLogitsPlan
+    E = 16 // dtype.itemsize
+    wide = torch.zeros(4, 9, V, dtype=dtype)
+    for logits in (wide[:, :1], wide[:, 8:], torch.zeros(4, 3, 5 * V + 3, dtype=dtype)[:, :, :V]):
+        plan = ProcessLogitsPlan(logits)
+        out = plan.out["logits"]
+        assert out.shape == logits.shape and out.stride(2) == 1
+        assert out.untyped_storage().nbytes() <= logits.shape[0] * logits.shape[1] * (V + E - 1) * dtype.itemsize
+        assert (plan.args.out_ld - plan.args.ld) % E == 0 and plan.args.out_ld >= V  # rows start alike
+    # ordinary rows keep their stride, as a verification of both sides' rows wants it
+    for logits in (wide, torch.zeros(4, 3, V + 5, dtype=dtype)[:, :, :V]):
+        assert ProcessLogitsPlan(logits).out["logits"].stride() == logits.stride()
