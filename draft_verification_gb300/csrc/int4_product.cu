@@ -823,16 +823,22 @@ __global__ void __launch_bounds__(Shape<N, G>::kThreads, 1)
 // ---------------------------------------------------------------------------
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-bool good_shape(int R, int V, int d, int group) {
-  return R >= 1 && R <= 65535 && V >= 1 && V <= 2097152 && (group == 32 || group == 64 || group == 128) && d >= 32 &&
-         d <= 65536 && d % group == 0;
-}
-
 // MMA N: the rows of a block, rounded up to a width that has a kernel.  (The
 // narrowest that fits: with 128256 x 4096 weights in groups of 128, evenly
 // divided, the widths take 66, 74, 85 and 122 us whatever part of their rows is
 // used.)
 int rows_tile(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128; }
+
+// the units of all row blocks
+long long units_of(int R, int V, int d) {
+  const int N = rows_tile(R);
+  return static_cast<long long>((R + N - 1) / N) * ((V + kTileV - 1) / kTileV) * ((d + kStageK - 1) / kStageK);
+}
+
+bool good_shape(int R, int V, int d, int group) {
+  return R >= 1 && R <= 65535 && V >= 1 && V <= 2097152 && (group == 32 || group == 64 || group == 128) && d >= 32 &&
+         d <= 65536 && d % group == 0 && units_of(R, V, d) < 1LL << 30;
+}
 
 size_t product_workspace(int R) {
   return kCounterBytes + static_cast<size_t>(2) * kMaxCtas * rows_tile(R) * kTileV * sizeof(float);
@@ -888,9 +894,7 @@ spec_status launch_product(const spec_int4_product_args& a, cudaStream_t s) {
   P.d = a.d;
   P.ntv = (a.V + kTileV - 1) / kTileV;
   P.nk = (a.d + kStageK - 1) / kStageK;
-  const long long units = static_cast<long long>((a.R + N - 1) / N) * P.ntv * P.nk;
-  if (units > 0x3fffffff) return SPEC_EINVAL;
-  P.units = static_cast<int>(units);
+  P.units = static_cast<int>(units_of(a.R, a.V, a.d));
   P.scales_ld = a.scales_ld;
   P.zeros_ld = a.zeros_ld;
   P.out_ld = a.out_ld;

@@ -190,9 +190,11 @@ typedef struct spec_int4_product_args {
   size_t workspace_bytes;
 } spec_int4_product_args;
 
-/* 0 for sizes outside the limits above.                                      */
+/* 0 for sizes outside the limits above, and where                            */
+/* ceil(R / 128) * ceil(V / 128) * ceil(d / 256) reaches 2^30.                */
 size_t spec_int4_product_workspace_size(int R, int V, int d, int group);
-/* SPEC_EINVAL, SPEC_EDTYPE, SPEC_EALIGN, SPEC_EWORKSPACE, SPEC_ECUDA.        */
+/* SPEC_EINVAL (all sizes for which that is 0), SPEC_EDTYPE, SPEC_EALIGN,     */
+/* SPEC_EWORKSPACE, SPEC_ECUDA.                                               */
 spec_status spec_int4_product(const spec_int4_product_args* args, cudaStream_t stream);
 
 #ifdef __cplusplus

@@ -25,3 +25,15 @@ def test_process_lists_end_where_counts_and_positions_fit(lib, name):
     assert size(*sizes(LIST + 1)) == 0 and size(*sizes((1 << 31) - 1)) == 0
     # one step further: the list is accepted, and the next refusal (a workspace that is too small) is reached
     assert lib.spec_process_logits(C.byref(A._process(**{name: LIST, "workspace_bytes": 1})), None) == -4
+
+
+def test_product_sizes_end_where_its_units_can_be_counted(lib):
+    # 2^30 units of 128 rows x 128 entries x 256 columns: refused, which the query says as well
+    size = lib.spec_int4_product_workspace_size
+    most = dict(V=2097152, d=65536, group=128, codes_ld=32768, x_ld=65536, scales_ld=2097152, zeros_ld=2097152,
+                out_ld=2097152)
+    assert size(255 * 128, 2097152, 65536, 128) > 0
+    for R in (255 * 128 + 1, 256 * 128, 65535):
+        assert size(R, 2097152, 65536, 128) == 0
+        assert lib.spec_int4_product(C.byref(A._product(R=R, **most)), None) == -1
+    assert size(65535, 1048576, 65536, 128) == 0 and size(65535, 1048448, 65536, 128) > 0
