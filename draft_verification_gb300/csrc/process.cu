@@ -18,8 +18,8 @@
 //  - Most calls build a slab's entries in the same kernel, as a table of the
 //    slab in shared memory, from the whole history, which is read while the
 //    first row's vectors are in flight.
-//  - Where the slabs would read too much history between them (long histories
-//    of many sequences over a large vocabulary), collect_kernel gathers each
+//  - Where that would have every SM read histories again and again (long ones of
+//    many sequences over a large vocabulary), collect_kernel gathers each
 //    sequence's distinct tokens once and writes their entries in ascending
 //    order to the workspace; the slabs' CTAs (launched dependent: their first
 //    vectors are in flight meanwhile) read a few hundred entries each.
@@ -478,10 +478,10 @@ struct Slab {
   }
 };
 
-// Threads an SM holds: as many as leave the kernel its registers (56, and 40
-// with listed entries).  Without the list, 128 sequences of 9 rows of 128256
-// tokens: 1024 threads 108 us, 1152 103, 1280 107; 16 trees of 64 rows of 50257:
-// 51, 52, 68.
+// Threads an SM holds: as many as leave the kernel its registers (56; with listed
+// entries 40, of which up to two are spilled).  Without the list, 128 sequences
+// of 9 rows of 128256 tokens: 1024 threads 108 us, 1152 103, 1280 107; 16 trees of
+// 64 rows of 50257: 51, 52, 68.
 __host__ __device__ constexpr int resident_threads(bool listed) { return listed ? 1536 : 1152; }
 
 template <typename T, int kThreads, int kVecs, bool kListed, bool kAligned>
@@ -813,7 +813,12 @@ int slabs_of(int V, long long ld) {
 }
 
 // Rows that a CTA takes: few sequences and slabs have a sequence's rows split
-// as well, into one round of CTAs.
+// as well, into as many CTAs as the registers have room for.  (With biases the
+// tables' shared memory has room for fewer: 3 of 256 threads instead of 4, 7 of
+// 128 instead of 9, and the rest run in a second round.  Split by that as well:
+// 32 sequences of 9 rows of 32000, 2048 tokens and 300 biases, 22.5 to 20.1 us
+// where tokens are uniform, 19.7 to 25.0 where frequent ones share a slab; one
+// sequence of 1024 rows of 700 67 to 94, 16 of 1024 rows of 32000 5.8 ms to 8.9.)
 template <typename T, int kThreads, int kVecs, bool kListed>
 int rows_of(const ProcessParams& p, int nsm) {
   const long long have = static_cast<long long>(slabs_of<T, kThreads, kVecs>(p.V, p.ld)) * p.B;
@@ -887,24 +892,48 @@ cudaError_t launch_collect(ProcessParams p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+// CTAs of the one-kernel form
+template <typename T, int kThreads, int kVecs>
+long long ctas_of(const ProcessParams& p, int nsm) {
+  const int rows = rows_of<T, kThreads, kVecs, false>(p, nsm);
+  return static_cast<long long>(slabs_of<T, kThreads, kVecs>(p.V, p.ld)) * p.B * ((p.n + rows - 1) / rows);
+}
+
 template <typename T>
 cudaError_t run_process(ProcessParams p, int nsm, cudaStream_t s) {
-  // One kernel or two: the one kernel's slabs each read the whole history; the
-  // second launch and the entries' way through the workspace cost 5 to 8 us.
-  // Measured (bfloat16, 9 rows, V = 128256; one kernel, two): 128 sequences of
-  // 500 tokens, 4M tokens read, 110 and 113 us; of 2000, 16M, 116 and 115; of
-  // 8000, 65M, 137 and 124, and where most of them are frequent tokens 180 and
-  // 130; 32 sequences of 4000, 8M, 35 and 43.
+  // (Here the host knows the buffers' widths, not the lists' lengths.)
   const int reads = p.history_ld + p.bias_ld;
+  // The form for one kernel: CTAs of 128 threads stream better (more of them
+  // overlap their phases), those of 256 get through a history sooner and read it
+  // half as often: worth it where reading comes to 400 tokens per row or more.
+  // Measured (bfloat16, 9 rows; 128 and 256 threads): V = 32000, 32 sequences of
+  // 200 tokens, 40 per row, 9.4 and 10.2 us; 2000, 400, 12.0 and 11.5; 8000,
+  // 1600, 24.9 and 20.1; V = 128256, 128 sequences of 500, 56 per row, 110 and 112.
+  const bool wide = reads > 400LL * rows_of<T, 128, 2, false>(p, nsm);
+  // One kernel or two.  With one, every CTA of a sequence (a slab and some of the
+  // rows) goes through the whole history.  With two, one CTA per sequence goes
+  // through it alone, once per range to mark its tokens and once per window of
+  // them; the second launch and the entries' way through the workspace cost 5 to
+  // 8 us.  So two are worth it where there is much to read (16M tokens by all
+  // slabs) and an SM reads 1.3 times as much or more with one.
+  // Measured (bfloat16, tokens uniform and mostly frequent ones; one kernel, two):
+  //   much to read or not, 9 rows, V = 128256: 128 sequences of 500 tokens (4M)
+  //     110 and 113 us; of 2000 (16M) 111 and 110; of 8192 (66M) 138 and 118, 132
+  //     and 116; 64 of 8192 (33M) 77 and 71; 32 of 8192 (16M) 43 and 47
+  //   an SM's reading with one over that with two, from 16M on: 1 row, V = 128256,
+  //     128 sequences of 32768 (4.5) 151 and 81, 134 and 65; 9 rows, V = 32000, 128
+  //     of 131072 (1.35) 330 and 324, 290 and 278; of 32768 (1.35) 128 and 137, 106
+  //     and 118; V = 128256, 32 of 32768 (1.1) 82 and 101, 81 and 117; 64 of 131072
+  //     (0.8) 413 and 557, 340 and 374; 16 of 32768 (0.6) 49 and 84, 76 and 113; 4
+  //     of 131072 (0.15) 91 and 421, 147 and 292.
   p.slabs = slabs_of<T, 128, 2>(p.V, p.ld);
-  if (static_cast<long long>(p.slabs) * p.B * reads <= (1LL << 24)) {
-    // CTAs of 128 threads stream better (more of them overlap their phases),
-    // those of 256 get through a history sooner and read it half as often: worth
-    // it where reading comes to 400 tokens per row or more.  Measured (bfloat16,
-    // 9 rows; 128 and 256 threads): V = 32000, 32 sequences of 200 tokens, 40 per
-    // row, 9.4 and 10.2 us; 2000, 400, 12.0 and 11.5; 8000, 1600, 24.9 and 20.1;
-    // V = 128256, 128 sequences of 500, 56 per row, 110 and 112.
-    if (reads > 400LL * rows_of<T, 128, 2, false>(p, nsm)) return launch_process<T, 256, 2, false>(p, nsm, s);
+  const bool much = static_cast<long long>(p.slabs) * p.B * reads > (1LL << 24);
+  const long long ctas = wide ? ctas_of<T, 256, 2>(p, nsm) : ctas_of<T, 128, 2>(p, nsm);
+  const int ranges = (p.V + 32 * kRangeWords - 1) / (32 * kRangeWords);
+  const long long passes = 2 * ranges - 1 + (p.capacity + kWindow - 1) / kWindow;
+  const int rounds = (p.B + nsm - 1) / nsm;  // of collecting CTAs, taken as one per SM
+  if (!much || 10 * ctas < 13 * passes * rounds * nsm) {
+    if (wide) return launch_process<T, 256, 2, false>(p, nsm, s);
     return launch_process<T, 128, 2, false>(p, nsm, s);
   }
   using Listed = Slab<T, 128, 2, true>;

@@ -220,3 +220,56 @@ def test_process_one_position_of_many(cuda_device):
         out = T.run_process(rows, w, cuda_device)
         assert out["logits"].untyped_storage().nbytes() < 2 * B * V * dtype.itemsize
         T.check_process(rows.contiguous(), out, w)
+
+
+GATHERED = [  # many sequences with long lists: their entries are gathered first
+    # B, n, V, pad, dtype, tokens below, kwargs
+    (150, 2, 20000, 0, "bf16", None, dict(H=12000, bias=10, density=0.8)),
+    (150, 2, 20001, 0, "bf16", None, dict(H=12002, bias=10)),
+    # more distinct tokens than one window holds, and more than 1024 entries in a slab, from one slab and from two
+    (150, 2, 66000, 0, "bf16", None, dict(H=20000, bias=500)),
+    (150, 2, 66000, 0, "bf16", 5000, dict(H=20000, bias=30, density=0.6)),
+    (150, 1, 66001, 3, "f32", 5000, dict(H=20001, bias=9)),
+    (150, 3, 66000, 3, "bf16", None, dict(H=14000, tree=True, bias=0)),
+    # exactly one bitmap of tokens, one token more, and more than one
+    (40, 2, 262144, 0, "bf16", None, dict(H=4000, tree=True)),
+    (40, 2, 262145, 7, "f32", None, dict(H=4000, density=0.3)),
+    (40, 2, 300001, 0, "bf16", None, dict(H=4000, bias=40, density=0.5)),
+    (40, 1, 300001, 7, "bf16", None, dict(H=40000, bias=3)),
+]
+
+
+@pytest.mark.parametrize("B,n,V,pad,dtype,below,kw", GATHERED, ids=lambda v: str(v) if not isinstance(v, dict) else None)
+def test_process_gathered(cuda_device, B, n, V, pad, dtype, below, kw):
+    import draft_verification_gb300 as dv
+    rng = np.random.default_rng(B * 7919 + n * 104729 + V)
+    w = T.make_process(rng, B, n, V, **kw)
+    w["history_len"][::2] = kw["H"]
+    if below:
+        w["history"] %= below
+    x = T.strided(B, n, V, pad, T.DTYPES[dtype], cuda_device)
+    x.copy_(torch.from_numpy(rng.normal(0, 3, (B, n, V)).astype(np.float32)))
+    args = {k: T.dev(v, cuda_device) for k, v in w.items()}
+    plan = dv.ProcessLogitsPlan(x, args.pop("tokens"), **args)
+    plan.workspace.fill_(0xa5)
+    out = plan.run()
+    assert not bool((plan.workspace == 0xa5).all())  # (it was used: the gathered form)
+    T.check_process(x, out, w)
+    first = T.bits(out["logits"]).copy()
+    assert np.array_equal(T.bits(T.run_process(x, w, cuda_device, out=x)["logits"]), first)
+
+
+@pytest.mark.parametrize("B,n,V,H", [(1, 9, 128256, 300000), (3, 2, 128256, 131072), (16, 1, 32000, 131072)])
+def test_process_few_long_histories_are_read_where_they_apply(cuda_device, B, n, V, H):
+    """One CTA per sequence would go through such a history alone, window by window (4 sequences of 131072 tokens
+    over 128256: 420 us against 93): the entries are not gathered, the workspace is not used."""
+    import draft_verification_gb300 as dv
+    rng = np.random.default_rng(51)
+    w = T.make_process(rng, B, n, V, H=H)
+    x = torch.from_numpy(rng.normal(0, 3, (B, n, V)).astype(np.float32)).to(cuda_device, torch.bfloat16)
+    args = {k: T.dev(v, cuda_device) for k, v in w.items()}
+    plan = dv.ProcessLogitsPlan(x, args.pop("tokens"), **args)
+    plan.workspace.fill_(0xa5)
+    out = plan.run()
+    assert bool((plan.workspace == 0xa5).all())
+    T.check_process(x, out, w)
