@@ -479,7 +479,7 @@ struct Slab {
 };
 
 // Threads an SM holds: as many as leave the kernel its registers (56; with listed
-// entries 40, of which up to two are spilled).  Without the list, 128 sequences
+// entries 40 and 4 to 64 bytes spilled).  Without the list, 128 sequences
 // of 9 rows of 128256 tokens: 1024 threads 108 us, 1152 103, 1280 107; 16 trees of
 // 64 rows of 50257: 51, 52, 68.
 __host__ __device__ constexpr int resident_threads(bool listed) { return listed ? 1536 : 1152; }
@@ -628,10 +628,20 @@ __global__ void __launch_bounds__(kThreads, resident_threads(kListed) / kThreads
   if constexpr (kListed) {
     pdl_wait();
     const int* offsets = P.offsets + static_cast<long long>(b) * (P.slabs + 1);
-    // rows that start within a vector take up to e - 1 tokens of the slab before
-    const int slab = blockIdx.z, from = P.ld % E && slab > 0 ? slab - 1 : slab;
-    e0 = __ldcg(offsets + from);
+    const int slab = blockIdx.z;
+    e0 = __ldcg(offsets + slab);
     tokens = __ldcg(offsets + slab + 1) - e0;
+    if (!kAligned && P.ld % E && slab > 0) {
+      // rows that start within a vector take up to e - 1 tokens of the slab before:
+      // some of its last entries.  (With all of them, 128 sequences of 9 rows of
+      // 128255 tokens, 8192 in the history: 138 us, so 133; of 50257 85 and 77.)
+      const int at = e0 - 1 - (tid & 31);
+      const bool ours = (tid & 31) < E - 1 && at >= __ldcg(offsets + slab - 1) &&
+                        __ldcg(P.entry_token + static_cast<long long>(b) * P.capacity + at) >= lo;
+      const int back = __popc(__ballot_sync(0xffffffffu, ours));
+      e0 -= back;
+      tokens += back;
+    }
     const long long src = static_cast<long long>(b) * P.capacity + e0;
     for (int e = tid; e < min(tokens, S::kCache); e += kThreads) {
       const int at = __ldcg(P.entry_token + src + e) - lo;
@@ -640,8 +650,7 @@ __global__ void __launch_bounds__(kThreads, resident_threads(kListed) / kThreads
       // (a penalty and a bias are two additions: such entries are read again)
       const bool both = minus != 0.f && plus != 0.f;
       c_add[e] = minus != 0.f ? -minus : plus;
-      // (places beyond the table: tokens of the slab before that no row takes)
-      c_place[e] = static_cast<unsigned short>((at < 0 ? 0x3fff : at) | (c & (kInPrompt | kMade) ? 0x4000 : 0) |
+      c_place[e] = static_cast<unsigned short>(at | (c & (kInPrompt | kMade) ? 0x4000 : 0) |
                                                (c & kDrafted || both ? 0x8000 : 0));
     }
     __syncthreads();

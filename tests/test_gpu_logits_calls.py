@@ -273,3 +273,21 @@ def test_process_few_long_histories_are_read_where_they_apply(cuda_device, B, n,
     out = plan.run()
     assert bool((plan.workspace == 0xa5).all())
     T.check_process(x, out, w)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [66000, 66001, 66003, 66004, 66007])
+def test_process_gathered_tokens_at_the_slabs_borders(cuda_device, V, dtype):
+    """Every token near a slab's border is touched; rows that start within a vector take some from the slab before."""
+    rng = np.random.default_rng(52)
+    B, n, H = 130, 2, 9000
+    slab = 1024 if dtype == "f32" else 2048
+    near = (np.arange(0, V, slab)[:, None] + np.arange(-9, 10)).ravel()
+    near = near[(near >= 0) & (near < V)].astype(np.int32)
+    w = T.make_process(rng, B, n, V, H=H, bias=40)
+    w["history"] = near[rng.integers(0, len(near), (B, H))]
+    w["history_len"][:] = H
+    w["tokens"] = near[rng.integers(0, len(near), (B, n))]
+    x = T.strided(B, n, V, 0, T.DTYPES[dtype], cuda_device)
+    x.copy_(torch.from_numpy(rng.normal(0, 3, (B, n, V)).astype(np.float32)))
+    T.check_process(x, T.run_process(x, w, cuda_device), w)
