@@ -187,6 +187,7 @@ LOGITS_SIGNATURES = {
     "spec_quantize_int4": (C.c_int, [C.POINTER(QuantizeInt4Args), _vp]),
     "spec_int4_product_workspace_size": (C.c_size_t, [C.c_int, C.c_int, C.c_int, C.c_int]),
     "spec_int4_product": (C.c_int, [C.POINTER(Int4ProductArgs), _vp]),
+    "spec_test_inject_product_copy_timeout": (C.c_int, [C.c_int]),
 }
 
 _LIB = None

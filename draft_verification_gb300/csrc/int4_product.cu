@@ -48,6 +48,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <map>
 #include <mutex>
@@ -86,6 +87,7 @@ struct I4Params {
   void* out;
   int out_bf16;
   int ragged;               // scales or zero points begin or end within a 16-byte block
+  unsigned stage_bytes;     // what a stage of weights waits for (kStageBytes; more: see the test hook)
   int* counters;
   float* partials;          // [2 * CTAs][N][128]
   int* error_word;
@@ -488,7 +490,7 @@ __global__ void __launch_bounds__(Shape<N, G>::kThreads, 1)
             }
             __syncwarp();  // the stage expects all its bytes before its one arrival
             if (leader) {
-              mbar_expect_tx(&wfull[w.slot], kStageBytes);
+              mbar_expect_tx(&wfull[w.slot], P.stage_bytes);
               tma_load_2d(wring + w.slot * kStageBytes, &tm_w, x, v0, &wfull[w.slot]);
             }
             w.next();
@@ -886,6 +888,11 @@ cudaError_t raise_smem() {
   return e;
 }
 
+// Test hook (spec_test_inject_product_copy_timeout): nonzero makes every stage
+// of weights wait for 16 bytes that never come, so that the bounded waits of the
+// roles behind it give up.  Zero in normal operation.
+std::atomic<unsigned> g_more_bytes{0};
+
 template <int N, int G>
 spec_status launch_product(const spec_int4_product_args& a, cudaStream_t s) {
   I4Params P{};
@@ -905,6 +912,7 @@ spec_status launch_product(const spec_int4_product_args& a, cudaStream_t s) {
   P.counters = static_cast<int*>(a.workspace);
   P.partials = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kCounterBytes);
   P.error_word = a.error_word;
+  P.stage_bytes = kStageBytes + g_more_bytes.load();
   // whether a matrix begins or ends within a 16-byte block (the kernel's test is
   // kept out of the common loop, where it cost 2 to 9 %: 33 rows 50257, 2048, 64
   // with zero points 28.7 us without it, 31.3 with it, 28.8 as it is)
@@ -952,6 +960,11 @@ spec_status launch_product(const spec_int4_product_args& a, cudaStream_t s) {
 
 }  // namespace
 }  // namespace sv
+
+extern "C" spec_status spec_test_inject_product_copy_timeout(int enable) {
+  sv::g_more_bytes = enable ? 16u : 0u;
+  return SPEC_OK;
+}
 
 extern "C" size_t spec_int4_product_workspace_size(int R, int V, int d, int group) {
   return sv::good_shape(R, V, d, group) ? sv::product_workspace(R) : 0;

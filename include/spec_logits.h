@@ -197,6 +197,14 @@ size_t spec_int4_product_workspace_size(int R, int V, int d, int group);
 /* SPEC_EWORKSPACE, SPEC_ECUDA.                                               */
 spec_status spec_int4_product(const spec_int4_product_args* args, cudaStream_t stream);
 
+/* Test hook for its bounded waits, as spec_verify.h has them for the          */
+/* verifications.  While enabled, every stage of weights of the calls launched */
+/* by this process waits for 16 bytes more than are copied, so its waits give  */
+/* up after about 65 ms: *error_word gets SPEC_ERR_INTERNAL, out is not        */
+/* written.  Nothing faults and nothing is left in flight.  Tests only: leave  */
+/* it disabled (the default) in any other use.  SPEC_OK.                       */
+spec_status spec_test_inject_product_copy_timeout(int enable);
+
 #ifdef __cplusplus
 }
 #endif
