@@ -33,12 +33,14 @@ def step(B=8, gamma=4, V=32000, d=1024, group=128, temperature=0.8, seed=0, devi
     w_draft = (f32(V, d) * 0.1).bfloat16()
     head = dv.quantize_int4(w_draft, group=group)
 
-    # per request: history (the first half is the prompt), penalties, a biased token, a grammar
+    # per request: history (the first half is the prompt) with room for the drafted tokens, penalties, a biased token,
+    # a grammar
     H = 64
+    history = torch.zeros((B, H + gamma), dtype=torch.int32, device=device)
+    history[:, :H] = torch.randint(0, V, (B, H), generator=g, device=device, dtype=torch.int32)
+    history_len = torch.full((B,), H, dtype=torch.int32, device=device)
     request = dict(
-        history=torch.randint(0, V, (B, H), generator=g, device=device, dtype=torch.int32),
-        history_len=torch.full((B,), H, dtype=torch.int32, device=device),
-        prompt_len=torch.full((B,), H // 2, dtype=torch.int32, device=device),
+        history=history, prompt_len=torch.full((B,), H // 2, dtype=torch.int32, device=device),
         repetition=torch.full((B,), 1.1, device=device), frequency=torch.full((B,), 0.2, device=device),
         presence=torch.full((B,), 0.1, device=device),
         bias_tokens=torch.full((B, 1), 7, dtype=torch.int32, device=device),
@@ -47,30 +49,34 @@ def step(B=8, gamma=4, V=32000, d=1024, group=128, temperature=0.8, seed=0, devi
     mask = torch.randint(-2 ** 31, 2 ** 31, (1, words), generator=g, device=device, dtype=torch.int64).to(torch.int32)
     half = torch.arange(B, device=device, dtype=torch.int32).view(B, 1) % 2 - 1  # every other request has the grammar
 
-    # draft gamma tokens one after another: row i follows the tokens drafted before it
+    # logits whose rows all start on 16 bytes, so that a position's rows can be processed where they are
+    rows = lambda n: torch.empty((B, n, (V + 7) // 8 * 8), dtype=torch.bfloat16, device=device)[:, :, :V]
+
+    # draft gamma tokens one after another: a position's row follows the history and the tokens drafted before it,
+    # which are appended to the history
     hidden = f32(B, gamma, d).bfloat16()
     tokens = torch.zeros((B, gamma), dtype=torch.int32, device=device)
-    draft = torch.empty((B, gamma, V), dtype=torch.bfloat16, device=device)
+    draft, so_far = rows(gamma), history_len.clone()
+    errors = torch.zeros_like(history_len)
     for i in range(gamma):
-        raw = dv.int4_product(hidden[:, i].contiguous(), head["codes"], head["scales"], group=group)["logits"]
-        draft[:, i] = raw
-        # rows 0 .. i of the chain; the last one is the row to draw from
-        rows = dv.process_logits(draft[:, :i + 1].contiguous(), tokens, mask=mask,
-                                 mask_index=half.expand(B, i + 1).contiguous(), **request)["logits"]
-        tokens[:, i] = draw(rows[:, i], temperature, g)
-    q = dv.process_logits(draft, tokens, mask=mask, mask_index=half.expand(B, gamma).contiguous(), **request)
+        dv.Int4ProductPlan(hidden[:, i], head["codes"], head["scales"], group=group, out=draft[:, i]).run()
+        row = draft[:, i:i + 1]
+        errors |= dv.process_logits(row, history_len=so_far, mask=mask, mask_index=half, out=row,
+                                    **request)["seq_error"]
+        tokens[:, i] = history[:, H + i] = draw(row[:, 0], temperature, g)
+        so_far += 1
 
-    # the target's rows at the gamma + 1 positions (here: the unquantised head), processed alike
-    target = torch.empty((B, gamma + 1, V), dtype=torch.bfloat16, device=device)
+    # the target's rows at the gamma + 1 positions (here: the unquantised head), processed alike: a chain's rows
+    # follow the history before the step and the drafted tokens before their own positions
+    target = rows(gamma + 1)
     target[:, :gamma] = hidden @ w_draft.t()
     target[:, gamma] = f32(B, d).bfloat16() @ w_draft.t()
-    p = dv.process_logits(target, tokens, mask=mask, mask_index=half.expand(B, gamma + 1).contiguous(),
-                          out=target, **request)
+    p = dv.process_logits(target, tokens, history_len=history_len, mask=mask,
+                          mask_index=half.expand(B, gamma + 1).contiguous(), out=target, **request)
 
-    out = dv.verify_chain(p["logits"], q["logits"], tokens, uni(B, gamma), uni(B), request["history_len"],
-                          temperature=temperature)
-    return dict(tokens=tokens, q=q["logits"], p=p["logits"], mask=mask, masked=half[:, 0] >= 0,
-                errors=q["seq_error"] | p["seq_error"], **out)
+    out = dv.verify_chain(target, draft, tokens, uni(B, gamma), uni(B), history_len, temperature=temperature)
+    return dict(tokens=tokens, q=draft, p=target, mask=mask, masked=half[:, 0] >= 0, errors=errors | p["seq_error"],
+                **out)
 
 
 if __name__ == "__main__":

@@ -34,6 +34,8 @@ extern "C" {
 /*  - tree: row i is node i's; it follows the history and the tokens of    */
 /*    the nodes on the path from the root to i, the root excluded (the     */
 /*    root's token is the history's last).                                 */
+/* One row alone, as drafting wants it, follows the history alone: append   */
+/* the tokens drafted so far to it (and count them in history_len).         */
 /* With s(v) = token v occurs in the history or on the path, and c(v) = its */
 /* occurrences in the history from prompt_len[b] on and on the path:       */
 /*    x1 = s ? (x > 0 ? x * (1 / repetition) : x * repetition) : x         */
