@@ -35,15 +35,16 @@
 //
 // What bounds it: for few rows HBM, which has to read half a byte per weight.
 // With 128256 x 4096 weights in groups of 128 (271 MB, 40 us at the measured
-// 6.8 TB/s) 1 row takes 64 us, 4.2 TB/s; 64 rows 80.  No role is alone at
+// 6.8 TB/s) 1 row takes 66 us, 4.1 TB/s; 64 rows 79.  No role is alone at
 // fault: a unit takes about 1150 cycles, of which the copying, MMA and epilogue
-// warps are each busy for 600 or more, and the warp schedulers issue in 62 % of
+// warps are each busy for 600 or more, and the warp schedulers issue in 64 % of
 // all cycles, most of it the unpacking.  Of 66 us (before tiles stayed whole)
 // 60 were left without the unpacking's arithmetic, 62 without the epilogue's, 64
 // without the weights' copies, 66 with one MMA of sixteen.  128 rows (134 GFLOP,
-// 70.6 us at the measured bfloat16 rate) take 114 us: there the epilogue's reads
+// 70.6 us at the measured bfloat16 rate) take 118 us: there the epilogue's reads
 // of tensor memory, N values per entry and group, are the longest.  Small groups
-// multiply those reads: with groups of 32, 16 rows took 87 us and 128 rows 247.
+// multiply those reads: with groups of 32, 16 rows take 82 us and 128 rows 239.
+// More rows take a pass over the weights per 128: 129 rows 221 us, 256 231.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -134,7 +135,7 @@ struct Shape {
   static constexpr int kXStages = N <= 32 ? 4 : N == 64 ? 3 : 2;
   static constexpr int kWStages = N <= 32 ? 8 : N == 64 ? 6 : 4;
   // registers per thread (warps 0-3, unpacking, epilogue): shares of what the
-  // launch holds
+  // launch holds (128 rows in groups of 32 spill one)
   static constexpr int kRegsLaunch = 65536 / kThreads / 8 * 8;
   static constexpr int kRegsCopy = 40;
   static constexpr int kRegsUnpack = N == 64 ? 64 : 72;
@@ -826,9 +827,8 @@ __global__ void __launch_bounds__(Shape<N, G>::kThreads, 1)
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // MMA N: the rows of a block, rounded up to a width that has a kernel.  (The
-// narrowest that fits: with 128256 x 4096 weights in groups of 128, evenly
-// divided, the widths take 66, 74, 85 and 122 us whatever part of their rows is
-// used.)
+// narrowest that fits: with 128256 x 4096 weights in groups of 128 the widths
+// take 65, 71, 79 and 118 us whatever part of their rows is used.)
 int rows_tile(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128; }
 
 // the units of all row blocks
@@ -926,7 +926,8 @@ spec_status launch_product(const spec_int4_product_args& a, cudaStream_t s) {
   // at the end of the call, its join included.  So tiles stay whole, or are cut
   // into the same number of equal parts (of 4 units or more, which begin and end
   // with a tile), where the longest CTA has at most 8 units more than an even
-  // division would give it.  Measured (V, d, group; evenly divided, and so):
+  // division would give it.  Measured (by graph replays, which read 2 to 4 %
+  // below single launches; V, d, group; evenly divided, and so):
   // 128 rows 128256, 4096, 128 124 and 114 us, 1 row 66 and 64; 33 rows 50257,
   // 2048, 64 31 and 27; 128 rows 1000, 8192, 64 33 and 23, 12800, 4096, 128
   // 27 and 22.  With 12 instead of 8 units: 16 rows 25000, 4096, 128 21 and 23,

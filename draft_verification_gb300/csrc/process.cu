@@ -25,13 +25,24 @@
 //    vectors are in flight meanwhile) read a few hundred entries each.
 // run_process has the rule and what it measured.
 //
-// What bounds it: HBM, which has to read every element with an allowed token
-// and write every element.  128 sequences of 9 rows of 128256 bfloat16 logits
-// with grammar masks and histories of up to 8192 tokens (613 MB): 111 us; a copy
-// of that size takes 90.5 at the measured 6.8 TB/s, and writing it alone 76.  16
-// trees of 64 nodes over 50257 tokens, whose rows start anywhere (212 MB): 52 us
-// against 31, of which the rewriting takes 9.  One row: 7 us, the launch.
-//
+// What bounds it: HBM, which has to read every vector with an allowed token and
+// write every element; where tokens are few, what precedes a CTA's first row.
+//  - 128 sequences of 9 rows of 128256 bfloat16 logits with grammar masks and
+//    histories of up to 8192 tokens: 109 us, of which collecting takes 15 and the
+//    rows 97.  All bytes are 613 MB, 90.5 us at the measured 6.8 TB/s; the masks
+//    leave a third of the vectors to read, 411 MB, and the kernel reads no others.
+//    That gains little (without masks 118 us), because writing is the slower half:
+//    a fill of the output alone takes 76 us, 3.9 TB/s, a copy of a third of it and
+//    a fill of the rest 87.
+//  - 16 trees of 64 nodes over 50257 tokens, whose rows start anywhere (212 MB, 31
+//    us; 141 MB as the masks leave it; a fill of the output 29): 53 us, without
+//    masks 59, over 50264 tokens 46.  DRAM is at 22 %, 45 % of the warps are
+//    active: latency between the barriers.
+//  - One row: 7 us, the launch.  One sequence of 9 rows with 131,072 tokens: 112 us,
+//    the history.
+//  - float32: the same 109 us for half as many sequences.  In place with masks the
+//    same; without masks 97 us for the first.
+
 // Vectors are aligned in memory: a row that starts at element m of its vector
 // has tokens [k e - m, k e - m + e) in vector k, so a row's part is the slab
 // shifted by m (entries of the slab before may belong to it), and mask bits are
@@ -714,7 +725,10 @@ __global__ void __launch_bounds__(kThreads, resident_threads(kListed) / kThreads
         c = count[at];
         plus = biased ? bias[at] : 0.f;
       }
-      if (c & kDrafted) {  // its occurrences on the way to the row
+      // Its occurrences on the way to the row.  (This grows with the square of a
+      // chain's rows: one of 1024 rows of 32000 logits takes 0.41 ms, 16 take 5.9,
+      // where their bytes take 0.31; a tree of 1024 nodes, with short paths, 59 us.)
+      if (c & kDrafted) {
         const int t = lo + at;
         if (tree) {
           for (int a = i; a > 0; a = s_par[a]) c += s_tok[a] == t;
@@ -864,8 +878,8 @@ cudaError_t launch_rows(ProcessParams p, int nsm, cudaStream_t s) {
 
 // Rows that all start and end up on a vector boundary need no shifts of their
 // mask bits and no choice of how to store.  Measured (128 sequences of 9 rows of
-// 128256 bfloat16 logits, masks, histories of 8192 tokens): 111 us, by the
-// kernel for any alignment 130; without masks 108 and 110.
+// 128256 bfloat16 logits, masks, histories of 8192 tokens): 109 us, by the
+// kernel for any alignment 129; without masks 118 and 124.
 template <typename T, int kThreads, int kVecs, bool kListed>
 cudaError_t launch_process(const ProcessParams& p, int nsm, cudaStream_t s) {
   constexpr int E = Lanes<T>::kN;
