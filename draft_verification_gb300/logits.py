@@ -9,10 +9,11 @@ the logits that a verification reads.
 
 As for the verifications, a plan binds its buffers once and ``run()`` launches
 without Python-side allocation (what a plan clears, it clears on the stream that
-is current where it is made: run it there, or behind it); the functions take one call's tensors (device
-tensors stay on the device; CPU tensors are copied there and the results back,
-complete on return).  With ``stream`` all of a function's work goes to that
-stream, behind what the current one holds; the results belong to it.
+is current where it is made: run it there, or behind it); the functions take one
+call's tensors (device tensors stay on the device; CPU tensors are copied there
+and the results back, complete on return).  With ``stream`` all of a function's
+work goes to that stream, behind what the current one holds; the results belong
+to it.
 """
 
 from __future__ import annotations
