@@ -1,7 +1,8 @@
 """Batched draft verification for speculative decoding on GB300 (sm_103a).
 
 The compute runs in the CUDA library libspecverify.so (C ABI in
-include/spec_verify.h and spec_logits.h); this package only builds it and marshals arguments.
+include/spec_verify.h, spec_logits.h and spec_cache.h); this package only builds
+it and marshals arguments.
 """
 
 from .api import (  # noqa: F401
@@ -13,7 +14,12 @@ from .api import (  # noqa: F401
 from .logits import (  # noqa: F401
     Int4ProductPlan, ProcessLogitsPlan, QuantizeInt4Plan, int4_product, process_logits, quantize_int4,
 )
+from .cache import (  # noqa: F401
+    AppendCachePlan, AttendCachePlan, PagedCache, RotateHeadsPlan, append_cache, attend_cache, rotary_frequencies,
+    rotate_heads, rotation_table,
+)
 from ._lib import (  # noqa: F401
-    ERR_INTERNAL, ERR_MASK, ERR_NONFINITE, ERR_PARENT, ERR_TOKEN, ERR_WINDOW, ERR_ZERO_MASS,
+    ERR_CACHE, ERR_INTERNAL, ERR_MASK, ERR_NONFINITE, ERR_PARENT, ERR_POSITION, ERR_TOKEN, ERR_WINDOW,
+    ERR_ZERO_MASS,
 )
 from .build import build as build_library, lib_path  # noqa: F401

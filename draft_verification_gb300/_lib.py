@@ -1,4 +1,5 @@
-"""ctypes view of the C ABI declared in include/spec_verify.h and spec_logits.h.
+"""ctypes view of the C ABI declared in include/spec_verify.h, spec_logits.h
+and spec_cache.h.
 
 Argument marshalling only: the structures below mirror the C structs field
 for field, and ``lib()`` loads the in-tree libspecverify.so.  There is no
@@ -18,6 +19,7 @@ SPEC_GREEDY, SPEC_SAMPLE = 0, 1
 SPEC_NOALLOC_SCRATCH_BYTES = 8 << 20
 ERR_TOKEN, ERR_PARENT, ERR_NONFINITE, ERR_ZERO_MASS, ERR_INTERNAL, ERR_WINDOW = 1, 2, 4, 8, 16, 32
 ERR_MASK = 64
+ERR_CACHE, ERR_POSITION = 128, 256
 
 _vp = C.c_void_p
 
@@ -157,6 +159,36 @@ class Int4ProductArgs(C.Structure):
     ]
 
 
+class RotateArgs(C.Structure):
+    _fields_ = [
+        ("B", C.c_int), ("n", C.c_int), ("H", C.c_int), ("D", C.c_int), ("rot", C.c_int), ("pairs", C.c_int),
+        ("transpose", C.c_int), ("dtype", C.c_int), ("x_ld", C.c_longlong * 3), ("out_ld", C.c_longlong * 3),
+        ("x", _vp), ("out", _vp), ("table", _vp), ("table_rows", C.c_int),
+        ("positions", _vp), ("prefix_len", _vp), ("seq_error", _vp), ("error_word", _vp)
+    ]
+
+
+class AppendArgs(C.Structure):
+    _fields_ = [
+        ("B", C.c_int), ("n", C.c_int), ("H", C.c_int), ("D", C.c_int), ("page", C.c_int), ("pages", C.c_int),
+        ("table_pages", C.c_int), ("rot", C.c_int), ("pairs", C.c_int), ("table_rows", C.c_int),
+        ("max_depth", C.c_int), ("dtype", C.c_int), ("k_ld", C.c_longlong * 3), ("v_ld", C.c_longlong * 3),
+        ("k", _vp), ("v", _vp), ("table", _vp), ("positions", _vp), ("prefix_len", _vp), ("count", _vp),
+        ("path_nodes", _vp), ("path_len", _vp), ("block_table", _vp), ("k_codes", _vp), ("v_codes", _vp),
+        ("k_exps", _vp), ("v_exps", _vp), ("seq_error", _vp), ("error_word", _vp)
+    ]
+
+
+class AttendArgs(C.Structure):
+    _fields_ = [
+        ("B", C.c_int), ("n", C.c_int), ("Hq", C.c_int), ("H", C.c_int), ("D", C.c_int), ("page", C.c_int),
+        ("pages", C.c_int), ("table_pages", C.c_int), ("scale", C.c_float), ("q_ld", C.c_longlong * 3),
+        ("out_ld", C.c_longlong * 3), ("q", _vp), ("out", _vp), ("prefix_len", _vp), ("count", _vp),
+        ("parent", _vp), ("block_table", _vp), ("k_codes", _vp), ("v_codes", _vp), ("k_exps", _vp),
+        ("v_exps", _vp), ("seq_error", _vp), ("error_word", _vp), ("workspace", _vp), ("workspace_bytes", C.c_size_t)
+    ]
+
+
 # every symbol include/spec_verify.h declares, with its ctypes signature
 SIGNATURES = {
     "spec_chain_workspace_size": (C.c_size_t, [C.c_int, C.c_int, C.c_int]),
@@ -190,6 +222,15 @@ LOGITS_SIGNATURES = {
     "spec_test_inject_product_copy_timeout": (C.c_int, [C.c_int]),
 }
 
+# every symbol include/spec_cache.h declares
+CACHE_SIGNATURES = {
+    "spec_rotation_table": (C.c_int, [C.c_int, C.c_int, _vp, C.c_double, _vp, _vp]),
+    "spec_rotate_heads": (C.c_int, [C.POINTER(RotateArgs), _vp]),
+    "spec_append_cache": (C.c_int, [C.POINTER(AppendArgs), _vp]),
+    "spec_attend_workspace_size": (C.c_size_t, [C.c_int] * 5),
+    "spec_attend_cache": (C.c_int, [C.POINTER(AttendArgs), _vp]),
+}
+
 _LIB = None
 
 
@@ -203,7 +244,7 @@ def lib() -> C.CDLL:
                 f"{path} is missing: build it with `python -m draft_verification_gb300.build` "
                 "(there is no CPU fallback)")
         handle = C.CDLL(path)
-        for name, (res, args) in {**SIGNATURES, **LOGITS_SIGNATURES}.items():
+        for name, (res, args) in {**SIGNATURES, **LOGITS_SIGNATURES, **CACHE_SIGNATURES}.items():
             fn = getattr(handle, name)
             fn.restype = res
             fn.argtypes = args

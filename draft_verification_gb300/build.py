@@ -22,7 +22,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "lib")
 LIB_NAME = "libspecverify.so"
 SOURCES = ["verify.cu", "api.cu", "noalloc.cu", "compact.cu", "clasp.cu", "pipeline_async.cu", "lm_head.cu",
-           "process.cu", "quantize.cu", "int4_product.cu"]
+           "process.cu", "quantize.cu", "int4_product.cu", "rotate.cu", "append.cu", "attend.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-Xptxas", "-v"]
 
@@ -65,7 +65,7 @@ def build(verbose: bool = False, force: bool = False, debug_checks: bool = False
     os.makedirs(out_dir, exist_ok=True)
     extra = ["-DSPEC_DEBUG_CHECKS"] if debug_checks else []
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    headers += [os.path.join(INCLUDE, f) for f in ("spec_verify.h", "spec_logits.h")]
+    headers += [os.path.join(INCLUDE, f) for f in ("spec_verify.h", "spec_logits.h", "spec_cache.h")]
     objs = []
     jobs = []
     for src in SOURCES:

@@ -1,0 +1,305 @@
+// Appending keys and values to the paged 8-bit cache (spec_append_cache).
+//
+// One CTA per page that gets rows, head and sequence: it alone reads and
+// writes that page of that head.  It reads its rows once for their largest
+// magnitude, which gives the page's exponent, and once more (from L1 or L2)
+// to rotate and round them.  Bound by memory: 2 x (element + code) bytes per
+// row, head and element.
+#include <algorithm>
+#include <cstdint>
+
+#include "cache.cuh"
+#include "heads.cuh"
+#include "internal.h"
+#include "spec_cache.h"
+
+namespace sv {
+namespace {
+
+constexpr int kAppendThreads = 256;
+
+struct AppendParams {
+  int n, H, D, page, pages, table_pages, rot, units, table_rows, path_ld;
+  bool pairs;
+  long long k_ld[3], v_ld[3];
+  const void* k;
+  const void* v;
+  const float* table;
+  const int* positions;
+  const int* prefix;
+  const int* count;
+  const int* path_nodes;
+  const int* path_len;
+  const int* block_table;
+  unsigned char* k_codes;
+  unsigned char* v_codes;
+  signed char* k_exps;
+  signed char* v_exps;
+  int* seq_error;
+  int* error_word;
+};
+
+// V float32 values, already scaled, to codes; what e4m3 does not reach becomes NaN (and `bad`).
+template <int V>
+__device__ __forceinline__ void store_codes(unsigned char* p, const float* x, float scale, bool& bad) {
+  float y[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    y[i] = x[i] * scale;
+    if (!(fabsf(y[i]) <= 448.f)) {
+      y[i] = __uint_as_float(0x7fc00000u);
+      bad = true;
+    }
+  }
+  if constexpr (V == 8) {
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(pack_e4m3(y[0], y[1]) | pack_e4m3(y[2], y[3]) << 16, pack_e4m3(y[4], y[5]) | pack_e4m3(y[6], y[7]) << 16);
+  } else if constexpr (V == 4) {
+    *reinterpret_cast<uint32_t*>(p) = pack_e4m3(y[0], y[1]) | pack_e4m3(y[2], y[3]) << 16;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) p[i] = static_cast<unsigned char>(pack_e4m3(y[i], 0.f));
+  }
+}
+
+// The page's earlier codes, scaled by 2^-shift, shift >= 1.
+__device__ void scale_codes(unsigned char* p, int bytes, int shift) {
+  const float f = shift > 126 ? 0.f : exp2i(-shift);
+  for (int o = threadIdx.x * 16; o < bytes; o += kAppendThreads * 16) {
+    uint4 w = *reinterpret_cast<uint4*>(p + o);
+    uint32_t* r = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 lo = unpack_e4m3(r[i] & 0xffffu), hi = unpack_e4m3(r[i] >> 16);
+      r[i] = pack_e4m3(lo.x * f, lo.y * f) | pack_e4m3(hi.x * f, hi.y * f) << 16;
+    }
+    *reinterpret_cast<uint4*>(p + o) = w;
+  }
+}
+
+// The least e with m <= 2^(e + 7), in range.
+__device__ __forceinline__ int exponent_of(float m) {
+  const uint32_t bits = __float_as_uint(m);
+  if (bits < (1u << 23)) return kLowExp;  // (0, or below 2^-126)
+  const int e = static_cast<int>(bits >> 23) - 127 + ((bits & 0x7fffffu) != 0 ? 1 : 0) - 7;
+  return min(kHighExp, max(kLowExp, e));
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams P) {
+  __shared__ float most_s[2][kAppendThreads / 32];
+  __shared__ int skip_s;
+  const int b = blockIdx.z, h = blockIdx.y, tid = threadIdx.x;
+  const int prefix = P.prefix ? P.prefix[b] : 0;
+  const int* path = P.path_nodes ? P.path_nodes + static_cast<long long>(b) * P.path_ld : nullptr;
+  const bool reports = blockIdx.x == 0 && h == 0;  // one CTA per sequence reports what concerns all of it
+  if (tid == 0) skip_s = 0;
+  __syncthreads();
+  int rows, bits = 0;
+  if (path) {
+    rows = P.path_len[b] + 1;
+    if (path[0] == -1) return;  // the verification's data-error marking
+    if (rows < 1 || rows > P.path_ld) bits |= SPEC_ERR_CACHE, rows = 0;
+    bool bad = false;
+    for (int i = tid; i < rows; i += kAppendThreads) bad |= path[i] < 0 || path[i] >= P.n;
+    if (bad) atomicOr(&skip_s, SPEC_ERR_PARENT);
+  } else {
+    rows = P.count ? P.count[b] : P.n;
+    if (rows < 0 || rows > P.n) bits |= SPEC_ERR_CACHE;
+  }
+  if (prefix < 0 || static_cast<long long>(prefix) + rows > static_cast<long long>(P.table_pages) * P.page)
+    bits |= SPEC_ERR_CACHE;
+  __syncthreads();
+  bits |= skip_s;
+  if (bits) {
+    if (reports && tid == 0) {
+      if (P.seq_error) atomicOr(P.seq_error + b, bits);
+      if (P.error_word) atomicOr(P.error_word, bits);
+    }
+    return;
+  }
+  const int entry = prefix / P.page + blockIdx.x;
+  const int start = entry * P.page;  // first token of the page
+  const int i0 = max(0, start - prefix), i1 = min(rows, start + P.page - prefix);
+  if (i0 >= i1) return;
+  const int page = P.block_table[static_cast<long long>(b) * P.table_pages + entry];
+  if (page < 0 || page >= P.pages) {
+    if (h == 0 && tid == 0) {
+      if (P.seq_error) atomicOr(P.seq_error + b, SPEC_ERR_CACHE);
+      if (P.error_word) atomicOr(P.error_word, SPEC_ERR_CACHE);
+    }
+    return;
+  }
+  const long long slab = static_cast<long long>(page) * P.H + h;
+  unsigned char* kc = P.k_codes + slab * P.page * P.D;
+  unsigned char* vc = P.v_codes + slab * P.page * P.D;
+  const T* k = static_cast<const T*>(P.k) + b * P.k_ld[0] + h * P.k_ld[2];
+  const T* v = static_cast<const T*>(P.v) + b * P.v_ld[0] + h * P.v_ld[2];
+  const int work = (i1 - i0) * P.units;
+
+  // the largest finite magnitudes
+  float mk = 0.f, mv = 0.f;
+  const auto most = [](float m, const float* x) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float a = fabsf(x[e]);
+      if (a < kInf) m = fmaxf(m, a);
+    }
+    return m;
+  };
+  for (int o = tid; o < work; o += kAppendThreads) {
+    const int i = i0 + o / P.units, u = o % P.units;
+    const long long r = path ? path[i] : i;
+    float x[V];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      load_elems<V>(k + r * P.k_ld[1] + (2 * u + half) * V, x);
+      mk = most(mk, x);
+      load_elems<V>(v + r * P.v_ld[1] + (2 * u + half) * V, x);
+      mv = most(mv, x);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+    mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+  }
+  if ((tid & 31) == 0) most_s[0][tid >> 5] = mk, most_s[1][tid >> 5] = mv;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kAppendThreads / 32; ++w) mk = fmaxf(mk, most_s[0][w]), mv = fmaxf(mv, most_s[1][w]);
+  int ek = exponent_of(mk), ev = exponent_of(mv);
+  if (start < prefix) {
+    const int ok = P.k_exps[slab], ov = P.v_exps[slab];
+    ek = max(ek, ok);
+    ev = max(ev, ov);
+    const int bytes = (prefix - start) * P.D;
+    if (ek > ok) scale_codes(kc, bytes, ek - ok);
+    if (ev > ov) scale_codes(vc, bytes, ev - ov);
+  }
+  __syncthreads();
+  if (tid == 0) {
+    P.k_exps[slab] = static_cast<signed char>(ek);
+    P.v_exps[slab] = static_cast<signed char>(ev);
+  }
+
+  // the codes
+  const float fk = exp2i(-ek), fv = exp2i(-ev);
+  bool bad = false, outside = false;
+  for (int o = tid; o < work; o += kAppendThreads) {
+    const int i = i0 + o / P.units, u = o % P.units;
+    const long long r = path ? path[i] : i;
+    const long long at = static_cast<long long>(prefix + i - start) * P.D;
+    const UnitPlace w = unit_place<V>(u, P.rot, P.pairs);
+    float a[V], c[V];
+    load_elems<V>(k + r * P.k_ld[1] + w.a, a);
+    load_elems<V>(k + r * P.k_ld[1] + w.b, c);
+    if (w.rotated) {
+      const int t = P.positions ? P.positions[static_cast<long long>(b) * P.n + r] : prefix + i;
+      float cs[V], sn[V];
+      if (t >= 0 && t < P.table_rows) {
+        const float* src = P.table + static_cast<long long>(t) * P.rot + u * V;
+        load_elems<V>(src, cs);
+        load_elems<V>(src + P.rot / 2, sn);
+      } else {
+        outside = true;
+#pragma unroll
+        for (int e = 0; e < V; ++e) cs[e] = sn[e] = __uint_as_float(0x7fc00000u);
+      }
+      rotate_unit<V>(a, c, cs, sn, P.pairs);
+      bool hit = false;
+      store_codes<V>(kc + at + w.a, a, fk, hit);
+      store_codes<V>(kc + at + w.b, c, fk, hit);
+      bad |= hit && t >= 0 && t < P.table_rows;
+    } else {
+      store_codes<V>(kc + at + w.a, a, fk, bad);
+      store_codes<V>(kc + at + w.b, c, fk, bad);
+    }
+    load_elems<V>(v + r * P.v_ld[1] + 2 * u * V, a);
+    load_elems<V>(v + r * P.v_ld[1] + (2 * u + 1) * V, c);
+    store_codes<V>(vc + at + 2 * u * V, a, fv, bad);
+    store_codes<V>(vc + at + (2 * u + 1) * V, c, fv, bad);
+  }
+  if (bad || outside) {
+    const int err = (bad ? SPEC_ERR_NONFINITE : 0) | (outside ? SPEC_ERR_POSITION : 0);
+    if (P.seq_error) atomicOr(P.seq_error + b, err);
+    if (P.error_word) atomicOr(P.error_word, err);
+  }
+}
+
+template <typename T>
+void launch_append(const AppendParams& p, int v, dim3 grid, cudaStream_t s) {
+  if (v == 8) {
+    if constexpr (sizeof(T) == 2) append_kernel<T, 8><<<grid, kAppendThreads, 0, s>>>(p);
+  } else if (v == 4) {
+    append_kernel<T, 4><<<grid, kAppendThreads, 0, s>>>(p);
+  } else {
+    append_kernel<T, 1><<<grid, kAppendThreads, 0, s>>>(p);
+  }
+}
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+}  // namespace
+}  // namespace sv
+
+extern "C" spec_status spec_append_cache(const spec_append_args* a, cudaStream_t stream) {
+  using namespace sv;
+  NvtxRange nvtx_range("spec_append_cache");
+  if (a == nullptr) return SPEC_EINVAL;
+  if (a->dtype != SPEC_F32 && a->dtype != SPEC_BF16) return SPEC_EDTYPE;
+  if (a->B < 1 || a->B > 65535 || a->n < 1 || a->n > (1 << 20) || a->H < 1 || a->H > 1024 || a->D < 16 || a->D > 256 ||
+      a->D % 16)
+    return SPEC_EINVAL;
+  if (a->page != 16 && a->page != 32 && a->page != 64 && a->page != 128) return SPEC_EINVAL;
+  if (a->pages < 1 || static_cast<long long>(a->pages) * a->H * a->page > 0x7fffffffLL || a->table_pages < 1 ||
+      static_cast<long long>(a->table_pages) * a->page > (1 << 30))
+    return SPEC_EINVAL;
+  if (a->rot < 0 || a->rot > a->D || a->rot % 2 || (a->rot && a->table_rows < 1)) return SPEC_EINVAL;
+  if (!a->k || !a->v || !a->block_table || !a->k_codes || !a->v_codes || !a->k_exps || !a->v_exps ||
+      (a->rot && !a->table))
+    return SPEC_EINVAL;
+  if ((a->path_nodes != nullptr) != (a->path_len != nullptr) || (a->path_nodes && a->count)) return SPEC_EINVAL;
+  if (a->path_nodes && (a->max_depth < 0 || a->max_depth > 65534)) return SPEC_EINVAL;
+  const int elem = a->dtype == SPEC_F32 ? 4 : 2;
+  if (!aligned(a->k, elem) || !aligned(a->v, elem) || (a->rot && !aligned(a->table, 16)) || !aligned(a->k_codes, 16) ||
+      !aligned(a->v_codes, 16))
+    return SPEC_EALIGN;
+  const int v = std::min(vector_width(elem, a->D, a->rot, a->k_ld, a->B, a->n, a->H, a->k),
+                         vector_width(elem, a->D, a->rot, a->v_ld, a->B, a->n, a->H, a->v));
+  AppendParams p{};
+  p.n = a->n;
+  p.H = a->H;
+  p.D = a->D;
+  p.page = a->page;
+  p.pages = a->pages;
+  p.table_pages = a->table_pages;
+  p.rot = a->rot;
+  p.units = a->D / (2 * v);
+  p.table_rows = a->table_rows;
+  p.path_ld = a->max_depth + 1;
+  p.pairs = a->pairs != 0;
+  for (int i = 0; i < 3; ++i) p.k_ld[i] = a->k_ld[i], p.v_ld[i] = a->v_ld[i];
+  p.k = a->k;
+  p.v = a->v;
+  p.table = a->table;
+  p.positions = a->positions;
+  p.prefix = a->prefix_len;
+  p.count = a->count;
+  p.path_nodes = a->path_nodes;
+  p.path_len = a->path_len;
+  p.block_table = a->block_table;
+  p.k_codes = static_cast<unsigned char*>(a->k_codes);
+  p.v_codes = static_cast<unsigned char*>(a->v_codes);
+  p.k_exps = a->k_exps;
+  p.v_exps = a->v_exps;
+  p.seq_error = a->seq_error;
+  p.error_word = a->error_word;
+  // the pages that so many rows can touch, wherever they start
+  const int rows = a->path_nodes ? p.path_ld : a->n;
+  const dim3 grid(static_cast<unsigned>((rows + a->page - 2) / a->page + 1), static_cast<unsigned>(a->H),
+                  static_cast<unsigned>(a->B));
+  if (a->dtype == SPEC_F32) launch_append<float>(p, v, grid, stream);
+  else launch_append<bf16_t>(p, v, grid, stream);
+  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
+}

@@ -29,11 +29,13 @@ Modules
                   rollbacks).
 ``logits``        the logit-side operators: processing of logits, 4-bit
                   quantisation and products with 4-bit weights.
+``cache``         the cache operators: rotary positions, appending to a paged
+                  cache of e4m3 codes, attention of a chain's or a tree's rows.
 
 Every function states the passage it follows.  Points where the pages are
 silent or ambiguous follow the readings listed in the design notes; each is
 repeated in the docstring that depends on it.
 """
 
-from . import (clasp, closed_forms, compact, consulted, consulted_tree, lm_head, logits,  # noqa: F401
+from . import (cache, clasp, closed_forms, compact, consulted, consulted_tree, lm_head, logits,  # noqa: F401
                pipeline, pipeline_async, verify)
