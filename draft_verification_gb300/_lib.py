@@ -229,6 +229,7 @@ CACHE_SIGNATURES = {
     "spec_append_cache": (C.c_int, [C.POINTER(AppendArgs), _vp]),
     "spec_attend_workspace_size": (C.c_size_t, [C.c_int] * 5),
     "spec_attend_cache": (C.c_int, [C.POINTER(AttendArgs), _vp]),
+    "spec_test_inject_cache_copy_timeout": (C.c_int, [C.c_int]),
 }
 
 _LIB = None

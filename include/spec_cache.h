@@ -216,6 +216,13 @@ size_t spec_attend_workspace_size(int B, int n, int Hq, int H, int D);
 /* SPEC_EINVAL, SPEC_EALIGN, SPEC_EWORKSPACE, SPEC_ECUDA as above.           */
 spec_status spec_attend_cache(const spec_attend_args* args, cudaStream_t stream);
 
+/* Test hook for its bounded waits, as spec_verify.h has them for the          */
+/* verifications.  While enabled, every tile of codes of the calls launched by */
+/* this process waits for 16 bytes more than are copied, so its waits give up   */
+/* after about 65 ms: *error_word gets SPEC_ERR_INTERNAL.  Nothing faults and  */
+/* nothing is left in flight.  Tests only.  SPEC_OK.                           */
+spec_status spec_test_inject_cache_copy_timeout(int enable);
+
 #ifdef __cplusplus
 }
 #endif
