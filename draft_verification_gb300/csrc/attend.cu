@@ -51,15 +51,17 @@ constexpr int kPanel = 16384;   // bytes of 128 tokens x 128 elements
 constexpr int kMaxRows = 1024;  // n
 constexpr int kMaxCtas = 160;
 constexpr int kAttendThreads = 512;
-constexpr int kScaleRing = 16, kPatchRing = 8;
+constexpr int kScaleRing = 16, kPatchRing = 8, kPieceRing = 4;
+constexpr int kFar = 30;  // value exponents of a tile that lie further apart than this
 
 // R: a block's rows; NP: panels of 128 elements of a head.
 template <int R, int NP>
 struct Shape {
-  static constexpr int kStages = NP == 1 ? (R == 64 ? 4 : 5) : 2;
+  static constexpr int kStages = NP == 1 ? (R > 32 ? 4 : 5) : 2;
+  static constexpr int kPRow = R == 48 ? 64 : R;  // bytes of a token's weights
   static constexpr int kSlot = NP * kPanel;
   static constexpr int kQHalf = NP * R * 128;  // hi or lo of a block's queries
-  static constexpr int kPHalf = kTile * R;     // hi or lo of a tile's weights
+  static constexpr int kPHalf = kTile * kPRow;  // hi or lo of a tile's weights
   static constexpr int kMaskBytes = 2 * kMaxRows * 8;
   static constexpr int kSmem = 1024 + 2 * kStages * kSlot + 4 * kQHalf + 4 * kPHalf + kMaskBytes + kMaxRows * 2;
   static constexpr uint32_t kTmemCols = (2 + 2 * NP) * R <= 128 ? 128 : 256;
@@ -91,7 +93,7 @@ __device__ __forceinline__ void report(const AttendParams& P, int b, int bits) {
 }
 
 // ---------------------------------------------------------------------------
-// the tiles of a call, in order
+// the tiles of a call, in order: sequence, head, block, tile
 // ---------------------------------------------------------------------------
 
 // A sequence's lengths; a sequence with a data error has none.
@@ -117,57 +119,16 @@ __device__ __forceinline__ int keys_of(const AttendParams& P, const Lengths& s, 
 }
 __device__ __forceinline__ int tiles_of(int keys) { return max(1, (keys + kTile - 1) / kTile); }
 
-// One after another, the pieces of blocks that a CTA works on.
-template <int R>
-struct Walk {
-  int b, h, block;
-  Lengths s;
-  int keys, tiles;  // the block's
-  int t0, t1;       // the piece's tiles
-  long long left;   // of the CTA, after this piece
-
-  __device__ void start(const AttendParams& P, int seq, long long offset, long long units) {
-    b = seq;
-    left = units;
-    if (units == 0) return;
-    s = lengths_of(P, b);
-    long long per = 0;
-    for (int i = 0; i < P.blocks; ++i) per += tiles_of(keys_of<R>(P, s, i));
-    h = static_cast<int>(offset / per);
-    int rest = static_cast<int>(offset % per);
-    for (block = 0;; ++block) {
-      keys = keys_of<R>(P, s, block);
-      tiles = tiles_of(keys);
-      if (rest < tiles) break;
-      rest -= tiles;
-    }
-    t0 = t1 = rest;  // (an empty piece before the first)
-  }
-  __device__ bool next(const AttendParams& P) {
-    if (left == 0) return false;
-    if (t1 == tiles) {
-      if (++block == P.blocks) {
-        block = 0;
-        if (++h == P.H) {
-          h = 0;
-          s = lengths_of(P, ++b);
-        }
-      }
-      keys = keys_of<R>(P, s, block);
-      tiles = tiles_of(keys);
-      t1 = 0;
-    }
-    t0 = t1;
-    t1 = static_cast<int>(min(static_cast<long long>(tiles), t0 + left));
-    left -= t1 - t0;
-    return true;
-  }
-  __device__ __forceinline__ int row0() const { return block * R; }
-  // From this tile on, rows differ in what they see, or see nothing at the end.
-  __device__ __forceinline__ int first_special() const {
-    return s.count > 1 ? s.prefix / kTile : keys % kTile ? keys / kTile : 0x7fffffff;
-  }
+// A piece of a block: what one CTA does of it.
+struct Piece {
+  int b, h, block, prefix;  // b < 0: no more
+  int count, keys, t0, t1;  // keys: the tokens that the block's rows can see; t0, t1: the piece's tiles
+  int part, bad, pad0, pad1;  // part: -1 all of the block, 1 its first tiles, 0 others; bad: a sequence with a data error
 };
+// From this tile on, rows differ in what they see, or see nothing at the end.
+__device__ __forceinline__ int first_special(const Piece& w) {
+  return w.count > 1 ? w.prefix / kTile : w.keys % kTile ? w.keys / kTile : 0x7fffffff;
+}
 
 // ---------------------------------------------------------------------------
 // device helpers
@@ -177,6 +138,7 @@ struct Walk {
 // or elsewhere in the CTA, ends the role.
 __device__ __forceinline__ bool at_wait(uint64_t* bar, unsigned parity, volatile int* fault) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+#pragma unroll 1
   for (int i = 0; i < kMaxPolls; ++i) {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     if (__any_sync(0xffffffffu, *fault)) return false;
@@ -189,6 +151,18 @@ __device__ __forceinline__ bool one_lane() {
   uint32_t p;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
   return p != 0;
+}
+
+// The four warps of a warpgroup meet, and go on only if all of them can (so
+// that they leave a role together when a wait gave up).
+__device__ __forceinline__ bool meet(int id, bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.and.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(all)
+      : "r"(ok ? 1u : 0u), "r"(id)
+      : "memory");
+  return all != 0;
 }
 
 // Shared-memory matrix descriptor: the 8-row (K-major) or 8-step (MN-major)
@@ -217,13 +191,28 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, ui
       : "memory");
 }
 
+// 8 consecutive float32 columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+// N columns, a multiple of 8
 template <int N>
 __device__ __forceinline__ void tmem_columns(uint32_t at, float* v) {
-  if constexpr (N == 16) {
+  if constexpr (N >= 32) {
+    tmem_ld32(at, v);
+    if constexpr (N > 32) tmem_columns<N - 32>(at + 32, v + 32);
+  } else if constexpr (N >= 16) {
     tmem_ld16(at, v);
+    if constexpr (N > 16) tmem_columns<N - 16>(at + 16, v + 16);
   } else {
-#pragma unroll
-    for (int i = 0; i < N; i += 32) tmem_ld32(at + i, v + i);
+    tmem_ld8(at, v);
   }
 }
 
@@ -234,7 +223,7 @@ __device__ __forceinline__ float warp_max(float x) {
   return m;
 }
 
-// The warp's sums of N columns (N 16 or 32): lane i gets column i % N's.
+// The warp's sums of N columns (N a power of two): lane i gets column i % N's.
 template <int N>
 __device__ __forceinline__ float column_sums(float* v, int lane) {
 #pragma unroll
@@ -247,7 +236,8 @@ __device__ __forceinline__ float column_sums(float* v, int lane) {
     }
   }
   float s = v[0];
-  if (N == 16) s += __shfl_xor_sync(0xffffffffu, s, 16);
+#pragma unroll
+  for (int o = N; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   return s;
 }
 
@@ -264,17 +254,12 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
   lo = d;
 }
 
-// The warps of a role meet at `bar` (one arrival each; a bounded wait).
-__device__ __forceinline__ bool meet(uint64_t* bar, unsigned parity, bool leader, volatile int* fault) {
-  __syncwarp();
-  if (leader) mbar_arrive(bar);
-  return at_wait(bar, parity, fault);
-}
+__device__ __forceinline__ float4 lds_f4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
 struct PageScale {
-  float ck, ve;  // 2^key exponent (NaN: not a page), value exponent
-  int far;       // the tile's value exponents lie far apart
-  int pad;
+  float ck, ve;   // 2^key exponent (NaN: not a page), value exponent
+  float ve_low;   // the tile's least value exponent
+  int far;        // the tile's value exponents lie far apart
 };
 
 // ---------------------------------------------------------------------------
@@ -285,23 +270,30 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const AttendParams P) {
   using S = Shape<R, NP>;
+  constexpr int kW = R / 2;  // columns of a warpgroup
   extern __shared__ __align__(1024) unsigned char at_dyn[];
-  __shared__ uint64_t kfull[S::kStages], kempty[S::kStages], vfull[S::kStages], vempty[S::kStages];
   // sfull: a tile's scores are there; sempty: read; pfull: its weights are in
   // shared memory; pempty: read by the products; ofull / oempty: its outputs;
-  // mfull / mempty: its maxima and sums of weights
-  __shared__ uint64_t sfull[2], sempty[2], pfull[2], pempty[2], ofull[2], oempty[2], mfull[2], mempty[2];
-  __shared__ uint64_t qfull[2], qempty[2], landed[kPatchRing], patched[kPatchRing], drain;
-  // meetings within a role
-  __shared__ uint64_t most_met[2], ref_met[2], mix_met[2], row_met[2], parent_met[2];
+  // mfull / mempty: its factors (mix_s); efull / eempty: a piece's sums of
+  // weights; qfull / qempty: its queries; rfull / rempty: its record;
+  // landed: a patched tile's V is there; patched: it is patched
+  struct Bars {
+    uint64_t kfull[S::kStages], kempty[S::kStages], vfull[S::kStages], vempty[S::kStages];
+    uint64_t sfull[2], sempty[2], pfull[2], pempty[2], ofull[2], oempty[2], mfull[2], mempty[2], efull[2], eempty[2];
+    uint64_t qfull[2], qempty[2], landed[kPatchRing], patched[kPatchRing], rfull[kPieceRing], rempty[kPieceRing], drain;
+  };
+  constexpr int kBars = sizeof(Bars) / 8;
+  __shared__ Bars bar;
   __shared__ uint32_t tmem_s;
-  __shared__ int fault_s, k_issued_s, v_issued_s, start_b;
-  __shared__ long long start_off, warp_sums[kAttendThreads / 32];
-  __shared__ PageScale scale_s[kScaleRing][8];
-  __shared__ __align__(16) float most_s[2][4][R], ref_s[2][R], top_s[2][R], sum_s[2][4][R], cq_s[2][R];
-  __shared__ __align__(16) float2 mix_s[2][R];
-  __shared__ float row_s[R];
-  __shared__ unsigned char token_s[2][R], nan_s[kPatchRing][kTile];
+  __shared__ int fault_s, k_issued_s, v_issued_s;
+  __shared__ __align__(16) Piece piece_s[kPieceRing];
+  __shared__ __align__(16) PageScale scale_s[kScaleRing][8];
+  __shared__ __align__(16) float most_s[2][2][4][32], most_x_s[2][4][32], ref_s[8][3][32], cq_s[2][R], sum_s[2][4][R];
+  __shared__ __align__(16) float2 mix_s[2][R], end_s[2][R];
+  __shared__ __align__(16) float row_s[R];
+  __shared__ long long place_s[R];
+  __shared__ unsigned char token_s[2][R];
+  __shared__ unsigned nan_s[kPatchRing][kTile / 32];
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const bool leader = one_lane();
@@ -315,107 +307,60 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
   volatile int* fault = &fault_s;
 
   pdl_launch_dependents();
-  if (tid == 0) {
-    for (int s = 0; s < S::kStages; ++s) {
-      mbar_init(&kfull[s], 1);
-      mbar_init(&kempty[s], 1);
-      mbar_init(&vfull[s], 1);
-      mbar_init(&vempty[s], 1);
-    }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&sfull[s], 2);
-      mbar_init(&sempty[s], 4);
-      mbar_init(&pfull[s], 4);
-      mbar_init(&pempty[s], 1);
-      mbar_init(&ofull[s], 1);
-      mbar_init(&oempty[s], 4);
-      mbar_init(&mfull[s], 4);
-      mbar_init(&mempty[s], 4);
-      mbar_init(&most_met[s], 4);
-      mbar_init(&ref_met[s], 4);
-      mbar_init(&mix_met[s], 4);
-      mbar_init(&row_met[s], 4);
-      mbar_init(&parent_met[s], 2);
-      mbar_init(&qfull[s], 2);
-      mbar_init(&qempty[s], 4);
-    }
-    for (int s = 0; s < kPatchRing; ++s) {
-      mbar_init(&landed[s], 1);
-      mbar_init(&patched[s], 2);
-    }
-    mbar_init(&drain, 1);
-    fault_s = k_issued_s = v_issued_s = 0;
+  if (tid < kBars) {
+    uint64_t* at = reinterpret_cast<uint64_t*>(&bar) + tid;
+    unsigned count = 1;
+    if (at >= bar.sempty && at < bar.pempty) count = 8;           // sempty, pfull
+    if (at >= bar.oempty && at < bar.mfull) count = 4;            // oempty
+    if (at >= bar.sfull && at < bar.sempty) count = 2;            // sfull
+    if (at >= bar.mfull && at < bar.mempty) count = 2;            // mfull
+    if (at >= bar.mempty && at < bar.efull) count = 4;            // mempty
+    if (at >= bar.efull && at < bar.eempty) count = 8;            // efull
+    if (at >= bar.eempty && at < bar.qfull) count = 4;            // eempty
+    if (at >= bar.qempty && at < bar.landed) count = 4;           // qempty
+    if (at >= bar.rempty && at < &bar.drain) count = 15;          // rempty
+    mbar_init(at, count);
     mbar_fence_init();
   }
+  if (tid == 0) fault_s = k_issued_s = v_issued_s = 0;
   if (warp == 1) {
     tmem_alloc(&tmem_s, S::kTmemCols);
     tmem_relinquish();
   }
-  // the CTA's run of tiles
-  long long total, mine = 0, before;
-  const int per = (P.B + kAttendThreads - 1) / kAttendThreads;
-  const int b0 = min(P.B, tid * per), b1 = min(P.B, b0 + per);
-  const auto tiles_of_seq = [&](int b) {
-    const Lengths s = lengths_of(P, b);
-    long long t = 0;
-    for (int i = 0; i < P.blocks; ++i) t += tiles_of(keys_of<R>(P, s, i));
-    return t * P.H;
-  };
-  for (int b = b0; b < b1; ++b) mine += tiles_of_seq(b);
-  before = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, before, o);
-    if (lane >= o) before += x;
-  }
-  if (lane == 31) warp_sums[warp] = before;
-  before -= mine;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  total = 0;
-  for (int w = 0; w < kAttendThreads / 32; ++w) {
-    if (w == warp) before += total;
-    total += warp_sums[w];
-  }
-  const long long ctas = min(static_cast<long long>(gridDim.x), total);
-  const int cta = blockIdx.x;
-  const long long u0 = cta < ctas ? total * cta / ctas : total, u1 = cta < ctas ? total * (cta + 1) / ctas : total;
-  if (u0 < u1 && u0 >= before && u0 < before + mine) {
-    long long at = before;
-    for (int b = b0; b < b1; ++b) {
-      const long long t = tiles_of_seq(b);
-      if (u0 < at + t) {
-        start_b = b;
-        start_off = u0 - at;
-        break;
-      }
-      at += t;
-    }
-  }
-  __syncthreads();
   const uint32_t tmem_sc = tmem_s, tmem_o = tmem_s + 2 * R;
-  Walk<R> w;
-  w.start(P, u0 < u1 ? start_b : 0, u0 < u1 ? start_off : 0, u1 - u0);
+
+  // the next piece, for all roles but the one that makes them
+  int pieces = 0;
+  const auto next_piece = [&](Piece& w) {
+    const int s = pieces % kPieceRing;
+    if (!at_wait(&bar.rfull[s], static_cast<unsigned>(pieces / kPieceRing) & 1u, fault)) return false;
+    w = piece_s[s];
+    __syncwarp();
+    if (leader) mbar_arrive(&bar.rempty[s]);
+    ++pieces;
+    return w.b >= 0;
+  };
 
   if (warp == 0) {
     // ---------------- pages ----------------
-    const int pp = kTile / P.page, slot_in = lane % pp, batch = 32 / pp;
+    const int pp = kTile / P.page, slot_in = lane % pp, mine = lane / pp, batch = 32 / pp;
+    const unsigned page_bytes = static_cast<unsigned>(P.page) * 128u;
     int it = 0;
     bool ok = true;
-    while (ok && w.next(P)) {
+    Piece w;
+    while (ok && next_piece(w)) {
       if (w.keys == 0) continue;
       const int* table = P.block_table + static_cast<long long>(w.b) * P.table_pages;
       // the pages of `batch` tiles, a lane each
-      const auto page_of = [&](int tb) {
-        const int tile = tb + lane / pp, at = tile * pp + slot_in;
-        return tile < w.t1 && at * P.page < w.keys ? __ldg(table + at) : 0;
-      };
-      int ahead = page_of(w.t0);
+      const auto has_page = [&](int tb) { return tb + mine < w.t1 && ((tb + mine) * pp + slot_in) * P.page < w.keys; };
+      int ahead = has_page(w.t0) ? __ldg(table + (w.t0 + mine) * pp + slot_in) : 0;
+#pragma unroll 1
       for (int tb = w.t0; ok && tb < w.t1; tb += batch) {
+        const bool has = has_page(tb);
         int page = ahead;
-        const int mine_t = tb + lane / pp;
-        const bool has = mine_t < w.t1 && (mine_t * pp + slot_in) * P.page < w.keys;
         const bool bad = has && (page < 0 || page >= P.pages);
         if (bad) report(P, w.b, SPEC_ERR_CACHE);
         if (!has || bad) page = 0;
@@ -425,49 +370,46 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
           ke = __ldg(P.k_exps + slab);
           ve = __ldg(P.v_exps + slab);
         }
-        ahead = page_of(tb + batch);
+        if (has_page(tb + batch)) ahead = __ldg(table + (tb + batch + mine) * pp + slot_in);
         int lo = has ? ve : 127, hi = has ? ve : -127;
         for (int o = 1; o < pp; o <<= 1) {
           lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
           hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
         }
+        PageScale x;
+        x.ck = bad ? __uint_as_float(0x7fc00000u) : exp2i(ke);
+        x.ve = static_cast<float>(ve);
+        x.ve_low = static_cast<float>(lo);
+        x.far = hi - lo > kFar;
         const unsigned groups = __ballot_sync(0xffffffffu, has);
+        const int y = static_cast<int>(slab * P.page);
+#pragma unroll 1
         for (int i = 0; i < batch && tb + i < w.t1; ++i, ++it) {
           const int s = it % S::kStages;
           const unsigned parity = (static_cast<unsigned>(it / S::kStages) & 1u) ^ 1u;
-          const bool here = has && lane / pp == i;
-          const unsigned bytes =
-              static_cast<unsigned>(__popc(groups >> (i * pp) & ((1u << pp) - 1u))) * static_cast<unsigned>(P.page) * 128u * NP +
-              P.more_bytes;
-          ok = at_wait(&kempty[s], parity, fault);
+          const unsigned bytes = static_cast<unsigned>(__popc(groups >> (i * pp) & ((1u << pp) - 1u))) * page_bytes * NP +
+                                 P.more_bytes;
+          unsigned char* dst = kring + s * S::kSlot + slot_in * page_bytes;
+          ok = at_wait(&bar.kempty[s], parity, fault);
           if (!ok) break;
-          if (lane / pp == i) {
-            PageScale x;
-            x.ck = bad ? __uint_as_float(0x7fc00000u) : exp2i(ke);
-            x.ve = static_cast<float>(ve);
-            x.far = hi - lo > 100;
-            scale_s[it % kScaleRing][slot_in] = x;
-          }
+          if (mine == i) scale_s[it % kScaleRing][slot_in] = x;
           __syncwarp();
-          if (leader) mbar_expect_tx(&kfull[s], bytes);
+          if (leader) mbar_expect_tx(&bar.kfull[s], bytes);
           __syncwarp();
-          if (here) {
+          if (mine == i && has) {
 #pragma unroll
-            for (int p = 0; p < NP; ++p)
-              tma_load_2d(kring + s * S::kSlot + p * kPanel + slot_in * P.page * 128, &tm_k, p * 128,
-                          static_cast<int>(slab * P.page), &kfull[s]);
+            for (int p = 0; p < NP; ++p) tma_load_2d(dst + p * kPanel, &tm_k, p * 128, y, &bar.kfull[s]);
           }
           __syncwarp();
           if (leader) k_issued_s = it + 1;
-          ok = at_wait(&vempty[s], parity, fault);
+          ok = at_wait(&bar.vempty[s], parity, fault);
           if (!ok) break;
-          if (leader) mbar_expect_tx(&vfull[s], bytes);
+          if (leader) mbar_expect_tx(&bar.vfull[s], bytes);
           __syncwarp();
-          if (here) {
+          dst += S::kStages * S::kSlot;
+          if (mine == i && has) {
 #pragma unroll
-            for (int p = 0; p < NP; ++p)
-              tma_load_2d(vring + s * S::kSlot + p * kPanel + slot_in * P.page * 128, &tm_v, p * 128,
-                          static_cast<int>(slab * P.page), &vfull[s]);
+            for (int p = 0; p < NP; ++p) tma_load_2d(dst + p * kPanel, &tm_v, p * 128, y, &bar.vfull[s]);
           }
           __syncwarp();
           if (leader) v_issued_s = it + 1;
@@ -485,41 +427,47 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     const auto outputs = [&](int j, int patch) {
       const int s = j % S::kStages, d = j & 1;
       const unsigned half = static_cast<unsigned>(j >> 1) & 1u;
-      if (!at_wait(&vfull[s], static_cast<unsigned>(j / S::kStages) & 1u, fault)) return false;
-      if (patch >= 0 && !at_wait(&patched[patch % kPatchRing], static_cast<unsigned>(patch / kPatchRing) & 1u, fault))
+      if (!at_wait(&bar.vfull[s], static_cast<unsigned>(j / S::kStages) & 1u, fault)) return false;
+      if (patch >= 0 && !at_wait(&bar.patched[patch % kPatchRing], static_cast<unsigned>(patch / kPatchRing) & 1u, fault))
         return false;
-      if (!at_wait(&pfull[d], half, fault) || !at_wait(&oempty[d], half ^ 1u, fault)) return false;
+      if (!at_wait(&bar.oempty[d], half ^ 1u, fault) || !at_wait(&bar.pfull[d], half, fault)) return false;
       tc_fence_after();
       if (leader) {
-        const uint64_t b = operand(smem_addr(pbuf + 2 * d * S::kPHalf), 8 * R, R);
+        const uint64_t b = operand(smem_addr(pbuf + 2 * d * S::kPHalf), 8 * S::kPRow, S::kPRow);
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
           const uint64_t a = operand(smem_addr(vring + s * S::kSlot + p * kPanel), 1024, 128);
 #pragma unroll
           for (int k = 0; k < 2 * kTile / 32; ++k)  // hi's 4 steps of 32 tokens, then lo's
             umma_e4m3(tmem_o + (d * NP + p) * R, a + static_cast<uint64_t>((k & 3) * (32 * 128 >> 4)),
-                      b + static_cast<uint64_t>((k >> 2) * (S::kPHalf >> 4) + (k & 3) * (32 * R >> 4)), idesc_o, k != 0);
+                      b + static_cast<uint64_t>((k >> 2) * (S::kPHalf >> 4) + (k & 3) * (32 * S::kPRow >> 4)), idesc_o,
+                      k != 0);
         }
-        umma_commit(&ofull[d]);
-        umma_commit(&vempty[s]);
-        umma_commit(&pempty[d]);
+        umma_commit(&bar.ofull[d]);
+        umma_commit(&bar.vempty[s]);
+        umma_commit(&bar.pempty[d]);
       }
       __syncwarp();
       return true;
     };
-    while (ok && w.next(P)) {
-      if (w.keys == 0) continue;
-      const int special = w.first_special(), qb = qn & 1;
-      ok = at_wait(&qfull[qb], static_cast<unsigned>(qn >> 1) & 1u, fault);
-      for (int t = w.t0; ok && t < w.t1; ++t, ++it) {
+    // one loop over tiles and the step behind the last: the outputs of the tile before, in one place
+    Piece w;
+    bool more = next_piece(w);
+    while (more && w.keys == 0) more = next_piece(w);
+    int t = more ? w.t0 : 0, special = more ? first_special(w) : 0;
+    while (ok) {
+      int patch = -1;
+      if (more) {
         const int s = it % S::kStages, d = it & 1;
-        ok = at_wait(&kfull[s], static_cast<unsigned>(it / S::kStages) & 1u, fault) &&
-             at_wait(&sempty[d], (static_cast<unsigned>(it >> 1) & 1u) ^ 1u, fault);
+        if (t == w.t0) ok = at_wait(&bar.qfull[qn & 1], static_cast<unsigned>(qn >> 1) & 1u, fault);
+        ok = ok && at_wait(&bar.kfull[s], static_cast<unsigned>(it / S::kStages) & 1u, fault) &&
+             at_wait(&bar.sempty[d], (static_cast<unsigned>(it >> 1) & 1u) ^ 1u, fault);
         if (!ok) break;
         tc_fence_after();
         if (leader) {
           const uint64_t a = operand(smem_addr(kring + s * S::kSlot), 1024, 128);
-          const uint64_t b = operand(smem_addr(qbuf + 2 * qb * S::kQHalf), 1024, 128);
+          const uint64_t b = operand(smem_addr(qbuf + 2 * (qn & 1) * S::kQHalf), 1024, 128);
+#pragma unroll 1
           for (int half = 0; half < 2; ++half)
 #pragma unroll
             for (int k = 0; k < 4 * NP; ++k)
@@ -527,142 +475,254 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 umma_e4m3(tmem_sc + d * R, a + static_cast<uint64_t>((k >> 2) * (kPanel >> 4) + (k & 3) * 2),
                           b + static_cast<uint64_t>(half * (S::kQHalf >> 4) + (k >> 2) * (R * 128 >> 4) + (k & 3) * 2),
                           idesc_s, half != 0 || k != 0);
-          umma_commit(&sfull[d]);
-          umma_commit(&kempty[s]);
-          mbar_arrive(&sfull[d]);  // what the copies' and queries' warps wrote is visible behind it
+          umma_commit(&bar.sfull[d]);
+          umma_commit(&bar.kempty[s]);
+          mbar_arrive(&bar.sfull[d]);  // what the copies' and queries' warps wrote is visible behind it
         }
         __syncwarp();
         if (t >= special) {
           // (a warp that comes to a barrier's phase two phases early would pass: the
-          // patching warps, which skip tiles, are told when their tile's V is there)
-          ok = at_wait(&vfull[s], static_cast<unsigned>(it / S::kStages) & 1u, fault);
+          // patching warp, which skips tiles, is told when its tile's V is there)
+          ok = at_wait(&bar.vfull[s], static_cast<unsigned>(it / S::kStages) & 1u, fault);
           if (!ok) break;
-          if (leader) mbar_arrive(&landed[patches % kPatchRing]);
+          patch = patches++;
+          if (leader) mbar_arrive(&bar.landed[patch % kPatchRing]);
         }
-        if (it > 0) ok = outputs(it - 1, last_patch);
-        last_patch = t >= special ? patches++ : -1;
       }
-      ++qn;
+      if (it > 0) ok = outputs(it - 1, last_patch);
+      if (!more || !ok) break;
+      last_patch = patch;
+      ++it;
+      if (++t == w.t1) {
+        ++qn;
+        do more = next_piece(w);
+        while (more && w.keys == 0);
+        if (more) {
+          t = w.t0;
+          special = first_special(w);
+        }
+      }
     }
-    if (ok && it > 0) ok = outputs(it - 1, last_patch);
     // every product issued has completed before tensor memory is released
-    if (leader) umma_commit(&drain);
+    if (leader) umma_commit(&bar.drain);
     __syncwarp();
-    mbar_wait(&drain, 0);
-  } else if (warp < 4) {
-    // ---------------- queries, masks, what no row sees ----------------
-    const int me = tid - 64;
-    constexpr int kLanes = 16 * NP;          // lanes of a row, 8 elements each
-    constexpr int kAtOnce = 64 / kLanes;     // rows of the two warps at a time
-    const auto prepare = [&](const Walk<R>& x, int n) {
-      const int qb = n & 1;
-      if (!at_wait(&qempty[qb], (static_cast<unsigned>(n >> 1) & 1u) ^ 1u, fault)) return false;
-      unsigned char* dst = qbuf + 2 * qb * S::kQHalf;
-      const int row0 = x.row0(), tok0 = row0 / P.G, d0 = lane % kLanes * 8;
-      constexpr int kBatch = R / kAtOnce < 8 ? R / kAtOnce : 8;
+    mbar_wait(&bar.drain, 0);
+  } else if (warp == 2) {
+    // ---------------- pieces, queries, masks ----------------
+    const auto lengths = [&](int b) { return lengths_of(P, b); };
+    const auto tiles_of_seq = [&](const Lengths& s) {
+      int n = 0;
 #pragma unroll 1
-      for (int r1 = 0; r1 < R; r1 += kBatch * kAtOnce) {
-        uint4 raw[kBatch];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int r = r1 + i * kAtOnce + me / kLanes, row = row0 + r, tok = row / P.G, g = row % P.G;
-          raw[i] = make_uint4(0, 0, 0, 0);
-          if (tok < x.s.count && d0 < P.D)
-            raw[i] = *reinterpret_cast<const uint4*>(P.q + x.b * P.q_ld[0] + tok * P.q_ld[1] +
-                                                     (x.h * P.G + g) * P.q_ld[2] + d0);
-        }
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int r = r1 + i * kAtOnce + me / kLanes;
-          const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-          float v[8], most = 0.f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            v[e] = e & 1 ? bf16_hi(u[e / 2]) : bf16_lo(u[e / 2]);
-            if (fabsf(v[e]) < kInf) most = fmaxf(most, fabsf(v[e]));
-            else v[e] = __uint_as_float(0x7fc00000u);
-          }
-#pragma unroll
-          for (int o = kLanes / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-          // the least exponent with most <= 448 2^eq
-          const uint32_t bits = __float_as_uint(most);
-          int eq = static_cast<int>(bits >> 23) - 127 - ((bits & 0x7fffffu) <= 0x600000u ? 8 : 7);
-          eq = max(eq, -100);
-          const float f = exp2i(-eq);
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float a = v[2 * e] * f, c = v[2 * e + 1] * f;
-            hi[e] = pack_e4m3(a, c);
-            const float2 back = unpack_e4m3(hi[e]);
-            lo[e] = pack_e4m3(a - back.x, c - back.y);
-          }
-          const uint32_t at = (d0 >> 7) * R * 128 + swizzled(r * 128 + (d0 & 127), 128);
-          *reinterpret_cast<uint2*>(dst + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-          *reinterpret_cast<uint2*>(dst + S::kQHalf + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-          if (d0 == 0) {
-            cq_s[qb][r] = exp2i(eq) * P.c;
-            token_s[qb][r] = static_cast<unsigned char>((row0 + r) / P.G - tok0);
-          }
-        }
-      }
-      if (P.parent) {
-        // which of the block's rows' tokens see drafted token j
-        unsigned long long* mask = mask_s + qb * kMaxRows;
-        const int* parent = P.parent + static_cast<long long>(x.b) * P.n;
-        bool bad = false;
-        for (int j = me; j < x.s.count; j += 64) {
-          int p = j ? __ldg(parent + j) : 0;
-          if (j && (p < 0 || p >= j)) {
-            bad = true;
-            p = 0;
-          }
-          parent_s[j] = static_cast<unsigned short>(p);
-          mask[j] = 0;
-        }
-        if (bad && x.h == 0) report(P, x.b, SPEC_ERR_PARENT);
-        if (!meet(&parent_met[0], static_cast<unsigned>(n) & 1u, leader, fault)) return false;
-        const int tok = tok0 + me;
-        if (tok < x.s.count && tok * P.G < row0 + R) {
-          const unsigned long long bit = 1ull << me;
-          for (int j = tok;; j = parent_s[j]) {
-            atomicOr(mask + j, bit);
-            if (j == 0) break;
-          }
-        }
-        if (!meet(&parent_met[1], static_cast<unsigned>(n) & 1u, leader, fault)) return false;
-      }
-      fence_proxy_async();
-      __syncwarp();
-      if (leader) mbar_arrive(&qfull[qb]);
-      return true;
+      for (int i = 0; i < P.blocks; ++i) n += tiles_of(keys_of<R>(P, s, i));
+      return n * P.H;
     };
-    Walk<R> ahead = w;
-    int qn = 0, it = 0, patches = 0;
+    int total = 0;
+#pragma unroll 1
+    for (int b = lane; b < P.B; b += 32) total += tiles_of_seq(lengths(b));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    // equal runs: `more` CTAs have one tile more than the others
+    const int ctas = min(static_cast<int>(gridDim.x), total), cta = blockIdx.x;
+    const int each = total / ctas, more = total - each * ctas;
+    const auto first_tile = [&](int c) { return each * c + min(c, more); };
+    const int u0 = first_tile(min(cta, ctas)), u1 = first_tile(min(cta + 1, ctas));
+    int left = u1 - u0;
+    // the sequence of tile u0, and the tile's place in it
+    int b = 0, offset = 0;
+    if (left > 0) {
+      int before = 0;
+#pragma unroll 1
+      for (int b1 = 0;; b1 += 32) {
+        const int n = b1 + lane < P.B ? tiles_of_seq(lengths(b1 + lane)) : 0;
+        int up = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, up, o);
+          if (lane >= o) up += x;
+        }
+        const unsigned over = __ballot_sync(0xffffffffu, before + up > u0);
+        if (over) {
+          const int l = __ffs(over) - 1;
+          b = b1 + l;
+          offset = u0 - before - __shfl_sync(0xffffffffu, up - n, l);
+          break;
+        }
+        before += __shfl_sync(0xffffffffu, up, 31);
+      }
+    }
+    Lengths s = lengths(b);
+    int h = 0, block = 0, keys = 0, tiles = 0, t1 = 0;
+    if (left > 0) {
+      const int per = tiles_of_seq(s) / P.H;
+      h = offset / per;
+      offset -= h * per;
+#pragma unroll 1
+      for (;; ++block) {
+        keys = keys_of<R>(P, s, block);
+        tiles = tiles_of(keys);
+        if (offset < tiles) break;
+        offset -= tiles;
+      }
+      t1 = offset;
+    }
+    int4 shared = make_int4(0, 0, 0, 0);
+    int qn = 0, made = 0;
     bool ok = true;
-    const auto next_full = [&](Walk<R>& x) {
-      while (x.next(P))
-        if (x.keys) return true;
-      return false;
-    };
-    bool more = next_full(ahead);
-    if (more) ok = prepare(ahead, qn++);
-    while (ok && next_full(w)) {
-      if (more) more = next_full(ahead);
-      if (more) ok = prepare(ahead, qn++);
-      const int special = w.first_special();
-      it += w.t1 - w.t0;
-      for (int t = max(w.t0, special); ok && t < w.t1; ++t, ++patches) {
-        const int j = it - (w.t1 - t), s = j % S::kStages;
-        ok = at_wait(&landed[patches % kPatchRing], static_cast<unsigned>(patches / kPatchRing) & 1u, fault) &&
-             at_wait(&vfull[s], static_cast<unsigned>(j / S::kStages) & 1u, fault);
+#pragma unroll 1
+    while (ok) {
+      const bool last = left == 0;
+      const int t0 = t1;
+      if (!last) {
+        t1 = min(tiles, t0 + left);
+        left -= t1 - t0;
+      }
+      const int rs = made % kPieceRing;
+      ok = at_wait(&bar.rempty[rs], (static_cast<unsigned>(made / kPieceRing) & 1u) ^ 1u, fault);
+      if (!ok) break;
+      Piece w;
+      w.b = last ? -1 : b;
+      w.h = h;
+      w.block = block;
+      w.prefix = s.prefix;
+      w.count = s.count;
+      w.keys = keys;
+      w.t0 = t0;
+      w.t1 = t1;
+      w.part = t0 == 0 ? (t1 == tiles ? -1 : 1) : 0;
+      w.bad = s.bad;
+      w.pad0 = w.pad1 = 0;
+      if (leader) piece_s[rs] = w;
+      __syncwarp();
+      if (leader) mbar_arrive(&bar.rfull[rs]);
+      ++made;
+      if (last) break;
+      if (w.part == 1) {
+        // the block's last tile is another CTA's
+        const int u = u1 + (tiles - t1) - 1, few = each + 1;
+        const int c = u < few * more ? u / few : more + (u - few * more) / each;
+        shared = make_int4(b, h, block, c - cta + 1);
+      }
+      if (keys > 0) {
+        // the block's rows: two e4m3 numbers for each element
+        constexpr int kLanes = 16 * NP;       // lanes of a row, 8 elements each
+        constexpr int kAtOnce = 32 / kLanes;  // rows at a time
+        constexpr int kBatch = 8;
+        const int qb = qn & 1, row0 = block * R, tok0 = row0 / P.G, d0 = lane % kLanes * 8;
+        ok = at_wait(&bar.qempty[qb], (static_cast<unsigned>(qn >> 1) & 1u) ^ 1u, fault);
         if (!ok) break;
-        for (int row = me; row < kTile; row += 64) {
+        unsigned char* dst = qbuf + 2 * qb * S::kQHalf;
+        const bf16_t* q = P.q + b * P.q_ld[0] + static_cast<long long>(h) * P.G * P.q_ld[2] + d0;
+#pragma unroll 1
+        for (int r1 = 0; r1 < R; r1 += kBatch * kAtOnce) {
+          uint4 raw[kBatch];
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int row = row0 + r1 + i * kAtOnce + lane / kLanes, tok = row / P.G, g = row - tok * P.G;
+            raw[i] = make_uint4(0, 0, 0, 0);
+            if (tok < s.count && d0 < P.D && r1 + i * kAtOnce < R)
+              raw[i] = *reinterpret_cast<const uint4*>(q + tok * P.q_ld[1] + g * P.q_ld[2]);
+          }
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int r = r1 + i * kAtOnce + lane / kLanes;
+            if (r1 + i * kAtOnce >= R) break;
+            const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+            float v[8], most = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              v[e] = e & 1 ? bf16_hi(u[e / 2]) : bf16_lo(u[e / 2]);
+              if (fabsf(v[e]) < kInf) most = fmaxf(most, fabsf(v[e]));
+              else v[e] = __uint_as_float(0x7fc00000u);
+            }
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+            // the least exponent with most <= 448 2^eq
+            const uint32_t bits = __float_as_uint(most);
+            const int eq =
+                max(static_cast<int>(bits >> 23) - 127 - ((bits & 0x7fffffu) <= 0x600000u ? 8 : 7), -100);
+            const float f = exp2i(-eq);
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float a = v[2 * e] * f, c = v[2 * e + 1] * f;
+              hi[e] = pack_e4m3(a, c);
+              const float2 back = unpack_e4m3(hi[e]);
+              lo[e] = pack_e4m3(a - back.x, c - back.y);
+            }
+            const uint32_t at = (d0 >> 7) * R * 128 + swizzled(r * 128 + (d0 & 127), 128);
+            *reinterpret_cast<uint2*>(dst + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+            *reinterpret_cast<uint2*>(dst + S::kQHalf + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+            if (d0 == 0) {
+              cq_s[qb][r] = exp2i(eq) * P.c;
+              token_s[qb][r] = static_cast<unsigned char>((row0 + r) / P.G - tok0);
+            }
+          }
+        }
+        if (P.parent) {
+          // which of the block's rows' tokens see drafted token j
+          unsigned long long* mask = mask_s + qb * kMaxRows;
+          const int* parent = P.parent + static_cast<long long>(b) * P.n;
+          bool bad = false;
+          for (int j = lane; j < s.count; j += 32) {
+            int p = j ? __ldg(parent + j) : 0;
+            if (j && (p < 0 || p >= j)) {
+              bad = true;
+              p = 0;
+            }
+            parent_s[j] = static_cast<unsigned short>(p);
+            mask[j] = 0;
+          }
+          if (bad && h == 0) report(P, b, SPEC_ERR_PARENT);
+          __syncwarp();
+          for (int i = lane; i < R; i += 32) {
+            const int tok = tok0 + i;
+            if (tok >= s.count || tok * P.G >= row0 + R) break;
+            const unsigned long long bit = 1ull << i;
+            for (int j = tok;; j = parent_s[j]) {
+              atomicOr(mask + j, bit);
+              if (j == 0) break;
+            }
+          }
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (leader) mbar_arrive(&bar.qfull[qb]);
+        ++qn;
+      }
+      if (t1 == tiles && left > 0) {
+        if (++block == P.blocks) {
+          block = 0;
+          if (++h == P.H) {
+            h = 0;
+            s = lengths(++b);
+          }
+        }
+        keys = keys_of<R>(P, s, block);
+        tiles = tiles_of(keys);
+        t1 = 0;
+      }
+    }
+    if (leader) P.shared[cta] = ok ? shared : make_int4(0, 0, 0, 0);
+  } else if (warp == 3) {
+    // ---------------- what no row sees, and NaN values among the drafted tokens ----------------
+    int it = 0, patches = 0;
+    bool ok = true;
+    Piece w;
+    while (ok && next_piece(w)) {
+      if (w.keys == 0) continue;
+      it += w.t1 - w.t0;
+      for (int t = max(w.t0, first_special(w)); ok && t < w.t1; ++t, ++patches) {
+        const int j = it - (w.t1 - t), s = j % S::kStages;
+        ok = at_wait(&bar.landed[patches % kPatchRing], static_cast<unsigned>(patches / kPatchRing) & 1u, fault) &&
+             at_wait(&bar.vfull[s], static_cast<unsigned>(j / S::kStages) & 1u, fault);
+        if (!ok) break;
+#pragma unroll 1
+        for (int row = lane; row < kTile; row += 32) {
           const int pos = t * kTile + row;
           unsigned char* v = vring + s * S::kSlot + row * 128;
           bool clear = pos >= w.keys, nan = false;
-          if (!clear && pos >= w.s.prefix) {
-#pragma unroll
+          if (!clear && pos >= w.prefix) {
+#pragma unroll 1
             for (int p = 0; p < NP; ++p)
 #pragma unroll
               for (int o = 0; o < 128; o += 16) {
@@ -673,130 +733,177 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             clear = nan;
           }
           if (clear) {
-#pragma unroll
+#pragma unroll 1
             for (int p = 0; p < NP; ++p)
 #pragma unroll
               for (int o = 0; o < 128; o += 16) *reinterpret_cast<uint4*>(v + p * kPanel + o) = make_uint4(0, 0, 0, 0);
           }
-          nan_s[patches % kPatchRing][row] = nan;
+          const unsigned all = __ballot_sync(0xffffffffu, nan);
+          if (leader) nan_s[patches % kPatchRing][row >> 5] = all;
         }
         fence_proxy_async();
         __syncwarp();
-        if (leader) mbar_arrive(&patched[patches % kPatchRing]);
+        if (leader) mbar_arrive(&bar.patched[patches % kPatchRing]);
       }
     }
   } else if (warp < 12) {
     // ---------------- weights ----------------
-    const int grp = (warp - 4) >> 2, q = warp & 3, row = q * 32 + lane;
+    // Both warpgroups work on every tile, each on half of the block's rows.
+    const int grp = (warp - 4) >> 2, q = warp & 3, row = q * 32 + lane, col0 = grp * kW;
     const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
+    const int page_row = row / P.page;
+    float* refs = ref_s[warp - 4][0];
     int it = 0, qn = 0, patches = 0;
-    bool ok = true;
-    while (ok && w.next(P)) {
+    bool ok = true;  // (what a wait of this warp's gave; the warpgroup goes by what its warps agree on)
+    Piece w;
+    while (true) {
+      const bool got = next_piece(w);
+      if (!meet(1 + grp, got)) break;
       if (w.keys == 0) continue;
-      const int special = w.first_special(), qb = qn & 1, tok0 = w.row0() / P.G;
-      for (int t = w.t0; ok && t < w.t1; ++t, ++it) {
-        const int patch = t >= special ? patches++ : -1;
-        if ((it & 1) != grp) continue;
+      const int special = first_special(w), qb = qn & 1, tok0 = w.block * R / P.G;
+      // lane i < kW, row col0 + i: log2 of the outputs' unit and of the sums'
+      float unit = -kInf, sum_unit = -kInf;
+      float2 sum[kW / 2];
+#pragma unroll
+      for (int i = 0; i < kW / 2; ++i) sum[i] = make_float2(0.f, 0.f);
+      bool go = true;
+#pragma unroll 1
+      for (int t = w.t0; t < w.t1; ++t, ++it) {
+        const int k = it & 1;
         const unsigned half = static_cast<unsigned>(it >> 1) & 1u;
-        ok = at_wait(&sfull[grp], half, fault);
-        if (!ok) break;
+        ok = at_wait(&bar.sfull[k], half, fault) && ok;
         tc_fence_after();
-        float y[R];
-        tmem_columns<R>(tmem_sc + grp * R + lanes, y);
+        float y[kW];
+        tmem_columns<kW>(tmem_sc + k * R + col0 + lanes, y);
         tc_fence_before();
         __syncwarp();
-        if (leader) mbar_arrive(&sempty[grp]);
-        const PageScale ps = scale_s[it % kScaleRing][row / P.page];
+        if (leader) mbar_arrive(&bar.sempty[k]);
+        const PageScale ps = scale_s[it % kScaleRing][page_row];
+        // y = score + value exponent
 #pragma unroll
-        for (int r = 0; r < R; r += 4) {
-          const float4 c = *reinterpret_cast<const float4*>(&cq_s[qb][r]);
-          y[r] = __fmaf_rn(y[r] * c.x, ps.ck, ps.ve);
-          y[r + 1] = __fmaf_rn(y[r + 1] * c.y, ps.ck, ps.ve);
-          y[r + 2] = __fmaf_rn(y[r + 2] * c.z, ps.ck, ps.ve);
-          y[r + 3] = __fmaf_rn(y[r + 3] * c.w, ps.ck, ps.ve);
+        for (int r = 0; r < kW; r += 4) {
+          const float4 c = lds_f4(&cq_s[qb][col0 + r]);
+          const float2 ck = make_float2(ps.ck, ps.ck), ve = make_float2(ps.ve, ps.ve);
+          const float2 a = ffma2(fmul2(make_float2(y[r], y[r + 1]), make_float2(c.x, c.y)), ck, ve);
+          const float2 b = ffma2(fmul2(make_float2(y[r + 2], y[r + 3]), make_float2(c.z, c.w)), ck, ve);
+          y[r] = a.x, y[r + 1] = a.y, y[r + 2] = b.x, y[r + 3] = b.y;
         }
-        if (patch >= 0) {
-          ok = at_wait(&patched[patch % kPatchRing], static_cast<unsigned>(patch / kPatchRing) & 1u, fault);
-          if (!ok) break;
-          const int pos = t * kTile + row, j = pos - w.s.prefix;
+        if (t >= special) {
+          const int patch = patches++;
+          ok = ok && at_wait(&bar.patched[patch % kPatchRing], static_cast<unsigned>(patch / kPatchRing) & 1u, fault);
+          const int pos = t * kTile + row, j = pos - w.prefix;
           unsigned long long seen = ~0ull;
           if (pos >= w.keys) seen = 0;
           else if (j >= 0 && P.parent) seen = mask_s[qb * kMaxRows + j];
           else if (j > tok0) seen = j - tok0 > 63 ? 0 : ~0ull << (j - tok0);
-          const bool nan = nan_s[patch % kPatchRing][row];
+          const bool nan = nan_s[patch % kPatchRing][q] >> lane & 1u;
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
+          for (int r = 0; r < kW; ++r) {
             if (nan) y[r] = __uint_as_float(0x7fc00000u);
-            if (!(seen >> token_s[qb][r] & 1ull)) y[r] = -kInf;
+            if (!(seen >> token_s[qb][col0 + r] & 1ull)) y[r] = -kInf;
           }
         }
-        // the columns' largest
-        float keep[R / 32 + 1];
+        // the rows' largest
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const float m = warp_max(y[r]);
-          if ((r & 31) == 0 || lane == (r & 31)) keep[r / 32] = m;
+        for (int r = 0; r < kW; r += 4) {
+          const float4 m = make_float4(warp_max(y[r]), warp_max(y[r + 1]), warp_max(y[r + 2]), warp_max(y[r + 3]));
+          if (leader) *reinterpret_cast<float4*>(&most_s[grp][k][q][r]) = m;
         }
-        ok = at_wait(&mempty[grp], half ^ 1u, fault);
-        if (!ok) break;
+        if (ps.far) {
 #pragma unroll
-        for (int r = 0; r < R; r += 32)
-          if (r + lane < R) most_s[grp][q][r + lane] = keep[r / 32];
-        ok = meet(&most_met[grp], half, leader, fault);
-        if (!ok) break;
-        if (row < R) {
-          const float m = fmaxf(fmaxf(most_s[grp][0][row], most_s[grp][1][row]),
-                                fmaxf(most_s[grp][2][row], most_s[grp][3][row]));
-          top_s[grp][row] = m - 8.f;
-          ref_s[grp][row] = m == -kInf ? 0.f : m - 8.f;
+          for (int r = 0; r < kW; ++r) {
+            const float m = warp_max(y[r] - ps.ve);
+            if (leader) most_x_s[grp][q][r] = m;
+          }
         }
-        ok = meet(&ref_met[grp], half, leader, fault);
-        if (!ok) break;
-        float e[R];
-#pragma unroll
-        for (int r = 0; r < R; r += 4) {
-          const float4 c = *reinterpret_cast<const float4*>(&ref_s[grp][r]);
-          e[r] = ex2(y[r] - c.x);
-          e[r + 1] = ex2(y[r + 1] - c.y);
-          e[r + 2] = ex2(y[r + 2] - c.z);
-          e[r + 3] = ex2(y[r + 3] - c.w);
+        go = meet(1 + grp, ok);
+        if (!go) break;
+        {
+          // every warp for itself: lane i's row
+          const float m = fmaxf(fmaxf(most_s[grp][k][0][lane], most_s[grp][k][1][lane]),
+                                fmaxf(most_s[grp][k][2][lane], most_s[grp][k][3][lane]));
+          const bool none = m == -kInf;
+          const float top = m - 8.f;
+          // of the scores without exponents, the sums' reference: the largest, or a bound of it
+          float most_x = m - ps.ve_low;
+          if (ps.far)
+            most_x = fmaxf(fmaxf(most_x_s[grp][0][lane], most_x_s[grp][1][lane]),
+                           fmaxf(most_x_s[grp][2][lane], most_x_s[grp][3][lane]));
+          const float next = fmaxf(unit, top), next_x = fmaxf(sum_unit, most_x);
+          refs[lane] = none ? 0.f : top;
+          refs[32 + lane] = sum_unit == -kInf ? 0.f : ex2(sum_unit - next_x);
+          refs[64 + lane] = none ? 0.f : ps.far ? next_x : ex2(most_x - next_x) * 0.00390625f;
+          if (q == 0) {
+            ok = at_wait(&bar.mempty[k], half ^ 1u, fault);
+            if (lane < kW)
+              mix_s[k][col0 + lane] = make_float2(unit == -kInf ? 0.f : ex2(unit - next), none ? 0.f : ex2(top - next));
+          }
+          unit = next;
+          sum_unit = next_x;
+          __syncwarp();
+          if (q == 0 && leader) mbar_arrive(&bar.mfull[k]);
         }
-        ok = at_wait(&pempty[grp], half ^ 1u, fault);
-        if (!ok) break;
-        unsigned char* p = pbuf + 2 * grp * S::kPHalf;
+        if (ps.far) {
+          // (2^(y - reference) may underflow where a page's values are tiny against another's)
 #pragma unroll
-        for (int r = 0; r < R; r += 16) {
-          uint32_t hi[8], lo[8];
+          for (int r = 0; r < kW; r += 2) {
+            sum[r / 2].x = __fmaf_rn(sum[r / 2].x, refs[32 + r], ex2((y[r] - ps.ve) - refs[64 + r]));
+            sum[r / 2].y = __fmaf_rn(sum[r / 2].y, refs[33 + r], ex2((y[r + 1] - ps.ve) - refs[65 + r]));
+          }
+          meet(1 + grp, true);  // (there is one most_x_s)
+        }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) split2(e[r + 2 * i], e[r + 2 * i + 1], hi[i], lo[i]);
-          const uint32_t at = swizzled(row * R + r, R);
-          *reinterpret_cast<uint4*>(p + at) =
-              make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, hi[4] | hi[5] << 16, hi[6] | hi[7] << 16);
-          *reinterpret_cast<uint4*>(p + S::kPHalf + at) =
-              make_uint4(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16, lo[4] | lo[5] << 16, lo[6] | lo[7] << 16);
+        for (int r = 0; r < kW; r += 4) {
+          const float4 c = lds_f4(refs + r);
+          y[r] = ex2(y[r] - c.x);
+          y[r + 1] = ex2(y[r + 1] - c.y);
+          y[r + 2] = ex2(y[r + 2] - c.z);
+          y[r + 3] = ex2(y[r + 3] - c.w);
+        }
+        ok = at_wait(&bar.pempty[k], half ^ 1u, fault) && ok;
+        unsigned char* p = pbuf + 2 * k * S::kPHalf;
+#pragma unroll
+        for (int r = 0; r < kW; r += 8) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) split2(y[r + 2 * i], y[r + 2 * i + 1], hi[i], lo[i]);
+          const uint32_t at = swizzled(row * S::kPRow + col0 + r, S::kPRow);
+          *reinterpret_cast<uint2*>(p + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+          *reinterpret_cast<uint2*>(p + S::kPHalf + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
         }
         fence_proxy_async();
         __syncwarp();
-        if (leader) mbar_arrive(&pfull[grp]);
-        // the sums of the weights themselves: without the values' exponents
+        if (leader) mbar_arrive(&bar.pfull[k]);
         if (!ps.far) {
-          const float f = exp2i(-static_cast<int>(ps.ve));
+          // the sums of the weights themselves: without the values' exponents
+          const float f = exp2i(static_cast<int>(ps.ve_low - ps.ve));
 #pragma unroll
-          for (int r = 0; r < R; ++r) e[r] *= f;
-        } else {
-          // (2^(y - reference) may underflow where a page's values are tiny against another's)
-#pragma unroll
-          for (int r = 0; r < R; ++r) e[r] = ex2((y[r] - ref_s[grp][r]) - ps.ve);
+          for (int r = 0; r < kW; r += 4) {
+            const float4 a = lds_f4(refs + 32 + r), b = lds_f4(refs + 64 + r);
+            sum[r / 2] = ffma2(sum[r / 2], make_float2(a.x, a.y),
+                               fmul2(make_float2(y[r], y[r + 1]), fmul2(make_float2(b.x, b.y), make_float2(f, f))));
+            sum[r / 2 + 1] = ffma2(sum[r / 2 + 1], make_float2(a.z, a.w),
+                                   fmul2(make_float2(y[r + 2], y[r + 3]), fmul2(make_float2(b.z, b.w), make_float2(f, f))));
+          }
         }
-        constexpr int kSum = R < 32 ? R : 32;
-#pragma unroll
-        for (int r = 0; r < R; r += kSum) {
-          const float s = column_sums<kSum>(e + r, lane);
-          if (lane < kSum) sum_s[grp][q][r + lane] = s;
-        }
-        __syncwarp();
-        if (leader) mbar_arrive(&mfull[grp]);
       }
+      // the piece's sums and units
+      if (!go) break;
+      ok = at_wait(&bar.eempty[qb], (static_cast<unsigned>(qn >> 1) & 1u) ^ 1u, fault) && ok;
+      if (!meet(1 + grp, ok)) break;
+      float all[kW];
+#pragma unroll
+      for (int i = 0; i < kW / 2; ++i) all[2 * i] = sum[i].x, all[2 * i + 1] = sum[i].y;
+      constexpr int kFirst = kW == 24 ? 16 : kW;
+      const float s = column_sums<kFirst>(all, lane);
+      if (lane < kFirst) sum_s[qb][q][col0 + lane] = s;
+      if constexpr (kW == 24) {
+        const float s2 = column_sums<8>(all + 16, lane);
+        if (lane < 8) sum_s[qb][q][col0 + 16 + lane] = s2;
+      }
+      if (q == 0 && lane < kW) end_s[qb][col0 + lane] = make_float2(unit, sum_unit);
+      __syncwarp();
+      if (leader) mbar_arrive(&bar.efull[qb]);
       ++qn;
     }
   } else {
@@ -804,113 +911,101 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     const int q = warp & 3, d = q * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
     int it = 0, qn = 0;
-    unsigned whole = 0;
     bool ok = true;
-    while (ok && w.next(P)) {
+    Piece w;
+    while (true) {
+      const bool got = next_piece(w);
+      if (!meet(3, got)) break;
+      const int row0 = w.block * R;
       if (w.keys == 0) {
-        if (w.s.bad || w.s.count < P.n) {
-          // rows of nothing
-          for (int r = 0; r < R && w.row0() + r < P.n * P.G; ++r) {
-            bf16_t* out = P.out + w.b * P.out_ld[0] + (w.row0() + r) / P.G * P.out_ld[1] +
-                          (w.h * P.G + (w.row0() + r) % P.G) * P.out_ld[2];
-            for (int e = d; e < P.D; e += 128) out[e] = 0;
-          }
+        // rows of nothing
+        for (int r = row0; r < min(row0 + R, P.n * P.G); ++r) {
+          const int tok = r / P.G;
+          bf16_t* out = P.out + w.b * P.out_ld[0] + tok * P.out_ld[1] + (w.h * P.G + r - tok * P.G) * P.out_ld[2];
+          for (int e = d; e < P.D; e += 128) out[e] = 0;
         }
-        if (w.s.bad && w.h == 0 && w.block == 0 && d == 0) report(P, w.b, SPEC_ERR_CACHE);
+        if (w.bad && w.h == 0 && w.block == 0 && d == 0) report(P, w.b, SPEC_ERR_CACHE);
         continue;
       }
-      float acc[NP][R];
+      const int qb = qn & 1;
+      const unsigned piece_half = static_cast<unsigned>(qn >> 1) & 1u;
+      float2 acc[NP][R / 2];
 #pragma unroll
       for (int p = 0; p < NP; ++p)
 #pragma unroll
-        for (int r = 0; r < R; ++r) acc[p][r] = 0.f;
-      // row d's: log2 of the unit of acc, the sum of weights and log2 of its unit
-      float unit = -kInf, sum = 0.f, sum_unit = -kInf;
+        for (int r = 0; r < R / 2; ++r) acc[p][r] = make_float2(0.f, 0.f);
+#pragma unroll 1
       for (int t = w.t0; ok && t < w.t1; ++t, ++it) {
         const int k = it & 1;
         const unsigned half = static_cast<unsigned>(it >> 1) & 1u;
-        ok = at_wait(&mfull[k], half, fault);
-        if (!ok) break;
-        if (d < R) {
-          const float top = top_s[k][d];
-          const float s = (sum_s[k][0][d] + sum_s[k][1][d]) + (sum_s[k][2][d] + sum_s[k][3][d]);
-          const float next = fmaxf(unit, top), ref = next == -kInf ? 0.f : next;
-          mix_s[k][d] = make_float2(unit == -kInf ? 0.f : ex2(unit - ref), top == -kInf ? 0.f : ex2(top - ref));
-          unit = next;
-          if (s != 0.f) {  // (a NaN too)
-            // s = part 2^power; the sums' unit is the largest 2^(top + power) so far
-            const int power = static_cast<int>(__float_as_uint(s) >> 23 & 255u) - 127;
-            const float su = (top == -kInf ? 0.f : top) + static_cast<float>(power);
-            const float sn = fmaxf(sum_unit, su);
-            sum = (sum_unit == -kInf ? 0.f : sum * ex2(sum_unit - sn)) + s * exp2i(min(126, max(-126, -power))) * ex2(su - sn);
-            sum_unit = sn;
-          }
-        }
-        __syncwarp();
-        if (leader) mbar_arrive(&mempty[k]);
-        ok = meet(&mix_met[k], half, leader, fault) && at_wait(&ofull[k], half, fault);
+        ok = at_wait(&bar.mfull[k], half, fault) && at_wait(&bar.ofull[k], half, fault);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
           if (p * 128 + q * 32 >= P.D) break;
-          float o[R];
-          tmem_columns<R>(tmem_o + (k * NP + p) * R + lanes, o);
 #pragma unroll
-          for (int r = 0; r < R; r += 2) {
-            const float4 m = *reinterpret_cast<const float4*>(&mix_s[k][r]);
-            acc[p][r] = __fmaf_rn(o[r], m.y, acc[p][r] * m.x);
-            acc[p][r + 1] = __fmaf_rn(o[r + 1], m.w, acc[p][r + 1] * m.z);
+          for (int r = 0; r < R; r += 16) {
+            float o[16];
+            tmem_ld16(tmem_o + (k * NP + p) * R + r + lanes, o);
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const float4 m = *reinterpret_cast<const float4*>(&mix_s[k][r + e]);
+              float2& x = acc[p][(r + e) / 2];
+              x = ffma2(make_float2(o[e], o[e + 1]), make_float2(m.y, m.w), fmul2(x, make_float2(m.x, m.z)));
+            }
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (leader) mbar_arrive(&oempty[k]);
+        if (leader) {
+          mbar_arrive(&bar.oempty[k]);
+          mbar_arrive(&bar.mempty[k]);
+        }
       }
-      if (!ok) break;
-      if (leader) mbar_arrive(&qempty[qn & 1]);
+      ok = ok && at_wait(&bar.efull[qb], piece_half, fault);
+      if (!meet(3, ok)) break;
+      constexpr int kLd = NP * 128 + 4;
+      float* part = P.parts + (static_cast<long long>(2 * blockIdx.x) + max(w.part, 0)) * R * kLd;
+      if (d < R) {
+        const float s = (sum_s[qb][0][d] + sum_s[qb][1][d]) + (sum_s[qb][2][d] + sum_s[qb][3][d]);
+        const float2 end = end_s[qb][d];
+        if (w.part < 0) {
+          const int tok = (row0 + d) / P.G, g = row0 + d - tok * P.G;
+          row_s[d] = s == 0.f ? 0.f : ex2(end.x - end.y) / s;
+          place_s[d] = tok >= P.n ? -1 : w.b * P.out_ld[0] + tok * P.out_ld[1] + (w.h * P.G + g) * P.out_ld[2];
+          if (tok >= w.count) row_s[d] = 0.f;
+        } else {
+          float* e = part + d * kLd + NP * 128;
+          __stcg(e, end.x);
+          __stcg(e + 1, s);
+          __stcg(e + 2, end.y);
+        }
+      }
+      if (!meet(3, true)) break;
+      if (leader) {
+        mbar_arrive(&bar.qempty[qb]);
+        mbar_arrive(&bar.eempty[qb]);
+      }
       ++qn;
-      if (w.t0 == 0 && w.t1 == w.tiles) {
-        if (d < R) row_s[d] = sum == 0.f ? 0.f : ex2(unit - sum_unit) / sum;
-        ok = meet(&row_met[0], whole & 1u, leader, fault);
-        if (!ok) break;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const int row = w.row0() + r, tok = row / P.G;
-          if (tok >= P.n) break;
-          bf16_t* out = P.out + w.b * P.out_ld[0] + tok * P.out_ld[1] + (w.h * P.G + row % P.G) * P.out_ld[2];
-          const float f = row_s[r];
+      for (int r = 0; r < R; ++r) {
+        const long long at = w.part < 0 ? place_s[r] : r * kLd;
+        if (at < 0) break;
 #pragma unroll
-          for (int p = 0; p < NP; ++p) {
+        for (int p = 0; p < NP; ++p) {
+          const float v = r & 1 ? acc[p][r / 2].y : acc[p][r / 2].x;
+          if (w.part < 0) {
             unsigned short bits;
-            asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(bits) : "f"(tok < w.s.count ? acc[p][r] * f : 0.f));
-            if (p * 128 + d < P.D) out[p * 128 + d] = bits;
+            const float f = row_s[r];
+            asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(bits) : "f"(f == 0.f ? 0.f : v * f));
+            if (p * 128 + d < P.D) P.out[at + p * 128 + d] = bits;
+          } else {
+            __stcg(part + at + p * 128 + d, v);
           }
         }
-        ok = meet(&row_met[1], whole++ & 1u, leader, fault);
-      } else {
-        constexpr int kLd = NP * 128 + 4;
-        float* part = P.parts + (static_cast<long long>(2 * cta) + (w.t0 == 0 ? 1 : 0)) * R * kLd;
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-          for (int p = 0; p < NP; ++p) __stcg(part + r * kLd + p * 128 + d, acc[p][r]);
-        if (d < R) {
-          float* end = part + d * kLd + NP * 128;
-          __stcg(end, unit);
-          __stcg(end + 1, sum);
-          __stcg(end + 2, sum_unit);
-        }
       }
-    }
-    // the block that this CTA begins and others end
-    if (ok && d == 0 && cta < ctas) {
-      int4 x = make_int4(0, 0, 0, 0);
-      if (u1 > u0 && w.t0 == 0 && w.t1 < w.tiles) {
-        const long long last = u1 + (w.tiles - w.t1) - 1;  // the block's last tile
-        x = make_int4(w.b, w.h, w.block, static_cast<int>(((last + 1) * ctas - 1) / total) - cta + 1);
-      }
-      P.shared[cta] = x;
+      if (!meet(3, true)) break;
     }
   }
 
@@ -919,13 +1014,12 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     // copies still in flight land before the CTA exits: wait (bounded) for
     // the last phase of every stage that was issued
     for (int k = max(0, k_issued_s - S::kStages); k < k_issued_s; ++k)
-      mbar_wait(&kfull[k % S::kStages], static_cast<unsigned>(k / S::kStages) & 1u);
+      mbar_wait(&bar.kfull[k % S::kStages], static_cast<unsigned>(k / S::kStages) & 1u);
     for (int k = max(0, v_issued_s - S::kStages); k < v_issued_s; ++k)
-      mbar_wait(&vfull[k % S::kStages], static_cast<unsigned>(k / S::kStages) & 1u);
+      mbar_wait(&bar.vfull[k % S::kStages], static_cast<unsigned>(k / S::kStages) & 1u);
     if (P.error_word) atomicOr(P.error_word, SPEC_ERR_INTERNAL);
-    P.shared[cta] = make_int4(0, 0, 0, 0);
+    P.shared[blockIdx.x] = make_int4(0, 0, 0, 0);
   }
-  if (tid == 0 && cta >= ctas) P.shared[cta] = make_int4(0, 0, 0, 0);
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
@@ -993,7 +1087,7 @@ bool good_shape(int B, int n, int Hq, int H, int D) {
 
 int block_rows(int n, int G, int D) {
   const int rows = n * G;
-  return rows <= 16 ? 16 : rows <= 32 || D > 128 ? 32 : 64;
+  return rows <= 16 ? 16 : rows <= 32 || D > 128 ? 32 : rows <= 48 ? 48 : 64;
 }
 
 size_t attend_workspace(int n, int Hq, int H, int D) {
@@ -1036,13 +1130,16 @@ std::atomic<unsigned> g_more_bytes{0};
 
 template <int R, int NP>
 spec_status launch_attend(const spec_attend_args& a, AttendParams& p, cudaStream_t s) {
+  p.blocks = (a.n * p.G + R - 1) / R;
+  // tiles are counted in 31 bits
+  const long long most = static_cast<long long>(a.table_pages) * a.page / kTile + 1;
+  if (most * p.blocks * a.H * a.B > 0x7fffffffLL) return SPEC_EINVAL;
   const int nsm = sm_count();
   if (nsm < 1) return SPEC_ECUDA;
   const long long rows = static_cast<long long>(a.pages) * a.H * a.page;
   CUtensorMap tk, tv;
   if (!code_map(&tk, a.k_codes, rows, a.D, a.page) || !code_map(&tv, a.v_codes, rows, a.D, a.page)) return SPEC_ECUDA;
   if (raise_smem<R, NP>() != cudaSuccess) return SPEC_ECUDA;
-  p.blocks = (a.n * p.G + R - 1) / R;
   p.more_bytes = g_more_bytes.load();
   const int ctas = std::min(nsm, kMaxCtas);
   attend_kernel<R, NP><<<ctas, kAttendThreads, Shape<R, NP>::kSmem, s>>>(tk, tv, p);
@@ -1118,6 +1215,7 @@ extern "C" spec_status spec_attend_cache(const spec_attend_args* a, cudaStream_t
   switch (R) {
     case 16: return launch_attend<16, 1>(*a, p, stream);
     case 32: return launch_attend<32, 1>(*a, p, stream);
+    case 48: return launch_attend<48, 1>(*a, p, stream);
     default: return launch_attend<64, 1>(*a, p, stream);
   }
 }

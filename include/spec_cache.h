@@ -213,7 +213,9 @@ typedef struct spec_attend_args {
 
 /* 0 for sizes outside the limits.                                           */
 size_t spec_attend_workspace_size(int B, int n, int Hq, int H, int D);
-/* SPEC_EINVAL, SPEC_EALIGN, SPEC_EWORKSPACE, SPEC_ECUDA as above.           */
+/* SPEC_EINVAL (also where B * H * ceil(n * Hq / H / 16) * (table_pages *     */
+/* page / 128 + 1) could reach 2^31), SPEC_EALIGN, SPEC_EWORKSPACE, SPEC_ECUDA */
+/* as above.                                                                 */
 spec_status spec_attend_cache(const spec_attend_args* args, cudaStream_t stream);
 
 /* Test hook for its bounded waits, as spec_verify.h has them for the          */
