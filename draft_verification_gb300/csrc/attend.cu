@@ -50,13 +50,18 @@ constexpr int kTile = 128;      // tokens per tile
 constexpr int kPanel = 16384;   // bytes of 128 tokens x 128 elements
 constexpr int kMaxRows = 1024;  // n
 constexpr int kMaxCtas = 160;
-constexpr int kAttendThreads = 512;
 constexpr int kScaleRing = 16, kPatchRing = 8, kPieceRing = 4;
+constexpr int kScores = 4;  // places of tiles' scores: those are two tiles ahead of the outputs, every group meets all phases of its places
 constexpr int kFar = 30;  // value exponents of a tile that lie further apart than this
 
 // R: a block's rows; NP: panels of 128 elements of a head.
 template <int R, int NP>
 struct Shape {
+  // the softmax warpgroups: kGroups, each with kW of the block's rows, of every
+  // tile or of every other one
+  static constexpr int kW = R == 16 ? 8 : 16, kColumns = R / kW, kTurns = kColumns == 2 ? 2 : 1;
+  static constexpr int kGroups = kColumns * kTurns;
+  static constexpr int kThreads = 128 * (2 + kGroups);
   static constexpr int kStages = NP == 1 ? (R > 32 ? 4 : 5) : 2;
   static constexpr int kPRow = R == 48 ? 64 : R;  // bytes of a token's weights
   static constexpr int kSlot = NP * kPanel;
@@ -64,8 +69,9 @@ struct Shape {
   static constexpr int kPHalf = kTile * kPRow;  // hi or lo of a tile's weights
   static constexpr int kMaskBytes = 2 * kMaxRows * 8;
   static constexpr int kSmem = 1024 + 2 * kStages * kSlot + 4 * kQHalf + 4 * kPHalf + kMaskBytes + kMaxRows * 2;
-  static constexpr uint32_t kTmemCols = (2 + 2 * NP) * R <= 128 ? 128 : 256;
-  static_assert((2 + 2 * NP) * R <= 256 && kStages + 3 <= kScaleRing && kStages < kPatchRing, "rings");
+  static constexpr int kCols = (kScores + 2 * NP) * R;
+  static constexpr uint32_t kTmemCols = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
+  static_assert(kCols <= 512 && kStages + 3 <= kScaleRing && kStages < kPatchRing, "rings");
 };
 
 struct AttendParams {
@@ -123,7 +129,7 @@ __device__ __forceinline__ int tiles_of(int keys) { return max(1, (keys + kTile 
 struct Piece {
   int b, h, block, prefix;  // b < 0: no more
   int count, keys, t0, t1;  // keys: the tokens that the block's rows can see; t0, t1: the piece's tiles
-  int part, bad, pad0, pad1;  // part: -1 all of the block, 1 its first tiles, 0 others; bad: a sequence with a data error
+  int part, pad[3];         // part: -1 all of the block, 1 its first tiles, 0 others
 };
 // From this tile on, rows differ in what they see, or see nothing at the end.
 __device__ __forceinline__ int first_special(const Piece& w) {
@@ -165,12 +171,14 @@ __device__ __forceinline__ bool meet(int id, bool ok) {
   return all != 0;
 }
 
-// Shared-memory matrix descriptor: the 8-row (K-major) or 8-step (MN-major)
-// groups `stride` bytes apart, the swizzle of `row` bytes (tc.cuh has the bits).
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t stride, int row) {
-  const uint64_t swizzle = row == 128 ? 2 : row == 64 ? 4 : row == 32 ? 6 : 0;
-  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | static_cast<uint64_t>(stride >> 4) << 16 |
-         static_cast<uint64_t>(stride >> 4) << 32 | static_cast<uint64_t>(1u) << 46 | swizzle << 61;
+// Shared-memory matrix descriptor (tc.cuh has the bits) in two words: the
+// address; the 8-row (K-major) or 8-step (MN-major) groups `stride` bytes
+// apart and the swizzle of `row` bytes.
+__device__ __forceinline__ uint32_t operand_low(uint32_t addr, uint32_t stride) {
+  return ((addr >> 4) & 0x3FFFu) | (stride >> 4) << 16;
+}
+__host__ __device__ constexpr uint32_t operand_high(uint32_t stride, int row) {
+  return (stride >> 4) | 1u << 14 | (row == 128 ? 2u : row == 64 ? 4u : row == 32 ? 6u : 0u) << 29;
 }
 // byte offset `o` of a tile whose rows have `row` bytes, after the swizzle
 __device__ __forceinline__ uint32_t swizzled(uint32_t o, int row) {
@@ -182,12 +190,24 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, int a_major, int
   return (1u << 4) | (static_cast<uint32_t>(a_major) << 15) | (static_cast<uint32_t>(b_major) << 16) |
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
-// D[tmem] (+)= A B, M x N x 32.
-__device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+// D[tmem] (+)= A B, M x N x 32, by the lane that `issues`.  The whole warp runs
+// it: in a branch of one lane the operands would leave the uniform registers
+// that the instruction takes, at some 50 cycles per product.
+template <bool kAccumulate>
+__device__ __forceinline__ void umma_e4m3(uint32_t issues, uint32_t d, uint32_t a, uint32_t a_high, uint32_t b,
+                                          uint32_t b_high, uint32_t idesc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1 : 0)
+      "{\n .reg .pred p, q;\n .reg .b64 da, db;\n mov.b64 da, {%1, %2};\n mov.b64 db, {%3, %4};\n"
+      " setp.ne.b32 p, %6, 0;\n setp.ne.b32 q, %7, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %5, p;\n}" ::"r"(d),
+      "r"(a), "r"(a_high), "r"(b), "r"(b_high), "r"(idesc), "n"(kAccumulate ? 1 : 0), "r"(issues)
+      : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t issues, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(smem_addr(bar)),
+      "r"(issues)
       : "memory");
 }
 
@@ -266,30 +286,32 @@ struct PageScale {
 // the kernel
 // ---------------------------------------------------------------------------
 template <int R, int NP>
-__global__ void __launch_bounds__(kAttendThreads, 1)
+__global__ void __launch_bounds__(Shape<R, NP>::kThreads, 1)
     attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const AttendParams P) {
   using S = Shape<R, NP>;
-  constexpr int kW = R / 2;  // columns of a warpgroup
+  constexpr int kW = S::kW, kFirstOut = 4 + 4 * S::kGroups;
   extern __shared__ __align__(1024) unsigned char at_dyn[];
-  // sfull: a tile's scores are there; sempty: read; pfull: its weights are in
-  // shared memory; pempty: read by the products; ofull / oempty: its outputs;
-  // mfull / mempty: its factors (mix_s); efull / eempty: a piece's sums of
+  // full / empty: a tile's codes; sfull: its scores are there; pfull / pempty:
+  // its weights in shared memory (its scores are read); ofull / oempty: its outputs;
+  // mfull / mempty: its maxima (top_s); efull / eempty: a piece's sums of
   // weights; qfull / qempty: its queries; rfull / rempty: its record;
   // landed: a patched tile's V is there; patched: it is patched
   struct Bars {
-    uint64_t kfull[S::kStages], kempty[S::kStages], vfull[S::kStages], vempty[S::kStages];
-    uint64_t sfull[2], sempty[2], pfull[2], pempty[2], ofull[2], oempty[2], mfull[2], mempty[2], efull[2], eempty[2];
+    uint64_t full[S::kStages], empty[S::kStages];
+    uint64_t sfull[kScores], pfull[2], pempty[2], ofull[2], oempty[2], mfull[2], mempty[2], efull[2], eempty[2];
     uint64_t qfull[2], qempty[2], landed[kPatchRing], patched[kPatchRing], rfull[kPieceRing], rempty[kPieceRing], drain;
   };
   constexpr int kBars = sizeof(Bars) / 8;
   __shared__ Bars bar;
   __shared__ uint32_t tmem_s;
-  __shared__ int fault_s, k_issued_s, v_issued_s;
+  __shared__ int fault_s, issued_s;
   __shared__ __align__(16) Piece piece_s[kPieceRing];
   __shared__ __align__(16) PageScale scale_s[kScaleRing][8];
-  __shared__ __align__(16) float most_s[2][2][4][32], most_x_s[2][4][32], ref_s[8][3][32], cq_s[2][R], sum_s[2][4][R];
-  __shared__ __align__(16) float2 mix_s[2][R], end_s[2][R];
+  __shared__ __align__(16) float most_s[S::kGroups][2][4][kW], most_x_s[S::kGroups][4][kW];
+  __shared__ __align__(16) float ref_s[4 * S::kGroups][3][kW], cq_s[2][R], top_s[2][R], sum_s[2][S::kTurns][4][R];
+  __shared__ __align__(16) float2 mix_s[2][R];
+  __shared__ float sum_unit_s[2][S::kTurns][R];
   __shared__ __align__(16) float row_s[R];
   __shared__ long long place_s[R];
   __shared__ unsigned char token_s[2][R];
@@ -310,19 +332,19 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
   if (tid < kBars) {
     uint64_t* at = reinterpret_cast<uint64_t*>(&bar) + tid;
     unsigned count = 1;
-    if (at >= bar.sempty && at < bar.pempty) count = 8;           // sempty, pfull
+    if (at >= bar.pfull && at < bar.pempty) count = 4 * S::kColumns;  // pfull
     if (at >= bar.oempty && at < bar.mfull) count = 4;            // oempty
-    if (at >= bar.sfull && at < bar.sempty) count = 2;            // sfull
-    if (at >= bar.mfull && at < bar.mempty) count = 2;            // mfull
+    if (at >= bar.sfull && at < bar.pfull) count = 2;             // sfull
+    if (at >= bar.mfull && at < bar.mempty) count = S::kColumns;  // mfull
     if (at >= bar.mempty && at < bar.efull) count = 4;            // mempty
-    if (at >= bar.efull && at < bar.eempty) count = 8;            // efull
+    if (at >= bar.efull && at < bar.eempty) count = 4 * S::kGroups;  // efull
     if (at >= bar.eempty && at < bar.qfull) count = 4;            // eempty
     if (at >= bar.qempty && at < bar.landed) count = 4;           // qempty
-    if (at >= bar.rempty && at < &bar.drain) count = 15;          // rempty
+    if (at >= bar.rempty && at < &bar.drain) count = 7 + 4 * S::kGroups;  // rempty
     mbar_init(at, count);
     mbar_fence_init();
   }
-  if (tid == 0) fault_s = k_issued_s = v_issued_s = 0;
+  if (tid == 0) fault_s = issued_s = 0;
   if (warp == 1) {
     tmem_alloc(&tmem_s, S::kTmemCols);
     tmem_relinquish();
@@ -330,7 +352,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem_sc = tmem_s, tmem_o = tmem_s + 2 * R;
+  const uint32_t tmem_sc = tmem_s, tmem_o = tmem_s + kScores * R;
 
   // the next piece, for all roles but the one that makes them
   int pieces = 0;
@@ -338,7 +360,13 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     const int s = pieces % kPieceRing;
     if (!at_wait(&bar.rfull[s], static_cast<unsigned>(pieces / kPieceRing) & 1u, fault)) return false;
     w = piece_s[s];
-    __syncwarp();
+    // (a shuffle makes a warp's value uniform to the compiler as well)
+    w.b = __shfl_sync(0xffffffffu, w.b, 0);
+    w.keys = __shfl_sync(0xffffffffu, w.keys, 0);
+    w.prefix = __shfl_sync(0xffffffffu, w.prefix, 0);
+    w.count = __shfl_sync(0xffffffffu, w.count, 0);
+    w.t0 = __shfl_sync(0xffffffffu, w.t0, 0);
+    w.t1 = __shfl_sync(0xffffffffu, w.t1, 0);
     if (leader) mbar_arrive(&bar.rempty[s]);
     ++pieces;
     return w.b >= 0;
@@ -352,7 +380,6 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     bool ok = true;
     Piece w;
     while (ok && next_piece(w)) {
-      if (w.keys == 0) continue;
       const int* table = P.block_table + static_cast<long long>(w.b) * P.table_pages;
       // the pages of `batch` tiles, a lane each
       const auto has_page = [&](int tb) { return tb + mine < w.t1 && ((tb + mine) * pp + slot_in) * P.page < w.keys; };
@@ -387,32 +414,24 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         for (int i = 0; i < batch && tb + i < w.t1; ++i, ++it) {
           const int s = it % S::kStages;
           const unsigned parity = (static_cast<unsigned>(it / S::kStages) & 1u) ^ 1u;
-          const unsigned bytes = static_cast<unsigned>(__popc(groups >> (i * pp) & ((1u << pp) - 1u))) * page_bytes * NP +
+          const unsigned bytes = static_cast<unsigned>(__popc(groups >> (i * pp) & ((1u << pp) - 1u))) * page_bytes * 2 * NP +
                                  P.more_bytes;
           unsigned char* dst = kring + s * S::kSlot + slot_in * page_bytes;
-          ok = at_wait(&bar.kempty[s], parity, fault);
+          ok = at_wait(&bar.empty[s], parity, fault);
           if (!ok) break;
           if (mine == i) scale_s[it % kScaleRing][slot_in] = x;
           __syncwarp();
-          if (leader) mbar_expect_tx(&bar.kfull[s], bytes);
+          if (leader) mbar_expect_tx(&bar.full[s], bytes);
           __syncwarp();
           if (mine == i && has) {
 #pragma unroll
-            for (int p = 0; p < NP; ++p) tma_load_2d(dst + p * kPanel, &tm_k, p * 128, y, &bar.kfull[s]);
-          }
-          __syncwarp();
-          if (leader) k_issued_s = it + 1;
-          ok = at_wait(&bar.vempty[s], parity, fault);
-          if (!ok) break;
-          if (leader) mbar_expect_tx(&bar.vfull[s], bytes);
-          __syncwarp();
-          dst += S::kStages * S::kSlot;
-          if (mine == i && has) {
+            for (int p = 0; p < NP; ++p) tma_load_2d(dst + p * kPanel, &tm_k, p * 128, y, &bar.full[s]);
 #pragma unroll
-            for (int p = 0; p < NP; ++p) tma_load_2d(dst + p * kPanel, &tm_v, p * 128, y, &bar.vfull[s]);
+            for (int p = 0; p < NP; ++p)
+              tma_load_2d(dst + S::kStages * S::kSlot + p * kPanel, &tm_v, p * 128, y, &bar.full[s]);
           }
           __syncwarp();
-          if (leader) v_issued_s = it + 1;
+          if (leader) issued_s = it + 1;
         }
       }
     }
@@ -421,86 +440,91 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     constexpr uint32_t idesc_s = idesc_e4m3(kTile, R, 0, 0), idesc_o = idesc_e4m3(128, R, 1, 1);
     const int steps = (P.D + 31) / 32;
     int it = 0, qn = 0, patches = 0;
-    int last_patch = -1;  // the tile before's place among the patched ones
     bool ok = true;
+    const uint32_t issues = leader ? 1u : 0u;
     // the outputs of tile j
     const auto outputs = [&](int j, int patch) {
       const int s = j % S::kStages, d = j & 1;
       const unsigned half = static_cast<unsigned>(j >> 1) & 1u;
-      if (!at_wait(&bar.vfull[s], static_cast<unsigned>(j / S::kStages) & 1u, fault)) return false;
       if (patch >= 0 && !at_wait(&bar.patched[patch % kPatchRing], static_cast<unsigned>(patch / kPatchRing) & 1u, fault))
         return false;
       if (!at_wait(&bar.oempty[d], half ^ 1u, fault) || !at_wait(&bar.pfull[d], half, fault)) return false;
       tc_fence_after();
-      if (leader) {
-        const uint64_t b = operand(smem_addr(pbuf + 2 * d * S::kPHalf), 8 * S::kPRow, S::kPRow);
+      const uint32_t b = operand_low(smem_addr(pbuf + 2 * d * S::kPHalf), 8 * S::kPRow);
+      constexpr uint32_t a_high = operand_high(1024, 128), b_high = operand_high(8 * S::kPRow, S::kPRow);
 #pragma unroll
-        for (int p = 0; p < NP; ++p) {
-          const uint64_t a = operand(smem_addr(vring + s * S::kSlot + p * kPanel), 1024, 128);
+      for (int p = 0; p < NP; ++p) {
+        const uint32_t a = operand_low(smem_addr(vring + s * S::kSlot + p * kPanel), 1024), o = tmem_o + (d * NP + p) * R;
+        umma_e4m3<false>(issues, o, a, a_high, b, b_high, idesc_o);
 #pragma unroll
-          for (int k = 0; k < 2 * kTile / 32; ++k)  // hi's 4 steps of 32 tokens, then lo's
-            umma_e4m3(tmem_o + (d * NP + p) * R, a + static_cast<uint64_t>((k & 3) * (32 * 128 >> 4)),
-                      b + static_cast<uint64_t>((k >> 2) * (S::kPHalf >> 4) + (k & 3) * (32 * S::kPRow >> 4)), idesc_o,
-                      k != 0);
-        }
-        umma_commit(&bar.ofull[d]);
-        umma_commit(&bar.vempty[s]);
-        umma_commit(&bar.pempty[d]);
+        for (int k = 1; k < 2 * kTile / 32; ++k)  // hi's 4 steps of 32 tokens, then lo's
+          umma_e4m3<true>(issues, o, a + (k & 3) * (32 * 128 >> 4), a_high,
+                          b + (k >> 2) * (S::kPHalf >> 4) + (k & 3) * (32 * S::kPRow >> 4), b_high, idesc_o);
       }
-      __syncwarp();
+      commit_if(issues, &bar.ofull[d]);
+      commit_if(issues, &bar.empty[s]);
+      commit_if(issues, &bar.pempty[d]);
       return true;
     };
-    // one loop over tiles and the step behind the last: the outputs of the tile before, in one place
+    // one loop over the tiles, scores two tiles ahead of the outputs
     Piece w;
     bool more = next_piece(w);
-    while (more && w.keys == 0) more = next_piece(w);
     int t = more ? w.t0 : 0, special = more ? first_special(w) : 0;
-    while (ok) {
+    int sb = 0, patch0 = -1, patch1 = -1;  // place of the scores; the last two tiles' among the patched ones
+    constexpr int kUnknown = 0x40000000;
+    int end = kUnknown;  // the number of tiles, once it is known
+    for (; it < end + 2; ++it) {
       int patch = -1;
-      if (more) {
-        const int s = it % S::kStages, d = it & 1;
-        if (t == w.t0) ok = at_wait(&bar.qfull[qn & 1], static_cast<unsigned>(qn >> 1) & 1u, fault);
-        ok = ok && at_wait(&bar.kfull[s], static_cast<unsigned>(it / S::kStages) & 1u, fault) &&
-             at_wait(&bar.sempty[d], (static_cast<unsigned>(it >> 1) & 1u) ^ 1u, fault);
-        if (!ok) break;
-        tc_fence_after();
-        if (leader) {
-          const uint64_t a = operand(smem_addr(kring + s * S::kSlot), 1024, 128);
-          const uint64_t b = operand(smem_addr(qbuf + 2 * (qn & 1) * S::kQHalf), 1024, 128);
+      // (where a piece's queries, or the codes' place, wait for the outputs of the tile two before: those first)
+      const bool outputs_first = more && (t == w.t0 || S::kStages == 2);
 #pragma unroll 1
-          for (int half = 0; half < 2; ++half)
-#pragma unroll
-            for (int k = 0; k < 4 * NP; ++k)
-              if (k < steps)
-                umma_e4m3(tmem_sc + d * R, a + static_cast<uint64_t>((k >> 2) * (kPanel >> 4) + (k & 3) * 2),
-                          b + static_cast<uint64_t>(half * (S::kQHalf >> 4) + (k >> 2) * (R * 128 >> 4) + (k & 3) * 2),
-                          idesc_s, half != 0 || k != 0);
-          umma_commit(&bar.sfull[d]);
-          umma_commit(&bar.kempty[s]);
-          mbar_arrive(&bar.sfull[d]);  // what the copies' and queries' warps wrote is visible behind it
-        }
-        __syncwarp();
-        if (t >= special) {
-          // (a warp that comes to a barrier's phase two phases early would pass: the
-          // patching warp, which skips tiles, is told when its tile's V is there)
-          ok = at_wait(&bar.vfull[s], static_cast<unsigned>(it / S::kStages) & 1u, fault);
+      for (int turn = 0; turn < 2 && ok; ++turn) {
+        if ((turn == 0) == outputs_first) {
+          if (it > 1) ok = outputs(it - 2, patch1);
+        } else if (more) {
+          const int s = it % S::kStages;
+          if (t == w.t0) ok = at_wait(&bar.qfull[qn & 1], static_cast<unsigned>(qn >> 1) & 1u, fault);
+          ok = ok && at_wait(&bar.full[s], static_cast<unsigned>(it / S::kStages) & 1u, fault);
           if (!ok) break;
-          patch = patches++;
-          if (leader) mbar_arrive(&bar.landed[patch % kPatchRing]);
+          tc_fence_after();
+          const uint32_t a = operand_low(smem_addr(kring + s * S::kSlot), 1024), d = tmem_sc + sb * R;
+          const uint32_t b = operand_low(smem_addr(qbuf + 2 * (qn & 1) * S::kQHalf), 1024);
+          constexpr uint32_t high = operand_high(1024, 128);
+          umma_e4m3<false>(issues, d, a, high, b, high, idesc_s);
+#pragma unroll
+          for (int k = 1; k < 8 * NP; ++k) {  // hi's steps of 32 elements, then lo's
+            const int step = k % (4 * NP);
+            if (step < steps)
+              umma_e4m3<true>(issues, d, a + (step >> 2) * (kPanel >> 4) + (step & 3) * 2, high,
+                              b + k / (4 * NP) * (S::kQHalf >> 4) + (step >> 2) * (R * 128 >> 4) + (step & 3) * 2, high,
+                              idesc_s);
+          }
+          commit_if(issues, &bar.sfull[sb]);
+          if (leader) mbar_arrive(&bar.sfull[sb]);  // what the copies' and queries' warps wrote is visible behind it
+          if (t >= special) {
+            // (a warp that comes to a barrier's phase two phases early would pass: the
+            // patching warp, which skips tiles, is told when its tile is there)
+            patch = patches++;
+            if (leader) mbar_arrive(&bar.landed[patch % kPatchRing]);
+          }
+          __syncwarp();
+          sb = sb == kScores - 1 ? 0 : sb + 1;
         }
       }
-      if (it > 0) ok = outputs(it - 1, last_patch);
-      if (!more || !ok) break;
-      last_patch = patch;
-      ++it;
-      if (++t == w.t1) {
+      if (!ok) break;
+      patch1 = patch0;
+      patch0 = patch;
+      if (more && ++t == w.t1) {
         ++qn;
-        do more = next_piece(w);
-        while (more && w.keys == 0);
+        more = next_piece(w);
         if (more) {
           t = w.t0;
           special = first_special(w);
+        } else {
+          end = it + 1;
         }
+      } else if (!more && end == kUnknown) {
+        break;  // (no tiles at all)
       }
     }
     // every product issued has completed before tensor memory is released
@@ -576,27 +600,39 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         t1 = min(tiles, t0 + left);
         left -= t1 - t0;
       }
-      const int rs = made % kPieceRing;
-      ok = at_wait(&bar.rempty[rs], (static_cast<unsigned>(made / kPieceRing) & 1u) ^ 1u, fault);
-      if (!ok) break;
-      Piece w;
-      w.b = last ? -1 : b;
-      w.h = h;
-      w.block = block;
-      w.prefix = s.prefix;
-      w.count = s.count;
-      w.keys = keys;
-      w.t0 = t0;
-      w.t1 = t1;
-      w.part = t0 == 0 ? (t1 == tiles ? -1 : 1) : 0;
-      w.bad = s.bad;
-      w.pad0 = w.pad1 = 0;
-      if (leader) piece_s[rs] = w;
-      __syncwarp();
-      if (leader) mbar_arrive(&bar.rfull[rs]);
-      ++made;
-      if (last) break;
-      if (w.part == 1) {
+      if (!last && keys == 0) {
+        // rows of nothing (a block of one tile that no other role hears of)
+#pragma unroll 1
+        for (int r = block * R; r < min(block * R + R, P.n * P.G); ++r) {
+          const int tok = r / P.G;
+          bf16_t* out = P.out + b * P.out_ld[0] + tok * P.out_ld[1] + (h * P.G + r - tok * P.G) * P.out_ld[2];
+          for (int e = lane; e < P.D; e += 32) out[e] = 0;
+        }
+        if (s.bad && h == 0 && block == 0 && leader) report(P, b, SPEC_ERR_CACHE);
+      } else {
+        const int rs = made % kPieceRing;
+        ok = at_wait(&bar.rempty[rs], (static_cast<unsigned>(made / kPieceRing) & 1u) ^ 1u, fault);
+        if (!ok) break;
+        if (leader) {
+          Piece w;
+          w.b = last ? -1 : b;
+          w.h = h;
+          w.block = block;
+          w.prefix = s.prefix;
+          w.count = s.count;
+          w.keys = keys;
+          w.t0 = t0;
+          w.t1 = t1;
+          w.part = t0 == 0 ? (t1 == tiles ? -1 : 1) : 0;
+          w.pad[0] = w.pad[1] = w.pad[2] = 0;
+          piece_s[rs] = w;
+        }
+        __syncwarp();
+        if (leader) mbar_arrive(&bar.rfull[rs]);
+        ++made;
+        if (last) break;
+      }
+      if (t0 == 0 && t1 < tiles) {
         // the block's last tile is another CTA's
         const int u = u1 + (tiles - t1) - 1, few = each + 1;
         const int c = u < few * more ? u / few : more + (u - few * more) / each;
@@ -709,12 +745,11 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     bool ok = true;
     Piece w;
     while (ok && next_piece(w)) {
-      if (w.keys == 0) continue;
       it += w.t1 - w.t0;
       for (int t = max(w.t0, first_special(w)); ok && t < w.t1; ++t, ++patches) {
         const int j = it - (w.t1 - t), s = j % S::kStages;
         ok = at_wait(&bar.landed[patches % kPatchRing], static_cast<unsigned>(patches / kPatchRing) & 1u, fault) &&
-             at_wait(&bar.vfull[s], static_cast<unsigned>(j / S::kStages) & 1u, fault);
+             at_wait(&bar.full[s], static_cast<unsigned>(j / S::kStages) & 1u, fault);
         if (!ok) break;
 #pragma unroll 1
         for (int row = lane; row < kTile; row += 32) {
@@ -746,38 +781,36 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         if (leader) mbar_arrive(&bar.patched[patches % kPatchRing]);
       }
     }
-  } else if (warp < 12) {
+  } else if (warp < kFirstOut) {
     // ---------------- weights ----------------
-    // Both warpgroups work on every tile, each on half of the block's rows.
-    const int grp = (warp - 4) >> 2, q = warp & 3, row = q * 32 + lane, col0 = grp * kW;
+    const int group = (warp - 4) >> 2, turn = group / S::kColumns, q = warp & 3, row = q * 32 + lane;
+    const int col0 = group % S::kColumns * kW;
     const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
     const int page_row = row / P.page;
-    float* refs = ref_s[warp - 4][0];
+    const int col = lane % kW;  // lanes i and i + kW do the same for row col0 + i
+    float(*refs)[kW] = ref_s[warp - 4];
     int it = 0, qn = 0, patches = 0;
     bool ok = true;  // (what a wait of this warp's gave; the warpgroup goes by what its warps agree on)
     Piece w;
     while (true) {
       const bool got = next_piece(w);
-      if (!meet(1 + grp, got)) break;
-      if (w.keys == 0) continue;
+      if (!meet(1 + group, got)) break;
       const int special = first_special(w), qb = qn & 1, tok0 = w.block * R / P.G;
-      // lane i < kW, row col0 + i: log2 of the outputs' unit and of the sums'
-      float unit = -kInf, sum_unit = -kInf;
+      float sum_unit = -kInf;  // log2 of the sums' unit, of row col0 + col
       float2 sum[kW / 2];
 #pragma unroll
       for (int i = 0; i < kW / 2; ++i) sum[i] = make_float2(0.f, 0.f);
       bool go = true;
 #pragma unroll 1
       for (int t = w.t0; t < w.t1; ++t, ++it) {
-        const int k = it & 1;
+        const int patch = t >= special ? patches++ : -1, k = it & 1;
+        if (S::kTurns == 2 && k != turn) continue;
         const unsigned half = static_cast<unsigned>(it >> 1) & 1u;
-        ok = at_wait(&bar.sfull[k], half, fault) && ok;
+        const int sb = it % kScores;
+        ok = at_wait(&bar.sfull[sb], static_cast<unsigned>(it / kScores) & 1u, fault) && ok;
         tc_fence_after();
         float y[kW];
-        tmem_columns<kW>(tmem_sc + k * R + col0 + lanes, y);
-        tc_fence_before();
-        __syncwarp();
-        if (leader) mbar_arrive(&bar.sempty[k]);
+        tmem_columns<kW>(tmem_sc + sb * R + col0 + lanes, y);
         const PageScale ps = scale_s[it % kScaleRing][page_row];
         // y = score + value exponent
 #pragma unroll
@@ -788,9 +821,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
           const float2 b = ffma2(fmul2(make_float2(y[r + 2], y[r + 3]), make_float2(c.z, c.w)), ck, ve);
           y[r] = a.x, y[r + 1] = a.y, y[r + 2] = b.x, y[r + 3] = b.y;
         }
-        if (t >= special) {
-          const int patch = patches++;
-          ok = ok && at_wait(&bar.patched[patch % kPatchRing], static_cast<unsigned>(patch / kPatchRing) & 1u, fault);
+        if (patch >= 0) {
+          ok = at_wait(&bar.patched[patch % kPatchRing], static_cast<unsigned>(patch / kPatchRing) & 1u, fault) && ok;
           const int pos = t * kTile + row, j = pos - w.prefix;
           unsigned long long seen = ~0ull;
           if (pos >= w.keys) seen = 0;
@@ -804,57 +836,53 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
           }
         }
         // the rows' largest
+        const int slot = S::kTurns == 2 ? it >> 1 & 1 : k;
 #pragma unroll
         for (int r = 0; r < kW; r += 4) {
           const float4 m = make_float4(warp_max(y[r]), warp_max(y[r + 1]), warp_max(y[r + 2]), warp_max(y[r + 3]));
-          if (leader) *reinterpret_cast<float4*>(&most_s[grp][k][q][r]) = m;
+          if (leader) *reinterpret_cast<float4*>(&most_s[group][slot][q][r]) = m;
         }
         if (ps.far) {
 #pragma unroll
           for (int r = 0; r < kW; ++r) {
             const float m = warp_max(y[r] - ps.ve);
-            if (leader) most_x_s[grp][q][r] = m;
+            if (leader) most_x_s[group][q][r] = m;
           }
         }
-        go = meet(1 + grp, ok);
+        go = meet(1 + group, ok);
         if (!go) break;
-        {
-          // every warp for itself: lane i's row
-          const float m = fmaxf(fmaxf(most_s[grp][k][0][lane], most_s[grp][k][1][lane]),
-                                fmaxf(most_s[grp][k][2][lane], most_s[grp][k][3][lane]));
-          const bool none = m == -kInf;
-          const float top = m - 8.f;
-          // of the scores without exponents, the sums' reference: the largest, or a bound of it
-          float most_x = m - ps.ve_low;
-          if (ps.far)
-            most_x = fmaxf(fmaxf(most_x_s[grp][0][lane], most_x_s[grp][1][lane]),
-                           fmaxf(most_x_s[grp][2][lane], most_x_s[grp][3][lane]));
-          const float next = fmaxf(unit, top), next_x = fmaxf(sum_unit, most_x);
-          refs[lane] = none ? 0.f : top;
-          refs[32 + lane] = sum_unit == -kInf ? 0.f : ex2(sum_unit - next_x);
-          refs[64 + lane] = none ? 0.f : ps.far ? next_x : ex2(most_x - next_x) * 0.00390625f;
-          if (q == 0) {
-            ok = at_wait(&bar.mempty[k], half ^ 1u, fault);
-            if (lane < kW)
-              mix_s[k][col0 + lane] = make_float2(unit == -kInf ? 0.f : ex2(unit - next), none ? 0.f : ex2(top - next));
-          }
-          unit = next;
-          sum_unit = next_x;
-          __syncwarp();
-          if (q == 0 && leader) mbar_arrive(&bar.mfull[k]);
+        // every warp for itself: a lane per row
+        const float m = fmaxf(fmaxf(most_s[group][slot][0][col], most_s[group][slot][1][col]),
+                              fmaxf(most_s[group][slot][2][col], most_s[group][slot][3][col]));
+        const bool none = m == -kInf;
+        refs[0][col] = none ? 0.f : m - 8.f;
+        if (q == 0) {
+          ok = at_wait(&bar.mempty[k], half ^ 1u, fault);
+          top_s[k][col0 + col] = m - 8.f;
         }
+        __syncwarp();
+        if (q == 0 && leader) mbar_arrive(&bar.mfull[k]);
+        // the sums' reference: the largest score without exponents, or a bound of it
+        float most_x = m - ps.ve_low;
         if (ps.far) {
           // (2^(y - reference) may underflow where a page's values are tiny against another's)
+          most_x = fmaxf(fmaxf(most_x_s[group][0][col], most_x_s[group][1][col]),
+                         fmaxf(most_x_s[group][2][col], most_x_s[group][3][col]));
+          const float next = fmaxf(sum_unit, most_x);
+          refs[1][col] = sum_unit == -kInf ? 0.f : ex2(sum_unit - next);
+          refs[2][col] = none ? 0.f : next;
+          sum_unit = next;
+          __syncwarp();
 #pragma unroll
           for (int r = 0; r < kW; r += 2) {
-            sum[r / 2].x = __fmaf_rn(sum[r / 2].x, refs[32 + r], ex2((y[r] - ps.ve) - refs[64 + r]));
-            sum[r / 2].y = __fmaf_rn(sum[r / 2].y, refs[33 + r], ex2((y[r + 1] - ps.ve) - refs[65 + r]));
+            sum[r / 2].x = __fmaf_rn(sum[r / 2].x, refs[1][r], ex2((y[r] - ps.ve) - refs[2][r]));
+            sum[r / 2].y = __fmaf_rn(sum[r / 2].y, refs[1][r + 1], ex2((y[r + 1] - ps.ve) - refs[2][r + 1]));
           }
-          meet(1 + grp, true);  // (there is one most_x_s)
+          meet(1 + group, true);  // (there is one most_x_s)
         }
 #pragma unroll
         for (int r = 0; r < kW; r += 4) {
-          const float4 c = lds_f4(refs + r);
+          const float4 c = lds_f4(&refs[0][r]);
           y[r] = ex2(y[r] - c.x);
           y[r + 1] = ex2(y[r + 1] - c.y);
           y[r + 2] = ex2(y[r + 2] - c.z);
@@ -872,14 +900,20 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
           *reinterpret_cast<uint2*>(p + S::kPHalf + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
         }
         fence_proxy_async();
+        tc_fence_before();
         __syncwarp();
         if (leader) mbar_arrive(&bar.pfull[k]);
         if (!ps.far) {
           // the sums of the weights themselves: without the values' exponents
+          const float next = fmaxf(sum_unit, most_x);
+          refs[1][col] = sum_unit == -kInf ? 0.f : ex2(sum_unit - next);
+          refs[2][col] = none ? 0.f : ex2(most_x - next) * 0.00390625f;
+          sum_unit = next;
+          __syncwarp();
           const float f = exp2i(static_cast<int>(ps.ve_low - ps.ve));
 #pragma unroll
           for (int r = 0; r < kW; r += 4) {
-            const float4 a = lds_f4(refs + 32 + r), b = lds_f4(refs + 64 + r);
+            const float4 a = lds_f4(&refs[1][r]), b = lds_f4(&refs[2][r]);
             sum[r / 2] = ffma2(sum[r / 2], make_float2(a.x, a.y),
                                fmul2(make_float2(y[r], y[r + 1]), fmul2(make_float2(b.x, b.y), make_float2(f, f))));
             sum[r / 2 + 1] = ffma2(sum[r / 2 + 1], make_float2(a.z, a.w),
@@ -887,21 +921,15 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
           }
         }
       }
-      // the piece's sums and units
+      // the piece's sums and their units
       if (!go) break;
       ok = at_wait(&bar.eempty[qb], (static_cast<unsigned>(qn >> 1) & 1u) ^ 1u, fault) && ok;
-      if (!meet(1 + grp, ok)) break;
+      if (!meet(1 + group, ok)) break;
       float all[kW];
 #pragma unroll
       for (int i = 0; i < kW / 2; ++i) all[2 * i] = sum[i].x, all[2 * i + 1] = sum[i].y;
-      constexpr int kFirst = kW == 24 ? 16 : kW;
-      const float s = column_sums<kFirst>(all, lane);
-      if (lane < kFirst) sum_s[qb][q][col0 + lane] = s;
-      if constexpr (kW == 24) {
-        const float s2 = column_sums<8>(all + 16, lane);
-        if (lane < 8) sum_s[qb][q][col0 + 16 + lane] = s2;
-      }
-      if (q == 0 && lane < kW) end_s[qb][col0 + lane] = make_float2(unit, sum_unit);
+      sum_s[qb][turn][q][col0 + col] = column_sums<kW>(all, lane);
+      if (q == 0) sum_unit_s[qb][turn][col0 + col] = sum_unit;
       __syncwarp();
       if (leader) mbar_arrive(&bar.efull[qb]);
       ++qn;
@@ -915,18 +943,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     Piece w;
     while (true) {
       const bool got = next_piece(w);
-      if (!meet(3, got)) break;
+      if (!meet(5, got)) break;
       const int row0 = w.block * R;
-      if (w.keys == 0) {
-        // rows of nothing
-        for (int r = row0; r < min(row0 + R, P.n * P.G); ++r) {
-          const int tok = r / P.G;
-          bf16_t* out = P.out + w.b * P.out_ld[0] + tok * P.out_ld[1] + (w.h * P.G + r - tok * P.G) * P.out_ld[2];
-          for (int e = d; e < P.D; e += 128) out[e] = 0;
-        }
-        if (w.bad && w.h == 0 && w.block == 0 && d == 0) report(P, w.b, SPEC_ERR_CACHE);
-        continue;
-      }
       const int qb = qn & 1;
       const unsigned piece_half = static_cast<unsigned>(qn >> 1) & 1u;
       float2 acc[NP][R / 2];
@@ -934,12 +952,22 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
       for (int p = 0; p < NP; ++p)
 #pragma unroll
         for (int r = 0; r < R / 2; ++r) acc[p][r] = make_float2(0.f, 0.f);
+      float unit = -kInf;  // log2 of the outputs' unit, of row d
+      bool go = true;
 #pragma unroll 1
-      for (int t = w.t0; ok && t < w.t1; ++t, ++it) {
+      for (int t = w.t0; t < w.t1; ++t, ++it) {
         const int k = it & 1;
         const unsigned half = static_cast<unsigned>(it >> 1) & 1u;
-        ok = at_wait(&bar.mfull[k], half, fault) && at_wait(&bar.ofull[k], half, fault);
-        if (!ok) break;
+        ok = at_wait(&bar.mfull[k], half, fault) && ok;
+        if (d < R) {
+          const float top = top_s[k][d], next = fmaxf(unit, top);
+          mix_s[k][d] = make_float2(unit == -kInf ? 0.f : ex2(unit - next), top == -kInf ? 0.f : ex2(top - next));
+          unit = next;
+        }
+        go = meet(5, ok);
+        if (!go) break;
+        if (leader) mbar_arrive(&bar.mempty[k]);
+        ok = at_wait(&bar.ofull[k], half, fault);
         tc_fence_after();
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
@@ -958,31 +986,35 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (leader) {
-          mbar_arrive(&bar.oempty[k]);
-          mbar_arrive(&bar.mempty[k]);
-        }
+        if (leader) mbar_arrive(&bar.oempty[k]);
       }
-      ok = ok && at_wait(&bar.efull[qb], piece_half, fault);
-      if (!meet(3, ok)) break;
+      if (!go) break;
+      ok = at_wait(&bar.efull[qb], piece_half, fault) && ok;
+      if (!meet(5, ok)) break;
       constexpr int kLd = NP * 128 + 4;
       float* part = P.parts + (static_cast<long long>(2 * blockIdx.x) + max(w.part, 0)) * R * kLd;
       if (d < R) {
-        const float s = (sum_s[qb][0][d] + sum_s[qb][1][d]) + (sum_s[qb][2][d] + sum_s[qb][3][d]);
-        const float2 end = end_s[qb][d];
+        float s = (sum_s[qb][0][0][d] + sum_s[qb][0][1][d]) + (sum_s[qb][0][2][d] + sum_s[qb][0][3][d]);
+        float su = sum_unit_s[qb][0][d];
+        if constexpr (S::kTurns == 2) {
+          const float s2 = (sum_s[qb][1][0][d] + sum_s[qb][1][1][d]) + (sum_s[qb][1][2][d] + sum_s[qb][1][3][d]);
+          const float su2 = sum_unit_s[qb][1][d], next = fmaxf(su, su2);
+          s = (su == -kInf ? s : s * ex2(su - next)) + (su2 == -kInf ? s2 : s2 * ex2(su2 - next));
+          su = next;
+        }
         if (w.part < 0) {
           const int tok = (row0 + d) / P.G, g = row0 + d - tok * P.G;
-          row_s[d] = s == 0.f ? 0.f : ex2(end.x - end.y) / s;
+          row_s[d] = s == 0.f ? 0.f : ex2(unit - su) / s;
           place_s[d] = tok >= P.n ? -1 : w.b * P.out_ld[0] + tok * P.out_ld[1] + (w.h * P.G + g) * P.out_ld[2];
           if (tok >= w.count) row_s[d] = 0.f;
         } else {
           float* e = part + d * kLd + NP * 128;
-          __stcg(e, end.x);
+          __stcg(e, unit);
           __stcg(e + 1, s);
-          __stcg(e + 2, end.y);
+          __stcg(e + 2, su);
         }
       }
-      if (!meet(3, true)) break;
+      meet(5, true);
       if (leader) {
         mbar_arrive(&bar.qempty[qb]);
         mbar_arrive(&bar.eempty[qb]);
@@ -1005,7 +1037,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
           }
         }
       }
-      if (!meet(3, true)) break;
+      meet(5, true);
     }
   }
 
@@ -1013,10 +1045,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
   if (*fault && tid == 0) {
     // copies still in flight land before the CTA exits: wait (bounded) for
     // the last phase of every stage that was issued
-    for (int k = max(0, k_issued_s - S::kStages); k < k_issued_s; ++k)
-      mbar_wait(&bar.kfull[k % S::kStages], static_cast<unsigned>(k / S::kStages) & 1u);
-    for (int k = max(0, v_issued_s - S::kStages); k < v_issued_s; ++k)
-      mbar_wait(&bar.vfull[k % S::kStages], static_cast<unsigned>(k / S::kStages) & 1u);
+    for (int k = max(0, issued_s - S::kStages); k < issued_s; ++k)
+      mbar_wait(&bar.full[k % S::kStages], static_cast<unsigned>(k / S::kStages) & 1u);
     if (P.error_word) atomicOr(P.error_word, SPEC_ERR_INTERNAL);
     P.shared[blockIdx.x] = make_int4(0, 0, 0, 0);
   }
@@ -1142,7 +1172,7 @@ spec_status launch_attend(const spec_attend_args& a, AttendParams& p, cudaStream
   if (raise_smem<R, NP>() != cudaSuccess) return SPEC_ECUDA;
   p.more_bytes = g_more_bytes.load();
   const int ctas = std::min(nsm, kMaxCtas);
-  attend_kernel<R, NP><<<ctas, kAttendThreads, Shape<R, NP>::kSmem, s>>>(tk, tv, p);
+  attend_kernel<R, NP><<<ctas, Shape<R, NP>::kThreads, Shape<R, NP>::kSmem, s>>>(tk, tv, p);
   if (cudaGetLastError() != cudaSuccess) return SPEC_ECUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>((std::min(R, a.n * p.G) + 3) / 4));
