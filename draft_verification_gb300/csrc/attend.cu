@@ -36,6 +36,7 @@
 #include <cstdint>
 #include <map>
 #include <mutex>
+#include <type_traits>
 
 #include "cache.cuh"
 #include "internal.h"
@@ -46,32 +47,33 @@
 namespace sv {
 namespace {
 
-constexpr int kTile = 128;      // tokens per tile
+constexpr int kTile = 128;      // tokens per tile; two tiles make a step
 constexpr int kPanel = 16384;   // bytes of 128 tokens x 128 elements
 constexpr int kMaxRows = 1024;  // n
 constexpr int kMaxCtas = 160;
+constexpr int kThreads = 512;
+constexpr int kMaskBytes = 10 * kMaxRows;  // of shared memory for a tree's masks, at most
 constexpr int kScaleRing = 16, kPatchRing = 8, kPieceRing = 4;
-constexpr int kScores = 4;  // places of tiles' scores: those are two tiles ahead of the outputs, every group meets all phases of its places
-constexpr int kFar = 30;  // value exponents of a tile that lie further apart than this
+constexpr int kFar = 9;    // value exponents of a step that lie further apart than this: 2^-9 is the least e4m3 code
+constexpr int kAhead = 2;  // tiles that K is copied ahead of V, as its products are ahead
 
 // R: a block's rows; NP: panels of 128 elements of a head.
 template <int R, int NP>
 struct Shape {
-  // the softmax warpgroups: kGroups, each with kW of the block's rows, of every
-  // tile or of every other one
-  static constexpr int kW = R == 16 ? 8 : 16, kColumns = R / kW, kTurns = kColumns == 2 ? 2 : 1;
-  static constexpr int kGroups = kColumns * kTurns;
-  static constexpr int kThreads = 128 * (2 + kGroups);
-  static constexpr int kStages = NP == 1 ? (R > 32 ? 4 : 5) : 2;
-  static constexpr int kPRow = R == 48 ? 64 : R;  // bytes of a token's weights
+  // places of K tiles, and as many of V tiles (each with barriers of its own: a
+  // warp has to meet all phases of a barrier that it waits on)
+  static constexpr int kStages = NP == 2 ? 2 : R == 16 ? 5 : R == 32 ? 4 : 3;
   static constexpr int kSlot = NP * kPanel;
-  static constexpr int kQHalf = NP * R * 128;  // hi or lo of a block's queries
-  static constexpr int kPHalf = kTile * kPRow;  // hi or lo of a tile's weights
-  static constexpr int kMaskBytes = 2 * kMaxRows * 8;
-  static constexpr int kSmem = 1024 + 2 * kStages * kSlot + 4 * kQHalf + 4 * kPHalf + kMaskBytes + kMaxRows * 2;
-  static constexpr int kCols = (kScores + 2 * NP) * R;
-  static constexpr uint32_t kTmemCols = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
-  static_assert(kCols <= 512 && kStages + 3 <= kScaleRing && kStages < kPatchRing, "rings");
+  static constexpr int kPRow = R == 48 ? 64 : R;  // bytes of a token's weights
+  static constexpr int kPHalf = 2 * kTile * kPRow;  // hi or lo of a step's weights
+  static constexpr int kQHalf = NP * R * 128;       // hi or lo of a block's queries
+  static constexpr int kScores = R > 32 ? 2 : 4;    // places of steps' scores
+  static constexpr int kOnes = 1024;                // a tile's factors of the sums of weights (one row of 128 bytes)
+  static constexpr int kSmem = 1024 + 2 * kStages * kSlot + 4 * kQHalf + 4 * kPHalf + 4 * kOnes;
+  static constexpr int kCols = (2 * kScores + 2 * NP + 2) * R;
+  static constexpr uint32_t kTmemCols = kCols <= 256 ? 256 : 512;
+  static_assert(kCols <= 512 && kStages + kAhead + 6 <= kScaleRing && 2 * kStages + kPatchRing <= 32, "rings");
+  using Mask = typename std::conditional<(R > 32), unsigned long long, unsigned>::type;  // a bit per token of a block
 };
 
 struct AttendParams {
@@ -193,14 +195,13 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, int a_major, int
 // D[tmem] (+)= A B, M x N x 32, by the lane that `issues`.  The whole warp runs
 // it: in a branch of one lane the operands would leave the uniform registers
 // that the instruction takes, at some 50 cycles per product.
-template <bool kAccumulate>
 __device__ __forceinline__ void umma_e4m3(uint32_t issues, uint32_t d, uint32_t a, uint32_t a_high, uint32_t b,
-                                          uint32_t b_high, uint32_t idesc) {
+                                          uint32_t b_high, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n .reg .pred p, q;\n .reg .b64 da, db;\n mov.b64 da, {%1, %2};\n mov.b64 db, {%3, %4};\n"
       " setp.ne.b32 p, %6, 0;\n setp.ne.b32 q, %7, 0;\n"
       " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %5, p;\n}" ::"r"(d),
-      "r"(a), "r"(a_high), "r"(b), "r"(b_high), "r"(idesc), "n"(kAccumulate ? 1 : 0), "r"(issues)
+      "r"(a), "r"(a_high), "r"(b), "r"(b_high), "r"(idesc), "r"(accumulate), "r"(issues)
       : "memory");
 }
 __device__ __forceinline__ void commit_if(uint32_t issues, uint64_t* bar) {
@@ -209,31 +210,6 @@ __device__ __forceinline__ void commit_if(uint32_t issues, uint64_t* bar) {
       " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(smem_addr(bar)),
       "r"(issues)
       : "memory");
-}
-
-// 8 consecutive float32 columns of this warp's 32 lanes.
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
-  uint32_t r[8];
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr)
-               : "memory");
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
-}
-// N columns, a multiple of 8
-template <int N>
-__device__ __forceinline__ void tmem_columns(uint32_t at, float* v) {
-  if constexpr (N >= 32) {
-    tmem_ld32(at, v);
-    if constexpr (N > 32) tmem_columns<N - 32>(at + 32, v + 32);
-  } else if constexpr (N >= 16) {
-    tmem_ld16(at, v);
-    if constexpr (N > 16) tmem_columns<N - 16>(at + 16, v + 16);
-  } else {
-    tmem_ld8(at, v);
-  }
 }
 
 // largest value of a warp (a NaN is passed over)
@@ -277,41 +253,48 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
 __device__ __forceinline__ float4 lds_f4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
 struct PageScale {
-  float ck, ve;   // 2^key exponent (NaN: not a page), value exponent
-  float ve_low;   // the tile's least value exponent
-  int far;        // the tile's value exponents lie far apart
+  float ck, ve;           // 2^key exponent (NaN: not a page), value exponent
+  float ve_low, ve_high;  // the tile's least and largest value exponents
+};
+
+// Where a CTA's n-th tile of K (or of V) is among N places, and its parity there.
+template <int N>
+struct Place {
+  int slot;
+  unsigned parity;
+  __device__ __forceinline__ explicit Place(unsigned number) : slot(number % N), parity(number / N & 1u) {}
 };
 
 // ---------------------------------------------------------------------------
 // the kernel
 // ---------------------------------------------------------------------------
 template <int R, int NP>
-__global__ void __launch_bounds__(Shape<R, NP>::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const AttendParams P) {
   using S = Shape<R, NP>;
-  constexpr int kW = S::kW, kFirstOut = 4 + 4 * S::kGroups;
   extern __shared__ __align__(1024) unsigned char at_dyn[];
-  // full / empty: a tile's codes; sfull: its scores are there; pfull / pempty:
-  // its weights in shared memory (its scores are read); ofull / oempty: its outputs;
-  // mfull / mempty: its maxima (top_s); efull / eempty: a piece's sums of
-  // weights; qfull / qempty: its queries; rfull / rempty: its record;
-  // landed: a patched tile's V is there; patched: it is patched
+  // kfull / kempty, vfull / vempty: a tile's K, V; sfull / sempty: a step's scores; pfull /
+  // pempty: its weights in shared memory; ofull / oempty: its outputs; mfull /
+  // mempty: its maxima (top_s); qfull / qempty: a piece's queries; rfull /
+  // rempty: its record; landed: V of a tile that is patched before it is vfull;
+  // patched: it is; drain: no product is under way
   struct Bars {
-    uint64_t full[S::kStages], empty[S::kStages];
-    uint64_t sfull[kScores], pfull[2], pempty[2], ofull[2], oempty[2], mfull[2], mempty[2], efull[2], eempty[2];
-    uint64_t qfull[2], qempty[2], landed[kPatchRing], patched[kPatchRing], rfull[kPieceRing], rempty[kPieceRing], drain;
+    uint64_t kfull[S::kStages], vfull[S::kStages], kempty[S::kStages], vempty[S::kStages];
+    uint64_t sfull[S::kScores], sempty[S::kScores], pfull[2], pempty[2], ofull[2], oempty[2], mfull[2], mempty[2];
+    uint64_t qfull[2], qempty[2], landed[kPatchRing], patched[kPatchRing], rfull[kPieceRing], rempty[kPieceRing], drain[2];
   };
   constexpr int kBars = sizeof(Bars) / 8;
   __shared__ Bars bar;
   __shared__ uint32_t tmem_s;
-  __shared__ int fault_s, issued_s;
+  __shared__ int fault_s;
+  __shared__ unsigned issued_s, parity_s;  // barriers that copies count on (kfull, vfull, landed), the last one's parity
   __shared__ __align__(16) Piece piece_s[kPieceRing];
   __shared__ __align__(16) PageScale scale_s[kScaleRing][8];
-  __shared__ __align__(16) float most_s[S::kGroups][2][4][kW], most_x_s[S::kGroups][4][kW];
-  __shared__ __align__(16) float ref_s[4 * S::kGroups][3][kW], cq_s[2][R], top_s[2][R], sum_s[2][S::kTurns][4][R];
-  __shared__ __align__(16) float2 mix_s[2][R];
-  __shared__ float sum_unit_s[2][S::kTurns][R];
+  __shared__ int place_of_page_s[kScaleRing][8];  // rows of the pages' copies, -1: none
+  __shared__ bool special_s[kScaleRing];          // tiles that are patched
+  __shared__ __align__(16) float most_s[2][2][4][R], ref_s[8][R], cq_s[2][R], top_s[2][R], sum_s[R];
+  __shared__ __align__(16) float2 mix_s[2][R], far_s[2][4][R];
   __shared__ __align__(16) float row_s[R];
   __shared__ long long place_s[R];
   __shared__ unsigned char token_s[2][R];
@@ -324,27 +307,29 @@ __global__ void __launch_bounds__(Shape<R, NP>::kThreads, 1)
   unsigned char* vring = kring + S::kStages * S::kSlot;
   unsigned char* qbuf = vring + S::kStages * S::kSlot;
   unsigned char* pbuf = qbuf + 4 * S::kQHalf;
-  unsigned long long* mask_s = reinterpret_cast<unsigned long long*>(pbuf + 4 * S::kPHalf);
-  unsigned short* parent_s = reinterpret_cast<unsigned short*>(mask_s + 2 * kMaxRows);
+  unsigned char* ones = pbuf + 4 * S::kPHalf;
+  using Mask = typename S::Mask;
+  Mask* mask_s = reinterpret_cast<Mask*>(ones + 4 * S::kOnes);  // [2][n], with parents
+  unsigned short* parent_s = reinterpret_cast<unsigned short*>(mask_s + 2 * P.n);
   volatile int* fault = &fault_s;
 
   pdl_launch_dependents();
   if (tid < kBars) {
     uint64_t* at = reinterpret_cast<uint64_t*>(&bar) + tid;
     unsigned count = 1;
-    if (at >= bar.pfull && at < bar.pempty) count = 4 * S::kColumns;  // pfull
-    if (at >= bar.oempty && at < bar.mfull) count = 4;            // oempty
-    if (at >= bar.sfull && at < bar.pfull) count = 2;             // sfull
-    if (at >= bar.mfull && at < bar.mempty) count = S::kColumns;  // mfull
-    if (at >= bar.mempty && at < bar.efull) count = 4;            // mempty
-    if (at >= bar.efull && at < bar.eempty) count = 4 * S::kGroups;  // efull
-    if (at >= bar.eempty && at < bar.qfull) count = 4;            // eempty
-    if (at >= bar.qempty && at < bar.landed) count = 4;           // qempty
-    if (at >= bar.rempty && at < &bar.drain) count = 7 + 4 * S::kGroups;  // rempty
+    if (at >= bar.sfull && at < bar.sempty) count = 2;   // sfull
+    if (at >= bar.sempty && at < bar.pempty) count = 4;  // sempty, pfull
+    if (at >= bar.oempty && at < bar.mfull) count = 4;   // oempty
+    if (at >= bar.mempty && at < bar.qfull) count = 4;   // mempty
+    if (at >= bar.qempty && at < bar.landed) count = 4;  // qempty
+    if (at >= bar.rempty && at < bar.drain) count = 15;  // rempty
     mbar_init(at, count);
     mbar_fence_init();
   }
-  if (tid == 0) fault_s = issued_s = 0;
+  if (tid == 0) fault_s = 0, issued_s = parity_s = 0u;
+  // (rows of the sums' factors that are not the first: of no use, but of defined values)
+  for (int i = tid; i < 4 * S::kOnes / 16; i += kThreads) reinterpret_cast<uint4*>(ones)[i] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async();
   if (warp == 1) {
     tmem_alloc(&tmem_s, S::kTmemCols);
     tmem_relinquish();
@@ -352,7 +337,7 @@ __global__ void __launch_bounds__(Shape<R, NP>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem_sc = tmem_s, tmem_o = tmem_s + kScores * R;
+  const uint32_t tmem_sc = tmem_s, tmem_o = tmem_s + 2 * S::kScores * R, tmem_l = tmem_o + 2 * NP * R;
 
   // the next piece, for all roles but the one that makes them
   int pieces = 0;
@@ -378,8 +363,44 @@ __global__ void __launch_bounds__(Shape<R, NP>::kThreads, 1)
     const unsigned page_bytes = static_cast<unsigned>(P.page) * 128u;
     int it = 0;
     bool ok = true;
+    // K or V of a tile to its place, counted on a barrier that is number `on` among kfull, vfull and landed
+    const auto copy = [&](const CUtensorMap* map, int tile, unsigned char* to, uint64_t* empty, uint64_t* full, int on,
+                          unsigned on_parity) {
+      const Place<S::kStages> at(tile);
+      const int y = lane < pp ? place_of_page_s[tile % kScaleRing][lane] : -1;
+      const unsigned bytes =
+          static_cast<unsigned>(__popc(__ballot_sync(0xffffffffu, y >= 0))) * page_bytes * NP + P.more_bytes;
+      if (!at_wait(&empty[at.slot], at.parity ^ 1u, fault)) return false;
+      if (leader) {
+        mbar_expect_tx(full, bytes);
+        issued_s |= 1u << on;
+        parity_s = (parity_s & ~(1u << on)) | on_parity << on;
+      }
+      __syncwarp();
+      if (y >= 0) {
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+          tma_load_2d(to + at.slot * S::kSlot + lane * page_bytes + p * kPanel, map, p * 128, y, full);
+      }
+      __syncwarp();
+      return true;
+    };
+    int patches = 0;
+    const auto copy_k = [&](int tile) {
+      const Place<S::kStages> at(tile);
+      return copy(&tm_k, tile, kring, bar.kempty, &bar.kfull[at.slot], at.slot, at.parity);
+    };
+    const auto copy_v = [&](int tile) {
+      if (special_s[tile % kScaleRing]) {
+        const Place<kPatchRing> at(patches++);
+        return copy(&tm_v, tile, vring, bar.vempty, &bar.landed[at.slot], 2 * S::kStages + at.slot, at.parity);
+      }
+      const Place<S::kStages> at(tile);
+      return copy(&tm_v, tile, vring, bar.vempty, &bar.vfull[at.slot], S::kStages + at.slot, at.parity);
+    };
     Piece w;
     while (ok && next_piece(w)) {
+      const int special = first_special(w);
       const int* table = P.block_table + static_cast<long long>(w.b) * P.table_pages;
       // the pages of `batch` tiles, a lane each
       const auto has_page = [&](int tb) { return tb + mine < w.t1 && ((tb + mine) * pp + slot_in) * P.page < w.keys; };
@@ -407,130 +428,68 @@ __global__ void __launch_bounds__(Shape<R, NP>::kThreads, 1)
         x.ck = bad ? __uint_as_float(0x7fc00000u) : exp2i(ke);
         x.ve = static_cast<float>(ve);
         x.ve_low = static_cast<float>(lo);
-        x.far = hi - lo > kFar;
-        const unsigned groups = __ballot_sync(0xffffffffu, has);
+        x.ve_high = static_cast<float>(hi);
         const int y = static_cast<int>(slab * P.page);
 #pragma unroll 1
         for (int i = 0; i < batch && tb + i < w.t1; ++i, ++it) {
-          const int s = it % S::kStages;
-          const unsigned parity = (static_cast<unsigned>(it / S::kStages) & 1u) ^ 1u;
-          const unsigned bytes = static_cast<unsigned>(__popc(groups >> (i * pp) & ((1u << pp) - 1u))) * page_bytes * 2 * NP +
-                                 P.more_bytes;
-          unsigned char* dst = kring + s * S::kSlot + slot_in * page_bytes;
-          ok = at_wait(&bar.empty[s], parity, fault);
-          if (!ok) break;
-          if (mine == i) scale_s[it % kScaleRing][slot_in] = x;
-          __syncwarp();
-          if (leader) mbar_expect_tx(&bar.full[s], bytes);
-          __syncwarp();
-          if (mine == i && has) {
-#pragma unroll
-            for (int p = 0; p < NP; ++p) tma_load_2d(dst + p * kPanel, &tm_k, p * 128, y, &bar.full[s]);
-#pragma unroll
-            for (int p = 0; p < NP; ++p)
-              tma_load_2d(dst + S::kStages * S::kSlot + p * kPanel, &tm_v, p * 128, y, &bar.full[s]);
+          if (mine == i) {
+            scale_s[it % kScaleRing][slot_in] = x;
+            place_of_page_s[it % kScaleRing][slot_in] = has ? y : -1;
           }
+          if (leader) special_s[it % kScaleRing] = tb + i >= special;
           __syncwarp();
-          if (leader) issued_s = it + 1;
+          ok = copy_k(it) && (tb + i - w.t0 < kAhead || copy_v(it - kAhead));
+          if (!ok) break;
         }
       }
+      // (V's last ones wait for no other piece, whose queries may wait for this one's end)
+      const int n = w.t1 - w.t0;
+#pragma unroll 1
+      for (int j = max(0, n - kAhead); ok && j < n; ++j) ok = copy_v(it - n + j);
     }
   } else if (warp == 1) {
-    // ---------------- products ----------------
-    constexpr uint32_t idesc_s = idesc_e4m3(kTile, R, 0, 0), idesc_o = idesc_e4m3(128, R, 1, 1);
+    // ---------------- scores ----------------
+    constexpr uint32_t idesc = idesc_e4m3(kTile, R, 0, 0), high = operand_high(1024, 128);
     const int steps = (P.D + 31) / 32;
-    int it = 0, qn = 0, patches = 0;
-    bool ok = true;
     const uint32_t issues = leader ? 1u : 0u;
-    // the outputs of tile j
-    const auto outputs = [&](int j, int patch) {
-      const int s = j % S::kStages, d = j & 1;
-      const unsigned half = static_cast<unsigned>(j >> 1) & 1u;
-      if (patch >= 0 && !at_wait(&bar.patched[patch % kPatchRing], static_cast<unsigned>(patch / kPatchRing) & 1u, fault))
-        return false;
-      if (!at_wait(&bar.oempty[d], half ^ 1u, fault) || !at_wait(&bar.pfull[d], half, fault)) return false;
-      tc_fence_after();
-      const uint32_t b = operand_low(smem_addr(pbuf + 2 * d * S::kPHalf), 8 * S::kPRow);
-      constexpr uint32_t a_high = operand_high(1024, 128), b_high = operand_high(8 * S::kPRow, S::kPRow);
-#pragma unroll
-      for (int p = 0; p < NP; ++p) {
-        const uint32_t a = operand_low(smem_addr(vring + s * S::kSlot + p * kPanel), 1024), o = tmem_o + (d * NP + p) * R;
-        umma_e4m3<false>(issues, o, a, a_high, b, b_high, idesc_o);
-#pragma unroll
-        for (int k = 1; k < 2 * kTile / 32; ++k)  // hi's 4 steps of 32 tokens, then lo's
-          umma_e4m3<true>(issues, o, a + (k & 3) * (32 * 128 >> 4), a_high,
-                          b + (k >> 2) * (S::kPHalf >> 4) + (k & 3) * (32 * S::kPRow >> 4), b_high, idesc_o);
-      }
-      commit_if(issues, &bar.ofull[d]);
-      commit_if(issues, &bar.empty[s]);
-      commit_if(issues, &bar.pempty[d]);
-      return true;
-    };
-    // one loop over the tiles, scores two tiles ahead of the outputs
+    int it = 0, step = 0, qn = 0;
+    bool ok = true;
     Piece w;
-    bool more = next_piece(w);
-    int t = more ? w.t0 : 0, special = more ? first_special(w) : 0;
-    int sb = 0, patch0 = -1, patch1 = -1;  // place of the scores; the last two tiles' among the patched ones
-    constexpr int kUnknown = 0x40000000;
-    int end = kUnknown;  // the number of tiles, once it is known
-    for (; it < end + 2; ++it) {
-      int patch = -1;
-      // (where a piece's queries, or the codes' place, wait for the outputs of the tile two before: those first)
-      const bool outputs_first = more && (t == w.t0 || S::kStages == 2);
+    while (ok && next_piece(w)) {
+      const uint32_t q_hi = operand_low(smem_addr(qbuf + 2 * (qn & 1) * S::kQHalf), 1024);
+      ok = at_wait(&bar.qfull[qn & 1], static_cast<unsigned>(qn >> 1) & 1u, fault);
+      ++qn;
 #pragma unroll 1
-      for (int turn = 0; turn < 2 && ok; ++turn) {
-        if ((turn == 0) == outputs_first) {
-          if (it > 1) ok = outputs(it - 2, patch1);
-        } else if (more) {
-          const int s = it % S::kStages;
-          if (t == w.t0) ok = at_wait(&bar.qfull[qn & 1], static_cast<unsigned>(qn >> 1) & 1u, fault);
-          ok = ok && at_wait(&bar.full[s], static_cast<unsigned>(it / S::kStages) & 1u, fault);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t a = operand_low(smem_addr(kring + s * S::kSlot), 1024), d = tmem_sc + sb * R;
-          const uint32_t b = operand_low(smem_addr(qbuf + 2 * (qn & 1) * S::kQHalf), 1024);
-          constexpr uint32_t high = operand_high(1024, 128);
-          umma_e4m3<false>(issues, d, a, high, b, high, idesc_s);
+      for (int t = w.t0; ok && t < w.t1; ++t, ++it) {
+        // (a step's two tiles, the second one perhaps missing)
+        const int sb = step % S::kScores, sub = (t - w.t0) & 1;
+        const Place<S::kStages> at(it);
+        if (sub == 0) ok = at_wait(&bar.sempty[sb], (static_cast<unsigned>(step / S::kScores) & 1u) ^ 1u, fault);
+        ok = ok && at_wait(&bar.kfull[at.slot], at.parity, fault);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t a = operand_low(smem_addr(kring + at.slot * S::kSlot), 1024), d = tmem_sc + (2 * sb + sub) * R;
+        umma_e4m3(issues, d, a, high, q_hi, high, idesc, 0u);
 #pragma unroll
-          for (int k = 1; k < 8 * NP; ++k) {  // hi's steps of 32 elements, then lo's
-            const int step = k % (4 * NP);
-            if (step < steps)
-              umma_e4m3<true>(issues, d, a + (step >> 2) * (kPanel >> 4) + (step & 3) * 2, high,
-                              b + k / (4 * NP) * (S::kQHalf >> 4) + (step >> 2) * (R * 128 >> 4) + (step & 3) * 2, high,
-                              idesc_s);
-          }
+        for (int k = 1; k < 8 * NP; ++k) {  // hi's steps of 32 elements, then lo's
+          const int e = k % (4 * NP);
+          if (e < steps)
+            umma_e4m3(issues, d, a + (e >> 2) * (kPanel >> 4) + (e & 3) * 2, high,
+                            q_hi + k / (4 * NP) * (S::kQHalf >> 4) + (e >> 2) * (R * 128 >> 4) + (e & 3) * 2, high,
+                      idesc, 1u);
+        }
+        commit_if(issues, &bar.kempty[at.slot]);
+        if (sub == 1 || t + 1 == w.t1) {
           commit_if(issues, &bar.sfull[sb]);
           if (leader) mbar_arrive(&bar.sfull[sb]);  // what the copies' and queries' warps wrote is visible behind it
-          if (t >= special) {
-            // (a warp that comes to a barrier's phase two phases early would pass: the
-            // patching warp, which skips tiles, is told when its tile is there)
-            patch = patches++;
-            if (leader) mbar_arrive(&bar.landed[patch % kPatchRing]);
-          }
-          __syncwarp();
-          sb = sb == kScores - 1 ? 0 : sb + 1;
+          ++step;
         }
-      }
-      if (!ok) break;
-      patch1 = patch0;
-      patch0 = patch;
-      if (more && ++t == w.t1) {
-        ++qn;
-        more = next_piece(w);
-        if (more) {
-          t = w.t0;
-          special = first_special(w);
-        } else {
-          end = it + 1;
-        }
-      } else if (!more && end == kUnknown) {
-        break;  // (no tiles at all)
+        __syncwarp();
       }
     }
     // every product issued has completed before tensor memory is released
-    if (leader) umma_commit(&bar.drain);
-    __syncwarp();
-    mbar_wait(&bar.drain, 0);
+    commit_if(issues, &bar.drain[0]);
+    mbar_wait(&bar.drain[0], 0);
   } else if (warp == 2) {
     // ---------------- pieces, queries, masks ----------------
     const auto lengths = [&](int b) { return lengths_of(P, b); };
@@ -696,7 +655,7 @@ __global__ void __launch_bounds__(Shape<R, NP>::kThreads, 1)
         }
         if (P.parent) {
           // which of the block's rows' tokens see drafted token j
-          unsigned long long* mask = mask_s + qb * kMaxRows;
+          Mask* mask = mask_s + qb * P.n;
           const int* parent = P.parent + static_cast<long long>(b) * P.n;
           bool bad = false;
           for (int j = lane; j < s.count; j += 32) {
@@ -713,7 +672,7 @@ __global__ void __launch_bounds__(Shape<R, NP>::kThreads, 1)
           for (int i = lane; i < R; i += 32) {
             const int tok = tok0 + i;
             if (tok >= s.count || tok * P.G >= row0 + R) break;
-            const unsigned long long bit = 1ull << i;
+            const Mask bit = static_cast<Mask>(1) << i;
             for (int j = tok;; j = parent_s[j]) {
               atomicOr(mask + j, bit);
               if (j == 0) break;
@@ -740,233 +699,308 @@ __global__ void __launch_bounds__(Shape<R, NP>::kThreads, 1)
     }
     if (leader) P.shared[cta] = ok ? shared : make_int4(0, 0, 0, 0);
   } else if (warp == 3) {
-    // ---------------- what no row sees, and NaN values among the drafted tokens ----------------
-    int it = 0, patches = 0;
+    // ---------------- outputs' products ----------------
+    // (and, before them, V of what no row sees, and NaN values among the drafted tokens)
+    constexpr uint32_t idesc = idesc_e4m3(128, R, 1, 1), idesc_l = idesc_e4m3(64, R, 0, 1);
+    constexpr uint32_t a_high = operand_high(1024, 128), b_high = operand_high(8 * S::kPRow, S::kPRow);
+    const uint32_t issues = leader ? 1u : 0u;
+    int it = 0, step = 0, patches = 0;
     bool ok = true;
     Piece w;
     while (ok && next_piece(w)) {
-      it += w.t1 - w.t0;
-      for (int t = max(w.t0, first_special(w)); ok && t < w.t1; ++t, ++patches) {
-        const int j = it - (w.t1 - t), s = j % S::kStages;
-        ok = at_wait(&bar.landed[patches % kPatchRing], static_cast<unsigned>(patches / kPatchRing) & 1u, fault) &&
-             at_wait(&bar.full[s], static_cast<unsigned>(j / S::kStages) & 1u, fault);
-        if (!ok) break;
+      const int special = first_special(w);
 #pragma unroll 1
-        for (int row = lane; row < kTile; row += 32) {
-          const int pos = t * kTile + row;
-          unsigned char* v = vring + s * S::kSlot + row * 128;
-          bool clear = pos >= w.keys, nan = false;
-          if (!clear && pos >= w.prefix) {
+      for (int t = w.t0; ok && t < w.t1; ++t, ++it) {
+        const int k = step & 1, sub = (t - w.t0) & 1;
+        const unsigned half = static_cast<unsigned>(step >> 1) & 1u;
+        if (sub == 0) {
+          // (the weights of a step wait for its patches)
 #pragma unroll 1
-            for (int p = 0; p < NP; ++p)
+          for (int u = max(t, special); ok && u < min(t + 2, w.t1); ++u, ++patches) {
+            ok = at_wait(&bar.landed[patches % kPatchRing], static_cast<unsigned>(patches / kPatchRing) & 1u, fault);
+            if (!ok) break;
+            const Place<S::kStages> at(it + u - t);
+#pragma unroll 1
+            for (int row = lane; row < kTile; row += 32) {
+              const int pos = u * kTile + row;
+              unsigned char* v = vring + at.slot * S::kSlot + row * 128;
+              bool clear = pos >= w.keys, nan = false;
+              if (!clear && pos >= w.prefix) {
+#pragma unroll 1
+                for (int p = 0; p < NP; ++p)
 #pragma unroll
-              for (int o = 0; o < 128; o += 16) {
-                const uint4 x = *reinterpret_cast<const uint4*>(v + p * kPanel + o);
-                const uint32_t m = 0x7f7f7f7fu, one = 0x01010101u;
-                nan |= ((((x.x & m) + one) | ((x.y & m) + one) | ((x.z & m) + one) | ((x.w & m) + one)) & 0x80808080u) != 0;
+                  for (int o = 0; o < 128; o += 16) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(v + p * kPanel + o);
+                    const uint32_t m = 0x7f7f7f7fu, one = 0x01010101u;
+                    nan |=
+                        ((((x.x & m) + one) | ((x.y & m) + one) | ((x.z & m) + one) | ((x.w & m) + one)) & 0x80808080u) != 0;
+                  }
+                clear = nan;
               }
-            clear = nan;
-          }
-          if (clear) {
+              if (clear) {
 #pragma unroll 1
-            for (int p = 0; p < NP; ++p)
+                for (int p = 0; p < NP; ++p)
 #pragma unroll
-              for (int o = 0; o < 128; o += 16) *reinterpret_cast<uint4*>(v + p * kPanel + o) = make_uint4(0, 0, 0, 0);
+                  for (int o = 0; o < 128; o += 16) *reinterpret_cast<uint4*>(v + p * kPanel + o) = make_uint4(0, 0, 0, 0);
+              }
+              const unsigned all = __ballot_sync(0xffffffffu, nan);
+              if (leader) nan_s[patches % kPatchRing][row >> 5] = all;
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (leader) {
+              mbar_arrive(&bar.patched[patches % kPatchRing]);
+              mbar_arrive(&bar.vfull[at.slot]);
+            }
           }
-          const unsigned all = __ballot_sync(0xffffffffu, nan);
-          if (leader) nan_s[patches % kPatchRing][row >> 5] = all;
+          ok = ok && at_wait(&bar.oempty[k], half ^ 1u, fault) && at_wait(&bar.pfull[k], half, fault);
         }
-        fence_proxy_async();
-        __syncwarp();
-        if (leader) mbar_arrive(&bar.patched[patches % kPatchRing]);
+        const Place<S::kStages> at(it);
+        ok = ok && at_wait(&bar.vfull[at.slot], at.parity, fault);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t b = operand_low(smem_addr(pbuf + 2 * k * S::kPHalf + sub * kTile * S::kPRow), 8 * S::kPRow);
+        const uint32_t a0 = operand_low(smem_addr(vring + at.slot * S::kSlot), 1024);
+        const uint32_t first = sub == 0 ? 0u : 1u;
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+          const uint32_t a = a0 + p * (kPanel >> 4), o = tmem_o + (k * NP + p) * R;
+#pragma unroll
+          for (int i = 0; i < 2 * kTile / 32; ++i)  // hi's 4 steps of 32 tokens, then lo's
+            umma_e4m3(issues, o, a + (i & 3) * (32 * 128 >> 4), a_high,
+                      b + (i >> 2) * (S::kPHalf >> 4) + (i & 3) * (32 * S::kPRow >> 4), b_high, idesc,
+                      i == 0 ? first : 1u);
+        }
+        // the sums of the weights: products with one row of factors (every 8 rows of
+        // the operand are the same, a stride of 0), the first of the 64 results is used
+        const uint32_t f = operand_low(smem_addr(ones + (2 * k + sub) * S::kOnes), 0);
+#pragma unroll
+        for (int i = 0; i < 2 * kTile / 32; ++i)
+          umma_e4m3(issues, tmem_l + k * R, f + (i & 3) * 2, operand_high(0, 128),
+                    b + (i >> 2) * (S::kPHalf >> 4) + (i & 3) * (32 * S::kPRow >> 4), b_high, idesc_l,
+                    i == 0 ? first : 1u);
+        commit_if(issues, &bar.vempty[at.slot]);
+        if (sub == 1 || t + 1 == w.t1) {
+          commit_if(issues, &bar.ofull[k]);
+          commit_if(issues, &bar.pempty[k]);
+          ++step;
+        }
       }
     }
-  } else if (warp < kFirstOut) {
+    commit_if(issues, &bar.drain[1]);
+    mbar_wait(&bar.drain[1], 0);
+  } else if (warp < 12) {
     // ---------------- weights ----------------
-    const int group = (warp - 4) >> 2, turn = group / S::kColumns, q = warp & 3, row = q * 32 + lane;
-    const int col0 = group % S::kColumns * kW;
+    // Every other step, all rows of the block; a thread has a token of each of
+    // the step's tiles.  The scores are read twice, for the maxima and for the
+    // weights, 16 rows at a time: the same few instructions again and again
+    // (what these warps wait for most is instructions).
+    const int turn = (warp - 4) >> 2, q = warp & 3, row = q * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
     const int page_row = row / P.page;
-    const int col = lane % kW;  // lanes i and i + kW do the same for row col0 + i
-    float(*refs)[kW] = ref_s[warp - 4];
-    int it = 0, qn = 0, patches = 0;
+    float* refs = ref_s[warp - 4];
+    unsigned char* weights = pbuf + 2 * turn * S::kPHalf;
+    unsigned char* factors = ones + 2 * turn * S::kOnes + row;
+    int it = 0, step = 0, qn = 0, patches = 0;
     bool ok = true;  // (what a wait of this warp's gave; the warpgroup goes by what its warps agree on)
     Piece w;
     while (true) {
       const bool got = next_piece(w);
-      if (!meet(1 + group, got)) break;
+      if (!meet(1 + turn, got)) break;
       const int special = first_special(w), qb = qn & 1, tok0 = w.block * R / P.G;
-      float sum_unit = -kInf;  // log2 of the sums' unit, of row col0 + col
-      float2 sum[kW / 2];
-#pragma unroll
-      for (int i = 0; i < kW / 2; ++i) sum[i] = make_float2(0.f, 0.f);
       bool go = true;
 #pragma unroll 1
-      for (int t = w.t0; t < w.t1; ++t, ++it) {
-        const int patch = t >= special ? patches++ : -1, k = it & 1;
-        if (S::kTurns == 2 && k != turn) continue;
-        const unsigned half = static_cast<unsigned>(it >> 1) & 1u;
-        const int sb = it % kScores;
-        ok = at_wait(&bar.sfull[sb], static_cast<unsigned>(it / kScores) & 1u, fault) && ok;
+      for (int t = w.t0; t < w.t1; t += 2, ++step) {
+        const int tiles = min(2, w.t1 - t);
+        const int at = it, patch = patches;
+        it += tiles;
+        patches += max(0, min(tiles, t + tiles - special));
+        if ((step & 1) != turn) continue;
+        const unsigned half = static_cast<unsigned>(step >> 1) & 1u;
+        const int sb = step % S::kScores;
+        ok = at_wait(&bar.sfull[sb], static_cast<unsigned>(step / S::kScores) & 1u, fault) && ok;
         tc_fence_after();
-        float y[kW];
-        tmem_columns<kW>(tmem_sc + sb * R + col0 + lanes, y);
-        const PageScale ps = scale_s[it % kScaleRing][page_row];
-        // y = score + value exponent
-#pragma unroll
-        for (int r = 0; r < kW; r += 4) {
-          const float4 c = lds_f4(&cq_s[qb][col0 + r]);
-          const float2 ck = make_float2(ps.ck, ps.ck), ve = make_float2(ps.ve, ps.ve);
-          const float2 a = ffma2(fmul2(make_float2(y[r], y[r + 1]), make_float2(c.x, c.y)), ck, ve);
-          const float2 b = ffma2(fmul2(make_float2(y[r + 2], y[r + 3]), make_float2(c.z, c.w)), ck, ve);
-          y[r] = a.x, y[r + 1] = a.y, y[r + 2] = b.x, y[r + 3] = b.y;
+        const PageScale ps0 = scale_s[at % kScaleRing][page_row], ps1 = scale_s[(at + tiles - 1) % kScaleRing][page_row];
+        // what the rows see of this thread's tokens
+        Mask seen0 = ~static_cast<Mask>(0), seen1 = seen0;
+        bool nan0 = false, nan1 = false;
+        if (t + tiles > special) {
+          const auto look = [&](int tile, int patch, Mask& seen, bool& nan) {
+            if (tile < special) return;
+            ok = at_wait(&bar.patched[patch % kPatchRing], static_cast<unsigned>(patch / kPatchRing) & 1u, fault) && ok;
+            const int pos = tile * kTile + row, j = pos - w.prefix;
+            if (pos >= w.keys) seen = 0;
+            else if (j >= 0 && P.parent) seen = mask_s[qb * P.n + j];
+            else if (j > tok0) seen = j - tok0 >= static_cast<int>(8 * sizeof(Mask)) ? 0 : ~static_cast<Mask>(0) << (j - tok0);
+            nan = nan_s[patch % kPatchRing][q] >> lane & 1u;
+          };
+          look(t, patch, seen0, nan0);
+          if (tiles == 2) look(t + 1, patch + (t >= special ? 1 : 0), seen1, nan1);
         }
-        if (patch >= 0) {
-          ok = at_wait(&bar.patched[patch % kPatchRing], static_cast<unsigned>(patch / kPatchRing) & 1u, fault) && ok;
-          const int pos = t * kTile + row, j = pos - w.prefix;
-          unsigned long long seen = ~0ull;
-          if (pos >= w.keys) seen = 0;
-          else if (j >= 0 && P.parent) seen = mask_s[qb * kMaxRows + j];
-          else if (j > tok0) seen = j - tok0 > 63 ? 0 : ~0ull << (j - tok0);
-          const bool nan = nan_s[patch % kPatchRing][q] >> lane & 1u;
+        // 16 rows' scores, base 2, plus the value exponent
+        const auto scores = [&](int sub, int c, float* y) {
+          tmem_ld16(tmem_sc + (2 * sb + sub) * R + c + lanes, y);
+          const float ck = sub ? ps1.ck : ps0.ck, ve = sub ? ps1.ve : ps0.ve;
+          const float2 ck2 = make_float2(ck, ck), ve2 = make_float2(ve, ve);
 #pragma unroll
-          for (int r = 0; r < kW; ++r) {
-            if (nan) y[r] = __uint_as_float(0x7fc00000u);
-            if (!(seen >> token_s[qb][col0 + r] & 1ull)) y[r] = -kInf;
+          for (int r = 0; r < 16; r += 4) {
+            const float4 f = lds_f4(&cq_s[qb][c + r]);
+            const float2 a = ffma2(fmul2(make_float2(y[r], y[r + 1]), make_float2(f.x, f.y)), ck2, ve2);
+            const float2 b = ffma2(fmul2(make_float2(y[r + 2], y[r + 3]), make_float2(f.z, f.w)), ck2, ve2);
+            y[r] = a.x, y[r + 1] = a.y, y[r + 2] = b.x, y[r + 3] = b.y;
           }
-        }
+          if (t + sub >= special) {
+            const Mask seen = sub ? seen1 : seen0;
+            const bool nan = sub ? nan1 : nan0;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+              if (nan) y[r] = __uint_as_float(0x7fc00000u);
+              if (!(seen >> token_s[qb][c + r] & 1)) y[r] = -kInf;
+            }
+          }
+        };
         // the rows' largest
-        const int slot = S::kTurns == 2 ? it >> 1 & 1 : k;
+        const int slot = step >> 1 & 1;
+#pragma unroll 1
+        for (int c = 0; c < R; c += 16) {
+          float top[16];
+          scores(0, c, top);
+          if (tiles == 2) {
+            float y[16];
+            scores(1, c, y);
 #pragma unroll
-        for (int r = 0; r < kW; r += 4) {
-          const float4 m = make_float4(warp_max(y[r]), warp_max(y[r + 1]), warp_max(y[r + 2]), warp_max(y[r + 3]));
-          if (leader) *reinterpret_cast<float4*>(&most_s[group][slot][q][r]) = m;
-        }
-        if (ps.far) {
+            for (int r = 0; r < 16; ++r) top[r] = fmaxf(top[r], y[r]);
+          }
 #pragma unroll
-          for (int r = 0; r < kW; ++r) {
-            const float m = warp_max(y[r] - ps.ve);
-            if (leader) most_x_s[group][q][r] = m;
+          for (int r = 0; r < 16; r += 4) {
+            const float4 m =
+                make_float4(warp_max(top[r]), warp_max(top[r + 1]), warp_max(top[r + 2]), warp_max(top[r + 3]));
+            if (leader) *reinterpret_cast<float4*>(&most_s[turn][slot][q][c + r]) = m;
           }
         }
-        go = meet(1 + group, ok);
+        go = meet(1 + turn, ok);
         if (!go) break;
         // every warp for itself: a lane per row
-        const float m = fmaxf(fmaxf(most_s[group][slot][0][col], most_s[group][slot][1][col]),
-                              fmaxf(most_s[group][slot][2][col], most_s[group][slot][3][col]));
-        const bool none = m == -kInf;
-        refs[0][col] = none ? 0.f : m - 8.f;
-        if (q == 0) {
-          ok = at_wait(&bar.mempty[k], half ^ 1u, fault);
-          top_s[k][col0 + col] = m - 8.f;
+        if (q == 0) ok = at_wait(&bar.mempty[turn], half ^ 1u, fault);
+#pragma unroll
+        for (int c = lane; c < R; c += 32) {
+          const float m = fmaxf(fmaxf(most_s[turn][slot][0][c], most_s[turn][slot][1][c]),
+                                fmaxf(most_s[turn][slot][2][c], most_s[turn][slot][3][c]));
+          refs[c] = m == -kInf ? 0.f : m - 8.f;
+          if (q == 0) top_s[turn][c] = m - 8.f;
+        }
+        ok = at_wait(&bar.pempty[turn], half ^ 1u, fault) && ok;
+        const float low = fminf(ps0.ve_low, ps1.ve_low);
+        if (fmaxf(ps0.ve_high, ps1.ve_high) - low > static_cast<float>(kFar)) {
+          // The values' exponents lie too far apart for the factors: the sums of
+          // the weights 2^x themselves, each warp's with its own largest as unit
+#pragma unroll 1
+          for (int c = 0; c < R; c += 16) {
+            float x[16], x1[16];
+            scores(0, c, x);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) x[r] -= ps0.ve, x1[r] = -kInf;
+            if (tiles == 2) {
+              scores(1, c, x1);
+#pragma unroll
+              for (int r = 0; r < 16; ++r) x1[r] -= ps1.ve;
+            }
+            float unit = -kInf;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+              const float m = warp_max(fmaxf(x[r], x1[r])), ref = m == -kInf ? 0.f : m;
+              x[r] = ex2(x[r] - ref) + ex2(x1[r] - ref);
+              if ((lane & 15) == r) unit = m;
+            }
+            const float sum = column_sums<16>(x, lane);
+            if (lane < 16) far_s[turn][q][c + lane] = make_float2(sum, unit);
+          }
+        } else {
+          const auto code = [&](float ve) {  // of 2^(low - ve), in [2^-9, 1]
+            const int e = static_cast<int>(low - ve);
+            return static_cast<unsigned char>(e >= -6 ? (e + 7) << 3 : 1 << (e + 9));
+          };
+          factors[0] = code(ps0.ve);
+          factors[S::kOnes] = code(ps1.ve);
         }
         __syncwarp();
-        if (q == 0 && leader) mbar_arrive(&bar.mfull[k]);
-        // the sums' reference: the largest score without exponents, or a bound of it
-        float most_x = m - ps.ve_low;
-        if (ps.far) {
-          // (2^(y - reference) may underflow where a page's values are tiny against another's)
-          most_x = fmaxf(fmaxf(most_x_s[group][0][col], most_x_s[group][1][col]),
-                         fmaxf(most_x_s[group][2][col], most_x_s[group][3][col]));
-          const float next = fmaxf(sum_unit, most_x);
-          refs[1][col] = sum_unit == -kInf ? 0.f : ex2(sum_unit - next);
-          refs[2][col] = none ? 0.f : next;
-          sum_unit = next;
-          __syncwarp();
+        if (q == 0 && leader) mbar_arrive(&bar.mfull[turn]);
+#pragma unroll 1
+        for (int sub = 0; sub < tiles; ++sub) {
+#pragma unroll 1
+          for (int c = 0; c < R; c += 16) {
+            float y[16];
+            scores(sub, c, y);
 #pragma unroll
-          for (int r = 0; r < kW; r += 2) {
-            sum[r / 2].x = __fmaf_rn(sum[r / 2].x, refs[1][r], ex2((y[r] - ps.ve) - refs[2][r]));
-            sum[r / 2].y = __fmaf_rn(sum[r / 2].y, refs[1][r + 1], ex2((y[r + 1] - ps.ve) - refs[2][r + 1]));
+            for (int r = 0; r < 16; r += 4) {
+              const float4 f = lds_f4(refs + c + r);
+              const float2 a = fadd2(make_float2(y[r], y[r + 1]), make_float2(-f.x, -f.y));
+              const float2 b = fadd2(make_float2(y[r + 2], y[r + 3]), make_float2(-f.z, -f.w));
+              y[r] = ex2(a.x), y[r + 1] = ex2(a.y), y[r + 2] = ex2(b.x), y[r + 3] = ex2(b.y);
+            }
+            uint32_t hi[8], lo[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) split2(y[2 * i], y[2 * i + 1], hi[i], lo[i]);
+            unsigned char* p = weights + swizzled((sub * kTile + row) * S::kPRow + c, S::kPRow);
+            *reinterpret_cast<uint4*>(p) =
+                make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, hi[4] | hi[5] << 16, hi[6] | hi[7] << 16);
+            *reinterpret_cast<uint4*>(p + S::kPHalf) =
+                make_uint4(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16, lo[4] | lo[5] << 16, lo[6] | lo[7] << 16);
           }
-          meet(1 + group, true);  // (there is one most_x_s)
         }
-#pragma unroll
-        for (int r = 0; r < kW; r += 4) {
-          const float4 c = lds_f4(&refs[0][r]);
-          y[r] = ex2(y[r] - c.x);
-          y[r + 1] = ex2(y[r + 1] - c.y);
-          y[r + 2] = ex2(y[r + 2] - c.z);
-          y[r + 3] = ex2(y[r + 3] - c.w);
-        }
-        ok = at_wait(&bar.pempty[k], half ^ 1u, fault) && ok;
-        unsigned char* p = pbuf + 2 * k * S::kPHalf;
-#pragma unroll
-        for (int r = 0; r < kW; r += 8) {
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) split2(y[r + 2 * i], y[r + 2 * i + 1], hi[i], lo[i]);
-          const uint32_t at = swizzled(row * S::kPRow + col0 + r, S::kPRow);
-          *reinterpret_cast<uint2*>(p + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-          *reinterpret_cast<uint2*>(p + S::kPHalf + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-        }
-        fence_proxy_async();
         tc_fence_before();
+        fence_proxy_async();
         __syncwarp();
-        if (leader) mbar_arrive(&bar.pfull[k]);
-        if (!ps.far) {
-          // the sums of the weights themselves: without the values' exponents
-          const float next = fmaxf(sum_unit, most_x);
-          refs[1][col] = sum_unit == -kInf ? 0.f : ex2(sum_unit - next);
-          refs[2][col] = none ? 0.f : ex2(most_x - next) * 0.00390625f;
-          sum_unit = next;
-          __syncwarp();
-          const float f = exp2i(static_cast<int>(ps.ve_low - ps.ve));
-#pragma unroll
-          for (int r = 0; r < kW; r += 4) {
-            const float4 a = lds_f4(&refs[1][r]), b = lds_f4(&refs[2][r]);
-            sum[r / 2] = ffma2(sum[r / 2], make_float2(a.x, a.y),
-                               fmul2(make_float2(y[r], y[r + 1]), fmul2(make_float2(b.x, b.y), make_float2(f, f))));
-            sum[r / 2 + 1] = ffma2(sum[r / 2 + 1], make_float2(a.z, a.w),
-                                   fmul2(make_float2(y[r + 2], y[r + 3]), fmul2(make_float2(b.z, b.w), make_float2(f, f))));
-          }
+        if (leader) {
+          mbar_arrive(&bar.sempty[sb]);
+          mbar_arrive(&bar.pfull[turn]);
         }
       }
-      // the piece's sums and their units
       if (!go) break;
-      ok = at_wait(&bar.eempty[qb], (static_cast<unsigned>(qn >> 1) & 1u) ^ 1u, fault) && ok;
-      if (!meet(1 + group, ok)) break;
-      float all[kW];
-#pragma unroll
-      for (int i = 0; i < kW / 2; ++i) all[2 * i] = sum[i].x, all[2 * i + 1] = sum[i].y;
-      sum_s[qb][turn][q][col0 + col] = column_sums<kW>(all, lane);
-      if (q == 0) sum_unit_s[qb][turn][col0 + col] = sum_unit;
-      __syncwarp();
-      if (leader) mbar_arrive(&bar.efull[qb]);
       ++qn;
     }
   } else {
     // ---------------- outputs ----------------
     const int q = warp & 3, d = q * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
-    int it = 0, qn = 0;
+    int it = 0, step = 0, qn = 0;
     bool ok = true;
     Piece w;
     while (true) {
       const bool got = next_piece(w);
-      if (!meet(5, got)) break;
-      const int row0 = w.block * R;
-      const int qb = qn & 1;
-      const unsigned piece_half = static_cast<unsigned>(qn >> 1) & 1u;
+      if (!meet(3, got)) break;
+      const int row0 = w.block * R, qb = qn & 1;
       float2 acc[NP][R / 2];
 #pragma unroll
       for (int p = 0; p < NP; ++p)
 #pragma unroll
         for (int r = 0; r < R / 2; ++r) acc[p][r] = make_float2(0.f, 0.f);
       float unit = -kInf;  // log2 of the outputs' unit, of row d
+      // of rows `lane` and `lane` + 32 (warp 0): the sum of weights, log2 of its unit
+      constexpr int kMine = (R + 31) / 32;
+      float sum[kMine], sum_unit[kMine];
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) sum[i] = 0.f, sum_unit[i] = -kInf;
+      const auto add = [&](int i, float s, float u) {  // s 2^u more (of nothing, u is -infinity and s 0 or NaN)
+        const float next = fmaxf(sum_unit[i], u);
+        sum[i] = (sum_unit[i] == -kInf ? sum[i] : sum[i] * ex2(sum_unit[i] - next)) + (u == -kInf ? s : s * ex2(u - next));
+        sum_unit[i] = next;
+      };
       bool go = true;
 #pragma unroll 1
-      for (int t = w.t0; t < w.t1; ++t, ++it) {
-        const int k = it & 1;
-        const unsigned half = static_cast<unsigned>(it >> 1) & 1u;
+      for (int t = w.t0; t < w.t1; t += 2, ++step) {
+        const int k = step & 1, tiles = min(2, w.t1 - t);
+        const unsigned half = static_cast<unsigned>(step >> 1) & 1u;
         ok = at_wait(&bar.mfull[k], half, fault) && ok;
         if (d < R) {
           const float top = top_s[k][d], next = fmaxf(unit, top);
           mix_s[k][d] = make_float2(unit == -kInf ? 0.f : ex2(unit - next), top == -kInf ? 0.f : ex2(top - next));
           unit = next;
         }
-        go = meet(5, ok);
+        go = meet(3, ok);
         if (!go) break;
-        if (leader) mbar_arrive(&bar.mempty[k]);
+        const PageScale ps0 = scale_s[it % kScaleRing][0], ps1 = scale_s[(it + tiles - 1) % kScaleRing][0];
+        it += tiles;
         ok = at_wait(&bar.ofull[k], half, fault);
         tc_fence_after();
 #pragma unroll
@@ -984,42 +1018,65 @@ __global__ void __launch_bounds__(Shape<R, NP>::kThreads, 1)
             }
           }
         }
+        if (q == 0) {
+          const float low = fminf(ps0.ve_low, ps1.ve_low);
+          const bool far = fmaxf(ps0.ve_high, ps1.ve_high) - low > static_cast<float>(kFar);
+          if (!far) {
+#pragma unroll 1
+            for (int r = 0; r < R; r += 16) {
+              float s[16];
+              tmem_ld16(tmem_l + k * R + r, s);
+              if (lane == 0) {
+#pragma unroll
+                for (int e = 0; e < 16; e += 4)
+                  *reinterpret_cast<float4*>(&sum_s[r + e]) = make_float4(s[e], s[e + 1], s[e + 2], s[e + 3]);
+              }
+            }
+            __syncwarp();
+          }
+#pragma unroll
+          for (int i = 0; i < kMine; ++i) {
+            const int r = min(lane + 32 * i, R - 1);
+            if (!far) {
+              add(i, sum_s[r], top_s[k][r] - low);
+            } else {
+              for (int v = 0; v < 4; ++v) add(i, far_s[k][v][r].x, far_s[k][v][r].y);
+            }
+          }
+        }
         tc_fence_before();
         __syncwarp();
-        if (leader) mbar_arrive(&bar.oempty[k]);
+        if (leader) {
+          mbar_arrive(&bar.oempty[k]);
+          mbar_arrive(&bar.mempty[k]);
+        }
       }
       if (!go) break;
-      ok = at_wait(&bar.efull[qb], piece_half, fault) && ok;
-      if (!meet(5, ok)) break;
       constexpr int kLd = NP * 128 + 4;
       float* part = P.parts + (static_cast<long long>(2 * blockIdx.x) + max(w.part, 0)) * R * kLd;
-      if (d < R) {
-        float s = (sum_s[qb][0][0][d] + sum_s[qb][0][1][d]) + (sum_s[qb][0][2][d] + sum_s[qb][0][3][d]);
-        float su = sum_unit_s[qb][0][d];
-        if constexpr (S::kTurns == 2) {
-          const float s2 = (sum_s[qb][1][0][d] + sum_s[qb][1][1][d]) + (sum_s[qb][1][2][d] + sum_s[qb][1][3][d]);
-          const float su2 = sum_unit_s[qb][1][d], next = fmaxf(su, su2);
-          s = (su == -kInf ? s : s * ex2(su - next)) + (su2 == -kInf ? s2 : s2 * ex2(su2 - next));
-          su = next;
-        }
-        if (w.part < 0) {
-          const int tok = (row0 + d) / P.G, g = row0 + d - tok * P.G;
-          row_s[d] = s == 0.f ? 0.f : ex2(unit - su) / s;
-          place_s[d] = tok >= P.n ? -1 : w.b * P.out_ld[0] + tok * P.out_ld[1] + (w.h * P.G + g) * P.out_ld[2];
-          if (tok >= w.count) row_s[d] = 0.f;
-        } else {
-          float* e = part + d * kLd + NP * 128;
-          __stcg(e, unit);
-          __stcg(e + 1, s);
-          __stcg(e + 2, su);
-        }
-      }
-      meet(5, true);
-      if (leader) {
-        mbar_arrive(&bar.qempty[qb]);
-        mbar_arrive(&bar.eempty[qb]);
-      }
+      if (d < R) row_s[d] = unit;
+      if (!meet(3, ok)) break;
+      if (leader) mbar_arrive(&bar.qempty[qb]);
       ++qn;
+      if (q == 0) {
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+          const int r = lane + 32 * i;
+          if (r >= R) break;
+          const float s = sum[i], u = row_s[r];
+          if (w.part < 0) {
+            const int tok = (row0 + r) / P.G, g = row0 + r - tok * P.G;
+            place_s[r] = tok >= P.n ? -1 : w.b * P.out_ld[0] + tok * P.out_ld[1] + (w.h * P.G + g) * P.out_ld[2];
+            row_s[r] = s == 0.f || tok >= w.count ? 0.f : ex2(u - sum_unit[i]) / s;
+          } else {
+            float* e = part + r * kLd + NP * 128;
+            __stcg(e, u);
+            __stcg(e + 1, s);
+            __stcg(e + 2, sum_unit[i]);
+          }
+        }
+      }
+      meet(3, true);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const long long at = w.part < 0 ? place_s[r] : r * kLd;
@@ -1037,7 +1094,7 @@ __global__ void __launch_bounds__(Shape<R, NP>::kThreads, 1)
           }
         }
       }
-      meet(5, true);
+      meet(3, true);
     }
   }
 
@@ -1045,8 +1102,10 @@ __global__ void __launch_bounds__(Shape<R, NP>::kThreads, 1)
   if (*fault && tid == 0) {
     // copies still in flight land before the CTA exits: wait (bounded) for
     // the last phase of every stage that was issued
-    for (int k = max(0, issued_s - S::kStages); k < issued_s; ++k)
-      mbar_wait(&bar.full[k % S::kStages], static_cast<unsigned>(k / S::kStages) & 1u);
+    uint64_t* first = bar.kfull;  // (vfull behind it)
+    for (int k = 0; k < 2 * S::kStages + kPatchRing; ++k)
+      if (issued_s >> k & 1u)
+        mbar_wait(k < 2 * S::kStages ? first + k : &bar.landed[k - 2 * S::kStages], parity_s >> k & 1u);
     if (P.error_word) atomicOr(P.error_word, SPEC_ERR_INTERNAL);
     P.shared[blockIdx.x] = make_int4(0, 0, 0, 0);
   }
@@ -1091,7 +1150,8 @@ __global__ void __launch_bounds__(128) join_kernel(const AttendParams P) {
       const float* e = part(i);
       const float u = __ldcg(e + NP * 128), su = __ldcg(e + NP * 128 + 2);
       const float f = u == -kInf ? 0.f : ex2(u - unit);
-      if (su != -kInf) sum += __ldcg(e + NP * 128 + 1) * ex2(su - sum_unit);
+      const float mine = __ldcg(e + NP * 128 + 1);
+      sum += su == -kInf ? mine : mine * ex2(su - sum_unit);
 #pragma unroll
       for (int p = 0; p < NP; ++p) acc[p] = __fmaf_rn(__ldcg(e + p * 128 + d), f, acc[p]);
     }
@@ -1117,7 +1177,8 @@ bool good_shape(int B, int n, int Hq, int H, int D) {
 
 int block_rows(int n, int G, int D) {
   const int rows = n * G;
-  return rows <= 16 ? 16 : rows <= 32 || D > 128 ? 32 : rows <= 48 ? 48 : 64;
+  // (of trees of more than 512 nodes the masks of 64 rows do not fit)
+  return rows <= 16 ? 16 : rows <= 32 || D > 128 || n > 512 ? 32 : rows <= 48 ? 48 : 64;
 }
 
 size_t attend_workspace(int n, int Hq, int H, int D) {
@@ -1148,7 +1209,8 @@ cudaError_t raise_smem() {
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lock(mu);
   if (done.count(dev)) return cudaSuccess;
-  e = cudaFuncSetAttribute(attend_kernel<R, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<R, NP>::kSmem);
+  e = cudaFuncSetAttribute(attend_kernel<R, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Shape<R, NP>::kSmem + kMaskBytes);
   if (e == cudaSuccess) done[dev] = true;
   return e;
 }
@@ -1172,7 +1234,9 @@ spec_status launch_attend(const spec_attend_args& a, AttendParams& p, cudaStream
   if (raise_smem<R, NP>() != cudaSuccess) return SPEC_ECUDA;
   p.more_bytes = g_more_bytes.load();
   const int ctas = std::min(nsm, kMaxCtas);
-  attend_kernel<R, NP><<<ctas, Shape<R, NP>::kThreads, Shape<R, NP>::kSmem, s>>>(tk, tv, p);
+  const int smem = Shape<R, NP>::kSmem + (p.parent ? a.n * static_cast<int>(2 * sizeof(typename Shape<R, NP>::Mask) + 2) : 0);
+  if (smem > Shape<R, NP>::kSmem + kMaskBytes) return SPEC_EINVAL;  // (block_rows sees to it)
+  attend_kernel<R, NP><<<ctas, kThreads, smem, s>>>(tk, tv, p);
   if (cudaGetLastError() != cudaSuccess) return SPEC_ECUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>((std::min(R, a.n * p.G) + 3) / 4));
