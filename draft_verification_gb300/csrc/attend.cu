@@ -47,32 +47,46 @@
 namespace sv {
 namespace {
 
-constexpr int kTile = 128;      // tokens per tile; two tiles make a step
+constexpr int kTile = 128;      // tokens per tile; one or two tiles make a step
 constexpr int kPanel = 16384;   // bytes of 128 tokens x 128 elements
 constexpr int kMaxRows = 1024;  // n
-constexpr int kMaxCtas = 160;
+constexpr int kMaxCtas = 320;
 constexpr int kThreads = 512;
 constexpr int kMaskBytes = 10 * kMaxRows;  // of shared memory for a tree's masks, at most
-constexpr int kScaleRing = 16, kPatchRing = 8, kPieceRing = 4;
+constexpr int kScaleRing = 32, kPatchRing = 8, kPieceRing = 4;
 constexpr int kFar = 9;    // value exponents of a step that lie further apart than this: 2^-9 is the least e4m3 code
-constexpr int kAhead = 2;  // tiles that K is copied ahead of V, as its products are ahead
 
 // R: a block's rows; NP: panels of 128 elements of a head.
 template <int R, int NP>
 struct Shape {
+  static constexpr int kCtas = NP == 1 && R <= 24 ? 2 : 1;  // per SM
+  static constexpr int kSubs = NP == 1 && R == 32 ? 2 : 1;  // tiles of a step
+  // An operand from shared memory costs its bytes (a product of 128 x 32 with 32
+  // rows some 60 cycles, with 64 hardly more), so K and V are taken once for hi
+  // and lo: as rows of their own, whose results are added later.  Where tensor
+  // memory is short (64 rows) the outputs' hi and lo are two products instead.
+  static constexpr bool kStacked = R <= 48;    // the outputs' hi and lo
+  static constexpr bool kStackedL = R <= 32;   // the sums' hi and lo
   // places of K tiles, and as many of V tiles (each with barriers of its own: a
   // warp has to meet all phases of a barrier that it waits on)
-  static constexpr int kStages = NP == 2 ? 2 : R == 16 ? 5 : R == 32 ? 4 : 3;
+  static constexpr int kStages = NP == 2 || kCtas == 2 ? 2 : 4;
   static constexpr int kSlot = NP * kPanel;
-  static constexpr int kPRow = R == 48 ? 64 : R;  // bytes of a token's weights
-  static constexpr int kPHalf = 2 * kTile * kPRow;  // hi or lo of a step's weights
-  static constexpr int kQHalf = NP * R * 128;       // hi or lo of a block's queries
-  static constexpr int kScores = R > 32 ? 2 : 4;    // places of steps' scores
-  static constexpr int kOnes = 1024;                // a tile's factors of the sums of weights (one row of 128 bytes)
-  static constexpr int kSmem = 1024 + 2 * kStages * kSlot + 4 * kQHalf + 4 * kPHalf + 4 * kOnes;
-  static constexpr int kCols = (2 * kScores + 2 * NP + 2) * R;
+  // a token's weights: hi's rows, then lo's, in one row of bytes, or in two planes
+  static constexpr int kPRow = !kStacked ? R : R == 48 ? 128 : R == 24 ? 64 : 2 * R;
+  static constexpr int kPPlane = kTile * kPRow;
+  static constexpr int kPTile = kPPlane * (kStacked ? 1 : 2);  // a tile's weights
+  static constexpr int kQBytes = NP * 2 * R * 128;  // a block's queries: of each panel hi's rows, then lo's
+  static constexpr int kScores = R <= 16 && NP == 1 ? 4 : 2;  // places of steps' scores
+  static constexpr int kCut = R == 48 ? 24 : R < 32 ? R : 32;  // rows that the softmax warps take at a time
+  static constexpr int kOnes = 1024;  // a tile's factors of the sums of weights (one row of 128 bytes)
+  static constexpr int kSmem = 1024 + 2 * kStages * kSlot + 2 * kQBytes + 2 * kSubs * (kPTile + kOnes);
+  static constexpr int kLBufs = R == 24 && kCtas == 2 ? 1 : 2;  // places of the sums
+  // (a product of bytes whose rows lie along the other axis takes 16 of them at a time)
+  static_assert(kStackedL ? 2 * R % 16 == 0 : R % 16 == 0, "the sums' products");
+  static constexpr int kSCols = 2 * R, kOCols = kStacked ? 2 * R : R, kLCols = kStackedL ? 2 * R : R;
+  static constexpr int kCols = kScores * kSubs * kSCols + 2 * NP * kOCols + kLBufs * kLCols;
   static constexpr uint32_t kTmemCols = kCols <= 256 ? 256 : 512;
-  static_assert(kCols <= 512 && kStages + kAhead + 6 <= kScaleRing && 2 * kStages + kPatchRing <= 32, "rings");
+  static_assert(kCols * kCtas <= 512 && (kScores + 4) * kSubs + kStages + 1 <= kScaleRing && 2 * kStages + kPatchRing <= 32, "rings");
   using Mask = typename std::conditional<(R > 32), unsigned long long, unsigned>::type;  // a bit per token of a block
 };
 
@@ -92,6 +106,7 @@ struct AttendParams {
   int* error_word;
   int4* shared;      // [ctas]: sequence, head, block and CTAs of the block that CTA begins and shares; 0 CTAs: none
   float* parts;      // [ctas][2][R][Dp + 4]: a part's sums, then log2 of their unit, its sum of weights and log2 of theirs
+  float2* far;       // [ctas][4][4][64]: of a step whose value exponents lie far apart, each warp's sums and units
   unsigned more_bytes;
 };
 
@@ -142,6 +157,16 @@ __device__ __forceinline__ int first_special(const Piece& w) {
 // device helpers
 // ---------------------------------------------------------------------------
 
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, unsigned parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Whole warps wait together (see int4_product.cu); a wait that gives up, here
 // or elsewhere in the CTA, ends the role.
 __device__ __forceinline__ bool at_wait(uint64_t* bar, unsigned parity, volatile int* fault) {
@@ -161,14 +186,15 @@ __device__ __forceinline__ bool one_lane() {
   return p != 0;
 }
 
-// The four warps of a warpgroup meet, and go on only if all of them can (so
-// that they leave a role together when a wait gave up).
+// The warps of a role, kCount threads, meet, and go on only if all of them can
+// (so that they leave the role together when a wait gave up).
+template <int kCount>
 __device__ __forceinline__ bool meet(int id, bool ok) {
   uint32_t all;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.and.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.and.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}"
       : "=r"(all)
-      : "r"(ok ? 1u : 0u), "r"(id)
+      : "r"(ok ? 1u : 0u), "r"(id), "n"(kCount)
       : "memory");
   return all != 0;
 }
@@ -182,6 +208,8 @@ __device__ __forceinline__ uint32_t operand_low(uint32_t addr, uint32_t stride) 
 __host__ __device__ constexpr uint32_t operand_high(uint32_t stride, int row) {
   return (stride >> 4) | 1u << 14 | (row == 128 ? 2u : row == 64 ? 4u : row == 32 ? 6u : 0u) << 29;
 }
+// A warp's common value, so that the compiler takes it for one.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 // byte offset `o` of a tile whose rows have `row` bytes, after the swizzle
 __device__ __forceinline__ uint32_t swizzled(uint32_t o, int row) {
   return o ^ ((o >> 3) & (row == 128 ? 0x70u : row == 64 ? 0x30u : row == 32 ? 0x10u : 0u));
@@ -237,20 +265,75 @@ __device__ __forceinline__ float column_sums(float* v, int lane) {
   return s;
 }
 
-// Two values as hi + lo, two e4m3 codes each.
-__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-  uint32_t h, back, rest;
-  unsigned short c, d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(b), "f"(a));
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c) : "r"(h));
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(c));
-  asm("sub.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(h), "r"(back));
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(d) : "r"(rest));
-  hi = c;
-  lo = d;
+// Four values as hi + lo, four e4m3 codes each.
+__device__ __forceinline__ void split4(float a, float b, float c, float d, uint32_t& hi, uint32_t& lo) {
+  asm("{\n .reg .b32 x, y, u, v;\n .reg .b16 p, q, r, s;\n"
+      " cvt.rn.f16x2.f32 x, %3, %2;\n cvt.rn.f16x2.f32 y, %5, %4;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 p, x;\n cvt.rn.satfinite.e4m3x2.f16x2 q, y;\n mov.b32 %0, {p, q};\n"
+      " cvt.rn.f16x2.e4m3x2 u, p;\n cvt.rn.f16x2.e4m3x2 v, q;\n sub.f16x2 x, x, u;\n sub.f16x2 y, y, v;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 r, x;\n cvt.rn.satfinite.e4m3x2.f16x2 s, y;\n mov.b32 %1, {r, s};\n}"
+      : "=r"(hi), "=r"(lo)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
 }
 
-__device__ __forceinline__ float4 lds_f4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+// Two float32 numbers in a register pair, each lane rounded as by itself (in
+// 64 bits throughout: as two floats the pairs cost moves at every operation).
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 pair(float a, float b) {
+  F2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float first_of(F2 x) { return __uint_as_float(static_cast<uint32_t>(x)); }
+__device__ __forceinline__ float second_of(F2 x) { return __uint_as_float(static_cast<uint32_t>(x >> 32)); }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ ulonglong2 lds_pairs(const void* p) { return *static_cast<const ulonglong2*>(p); }
+
+// Consecutive float32 columns of this warp's 32 lanes, in pairs.
+__device__ __forceinline__ void tmem_load8(uint32_t taddr, F2* v) {
+  asm volatile(
+      "{\n .reg .b32 a<8>;\n tcgen05.ld.sync.aligned.32x32b.x8.b32 {a0, a1, a2, a3, a4, a5, a6, a7}, [%4];\n"
+      " tcgen05.wait::ld.sync.aligned;\n"
+      " mov.b64 %0, {a0, a1};\n mov.b64 %1, {a2, a3};\n mov.b64 %2, {a4, a5};\n mov.b64 %3, {a6, a7};\n}"
+      : "=l"(v[0]), "=l"(v[1]), "=l"(v[2]), "=l"(v[3])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_load16(uint32_t taddr, F2* v) {
+  asm volatile(
+      "{\n .reg .b32 a<16>;\n"
+      " tcgen05.ld.sync.aligned.32x32b.x16.b32 {a0, a1, a2, a3, a4, a5, a6, a7, a8, a9, a10, a11, a12, a13, a14, a15}, "
+      "[%8];\n tcgen05.wait::ld.sync.aligned;\n"
+      " mov.b64 %0, {a0, a1};\n mov.b64 %1, {a2, a3};\n mov.b64 %2, {a4, a5};\n mov.b64 %3, {a6, a7};\n"
+      " mov.b64 %4, {a8, a9};\n mov.b64 %5, {a10, a11};\n mov.b64 %6, {a12, a13};\n mov.b64 %7, {a14, a15};\n}"
+      : "=l"(v[0]), "=l"(v[1]), "=l"(v[2]), "=l"(v[3]), "=l"(v[4]), "=l"(v[5]), "=l"(v[6]), "=l"(v[7])
+      : "r"(taddr)
+      : "memory");
+}
+// N columns, a multiple of 8
+template <int N>
+__device__ __forceinline__ void tmem_pairs(uint32_t taddr, F2* v) {
+  if constexpr (N >= 16) {
+    tmem_load16(taddr, v);
+    if constexpr (N > 16) tmem_pairs<N - 16>(taddr + 16, v + 8);
+  } else {
+    tmem_load8(taddr, v);
+  }
+}
 
 struct PageScale {
   float ck, ve;           // 2^key exponent (NaN: not a page), value exponent
@@ -269,10 +352,11 @@ struct Place {
 // the kernel
 // ---------------------------------------------------------------------------
 template <int R, int NP>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, Shape<R, NP>::kCtas)
     attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const AttendParams P) {
   using S = Shape<R, NP>;
+  constexpr int kCut = S::kCut;
   extern __shared__ __align__(1024) unsigned char at_dyn[];
   // kfull / kempty, vfull / vempty: a tile's K, V; sfull / sempty: a step's scores; pfull /
   // pempty: its weights in shared memory; ofull / oempty: its outputs; mfull /
@@ -288,13 +372,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Bars bar;
   __shared__ uint32_t tmem_s;
   __shared__ int fault_s;
-  __shared__ unsigned issued_s, parity_s;  // barriers that copies count on (kfull, vfull, landed), the last one's parity
+  __shared__ unsigned issued_s, parity_s;  // (see the copying warp)
   __shared__ __align__(16) Piece piece_s[kPieceRing];
   __shared__ __align__(16) PageScale scale_s[kScaleRing][8];
-  __shared__ int place_of_page_s[kScaleRing][8];  // rows of the pages' copies, -1: none
-  __shared__ bool special_s[kScaleRing];          // tiles that are patched
-  __shared__ __align__(16) float most_s[2][2][4][R], ref_s[8][R], cq_s[2][R], top_s[2][R], sum_s[R];
-  __shared__ __align__(16) float2 mix_s[2][R], far_s[2][4][R];
+  __shared__ int copies_s[kScaleRing][9];  // rows of the pages' copies, -1: none; a copy's bytes, negative: patched
+  __shared__ __align__(16) float most_s[2][2][4][kCut], ref_s[8][kCut], cq_s[2][R], top_s[2][R], sum_s[R];
+  __shared__ __align__(16) float keep_s[2][R], take_s[2][R];
   __shared__ __align__(16) float row_s[R];
   __shared__ long long place_s[R];
   __shared__ unsigned char token_s[2][R];
@@ -306,12 +389,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                           ~static_cast<uintptr_t>(1023));
   unsigned char* vring = kring + S::kStages * S::kSlot;
   unsigned char* qbuf = vring + S::kStages * S::kSlot;
-  unsigned char* pbuf = qbuf + 4 * S::kQHalf;
-  unsigned char* ones = pbuf + 4 * S::kPHalf;
+  unsigned char* pbuf = qbuf + 2 * S::kQBytes;
+  unsigned char* ones = pbuf + 2 * S::kSubs * S::kPTile;
   using Mask = typename S::Mask;
-  Mask* mask_s = reinterpret_cast<Mask*>(ones + 4 * S::kOnes);  // [2][n], with parents
+  Mask* mask_s = reinterpret_cast<Mask*>(ones + 2 * S::kSubs * S::kOnes);  // [2][n], with parents
   unsigned short* parent_s = reinterpret_cast<unsigned short*>(mask_s + 2 * P.n);
   volatile int* fault = &fault_s;
+  float2* far_sums = P.far + blockIdx.x * 1024;
 
   pdl_launch_dependents();
   if (tid < kBars) {
@@ -328,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (tid == 0) fault_s = 0, issued_s = parity_s = 0u;
   // (rows of the sums' factors that are not the first: of no use, but of defined values)
-  for (int i = tid; i < 4 * S::kOnes / 16; i += kThreads) reinterpret_cast<uint4*>(ones)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = tid; i < 2 * S::kSubs * S::kOnes / 16; i += kThreads) reinterpret_cast<uint4*>(ones)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async();
   if (warp == 1) {
     tmem_alloc(&tmem_s, S::kTmemCols);
@@ -337,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem_sc = tmem_s, tmem_o = tmem_s + 2 * S::kScores * R, tmem_l = tmem_o + 2 * NP * R;
+  const uint32_t tmem_sc = tmem_s, tmem_o = tmem_s + S::kScores * S::kSubs * S::kSCols, tmem_l = tmem_o + 2 * NP * S::kOCols;
 
   // the next piece, for all roles but the one that makes them
   int pieces = 0;
@@ -359,44 +443,51 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ---------------- pages ----------------
+    // (some 40 instructions per copy: more, and this warp would be what the others wait for)
     const int pp = kTile / P.page, slot_in = lane % pp, mine = lane / pp, batch = 32 / pp;
     const unsigned page_bytes = static_cast<unsigned>(P.page) * 128u;
     int it = 0;
     bool ok = true;
-    // K or V of a tile to its place, counted on a barrier that is number `on` among kfull, vfull and landed
-    const auto copy = [&](const CUtensorMap* map, int tile, unsigned char* to, uint64_t* empty, uint64_t* full, int on,
-                          unsigned on_parity) {
-      const Place<S::kStages> at(tile);
-      const int y = lane < pp ? place_of_page_s[tile % kScaleRing][lane] : -1;
-      const unsigned bytes =
-          static_cast<unsigned>(__popc(__ballot_sync(0xffffffffu, y >= 0))) * page_bytes * NP + P.more_bytes;
-      if (!at_wait(&empty[at.slot], at.parity ^ 1u, fault)) return false;
-      if (leader) {
-        mbar_expect_tx(full, bytes);
-        issued_s |= 1u << on;
-        parity_s = (parity_s & ~(1u << on)) | on_parity << on;
+    unsigned issued = 0, parities = 0;  // barriers that copies count on (kfull, vfull, landed), the last one's parity
+    const auto count_on = [&](uint64_t* full, int number, unsigned parity, unsigned bytes) {
+      if (leader) mbar_expect_tx(full, bytes);
+      issued |= 1u << number;
+      parities = (parities & ~(1u << number)) | parity << number;
+    };
+    int kslot = 0, vslot = 0, vt = 0, patches = 0;  // the places of the next tiles, the next tile of V
+    unsigned kparity = 0, vparity = 0;
+    const auto v_free = [&] { return vt < it && __all_sync(0xffffffffu, mbar_test(&bar.vempty[vslot], vparity ^ 1u)); };
+    const auto copy_v = [&] {
+      const int x = copies_s[vt % kScaleRing][lane < 9 ? lane : 8];  // rows of the pages' copies, bytes and a flag
+      const unsigned y = static_cast<unsigned>(__shfl_sync(0xffffffffu, x, 8));
+      const unsigned bytes = y & 0x7fffffffu;
+      uint64_t* full = &bar.vfull[vslot];
+      if (y >> 31) {  // a tile that is patched
+        full = &bar.landed[patches % kPatchRing];
+        count_on(full, 2 * S::kStages + patches % kPatchRing, static_cast<unsigned>(patches / kPatchRing) & 1u, bytes);
+        ++patches;
+      } else {
+        count_on(full, S::kStages + vslot, vparity, bytes);
       }
-      __syncwarp();
-      if (y >= 0) {
+      if (lane < pp && x >= 0) {
 #pragma unroll
         for (int p = 0; p < NP; ++p)
-          tma_load_2d(to + at.slot * S::kSlot + lane * page_bytes + p * kPanel, map, p * 128, y, full);
+          tma_load_2d(vring + vslot * S::kSlot + lane * page_bytes + p * kPanel, &tm_v, p * 128, x, full);
       }
       __syncwarp();
-      return true;
+      ++vt;
+      if (++vslot == S::kStages) vslot = 0, vparity ^= 1u;
     };
-    int patches = 0;
-    const auto copy_k = [&](int tile) {
-      const Place<S::kStages> at(tile);
-      return copy(&tm_k, tile, kring, bar.kempty, &bar.kfull[at.slot], at.slot, at.parity);
-    };
-    const auto copy_v = [&](int tile) {
-      if (special_s[tile % kScaleRing]) {
-        const Place<kPatchRing> at(patches++);
-        return copy(&tm_v, tile, vring, bar.vempty, &bar.landed[at.slot], 2 * S::kStages + at.slot, at.parity);
+    // Waits for a barrier; V's copies go on meanwhile.
+    const auto wait_for = [&](uint64_t* on, unsigned parity) {
+#pragma unroll 1
+      for (int polls = 0; polls < 8 * kMaxPolls; ++polls) {
+        if (v_free()) copy_v();
+        if (__all_sync(0xffffffffu, mbar_test(on, parity))) return true;
+        if ((polls & 15) == 15 && __any_sync(0xffffffffu, *fault)) return false;
       }
-      const Place<S::kStages> at(tile);
-      return copy(&tm_v, tile, vring, bar.vempty, &bar.vfull[at.slot], S::kStages + at.slot, at.parity);
+      *fault = 1;
+      return false;
     };
     Piece w;
     while (ok && next_piece(w)) {
@@ -429,57 +520,75 @@ __global__ void __launch_bounds__(kThreads, 1)
         x.ve = static_cast<float>(ve);
         x.ve_low = static_cast<float>(lo);
         x.ve_high = static_cast<float>(hi);
-        const int y = static_cast<int>(slab * P.page);
+        const int y = has ? static_cast<int>(slab * P.page) : -1;
+        // the bytes of this lane's tile's K, or V, and whether it is patched
+        const unsigned all = __ballot_sync(0xffffffffu, has);
+        const unsigned bytes =
+            static_cast<unsigned>(__popc(all >> (mine * pp) & ((1u << pp) - 1u))) * page_bytes * NP + P.more_bytes;
+        const int flags = static_cast<int>(bytes | (tb + mine >= special ? 0x80000000u : 0u));
 #pragma unroll 1
-        for (int i = 0; i < batch && tb + i < w.t1; ++i, ++it) {
+        for (int i = 0; i < batch && tb + i < w.t1; ++i) {
           if (mine == i) {
-            scale_s[it % kScaleRing][slot_in] = x;
-            place_of_page_s[it % kScaleRing][slot_in] = has ? y : -1;
+            const int at = it % kScaleRing;
+            scale_s[at][slot_in] = x;
+            copies_s[at][slot_in] = y;
+            if (slot_in == 0) copies_s[at][8] = flags;
           }
-          if (leader) special_s[it % kScaleRing] = tb + i >= special;
           __syncwarp();
-          ok = copy_k(it) && (tb + i - w.t0 < kAhead || copy_v(it - kAhead));
+          const unsigned k_bytes = __shfl_sync(0xffffffffu, bytes, i * pp);
+          ok = wait_for(&bar.kempty[kslot], kparity ^ 1u);
           if (!ok) break;
+          count_on(&bar.kfull[kslot], kslot, kparity, k_bytes);
+          if (mine == i && has) {
+#pragma unroll
+            for (int p = 0; p < NP; ++p)
+              tma_load_2d(kring + kslot * S::kSlot + slot_in * page_bytes + p * kPanel, &tm_k, p * 128, y,
+                          &bar.kfull[kslot]);
+          }
+          __syncwarp();
+          ++it;
+          if (++kslot == S::kStages) kslot = 0, kparity ^= 1u;
         }
       }
-      // (V's last ones wait for no other piece, whose queries may wait for this one's end)
-      const int n = w.t1 - w.t0;
-#pragma unroll 1
-      for (int j = max(0, n - kAhead); ok && j < n; ++j) ok = copy_v(it - n + j);
+      // the next record, which may come only when this piece is done
+      ok = ok && wait_for(&bar.rfull[pieces % kPieceRing], static_cast<unsigned>(pieces / kPieceRing) & 1u);
     }
+    while (ok && vt < it) {
+      ok = at_wait(&bar.vempty[vslot], vparity ^ 1u, fault);
+      if (ok) copy_v();
+    }
+    if (leader) issued_s = issued, parity_s = parities;
   } else if (warp == 1) {
     // ---------------- scores ----------------
-    constexpr uint32_t idesc = idesc_e4m3(kTile, R, 0, 0), high = operand_high(1024, 128);
+    constexpr uint32_t idesc = idesc_e4m3(kTile, 2 * R, 0, 0), high = operand_high(1024, 128);
     const int steps = (P.D + 31) / 32;
     const uint32_t issues = leader ? 1u : 0u;
     int it = 0, step = 0, qn = 0;
     bool ok = true;
     Piece w;
     while (ok && next_piece(w)) {
-      const uint32_t q_hi = operand_low(smem_addr(qbuf + 2 * (qn & 1) * S::kQHalf), 1024);
+      const uint32_t q = uniform(operand_low(smem_addr(qbuf + (qn & 1) * S::kQBytes), 1024));
       ok = at_wait(&bar.qfull[qn & 1], static_cast<unsigned>(qn >> 1) & 1u, fault);
       ++qn;
 #pragma unroll 1
       for (int t = w.t0; ok && t < w.t1; ++t, ++it) {
         // (a step's two tiles, the second one perhaps missing)
-        const int sb = step % S::kScores, sub = (t - w.t0) & 1;
+        const int sb = step % S::kScores, sub = S::kSubs == 2 ? (t - w.t0) & 1 : 0;
         const Place<S::kStages> at(it);
         if (sub == 0) ok = at_wait(&bar.sempty[sb], (static_cast<unsigned>(step / S::kScores) & 1u) ^ 1u, fault);
         ok = ok && at_wait(&bar.kfull[at.slot], at.parity, fault);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t a = operand_low(smem_addr(kring + at.slot * S::kSlot), 1024), d = tmem_sc + (2 * sb + sub) * R;
-        umma_e4m3(issues, d, a, high, q_hi, high, idesc, 0u);
+        const uint32_t a = uniform(operand_low(smem_addr(kring + at.slot * S::kSlot), 1024));
+        const uint32_t d = uniform(tmem_sc + (S::kSubs * sb + sub) * S::kSCols);
+        umma_e4m3(issues, d, a, high, q, high, idesc, 0u);
 #pragma unroll
-        for (int k = 1; k < 8 * NP; ++k) {  // hi's steps of 32 elements, then lo's
-          const int e = k % (4 * NP);
+        for (int e = 1; e < 4 * NP; ++e)  // steps of 32 elements
           if (e < steps)
             umma_e4m3(issues, d, a + (e >> 2) * (kPanel >> 4) + (e & 3) * 2, high,
-                            q_hi + k / (4 * NP) * (S::kQHalf >> 4) + (e >> 2) * (R * 128 >> 4) + (e & 3) * 2, high,
-                      idesc, 1u);
-        }
+                      q + (e >> 2) * (2 * R * 128 >> 4) + (e & 3) * 2, high, idesc, 1u);
         commit_if(issues, &bar.kempty[at.slot]);
-        if (sub == 1 || t + 1 == w.t1) {
+        if (sub == S::kSubs - 1 || t + 1 == w.t1) {
           commit_if(issues, &bar.sfull[sb]);
           if (leader) mbar_arrive(&bar.sfull[sb]);  // what the copies' and queries' warps wrote is visible behind it
           ++step;
@@ -601,11 +710,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the block's rows: two e4m3 numbers for each element
         constexpr int kLanes = 16 * NP;       // lanes of a row, 8 elements each
         constexpr int kAtOnce = 32 / kLanes;  // rows at a time
-        constexpr int kBatch = 8;
+        constexpr int kBatch = S::kCtas == 2 ? 4 : 8;
         const int qb = qn & 1, row0 = block * R, tok0 = row0 / P.G, d0 = lane % kLanes * 8;
         ok = at_wait(&bar.qempty[qb], (static_cast<unsigned>(qn >> 1) & 1u) ^ 1u, fault);
         if (!ok) break;
-        unsigned char* dst = qbuf + 2 * qb * S::kQHalf;
+        unsigned char* dst = qbuf + qb * S::kQBytes;
         const bf16_t* q = P.q + b * P.q_ld[0] + static_cast<long long>(h) * P.G * P.q_ld[2] + d0;
 #pragma unroll 1
         for (int r1 = 0; r1 < R; r1 += kBatch * kAtOnce) {
@@ -644,9 +753,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float2 back = unpack_e4m3(hi[e]);
               lo[e] = pack_e4m3(a - back.x, c - back.y);
             }
-            const uint32_t at = (d0 >> 7) * R * 128 + swizzled(r * 128 + (d0 & 127), 128);
+            const uint32_t at = (d0 >> 7) * 2 * R * 128 + swizzled(r * 128 + (d0 & 127), 128);
             *reinterpret_cast<uint2*>(dst + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-            *reinterpret_cast<uint2*>(dst + S::kQHalf + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+            *reinterpret_cast<uint2*>(dst + R * 128 + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
             if (d0 == 0) {
               cq_s[qb][r] = exp2i(eq) * P.c;
               token_s[qb][r] = static_cast<unsigned char>((row0 + r) / P.G - tok0);
@@ -701,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 3) {
     // ---------------- outputs' products ----------------
     // (and, before them, V of what no row sees, and NaN values among the drafted tokens)
-    constexpr uint32_t idesc = idesc_e4m3(128, R, 1, 1), idesc_l = idesc_e4m3(64, R, 0, 1);
+    constexpr uint32_t idesc = idesc_e4m3(128, S::kOCols, 1, 1), idesc_l = idesc_e4m3(64, S::kLCols, 0, 1);
     constexpr uint32_t a_high = operand_high(1024, 128), b_high = operand_high(8 * S::kPRow, S::kPRow);
     const uint32_t issues = leader ? 1u : 0u;
     int it = 0, step = 0, patches = 0;
@@ -711,12 +820,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int special = first_special(w);
 #pragma unroll 1
       for (int t = w.t0; ok && t < w.t1; ++t, ++it) {
-        const int k = step & 1, sub = (t - w.t0) & 1;
+        const int k = step & 1, sub = S::kSubs == 2 ? (t - w.t0) & 1 : 0;
         const unsigned half = static_cast<unsigned>(step >> 1) & 1u;
         if (sub == 0) {
           // (the weights of a step wait for its patches)
 #pragma unroll 1
-          for (int u = max(t, special); ok && u < min(t + 2, w.t1); ++u, ++patches) {
+          for (int u = max(t, special); ok && u < min(t + S::kSubs, w.t1); ++u, ++patches) {
             ok = at_wait(&bar.landed[patches % kPatchRing], static_cast<unsigned>(patches / kPatchRing) & 1u, fault);
             if (!ok) break;
             const Place<S::kStages> at(it + u - t);
@@ -759,28 +868,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = ok && at_wait(&bar.vfull[at.slot], at.parity, fault);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t b = operand_low(smem_addr(pbuf + 2 * k * S::kPHalf + sub * kTile * S::kPRow), 8 * S::kPRow);
-        const uint32_t a0 = operand_low(smem_addr(vring + at.slot * S::kSlot), 1024);
+        const uint32_t b = uniform(operand_low(smem_addr(pbuf + (S::kSubs * k + sub) * S::kPTile), 8 * S::kPRow));
+        const uint32_t a0 = uniform(operand_low(smem_addr(vring + at.slot * S::kSlot), 1024));
+        const uint32_t o0 = uniform(tmem_o + k * NP * S::kOCols), l = uniform(tmem_l + (S::kLBufs == 2 ? k : 0) * S::kLCols);
         const uint32_t first = sub == 0 ? 0u : 1u;
+        constexpr int kB = 32 * S::kPRow >> 4, kPlane = S::kPPlane >> 4;  // 32 tokens, lo's plane
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-          const uint32_t a = a0 + p * (kPanel >> 4), o = tmem_o + (k * NP + p) * R;
+          const uint32_t a = a0 + p * (kPanel >> 4), o = o0 + p * S::kOCols;
 #pragma unroll
-          for (int i = 0; i < 2 * kTile / 32; ++i)  // hi's 4 steps of 32 tokens, then lo's
-            umma_e4m3(issues, o, a + (i & 3) * (32 * 128 >> 4), a_high,
-                      b + (i >> 2) * (S::kPHalf >> 4) + (i & 3) * (32 * S::kPRow >> 4), b_high, idesc,
+          for (int i = 0; i < (S::kStacked ? 4 : 8); ++i)  // 4 steps of 32 tokens, hi's, then lo's
+            umma_e4m3(issues, o, a + (i & 3) * (32 * 128 >> 4), a_high, b + (i >> 2) * kPlane + (i & 3) * kB, b_high, idesc,
                       i == 0 ? first : 1u);
+        }
+        if (S::kLBufs == 1 && sub == 0 && step > 0) {
+          ok = at_wait(&bar.oempty[k ^ 1], static_cast<unsigned>((step - 1) >> 1) & 1u, fault);
+          if (!ok) break;
         }
         // the sums of the weights: products with one row of factors (every 8 rows of
         // the operand are the same, a stride of 0), the first of the 64 results is used
-        const uint32_t f = operand_low(smem_addr(ones + (2 * k + sub) * S::kOnes), 0);
+        const uint32_t f = uniform(operand_low(smem_addr(ones + (S::kSubs * k + sub) * S::kOnes), 0));
+        constexpr int kLo = S::kStacked ? R >> 4 : kPlane;  // from hi's weights to lo's
 #pragma unroll
-        for (int i = 0; i < 2 * kTile / 32; ++i)
-          umma_e4m3(issues, tmem_l + k * R, f + (i & 3) * 2, operand_high(0, 128),
-                    b + (i >> 2) * (S::kPHalf >> 4) + (i & 3) * (32 * S::kPRow >> 4), b_high, idesc_l,
+        for (int i = 0; i < (S::kStackedL ? 4 : 8); ++i)
+          umma_e4m3(issues, l, f + (i & 3) * 2, operand_high(0, 128), b + (i >> 2) * kLo + (i & 3) * kB, b_high, idesc_l,
                     i == 0 ? first : 1u);
         commit_if(issues, &bar.vempty[at.slot]);
-        if (sub == 1 || t + 1 == w.t1) {
+        if (sub == S::kSubs - 1 || t + 1 == w.t1) {
           commit_if(issues, &bar.ofull[k]);
           commit_if(issues, &bar.pempty[k]);
           ++step;
@@ -791,27 +905,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_wait(&bar.drain[1], 0);
   } else if (warp < 12) {
     // ---------------- weights ----------------
-    // Every other step, all rows of the block; a thread has a token of each of
-    // the step's tiles.  The scores are read twice, for the maxima and for the
-    // weights, 16 rows at a time: the same few instructions again and again
-    // (what these warps wait for most is instructions).
+    // Every other step, kCut of the block's rows at a time; a thread has a token
+    // of each of the step's tiles and keeps its scores in registers.
     const int turn = (warp - 4) >> 2, q = warp & 3, row = q * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
     const int page_row = row / P.page;
+    const int col = lane < kCut ? lane : 0;  // the row that this lane sees to
     float* refs = ref_s[warp - 4];
-    unsigned char* weights = pbuf + 2 * turn * S::kPHalf;
-    unsigned char* factors = ones + 2 * turn * S::kOnes + row;
+    unsigned char* weights = pbuf + S::kSubs * turn * S::kPTile;
     int it = 0, step = 0, qn = 0, patches = 0;
     bool ok = true;  // (what a wait of this warp's gave; the warpgroup goes by what its warps agree on)
     Piece w;
     while (true) {
       const bool got = next_piece(w);
-      if (!meet(1 + turn, got)) break;
+      if (!meet<128>(1 + turn, got)) break;
       const int special = first_special(w), qb = qn & 1, tok0 = w.block * R / P.G;
       bool go = true;
 #pragma unroll 1
-      for (int t = w.t0; t < w.t1; t += 2, ++step) {
-        const int tiles = min(2, w.t1 - t);
+      for (int t = w.t0; t < w.t1; t += S::kSubs, ++step) {
+        const int tiles = S::kSubs == 2 ? min(2, w.t1 - t) : 1;
         const int at = it, patch = patches;
         it += tiles;
         patches += max(0, min(tiles, t + tiles - special));
@@ -822,132 +934,139 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const PageScale ps0 = scale_s[at % kScaleRing][page_row], ps1 = scale_s[(at + tiles - 1) % kScaleRing][page_row];
         // what the rows see of this thread's tokens
+        using Mask = typename S::Mask;
+        const bool special_step = t + tiles > special;
         Mask seen0 = ~static_cast<Mask>(0), seen1 = seen0;
         bool nan0 = false, nan1 = false;
-        if (t + tiles > special) {
+        if (special_step) {
           const auto look = [&](int tile, int patch, Mask& seen, bool& nan) {
             if (tile < special) return;
             ok = at_wait(&bar.patched[patch % kPatchRing], static_cast<unsigned>(patch / kPatchRing) & 1u, fault) && ok;
             const int pos = tile * kTile + row, j = pos - w.prefix;
             if (pos >= w.keys) seen = 0;
             else if (j >= 0 && P.parent) seen = mask_s[qb * P.n + j];
-            else if (j > tok0) seen = j - tok0 >= static_cast<int>(8 * sizeof(Mask)) ? 0 : ~static_cast<Mask>(0) << (j - tok0);
+            else if (j > tok0) seen = j - tok0 >= static_cast<int>(8 * sizeof(Mask)) ? 0 : seen << (j - tok0);
             nan = nan_s[patch % kPatchRing][q] >> lane & 1u;
           };
           look(t, patch, seen0, nan0);
           if (tiles == 2) look(t + 1, patch + (t >= special ? 1 : 0), seen1, nan1);
         }
-        // 16 rows' scores, base 2, plus the value exponent
-        const auto scores = [&](int sub, int c, float* y) {
-          tmem_ld16(tmem_sc + (2 * sb + sub) * R + c + lanes, y);
-          const float ck = sub ? ps1.ck : ps0.ck, ve = sub ? ps1.ve : ps0.ve;
-          const float2 ck2 = make_float2(ck, ck), ve2 = make_float2(ve, ve);
-#pragma unroll
-          for (int r = 0; r < 16; r += 4) {
-            const float4 f = lds_f4(&cq_s[qb][c + r]);
-            const float2 a = ffma2(fmul2(make_float2(y[r], y[r + 1]), make_float2(f.x, f.y)), ck2, ve2);
-            const float2 b = ffma2(fmul2(make_float2(y[r + 2], y[r + 3]), make_float2(f.z, f.w)), ck2, ve2);
-            y[r] = a.x, y[r + 1] = a.y, y[r + 2] = b.x, y[r + 3] = b.y;
-          }
-          if (t + sub >= special) {
-            const Mask seen = sub ? seen1 : seen0;
-            const bool nan = sub ? nan1 : nan0;
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-              if (nan) y[r] = __uint_as_float(0x7fc00000u);
-              if (!(seen >> token_s[qb][c + r] & 1)) y[r] = -kInf;
-            }
-          }
-        };
-        // the rows' largest
-        const int slot = step >> 1 & 1;
-#pragma unroll 1
-        for (int c = 0; c < R; c += 16) {
-          float top[16];
-          scores(0, c, top);
-          if (tiles == 2) {
-            float y[16];
-            scores(1, c, y);
-#pragma unroll
-            for (int r = 0; r < 16; ++r) top[r] = fmaxf(top[r], y[r]);
-          }
-#pragma unroll
-          for (int r = 0; r < 16; r += 4) {
-            const float4 m =
-                make_float4(warp_max(top[r]), warp_max(top[r + 1]), warp_max(top[r + 2]), warp_max(top[r + 3]));
-            if (leader) *reinterpret_cast<float4*>(&most_s[turn][slot][q][c + r]) = m;
-          }
-        }
-        go = meet(1 + turn, ok);
-        if (!go) break;
-        // every warp for itself: a lane per row
-        if (q == 0) ok = at_wait(&bar.mempty[turn], half ^ 1u, fault);
-#pragma unroll
-        for (int c = lane; c < R; c += 32) {
-          const float m = fmaxf(fmaxf(most_s[turn][slot][0][c], most_s[turn][slot][1][c]),
-                                fmaxf(most_s[turn][slot][2][c], most_s[turn][slot][3][c]));
-          refs[c] = m == -kInf ? 0.f : m - 8.f;
-          if (q == 0) top_s[turn][c] = m - 8.f;
-        }
-        ok = at_wait(&bar.pempty[turn], half ^ 1u, fault) && ok;
         const float low = fminf(ps0.ve_low, ps1.ve_low);
-        if (fmaxf(ps0.ve_high, ps1.ve_high) - low > static_cast<float>(kFar)) {
-          // The values' exponents lie too far apart for the factors: the sums of
-          // the weights 2^x themselves, each warp's with its own largest as unit
+        const bool far = fmaxf(ps0.ve_high, ps1.ve_high) - low > static_cast<float>(kFar);
 #pragma unroll 1
-          for (int c = 0; c < R; c += 16) {
-            float x[16], x1[16];
-            scores(0, c, x);
+        for (int c = 0; c < R; c += kCut) {
+          // scores, base 2, plus the value exponent, of rows c on
+          F2 y0[kCut / 2], y1[kCut / 2];
+          const auto scores = [&](int sub, const PageScale& ps, F2* y) {
+            const uint32_t from = tmem_sc + (S::kSubs * sb + sub) * S::kSCols + c + lanes;
+            const F2 ck = pair(ps.ck, ps.ck), ve = pair(ps.ve, ps.ve);
+            tmem_pairs<kCut>(from, y);
 #pragma unroll
-            for (int r = 0; r < 16; ++r) x[r] -= ps0.ve, x1[r] = -kInf;
-            if (tiles == 2) {
-              scores(1, c, x1);
-#pragma unroll
-              for (int r = 0; r < 16; ++r) x1[r] -= ps1.ve;
+            for (int i = 0; i < kCut / 2; i += 4) {  // hi's and lo's
+              F2 lo[4];
+              tmem_load8(from + R + 2 * i, lo);
+              const ulonglong2 f = lds_pairs(&cq_s[qb][c + 2 * i]), g = lds_pairs(&cq_s[qb][c + 2 * i + 4]);
+              y[i] = fma2(mul2(add2(y[i], lo[0]), f.x), ck, ve);
+              y[i + 1] = fma2(mul2(add2(y[i + 1], lo[1]), f.y), ck, ve);
+              y[i + 2] = fma2(mul2(add2(y[i + 2], lo[2]), g.x), ck, ve);
+              y[i + 3] = fma2(mul2(add2(y[i + 3], lo[3]), g.y), ck, ve);
             }
-            float unit = -kInf;
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-              const float m = warp_max(fmaxf(x[r], x1[r])), ref = m == -kInf ? 0.f : m;
-              x[r] = ex2(x[r] - ref) + ex2(x1[r] - ref);
-              if ((lane & 15) == r) unit = m;
-            }
-            const float sum = column_sums<16>(x, lane);
-            if (lane < 16) far_s[turn][q][c + lane] = make_float2(sum, unit);
-          }
-        } else {
-          const auto code = [&](float ve) {  // of 2^(low - ve), in [2^-9, 1]
-            const int e = static_cast<int>(low - ve);
-            return static_cast<unsigned char>(e >= -6 ? (e + 7) << 3 : 1 << (e + 9));
           };
-          factors[0] = code(ps0.ve);
-          factors[S::kOnes] = code(ps1.ve);
-        }
-        __syncwarp();
-        if (q == 0 && leader) mbar_arrive(&bar.mfull[turn]);
-#pragma unroll 1
-        for (int sub = 0; sub < tiles; ++sub) {
-#pragma unroll 1
-          for (int c = 0; c < R; c += 16) {
-            float y[16];
-            scores(sub, c, y);
+          scores(0, ps0, y0);
+          if (tiles == 2) {
+            scores(1, ps1, y1);
+          } else {
 #pragma unroll
-            for (int r = 0; r < 16; r += 4) {
-              const float4 f = lds_f4(refs + c + r);
-              const float2 a = fadd2(make_float2(y[r], y[r + 1]), make_float2(-f.x, -f.y));
-              const float2 b = fadd2(make_float2(y[r + 2], y[r + 3]), make_float2(-f.z, -f.w));
-              y[r] = ex2(a.x), y[r + 1] = ex2(a.y), y[r + 2] = ex2(b.x), y[r + 3] = ex2(b.y);
-            }
-            uint32_t hi[8], lo[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) split2(y[2 * i], y[2 * i + 1], hi[i], lo[i]);
-            unsigned char* p = weights + swizzled((sub * kTile + row) * S::kPRow + c, S::kPRow);
-            *reinterpret_cast<uint4*>(p) =
-                make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, hi[4] | hi[5] << 16, hi[6] | hi[7] << 16);
-            *reinterpret_cast<uint4*>(p + S::kPHalf) =
-                make_uint4(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16, lo[4] | lo[5] << 16, lo[6] | lo[7] << 16);
+            for (int i = 0; i < kCut / 2; ++i) y1[i] = pair(-kInf, -kInf);
           }
+          if (special_step) {
+            const auto cover = [&](F2* y, Mask seen, bool nan) {
+              const float none = -kInf, lost = __uint_as_float(0x7fc00000u);
+#pragma unroll
+              for (int i = 0; i < kCut / 2; ++i) {
+                const bool see0 = seen >> token_s[qb][c + 2 * i] & 1, see1 = seen >> token_s[qb][c + 2 * i + 1] & 1;
+                y[i] = pair(!see0 ? none : nan ? lost : first_of(y[i]), !see1 ? none : nan ? lost : second_of(y[i]));
+              }
+            };
+            cover(y0, seen0, nan0);
+            if (tiles == 2) cover(y1, seen1, nan1);
+          }
+          // the rows' largest (stored by all lanes: a branch costs the warp more)
+          const int slot = S::kCut == R ? step >> 1 & 1 : c == 0 ? 0 : 1;
+          const auto top = [&](int i) {
+            return make_float2(warp_max(fmaxf(first_of(y0[i]), first_of(y1[i]))),
+                               warp_max(fmaxf(second_of(y0[i]), second_of(y1[i]))));
+          };
+#pragma unroll
+          for (int i = 0; i < kCut / 2; i += 2) {
+            const float2 a = top(i), b = top(i + 1);
+            *reinterpret_cast<float4*>(&most_s[turn][slot][q][2 * i]) = make_float4(a.x, a.y, b.x, b.y);
+          }
+          go = meet<128>(1 + turn, ok);
+          if (!go) break;
+          // every warp for itself: a lane per row
+          const float m = fmaxf(fmaxf(most_s[turn][slot][0][col], most_s[turn][slot][1][col]),
+                                fmaxf(most_s[turn][slot][2][col], most_s[turn][slot][3][col]));
+          refs[col] = m == -kInf ? 0.f : 8.f - m;  // (negated)
+          __syncwarp();
+          if (q == 0) {
+            if (c == 0) ok = at_wait(&bar.mempty[turn], half ^ 1u, fault);
+            top_s[turn][c + col] = m - 8.f;
+            __syncwarp();
+            if (leader && c + kCut == R) mbar_arrive(&bar.mfull[turn]);
+          }
+          if (far) {
+            // The values' exponents lie too far apart for the factors: the sums of
+            // the weights 2^x themselves, each warp's with its own largest as unit
+#pragma unroll
+            for (int r = 0; r < kCut; ++r) {
+              const float x0 = (r & 1 ? second_of(y0[r / 2]) : first_of(y0[r / 2])) - ps0.ve;
+              const float x1 = (r & 1 ? second_of(y1[r / 2]) : first_of(y1[r / 2])) - ps1.ve;
+              const float unit = warp_max(fmaxf(x0, x1)), ref = unit == -kInf ? 0.f : unit;
+              float sum = ex2(x0 - ref) + ex2(x1 - ref);
+#pragma unroll
+              for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+              if (lane == 0) __stcg(far_sums + (4 * (step & 3) + q) * 64 + c + r, make_float2(sum, unit));
+            }
+          }
+          if (c == 0) {
+            ok = at_wait(&bar.pempty[turn], half ^ 1u, fault) && ok;
+            const auto code = [&](float ve) {  // of 2^(low - ve), in [2^-9, 1]
+              const int e = static_cast<int>(low - ve);
+              return static_cast<unsigned char>(e >= -6 ? (e + 7) << 3 : 1 << (e + 9));
+            };
+            if (!far) {
+              ones[S::kSubs * turn * S::kOnes + row] = code(ps0.ve);
+              if (S::kSubs == 2) ones[(S::kSubs * turn + 1) * S::kOnes + row] = code(ps1.ve);
+            }
+          }
+          const auto store = [&](int sub, const F2* y) {
+            uint32_t hi[kCut / 4], lo[kCut / 4];
+#pragma unroll
+            for (int i = 0; i < kCut / 2; i += 2) {
+              const ulonglong2 f = lds_pairs(refs + 2 * i);
+              const F2 a = add2(y[i], f.x), b = add2(y[i + 1], f.y);
+              split4(ex2(first_of(a)), ex2(second_of(a)), ex2(first_of(b)), ex2(second_of(b)), hi[i / 2], lo[i / 2]);
+            }
+            const auto put = [&](int at, const uint32_t* x) {
+              unsigned char* p = weights + sub * S::kPTile;
+              if constexpr (kCut % 16 == 0) {
+#pragma unroll
+                for (int i = 0; i < kCut / 4; i += 4)
+                  *reinterpret_cast<uint4*>(p + swizzled(at + 4 * i, S::kPRow)) = make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+              } else {
+#pragma unroll
+                for (int i = 0; i < kCut / 4; i += 2)
+                  *reinterpret_cast<uint2*>(p + swizzled(at + 4 * i, S::kPRow)) = make_uint2(x[i], x[i + 1]);
+              }
+            };
+            put(row * S::kPRow + c, hi);
+            put(row * S::kPRow + c + (S::kStacked ? R : S::kPPlane), lo);
+          };
+          store(0, y0);
+          if (tiles == 2) store(1, y1);
         }
+        if (!go) break;
         tc_fence_before();
         fence_proxy_async();
         __syncwarp();
@@ -968,16 +1087,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     Piece w;
     while (true) {
       const bool got = next_piece(w);
-      if (!meet(3, got)) break;
+      if (!meet<128>(3, got)) break;
       const int row0 = w.block * R, qb = qn & 1;
-      float2 acc[NP][R / 2];
+      F2 acc[NP][R / 2];
 #pragma unroll
       for (int p = 0; p < NP; ++p)
 #pragma unroll
-        for (int r = 0; r < R / 2; ++r) acc[p][r] = make_float2(0.f, 0.f);
+        for (int r = 0; r < R / 2; ++r) acc[p][r] = 0;
       float unit = -kInf;  // log2 of the outputs' unit, of row d
       // of rows `lane` and `lane` + 32 (warp 0): the sum of weights, log2 of its unit
-      constexpr int kMine = (R + 31) / 32;
+      constexpr int kMine = (R + 31) / 32, kSome = R % 16 ? 8 : 16;
       float sum[kMine], sum_unit[kMine];
 #pragma unroll
       for (int i = 0; i < kMine; ++i) sum[i] = 0.f, sum_unit[i] = -kInf;
@@ -988,17 +1107,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       bool go = true;
 #pragma unroll 1
-      for (int t = w.t0; t < w.t1; t += 2, ++step) {
-        const int k = step & 1, tiles = min(2, w.t1 - t);
+      for (int t = w.t0; t < w.t1; t += S::kSubs, ++step) {
+        const int k = step & 1, tiles = S::kSubs == 2 ? min(2, w.t1 - t) : 1;
         const unsigned half = static_cast<unsigned>(step >> 1) & 1u;
         ok = at_wait(&bar.mfull[k], half, fault) && ok;
         if (d < R) {
           const float top = top_s[k][d], next = fmaxf(unit, top);
-          mix_s[k][d] = make_float2(unit == -kInf ? 0.f : ex2(unit - next), top == -kInf ? 0.f : ex2(top - next));
+          keep_s[k][d] = unit == -kInf ? 0.f : ex2(unit - next);
+          take_s[k][d] = top == -kInf ? 0.f : ex2(top - next);
           unit = next;
         }
-        go = meet(3, ok);
+        float tops[kMine];  // of warp 0's rows
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) tops[i] = q == 0 ? top_s[k][min(lane + 32 * i, R - 1)] : 0.f;
+        go = meet<128>(3, ok);
         if (!go) break;
+        if (leader) mbar_arrive(&bar.mempty[k]);
         const PageScale ps0 = scale_s[it % kScaleRing][0], ps1 = scale_s[(it + tiles - 1) % kScaleRing][0];
         it += tiles;
         ok = at_wait(&bar.ofull[k], half, fault);
@@ -1007,14 +1131,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int p = 0; p < NP; ++p) {
           if (p * 128 + q * 32 >= P.D) break;
 #pragma unroll
-          for (int r = 0; r < R; r += 16) {
-            float o[16];
-            tmem_ld16(tmem_o + (k * NP + p) * R + r + lanes, o);
+          for (int r = 0; r < R; r += kSome) {
+            F2 o[kSome / 2];
+            tmem_pairs<kSome>(tmem_o + (k * NP + p) * S::kOCols + r + lanes, o);
+            if constexpr (S::kStacked) {
+              F2 lo[kSome / 2];
+              tmem_pairs<kSome>(tmem_o + (k * NP + p) * S::kOCols + R + r + lanes, lo);
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              const float4 m = *reinterpret_cast<const float4*>(&mix_s[k][r + e]);
-              float2& x = acc[p][(r + e) / 2];
-              x = ffma2(make_float2(o[e], o[e + 1]), make_float2(m.y, m.w), fmul2(x, make_float2(m.x, m.z)));
+              for (int i = 0; i < kSome / 2; ++i) o[i] = add2(o[i], lo[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < kSome / 2; i += 2) {
+              const ulonglong2 old = lds_pairs(&keep_s[k][r + 2 * i]), fresh = lds_pairs(&take_s[k][r + 2 * i]);
+              acc[p][r / 2 + i] = fma2(o[i], fresh.x, mul2(acc[p][r / 2 + i], old.x));
+              acc[p][r / 2 + i + 1] = fma2(o[i + 1], fresh.y, mul2(acc[p][r / 2 + i + 1], old.y));
             }
           }
         }
@@ -1023,13 +1153,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool far = fmaxf(ps0.ve_high, ps1.ve_high) - low > static_cast<float>(kFar);
           if (!far) {
 #pragma unroll 1
-            for (int r = 0; r < R; r += 16) {
-              float s[16];
-              tmem_ld16(tmem_l + k * R + r, s);
+            for (int r = 0; r < R; r += kSome) {
+              F2 s[kSome / 2];
+              tmem_pairs<kSome>(tmem_l + (S::kLBufs == 2 ? k : 0) * S::kLCols + r, s);
+              if constexpr (S::kStackedL) {
+                F2 lo[kSome / 2];
+                tmem_pairs<kSome>(tmem_l + (S::kLBufs == 2 ? k : 0) * S::kLCols + R + r, lo);
+#pragma unroll
+                for (int e = 0; e < kSome / 2; ++e) s[e] = add2(s[e], lo[e]);
+              }
               if (lane == 0) {
 #pragma unroll
-                for (int e = 0; e < 16; e += 4)
-                  *reinterpret_cast<float4*>(&sum_s[r + e]) = make_float4(s[e], s[e + 1], s[e + 2], s[e + 3]);
+                for (int e = 0; e < kSome / 2; e += 2)
+                  *reinterpret_cast<ulonglong2*>(&sum_s[r + 2 * e]) = make_ulonglong2(s[e], s[e + 1]);
               }
             }
             __syncwarp();
@@ -1038,24 +1174,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < kMine; ++i) {
             const int r = min(lane + 32 * i, R - 1);
             if (!far) {
-              add(i, sum_s[r], top_s[k][r] - low);
+              add(i, sum_s[r], tops[i] - low);
             } else {
-              for (int v = 0; v < 4; ++v) add(i, far_s[k][v][r].x, far_s[k][v][r].y);
+              for (int v = 0; v < 4; ++v) {
+                const float2 x = __ldcg(far_sums + (4 * (step & 3) + v) * 64 + r);
+                add(i, x.x, x.y);
+              }
             }
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (leader) {
-          mbar_arrive(&bar.oempty[k]);
-          mbar_arrive(&bar.mempty[k]);
-        }
+        if (leader) mbar_arrive(&bar.oempty[k]);
       }
       if (!go) break;
       constexpr int kLd = NP * 128 + 4;
       float* part = P.parts + (static_cast<long long>(2 * blockIdx.x) + max(w.part, 0)) * R * kLd;
       if (d < R) row_s[d] = unit;
-      if (!meet(3, ok)) break;
+      if (!meet<128>(3, ok)) break;
       if (leader) mbar_arrive(&bar.qempty[qb]);
       ++qn;
       if (q == 0) {
@@ -1076,14 +1212,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      meet(3, true);
+      meet<128>(3, true);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const long long at = w.part < 0 ? place_s[r] : r * kLd;
         if (at < 0) break;
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-          const float v = r & 1 ? acc[p][r / 2].y : acc[p][r / 2].x;
+          const float v = r & 1 ? second_of(acc[p][r / 2]) : first_of(acc[p][r / 2]);
           if (w.part < 0) {
             unsigned short bits;
             const float f = row_s[r];
@@ -1094,7 +1230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      meet(3, true);
+      meet<128>(3, true);
     }
   }
 
@@ -1178,12 +1314,14 @@ bool good_shape(int B, int n, int Hq, int H, int D) {
 int block_rows(int n, int G, int D) {
   const int rows = n * G;
   // (of trees of more than 512 nodes the masks of 64 rows do not fit)
-  return rows <= 16 ? 16 : rows <= 32 || D > 128 || n > 512 ? 32 : rows <= 48 ? 48 : 64;
+  if (D > 128) return rows <= 16 ? 16 : 32;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 24 ? 24 : rows <= 32 || n > 512 ? 32 : rows <= 48 ? 48 : 64;
 }
 
 size_t attend_workspace(int n, int Hq, int H, int D) {
   const int R = block_rows(n, Hq / H, D), ld = (D > 128 ? 256 : 128) + 4;
-  return align256(kMaxCtas * sizeof(int4)) + static_cast<size_t>(2) * kMaxCtas * R * ld * sizeof(float);
+  return align256(kMaxCtas * sizeof(int4)) + static_cast<size_t>(kMaxCtas) * 1024 * sizeof(float2) +
+         static_cast<size_t>(2) * kMaxCtas * R * ld * sizeof(float);
 }
 
 // Codes as rows of D bytes: boxes of a page's tokens x 128 elements, 128-byte swizzle, zeros beyond D.
@@ -1233,7 +1371,7 @@ spec_status launch_attend(const spec_attend_args& a, AttendParams& p, cudaStream
   if (!code_map(&tk, a.k_codes, rows, a.D, a.page) || !code_map(&tv, a.v_codes, rows, a.D, a.page)) return SPEC_ECUDA;
   if (raise_smem<R, NP>() != cudaSuccess) return SPEC_ECUDA;
   p.more_bytes = g_more_bytes.load();
-  const int ctas = std::min(nsm, kMaxCtas);
+  const int ctas = std::min(nsm * Shape<R, NP>::kCtas, kMaxCtas);
   const int smem = Shape<R, NP>::kSmem + (p.parent ? a.n * static_cast<int>(2 * sizeof(typename Shape<R, NP>::Mask) + 2) : 0);
   if (smem > Shape<R, NP>::kSmem + kMaskBytes) return SPEC_EINVAL;  // (block_rows sees to it)
   attend_kernel<R, NP><<<ctas, kThreads, smem, s>>>(tk, tv, p);
@@ -1303,11 +1441,14 @@ extern "C" spec_status spec_attend_cache(const spec_attend_args* a, cudaStream_t
   p.seq_error = a->seq_error;
   p.error_word = a->error_word;
   p.shared = static_cast<int4*>(a->workspace);
-  p.parts = reinterpret_cast<float*>(static_cast<char*>(a->workspace) + align256(kMaxCtas * sizeof(int4)));
+  p.far = reinterpret_cast<float2*>(static_cast<char*>(a->workspace) + align256(kMaxCtas * sizeof(int4)));
+  p.parts = reinterpret_cast<float*>(p.far + kMaxCtas * 1024);
   const int R = block_rows(a->n, p.G, a->D);
   if (a->D > 128) return R == 16 ? launch_attend<16, 2>(*a, p, stream) : launch_attend<32, 2>(*a, p, stream);
   switch (R) {
+    case 8: return launch_attend<8, 1>(*a, p, stream);
     case 16: return launch_attend<16, 1>(*a, p, stream);
+    case 24: return launch_attend<24, 1>(*a, p, stream);
     case 32: return launch_attend<32, 1>(*a, p, stream);
     case 48: return launch_attend<48, 1>(*a, p, stream);
     default: return launch_attend<64, 1>(*a, p, stream);

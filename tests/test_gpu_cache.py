@@ -320,7 +320,9 @@ ATTENDS = [
     (2, 150, 2, 2, 32, 32, (10, 129), True, "plain"), (1, 2, 64, 1, 128, 64, (255,), False, "plain"),
     (2, 1, 5, 5, 48, 128, (126, 127), False, "plain"), (40, 2, 4, 2, 64, 16, tuple(range(0, 80, 2)), False, "plain"),
     (1, 4, 8, 8, 128, 128, (9000,), False, "plain"),
+    (2, 20, 4, 2, 128, 32, (700, 260), True, "plain"), (3, 11, 4, 1, 80, 16, (200, 5, 1333), False, "plain"),
     # many tiles per CTA, over the ends of sequences
+    (3, 9, 64, 16, 128, 64, (1500, 777, 2301), False, "plain"),
     (5, 3, 12, 12, 80, 32, (3001, 2500, 2222, 1999, 3000), False, "plain"),
     (9, 2, 48, 48, 64, 16, (700, 1, 64, 900, 333, 511, 513, 127, 128), True, "plain"),
     (6, 20, 32, 32, 128, 128, (1500, 300, 1301, 1, 1000, 640), True, "plain"),
