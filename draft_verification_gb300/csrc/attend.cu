@@ -60,16 +60,17 @@ constexpr int kFar = 9;    // value exponents of a step that lie further apart t
 template <int R, int NP>
 struct Shape {
   static constexpr int kCtas = NP == 1 && R <= 24 ? 2 : 1;  // per SM
-  static constexpr int kSubs = NP == 1 && R == 32 ? 2 : 1;  // tiles of a step
+  static constexpr int kSubs = NP == 1 && R >= 32 ? 2 : 1;  // tiles of a step
   // An operand from shared memory costs its bytes (a product of 128 x 32 with 32
   // rows some 60 cycles, with 64 hardly more), so K and V are taken once for hi
   // and lo: as rows of their own, whose results are added later.  Where tensor
   // memory is short (64 rows) the outputs' hi and lo are two products instead.
-  static constexpr bool kStacked = R <= 48;    // the outputs' hi and lo
-  static constexpr bool kStackedL = R <= 32;   // the sums' hi and lo
+  static constexpr bool kStackedS = R <= 32;   // the scores' hi and lo
+  static constexpr bool kStacked = R <= 48;    // the outputs'
+  static constexpr bool kStackedL = R <= 32;   // the sums'
   // places of K tiles, and as many of V tiles (each with barriers of its own: a
   // warp has to meet all phases of a barrier that it waits on)
-  static constexpr int kStages = NP == 2 || kCtas == 2 ? 2 : 4;
+  static constexpr int kStages = NP == 2 || kCtas == 2 ? 2 : R > 32 ? 3 : 4;
   static constexpr int kSlot = NP * kPanel;
   // a token's weights: hi's rows, then lo's, in one row of bytes, or in two planes
   static constexpr int kPRow = !kStacked ? R : R == 48 ? 128 : R == 24 ? 64 : 2 * R;
@@ -83,7 +84,7 @@ struct Shape {
   static constexpr int kLBufs = R == 24 && kCtas == 2 ? 1 : 2;  // places of the sums
   // (a product of bytes whose rows lie along the other axis takes 16 of them at a time)
   static_assert(kStackedL ? 2 * R % 16 == 0 : R % 16 == 0, "the sums' products");
-  static constexpr int kSCols = 2 * R, kOCols = kStacked ? 2 * R : R, kLCols = kStackedL ? 2 * R : R;
+  static constexpr int kSCols = kStackedS ? 2 * R : R, kOCols = kStacked ? 2 * R : R, kLCols = kStackedL ? 2 * R : R;
   static constexpr int kCols = kScores * kSubs * kSCols + 2 * NP * kOCols + kLBufs * kLCols;
   static constexpr uint32_t kTmemCols = kCols <= 256 ? 256 : 512;
   static_assert(kCols * kCtas <= 512 && (kScores + 4) * kSubs + kStages + 1 <= kScaleRing && 2 * kStages + kPatchRing <= 32, "rings");
@@ -276,6 +277,13 @@ __device__ __forceinline__ void split4(float a, float b, float c, float d, uint3
       : "f"(a), "f"(b), "f"(c), "f"(d));
 }
 
+// 8 bytes of global memory to shared memory, or zeros; and the thread's wait for all of them.
+__device__ __forceinline__ void copy8_async(void* to, const void* from, bool has) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_addr(to)), "l"(from), "r"(has ? 8 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // Two float32 numbers in a register pair, each lane rounded as by itself (in
 // 64 bits throughout: as two floats the pairs cost moves at every operation).
 using F2 = unsigned long long;
@@ -302,6 +310,13 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
   return d;
 }
 __device__ __forceinline__ ulonglong2 lds_pairs(const void* p) { return *static_cast<const ulonglong2*>(p); }
+
+// Both rounded to bfloat16, the first in the lower half.
+__device__ __forceinline__ uint32_t pack_bf16(F2 x) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(second_of(x)), "f"(first_of(x)));
+  return d;
+}
 
 // Consecutive float32 columns of this warp's 32 lanes, in pairs.
 __device__ __forceinline__ void tmem_load8(uint32_t taddr, F2* v) {
@@ -361,12 +376,12 @@ __global__ void __launch_bounds__(kThreads, Shape<R, NP>::kCtas)
   // kfull / kempty, vfull / vempty: a tile's K, V; sfull / sempty: a step's scores; pfull /
   // pempty: its weights in shared memory; ofull / oempty: its outputs; mfull /
   // mempty: its maxima (top_s); qfull / qempty: a piece's queries; rfull /
-  // rempty: its record; landed: V of a tile that is patched before it is vfull;
-  // patched: it is; drain: no product is under way
+  // rempty: its record; landed: V of a tile that is patched before it is
+  // vfull; drain: no product is under way
   struct Bars {
     uint64_t kfull[S::kStages], vfull[S::kStages], kempty[S::kStages], vempty[S::kStages];
     uint64_t sfull[S::kScores], sempty[S::kScores], pfull[2], pempty[2], ofull[2], oempty[2], mfull[2], mempty[2];
-    uint64_t qfull[2], qempty[2], landed[kPatchRing], patched[kPatchRing], rfull[kPieceRing], rempty[kPieceRing], drain[2];
+    uint64_t qfull[2], qempty[2], landed[kPatchRing], rfull[kPieceRing], rempty[kPieceRing], drain[2];
   };
   constexpr int kBars = sizeof(Bars) / 8;
   __shared__ Bars bar;
@@ -379,9 +394,8 @@ __global__ void __launch_bounds__(kThreads, Shape<R, NP>::kCtas)
   __shared__ __align__(16) float most_s[2][2][4][kCut], ref_s[8][kCut], cq_s[2][R], top_s[2][R], sum_s[R];
   __shared__ __align__(16) float keep_s[2][R], take_s[2][R];
   __shared__ __align__(16) float row_s[R];
-  __shared__ long long place_s[R];
+  __shared__ __align__(16) long long place_s[R];
   __shared__ unsigned char token_s[2][R];
-  __shared__ unsigned nan_s[kPatchRing][kTile / 32];
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const bool leader = one_lane();
@@ -560,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, Shape<R, NP>::kCtas)
     if (leader) issued_s = issued, parity_s = parities;
   } else if (warp == 1) {
     // ---------------- scores ----------------
-    constexpr uint32_t idesc = idesc_e4m3(kTile, 2 * R, 0, 0), high = operand_high(1024, 128);
+    constexpr uint32_t idesc = idesc_e4m3(kTile, S::kSCols, 0, 0), high = operand_high(1024, 128);
     const int steps = (P.D + 31) / 32;
     const uint32_t issues = leader ? 1u : 0u;
     int it = 0, step = 0, qn = 0;
@@ -587,6 +601,13 @@ __global__ void __launch_bounds__(kThreads, Shape<R, NP>::kCtas)
           if (e < steps)
             umma_e4m3(issues, d, a + (e >> 2) * (kPanel >> 4) + (e & 3) * 2, high,
                       q + (e >> 2) * (2 * R * 128 >> 4) + (e & 3) * 2, high, idesc, 1u);
+        if constexpr (!S::kStackedS) {
+#pragma unroll
+          for (int e = 0; e < 4 * NP; ++e)
+            if (e < steps)
+              umma_e4m3(issues, d, a + (e >> 2) * (kPanel >> 4) + (e & 3) * 2, high,
+                        q + (R * 128 >> 4) + (e >> 2) * (2 * R * 128 >> 4) + (e & 3) * 2, high, idesc, 1u);
+        }
         commit_if(issues, &bar.kempty[at.slot]);
         if (sub == S::kSubs - 1 || t + 1 == w.t1) {
           commit_if(issues, &bar.sfull[sb]);
@@ -707,60 +728,51 @@ __global__ void __launch_bounds__(kThreads, Shape<R, NP>::kCtas)
         shared = make_int4(b, h, block, c - cta + 1);
       }
       if (keys > 0) {
-        // the block's rows: two e4m3 numbers for each element
+        // The block's rows: two e4m3 numbers for each element.  A lane's 8 elements
+        // of a row are copied to where their 16 codes will lie, all rows at once, and
+        // are turned into codes there.  (One warp does it beside the other roles'
+        // work: short loops, since it waits for instructions most of all.)
         constexpr int kLanes = 16 * NP;       // lanes of a row, 8 elements each
         constexpr int kAtOnce = 32 / kLanes;  // rows at a time
-        constexpr int kBatch = S::kCtas == 2 ? 4 : 8;
-        const int qb = qn & 1, row0 = block * R, tok0 = row0 / P.G, d0 = lane % kLanes * 8;
+        const int qb = qn & 1, row0 = block * R, tok0 = row0 / P.G, d0 = lane % kLanes * 8, r0 = lane / kLanes;
         ok = at_wait(&bar.qempty[qb], (static_cast<unsigned>(qn >> 1) & 1u) ^ 1u, fault);
         if (!ok) break;
-        unsigned char* dst = qbuf + qb * S::kQBytes;
-        const bf16_t* q = P.q + b * P.q_ld[0] + static_cast<long long>(h) * P.G * P.q_ld[2] + d0;
-#pragma unroll 1
-        for (int r1 = 0; r1 < R; r1 += kBatch * kAtOnce) {
-          uint4 raw[kBatch];
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            const int row = row0 + r1 + i * kAtOnce + lane / kLanes, tok = row / P.G, g = row - tok * P.G;
-            raw[i] = make_uint4(0, 0, 0, 0);
-            if (tok < s.count && d0 < P.D && r1 + i * kAtOnce < R)
-              raw[i] = *reinterpret_cast<const uint4*>(q + tok * P.q_ld[1] + g * P.q_ld[2]);
+        unsigned char* dst = qbuf + qb * S::kQBytes + (d0 >> 7) * 2 * R * 128;
+        const auto place = [&](int r) { return dst + swizzled(r * 128 + (d0 & 127), 128); };
+        {
+          const bf16_t* q = P.q + b * P.q_ld[0] + static_cast<long long>(h) * P.G * P.q_ld[2] + d0;
+          int tok = (row0 + r0) / P.G, g = row0 + r0 - tok * P.G;
+#pragma unroll 2
+          for (int r = r0; r < R; r += kAtOnce) {
+            const bool has = tok < s.count && d0 < P.D;
+            const bf16_t* from = has ? q + tok * P.q_ld[1] + g * P.q_ld[2] : P.q;
+            unsigned char* to = place(r);
+            copy8_async(to, from, has);
+            copy8_async(to + R * 128, from + (has ? 4 : 0), has);
+            if (d0 == 0) token_s[qb][r] = static_cast<unsigned char>(tok - tok0);
+            for (g += kAtOnce; g >= P.G; g -= P.G) ++tok;
           }
+          copies_wait();
+        }
+#pragma unroll 2
+        for (int r = r0; r < R; r += kAtOnce) {
+          uint2* to = reinterpret_cast<uint2*>(place(r));
+          const uint2 x = to[0], y = to[R * 16];
+          const uint32_t sign = 0x7fff7fffu;
+          uint32_t m = __vmaxu2(__vmaxu2(x.x & sign, x.y & sign), __vmaxu2(y.x & sign, y.y & sign));
 #pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            const int r = r1 + i * kAtOnce + lane / kLanes;
-            if (r1 + i * kAtOnce >= R) break;
-            const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-            float v[8], most = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              v[e] = e & 1 ? bf16_hi(u[e / 2]) : bf16_lo(u[e / 2]);
-              if (fabsf(v[e]) < kInf) most = fmaxf(most, fabsf(v[e]));
-              else v[e] = __uint_as_float(0x7fc00000u);
-            }
-#pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-            // the least exponent with most <= 448 2^eq
-            const uint32_t bits = __float_as_uint(most);
-            const int eq =
-                max(static_cast<int>(bits >> 23) - 127 - ((bits & 0x7fffffu) <= 0x600000u ? 8 : 7), -100);
-            const float f = exp2i(-eq);
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float a = v[2 * e] * f, c = v[2 * e + 1] * f;
-              hi[e] = pack_e4m3(a, c);
-              const float2 back = unpack_e4m3(hi[e]);
-              lo[e] = pack_e4m3(a - back.x, c - back.y);
-            }
-            const uint32_t at = (d0 >> 7) * 2 * R * 128 + swizzled(r * 128 + (d0 & 127), 128);
-            *reinterpret_cast<uint2*>(dst + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-            *reinterpret_cast<uint2*>(dst + R * 128 + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-            if (d0 == 0) {
-              cq_s[qb][r] = exp2i(eq) * P.c;
-              token_s[qb][r] = static_cast<unsigned char>((row0 + r) / P.G - tok0);
-            }
-          }
+          for (int o = kLanes / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+          m = max(m & 0xffffu, m >> 16);  // the row's largest magnitude
+          const bool lost = m >= 0x7f80u;
+          // the least exponent with magnitude <= 448 2^eq
+          const int eq = lost ? 0 : max(static_cast<int>(m >> 7) - 127 - ((m & 0x7fu) <= 0x60u ? 8 : 7), -100);
+          const float f = exp2i(-eq);
+          uint2 hi, lo;
+          split4(bf16_lo(x.x) * f, bf16_hi(x.x) * f, bf16_lo(x.y) * f, bf16_hi(x.y) * f, hi.x, lo.x);
+          split4(bf16_lo(y.x) * f, bf16_hi(y.x) * f, bf16_lo(y.y) * f, bf16_hi(y.y) * f, hi.y, lo.y);
+          to[0] = hi;
+          to[R * 16] = lo;
+          if (d0 == 0) cq_s[qb][r] = lost ? __uint_as_float(0x7fc00000u) : exp2i(eq) * P.c;
         }
         if (P.parent) {
           // which of the block's rows' tokens see drafted token j
@@ -809,61 +821,19 @@ __global__ void __launch_bounds__(kThreads, Shape<R, NP>::kCtas)
     if (leader) P.shared[cta] = ok ? shared : make_int4(0, 0, 0, 0);
   } else if (warp == 3) {
     // ---------------- outputs' products ----------------
-    // (and, before them, V of what no row sees, and NaN values among the drafted tokens)
     constexpr uint32_t idesc = idesc_e4m3(128, S::kOCols, 1, 1), idesc_l = idesc_e4m3(64, S::kLCols, 0, 1);
     constexpr uint32_t a_high = operand_high(1024, 128), b_high = operand_high(8 * S::kPRow, S::kPRow);
     const uint32_t issues = leader ? 1u : 0u;
-    int it = 0, step = 0, patches = 0;
+    int it = 0, step = 0;
     bool ok = true;
     Piece w;
     while (ok && next_piece(w)) {
-      const int special = first_special(w);
 #pragma unroll 1
       for (int t = w.t0; ok && t < w.t1; ++t, ++it) {
         const int k = step & 1, sub = S::kSubs == 2 ? (t - w.t0) & 1 : 0;
         const unsigned half = static_cast<unsigned>(step >> 1) & 1u;
-        if (sub == 0) {
-          // (the weights of a step wait for its patches)
-#pragma unroll 1
-          for (int u = max(t, special); ok && u < min(t + S::kSubs, w.t1); ++u, ++patches) {
-            ok = at_wait(&bar.landed[patches % kPatchRing], static_cast<unsigned>(patches / kPatchRing) & 1u, fault);
-            if (!ok) break;
-            const Place<S::kStages> at(it + u - t);
-#pragma unroll 1
-            for (int row = lane; row < kTile; row += 32) {
-              const int pos = u * kTile + row;
-              unsigned char* v = vring + at.slot * S::kSlot + row * 128;
-              bool clear = pos >= w.keys, nan = false;
-              if (!clear && pos >= w.prefix) {
-#pragma unroll 1
-                for (int p = 0; p < NP; ++p)
-#pragma unroll
-                  for (int o = 0; o < 128; o += 16) {
-                    const uint4 x = *reinterpret_cast<const uint4*>(v + p * kPanel + o);
-                    const uint32_t m = 0x7f7f7f7fu, one = 0x01010101u;
-                    nan |=
-                        ((((x.x & m) + one) | ((x.y & m) + one) | ((x.z & m) + one) | ((x.w & m) + one)) & 0x80808080u) != 0;
-                  }
-                clear = nan;
-              }
-              if (clear) {
-#pragma unroll 1
-                for (int p = 0; p < NP; ++p)
-#pragma unroll
-                  for (int o = 0; o < 128; o += 16) *reinterpret_cast<uint4*>(v + p * kPanel + o) = make_uint4(0, 0, 0, 0);
-              }
-              const unsigned all = __ballot_sync(0xffffffffu, nan);
-              if (leader) nan_s[patches % kPatchRing][row >> 5] = all;
-            }
-            fence_proxy_async();
-            __syncwarp();
-            if (leader) {
-              mbar_arrive(&bar.patched[patches % kPatchRing]);
-              mbar_arrive(&bar.vfull[at.slot]);
-            }
-          }
-          ok = ok && at_wait(&bar.oempty[k], half ^ 1u, fault) && at_wait(&bar.pfull[k], half, fault);
-        }
+        if (sub == 0)
+          ok = at_wait(&bar.oempty[k], half ^ 1u, fault) && at_wait(&bar.pfull[k], half, fault);
         const Place<S::kStages> at(it);
         ok = ok && at_wait(&bar.vfull[at.slot], at.parity, fault);
         if (!ok) break;
@@ -939,17 +909,43 @@ __global__ void __launch_bounds__(kThreads, Shape<R, NP>::kCtas)
         Mask seen0 = ~static_cast<Mask>(0), seen1 = seen0;
         bool nan0 = false, nan1 = false;
         if (special_step) {
-          const auto look = [&](int tile, int patch, Mask& seen, bool& nan) {
+          // V of what no row sees is cleared, and NaN values of drafted tokens, which
+          // are passed on by the scores (a drafted token that a row does not see must
+          // not reach it).  Of the ring's phases this warp meets some: 8 patched tiles
+          // earlier is at least 4 steps earlier, whose outputs are known to be done.
+          const auto look = [&](int tile, int number, int patch, Mask& seen, bool& nan) {
             if (tile < special) return;
-            ok = at_wait(&bar.patched[patch % kPatchRing], static_cast<unsigned>(patch / kPatchRing) & 1u, fault) && ok;
             const int pos = tile * kTile + row, j = pos - w.prefix;
-            if (pos >= w.keys) seen = 0;
+            bool clear = pos >= w.keys;
+            if (clear) seen = 0;
             else if (j >= 0 && P.parent) seen = mask_s[qb * P.n + j];
             else if (j > tok0) seen = j - tok0 >= static_cast<int>(8 * sizeof(Mask)) ? 0 : seen << (j - tok0);
-            nan = nan_s[patch % kPatchRing][q] >> lane & 1u;
+            ok = at_wait(&bar.landed[patch % kPatchRing], static_cast<unsigned>(patch / kPatchRing) & 1u, fault) && ok;
+            const Place<S::kStages> v_at(number);
+            unsigned char* v = vring + v_at.slot * S::kSlot + row * 128;
+            if (!clear && j >= 0) {
+#pragma unroll 1
+              for (int p = 0; p < NP; ++p)
+#pragma unroll 2
+                for (int o = 0; o < 8; ++o) {
+                  const uint4 x = *reinterpret_cast<const uint4*>(v + p * kPanel + ((o + lane) & 7) * 16);
+                  const uint32_t m = 0x7f7f7f7fu, one = 0x01010101u;
+                  nan |= ((((x.x & m) + one) | ((x.y & m) + one) | ((x.z & m) + one) | ((x.w & m) + one)) & 0x80808080u) != 0;
+                }
+              clear = nan;
+            }
+            if (clear) {
+#pragma unroll 1
+              for (int p = 0; p < NP; ++p)
+#pragma unroll 2
+                for (int o = 0; o < 8; ++o)
+                  *reinterpret_cast<uint4*>(v + p * kPanel + ((o + lane) & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            // (the outputs' products wait for the weights too, hence for all four warps)
+            if (q == 0 && leader) mbar_arrive(&bar.vfull[v_at.slot]);
           };
-          look(t, patch, seen0, nan0);
-          if (tiles == 2) look(t + 1, patch + (t >= special ? 1 : 0), seen1, nan1);
+          look(t, at, patch, seen0, nan0);
+          if (tiles == 2) look(t + 1, at + 1, patch + (t >= special ? 1 : 0), seen1, nan1);
         }
         const float low = fminf(ps0.ve_low, ps1.ve_low);
         const bool far = fmaxf(ps0.ve_high, ps1.ve_high) - low > static_cast<float>(kFar);
@@ -963,13 +959,17 @@ __global__ void __launch_bounds__(kThreads, Shape<R, NP>::kCtas)
             tmem_pairs<kCut>(from, y);
 #pragma unroll
             for (int i = 0; i < kCut / 2; i += 4) {  // hi's and lo's
-              F2 lo[4];
-              tmem_load8(from + R + 2 * i, lo);
+              if constexpr (S::kStackedS) {
+                F2 lo[4];
+                tmem_load8(from + R + 2 * i, lo);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[i + j] = add2(y[i + j], lo[j]);
+              }
               const ulonglong2 f = lds_pairs(&cq_s[qb][c + 2 * i]), g = lds_pairs(&cq_s[qb][c + 2 * i + 4]);
-              y[i] = fma2(mul2(add2(y[i], lo[0]), f.x), ck, ve);
-              y[i + 1] = fma2(mul2(add2(y[i + 1], lo[1]), f.y), ck, ve);
-              y[i + 2] = fma2(mul2(add2(y[i + 2], lo[2]), g.x), ck, ve);
-              y[i + 3] = fma2(mul2(add2(y[i + 3], lo[3]), g.y), ck, ve);
+              y[i] = fma2(mul2(y[i], f.x), ck, ve);
+              y[i + 1] = fma2(mul2(y[i + 1], f.y), ck, ve);
+              y[i + 2] = fma2(mul2(y[i + 2], g.x), ck, ve);
+              y[i + 3] = fma2(mul2(y[i + 3], g.y), ck, ve);
             }
           };
           scores(0, ps0, y0);
@@ -1202,8 +1202,8 @@ __global__ void __launch_bounds__(kThreads, Shape<R, NP>::kCtas)
           const float s = sum[i], u = row_s[r];
           if (w.part < 0) {
             const int tok = (row0 + r) / P.G, g = row0 + r - tok * P.G;
-            place_s[r] = tok >= P.n ? -1 : w.b * P.out_ld[0] + tok * P.out_ld[1] + (w.h * P.G + g) * P.out_ld[2];
-            row_s[r] = s == 0.f || tok >= w.count ? 0.f : ex2(u - sum_unit[i]) / s;
+            place_s[r] = w.b * P.out_ld[0] + tok * P.out_ld[1] + (w.h * P.G + g) * P.out_ld[2];
+            row_s[r] = s == 0.f ? 0.f : ex2(u - sum_unit[i]) / s;
           } else {
             float* e = part + r * kLd + NP * 128;
             __stcg(e, u);
@@ -1213,20 +1213,35 @@ __global__ void __launch_bounds__(kThreads, Shape<R, NP>::kCtas)
         }
       }
       meet<128>(3, true);
+      if (w.part >= 0) {
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const long long at = w.part < 0 ? place_s[r] : r * kLd;
-        if (at < 0) break;
+        for (int p = 0; p < NP; ++p)
+#pragma unroll
+          for (int r = 0; r < R; r += 2) {
+            __stcg(part + r * kLd + p * 128 + d, first_of(acc[p][r / 2]));
+            __stcg(part + (r + 1) * kLd + p * 128 + d, second_of(acc[p][r / 2]));
+          }
+      } else {
+        const int live = w.count * P.G - row0, all = P.n * P.G - row0;  // rows with a result, rows
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-          const float v = r & 1 ? second_of(acc[p][r / 2]) : first_of(acc[p][r / 2]);
-          if (w.part < 0) {
-            unsigned short bits;
-            const float f = row_s[r];
-            asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(bits) : "f"(f == 0.f ? 0.f : v * f));
-            if (p * 128 + d < P.D) P.out[at + p * 128 + d] = bits;
-          } else {
-            __stcg(part + at + p * 128 + d, v);
+          bf16_t* out = P.out + p * 128 + d;
+          const bool has = p * 128 + d < P.D;
+#pragma unroll
+          for (int r = 0; r < R; r += 4) {
+            if (r >= live) break;
+            const ulonglong2 f = lds_pairs(row_s + r);
+            const longlong2 to0 = *reinterpret_cast<const longlong2*>(place_s + r);
+            const longlong2 to1 = *reinterpret_cast<const longlong2*>(place_s + r + 2);
+            const uint32_t x = pack_bf16(mul2(acc[p][r / 2], f.x)), y = pack_bf16(mul2(acc[p][r / 2 + 1], f.y));
+            if (has) out[to0.x] = static_cast<bf16_t>(x);
+            if (has && r + 1 < live) out[to0.y] = static_cast<bf16_t>(x >> 16);
+            if (has && r + 2 < live) out[to1.x] = static_cast<bf16_t>(y);
+            if (has && r + 3 < live) out[to1.y] = static_cast<bf16_t>(y >> 16);
+          }
+          if (has) {
+#pragma unroll 1
+            for (int r = max(live, 0); r < min(R, all); ++r) out[place_s[r]] = 0;
           }
         }
       }
