@@ -88,7 +88,7 @@ struct Shape {
   static constexpr int kCols = kScores * kSubs * kSCols + 2 * NP * kOCols + kLBufs * kLCols;
   static constexpr uint32_t kTmemCols = kCols <= 256 ? 256 : 512;
   static_assert(kCols * kCtas <= 512 && (kScores + 4) * kSubs + kStages + 1 <= kScaleRing && 2 * kStages + kPatchRing <= 32, "rings");
-  using Mask = typename std::conditional<(R > 32), unsigned long long, unsigned>::type;  // a bit per token of a block
+  using Mask = typename std::conditional<(R > 32), unsigned long long, unsigned>::type;  // a bit per row of a block
 };
 
 struct AttendParams {
@@ -395,7 +395,6 @@ __global__ void __launch_bounds__(kThreads, Shape<R, NP>::kCtas)
   __shared__ __align__(16) float keep_s[2][R], take_s[2][R];
   __shared__ __align__(16) float row_s[R];
   __shared__ __align__(16) long long place_s[R];
-  __shared__ unsigned char token_s[2][R];
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const bool leader = one_lane();
@@ -742,20 +741,21 @@ __global__ void __launch_bounds__(kThreads, Shape<R, NP>::kCtas)
         {
           const bf16_t* q = P.q + b * P.q_ld[0] + static_cast<long long>(h) * P.G * P.q_ld[2] + d0;
           int tok = (row0 + r0) / P.G, g = row0 + r0 - tok * P.G;
-#pragma unroll 2
-          for (int r = r0; r < R; r += kAtOnce) {
+#pragma unroll 4
+          for (int r1 = 0; r1 < R; r1 += kAtOnce) {
+            const int r = r1 + r0;
             const bool has = tok < s.count && d0 < P.D;
             const bf16_t* from = has ? q + tok * P.q_ld[1] + g * P.q_ld[2] : P.q;
             unsigned char* to = place(r);
             copy8_async(to, from, has);
             copy8_async(to + R * 128, from + (has ? 4 : 0), has);
-            if (d0 == 0) token_s[qb][r] = static_cast<unsigned char>(tok - tok0);
             for (g += kAtOnce; g >= P.G; g -= P.G) ++tok;
           }
-          copies_wait();
         }
-#pragma unroll 2
-        for (int r = r0; r < R; r += kAtOnce) {
+        copies_wait();
+#pragma unroll 4
+        for (int r1 = 0; r1 < R; r1 += kAtOnce) {
+          const int r = r1 + r0;
           uint2* to = reinterpret_cast<uint2*>(place(r));
           const uint2 x = to[0], y = to[R * 16];
           const uint32_t sign = 0x7fff7fffu;
@@ -775,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, Shape<R, NP>::kCtas)
           if (d0 == 0) cq_s[qb][r] = lost ? __uint_as_float(0x7fc00000u) : exp2i(eq) * P.c;
         }
         if (P.parent) {
-          // which of the block's rows' tokens see drafted token j
+          // which of the block's rows see drafted token j
           Mask* mask = mask_s + qb * P.n;
           const int* parent = P.parent + static_cast<long long>(b) * P.n;
           bool bad = false;
@@ -790,12 +790,14 @@ __global__ void __launch_bounds__(kThreads, Shape<R, NP>::kCtas)
           }
           if (bad && h == 0) report(P, b, SPEC_ERR_PARENT);
           __syncwarp();
-          for (int i = lane; i < R; i += 32) {
-            const int tok = tok0 + i;
-            if (tok >= s.count || tok * P.G >= row0 + R) break;
-            const Mask bit = static_cast<Mask>(1) << i;
+          for (int tok = tok0 + lane; tok < s.count && tok * P.G < row0 + R; tok += 32) {
+            const int from = max(tok * P.G - row0, 0), many = min((tok + 1) * P.G - row0, R) - from;
+            const Mask bits = (~static_cast<Mask>(0) >> (8 * sizeof(Mask) - many)) << from;
             for (int j = tok;; j = parent_s[j]) {
-              atomicOr(mask + j, bit);
+              unsigned* m = reinterpret_cast<unsigned*>(mask + j);
+              if (static_cast<unsigned>(bits)) atomicOr(m, static_cast<unsigned>(bits));
+              if constexpr (sizeof(Mask) == 8)
+                if (bits >> 32) atomicOr(m + 1, static_cast<unsigned>(bits >> 32));
               if (j == 0) break;
             }
           }
@@ -889,7 +891,7 @@ __global__ void __launch_bounds__(kThreads, Shape<R, NP>::kCtas)
     while (true) {
       const bool got = next_piece(w);
       if (!meet<128>(1 + turn, got)) break;
-      const int special = first_special(w), qb = qn & 1, tok0 = w.block * R / P.G;
+      const int special = first_special(w), qb = qn & 1;
       bool go = true;
 #pragma unroll 1
       for (int t = w.t0; t < w.t1; t += S::kSubs, ++step) {
@@ -919,7 +921,7 @@ __global__ void __launch_bounds__(kThreads, Shape<R, NP>::kCtas)
             bool clear = pos >= w.keys;
             if (clear) seen = 0;
             else if (j >= 0 && P.parent) seen = mask_s[qb * P.n + j];
-            else if (j > tok0) seen = j - tok0 >= static_cast<int>(8 * sizeof(Mask)) ? 0 : seen << (j - tok0);
+            else if (j * P.G > w.block * R) seen = j * P.G >= w.block * R + R ? 0 : seen << (j * P.G - w.block * R);
             ok = at_wait(&bar.landed[patch % kPatchRing], static_cast<unsigned>(patch / kPatchRing) & 1u, fault) && ok;
             const Place<S::kStages> v_at(number);
             unsigned char* v = vring + v_at.slot * S::kSlot + row * 128;
@@ -980,13 +982,16 @@ __global__ void __launch_bounds__(kThreads, Shape<R, NP>::kCtas)
             for (int i = 0; i < kCut / 2; ++i) y1[i] = pair(-kInf, -kInf);
           }
           if (special_step) {
-            const auto cover = [&](F2* y, Mask seen, bool nan) {
+            const auto cover = [&](F2* y, Mask rows, bool nan) {
+              const unsigned seen = static_cast<unsigned>(rows >> c);
               const float none = -kInf, lost = __uint_as_float(0x7fc00000u);
+              if (nan) {
 #pragma unroll
-              for (int i = 0; i < kCut / 2; ++i) {
-                const bool see0 = seen >> token_s[qb][c + 2 * i] & 1, see1 = seen >> token_s[qb][c + 2 * i + 1] & 1;
-                y[i] = pair(!see0 ? none : nan ? lost : first_of(y[i]), !see1 ? none : nan ? lost : second_of(y[i]));
+                for (int i = 0; i < kCut / 2; ++i) y[i] = pair(lost, lost);
               }
+#pragma unroll
+              for (int i = 0; i < kCut / 2; ++i)
+                y[i] = pair(seen & 1u << 2 * i ? first_of(y[i]) : none, seen & 2u << 2 * i ? second_of(y[i]) : none);
             };
             cover(y0, seen0, nan0);
             if (tiles == 2) cover(y1, seen1, nan1);
@@ -1272,46 +1277,55 @@ __global__ void __launch_bounds__(kThreads, Shape<R, NP>::kCtas)
 template <int R, int NP>
 __global__ void __launch_bounds__(128) join_kernel(const AttendParams P) {
   constexpr int kLd = NP * 128 + 4;
+  __shared__ float factor_s[4][kMaxCtas];
   pdl_wait();
   const int4 it = __ldcg(P.shared + blockIdx.x);
   if (it.w == 0) return;
-  const int d = threadIdx.x;
+  const int lane = threadIdx.x & 31, r = blockIdx.y * 4 + (threadIdx.x >> 5);
+  float* factors = factor_s[threadIdx.x >> 5];
   const Lengths s = lengths_of(P, it.x);
-  for (int r = blockIdx.y * 4; r < blockIdx.y * 4 + 4; ++r) {
-    const int row = it.z * R + r, tok = row / P.G;
-    if (tok >= P.n) return;
-    bf16_t* out = P.out + it.x * P.out_ld[0] + tok * P.out_ld[1] + (it.y * P.G + row % P.G) * P.out_ld[2];
-    if (tok >= s.count) {
-      for (int e = d; e < P.D; e += 128) out[e] = 0;
-      continue;
-    }
-    const auto part = [&](int i) {
-      return P.parts + (static_cast<long long>(2 * (blockIdx.x + i)) + (i == 0 ? 1 : 0)) * R * kLd + r * kLd;
-    };
-    float unit = -kInf, sum_unit = -kInf;
+  const int row = it.z * R + r, tok = row / P.G;
+  if (tok >= P.n) return;
+  bf16_t* out = P.out + it.x * P.out_ld[0] + tok * P.out_ld[1] + (it.y * P.G + row % P.G) * P.out_ld[2];
+  const auto part = [&](int i) {
+    return P.parts + (static_cast<long long>(2 * (blockIdx.x + i)) + (i == 0 ? 1 : 0)) * R * kLd + r * kLd;
+  };
+  float unit = -kInf, sum_unit = -kInf, sum = 0.f;
+  for (int i = lane; i < it.w; i += 32) {
+    const float4 x = __ldcg(reinterpret_cast<const float4*>(part(i) + NP * 128));
+    unit = fmaxf(unit, x.x);
+    sum_unit = fmaxf(sum_unit, x.z);
+  }
+  unit = warp_max(unit);
+  sum_unit = warp_max(sum_unit);
+  for (int i = lane; i < it.w; i += 32) {
+    const float4 x = __ldcg(reinterpret_cast<const float4*>(part(i) + NP * 128));
+    factors[i] = x.x == -kInf ? 0.f : ex2(x.x - unit);
+    sum += x.z == -kInf ? x.y : x.y * ex2(x.z - sum_unit);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  __syncwarp();
+  const float f = sum == 0.f || tok >= s.count ? 0.f : ex2(unit - sum_unit) / sum;
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
     for (int i = 0; i < it.w; ++i) {
-      const float* e = part(i) + NP * 128;
-      unit = fmaxf(unit, __ldcg(e));
-      sum_unit = fmaxf(sum_unit, __ldcg(e + 2));
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(part(i) + p * 128 + lane * 4));
+      const float g = factors[i];
+      acc = make_float4(__fmaf_rn(x.x, g, acc.x), __fmaf_rn(x.y, g, acc.y), __fmaf_rn(x.z, g, acc.z),
+                        __fmaf_rn(x.w, g, acc.w));
     }
-    float acc[NP], sum = 0.f;
-#pragma unroll
-    for (int p = 0; p < NP; ++p) acc[p] = 0.f;
-    for (int i = 0; i < it.w; ++i) {
-      const float* e = part(i);
-      const float u = __ldcg(e + NP * 128), su = __ldcg(e + NP * 128 + 2);
-      const float f = u == -kInf ? 0.f : ex2(u - unit);
-      const float mine = __ldcg(e + NP * 128 + 1);
-      sum += su == -kInf ? mine : mine * ex2(su - sum_unit);
-#pragma unroll
-      for (int p = 0; p < NP; ++p) acc[p] = __fmaf_rn(__ldcg(e + p * 128 + d), f, acc[p]);
-    }
-    const float f = sum == 0.f ? 0.f : ex2(unit - sum_unit) / sum;
-#pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      unsigned short bits;
-      asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(bits) : "f"(acc[p] * f));
-      if (p * 128 + d < P.D) out[p * 128 + d] = bits;
+    const bool live = tok < s.count;  // (the parts of the other rows are of no meaning)
+    const uint32_t lo = live ? pack_bf16(pair(acc.x * f, acc.y * f)) : 0u;
+    const uint32_t hi = live ? pack_bf16(pair(acc.z * f, acc.w * f)) : 0u;
+    const int e = p * 128 + lane * 4;  // (D is a multiple of 16)
+    if (e < P.D) {
+      out[e] = static_cast<bf16_t>(lo);
+      out[e + 1] = static_cast<bf16_t>(lo >> 16);
+      out[e + 2] = static_cast<bf16_t>(hi);
+      out[e + 3] = static_cast<bf16_t>(hi >> 16);
     }
   }
 }
