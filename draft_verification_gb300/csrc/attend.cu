@@ -427,6 +427,15 @@ __global__ void __launch_bounds__(kThreads, Shape<R, NP>::kCtas)
   // (rows of the sums' factors that are not the first: of no use, but of defined values)
   for (int i = tid; i < 2 * S::kSubs * S::kOnes / 16; i += kThreads) reinterpret_cast<uint4*>(ones)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async();
+  // the tiles of a sequence; those of this lane's, found while tensor memory is allocated
+  const auto lengths = [&](int b) { return lengths_of(P, b); };
+  const auto tiles_of_seq = [&](const Lengths& s) {
+    int n = 0;
+#pragma unroll 1
+    for (int i = 0; i < P.blocks; ++i) n += tiles_of(keys_of<R>(P, s, i));
+    return n * P.H;
+  };
+  const int own = warp == 2 && lane < P.B ? tiles_of_seq(lengths(lane)) : 0;
   if (warp == 1) {
     tmem_alloc(&tmem_s, S::kTmemCols);
     tmem_relinquish();
@@ -621,16 +630,9 @@ __global__ void __launch_bounds__(kThreads, Shape<R, NP>::kCtas)
     mbar_wait(&bar.drain[0], 0);
   } else if (warp == 2) {
     // ---------------- pieces, queries, masks ----------------
-    const auto lengths = [&](int b) { return lengths_of(P, b); };
-    const auto tiles_of_seq = [&](const Lengths& s) {
-      int n = 0;
+    int total = own;
 #pragma unroll 1
-      for (int i = 0; i < P.blocks; ++i) n += tiles_of(keys_of<R>(P, s, i));
-      return n * P.H;
-    };
-    int total = 0;
-#pragma unroll 1
-    for (int b = lane; b < P.B; b += 32) total += tiles_of_seq(lengths(b));
+    for (int b = lane + 32; b < P.B; b += 32) total += tiles_of_seq(lengths(b));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     // equal runs: `more` CTAs have one tile more than the others
@@ -645,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, Shape<R, NP>::kCtas)
       int before = 0;
 #pragma unroll 1
       for (int b1 = 0;; b1 += 32) {
-        const int n = b1 + lane < P.B ? tiles_of_seq(lengths(b1 + lane)) : 0;
+        const int n = b1 == 0 ? own : b1 + lane < P.B ? tiles_of_seq(lengths(b1 + lane)) : 0;
         int up = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
