@@ -16,7 +16,6 @@
 namespace sv {
 namespace {
 
-constexpr int kAppendThreads = 256;
 
 struct AppendParams {
   int n, H, D, page, pages, table_pages, rot, units, table_rows, path_ld;
@@ -63,9 +62,10 @@ __device__ __forceinline__ void store_codes(unsigned char* p, const float* x, fl
 }
 
 // The page's earlier codes, scaled by 2^-shift, shift >= 1.
+template <int TH>
 __device__ void scale_codes(unsigned char* p, int bytes, int shift) {
   const float f = shift > 126 ? 0.f : exp2i(-shift);
-  for (int o = threadIdx.x * 16; o < bytes; o += kAppendThreads * 16) {
+  for (int o = threadIdx.x * 16; o < bytes; o += TH * 16) {
     uint4 w = *reinterpret_cast<uint4*>(p + o);
     uint32_t* r = reinterpret_cast<uint32_t*>(&w);
 #pragma unroll
@@ -85,32 +85,34 @@ __device__ __forceinline__ int exponent_of(float m) {
   return min(kHighExp, max(kLowExp, e));
 }
 
-template <typename T, int V>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams P) {
-  __shared__ float most_s[2][kAppendThreads / 32];
+// TH threads; kHold: units of a page's rows that a thread keeps in registers
+// between the two passes, 0: none (they are read twice)
+template <typename T, int V, int TH, int kHold>
+__global__ void __launch_bounds__(TH, kHold == 1 || kHold == 2 ? 3 : 1) append_kernel(const AppendParams P) {
+  __shared__ float most_s[2][TH / 32];
   __shared__ int skip_s;
   const int b = blockIdx.z, h = blockIdx.y, tid = threadIdx.x;
   const int prefix = P.prefix ? P.prefix[b] : 0;
   const int* path = P.path_nodes ? P.path_nodes + static_cast<long long>(b) * P.path_ld : nullptr;
   const bool reports = blockIdx.x == 0 && h == 0;  // one CTA per sequence reports what concerns all of it
-  if (tid == 0) skip_s = 0;
-  __syncthreads();
   int rows, bits = 0;
   if (path) {
     rows = P.path_len[b] + 1;
     if (path[0] == -1) return;  // the verification's data-error marking
+    if (tid == 0) skip_s = 0;
+    __syncthreads();
     if (rows < 1 || rows > P.path_ld) bits |= SPEC_ERR_CACHE, rows = 0;
     bool bad = false;
-    for (int i = tid; i < rows; i += kAppendThreads) bad |= path[i] < 0 || path[i] >= P.n;
+    for (int i = tid; i < rows; i += TH) bad |= path[i] < 0 || path[i] >= P.n;
     if (bad) atomicOr(&skip_s, SPEC_ERR_PARENT);
+    __syncthreads();
+    bits |= skip_s;
   } else {
     rows = P.count ? P.count[b] : P.n;
     if (rows < 0 || rows > P.n) bits |= SPEC_ERR_CACHE;
   }
   if (prefix < 0 || static_cast<long long>(prefix) + rows > static_cast<long long>(P.table_pages) * P.page)
     bits |= SPEC_ERR_CACHE;
-  __syncthreads();
-  bits |= skip_s;
   if (bits) {
     if (reports && tid == 0) {
       if (P.seq_error) atomicOr(P.seq_error + b, bits);
@@ -123,16 +125,6 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   const int i0 = max(0, start - prefix), i1 = min(rows, start + P.page - prefix);
   if (i0 >= i1) return;
   const int page = P.block_table[static_cast<long long>(b) * P.table_pages + entry];
-  if (page < 0 || page >= P.pages) {
-    if (h == 0 && tid == 0) {
-      if (P.seq_error) atomicOr(P.seq_error + b, SPEC_ERR_CACHE);
-      if (P.error_word) atomicOr(P.error_word, SPEC_ERR_CACHE);
-    }
-    return;
-  }
-  const long long slab = static_cast<long long>(page) * P.H + h;
-  unsigned char* kc = P.k_codes + slab * P.page * P.D;
-  unsigned char* vc = P.v_codes + slab * P.page * P.D;
   const T* k = static_cast<const T*>(P.k) + b * P.k_ld[0] + h * P.k_ld[2];
   const T* v = static_cast<const T*>(P.v) + b * P.v_ld[0] + h * P.v_ld[2];
   const int work = (i1 - i0) * P.units;
@@ -147,18 +139,63 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
     }
     return m;
   };
-  for (int o = tid; o < work; o += kAppendThreads) {
-    const int i = i0 + o / P.units, u = o % P.units;
-    const long long r = path ? path[i] : i;
-    float x[V];
+  // a thread's units, TH apart, without a division for each
+  const int step_i = TH / P.units, step_u = TH % P.units;
+  const auto next = [&](int& i, int& u) {
+    i += step_i;
+    u += step_u;
+    if (u >= P.units) u -= P.units, ++i;
+  };
+  uint4 raw[kHold ? kHold : 1][4];
+  {
+    int i = i0 + tid / P.units, u = tid % P.units;
+    if constexpr (kHold > 0) {
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      load_elems<V>(k + r * P.k_ld[1] + (2 * u + half) * V, x);
-      mk = most(mk, x);
-      load_elems<V>(v + r * P.v_ld[1] + (2 * u + half) * V, x);
-      mv = most(mv, x);
+      for (int j = 0; j < kHold; ++j, next(i, u)) {
+        if (tid + j * TH >= work) break;
+        const long long r = path ? path[i] : i;
+        const UnitPlace w = unit_place<V>(u, P.rot, P.pairs);
+        raw[j][0] = __ldcs(reinterpret_cast<const uint4*>(k + r * P.k_ld[1] + w.a));
+        raw[j][1] = __ldcs(reinterpret_cast<const uint4*>(k + r * P.k_ld[1] + w.b));
+        raw[j][2] = __ldcs(reinterpret_cast<const uint4*>(v + r * P.v_ld[1] + 2 * u * V));
+        raw[j][3] = __ldcs(reinterpret_cast<const uint4*>(v + r * P.v_ld[1] + (2 * u + 1) * V));
+      }
+#pragma unroll
+      for (int j = 0; j < kHold; ++j) {
+        if (tid + j * TH >= work) break;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float x[V];
+          load_elems<V>(reinterpret_cast<const T*>(&raw[j][half]), x);
+          mk = most(mk, x);
+          load_elems<V>(reinterpret_cast<const T*>(&raw[j][2 + half]), x);
+          mv = most(mv, x);
+        }
+      }
+    } else {
+      for (int o = tid; o < work; o += TH, next(i, u)) {
+        const long long r = path ? path[i] : i;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float x[V];
+          load_elems<V>(k + r * P.k_ld[1] + (2 * u + half) * V, x);
+          mk = most(mk, x);
+          load_elems<V>(v + r * P.v_ld[1] + (2 * u + half) * V, x);
+          mv = most(mv, x);
+        }
+      }
     }
   }
+  if (page < 0 || page >= P.pages) {
+    if (h == 0 && tid == 0) {
+      if (P.seq_error) atomicOr(P.seq_error + b, SPEC_ERR_CACHE);
+      if (P.error_word) atomicOr(P.error_word, SPEC_ERR_CACHE);
+    }
+    return;
+  }
+  const long long slab = static_cast<long long>(page) * P.H + h;
+  unsigned char* kc = P.k_codes + slab * P.page * P.D;
+  unsigned char* vc = P.v_codes + slab * P.page * P.D;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
@@ -167,15 +204,15 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   if ((tid & 31) == 0) most_s[0][tid >> 5] = mk, most_s[1][tid >> 5] = mv;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kAppendThreads / 32; ++w) mk = fmaxf(mk, most_s[0][w]), mv = fmaxf(mv, most_s[1][w]);
+  for (int w = 0; w < TH / 32; ++w) mk = fmaxf(mk, most_s[0][w]), mv = fmaxf(mv, most_s[1][w]);
   int ek = exponent_of(mk), ev = exponent_of(mv);
   if (start < prefix) {
     const int ok = P.k_exps[slab], ov = P.v_exps[slab];
     ek = max(ek, ok);
     ev = max(ev, ov);
     const int bytes = (prefix - start) * P.D;
-    if (ek > ok) scale_codes(kc, bytes, ek - ok);
-    if (ev > ov) scale_codes(vc, bytes, ev - ov);
+    if (ek > ok) scale_codes<TH>(kc, bytes, ek - ok);
+    if (ev > ov) scale_codes<TH>(vc, bytes, ev - ov);
   }
   __syncthreads();
   if (tid == 0) {
@@ -186,14 +223,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   // the codes
   const float fk = exp2i(-ek), fv = exp2i(-ev);
   bool bad = false, outside = false;
-  for (int o = tid; o < work; o += kAppendThreads) {
-    const int i = i0 + o / P.units, u = o % P.units;
-    const long long r = path ? path[i] : i;
+  const auto put = [&](int i, int u, long long r, const UnitPlace& w, float* a, float* c, const float* x, const float* y) {
     const long long at = static_cast<long long>(prefix + i - start) * P.D;
-    const UnitPlace w = unit_place<V>(u, P.rot, P.pairs);
-    float a[V], c[V];
-    load_elems<V>(k + r * P.k_ld[1] + w.a, a);
-    load_elems<V>(k + r * P.k_ld[1] + w.b, c);
     if (w.rotated) {
       const int t = P.positions ? P.positions[static_cast<long long>(b) * P.n + r] : prefix + i;
       float cs[V], sn[V];
@@ -215,10 +246,32 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
       store_codes<V>(kc + at + w.a, a, fk, bad);
       store_codes<V>(kc + at + w.b, c, fk, bad);
     }
-    load_elems<V>(v + r * P.v_ld[1] + 2 * u * V, a);
-    load_elems<V>(v + r * P.v_ld[1] + (2 * u + 1) * V, c);
-    store_codes<V>(vc + at + 2 * u * V, a, fv, bad);
-    store_codes<V>(vc + at + (2 * u + 1) * V, c, fv, bad);
+    store_codes<V>(vc + at + 2 * u * V, x, fv, bad);
+    store_codes<V>(vc + at + (2 * u + 1) * V, y, fv, bad);
+  };
+  int i = i0 + tid / P.units, u = tid % P.units;
+  if constexpr (kHold > 0) {
+#pragma unroll
+    for (int j = 0; j < kHold; ++j, next(i, u)) {
+      if (tid + j * TH >= work) break;
+      float a[V], c[V], x[V], y[V];
+      load_elems<V>(reinterpret_cast<const T*>(&raw[j][0]), a);
+      load_elems<V>(reinterpret_cast<const T*>(&raw[j][1]), c);
+      load_elems<V>(reinterpret_cast<const T*>(&raw[j][2]), x);
+      load_elems<V>(reinterpret_cast<const T*>(&raw[j][3]), y);
+      put(i, u, path ? path[i] : i, unit_place<V>(u, P.rot, P.pairs), a, c, x, y);
+    }
+  } else {
+    for (int o = tid; o < work; o += TH, next(i, u)) {
+      const long long r = path ? path[i] : i;
+      const UnitPlace w = unit_place<V>(u, P.rot, P.pairs);
+      float a[V], c[V], x[V], y[V];
+      load_elems<V>(k + r * P.k_ld[1] + w.a, a);
+      load_elems<V>(k + r * P.k_ld[1] + w.b, c);
+      load_elems<V>(v + r * P.v_ld[1] + 2 * u * V, x);
+      load_elems<V>(v + r * P.v_ld[1] + (2 * u + 1) * V, y);
+      put(i, u, r, w, a, c, x, y);
+    }
   }
   if (bad || outside) {
     const int err = (bad ? SPEC_ERR_NONFINITE : 0) | (outside ? SPEC_ERR_POSITION : 0);
@@ -227,14 +280,34 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   }
 }
 
+template <typename T, int V>
+void launch_width(const AppendParams& p, dim3 grid, cudaStream_t s) {
+  if constexpr (V * sizeof(T) == 16) {
+    const int most = std::min(p.page, p.path_nodes ? p.path_ld : p.n) * p.units;  // a page's units, at most
+    if (most <= 256) {
+      append_kernel<T, V, 256, 1><<<grid, 256, 0, s>>>(p);
+      return;
+    }
+    if (most <= 512) {
+      append_kernel<T, V, 256, 2><<<grid, 256, 0, s>>>(p);
+      return;
+    }
+    if (most <= 2048) {
+      append_kernel<T, V, 512, 4><<<grid, 512, 0, s>>>(p);
+      return;
+    }
+  }
+  append_kernel<T, V, 256, 0><<<grid, 256, 0, s>>>(p);
+}
+
 template <typename T>
 void launch_append(const AppendParams& p, int v, dim3 grid, cudaStream_t s) {
   if (v == 8) {
-    if constexpr (sizeof(T) == 2) append_kernel<T, 8><<<grid, kAppendThreads, 0, s>>>(p);
+    if constexpr (sizeof(T) == 2) launch_width<T, 8>(p, grid, s);
   } else if (v == 4) {
-    append_kernel<T, 4><<<grid, kAppendThreads, 0, s>>>(p);
+    launch_width<T, 4>(p, grid, s);
   } else {
-    append_kernel<T, 1><<<grid, kAppendThreads, 0, s>>>(p);
+    launch_width<T, 1>(p, grid, s);
   }
 }
 

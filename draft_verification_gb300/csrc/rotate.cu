@@ -32,7 +32,8 @@ __global__ void __launch_bounds__(256)
 }
 
 struct RotateParams {
-  int n, H, D, rot, units, groups, table_rows;  // groups of kHeads heads
+  unsigned n, units;
+  int H, D, rot, groups, table_rows;  // groups of kHeads heads
   long long rows;                               // B * n
   bool pairs, transpose;
   long long x_ld[3], out_ld[3];
@@ -49,11 +50,14 @@ template <typename T, int V>
 __global__ void __launch_bounds__(kRotateThreads) rotate_kernel(const RotateParams P) {
   const long long at = static_cast<long long>(blockIdx.x) * kRotateThreads + threadIdx.x;
   const long long per_row = static_cast<long long>(P.units) * P.groups;
-  const long long row = at / per_row;
+  // (divisions of 64 bits would take as long as the rest)
+  const bool few = P.rows * per_row <= 0xffffffffLL;
+  const long long row = few ? static_cast<unsigned>(at) / static_cast<unsigned>(per_row) : at / per_row;
   if (row >= P.rows) return;
-  const int rest = static_cast<int>(at % per_row);
-  const int u = rest % P.units, h0 = rest / P.units * kHeads;
-  const int b = static_cast<int>(row / P.n), i = static_cast<int>(row % P.n);
+  const unsigned rest = static_cast<unsigned>(at - row * per_row);
+  const int u = static_cast<int>(rest % P.units), h0 = static_cast<int>(rest / P.units) * kHeads;
+  const int b = few ? static_cast<int>(static_cast<unsigned>(row) / P.n) : static_cast<int>(row / P.n);
+  const int i = static_cast<int>(row - static_cast<long long>(b) * P.n);
   const UnitPlace w = unit_place<V>(u, P.rot, P.pairs);
   float cs[V], sn[V];
   if (w.rotated) {
