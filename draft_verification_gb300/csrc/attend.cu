@@ -54,7 +54,10 @@ constexpr int kMaxCtas = 320;
 constexpr int kThreads = 512;
 constexpr int kMaskBytes = 10 * kMaxRows;  // of shared memory for a tree's masks, at most
 constexpr int kScaleRing = 32, kPatchRing = 8, kPieceRing = 4;
-constexpr int kFar = 9;    // value exponents of a step that lie further apart than this: 2^-9 is the least e4m3 code
+// Value exponents of a step that lie further apart than this: its weights are
+// summed apart.  Weights are held to 2^-18 of the step's largest, exponents
+// included, so their sum without them to 2^(kFar - 18) of the largest per token.
+constexpr int kFar = 3;
 
 // R: a block's rows; NP: panels of 128 elements of a head.
 template <int R, int NP>

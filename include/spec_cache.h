@@ -166,12 +166,14 @@ spec_status spec_append_cache(const spec_append_args* args, cudaStream_t stream)
 /* q bfloat16, out bfloat16.  Scores, maxima, weights, their sums and the   */
 /* output's sums are float32; a query enters the products as the sum of two */
 /* e4m3 numbers relative to its own largest element (exact to 2^-18 of that */
-/* element), a weight as the sum of two relative to the largest of its 128  */
-/* tokens (to 2^-8 of itself, or 2^-18 of that largest), codes as they are. */
+/* element), a weight times its page's 2^exponent as the sum of two relative */
+/* to the largest of up to 256 tokens around it (to 2^-8 of itself, or 2^-18 */
+/* of that largest), codes as they are.                                     */
 /*  - Rows i >= count[b] get zeros.                                         */
 /*  - A NaN code, or a NaN or infinite query element, makes NaN of the rows  */
-/*    that read it, and of no others.  Codes behind a sequence's last token */
-/*    are not used, whatever they hold.                                     */
+/*    that read it (a value's NaN of its element at least, a drafted token's */
+/*    of all elements), and of no others.  Codes behind a sequence's last   */
+/*    token are not used, whatever they hold.                               */
 /*  - A prefix_len < 0, a count outside [0, n] or tokens past the block     */
 /*    table set SPEC_ERR_CACHE: the sequence's rows are zeros.  A page       */
 /*    outside [0, pages) sets SPEC_ERR_CACHE: the rows that read it are NaN. */

@@ -206,9 +206,14 @@ def attend_cache(q, cache, block_table, prefix_len=None, count=None, parent=None
     dict of what an error bound is made of, error bits [B]):
 
       mass   sum_t w_t |v_t| / sum_t w_t, as out
-      floor  sum over tiles of `tile` tokens of the tile's largest w times the
-             sum of its |v|, over sum_t w_t, as out.  Weights here carry the
-             value exponent of their page in both sums, as the kernel's do
+      floor  sum over tiles of `tile` tokens of the largest w of the tile and
+             its two neighbours (weights are rounded relative to the largest of
+             one or two tiles next to each other) times the tile's sum of |v|,
+             over sum_t w_t, as out.  Weights here carry the value exponent of
+             their page in both sums, as the kernel's do
+      sums   the same for the sum of the weights: sum over tiles of the largest
+             w of the tile and its neighbours, without exponents, times the
+             tile's tokens, over sum_t w_t, [B, n, Hq]
       score  the largest |scale * q . k| term sum of a row: scale * max |q| *
              max_t sum |k|, [B, n, Hq]
     """
@@ -216,7 +221,8 @@ def attend_cache(q, cache, block_table, prefix_len=None, count=None, parent=None
     pages, H, page, _ = cache["k_codes"].shape
     scale = 1.0 / np.sqrt(D) if scale is None else scale
     out = np.zeros((B, n, Hq, D))
-    bound = dict(mass=np.zeros_like(out), floor=np.zeros_like(out), score=np.zeros((B, n, Hq)))
+    bound = dict(mass=np.zeros_like(out), floor=np.zeros_like(out), score=np.zeros((B, n, Hq)),
+                 sums=np.zeros((B, n, Hq)))
     err = np.zeros(B, np.int32)
     kv, vv = cache_values(cache["k_codes"], cache["k_exps"]), VALUES[cache["v_codes"]]
     ve = 2.0 ** cache["v_exps"].astype(np.float64)
@@ -250,9 +256,12 @@ def attend_cache(q, cache, block_table, prefix_len=None, count=None, parent=None
                         ws = w * s[seen]
                         out[b, i, g] = ws @ v[seen] / w.sum()
                         bound["mass"][b, i, g] = ws @ np.abs(v[seen]) / w.sum()
-                        for t0 in range(0, keys, tile):
-                            mine = (t[seen] >= t0) & (t[seen] < t0 + tile)
-                            if mine.any():
-                                bound["floor"][b, i, g] += ws[mine].max() * np.abs(v[seen][mine]).sum(0) / w.sum()
+                        mine = t[seen] // tile
+                        tops = np.zeros((2, keys // tile + 3))
+                        for m, y in enumerate((ws, w)):
+                            np.fmax.at(tops[m], mine + 1, y)
+                        tops = np.fmax(np.fmax(tops[:, :-2], tops[:, 1:-1]), tops[:, 2:])
+                        bound["floor"][b, i, g] = (tops[0][mine] @ np.abs(np.nan_to_num(v[seen]))) / w.sum()
+                        bound["sums"][b, i, g] = tops[1][mine].sum() / w.sum()
                     bound["score"][b, i, g] = scale * np.abs(q[b, i, g]).max() * np.abs(k[seen]).sum(1).max()
     return out, bound, err

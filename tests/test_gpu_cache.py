@@ -10,7 +10,9 @@ equality.  Attention, with u = finfo(type).eps / 2 the half step of a type
            `score` the largest sum of a row's terms' magnitudes;
   weights  off by e from their score, by 2^-8 from two e4m3 numbers after a
            step of float16 (2^-11), or by 2^-18 of the largest weight of their
-           128 tokens (`floor`); their float32 sum by e and a few u32 per tile;
+           one or two tiles (`floor`; both with their pages' value exponents);
+           their sum by e, a few u32 per tile, and the floor without the
+           exponents, which may lie 2^3 apart (`sums`);
   out      the weighted sum of magnitudes (`mass`) times both, and u16 of
            itself for its own rounding.
 """
@@ -289,8 +291,13 @@ def make_attend(rng, B, n, Hq, H, D, page, prefix, tree, spread=1.0):
 
 
 def attend_bound(out, bound, D):
+    # Scores: queries to 2^-18, D products and their scaling in float32.  Weights: e4m3 twice is 2^-4 * 2^-4 of
+    # themselves, and 2^-11 for the float16 on the way, or 2^-18 of the largest near them (2^-10 of 256: half a step
+    # of the least e4m3 codes), once more where float16's own rounding adds to it.  The sum of the weights is made of
+    # the same numbers, each divided by its value exponent: up to 2^3 times the floor.
     e = (bound["score"] * (2.0 ** -18 + (2 * D + 16) * U32))[..., None]
-    return bound["mass"] * (2.0 ** -8 + 2.0 ** -11 + 2 * e + 2.0 ** -17) + bound["floor"] * 2.0 ** -17 + np.abs(out) * U16
+    return (bound["mass"] * (2.0 ** -8 + 2.0 ** -11 + 2 * e + 2.0 ** -17) + bound["floor"] * 2.0 ** -17 +
+            np.abs(out) * (U16 + bound["sums"][..., None] * 2.0 ** -15))
 
 
 def check_attend(w, got, rows=None, **kw):
@@ -327,6 +334,13 @@ ATTENDS = [
     (9, 2, 48, 48, 64, 16, (700, 1, 64, 900, 333, 511, 513, 127, 128), True, "plain"),
     (6, 20, 32, 32, 128, 128, (1500, 300, 1301, 1, 1000, 640), True, "plain"),
     (4, 2, 64, 16, 256, 64, (1500, 777, 1301, 900), False, "plain"),
+    # each size of a block, with rows of its own number and with fewer
+    (2, 12, 4, 1, 128, 64, (1030, 257), True, "plain"), (2, 47, 1, 1, 64, 16, (250, 255), True, "fused"),
+    (1, 16, 4, 1, 128, 32, (900,), False, "plain"), (2, 3, 7, 1, 128, 16, (515, 260), True, "heads"),
+    (2, 5, 3, 1, 112, 128, (1000, 128), False, "plain"), (2, 4, 8, 1, 176, 64, (500, 3), True, "plain"),
+    (3, 2, 8, 1, 256, 128, (129, 640, 2), False, "fused"), (2, 1, 8, 1, 96, 64, (2048, 1023), False, "plain"),
+    # long trees
+    (1, 513, 2, 1, 64, 64, (65,), True, "fused"), (1, 1024, 1, 1, 32, 128, (300,), True, "plain"),
 ]
 
 
@@ -340,6 +354,44 @@ def test_attend(cuda_device, B, n, Hq, H, D, page, prefix, tree, layout):
     count[-1] = n
     got = run_attend(w, layout, count=count, scale=0.3)
     check_attend(w, got, count=count, scale=0.3)
+
+
+@pytest.mark.parametrize("n,G", [(2, 4), (6, 4), (8, 4), (12, 4), (16, 4)])
+@pytest.mark.parametrize("tree", [False, True])
+def test_attend_counts(cuda_device, n, G, tree):
+    """Sequences of every count of rows, some without a token, between long ones."""
+    rng = np.random.default_rng(n)
+    prefix = (0, 400, 0, 128, 1, 0, 255, 0, 640, 0)
+    w = make_attend(rng, len(prefix), n, 2 * G, 2, 128, 64, prefix, tree)
+    count = np.array([0, n, 0, 1, n - 1, 0, 0, n, 2, 1], np.int32)
+    check_attend(w, run_attend(w, count=count), count=count)
+
+
+@pytest.mark.parametrize("n,G,D", [(2, 4, 128), (6, 4, 128), (8, 4, 64), (12, 4, 128), (16, 4, 80), (3, 4, 256)])
+@pytest.mark.parametrize("apart", [3, 4, 40])
+def test_attend_value_exponents_apart(cuda_device, n, G, D, apart):
+    """Pages whose value exponents lie near one another, or too far for one sum, over several steps."""
+    rng = np.random.default_rng(100 * n + apart)
+    w = make_attend(rng, 3, n, 2 * G, 2, D, 32, (1100, 515, 31), True)
+    w["c"]["v_exps"] = (rng.integers(0, 2, w["c"]["v_exps"].shape) * apart - apart // 2).astype(np.int8)
+    check_attend(w, run_attend(w))
+
+
+@pytest.mark.parametrize("n,G", [(2, 4), (6, 4), (8, 4), (12, 4), (16, 4)])
+def test_attend_nan_of_drafted_tokens(cuda_device, n, G):
+    """NaN values of drafted tokens, over the end of a tile, reach the rows that see them and no others."""
+    rng = np.random.default_rng(n)
+    w = make_attend(rng, 2, n, 2 * G, 2, 128, 16, (255, 510), True)
+    for b, past in enumerate((255, 510)):
+        for j in (n - 1, n // 2):
+            at = past + j
+            w["c"]["v_codes"][w["table"][b, at // 16], 1, at % 16, 5] = 0x7F
+    got = run_attend(w)
+    want, bound, _ = O.attend_cache(w["q"], w["c"], w["table"], w["prefix"], parent=w["parent"])
+    y, hit = got["out"].double().cpu().numpy(), np.isnan(want).any(3)
+    # (a drafted token's NaN takes all elements of the rows that read it)
+    assert np.array_equal(np.isnan(y).any(3), hit) and np.isnan(y[hit][:, 5]).all() and hit.any() and not hit.all()
+    assert (np.abs(y - want)[~hit] <= attend_bound(want, bound, 128)[~hit]).all()
 
 
 @pytest.mark.parametrize("spread", [0.0, 1e-3, 30.0])
