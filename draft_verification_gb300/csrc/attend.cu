@@ -1,8 +1,8 @@
 // Attention of drafted rows over the paged 8-bit cache (spec_attend_cache).
 //
 // The rows of one sequence that read one head of the cache, n rows of Hq / H
-// query heads each, are cut into blocks of R (16, 32 or 64).  For a tile of
-// 128 tokens a block needs
+// query heads each, are cut into blocks of R (8 to 64).  For a tile of 128
+// tokens a block needs
 //    S^T [128 tokens x R] = K [128 x D] Q^T,   O^T [D x R] = V^T [D x 128] P^T,
 // P = 2^(scores - maximum): tokens, then elements, are the 128 rows of a
 // tensor-core product and the block's rows its N columns, so that few rows
@@ -10,26 +10,36 @@
 // lie in memory (tcgen05.mma kind::f8f6f4), K with D and V with the tokens as
 // the inner products' axis; nothing is unpacked.  The other operands keep
 // their precision as sums of two e4m3 numbers x = hi + lo, lo = e4m3(x - hi),
-// two products into the same accumulators:
+// side by side as rows of one product:
 //    a query relative to its largest element (bfloat16's 8 significant bits
 //       are the two's, so it is exact down to 2^-18 of that element);
-//    a weight relative to the largest of its tile and row, hence from 256
-//       down to 2^-9 / 2: rows whose first tokens have nearly all the weight
-//       keep the others' precision.
+//    a weight relative to the largest of its step (one or two tiles) and row,
+//       hence from 256 down to 2^-9 / 2: rows whose first tokens have nearly
+//       all the weight keep the others' precision.
 // A page's exponents are 2's powers and uniform over a token: one factor per
 // thread for K; V's exponent is added to the score before the maximum, so that
-// P carries it (y = x + ve), and the sum of the weights takes it back.
+// P carries it (y = x + ve).  The sum of the weights is a third product, of P
+// with one row of factors 2^(least ve - ve) that take it back; where a step's
+// exponents lie far apart the weights' warps sum 2^x themselves.
 //
-// One persistent CTA per SM takes an equal run of the tiles of all blocks,
-// in the order sequence, head, block; a block that two CTAs share is left in
-// parts in the workspace and joined by a second kernel (in order, so that the
-// sums do not depend on the timing).  Warps: 0 copies pages (TMA, 128-byte
-// swizzle) into rings of K and V tiles; 1 issues the products; 2 and 3 bring
-// in queries, tree masks and clear what lies behind the last token; 4-7 and
-// 8-11 turn the scores of every other tile into weights; 12-15 add the tiles'
-// outputs up in registers.
+// Persistent CTAs, two per SM up to 24 rows, take equal runs of the tiles of
+// all blocks, in the order sequence, head, block; a block that CTAs share is
+// left in parts in the workspace and joined by a second kernel (in order, so
+// that the sums do not depend on the timing).  Warps: 0 copies pages (TMA,
+// 128-byte swizzle) into rings of K and V tiles; 1 issues the scores' products;
+// 2 finds the pieces of the CTA's run and makes their queries' codes and tree
+// masks; 3 issues the outputs' products; 4-7 and 8-11 turn the scores of every
+// other step into weights (and clear V behind the last token); 12-15 add the
+// steps' outputs up in registers.  All waits are bounded, and the warps of a
+// role leave it together.
 //
-// Bound by the bytes of the cache for a few rows.
+// What bounds it: up to 32 rows the bytes (1.07 GB of cache, 8 heads of 128,
+// 4 query heads each: 2 rows 168 us, 95 % of a copy's rate; 6 rows 183, 88 %;
+// 8 rows 196, 82 %), above that the instructions of the weights' warps (12
+// rows, blocks of 48: 245 us, 66 %; 16, blocks of 64: 277, 58 %): some 18 per
+// score, at a third of the issue slots.  Short calls are latency: one piece
+// takes about 14,000 cycles from launch to the end, a third of it until the
+// lengths, the block table and the queries have come.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -418,6 +428,7 @@ __global__ void __launch_bounds__(kThreads, Shape<R, NP>::kCtas)
     uint64_t* at = reinterpret_cast<uint64_t*>(&bar) + tid;
     unsigned count = 1;
     if (at >= bar.sfull && at < bar.sempty) count = 2;   // sfull
+    if (at >= bar.ofull && at < bar.oempty) count = 2;   // ofull
     if (at >= bar.sempty && at < bar.pempty) count = 4;  // sempty, pfull
     if (at >= bar.oempty && at < bar.mfull) count = 4;   // oempty
     if (at >= bar.mempty && at < bar.qfull) count = 4;   // mempty
@@ -873,6 +884,7 @@ __global__ void __launch_bounds__(kThreads, Shape<R, NP>::kCtas)
         commit_if(issues, &bar.vempty[at.slot]);
         if (sub == S::kSubs - 1 || t + 1 == w.t1) {
           commit_if(issues, &bar.ofull[k]);
+          if (leader) mbar_arrive(&bar.ofull[k]);  // what the weights' warps wrote is visible behind it
           commit_if(issues, &bar.pempty[k]);
           ++step;
         }
@@ -1345,11 +1357,23 @@ bool good_shape(int B, int n, int Hq, int H, int D) {
          D >= 16 && D <= 256 && D % 16 == 0;
 }
 
+// The rows of a block: those that need the least time per tile of 128 tokens,
+// blocks times what a tile took with so many rows (ns per SM, 1.07 GB of cache,
+// 4 query heads per head, 128 elements; the bytes alone take 740).  For 2 x 36
+// rows two blocks of 48 so take 1130 each, two of 64 would take 1290.
 int block_rows(int n, int G, int D) {
   const int rows = n * G;
-  // (of trees of more than 512 nodes the masks of 64 rows do not fit)
-  if (D > 128) return rows <= 16 ? 16 : 32;
-  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 24 ? 24 : rows <= 32 || n > 512 ? 32 : rows <= 48 ? 48 : 64;
+  if (D > 128) return rows <= 16 ? 16 : 32;  // (registers and tensor memory hold no more)
+  static constexpr int kRows[6] = {8, 16, 24, 32, 48, 64}, kTime[6] = {780, 820, 850, 910, 1130, 1290};
+  int best = 0;
+  long long least = 0;
+  // (of trees of more than 512 nodes the masks of 64 bits do not fit)
+  for (int i = 0; i < (n > 512 ? 4 : 6); ++i) {
+    const long long time = static_cast<long long>((rows + kRows[i] - 1) / kRows[i]) * kTime[i];
+    if (i == 0 || time <= least) least = time, best = i;
+    if (rows <= kRows[i]) break;
+  }
+  return kRows[best];
 }
 
 size_t attend_workspace(int n, int Hq, int H, int D) {
