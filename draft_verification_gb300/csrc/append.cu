@@ -206,6 +206,28 @@ __global__ void __launch_bounds__(TH, kHold == 1 || kHold == 2 ? 3 : 1) append_k
   const long long slab = static_cast<long long>(page) * P.H + h;
   unsigned char* kc = P.k_codes + slab * P.page * P.D;
   unsigned char* vc = P.v_codes + slab * P.page * P.D;
+  // (what is needed behind the barrier is on its way before it)
+  const bool older = start < prefix;
+  const int ok = older ? P.k_exps[slab] : kLowExp, ov = older ? P.v_exps[slab] : kLowExp;
+  const auto turn = [&](int i, int u, long long r, float* cs, float* sn) {
+    const int t = P.positions ? P.positions[static_cast<long long>(b) * P.n + r] : prefix + i;
+    if (t >= 0 && t < P.table_rows) {
+      const float* src = P.table + static_cast<long long>(t) * P.rot + u * V;
+      load_elems<V>(src, cs);
+      load_elems<V>(src + P.rot / 2, sn);
+      return true;
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) cs[e] = sn[e] = __uint_as_float(0x7fc00000u);
+    return false;
+  };
+  float turn_c[V], turn_s[V];
+  bool turn_inside = false;
+  if constexpr (kHold == 1) {
+    const int i = i0 + tid / P.units, u = tid % P.units;
+    if (tid < work && unit_place<V>(u, P.rot, P.pairs).rotated)
+      turn_inside = turn(i, u, path ? path[i] : i, turn_c, turn_s);
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
@@ -216,8 +238,7 @@ __global__ void __launch_bounds__(TH, kHold == 1 || kHold == 2 ? 3 : 1) append_k
 #pragma unroll
   for (int w = 0; w < TH / 32; ++w) mk = fmaxf(mk, most_s[0][w]), mv = fmaxf(mv, most_s[1][w]);
   int ek = exponent_of(mk), ev = exponent_of(mv);
-  if (start < prefix) {
-    const int ok = P.k_exps[slab], ov = P.v_exps[slab];
+  if (older) {
     ek = max(ek, ok);
     ev = max(ev, ov);
     const int bytes = (prefix - start) * P.D;
@@ -236,22 +257,21 @@ __global__ void __launch_bounds__(TH, kHold == 1 || kHold == 2 ? 3 : 1) append_k
   const auto put = [&](int i, int u, long long r, const UnitPlace& w, float* a, float* c, const float* x, const float* y) {
     const long long at = static_cast<long long>(prefix + i - start) * P.D;
     if (w.rotated) {
-      const int t = P.positions ? P.positions[static_cast<long long>(b) * P.n + r] : prefix + i;
+      bool inside;
       float cs[V], sn[V];
-      if (t >= 0 && t < P.table_rows) {
-        const float* src = P.table + static_cast<long long>(t) * P.rot + u * V;
-        load_elems<V>(src, cs);
-        load_elems<V>(src + P.rot / 2, sn);
-      } else {
-        outside = true;
+      if constexpr (kHold == 1) {
+        inside = turn_inside;
 #pragma unroll
-        for (int e = 0; e < V; ++e) cs[e] = sn[e] = __uint_as_float(0x7fc00000u);
+        for (int e = 0; e < V; ++e) cs[e] = turn_c[e], sn[e] = turn_s[e];
+      } else {
+        inside = turn(i, u, r, cs, sn);
       }
+      outside |= !inside;
       rotate_unit<V>(a, c, cs, sn, P.pairs);
       bool hit = false;
       store_codes<V>(kc + at + w.a, a, fk, hit);
       store_codes<V>(kc + at + w.b, c, fk, hit);
-      bad |= hit && t >= 0 && t < P.table_rows;
+      bad |= hit && inside;
     } else {
       store_codes<V>(kc + at + w.a, a, fk, bad);
       store_codes<V>(kc + at + w.b, c, fk, bad);

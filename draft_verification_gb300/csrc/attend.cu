@@ -1307,16 +1307,19 @@ __global__ void __launch_bounds__(128) join_kernel(const AttendParams P) {
   const auto part = [&](int i) {
     return P.parts + (static_cast<long long>(2 * (blockIdx.x + i)) + (i == 0 ? 1 : 0)) * R * kLd + r * kLd;
   };
-  float unit = -kInf, sum_unit = -kInf, sum = 0.f;
-  for (int i = lane; i < it.w; i += 32) {
-    const float4 x = __ldcg(reinterpret_cast<const float4*>(part(i) + NP * 128));
+  // (the first 32 parts' sums are read once)
+  const auto sums = [&](int i) { return __ldcg(reinterpret_cast<const float4*>(part(i) + NP * 128)); };
+  const float4 own = lane < it.w ? sums(lane) : make_float4(-kInf, 0.f, -kInf, 0.f);
+  float unit = own.x, sum_unit = own.z, sum = 0.f;
+  for (int i = lane + 32; i < it.w; i += 32) {
+    const float4 x = sums(i);
     unit = fmaxf(unit, x.x);
     sum_unit = fmaxf(sum_unit, x.z);
   }
   unit = warp_max(unit);
   sum_unit = warp_max(sum_unit);
   for (int i = lane; i < it.w; i += 32) {
-    const float4 x = __ldcg(reinterpret_cast<const float4*>(part(i) + NP * 128));
+    const float4 x = i == lane ? own : sums(i);
     factors[i] = x.x == -kInf ? 0.f : ex2(x.x - unit);
     sum += x.z == -kInf ? x.y : x.y * ex2(x.z - sum_unit);
   }
