@@ -8,11 +8,12 @@
 // bf16, 4 for those of fp32), loaded before the block table's answer is
 // there.  Larger pages, and rows that start anywhere, are read twice.
 //
-// Bound by memory, 2 x (element + code) bytes per row, head and element, and
-// by what a CTA waits for one after another: its lengths, its rows, the
-// rotation's rows, an older page's exponent.  4 x 8191 rows of 8 heads of 128,
-// bf16: 55 us, 3.7 TB/s, 0.56 of a copy's rate; read twice, by 256 threads
-// with more registers to spare, 62 us; with four units for every page 70 us
+// Bound by memory, 2 x (element + code) bytes per row, head and element, by
+// instructions and by what a CTA waits for one after another: its lengths, its
+// rows, the rotation's rows, an older page's exponent.  4 x 8191 rows of 8
+// heads of 128, bf16: 48 us, 4.3 TB/s, 0.64 of a copy's rate; with a test of
+// the range per element instead of per vector 53, with three CTAs per SM
+// instead of four 50, read twice 62, with room for four units in every page 70
 // (fewer CTAs per SM).  A drafted chain (64 x 6 rows) takes 16 us, nearly all
 // of it launch and latency.
 #include <algorithm>
@@ -48,17 +49,29 @@ struct AppendParams {
   int* error_word;
 };
 
-// V float32 values, already scaled, to codes; what e4m3 does not reach becomes NaN (and `bad`).
+// The larger magnitude, with some sign; NaN if one is.
+__device__ __forceinline__ float larger(float a, float b) {
+  float m;
+  asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+
+// V float32 values times `scale` to codes; what e4m3 does not reach becomes NaN
+// (and `bad`).  One test for all of them: it is instructions that a long call
+// waits for.
 template <int V>
 __device__ __forceinline__ void store_codes(unsigned char* p, const float* x, float scale, bool& bad) {
-  float y[V];
+  float y[V], m = 0.f;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     y[i] = x[i] * scale;
-    if (!(fabsf(y[i]) <= 448.f)) {
-      y[i] = __uint_as_float(0x7fc00000u);
-      bad = true;
-    }
+    m = larger(m, y[i]);
+  }
+  if (!(fabsf(m) <= 448.f)) {
+    bad = true;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (!(fabsf(y[i]) <= 448.f)) y[i] = __uint_as_float(0x7fc00000u);
   }
   if constexpr (V == 8) {
     *reinterpret_cast<uint2*>(p) =
@@ -98,7 +111,7 @@ __device__ __forceinline__ int exponent_of(float m) {
 // TH threads; kHold: units of a page's rows that a thread keeps in registers
 // between the two passes, 0: none (they are read twice)
 template <typename T, int V, int TH, int kHold>
-__global__ void __launch_bounds__(TH, kHold == 1 || kHold == 2 ? 3 : 1) append_kernel(const AppendParams P) {
+__global__ void __launch_bounds__(TH, kHold == 2 ? 4 : kHold == 1 ? 3 : 1) append_kernel(const AppendParams P) {
   __shared__ float most_s[2][TH / 32];
   __shared__ int skip_s;
   const int b = blockIdx.z, h = blockIdx.y, tid = threadIdx.x;
@@ -170,16 +183,49 @@ __global__ void __launch_bounds__(TH, kHold == 1 || kHold == 2 ? 3 : 1) append_k
         raw[j][2] = __ldcs(reinterpret_cast<const uint4*>(v + r * P.v_ld[1] + 2 * u * V));
         raw[j][3] = __ldcs(reinterpret_cast<const uint4*>(v + r * P.v_ld[1] + (2 * u + 1) * V));
       }
+      // (all magnitudes first; infinities and NaN are set aside only where there are some)
+      if constexpr (sizeof(T) == 2) {
+        uint32_t m[2] = {0u, 0u};
 #pragma unroll
-      for (int j = 0; j < kHold; ++j) {
-        if (tid + j * TH >= work) break;
+        for (int j = 0; j < kHold; ++j) {
+          if (tid + j * TH >= work) break;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float x[V];
-          load_elems<V>(reinterpret_cast<const T*>(&raw[j][half]), x);
-          mk = most(mk, x);
-          load_elems<V>(reinterpret_cast<const T*>(&raw[j][2 + half]), x);
-          mv = most(mv, x);
+          for (int e = 0; e < 4; ++e) {
+            const uint4& w = raw[j][e];
+            const uint32_t s = 0x7fff7fffu;
+            m[e >> 1] = __vmaxu2(m[e >> 1], __vmaxu2(__vmaxu2(w.x & s, w.y & s), __vmaxu2(w.z & s, w.w & s)));
+          }
+        }
+        mk = __uint_as_float(max(m[0] & 0xffffu, m[0] >> 16) << 16);
+        mv = __uint_as_float(max(m[1] & 0xffffu, m[1] >> 16) << 16);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kHold; ++j) {
+          if (tid + j * TH >= work) break;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint4& w = raw[j][e];
+            float& m = e < 2 ? mk : mv;
+            m = larger(larger(larger(m, __uint_as_float(w.x)), __uint_as_float(w.y)),
+                       larger(__uint_as_float(w.z), __uint_as_float(w.w)));
+          }
+        }
+        mk = fabsf(mk);
+        mv = fabsf(mv);
+      }
+      if (!(mk < kInf) || !(mv < kInf)) {
+        mk = mv = 0.f;
+#pragma unroll
+        for (int j = 0; j < kHold; ++j) {
+          if (tid + j * TH >= work) break;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            float x[V];
+            load_elems<V>(reinterpret_cast<const T*>(&raw[j][half]), x);
+            mk = most(mk, x);
+            load_elems<V>(reinterpret_cast<const T*>(&raw[j][2 + half]), x);
+            mv = most(mv, x);
+          }
         }
       }
     } else {
