@@ -261,24 +261,6 @@ __device__ __forceinline__ float warp_max(float x) {
   return m;
 }
 
-// The warp's sums of N columns (N a power of two): lane i gets column i % N's.
-template <int N>
-__device__ __forceinline__ float column_sums(float* v, int lane) {
-#pragma unroll
-  for (int o = N / 2; o > 0; o >>= 1) {
-    const bool up = (lane & o) != 0;
-#pragma unroll
-    for (int j = 0; j < o; ++j) {
-      const float give = up ? v[j] : v[j + o], keep = up ? v[j + o] : v[j];
-      v[j] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-    }
-  }
-  float s = v[0];
-#pragma unroll
-  for (int o = N; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
-}
-
 // Four values as hi + lo, four e4m3 codes each.
 __device__ __forceinline__ void split4(float a, float b, float c, float d, uint32_t& hi, uint32_t& lo) {
   asm("{\n .reg .b32 x, y, u, v;\n .reg .b16 p, q, r, s;\n"

@@ -171,9 +171,9 @@ spec_status spec_append_cache(const spec_append_args* args, cudaStream_t stream)
 /* of that largest), codes as they are.                                     */
 /*  - Rows i >= count[b] get zeros.                                         */
 /*  - A NaN code, or a NaN or infinite query element, makes NaN of the rows  */
-/*    that read it (a value's NaN of its element at least, a drafted token's */
-/*    of all elements), and of no others.  Codes behind a sequence's last   */
-/*    token are not used, whatever they hold.                               */
+/*    that read it (a value's NaN of its element of them at least), and of  */
+/*    no others.  Codes behind a sequence's last token are not used,        */
+/*    whatever they hold.                                                   */
 /*  - A prefix_len < 0, a count outside [0, n] or tokens past the block     */
 /*    table set SPEC_ERR_CACHE: the sequence's rows are zeros.  A page       */
 /*    outside [0, pages) sets SPEC_ERR_CACHE: the rows that read it are NaN. */

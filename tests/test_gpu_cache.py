@@ -389,7 +389,7 @@ def test_attend_nan_of_drafted_tokens(cuda_device, n, G):
     got = run_attend(w)
     want, bound, _ = O.attend_cache(w["q"], w["c"], w["table"], w["prefix"], parent=w["parent"])
     y, hit = got["out"].double().cpu().numpy(), np.isnan(want).any(3)
-    # (a drafted token's NaN takes all elements of the rows that read it)
+    # (a drafted token's NaN may take all elements of the rows that read it)
     assert np.array_equal(np.isnan(y).any(3), hit) and np.isnan(y[hit][:, 5]).all() and hit.any() and not hit.all()
     assert (np.abs(y - want)[~hit] <= attend_bound(want, bound, 128)[~hit]).all()
 
