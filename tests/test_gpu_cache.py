@@ -260,6 +260,29 @@ def test_append_data_errors(cuda_device):
     assert out["error_word"].tolist() == [E.ERR_NONFINITE | E.ERR_CACHE | E.ERR_POSITION]
 
 
+@pytest.mark.parametrize("page,D,n,dtype", [
+    (16, 32, 20, "bf16"), (64, 128, 100, "bf16"), (128, 256, 140, "bf16"), (64, 64, 70, "f32"), (128, 128, 130, "f32"),
+    (128, 256, 128, "f32"), (32, 48, 40, "bf16"),
+])
+def test_append_non_finite_rows(cuda_device, page, D, n, dtype):
+    """NaN and infinities beside finite rows, in pages of every size: the finite ones alone make the exponent."""
+    rng = np.random.default_rng(page + D)
+    B, H = 3, 2
+    k, v = (rounded(rng.normal(0, 1, (B, n, H, D)) * 2.0 ** rng.integers(-20, 20, (B, 1, H, 1)), dtype) for _ in range(2))
+    k[0, n // 2, 0, D - 1], k[0, 1, 1, 3], v[1, n - 1, 1, 0], v[1, 0, 0, D // 2] = np.nan, -np.inf, np.inf, np.nan
+    prefix = np.array([3, page - 1, 0], np.int32)
+    width = (page - 1 + n) // page + 1
+    table = rng.permutation(B * width).reshape(B, width).astype(np.int32)
+    turns = O.rotation_table(page + n, rng.random(8))
+    c = make_cache(rng, B * width, H, page, D)
+    want, err = O.append_cache(k, v, c, table, prefix, turns)
+    assert list(err) == [dv.ERR_NONFINITE, dv.ERR_NONFINITE, 0]
+    got = on_gpu(c)
+    out = dv.append_cache(dev(k).to(DTYPES[dtype]), dev(v).to(DTYPES[dtype]), got, dev(table), dev(prefix), table=dev(turns))
+    check_cache(got, want)
+    assert np.array_equal(out["seq_error"].cpu().numpy(), err)
+
+
 # ---------------------------------------------------------------------------
 # attention
 # ---------------------------------------------------------------------------
