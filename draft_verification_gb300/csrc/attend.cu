@@ -72,8 +72,13 @@ constexpr int kFar = 3;
 // R: a block's rows; NP: panels of 128 elements of a head.
 template <int R, int NP>
 struct Shape {
-  static constexpr int kCtas = NP == 1 && R <= 24 ? 2 : 1;  // per SM
-  static constexpr int kSubs = NP == 1 && R >= 32 ? 2 : 1;  // tiles of a step
+  // CTAs per SM: two, whose roles fill each other's waits, as long as registers
+  // (64 a thread) and memories hold them (64 chains of 6 rows of 4 heads, 24 rows:
+  // 190 us, one per SM 225).  Tiles of a step: two share a maximum, a meeting and
+  // their hand-overs (36 rows, 2 x 131072 tokens: 187 us, of one tile 192; with
+  // 24 rows, one CTA per SM, two tiles took 241 us, one 225).
+  static constexpr int kCtas = NP == 1 && R <= 24 ? 2 : 1;
+  static constexpr int kSubs = NP == 1 && R >= 32 ? 2 : 1;
   // An operand from shared memory costs its bytes (a product of 128 x 32 with 32
   // rows some 60 cycles, with 64 hardly more), so K and V are taken once for hi
   // and lo: as rows of their own, whose results are added later.  Where tensor
