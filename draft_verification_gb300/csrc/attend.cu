@@ -1024,20 +1024,6 @@ __global__ void __launch_bounds__(kThreads, Shape<R, NP>::kCtas)
             __syncwarp();
             if (leader && c + kCut == R) mbar_arrive(&bar.mfull[turn]);
           }
-          if (far) {
-            // The values' exponents lie too far apart for the factors: the sums of
-            // the weights 2^x themselves, each warp's with its own largest as unit
-#pragma unroll
-            for (int r = 0; r < kCut; ++r) {
-              const float x0 = (r & 1 ? second_of(y0[r / 2]) : first_of(y0[r / 2])) - ps0.ve;
-              const float x1 = (r & 1 ? second_of(y1[r / 2]) : first_of(y1[r / 2])) - ps1.ve;
-              const float unit = warp_max(fmaxf(x0, x1)), ref = unit == -kInf ? 0.f : unit;
-              float sum = ex2(x0 - ref) + ex2(x1 - ref);
-#pragma unroll
-              for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-              if (lane == 0) __stcg(far_sums + (4 * (step & 3) + q) * 64 + c + r, make_float2(sum, unit));
-            }
-          }
           if (c == 0) {
             ok = at_wait(&bar.pempty[turn], half ^ 1u, fault) && ok;
             const auto code = [&](float ve) {  // of 2^(low - ve), in [2^-9, 1]
@@ -1047,6 +1033,23 @@ __global__ void __launch_bounds__(kThreads, Shape<R, NP>::kCtas)
             if (!far) {
               ones[S::kSubs * turn * S::kOnes + row] = code(ps0.ve);
               if (S::kSubs == 2) ones[(S::kSubs * turn + 1) * S::kOnes + row] = code(ps1.ve);
+            }
+          }
+          if (far) {
+            // The values' exponents lie too far apart for the factors: the sums of
+            // the weights 2^x themselves, each warp's with its own largest as unit.
+            // (Behind the wait for pempty: the products of step - 2 are done, so
+            // they were begun, behind oempty of step - 4, whose sums lay in this
+            // place: they have been read.)
+#pragma unroll
+            for (int r = 0; r < kCut; ++r) {
+              const float x0 = (r & 1 ? second_of(y0[r / 2]) : first_of(y0[r / 2])) - ps0.ve;
+              const float x1 = (r & 1 ? second_of(y1[r / 2]) : first_of(y1[r / 2])) - ps1.ve;
+              const float unit = warp_max(fmaxf(x0, x1)), ref = unit == -kInf ? 0.f : unit;
+              float sum = ex2(x0 - ref) + ex2(x1 - ref);
+#pragma unroll
+              for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+              if (lane == 0) __stcg(far_sums + (4 * (step & 3) + q) * 64 + c + r, make_float2(sum, unit));
             }
           }
           const auto store = [&](int sub, const F2* y) {
