@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, Shape<R, NP>::kCtas)
         }
         PageScale x;
         x.ck = bad ? __uint_as_float(0x7fc00000u) : exp2i(ke);
-        x.ve = static_cast<float>(ve);
+        x.ve = static_cast<float>(has ? ve : lo);  // (behind the last page: one that is there)
         x.ve_low = static_cast<float>(lo);
         x.ve_high = static_cast<float>(hi);
         const int y = has ? static_cast<int>(slab * P.page) : -1;
@@ -1026,11 +1026,11 @@ __global__ void __launch_bounds__(kThreads, Shape<R, NP>::kCtas)
           }
           if (c == 0) {
             ok = at_wait(&bar.pempty[turn], half ^ 1u, fault) && ok;
-            const auto code = [&](float ve) {  // of 2^(low - ve), in [2^-9, 1]
-              const int e = static_cast<int>(low - ve);
-              return static_cast<unsigned char>(e >= -6 ? (e + 7) << 3 : 1 << (e + 9));
-            };
             if (!far) {
+              static_assert(kFar <= 6, "normal e4m3 numbers");
+              const auto code = [&](float ve) {  // of 2^(low - ve), in [2^-kFar, 1]
+                return static_cast<unsigned char>((static_cast<int>(low - ve) + 7) << 3);
+              };
               ones[S::kSubs * turn * S::kOnes + row] = code(ps0.ve);
               if (S::kSubs == 2) ones[(S::kSubs * turn + 1) * S::kOnes + row] = code(ps1.ve);
             }

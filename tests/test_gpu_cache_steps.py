@@ -117,3 +117,14 @@ def test_attend_many_steps(cuda_device, n, G, D, tree, apart):
     for _ in range(20):
         assert torch.equal(plan.run()["out"], first)
     assert not plan.out["error_word"].any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,G,D", [(2, 4, 128), (4, 4, 128), (6, 4, 128), (8, 4, 64), (12, 4, 128), (16, 4, 80), (3, 4, 256)])
+@pytest.mark.parametrize("exponents", [(100, 98), (60, 60), (-58, -60), (-100, -99)])
+def test_attend_tiles_without_all_their_pages(cuda_device, n, G, D, exponents):
+    """Tiles that end after one page and more, of values whose exponents are all far from 0."""
+    rng = np.random.default_rng(n + 1000 + exponents[0])
+    w = T.make_attend(rng, 4, n, G, 1, D, 16, (250, 128, 3, 391), False)
+    w["c"]["v_exps"] = rng.choice(np.array(exponents, np.int8), w["c"]["v_exps"].shape)
+    T.check_attend(w, T.run_attend(w))
