@@ -156,10 +156,28 @@ def _heads(t, name, dtypes=None):
 
 def _own_rows(t, name):
     """A tensor that is written: no two of its elements in one place."""
-    at = sorted((s, n) for s, n in zip(t.stride(), t.shape) if n > 1)
-    for i, (s, n) in enumerate(at):
-        if s < (1 if i == 0 else (at[i - 1][1] - 1) * at[i - 1][0] + 1):
-            raise ValueError(f"{name}: elements overlap")
+    axes = sorted((s, n) for s, n in zip(t.stride(), t.shape) if n > 1)
+    extent = 1  # of the axes so far: from the first of their places to the last
+    for s, n in axes:
+        if s < extent:
+            break
+        extent += (n - 1) * s
+    else:
+        return  # (each axis steps over all that the smaller ones reach)
+
+    def meets(i, at, moved):
+        """Whether steps along axes 0 .. i, not all of no length, lead from `at` to 0."""
+        if i < 0:
+            return moved and at == 0
+        s, n = axes[i]
+        reach = sum((m - 1) * r for r, m in axes[:i])
+        if s == 0:
+            return True
+        first, last = max(1 - n, -((at + reach) // s)), min(n - 1, (reach - at) // s)
+        return any(meets(i - 1, at + d * s, moved or d != 0) for d in range(first, last + 1))
+
+    if meets(len(axes) - 1, 0, False):
+        raise ValueError(f"{name}: elements overlap")
 
 
 def _table_of(table, D, name="table"):
