@@ -121,26 +121,65 @@ def rotation_table(rows, rot, *, freq=None, base=10000.0, magnitude=1.0, device=
 class _CachePlan(_DevicePlan):
     """A plan that runs on its tensors' device, whichever is current."""
 
+    _cleared = None  # the event behind which the error words are zero, and the streams that are behind it
+    _behind = frozenset()
+    _kept = True
+
+    @classmethod
+    def _once(cls, *args, **kw):
+        """One run, where it is made, of a plan that nobody keeps."""
+        plan = cls.__new__(cls)
+        plan._kept = False
+        plan.__init__(*args, **kw)
+        return plan.run()
+
     def run(self, stream=None):
-        """Launch on `stream` (None: the device's current one); returns the outputs."""
-        index = self._dev.index
-        if stream is None and torch.cuda.current_device() == index:
-            return super().run()
-        if stream is not None and stream.device != self._dev:
+        """Launch on `stream` (None: the device's current one); returns the
+        outputs.  A run comes behind the making of the plan and clear_errors(),
+        whatever streams they were on; in a graph's capture, which cannot wait for
+        another stream, they have to be complete (torch.cuda.graph sees to it)
+        or on the captured stream."""
+        if stream is None:
+            stream = torch.cuda.current_stream(self._dev)
+        elif stream.device != self._dev:
             raise ValueError(f"stream: on {stream.device}, expected {self._dev}")
+        if self._cleared is not None and stream.cuda_stream not in self._behind:
+            self._wait(stream)
+        if torch.cuda.current_device() == self._dev.index:
+            return super().run(stream)
         with torch.cuda.device(self._dev):
             return super().run(stream)
 
     def clear_errors(self, stream=None):
         """Zero seq_error and error_word, on `stream` (None: the current one)."""
         with torch.cuda.stream(stream):
-            self.out["seq_error"].zero_()
-            self.out["error_word"].zero_()
+            self._words.zero_()
+            self._mark(torch.cuda.current_stream(self._dev))
 
     def _errors(self, a, B, dev):
-        self.out["seq_error"] = torch.zeros(B, dtype=torch.int32, device=dev)
-        self.out["error_word"] = torch.zeros(1, dtype=torch.int32, device=dev)
+        self._words = torch.zeros(B + 1, dtype=torch.int32, device=dev)
+        self.out["seq_error"], self.out["error_word"] = self._words[:B], self._words[B:]
         a.seq_error, a.error_word = _ptr(self.out["seq_error"]), _ptr(self.out["error_word"])
+        if self._kept and dev.type == "cuda":
+            self._mark(torch.cuda.current_stream(dev))
+
+    def _mark(self, stream):
+        """`stream`, its device's current one, has zeroed the error words (and
+        holds the work that used the plan's memory before)."""
+        if torch.cuda.current_device() == stream.device_index:
+            captured = torch.cuda.is_current_stream_capturing()
+        else:
+            with torch.cuda.stream(stream):
+                captured = torch.cuda.is_current_stream_capturing()
+        if not captured:  # (a captured clearing is the graph's)
+            self._cleared, self._behind = stream.record_event(), {stream.cuda_stream}
+
+    def _wait(self, stream):
+        with torch.cuda.stream(stream):
+            if torch.cuda.is_current_stream_capturing():
+                return
+        stream.wait_event(self._cleared)
+        self._behind.add(stream.cuda_stream)
 
 
 def _heads(t, name, dtypes=None):
@@ -365,8 +404,8 @@ def rotate_heads(x, table, *, positions=None, prefix_len=None, pairs=False, tran
     with _work_on(stream, [x, table, positions, prefix_len, out]):
         if host:
             x, positions, prefix_len = _to_device([x, positions, prefix_len], table.device)
-        return _results(RotateHeadsPlan(x, table, positions=positions, prefix_len=prefix_len, pairs=pairs,
-                                        transpose=transpose, out=out).run(), host)
+        return _results(RotateHeadsPlan._once(x, table, positions=positions, prefix_len=prefix_len, pairs=pairs,
+                                              transpose=transpose, out=out), host)
 
 
 def append_cache(k, v, cache, block_table, prefix_len=None, *, table=None, pairs=False, positions=None, count=None,
@@ -379,9 +418,9 @@ def append_cache(k, v, cache, block_table, prefix_len=None, *, table=None, pairs
         if host:
             given = _to_device(given, cache.device)
         k, v, block_table, prefix_len, positions, count, path_nodes, path_len = given
-        return _results(AppendCachePlan(k, v, cache, block_table, prefix_len, table=table, pairs=pairs,
-                                        positions=positions, count=count, path_nodes=path_nodes,
-                                        path_len=path_len).run(), host)
+        return _results(AppendCachePlan._once(k, v, cache, block_table, prefix_len, table=table, pairs=pairs,
+                                              positions=positions, count=count, path_nodes=path_nodes,
+                                              path_len=path_len), host)
 
 
 def attend_cache(q, cache, block_table, prefix_len=None, *, count=None, parent=None, scale=None, out=None,
@@ -396,5 +435,5 @@ def attend_cache(q, cache, block_table, prefix_len=None, *, count=None, parent=N
         if host:
             given = _to_device(given, cache.device)
         q, block_table, prefix_len, count, parent = given
-        return _results(AttendCachePlan(q, cache, block_table, prefix_len, count=count, parent=parent, scale=scale,
-                                        out=out).run(), host)
+        return _results(AttendCachePlan._once(q, cache, block_table, prefix_len, count=count, parent=parent, scale=scale,
+                                              out=out), host)
