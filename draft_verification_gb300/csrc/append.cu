@@ -120,11 +120,12 @@ __global__ void __launch_bounds__(TH, kHold == 2 ? 4 : kHold == 1 ? 3 : 1) appen
   const bool reports = blockIdx.x == 0 && h == 0;  // one CTA per sequence reports what concerns all of it
   int rows, bits = 0;
   if (path) {
-    rows = P.path_len[b] + 1;
+    const int depth = P.path_len[b];
     if (path[0] == -1) return;  // the verification's data-error marking
     if (tid == 0) skip_s = 0;
     __syncthreads();
-    if (rows < 1 || rows > P.path_ld) bits |= SPEC_ERR_CACHE, rows = 0;
+    if (depth < 0 || depth >= P.path_ld) bits |= SPEC_ERR_CACHE;
+    rows = bits ? 0 : depth + 1;
     bool bad = false;
     for (int i = tid; i < rows; i += TH) bad |= path[i] < 0 || path[i] >= P.n;
     if (bad) atomicOr(&skip_s, SPEC_ERR_PARENT);
