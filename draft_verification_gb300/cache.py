@@ -276,8 +276,8 @@ class AppendCachePlan(_CachePlan):
 
     k, v [B, n, H, D] float32 or bfloat16 (any strides with contiguous heads),
     cache a PagedCache, block_table int32 [B, P]: each sequence's pages in the
-    order of its tokens.  Row i goes to token prefix_len[b] + i (int32 [B];
-    None: 0).  count int32 [B]: the rows of each sequence (None: n).
+    order of its tokens (no page twice among those that get rows).  Row i goes
+    to token prefix_len[b] + i (int32 [B]; None: 0).  count int32 [B]: the rows of each sequence (None: n).
     path_nodes int32 [B, depth + 1] and path_len int32 [B], as a tree
     verification returns them: instead, the rows of the kept path.  table: keys
     are rotated (RotateHeadsPlan), each by positions int32 [B, n] or by the

@@ -8,14 +8,17 @@
 // bf16, 4 for those of fp32), loaded before the block table's answer is
 // there.  Larger pages, and rows that start anywhere, are read twice.
 //
-// Bound by memory, 2 x (element + code) bytes per row, head and element, by
-// instructions and by what a CTA waits for one after another: its lengths, its
-// rows, the rotation's rows, an older page's exponent.  4 x 8191 rows of 8
-// heads of 128, bf16: 48 us, 4.3 TB/s, 0.64 of a copy's rate; with a test of
-// the range per element instead of per vector 53, with three CTAs per SM
-// instead of four 50, read twice 62, with room for four units in every page 70
-// (fewer CTAs per SM).  A drafted chain (64 x 6 rows) takes 16 us, nearly all
-// of it launch and latency.
+// It moves 2 x (element + code) bytes per row, head and element.  4 x 8191 rows
+// of 8 heads of 128, bf16: 48 us, 4.2 TB/s, 0.63 of a copy's rate.  What bounds
+// that: instructions (70 % of the issue slots, DRAM 44 % busy) and three waits
+// of a CTA one behind another (its lengths; the page's name beside its rows; an
+// older page's exponents beside the rotation's rows, which every head reads
+// again, from L2).  When they were tried: a test of the range per element
+// instead of per vector 53 us, three CTAs per SM instead of four 50, rows read
+// twice 62, room for four units in every page 70 (fewer CTAs per SM).  Pages of
+// more units than two per thread run at one CTA of 512 threads per SM: the same
+// rows in pages of 128 72 us, in fp32 111 us (0.46).  A drafted chain (64 x 6
+// rows) takes 5.4 us in a graph, one row 2.6; a call from the host costs more.
 #include <algorithm>
 #include <cstdint>
 

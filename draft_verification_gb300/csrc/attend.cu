@@ -34,12 +34,15 @@
 // role leave it together.
 //
 // What bounds it: up to 32 rows the bytes (1.07 GB of cache, 8 heads of 128,
-// 4 query heads each: 2 rows 168 us, 95 % of a copy's rate; 6 rows 183, 88 %;
-// 8 rows 196, 82 %), above that the instructions of the weights' warps (12
-// rows, blocks of 48: 245 us, 66 %; 16, blocks of 64: 277, 58 %): some 18 per
-// score, at a third of the issue slots.  Short calls are latency: one piece
-// takes about 14,000 cycles from launch to the end, a third of it until the
-// lengths, the block table and the queries have come.
+// 4 query heads each: 2 rows 167 us, 96 % of a copy's rate; 6 rows 176, 91 %;
+// 8 rows 192, 84 %), above that the instructions of the weights' warps (12
+// rows, blocks of 48: 241 us, 67 %; 16, blocks of 64: 285, 57 %): some 18 per
+// score, at a third of the issue slots.  Beside its tiles (1.16 us each with 64
+// rows) a block costs queries, masks, outputs and its share of the joining: 16
+// trees of 64 nodes take 110 us + 1.16 us per tile of a CTA, 3.4 blocks each.
+// Short calls are latency: one piece takes about 14,000 cycles from launch to
+// the end, a third of it until the lengths, the block table and the queries
+// have come.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -73,10 +76,12 @@ constexpr int kFar = 3;
 template <int R, int NP>
 struct Shape {
   // CTAs per SM: two, whose roles fill each other's waits, as long as registers
-  // (64 a thread) and memories hold them (64 chains of 6 rows of 4 heads, 24 rows:
-  // 190 us, one per SM 225).  Tiles of a step: two share a maximum, a meeting and
-  // their hand-overs (36 rows, 2 x 131072 tokens: 187 us, of one tile 192; with
-  // 24 rows, one CTA per SM, two tiles took 241 us, one 225).
+  // (64 a thread) and memories hold them.  Tiles of a step: two share a maximum, a
+  // meeting and their hand-overs.  Measured both ways on the form that the kernel
+  // had when this was chosen (its calls take 150 and 132 us now): 64 chains of 6
+  // rows of 4 heads, 24 rows, two CTAs per SM 190 us, one 225; 36 rows, 2 x 131072
+  // tokens, steps of two tiles 187 us, of one 192; 24 rows, one CTA per SM, steps
+  // of two tiles 241 us, of one 225.
   static constexpr int kCtas = NP == 1 && R <= 24 ? 2 : 1;
   static constexpr int kSubs = NP == 1 && R >= 32 ? 2 : 1;
   // An operand from shared memory costs its bytes (a product of 128 x 32 with 32
@@ -1360,7 +1365,8 @@ int block_rows(int n, int G, int D) {
   static constexpr int kRows[6] = {8, 16, 24, 32, 48, 64}, kTime[6] = {780, 820, 850, 910, 1130, 1290};
   int best = 0;
   long long least = 0;
-  // (of trees of more than 512 nodes the masks of 64 bits do not fit)
+  // (the masks of 64 bits of a tree of more than 512 nodes do not fit; chains of as
+  // many rows have none, but the workspace is asked for without word of parents)
   for (int i = 0; i < (n > 512 ? 4 : 6); ++i) {
     const long long time = static_cast<long long>((rows + kRows[i] - 1) / kRows[i]) * kTime[i];
     if (i == 0 || time <= least) least = time, best = i;

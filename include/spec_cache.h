@@ -106,7 +106,8 @@ spec_status spec_rotate_heads(const spec_rotate_args* args, cudaStream_t stream)
 /* code.  Where e grows, the page's tokens before prefix_len[b] are scaled   */
 /* along (exact but for codes that become subnormal).  Nothing else of the  */
 /* cache changes.                                                           */
-/*  - Two sequences' appended rows must not share a page.                   */
+/*  - No two entries of the block table that get rows, of one sequence or of */
+/*    two, may name the same page.                                           */
 /*  - A NaN, an infinity or a y beyond 448 * 2^e becomes a NaN code and sets */
 /*    SPEC_ERR_NONFINITE.                                                   */
 /*  - A position outside the table sets SPEC_ERR_POSITION: the key's rotated */
