@@ -154,7 +154,8 @@ class _CachePlan(_DevicePlan):
         """Zero seq_error and error_word, on `stream` (None: the current one)."""
         with torch.cuda.stream(stream):
             self._words.zero_()
-            self._mark(torch.cuda.current_stream(self._dev))
+            if self._dev.type == "cuda":
+                self._mark(torch.cuda.current_stream(self._dev))
 
     def _errors(self, a, B, dev):
         self._words = torch.zeros(B + 1, dtype=torch.int32, device=dev)

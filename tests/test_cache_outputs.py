@@ -1,4 +1,4 @@
-"""Which tensors the cache operators take to write to: those whose elements lie in places of their own."""
+"""What the cache operators write to: outputs whose elements lie in places of their own, and error words."""
 
 import itertools
 
@@ -42,3 +42,16 @@ def test_attended_heads_lie_apart():
     dv.AttendCachePlan(q, cache, pages, out=view((2, 3, 1, 16), (48, 16, 16, 1)))
     with pytest.raises(ValueError, match="elements overlap"):
         dv.AttendCachePlan(q, cache, pages, out=view((2, 3, 1, 16), (33, 16, 16, 1)))
+
+
+def test_error_words_of_plans_on_host_tensors():
+    """(Such plans refuse to run.)"""
+    cache = dv.PagedCache.empty(4, 1, 16, 16, device="cpu")
+    x, pages = torch.zeros((2, 3, 1, 16), dtype=torch.bfloat16), torch.zeros((2, 4), dtype=torch.int32)
+    for plan in (dv.RotateHeadsPlan(x, torch.zeros(5, 16)), dv.AppendCachePlan(x, x, cache, pages),
+                 dv.AttendCachePlan(x, cache, pages)):
+        assert plan.out["seq_error"].tolist() == [0, 0] and plan.out["error_word"].tolist() == [0]
+        plan.out["seq_error"][1], plan.out["error_word"][0] = 2, 3
+        assert plan.out["seq_error"].tolist() == [0, 2] and plan.out["error_word"].tolist() == [3]
+        plan.clear_errors()
+        assert not plan.out["seq_error"].any() and not plan.out["error_word"].any()
