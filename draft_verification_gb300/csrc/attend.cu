@@ -39,7 +39,8 @@
 // rows, blocks of 48: 241 us, 67 %; 16, blocks of 64: 285, 57 %): some 18 per
 // score, at a third of the issue slots.  Beside its tiles (1.16 us each with 64
 // rows) a block costs queries, masks, outputs and its share of the joining: 16
-// trees of 64 nodes take 110 us + 1.16 us per tile of a CTA, 3.4 blocks each.
+// trees of 64 nodes over 4096 tokens take 236 us, 127 of them for the 110 tiles
+// of a CTA, the others for its 3.4 blocks.
 // Short calls are latency: one piece takes about 14,000 cycles from launch to
 // the end, a third of it until the lengths, the block table and the queries
 // have come.
